@@ -71,7 +71,7 @@ def draw(rng):
     typ = rng.choice(["bf16", "bf16", "fp16"])
     hq, hkv = _heads(rng)
     if op == "table":
-        return {"op": "table", "rows": _log_int(rng, 1, 131200), "rot": 2 * rng.randint(2, 64),
+        return {"op": "table", "rows": _log_int(rng, 2, 131200), "rot": 2 * rng.randint(2, 64),
                 "base": rng.choice([10000.0, 500000.0, 1000000.0]),
                 "scaling": rng.choice(["none", "linear", "ntk", "parts"]), "factor": rng.uniform(1.0, 16.0),
                 "orig": _log_int(rng, 1024, 32768)}
