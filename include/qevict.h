@@ -384,6 +384,119 @@ qevict_status qevict_diag_route(qevict_diag *diag, qevict_stream_t stream);
 qevict_status qevict_diag_read(qevict_diag *diag, qevict_diag_report *out, qevict_stream_t stream);
 qevict_status qevict_diag_destroy(qevict_diag *diag);
 
+/* ---- Rotary positions (QEvict §4.3, "Cache Execution", leaves them to the model: the queries and keys
+ * given to this library already carry them).  Position p turns channel pair i by p * theta_i;
+ * a pair (x1, x2) becomes factor * (x1 c - x2 s, x2 c + x1 s) with c, s the cosine and sine.
+ * theta_i = base^(-2i / rot_dim), scaled for contexts longer than the model's (s = factor below):
+ *   QEVICT_ROPE_NONE    theta_i;
+ *   QEVICT_ROPE_LINEAR  theta_i / s (positions interpolated);
+ *   QEVICT_ROPE_NTK     base * s^(rot_dim / (rot_dim - 2)) in place of base (needs rot_dim >= 4);
+ *   QEVICT_ROPE_PARTS   keep * theta_i + (1 - keep) * theta_i / s, where keep rises from 0 to 1 while the
+ *                       turns of pair i over the original context, orig_len * theta_i / (2 pi), rise from
+ *                       low to high (by-parts interpolation: low = 1, high = 32 in YaRN, arXiv 2309.00071;
+ *                       its magnitude 0.1 ln(s) + 1 is the `factor` of qevict_rope_apply). */
+enum { QEVICT_ROPE_NONE = 0, QEVICT_ROPE_LINEAR = 1, QEVICT_ROPE_NTK = 2, QEVICT_ROPE_PARTS = 3 };
+typedef struct {
+  int32_t rot_dim;      /* channels that rotate: even, 2..512 */
+  int32_t scaling;
+  double base;          /* > 0 */
+  double factor;        /* context stretch s > 0 (unused by NONE) */
+  double orig_len, low, high;   /* PARTS: orig_len > 0, 0 <= low < high */
+} qevict_rope_config;
+/* theta_i of every pair, host fp64 [rot_dim / 2].  Host only. */
+qevict_status qevict_rope_angles(const qevict_rope_config *cfg, double *theta);
+/* d_table: fp32 [rows][rot_dim / 2][2], row r = (cos, sin) of position first + r, each within 2^-23 of the
+ * exact value of position * theta_i.  With rot_dim = 128 and first = 0 it is the table of qevict_set_rope_table.
+ * 8-byte aligned; 0 <= first, 1 <= rows, first + rows <= 2^31. */
+qevict_status qevict_rope_table(const qevict_rope_config *cfg, int64_t first, int64_t rows, float *d_table,
+                                qevict_stream_t stream);
+
+enum { QEVICT_BF16 = 0, QEVICT_FP16 = 1, QEVICT_FP32 = 2 };
+/* Rotates the heads of h_q queries and h_k keys per token (either may be 0, its pointers then NULL).
+ * Strides are in elements, {batch, token, head}, channels contiguous; input strides may be 0 or in any
+ * order, output strides may not put two elements in one place. */
+typedef struct {
+  int32_t dtype;        /* QEVICT_BF16, QEVICT_FP16, QEVICT_FP32 */
+  int32_t batch, seq, h_q, h_k;
+  int32_t d_head;       /* 2..1024 */
+  int32_t rot_dim;      /* the first rot_dim channels of a head rotate, the others pass unchanged */
+  int32_t interleaved;  /* pairs (2i, 2i + 1) instead of (i, i + rot_dim / 2) */
+  int32_t inverse;      /* rotate back; with the same factor also the gradient of the forward call */
+  float factor;         /* of the rotated channels */
+  int64_t table_rows, pos0;   /* rows of d_table; position of token 0 when d_positions is NULL */
+  int64_t q_in[3], q_out[3], k_in[3], k_out[3];
+} qevict_rope_desc;
+/* d_table: fp32 [table_rows][rot_dim / 2][2], 16-byte aligned.  d_positions: int32 [batch][seq], or NULL
+ * for pos0 + t.  A tensor may be rotated in place (same pointer and strides); any other overlap of a
+ * tensor's input and output is QEVICT_EINVAL, as are positions past the table when d_positions is NULL.  A token whose
+ * d_positions entry lies outside [0, table_rows) is not written and sets bit 8 of *d_status, a device
+ * word that the caller clears. */
+qevict_status qevict_rope_apply(const qevict_rope_desc *desc, const float *d_table, const int32_t *d_positions,
+                                const void *q_in, void *q_out, const void *k_in, void *k_out, int32_t *d_status,
+                                qevict_stream_t stream);
+
+/* ---- Attention over a dense KV cache: prompts, the last chunk of a longer context, single tokens.
+ * Sequence b holds kv_len[b] keys, key j at position j, and q_len[b] queries, the last ones: query i sits at position
+ * p = kv_len[b] - q_len[b] + i.  Query head h reads KV head h / (h_q / h_kv).
+ *   s_j = q . k_j * scale;  softcap > 0: s_j = softcap * tanh(s_j / softcap);  slopes: s_j -= slopes[h] * |p - j|
+ *   out = sum_j softmax(s)_j v_j,  lse = log sum_j exp(s_j)    over the visible keys
+ * Key j < kv_len[b] is visible to position p when (causal = 0, or j <= p, or j < prefix_len[b]) and, with
+ * doc_ids, positions j and p lie in one document, a document being a run of equal ids (a query before
+ * position 0 then sees nothing).  A row that sees nothing gets out = 0, lse = -inf.  What stands in
+ * invisible keys and values (infinities, NaN) does not reach a row; visible ones propagate.  Rows behind
+ * q_len[b] are not written.  Softmax statistics and sums are fp32; the probabilities are rounded to the
+ * input type for the product with the values, and the output once.
+ * Results do not change from run to run. */
+typedef struct {
+  int32_t dtype;                           /* QEVICT_BF16 or QEVICT_FP16, of q, k, v and out */
+  int32_t batch, s_q, s_kv, h_q, h_kv;     /* s_kv: keys the cache has room for; h_q / h_kv whole, at most 128 */
+  int32_t d_head;                          /* 128 */
+  int32_t causal;
+  float scale;                             /* > 0; 0 = 1 / sqrt(d_head) */
+  float softcap;                           /* >= 0; 0 = none */
+  /* strides in elements, {batch, token, head}, channels contiguous: multiples of 8; a batch stride of q, k, v may be
+   * 0 (one cache for all); out's may not put two elements in one place */
+  int64_t q[3], k[3], v[3], o[3];
+} qevict_attn_desc;
+/* Optional device arrays, NULL = absent: kv_len absent = s_kv, q_len absent = s_q.  Lengths outside
+ * [0, s_kv] / [0, s_q] are clamped and set bit 8 of the status word. prefix_len needs causal = 1. */
+typedef struct {
+  const float *slopes;         /* [h_q] fp32 */
+  const int32_t *q_len;        /* [batch] */
+  const int32_t *kv_len;       /* [batch] */
+  const int32_t *prefix_len;   /* [batch] */
+  const int32_t *doc_ids;      /* [batch][s_kv] */
+} qevict_attn_mask;
+/* Bytes of device workspace of a call (a bound for every mask).  The workspace is 256-byte aligned; its first 256 bytes
+ * hold the status word and must be cleared once before its first use.  Calls that may overlap on the
+ * GPU (two streams, two replayed graphs) need workspaces of their own. */
+qevict_status qevict_attn_bytes(const qevict_attn_desc *desc, size_t *bytes);
+/* q [batch][s_q][h_q][128], k, v [batch][s_kv][h_kv][128], out like q (16-byte aligned); lse fp32
+ * [batch][s_q][h_q] or NULL. */
+qevict_status qevict_attn(const qevict_attn_desc *desc, const qevict_attn_mask *mask, const void *q, const void *k,
+                          const void *v, void *out, float *lse, void *d_work, size_t bytes, qevict_stream_t stream);
+
+/* ---- Attention of a batch whose sequences share one prefix (decode steps behind a common prompt): the
+ * prefix's keys are read once for all sequences.  Sequence b sees the s_prefix shared keys and its own
+ * kv_len[b] keys, which follow them (key j at position s_prefix + j; the newest tokens' keys are among
+ * them), causally: query i sits at position s_prefix + kv_len[b] - s_q + i.  Equal to qevict_attn over
+ * the joined keys.  s_q * h_q / h_kv <= 128.  desc: s_kv is the room for own keys, causal must be 1. */
+typedef struct {
+  qevict_attn_desc attn;
+  int32_t s_prefix;            /* >= 1 */
+  int64_t k_prefix[2], v_prefix[2];   /* strides {token, head} */
+} qevict_prefix_attn_desc;
+qevict_status qevict_prefix_attn_bytes(const qevict_prefix_attn_desc *desc, size_t *bytes);
+/* k_prefix, v_prefix [s_prefix][h_kv][128]; slopes [h_q] and kv_len [batch] as above or NULL. */
+qevict_status qevict_prefix_attn(const qevict_prefix_attn_desc *desc, const float *slopes, const int32_t *kv_len,
+                                 const void *q, const void *k_prefix, const void *v_prefix, const void *k,
+                                 const void *v, void *out, float *lse, void *d_work, size_t bytes,
+                                 qevict_stream_t stream);
+
+/* The status word at d_status (the one of qevict_rope_apply, or the start of an attention workspace):
+ * synchronises `stream`, copies the word to *host_word (may be NULL) and clears it.  QEVICT_EDEVICE if it was set. */
+qevict_status qevict_ops_status(void *d_status, int32_t *host_word, qevict_stream_t stream);
+
 /* Frees the host handle (the arena stays the caller's). */
 qevict_status qevict_destroy(qevict_cache *cache);
 

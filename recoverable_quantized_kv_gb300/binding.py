@@ -68,6 +68,35 @@ class DiagReport(ctypes.Structure):
                 ("lag", ctypes.c_int64 * 32)]
 
 
+class RopeConfig(ctypes.Structure):
+    _fields_ = [("rot_dim", ctypes.c_int32), ("scaling", ctypes.c_int32)] + \
+               [(n, ctypes.c_double) for n in ("base", "factor", "orig_len", "low", "high")]
+
+
+_Stride3 = ctypes.c_int64 * 3
+_Stride2 = ctypes.c_int64 * 2
+
+
+class RopeDesc(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("dtype", "batch", "seq", "h_q", "h_k", "d_head", "rot_dim", "interleaved",
+                                             "inverse")] + \
+               [("factor", ctypes.c_float), ("table_rows", ctypes.c_int64), ("pos0", ctypes.c_int64)] + \
+               [(n, _Stride3) for n in ("q_in", "q_out", "k_in", "k_out")]
+
+
+class AttnDesc(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("dtype", "batch", "s_q", "s_kv", "h_q", "h_kv", "d_head", "causal")] + \
+               [("scale", ctypes.c_float), ("softcap", ctypes.c_float)] + [(n, _Stride3) for n in ("q", "k", "v", "o")]
+
+
+class AttnMask(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("slopes", "q_len", "kv_len", "prefix_len", "doc_ids")]
+
+
+class PrefixAttnDesc(ctypes.Structure):
+    _fields_ = [("attn", AttnDesc), ("s_prefix", ctypes.c_int32), ("k_prefix", _Stride2), ("v_prefix", _Stride2)]
+
+
 _lib = None
 
 
@@ -108,6 +137,14 @@ def load() -> ctypes.CDLL:
         "qevict_prefill_scores_noalloc_status": [P],
         "qevict_debug_cap_free_slots": [P, I32],
         "qevict_read_status": [P, ctypes.POINTER(I32), P],
+        "qevict_rope_angles": [ctypes.POINTER(RopeConfig), ctypes.POINTER(ctypes.c_double)],
+        "qevict_rope_table": [ctypes.POINTER(RopeConfig), I64, I64, P, P],
+        "qevict_rope_apply": [ctypes.POINTER(RopeDesc), P, P, P, P, P, P, P, P],
+        "qevict_attn_bytes": [ctypes.POINTER(AttnDesc), ctypes.POINTER(ctypes.c_size_t)],
+        "qevict_attn": [ctypes.POINTER(AttnDesc), ctypes.POINTER(AttnMask), P, P, P, P, P, P, ctypes.c_size_t, P],
+        "qevict_prefix_attn_bytes": [ctypes.POINTER(PrefixAttnDesc), ctypes.POINTER(ctypes.c_size_t)],
+        "qevict_prefix_attn": [ctypes.POINTER(PrefixAttnDesc)] + [P] * 10 + [ctypes.c_size_t, P],
+        "qevict_ops_status": [P, ctypes.POINTER(I32), P],
     }
     for name, args in sig.items():
         fn = getattr(lib, name)
@@ -128,7 +165,8 @@ def exported_symbols():
             "qevict_export_state", "qevict_import_state", "qevict_set_rope_table", "qevict_diag_bytes",
             "qevict_diag_init", "qevict_diag_route", "qevict_diag_read", "qevict_diag_destroy",
             "qevict_selftest_wait", "qevict_prefill_scores_noalloc_status", "qevict_debug_cap_free_slots",
-            "qevict_read_status"]
+            "qevict_read_status", "qevict_rope_angles", "qevict_rope_table", "qevict_rope_apply", "qevict_attn_bytes",
+            "qevict_attn", "qevict_prefix_attn_bytes", "qevict_prefix_attn", "qevict_ops_status"]
 
 
 def _check(status: int, where: str):
@@ -336,3 +374,261 @@ class Diagnostics:
             self.close()
         except Exception:
             pass
+
+
+# ---------------------------------------------------------------------------------------------- operators
+# Rotary positions and attention over dense tensors (no cache handle).  Tensors keep their strides; a call
+# runs on the device of its first tensor, on `stream` or that device's current stream.
+
+_ROPE_SCALING = {"none": 0, "linear": 1, "ntk": 2, "parts": 3}
+
+
+def _dtype_code(dtype, where, allowed):
+    import torch
+    code = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}.get(dtype)
+    if code is None or code not in allowed:
+        raise QEvictError(EINVAL, where, f"unsupported dtype {dtype}")
+    return code
+
+
+def _need(ok, where, what):
+    if not ok:
+        raise QEvictError(EINVAL, where, what)
+
+
+def _tensor(t, where, name, shape, dtype, device, dense=False):
+    """Checks one tensor argument: CUDA, on the call's device, of this shape and dtype, channels contiguous."""
+    _need(t.is_cuda and t.device == device, where, f"{name} must be a CUDA tensor on {device}")
+    _need(tuple(t.shape) == tuple(shape), where, f"{name} must have shape {tuple(shape)}, has {tuple(t.shape)}")
+    _need(t.dtype == dtype, where, f"{name} must be {dtype}, is {t.dtype}")
+    if dense:
+        _need(t.is_contiguous(), where, f"{name} must be contiguous")
+    else:
+        _need(t.shape[-1] == 1 or t.stride(-1) == 1, where, f"{name}'s channels must be contiguous")
+
+
+class _on:
+    """The device and stream of a call: makes the device current, and tells the allocator about tensors that
+    are used on a stream other than the device's current one."""
+
+    def __init__(self, device, stream, tensors=()):
+        import torch
+        self.guard = torch.cuda.device(device)
+        self.device, self.stream, self.tensors = device, stream, tensors
+
+    def __enter__(self):
+        import torch
+        self.guard.__enter__()
+        cur = torch.cuda.current_stream(self.device)
+        if self.stream is None or self.stream == cur:
+            return cur.cuda_stream
+        for t in self.tensors:
+            if t is not None:
+                t.record_stream(self.stream)
+        return self.stream.cuda_stream
+
+    def __exit__(self, *exc):
+        return self.guard.__exit__(*exc)
+
+
+def _ops_status(word, where, stream):
+    with _on(word.device, stream) as s:
+        _check(load().qevict_ops_status(_ptr(word), None, s), where)
+
+
+def _rope_config(rot_dim, base, scaling, factor, orig_len, low, high):
+    _need(scaling in _ROPE_SCALING, "rope", f"scaling must be one of {sorted(_ROPE_SCALING)}, is {scaling!r}")
+    return RopeConfig(int(rot_dim), _ROPE_SCALING[scaling], float(base), float(factor), float(orig_len), float(low),
+                      float(high))
+
+
+def rope_angles(rot_dim=128, base=10000.0, scaling="none", factor=1.0, orig_len=0, low=1.0, high=32.0):
+    """Angle per position of every rotated pair, as a list of floats (host fp64)."""
+    cfg = _rope_config(rot_dim, base, scaling, factor, orig_len, low, high)
+    out = (ctypes.c_double * max(1, int(rot_dim) // 2))()
+    _check(load().qevict_rope_angles(ctypes.byref(cfg), out), "qevict_rope_angles")
+    return list(out)
+
+
+def rope_table(rows, rot_dim=128, base=10000.0, scaling="none", factor=1.0, orig_len=0, low=1.0, high=32.0, first=0,
+               out=None, device="cuda", stream=None):
+    """fp32 [rows][rot_dim / 2][2] table of (cos, sin) of the positions from `first` on, for Rope and (rot_dim 128,
+    first 0) Cache.set_rope_table.  scaling: "none", "linear", "ntk" or "parts"; see qevict_rope_config."""
+    import torch
+    cfg = _rope_config(rot_dim, base, scaling, factor, orig_len, low, high)
+    rows = int(rows)
+    _need(rows >= 1 and cfg.rot_dim >= 2 and cfg.rot_dim % 2 == 0, "rope_table", "rows and an even rot_dim of at least 2")
+    if out is None:
+        rope_angles(rot_dim, base, scaling, factor, orig_len, low, high)   # refuses before anything is allocated
+        with torch.cuda.device(device), torch.cuda.stream(stream):
+            out = torch.empty(rows, cfg.rot_dim // 2, 2, dtype=torch.float32, device=device)
+    _tensor(out, "rope_table", "out", (rows, cfg.rot_dim // 2, 2), torch.float32, out.device, dense=True)
+    with _on(out.device, stream, (out,)) as s:
+        _check(load().qevict_rope_table(ctypes.byref(cfg), int(first), rows, _ptr(out), s), "qevict_rope_table")
+    return out
+
+
+class Rope:
+    """Rotations with one (cos, sin) table (fp32 [rows][rot_dim / 2][2], e.g. from rope_table)."""
+
+    def __init__(self, table):
+        import torch
+        load()
+        _need(table.dim() == 3 and table.shape[2] == 2, "Rope", "table must have shape [rows][rot_dim / 2][2]")
+        _tensor(table, "Rope", "table", table.shape, torch.float32, table.device, dense=True)
+        self.table = table
+        self.status = torch.zeros(1, dtype=torch.int32, device=table.device)
+
+    def apply(self, q, k=None, positions=None, pos0=0, interleaved=False, inverse=False, factor=1.0, q_out=None,
+              k_out=None, stream=None):
+        """Rotates q [batch][seq][heads][d] and, if given, k; returns (q_out, k_out), new tensors unless given
+        (q_out=q rotates in place).  positions: int32 [batch][seq], default pos0 + t.  inverse=True rotates back
+        and, with the same factor, is the gradient of the forward call.  Tokens whose position is outside the
+        table are not written; check() reports them."""
+        import torch
+        where = "Rope.apply"
+        dev = self.table.device
+        _need(q.dim() == 4 and (k is None or k.dim() == 4), where, "q and k must be [batch][seq][heads][d]")
+        b, s, hq, d = q.shape
+        _tensor(q, where, "q", q.shape, q.dtype, dev)
+        if k is not None:
+            _tensor(k, where, "k", (b, s, k.shape[2], d), q.dtype, dev)
+        if positions is not None:
+            _tensor(positions, where, "positions", (b, s), torch.int32, dev, dense=True)
+        _need(k is not None or k_out is None, where, "k_out without k")
+        outs = []
+        for name, x, o in (("q_out", q, q_out), ("k_out", k, k_out)):
+            if o is None and x is not None:
+                with torch.cuda.device(dev), torch.cuda.stream(stream):
+                    o = torch.empty(x.shape, dtype=x.dtype, device=dev)
+            if o is not None:
+                _tensor(o, where, name, x.shape, x.dtype, dev)
+            outs.append(o)
+        desc = RopeDesc(_dtype_code(q.dtype, where, (0, 1, 2)), b, s, hq, 0 if k is None else k.shape[2], d,
+                        2 * self.table.shape[1], int(bool(interleaved)), int(bool(inverse)), float(factor),
+                        self.table.shape[0], int(pos0), _Stride3(*q.stride()[:3]), _Stride3(*outs[0].stride()[:3]))
+        if k is not None:
+            desc.k_in, desc.k_out = _Stride3(*k.stride()[:3]), _Stride3(*outs[1].stride()[:3])
+        with _on(dev, stream, (q, k, positions, self.table, self.status, *outs)) as st:
+            _check(load().qevict_rope_apply(ctypes.byref(desc), _ptr(self.table), _ptr(positions), _ptr(q),
+                                            _ptr(outs[0]), _ptr(k), _ptr(outs[1]), _ptr(self.status), st),
+                   "qevict_rope_apply")
+        return outs[0], outs[1]
+
+    def check(self, stream=None):
+        """Raises EDEVICE if a call since the last check met a position outside the table (synchronises)."""
+        _ops_status(self.status, "Rope.check", stream)
+
+
+class _AttnPlan:
+    """Sizes, options and the workspace of an attention operator.  A plan serves one call at a time: calls that can
+    overlap on the GPU (two streams, two replayed graphs) need plans of their own."""
+
+    def _setup(self, where, batch, s_q, s_kv, h_q, h_kv, dtype, causal, softcap, scale, device):
+        import torch
+        self.desc = AttnDesc(_dtype_code(dtype, where, (0, 1)), int(batch), int(s_q), int(s_kv), int(h_q), int(h_kv), 128,
+                             int(bool(causal)), float(scale), float(softcap))
+        self.dtype = dtype
+        self.device = torch.device(device)
+        if self.device.type == "cuda" and self.device.index is None and torch.cuda.is_available():
+            self.device = torch.device("cuda", torch.cuda.current_device())
+        d = self.desc
+        dense = lambda s, h: _Stride3(s * h * 128, h * 128, 128)   # noqa: E731
+        d.q = d.o = dense(max(1, d.s_q), max(1, d.h_q))
+        d.k = d.v = dense(max(1, d.s_kv), max(1, d.h_kv))
+
+    def _workspace(self, nbytes):
+        import torch
+        self.work = torch.empty(nbytes, dtype=torch.uint8, device=self.device)
+        self.work[:256].zero_()
+
+    def _tensors(self, where, q, k, v, out, lse, stream):
+        import torch
+        d = self.desc
+        q_shape, kv_shape = (d.batch, d.s_q, d.h_q, 128), (d.batch, d.s_kv, d.h_kv, 128)
+        _tensor(q, where, "q", q_shape, self.dtype, self.device)
+        _tensor(k, where, "k", kv_shape, self.dtype, self.device)
+        _tensor(v, where, "v", kv_shape, self.dtype, self.device)
+        with torch.cuda.device(self.device), torch.cuda.stream(stream):
+            if out is None:
+                out = torch.empty(q_shape, dtype=self.dtype, device=self.device)
+            if lse is None:
+                lse = torch.empty(q_shape[:3], dtype=torch.float32, device=self.device)
+        _tensor(out, where, "out", q_shape, self.dtype, self.device)
+        _tensor(lse, where, "lse", q_shape[:3], torch.float32, self.device, dense=True)
+        desc = type(d).from_buffer_copy(d)   # a call's strides are its own
+        desc.q, desc.k, desc.v, desc.o = (_Stride3(*t.stride()[:3]) for t in (q, k, v, out))
+        return desc, out, lse
+
+    def _array(self, where, name, t, shape, dtype):
+        if t is not None:
+            _tensor(t, where, name, shape, dtype, self.device, dense=True)
+        return t
+
+    def check(self, stream=None):
+        """Raises EDEVICE if a call since the last check recorded a fault: a length outside its range (clamped), or
+        a wait that ran out (synchronises)."""
+        _ops_status(self.work, type(self).__name__ + ".check", stream)
+
+
+class Attention(_AttnPlan):
+    """Attention of the last q_len[b] positions of every sequence over a dense KV cache: prompts (s_q = s_kv), a
+    prompt's last chunk, single tokens (s_q = 1).  See qevict_attn for the masks and the definition."""
+
+    def __init__(self, batch, s_q, s_kv, h_q, h_kv, dtype=None, causal=True, softcap=0.0, scale=0.0, device="cuda"):
+        import torch
+        self._setup("Attention", batch, s_q, s_kv, h_q, h_kv, dtype or torch.bfloat16, causal, softcap, scale, device)
+        n = ctypes.c_size_t()
+        with torch.cuda.device(self.device):
+            _check(load().qevict_attn_bytes(ctypes.byref(self.desc), ctypes.byref(n)), "qevict_attn_bytes")
+        self._workspace(n.value)
+
+    def run(self, q, k, v, out=None, lse=None, slopes=None, q_len=None, kv_len=None, prefix_len=None, doc_ids=None,
+            stream=None):
+        """q [batch][s_q][h_q][128], k, v [batch][s_kv][h_kv][128], any strides that are multiples of 8 elements;
+        returns (out, lse), new tensors unless given.  Rows behind q_len[b] are not written."""
+        import torch
+        where, d = "Attention.run", self.desc
+        desc, out, lse = self._tensors(where, q, k, v, out, lse, stream)
+        arrays = [self._array(where, "slopes", slopes, (d.h_q,), torch.float32)]
+        for name, t in (("q_len", q_len), ("kv_len", kv_len), ("prefix_len", prefix_len)):
+            arrays.append(self._array(where, name, t, (d.batch,), torch.int32))
+        arrays.append(self._array(where, "doc_ids", doc_ids, (d.batch, d.s_kv), torch.int32))
+        mask = AttnMask(*(_ptr(t) for t in arrays))
+        with _on(self.device, stream, (q, k, v, out, lse, self.work, *arrays)) as s:
+            _check(load().qevict_attn(ctypes.byref(desc), ctypes.byref(mask), _ptr(q), _ptr(k), _ptr(v), _ptr(out),
+                                      _ptr(lse), _ptr(self.work), self.work.numel(), s), "qevict_attn")
+        return out, lse
+
+
+class PrefixAttention(_AttnPlan):
+    """Causal attention of s_q new tokens of every sequence over a prefix that all sequences share (read once) and
+    each sequence's own keys behind it.  s_kv: room for own keys.  See qevict_prefix_attn."""
+
+    def __init__(self, batch, s_q, s_prefix, s_kv, h_q, h_kv, dtype=None, softcap=0.0, scale=0.0, device="cuda"):
+        import torch
+        self._setup("PrefixAttention", batch, s_q, s_kv, h_q, h_kv, dtype or torch.bfloat16, True, softcap, scale, device)
+        self.s_prefix = int(s_prefix)
+        n = ctypes.c_size_t()
+        st = _Stride2(self.desc.h_kv * 128, 128)
+        pd = PrefixAttnDesc(self.desc, self.s_prefix, st, st)
+        with torch.cuda.device(self.device):
+            _check(load().qevict_prefix_attn_bytes(ctypes.byref(pd), ctypes.byref(n)), "qevict_prefix_attn_bytes")
+        self._workspace(n.value)
+
+    def run(self, q, k_prefix, v_prefix, k, v, out=None, lse=None, slopes=None, kv_len=None, stream=None):
+        """q [batch][s_q][h_q][128], k_prefix, v_prefix [s_prefix][h_kv][128], k, v [batch][s_kv][h_kv][128];
+        returns (out, lse), new tensors unless given."""
+        import torch
+        where, d = "PrefixAttention.run", self.desc
+        desc, out, lse = self._tensors(where, q, k, v, out, lse, stream)
+        for name, t in (("k_prefix", k_prefix), ("v_prefix", v_prefix)):
+            _tensor(t, where, name, (self.s_prefix, d.h_kv, 128), self.dtype, self.device)
+        self._array(where, "slopes", slopes, (d.h_q,), torch.float32)
+        self._array(where, "kv_len", kv_len, (d.batch,), torch.int32)
+        pd = PrefixAttnDesc(desc, self.s_prefix, _Stride2(*k_prefix.stride()[:2]), _Stride2(*v_prefix.stride()[:2]))
+        with _on(self.device, stream, (q, k_prefix, v_prefix, k, v, out, lse, slopes, kv_len, self.work)) as s:
+            _check(load().qevict_prefix_attn(ctypes.byref(pd), _ptr(slopes), _ptr(kv_len), _ptr(q), _ptr(k_prefix),
+                                             _ptr(v_prefix), _ptr(k), _ptr(v), _ptr(out), _ptr(lse), _ptr(self.work),
+                                             self.work.numel(), s), "qevict_prefix_attn")
+        return out, lse

@@ -1,0 +1,360 @@
+// Attention over a dense KV cache and of a batch behind a shared prefix: argument checks, split rules,
+// workspace layout, the document scan and the merge of split results.  The attention kernel itself is in
+// attn_dev.cuh.
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cmath>
+#include <cstdint>
+
+#include "attn_dev.cuh"
+#include "qevict.h"
+
+namespace qv {
+cudaError_t launch_attn_bf16(const AttnArgs &P, int grid, bool cap, bool bias, cudaStream_t s);
+cudaError_t launch_attn_fp16(const AttnArgs &P, int grid, bool cap, bool bias, cudaStream_t s);
+
+// First and past-the-last position of every position's run of equal ids.  One CTA per sequence; thread i
+// takes the i-th of 1024 consecutive pieces, finds the first and last run start in it, and two block
+// scans carry the last start before and the first start after each piece.
+constexpr int RUN_THREADS = 1024;
+__global__ void __launch_bounds__(RUN_THREADS) doc_runs_kernel(const int *ids, int s_kv, int2 *runs) {
+  __shared__ int last[RUN_THREADS], first[RUN_THREADS];
+  const int *id = ids + (size_t)blockIdx.x * s_kv;
+  int2 *out = runs + (size_t)blockIdx.x * s_kv;
+  const int piece = (s_kv + RUN_THREADS - 1) / RUN_THREADS, t = threadIdx.x;
+  const int lo = min(s_kv, t * piece), hi = min(s_kv, lo + piece);
+  auto starts = [&](int p) { return p == 0 || id[p] != id[p - 1]; };
+  int f = s_kv, l = -1;
+  for (int p = lo; p < hi; ++p)
+    if (starts(p)) {
+      if (f == s_kv) f = p;
+      l = p;
+    }
+  last[t] = l;
+  first[t] = f;
+  __syncthreads();
+  for (int o = 1; o < RUN_THREADS; o <<= 1) {   // inclusive scans: max from the left, min from the right
+    const int a = t >= o ? last[t - o] : -1, b = t + o < RUN_THREADS ? first[t + o] : s_kv;
+    __syncthreads();
+    last[t] = max(last[t], a);
+    first[t] = min(first[t], b);
+    __syncthreads();
+  }
+  int begin = t ? last[t - 1] : 0;
+  int end = 0;   // past the current run, found when a run starts
+  for (int p = lo; p < hi; ++p) {
+    if (p == lo || starts(p)) {
+      if (starts(p)) begin = p;
+      end = p + 1;
+      while (end < hi && !starts(end)) ++end;
+      if (end == hi) end = t + 1 < RUN_THREADS ? first[t + 1] : s_kv;
+    }
+    out[p] = make_int2(begin, end);
+  }
+}
+
+struct CombineArgs {
+  const float *part_o, *part_l;
+  void *out;
+  float *lse;
+  const int *q_len;
+  int64_t so[3], rows;
+  int n, batch, s_q, h_q;
+};
+
+// One warp per row (sequence, query, head): out = sum_s 2^(lse_s - L) out_s, L the log2-sum-exp over the
+// splits; 512 bytes per split and row, read once.
+template <bool FP16>
+__global__ void __launch_bounds__(256) attn_combine_kernel(const CombineArgs A) {
+  const int64_t row = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
+  const int lane = threadIdx.x & 31;
+  if (row >= A.rows) return;
+  const int h = (int)(row % A.h_q);
+  const int64_t x = row / A.h_q;
+  const int i = (int)(x % A.s_q), b = (int)(x / A.s_q);
+  if (A.q_len && i >= A.q_len[b]) return;
+  float mx = -INFINITY;
+  for (int s = lane; s < A.n; s += 32) mx = fmaxf(mx, A.part_l[s * A.rows + row]);
+  for (int o = 16; o; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+  const float mu = mx == -INFINITY ? 0.f : mx;
+  float l = 0.f;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int s0 = 0; s0 < A.n; s0 += 32) {
+    const float w = s0 + lane < A.n ? ex2(A.part_l[(s0 + lane) * A.rows + row] - mu) : 0.f;
+    l += w;
+    const int m = min(32, A.n - s0);
+#pragma unroll 4
+    for (int s = 0; s < m; ++s) {
+      const float ws = __shfl_sync(0xffffffffu, w, s);
+      if (ws != 0.f) {   // a split without keys for the row wrote no output (NaN weights go on)
+        const float4 o = *reinterpret_cast<const float4 *>(A.part_o + ((s0 + s) * A.rows + row) * D + 4 * lane);
+        acc.x = fmaf(ws, o.x, acc.x);
+        acc.y = fmaf(ws, o.y, acc.y);
+        acc.z = fmaf(ws, o.z, acc.z);
+        acc.w = fmaf(ws, o.w, acc.w);
+      }
+    }
+  }
+  for (int o = 16; o; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+  *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(A.out) + b * A.so[0] + i * A.so[1] + h * A.so[2] + 4 * lane) =
+      make_uint2(pack2<FP16>(acc.x * inv, acc.y * inv), pack2<FP16>(acc.z * inv, acc.w * inv));
+  if (lane == 0 && A.lse) A.lse[row] = l == 0.f ? -INFINITY : (mu + log2f(l)) * 0.69314718055994531f;
+}
+
+namespace {
+
+int64_t align256(int64_t x) { return (x + 255) & ~int64_t(255); }
+
+int sm_count() {
+  int dev = 0, n = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess ||
+      n <= 0) {
+    cudaGetLastError();
+    return 152;
+  }
+  return n;
+}
+
+// [tokens][heads][128] tensors of `batch` sequences as a 4-D tensor map; a box is 64 channels x `bh` heads x
+// `bt` tokens x `bb` sequences, 128-byte swizzled.  batch: 1 when the batch stride is 0.
+bool dense_map(CUtensorMap *map, bool fp16, const void *base, int64_t heads, int64_t tokens, int64_t batch, int64_t st_h,
+               int64_t st_t, int64_t st_b, int bh, int bt, int bb) {
+  PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
+  if (!enc) return false;
+  const cuuint64_t dims[4] = {(cuuint64_t)D, (cuuint64_t)heads, (cuuint64_t)tokens, (cuuint64_t)batch};
+  // a dimension of one element has no step: any valid one will do
+  const cuuint64_t strides[3] = {(cuuint64_t)(heads > 1 ? st_h : D) * 2, (cuuint64_t)(tokens > 1 ? st_t : D) * 2,
+                                 (cuuint64_t)(batch > 1 ? st_b : D) * 2};
+  const cuuint32_t box[4] = {64, (cuuint32_t)bh, (cuuint32_t)bt, (cuuint32_t)bb};
+  const cuuint32_t estr[4] = {1, 1, 1, 1};
+  return enc(map, fp16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void *>(base),
+             dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+struct AttnPlan {
+  int G, tpt, n_pr, ns, items;
+  int pre, nb, n_prp, nsp, items_p;
+  int64_t rows, off_runs, off_l, off_o, bytes;
+};
+
+bool stride_ok(int64_t st, int64_t size, bool zero) {
+  if (size <= 1) return true;
+  return st % 8 == 0 && st < (1ll << 38) && (st > 0 || (zero && st == 0));
+}
+
+qevict_status attn_plan(const qevict_attn_desc *d, int s_prefix, AttnPlan *p) {
+  if (!d || d->dtype < 0 || d->dtype > 1 || d->batch < 1 || d->s_q < 1 || d->s_kv < 1 || d->h_kv < 1 || d->h_q < d->h_kv ||
+      d->h_q % d->h_kv || d->h_q / d->h_kv > AT_TILE || d->d_head != D || d->causal < 0 || d->causal > 1 ||
+      !(d->scale >= 0.f) || !std::isfinite(d->scale) || !(d->softcap >= 0.f) || !std::isfinite(d->softcap))
+    return QEVICT_EINVAL;
+  if (d->s_q > (1 << 30) || d->s_kv > (1 << 30) || s_prefix < 0 || s_prefix > (1 << 30)) return QEVICT_EINVAL;
+  for (int n = 0; n < 3; ++n) {
+    const int64_t *st = n == 0 ? d->q : n == 1 ? d->k : d->v;
+    if (!stride_ok(st[0], d->batch, true) || !stride_ok(st[1], n ? d->s_kv : d->s_q, false) ||
+        !stride_ok(st[2], n ? d->h_kv : d->h_q, false))
+      return QEVICT_EINVAL;
+  }
+  if (!stride_ok(d->o[0], d->batch, false) || !stride_ok(d->o[1], d->s_q, false) || !stride_ok(d->o[2], d->h_q, false))
+    return QEVICT_EINVAL;
+  *p = AttnPlan();
+  p->G = d->h_q / d->h_kv;
+  p->tpt = AT_TILE / p->G;
+  p->rows = (int64_t)d->batch * d->s_q * d->h_q;
+  const int64_t sms = sm_count();
+  const int64_t n_qt = (d->s_q + p->tpt - 1) / p->tpt, n_pr = (n_qt + 1) / 2;
+  const int64_t base = (int64_t)d->batch * d->h_kv * n_pr, tiles = (d->s_kv + AT_TILE - 1) / AT_TILE;
+  if (base > (1 << 24) || p->rows > (1ll << 40)) return QEVICT_EINVAL;
+  // Splits of the keys while the items leave SMs idle, each split with at least four key tiles (two per slot)
+  const int64_t min_tiles = 4;
+  const int64_t ns = std::max<int64_t>(1, std::min(sms / base, tiles / min_tiles));
+  p->n_pr = (int)n_pr;
+  p->ns = (int)ns;
+  int64_t items_p = 0;
+  if (s_prefix) {
+    if (!d->causal || (int64_t)d->s_q * p->G > AT_TILE) return QEVICT_EINVAL;
+    p->pre = s_prefix;
+    p->nb = std::min(p->tpt / d->s_q, 256);
+    const int64_t n_qtp = (d->batch + p->nb - 1) / p->nb, n_prp = (n_qtp + 1) / 2;
+    const int64_t base_p = d->h_kv * n_prp, tiles_p = (s_prefix + AT_TILE - 1) / AT_TILE;
+    p->n_prp = (int)n_prp;
+    p->nsp = (int)std::max<int64_t>(1, std::min(sms / base_p, tiles_p / min_tiles));
+    items_p = base_p * p->nsp;
+  }
+  if (base * ns + items_p > (1 << 28)) return QEVICT_EINVAL;
+  p->items_p = (int)items_p;
+  p->items = (int)(base * ns + items_p);
+  int64_t off = 256;
+  p->off_runs = off;
+  if (!s_prefix) off += align256((int64_t)d->batch * d->s_kv * 8);
+  const int64_t parts = p->ns + p->nsp;
+  p->off_l = off;
+  p->off_o = off;
+  if (parts > 1) {
+    off += align256(parts * p->rows * 4);
+    p->off_o = off;
+    off += align256(parts * p->rows * D * 4);
+  }
+  p->bytes = off;
+  return QEVICT_OK;
+}
+
+bool o_disjoint(const qevict_attn_desc *d) {
+  int64_t size[3] = {d->batch, d->s_q, d->h_q}, reach = D;
+  for (int n = 0; n < 3; ++n) {
+    int best = -1;
+    for (int i = 0; i < 3; ++i)
+      if (size[i] > 1 && (best < 0 || d->o[i] < d->o[best])) best = i;
+    if (best < 0) break;
+    if (d->o[best] < reach) return false;
+    reach += d->o[best] * (size[best] - 1);
+    size[best] = 1;
+  }
+  return true;
+}
+
+qevict_status attn_launch(const qevict_attn_desc *d, const AttnPlan &pl, const qevict_attn_mask *mask,
+                          const qevict_prefix_attn_desc *pd, const void *q, const void *kp, const void *vp, const void *k,
+                          const void *v, void *out, float *lse, void *d_work, size_t bytes, cudaStream_t s) {
+  if (!q || !k || !v || !out || !d_work || (((uintptr_t)q | (uintptr_t)k | (uintptr_t)v | (uintptr_t)out) & 15) ||
+      ((uintptr_t)lse & 3) || ((uintptr_t)d_work & 255) || !o_disjoint(d))
+    return QEVICT_EINVAL;
+  qevict_attn_mask none = {};
+  const qevict_attn_mask &m = mask ? *mask : none;
+  if (((uintptr_t)m.slopes | (uintptr_t)m.q_len | (uintptr_t)m.kv_len | (uintptr_t)m.prefix_len | (uintptr_t)m.doc_ids) & 3)
+    return QEVICT_EINVAL;
+  if (m.prefix_len && !d->causal) return QEVICT_EINVAL;
+  if ((int64_t)bytes < pl.bytes) return QEVICT_ENOMEM;
+  uint8_t *w = static_cast<uint8_t *>(d_work);
+  AttnArgs A = {};
+  A.q = q, A.k = k, A.v = v, A.kp = kp, A.vp = vp;
+  A.out = out;
+  A.lse = lse;
+  A.status = reinterpret_cast<int *>(w);
+  A.slopes = m.slopes, A.q_len = m.q_len, A.kv_len = m.kv_len, A.prefix_len = m.prefix_len;
+  for (int i = 0; i < 3; ++i) A.sq[i] = d->q[i], A.sk[i] = d->k[i], A.sv[i] = d->v[i], A.so[i] = d->o[i];
+  A.rows = pl.rows;
+  A.batch = d->batch, A.s_q = d->s_q, A.s_kv = d->s_kv, A.h_q = d->h_q, A.h_kv = d->h_kv, A.G = pl.G, A.causal = d->causal;
+  A.mul_q = d->batch > 1 && d->q[0] ? 1 : 0;
+  A.mul_k = d->batch > 1 && d->k[0] ? 1 : 0;
+  A.mul_v = d->batch > 1 && d->v[0] ? 1 : 0;
+  A.tpt = pl.tpt, A.n_pr = pl.n_pr, A.ns = pl.ns;
+  A.pre = pl.pre, A.nb = pl.nb, A.n_prp = pl.n_prp, A.nsp = pl.nsp;
+  A.items = pl.items, A.items_p = pl.items_p;
+  const float scale = d->scale > 0.f ? d->scale : 1.f / std::sqrt((float)D), log2e = 1.4426950408889634f;
+  A.scale_log2 = scale * log2e;
+  if (d->softcap > 0.f) {
+    A.cap_in = 2.f * log2e * scale / d->softcap;
+    A.cap_log2 = d->softcap * log2e;
+  }
+  const bool fp16 = d->dtype == QEVICT_FP16;
+  const int qb = A.mul_q ? d->batch : 1, kb = A.mul_k ? d->batch : 1, vb = A.mul_v ? d->batch : 1;
+  bool ok = dense_map(&A.tq, fp16, q, d->h_q, d->s_q, qb, d->q[2], d->q[1], d->q[0], pl.G, pl.tpt, 1) &&
+            dense_map(&A.tk, fp16, k, d->h_kv, d->s_kv, kb, d->k[2], d->k[1], d->k[0], 1, AT_TILE, 1) &&
+            dense_map(&A.tv, fp16, v, d->h_kv, d->s_kv, vb, d->v[2], d->v[1], d->v[0], 1, AT_TILE, 1);
+  if (pd) {
+    A.skp[0] = pd->k_prefix[0], A.skp[1] = pd->k_prefix[1], A.svp[0] = pd->v_prefix[0], A.svp[1] = pd->v_prefix[1];
+    ok = ok && dense_map(&A.tqp, fp16, q, d->h_q, d->s_q, d->batch, d->q[2], d->q[1], d->q[0], pl.G, d->s_q, pl.nb) &&
+         dense_map(&A.tkp, fp16, kp, d->h_kv, pl.pre, 1, pd->k_prefix[1], pd->k_prefix[0], 0, 1, AT_TILE, 1) &&
+         dense_map(&A.tvp, fp16, vp, d->h_kv, pl.pre, 1, pd->v_prefix[1], pd->v_prefix[0], 0, 1, AT_TILE, 1);
+  }
+  if (!ok) return QEVICT_EINVAL;
+  if (m.doc_ids) {
+    A.runs = reinterpret_cast<int2 *>(w + pl.off_runs);
+    doc_runs_kernel<<<d->batch, RUN_THREADS, 0, s>>>(m.doc_ids, d->s_kv, const_cast<int2 *>(A.runs));
+    if (cudaGetLastError() != cudaSuccess) return QEVICT_ECUDA;
+  }
+  const int parts = pl.ns + pl.nsp;
+  if (parts > 1) {
+    A.part_l = reinterpret_cast<float *>(w + pl.off_l);
+    A.part_o = reinterpret_cast<float *>(w + pl.off_o);
+  }
+  const int grid = std::min(pl.items, sm_count());
+  if ((fp16 ? launch_attn_fp16 : launch_attn_bf16)(A, grid, d->softcap > 0.f, m.slopes != nullptr, s) != cudaSuccess)
+    return QEVICT_ECUDA;
+  if (parts > 1) {
+    CombineArgs C = {};
+    C.part_o = A.part_o, C.part_l = A.part_l;
+    C.out = out, C.lse = lse;
+    C.q_len = m.q_len;
+    for (int i = 0; i < 3; ++i) C.so[i] = d->o[i];
+    C.rows = pl.rows;
+    C.n = parts, C.batch = d->batch, C.s_q = d->s_q, C.h_q = d->h_q;
+    const unsigned blocks = (unsigned)((pl.rows + 7) / 8);
+    if (fp16)
+      attn_combine_kernel<true><<<blocks, 256, 0, s>>>(C);
+    else
+      attn_combine_kernel<false><<<blocks, 256, 0, s>>>(C);
+    if (cudaGetLastError() != cudaSuccess) return QEVICT_ECUDA;
+  }
+  return QEVICT_OK;
+}
+
+}  // namespace
+}  // namespace qv
+
+extern "C" {
+
+qevict_status qevict_attn_bytes(const qevict_attn_desc *desc, size_t *bytes) {
+  qv::AttnPlan p;
+  if (!bytes) return QEVICT_EINVAL;
+  const qevict_status st = qv::attn_plan(desc, 0, &p);
+  if (st == QEVICT_OK) *bytes = (size_t)p.bytes;
+  return st;
+}
+
+qevict_status qevict_attn(const qevict_attn_desc *desc, const qevict_attn_mask *mask, const void *q, const void *k,
+                          const void *v, void *out, float *lse, void *d_work, size_t bytes, qevict_stream_t stream) {
+  qv::AttnPlan p;
+  const qevict_status st = qv::attn_plan(desc, 0, &p);
+  if (st != QEVICT_OK) return st;
+  return qv::attn_launch(desc, p, mask, nullptr, q, nullptr, nullptr, k, v, out, lse, d_work, bytes,
+                         reinterpret_cast<cudaStream_t>(stream));
+}
+
+static qevict_status prefix_plan(const qevict_prefix_attn_desc *d, qv::AttnPlan *p) {
+  if (!d || d->s_prefix < 1) return QEVICT_EINVAL;
+  if (!qv::stride_ok(d->k_prefix[0], d->s_prefix, false) || !qv::stride_ok(d->v_prefix[0], d->s_prefix, false) ||
+      !qv::stride_ok(d->k_prefix[1], d->attn.h_kv, false) || !qv::stride_ok(d->v_prefix[1], d->attn.h_kv, false))
+    return QEVICT_EINVAL;
+  if (d->attn.batch > 1 && d->attn.q[0] == 0) return QEVICT_EINVAL;
+  return qv::attn_plan(&d->attn, d->s_prefix, p);
+}
+
+qevict_status qevict_prefix_attn_bytes(const qevict_prefix_attn_desc *desc, size_t *bytes) {
+  qv::AttnPlan p;
+  if (!bytes) return QEVICT_EINVAL;
+  const qevict_status st = prefix_plan(desc, &p);
+  if (st == QEVICT_OK) *bytes = (size_t)p.bytes;
+  return st;
+}
+
+qevict_status qevict_prefix_attn(const qevict_prefix_attn_desc *desc, const float *slopes, const int32_t *kv_len,
+                                 const void *q, const void *k_prefix, const void *v_prefix, const void *k,
+                                 const void *v, void *out, float *lse, void *d_work, size_t bytes,
+                                 qevict_stream_t stream) {
+  qv::AttnPlan p;
+  const qevict_status st = prefix_plan(desc, &p);
+  if (st != QEVICT_OK) return st;
+  if (!k_prefix || !v_prefix || (((uintptr_t)k_prefix | (uintptr_t)v_prefix) & 15)) return QEVICT_EINVAL;
+  qevict_attn_mask m = {};
+  m.slopes = slopes;
+  m.kv_len = kv_len;
+  return qv::attn_launch(&desc->attn, p, &m, desc, q, k_prefix, v_prefix, k, v, out, lse, d_work, bytes,
+                         reinterpret_cast<cudaStream_t>(stream));
+}
+
+qevict_status qevict_ops_status(void *d_status, int32_t *host_word, qevict_stream_t stream) {
+  if (!d_status || ((uintptr_t)d_status & 3)) return QEVICT_EINVAL;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  int word = 0;
+  if (cudaMemcpyAsync(&word, d_status, sizeof(int), cudaMemcpyDeviceToHost, s) != cudaSuccess ||
+      cudaMemsetAsync(d_status, 0, sizeof(int), s) != cudaSuccess || cudaStreamSynchronize(s) != cudaSuccess)
+    return QEVICT_ECUDA;
+  if (host_word) *host_word = word;
+  return word ? QEVICT_EDEVICE : QEVICT_OK;
+}
+
+}  // extern "C"

@@ -1,0 +1,781 @@
+// Attention over a dense KV cache on the 5th-generation tensor cores: parameters shared by the kernel's
+// translation units and the host side, and the kernel itself.
+//
+// Online softmax in base 2 over key tiles of 128: with x_j the (capped, biased) logit times log2 e,
+//   m' = max(m, max x),  l' = l 2^(m - m') + sum 2^(x - m'),  O' = O 2^(m - m') + 2^(x - m') V,
+// out = O / l, lse = (m + log2 l) ln 2.
+#pragma once
+
+#include "smem_optin.h"
+#include "tc_dev.cuh"
+
+namespace qv {
+
+constexpr int AT_TILE = 128;                          // rows of a query tile, keys of a key tile
+constexpr int AT_STAGES = 5;                          // key / value tiles in flight
+constexpr int AT_TILE_BYTES = AT_TILE * D * 2;        // 32 KB: two 128-byte-swizzled halves of 64 channels
+constexpr int AT_HALF_BYTES = AT_TILE_BYTES / 2;
+constexpr int AT_THREADS = 384;                       // two softmax warpgroups, one of helper warps
+constexpr int AT_OFF_KV = 2 * AT_TILE_BYTES;
+constexpr int AT_OFF_ML = AT_OFF_KV + AT_STAGES * AT_TILE_BYTES;   // [2][128] fp32: slot 1's m and l
+constexpr int AT_OFF_BAR = AT_OFF_ML + 2 * AT_TILE * 4;
+constexpr int AT_NBAR = 3 * AT_STAGES + 2 + 6;
+constexpr int AT_OFF_MISC = AT_OFF_BAR + AT_NBAR * 8;              // tmem address, flags
+constexpr int AT_SMEM = 1024 + AT_OFF_MISC + 4 * (2 + 2 * AT_STAGES + 2);
+static_assert(AT_SMEM <= 232448, "one CTA per SM");
+// launch: 384 threads x 168 registers; softmax warps take 216, helper warps give down to 72
+static_assert(256 * 216 + 128 * 72 <= 384 * 168, "register split");
+
+struct AttnArgs {
+  CUtensorMap tq, tk, tv;      // queries and own keys of each sequence
+  CUtensorMap tqp, tkp, tvp;   // queries of all sequences stacked, shared prefix
+  const void *k, *v, *q, *kp, *vp;
+  void *out;
+  float *lse;
+  float *part_o, *part_l;      // [split][row][128], [split][row] (log2 domain); NULL: written directly
+  int *status;
+  const float *slopes;
+  const int *q_len, *kv_len, *prefix_len;
+  const int2 *runs;            // [batch][s_kv]: first and past-the-last position of every position's document
+  int64_t sq[3], sk[3], sv[3], so[3], skp[2], svp[2];
+  int64_t rows;                // batch * s_q * h_q
+  int batch, s_q, s_kv, h_q, h_kv, G, causal;
+  int mul_q, mul_k, mul_v;     // batch coordinate of the tensor maps: 0 for a batch stride of 0
+  int tpt, n_pr, ns;           // own keys: tokens per row tile, pairs of row tiles, splits
+  int pre, nb, n_prp, nsp;     // prefix: keys, sequences per row tile, pairs of row tiles, splits
+  int items_p, items;          // prefix items, all items
+  float scale_log2;            // logit scale * log2 e
+  float cap_in, cap_log2;      // softcap: 2 log2 e * scale / cap, cap * log2 e
+};
+
+// A work item: one or two row tiles of one KV head against one split of a key range.  pair: slot 0 and 1
+// hold two row tiles and both see every key tile.  Otherwise one row tile in both slots, slot s taking
+// every second key tile.
+struct AttnItem {
+  bool prefix, pair;
+  int b, g, tile0, sp;
+  int kl, ql;                  // keys and queries of the sequence
+  int n, t_hi;                 // key tiles t_hi - 1, t_hi - 2, ... (n of them)
+  int clean_lo, clean_hi;      // keys that every row of the item sees
+  int key_lo, key_hi;          // keys that some row sees
+};
+
+__device__ __forceinline__ int clampi(int x, int lo, int hi) { return x < lo ? lo : x > hi ? hi : x; }
+
+// Visible keys [x, y) of position p.  Both ends grow with p.
+__device__ __forceinline__ int2 attn_interval(const AttnArgs &P, int b, int p, int kl) {
+  int lo = 0, hi = kl;
+  if (P.causal) {
+    const int pre = P.prefix_len ? clampi(P.prefix_len[b], 0, kl) : 0;
+    hi = min(max(p + 1, pre), kl);
+  }
+  if (P.runs) {
+    if (p < 0) return make_int2(0, 0);
+    const int2 r = P.runs[(size_t)b * P.s_kv + p];
+    lo = r.x;
+    hi = min(hi, r.y);
+  }
+  return make_int2(lo, max(hi, lo));
+}
+
+__device__ __forceinline__ AttnItem attn_item(const AttnArgs &P, int it) {
+  AttnItem I;
+  int lo, hi;
+  if (it < P.items_p) {
+    I.prefix = true;
+    I.g = it % P.h_kv;
+    const int x = it / P.h_kv;
+    I.sp = x % P.nsp;
+    I.tile0 = 2 * (x / P.nsp);
+    I.b = 0;
+    I.kl = P.pre;
+    I.ql = P.s_q;
+    I.pair = (I.tile0 + 1) * P.nb < P.batch;
+    I.clean_lo = I.key_lo = 0;
+    I.clean_hi = I.key_hi = P.pre;
+    lo = 0;
+    hi = (P.pre + AT_TILE - 1) / AT_TILE;
+    const int per = (hi + P.nsp - 1) / P.nsp;
+    lo = I.sp * per;
+    hi = min(hi, lo + per);
+  } else {
+    it -= P.items_p;
+    I.prefix = false;
+    I.g = it % P.h_kv;
+    int x = it / P.h_kv;
+    I.b = x % P.batch;
+    x /= P.batch;
+    I.sp = x % P.ns;
+    const int pr = P.n_pr - 1 - x / P.ns;   // causal: the longest rows first
+    I.tile0 = 2 * pr;
+    I.kl = P.kv_len ? clampi(P.kv_len[I.b], 0, P.s_kv) : P.s_kv;
+    I.ql = P.q_len ? clampi(P.q_len[I.b], 0, P.s_q) : P.s_q;
+    const int i0 = I.tile0 * P.tpt, i1 = min(I.ql, i0 + 2 * P.tpt);
+    I.pair = i0 + P.tpt < I.ql;
+    I.clean_lo = I.clean_hi = I.key_lo = I.key_hi = 0;
+    lo = hi = 0;
+    if (i0 < i1) {
+      const int p0 = I.kl - I.ql + i0;
+      const int2 a = attn_interval(P, I.b, p0, I.kl), z = attn_interval(P, I.b, p0 + (i1 - 1 - i0), I.kl);
+      I.key_lo = a.x;
+      I.key_hi = z.y;
+      I.clean_lo = z.x;
+      I.clean_hi = a.y;
+      if (I.key_hi > I.key_lo) {
+        lo = I.key_lo / AT_TILE;
+        hi = (I.key_hi + AT_TILE - 1) / AT_TILE;
+      }
+    }
+    const int per = (hi - lo + P.ns - 1) / P.ns;
+    lo += I.sp * per;
+    hi = min(hi, lo + per);
+  }
+  I.n = max(0, hi - lo);
+  I.t_hi = hi;
+  return I;
+}
+
+// Whether some row of the item does not see some key of tile t: only there can a value that is not finite
+// stand in a masked place (a masked probability is 0, and 0 * NaN is not).
+__device__ __forceinline__ bool attn_mixed(const AttnItem &I, int t) {
+  return t * AT_TILE < I.clean_lo || (t + 1) * AT_TILE > I.clean_hi;
+}
+
+// Row r of the slot's tile: sequence b, query i (false: the row is padding).
+__device__ __forceinline__ bool attn_row(const AttnArgs &P, const AttnItem &I, int slot, int r, int &b, int &i, int &h) {
+  const int tile = I.tile0 + (I.pair ? slot : 0), tok = r / P.G;
+  h = I.g * P.G + (r - tok * P.G);
+  if (I.prefix) {
+    const int bl = tok / P.s_q;
+    b = tile * P.nb + bl;
+    i = tok - bl * P.s_q;
+    return bl < P.nb && b < P.batch;
+  }
+  b = I.b;
+  i = tile * P.tpt + tok;
+  return tok < P.tpt && i < I.ql;
+}
+
+// Bounded wait on an mbarrier phase: as mbar_wait with a limit of 4 s, since a slot that recomputes rows on
+// the CUDA cores (attn_exact_rows) holds the others up for longer than the 200 ms of the other kernels.
+__device__ __forceinline__ bool attn_wait(uint64_t *bar, uint32_t parity, int *status) {
+  if (mbar_try_wait(bar, parity)) return true;
+  const uint64_t t0 = globaltimer_ns();
+  for (uint32_t it = 0;; ++it) {
+    if (mbar_try_wait(bar, parity)) return true;
+    if ((it & 255u) == 255u && globaltimer_ns() - t0 > 4000000000ull) {
+      atomicOr(status, QV_ERR_TIMEOUT);
+      return false;
+    }
+  }
+}
+
+// ----------------------------------------------------------------------------- tensor memory and products
+
+__device__ __forceinline__ void tma_load_4d_at(uint32_t dst, const CUtensorMap *map, int x, int y, int z, int w,
+                                               uint64_t *bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], "
+      "[%6];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(smem_u32(bar))
+      : "memory");
+}
+// D (+)= A B with A in tensor memory
+__device__ __forceinline__ void tc_mma_ta(uint32_t tmem, uint32_t ta, uint64_t db, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}" ::"r"(tmem),
+      "r"(ta), "l"(db), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+// shared-memory descriptor of a value tile: [128 keys][64 channels] halves, channels contiguous (the N side of
+// P V is the contiguous one), 128-byte swizzle; 64-channel blocks 16 KB apart, 8-key groups 1024 B apart
+__device__ __forceinline__ uint64_t umma_desc_v(uint32_t saddr) {
+  return (uint64_t)((saddr & 0x3FFFFu) >> 4) | ((uint64_t)(AT_HALF_BYTES >> 4) << 16) | ((uint64_t)(1024 >> 4) << 32) |
+         ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
+}
+
+#define QV_R16(r, o)                                                                                               \
+  "r"((r)[(o) + 0]), "r"((r)[(o) + 1]), "r"((r)[(o) + 2]), "r"((r)[(o) + 3]), "r"((r)[(o) + 4]), "r"((r)[(o) + 5]), \
+      "r"((r)[(o) + 6]), "r"((r)[(o) + 7]), "r"((r)[(o) + 8]), "r"((r)[(o) + 9]), "r"((r)[(o) + 10]),               \
+      "r"((r)[(o) + 11]), "r"((r)[(o) + 12]), "r"((r)[(o) + 13]), "r"((r)[(o) + 14]), "r"((r)[(o) + 15])
+#define QV_W16(r, o)                                                                                                  \
+  "=r"((r)[(o) + 0]), "=r"((r)[(o) + 1]), "=r"((r)[(o) + 2]), "=r"((r)[(o) + 3]), "=r"((r)[(o) + 4]),                 \
+      "=r"((r)[(o) + 5]), "=r"((r)[(o) + 6]), "=r"((r)[(o) + 7]), "=r"((r)[(o) + 8]), "=r"((r)[(o) + 9]),             \
+      "=r"((r)[(o) + 10]), "=r"((r)[(o) + 11]), "=r"((r)[(o) + 12]), "=r"((r)[(o) + 13]), "=r"((r)[(o) + 14]),        \
+      "=r"((r)[(o) + 15])
+
+// 32 columns of this thread's lane; the caller waits (tmem_wait_ld) before it uses them
+__device__ __forceinline__ void tmem_ld32(uint32_t addr, uint32_t *r) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,"
+      "%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : QV_W16(r, 0), QV_W16(r, 16)
+      : "r"(addr));
+}
+__device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t *r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15};" ::QV_R16(
+          r, 0),
+      "r"(addr)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+__device__ __forceinline__ float rcp_approx(float x) {   // relative error about 2^-23
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+template <bool FP16>
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+  if (FP16) {
+    __half2 v = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<uint32_t *>(&v);
+  }
+  return pack_bf16(lo, hi);
+}
+template <bool FP16>
+__device__ __forceinline__ float2 unpack2(uint32_t v) {
+  if (FP16) return __half22float2(*reinterpret_cast<__half2 *>(&v));
+  return make_float2(bf16_lo(v), bf16_hi(v));
+}
+
+// ----------------------------------------------------------------------------- rows with values that are not finite
+
+// The rows of one warp of a slot recomputed on the CUDA cores, every visible key of the item's own tiles in
+// turn and no masked value touched.  Reached when a value that some row of the item sees and another does not is an infinity or
+// NaN: the tensor-core product then ran with that value as 0.  Writes O (unnormalised), m, l of row r
+// through `emit(r, acc, m, l)`, the warp's lanes holding four channels each.
+template <bool FP16, typename Emit>
+__device__ __forceinline__ void attn_exact_rows(const AttnArgs &P, const AttnItem &I, int slot, int warp, int lane, bool cap,
+                                                const Emit &emit) {
+  const uint16_t *kb, *vb;
+  int64_t kst, vst;
+  if (I.prefix) {
+    kb = static_cast<const uint16_t *>(P.kp) + I.g * P.skp[1];
+    vb = static_cast<const uint16_t *>(P.vp) + I.g * P.svp[1];
+    kst = P.skp[0], vst = P.svp[0];
+  } else {
+    kb = static_cast<const uint16_t *>(P.k) + I.b * P.sk[0] + I.g * P.sk[2];
+    vb = static_cast<const uint16_t *>(P.v) + I.b * P.sv[0] + I.g * P.sv[2];
+    kst = P.sk[1], vst = P.sv[1];
+  }
+  for (int rr = 0; rr < 32; ++rr) {
+    const int r = warp * 32 + rr;
+    int b, i, h;
+    if (!attn_row(P, I, slot, r, b, i, h)) continue;
+    const uint16_t *q = static_cast<const uint16_t *>(P.q) + b * P.sq[0] + i * P.sq[1] + h * P.sq[2];
+    int p, lo, hi;
+    if (I.prefix) {
+      const int kl = P.kv_len ? clampi(P.kv_len[b], 0, P.s_kv) : P.s_kv;
+      p = P.pre + kl - P.s_q + i;
+      lo = 0, hi = P.pre;
+    } else {
+      p = I.kl - I.ql + i;
+      const int2 v = attn_interval(P, b, p, I.kl);
+      lo = v.x, hi = v.y;
+    }
+    const float slope = P.slopes ? P.slopes[h] * 1.4426950408889634f : 0.f;
+    float m = -INFINITY, l = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};
+    for (int j = 0; j < I.n; ++j) {
+      const int t = I.t_hi - 1 - j;
+      for (int c0 = t * AT_TILE; c0 < (t + 1) * AT_TILE; c0 += 32) {
+        if (c0 + 32 <= lo || c0 >= hi) continue;
+        const int key = c0 + lane;
+        const bool seen = key >= lo && key < hi;
+        float x = -INFINITY;
+        if (seen) {
+          const uint32_t *kr = reinterpret_cast<const uint32_t *>(kb + (int64_t)key * kst);
+          const uint32_t *qr = reinterpret_cast<const uint32_t *>(q);
+          float s = 0.f;
+          for (int d = 0; d < D / 2; ++d) {
+            const float2 a = unpack2<FP16>(kr[d]), c = unpack2<FP16>(qr[d]);
+            s = fmaf(a.x, c.x, s);
+            s = fmaf(a.y, c.y, s);
+          }
+          x = cap ? P.cap_log2 * (1.f - 2.f * rcp_approx(1.f + ex2(s * P.cap_in))) : s * P.scale_log2;
+          x -= slope * fabsf((float)(p - key));
+        }
+        float mx = x;
+        for (int o = 16; o; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+        const float mn = fmaxf(m, mx), mu = mn == -INFINITY ? 0.f : mn;
+        const float f = ex2(m - mu), pr = seen ? ex2(x - mu) : 0.f;
+        m = mn;
+        l = l * f;
+        for (int c = 0; c < 4; ++c) acc[c] *= f;
+        float ps = pr;
+        for (int o = 16; o; o >>= 1) ps += __shfl_xor_sync(0xffffffffu, ps, o);
+        l += ps;
+        for (int k = max(0, lo - c0); k < min(32, hi - c0); ++k) {   // visible keys only
+          const float pk = __shfl_sync(0xffffffffu, pr, k);
+          const uint2 w = *reinterpret_cast<const uint2 *>(vb + (int64_t)(c0 + k) * vst + lane * 4);
+          const float2 a = unpack2<FP16>(w.x), c = unpack2<FP16>(w.y);
+          acc[0] = fmaf(pk, a.x, acc[0]);
+          acc[1] = fmaf(pk, a.y, acc[1]);
+          acc[2] = fmaf(pk, c.x, acc[2]);
+          acc[3] = fmaf(pk, c.y, acc[3]);
+        }
+      }
+    }
+    emit(r, b, i, h, acc, m, l);
+  }
+}
+
+// ----------------------------------------------------------------------------- the kernel
+
+// One persistent CTA per SM.  Two softmax warpgroups (slots), each thread owning one row of its slot's
+// 128-row tile, and four helper warps: TMA loads, MMA issue, and two that look for values that are not
+// finite in partly masked tiles.  Rows of a tile are (token, query head of the group), so the group's heads share every key
+// tile.  Tensor memory: S of slot s at columns 128 s, overwritten in place by the probabilities (16-bit, the A operand of
+// P V), O of slot s at 256 + 128 s.  The tensor pipe alternates between the slots: while slot 0 turns
+// S into P, it runs slot 1's products.
+// Key tiles are taken from the last to the first, so a causal row meets its diagonal, and a distance bias its largest
+// logits, first.  The running max moves only when a row's max has grown by more than 2^8 (then the warp rescales its
+// rows of O in tensor memory): until then p reaches at most 2^8, which fp32 sums and 16-bit probabilities hold as well.
+// Every wait is bounded; the TMEM columns are released on every path.
+template <bool FP16, bool CAP, bool BIAS>
+__global__ void __launch_bounds__(AT_THREADS, 1) attn_kernel(const __grid_constant__ AttnArgs P) {
+  extern __shared__ uint8_t at_smem_raw[];
+  uint8_t *sm = at_smem_raw + ((1024 - (smem_u32(at_smem_raw) & 1023)) & 1023);   // swizzle atoms: 1024-aligned
+  uint64_t *bars = reinterpret_cast<uint64_t *>(sm + AT_OFF_BAR);
+  uint64_t *full = bars, *empty = full + AT_STAGES, *gfull = empty + AT_STAGES;
+  uint64_t *qfull = gfull + AT_STAGES, *qempty = qfull + 1;
+  uint64_t *sfull = qempty + 1, *pfull = sfull + 2, *ofull = pfull + 2;
+  uint32_t *misc = reinterpret_cast<uint32_t *>(sm + AT_OFF_MISC);
+  uint32_t *tmem_slot = misc;
+  volatile uint32_t *badstage = misc + 2, *badslot = badstage + 2 * AT_STAGES;
+  float *ml = reinterpret_cast<float *>(sm + AT_OFF_ML);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  int *status = P.status;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < AT_NBAR; ++i) {
+      const uint64_t *p = &bars[i];
+      const bool four = p >= pfull && p < pfull + 2, two = p >= ofull && p < ofull + 2;
+      mbar_init(&bars[i], four ? 4 : two ? 2 : 1);
+    }
+    fence_mbar_init();
+  }
+  if (warp == 9) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)), "r"(512)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+
+  if (warp >= 8) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+    if (warp == 8) {
+      if (lane == 0) {   // ---- TMA loads
+        const uint32_t qbytes = (uint32_t)(P.G * P.tpt) * 128u;   // half of a query tile
+        const uint32_t qpbytes = (uint32_t)(P.G * P.s_q * P.nb) * 128u;
+        uint32_t c = 0, qc = 0, gc = 0;
+        bool ok = true;
+        for (int it = blockIdx.x; ok && it < P.items; it += gridDim.x) {
+          const AttnItem I = attn_item(P, it);
+          if (!I.prefix && ((P.kv_len && (P.kv_len[I.b] < 0 || P.kv_len[I.b] > P.s_kv)) ||
+                            (P.q_len && (P.q_len[I.b] < 0 || P.q_len[I.b] > P.s_q))))
+            atomicOr(status, QV_ERR_BOUNDS);
+          if (I.n == 0) continue;
+          const CUtensorMap *mq = I.prefix ? &P.tqp : &P.tq, *mk = I.prefix ? &P.tkp : &P.tk,
+                            *mv = I.prefix ? &P.tvp : &P.tv;
+          if (!(ok = attn_wait(qempty, (qc & 1) ^ 1, status))) break;
+          const uint32_t qb = I.prefix ? qpbytes : qbytes;
+          mbar_arrive_expect_tx(qfull, qb * (I.pair ? 4 : 2));
+          for (int s = 0; s < (I.pair ? 2 : 1); ++s) {
+            const uint32_t dst = smem_u32(sm) + s * AT_TILE_BYTES;
+            const int tok = I.prefix ? 0 : (I.tile0 + s) * P.tpt, bb = I.prefix ? (I.tile0 + s) * P.nb : I.b * P.mul_q;
+            tma_load_4d_at(dst, mq, 0, I.g * P.G, tok, bb, qfull);
+            tma_load_4d_at(dst + AT_HALF_BYTES, mq, 64, I.g * P.G, tok, bb, qfull);
+          }
+          ++qc;
+          auto load = [&](const CUtensorMap *map, int j, int bb, bool value) {
+            const uint32_t st = c % AT_STAGES;
+            if (!ok || !(ok = attn_wait(&empty[st], ((c / AT_STAGES) & 1) ^ 1, status))) return;
+            const uint32_t dst = smem_u32(sm) + AT_OFF_KV + st * AT_TILE_BYTES;
+            const int t = I.t_hi - 1 - j;
+            // values of a partly masked tile reach the checking warps first, which then fill the stage's barrier
+            uint64_t *bar = &full[st];
+            if (value && attn_mixed(I, t)) bar = &gfull[gc++ % AT_STAGES];
+            mbar_arrive_expect_tx(bar, AT_TILE_BYTES);
+            tma_load_4d_at(dst, map, 0, I.g, t * AT_TILE, bb, bar);
+            tma_load_4d_at(dst + AT_HALF_BYTES, map, 64, I.g, t * AT_TILE, bb, bar);
+            ++c;
+          };
+          const int bk = I.b * P.mul_k, bv = I.b * P.mul_v;
+          // in the order of their last use: K0 V0 K1 V1 .. for a pair; K0 K1 V0 K2 V1 K3 .. otherwise
+          load(mk, 0, bk, false);
+          if (!I.pair && I.n > 1) load(mk, 1, bk, false);
+          for (int j = 0; ok && j < I.n; ++j) {
+            load(mv, j, bv, true);
+            const int jk = j + (I.pair ? 1 : 2);
+            if (jk < I.n) load(mk, jk, bk, false);
+          }
+        }
+        // copies still in flight land before the CTA leaves
+        for (uint32_t i = c > AT_STAGES ? c - AT_STAGES : 0; i < c; ++i)
+          attn_wait(&full[i % AT_STAGES], (i / AT_STAGES) & 1, status);
+        if (qc) attn_wait(qfull, (qc - 1) & 1, status);
+      }
+    } else if (warp == 9) {
+      if (lane == 0) {   // ---- MMA issue
+        constexpr uint32_t ab = FP16 ? 0u : 1u;
+        constexpr uint32_t ID_S = (1u << 4) | (ab << 7) | (ab << 10) | ((uint32_t)(AT_TILE >> 3) << 17) |
+                                  ((uint32_t)(AT_TILE >> 4) << 24);
+        constexpr uint32_t ID_O = ID_S | (1u << 16);   // B (values) with its N side contiguous
+        uint32_t base = 0, qc = 0, pc[2] = {0, 0};
+        bool ok = true;
+        for (int it = blockIdx.x; ok && it < P.items; it += gridDim.x) {
+          const AttnItem I = attn_item(P, it);
+          if (I.n == 0) continue;
+          const int n = I.n, ns[2] = {I.pair ? n : (n + 1) >> 1, I.pair ? n : n >> 1};
+          uint32_t bad = 0;
+          if (!(ok = attn_wait(qfull, qc & 1, status))) break;
+          ++qc;
+          auto issue_s = [&](int s, int i) {
+            const int j = I.pair ? i : 2 * i + s;
+            const uint32_t cc = base + (I.pair ? 2 * j : j < 2 ? j : 2 * j - 1), st = cc % AT_STAGES;
+            if (!ok || !(ok = attn_wait(&full[st], (cc / AT_STAGES) & 1, status))) return;
+            tc_fence_after();
+            const uint32_t a0 = smem_u32(sm) + (I.pair ? s * AT_TILE_BYTES : 0);
+            const uint32_t b0 = smem_u32(sm) + AT_OFF_KV + st * AT_TILE_BYTES;
+#pragma unroll
+            for (int kk = 0; kk < D / 16; ++kk) {
+              const uint32_t off = (kk >> 2) * AT_HALF_BYTES + (kk & 3) * 32;
+              tc_mma(tmem + 128 * s, umma_desc(a0 + off), umma_desc(b0 + off), ID_S, kk > 0 ? 1u : 0u);
+            }
+            tc_commit(&sfull[s]);
+            if (!I.pair || s == 1) tc_commit(&empty[st]);
+          };
+          issue_s(0, 0);
+          if (ns[1]) issue_s(1, 0);
+          if (ns[0] == 1) tc_commit(qempty);
+          for (int i = 0; ok && i < ns[0]; ++i) {
+            for (int s = 0; ok && s < 2; ++s) {
+              if (i >= ns[s]) continue;
+              const int j = I.pair ? i : 2 * i + s, t = I.t_hi - 1 - j;
+              const uint32_t cc = base + (I.pair ? 2 * j + 1 : j + min(n, j + 2)), st = cc % AT_STAGES;
+              if (!(ok = attn_wait(&full[st], (cc / AT_STAGES) & 1, status))) break;
+              if (attn_mixed(I, t)) bad |= badstage[2 * st] | badstage[2 * st + 1];
+              if (!(ok = attn_wait(&pfull[s], pc[s] & 1, status))) break;
+              ++pc[s];
+              tc_fence_after();
+              const uint32_t v0 = smem_u32(sm) + AT_OFF_KV + st * AT_TILE_BYTES;
+#pragma unroll
+              for (int kk = 0; kk < AT_TILE / 16; ++kk)
+                tc_mma_ta(tmem + 256 + 128 * s, tmem + 128 * s + 8 * kk, umma_desc_v(v0 + kk * 2048), ID_O,
+                          (i > 0 || kk > 0) ? 1u : 0u);
+              if (!I.pair || s == 1) tc_commit(&empty[st]);
+              if (i + 1 < ns[s]) {
+                issue_s(s, i + 1);
+                if (i + 1 == ns[0] - 1 && (s == 1 || ns[1] < ns[0])) tc_commit(qempty);
+              } else {
+                badslot[s] = bad;
+                tc_commit(&ofull[s]);
+                mbar_arrive(&ofull[s]);   // the thread's own arrival orders badslot before the reader
+              }
+            }
+          }
+          base += 2 * n;
+        }
+        // every MMA issued above has completed before the CTA leaves: the softmax warps wait for ofull
+      }
+    } else {   // ---- two warps that look over the values of partly masked tiles
+      const int w = warp - 10;
+      uint32_t base = 0, gc = 0;
+      bool ok = true;
+      for (int it = blockIdx.x; it < P.items; it += gridDim.x) {
+        const AttnItem I = attn_item(P, it);
+        for (int j = 0; j < I.n; ++j) {
+          const int t = I.t_hi - 1 - j;
+          if (!attn_mixed(I, t)) continue;
+          const uint32_t st = (base + (I.pair ? 2 * j + 1 : j + min(I.n, j + 2))) % AT_STAGES;
+          if (ok) ok = attn_wait(&gfull[gc % AT_STAGES], (gc / AT_STAGES) & 1, status);
+          ++gc;
+          uint8_t *v = sm + AT_OFF_KV + st * AT_TILE_BYTES;
+          bool bad = false, dirty = false;
+          for (int k = w * 4 + (lane >> 3); k < AT_TILE; k += 8) {   // eight lanes per key and half
+            const int key = t * AT_TILE + k;
+            if (key >= I.clean_lo && key < I.clean_hi) continue;
+#pragma unroll
+            for (int hf = 0; hf < 2; ++hf) {
+              uint32_t *p = reinterpret_cast<uint32_t *>(v + hf * AT_HALF_BYTES + k * 128 + (lane & 7) * 16);
+              const uint4 x = lds128(p);
+              const uint32_t wv[4] = {x.x, x.y, x.z, x.w};
+              constexpr uint32_t E = FP16 ? 0x7C00u : 0x7F80u;
+#pragma unroll
+              for (int q = 0; q < 4; ++q) {
+                const bool lo = (wv[q] & E) == E, hi = (wv[q] & (E << 16)) == (E << 16);
+                if (lo | hi) {
+                  p[q] = (lo ? 0u : wv[q] & 0xFFFFu) | (hi ? 0u : wv[q] & 0xFFFF0000u);
+                  dirty = true;
+                  bad |= key >= I.key_lo && key < I.key_hi;   // some row sees it
+                }
+              }
+            }
+          }
+          if (dirty) fence_proxy_async();   // the products read shared memory through the async proxy
+          const uint32_t any = __ballot_sync(0xffffffffu, bad);
+          if (lane == 0) badstage[2 * st + w] = any != 0;
+          asm volatile("bar.sync 3, 64;" ::: "memory");
+          if (w == 0 && lane == 0) mbar_arrive(&full[st]);
+          __syncwarp();
+        }
+        base += 2 * I.n;
+      }
+    }
+  } else {   // ---- softmax: slot = warpgroup, thread = row
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
+    const int slot = warp >> 2, wq = warp & 3, row = wq * 32 + lane;
+    const uint32_t lane_base = tmem + ((uint32_t)(wq * 32) << 16);
+    const uint32_t ts = lane_base + 128 * slot, to = lane_base + 256 + 128 * slot;
+    uint32_t sc = 0, oc = 0;
+    bool ok = true;   // after a wait that ran out the loops go on without waiting, so both slots meet at every barrier
+    for (int it = blockIdx.x; it < P.items; it += gridDim.x) {
+      const AttnItem I = attn_item(P, it);
+      const int n_s = I.pair ? I.n : (I.n + 1 - slot) >> 1;
+      int b, i, h;
+      const bool valid = attn_row(P, I, slot, row, b, i, h);
+      const bool any_row = __any_sync(0xffffffffu, valid);
+      int lo = 0, hi = 0;
+      float pos = 0.f, slope = 0.f;
+      if (valid) {
+        if (I.prefix) {
+          hi = P.pre;
+          if (BIAS) pos = (float)(P.pre + (P.kv_len ? clampi(P.kv_len[b], 0, P.s_kv) : P.s_kv) - P.s_q + i);
+        } else {
+          const int p = I.kl - I.ql + i;
+          const int2 v = attn_interval(P, b, p, I.kl);
+          lo = v.x, hi = v.y;
+          if (BIAS) pos = (float)p;
+        }
+        if (BIAS) slope = P.slopes[h] * 1.4426950408889634f;
+      }
+      // x = value * scale2 + off: the products themselves, or with BIAS the finished logit
+      const float scale2 = BIAS ? 1.f : CAP ? 2.f * P.cap_log2 : P.scale_log2;
+      float m = -INFINITY, l = 0.f;
+      for (int k = 0; k < n_s; ++k) {
+        const int t = I.t_hi - 1 - (I.pair ? k : 2 * k + slot), c0 = t * AT_TILE;
+        if (ok) ok = attn_wait(&sfull[slot], sc & 1, status);
+        ++sc;
+        __syncwarp();
+        tc_fence_after();
+        if (any_row) {
+          uint32_t raw[AT_TILE];
+          float *v = reinterpret_cast<float *>(raw);
+#pragma unroll
+          for (int q = 0; q < 4; ++q) tmem_ld32(ts + 32 * q, raw + 32 * q);
+          tmem_wait_ld();
+          if (CAP) {   // cap tanh(s / cap) = cap (1 + 2 r), r = -1 / (1 + 2^(2 log2e s / cap))
+#pragma unroll
+            for (int j = 0; j < AT_TILE; ++j) v[j] = rcp_approx(-1.f - ex2(v[j] * P.cap_in));
+          }
+          if (BIAS) {
+            const float d0 = pos - (float)c0;
+#pragma unroll
+            for (int j = 0; j < AT_TILE; ++j)
+              v[j] = fmaf(-slope, fabsf(d0 - (float)j), CAP ? fmaf(v[j], 2.f * P.cap_log2, 0.f) : v[j] * P.scale_log2);
+          }
+          const int a = lo - c0, z = hi - c0;   // the row sees columns [a, z)
+          if (__any_sync(0xffffffffu, a > 0 || z < AT_TILE)) {
+#pragma unroll
+            for (int j = 0; j < AT_TILE; ++j)
+              if (j < a || j >= z) v[j] = -INFINITY;
+          }
+          float x0 = v[0], x1 = v[1];
+#pragma unroll
+          for (int j = 2; j < AT_TILE - 2; j += 4) {
+            x0 = max3(x0, v[j], v[j + 1]);
+            x1 = max3(x1, v[j + 2], v[j + 3]);
+          }
+          x0 = max3(x0, v[AT_TILE - 2], v[AT_TILE - 1]);
+          const float mx = fmaxf(x0, x1) * scale2;
+          const bool grow = mx > m + 8.f;   // also the first finite max (m = -inf)
+          if (__any_sync(0xffffffffu, grow)) {
+            const float mn = fmaxf(m, mx), f = m == -INFINITY ? 0.f : ex2(m - mn);
+            m = mn;
+            l *= f;
+            if (k > 0) {
+#pragma unroll
+              for (int q = 0; q < 4; ++q) {
+                uint32_t o[32];
+                tmem_ld32(to + 32 * q, o);
+                tmem_wait_ld();
+#pragma unroll
+                for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
+                tmem_st16(to + 32 * q, o);
+                tmem_st16(to + 32 * q + 16, o + 16);
+              }
+            }
+          }
+          const float mu = m == -INFINITY ? 0.f : m;
+          float a0 = 0.f, a1 = 0.f, a2 = 0.f, a3 = 0.f;
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            uint32_t pk[16];
+#pragma unroll
+            for (int j = 0; j < 32; j += 4) {
+              const int jj = 32 * q + j;
+              float e0, e1, e2, e3;
+              fma2(e0, e1, v[jj], v[jj + 1], scale2, scale2, -mu, -mu);
+              fma2(e2, e3, v[jj + 2], v[jj + 3], scale2, scale2, -mu, -mu);
+              e0 = ex2(e0), e1 = ex2(e1), e2 = ex2(e2), e3 = ex2(e3);
+              add2(a0, a1, e0, e1);
+              add2(a2, a3, e2, e3);
+              pk[j / 2] = pack2<FP16>(e0, e1);
+              pk[j / 2 + 1] = pack2<FP16>(e2, e3);
+            }
+            tmem_st16(ts + 16 * q, pk);
+          }
+          l += (a0 + a1) + (a2 + a3);
+          tmem_wait_st();
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&pfull[slot]);
+      }
+      // ---- the item's rows are done
+      const float off = CAP ? P.cap_log2 : 0.f;   // of the base-2 logits
+      const int split = I.prefix ? P.ns + I.sp : I.sp;
+      bool bad = false;
+      if (n_s > 0) {
+        if (ok) ok = attn_wait(&ofull[slot], oc & 1, status);
+        ++oc;
+        bad = badslot[slot] != 0;
+        __syncwarp();
+        tc_fence_after();
+      }
+      // a single row tile: slot 0 joins its rows with slot 1's, which stand in the same lanes
+      const bool join = !I.pair && I.n > 1;
+      const bool writes = I.pair || slot == 0;
+      float m1 = -INFINITY, l1 = 0.f;
+      if (join) {
+        if (slot == 1) {
+          ml[row] = m;
+          ml[AT_TILE + row] = l;
+        }
+        tc_fence_before();
+        asm volatile("bar.sync 1, 256;" ::: "memory");
+        tc_fence_after();
+        if (slot == 0) {
+          m1 = ml[row];
+          l1 = ml[AT_TILE + row];
+          bad |= badslot[1] != 0;
+        }
+      }
+      if (writes && any_row) {
+        const float mm = fmaxf(m, m1), mu = mm == -INFINITY ? 0.f : mm;
+        const float w0 = ex2(m - mu), w1 = ex2(m1 - mu);
+        const float lt = l * w0 + l1 * w1;
+        const float inv = lt == 0.f ? 0.f : 1.f / lt;   // an empty row is 0
+        const float lse2 = lt == 0.f ? -INFINITY : mu + off + log2f(lt);
+        const int64_t prow = ((int64_t)b * P.s_q + i) * P.h_q + h;
+        if (!bad) {
+          if (valid) {
+            if (P.part_o)
+              P.part_l[split * P.rows + prow] = lse2;
+            else if (P.lse)
+              P.lse[prow] = lse2 * 0.69314718055994531f;
+          }
+          const bool have0 = n_s > 0;
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            uint32_t o[32];
+            float *of = reinterpret_cast<float *>(o);
+            __syncwarp();
+            if (have0) {
+              tmem_ld32(to + 32 * q, o);
+              if (join) {
+                uint32_t o1[32];
+                tmem_ld32(to + 128 + 32 * q, o1);
+                tmem_wait_ld();
+#pragma unroll
+                for (int j = 0; j < 32; ++j) of[j] = of[j] * w0 + __uint_as_float(o1[j]) * w1;
+              } else {
+                tmem_wait_ld();
+              }
+            }
+            const float sc_o = join ? inv : inv * w0;
+#pragma unroll
+            for (int j = 0; j < 32; ++j) of[j] = have0 && inv != 0.f ? of[j] * sc_o : 0.f;
+            if (valid) {
+              if (P.part_o) {
+                float4 *dst = reinterpret_cast<float4 *>(P.part_o + (split * P.rows + prow) * D + 32 * q);
+                if (lse2 != -INFINITY)
+#pragma unroll
+                  for (int j = 0; j < 8; ++j) dst[j] = make_float4(of[4 * j], of[4 * j + 1], of[4 * j + 2], of[4 * j + 3]);
+              } else {
+                uint4 *dst = reinterpret_cast<uint4 *>(static_cast<uint16_t *>(P.out) + b * P.so[0] + i * P.so[1] +
+                                                       h * P.so[2] + 32 * q);
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                  dst[j] = make_uint4(pack2<FP16>(of[8 * j], of[8 * j + 1]), pack2<FP16>(of[8 * j + 2], of[8 * j + 3]),
+                                      pack2<FP16>(of[8 * j + 4], of[8 * j + 5]), pack2<FP16>(of[8 * j + 6], of[8 * j + 7]));
+              }
+            }
+          }
+        } else {
+          attn_exact_rows<FP16>(P, I, slot, wq, lane, CAP,
+                                [&](int, int rb, int ri, int rh, const float (&acc)[4], float rm, float rl) {
+            const int64_t pr = ((int64_t)rb * P.s_q + ri) * P.h_q + rh;
+            const float ri_l = rl == 0.f ? 0.f : 1.f / rl;
+            const float ls = rl == 0.f ? -INFINITY : rm + log2f(rl);
+            const float o0 = rl == 0.f ? 0.f : acc[0] * ri_l, o1 = rl == 0.f ? 0.f : acc[1] * ri_l;
+            const float o2 = rl == 0.f ? 0.f : acc[2] * ri_l, o3 = rl == 0.f ? 0.f : acc[3] * ri_l;
+            if (P.part_o) {
+              if (lane == 0) P.part_l[split * P.rows + pr] = ls;
+              *reinterpret_cast<float4 *>(P.part_o + (split * P.rows + pr) * D + 4 * lane) = make_float4(o0, o1, o2, o3);
+            } else {
+              if (lane == 0 && P.lse) P.lse[pr] = ls * 0.69314718055994531f;
+              *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(P.out) + rb * P.so[0] + ri * P.so[1] + rh * P.so[2] +
+                                         4 * lane) = make_uint2(pack2<FP16>(o0, o1), pack2<FP16>(o2, o3));
+            }
+          });
+        }
+      }
+      if (join) {
+        tc_fence_before();
+        asm volatile("bar.sync 1, 256;" ::: "memory");   // slot 1 keeps its O until slot 0 has read it
+        tc_fence_after();
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 9) {
+    tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512) : "memory");
+  }
+}
+
+template <bool FP16>
+cudaError_t launch_attn_type(const AttnArgs &P, int grid, bool cap, bool bias, cudaStream_t s) {
+  static SmemOptIn o[4];
+  cudaError_t e;
+#define QV_ATTN(C, B)                                                         \
+  do {                                                                        \
+    e = o[2 * C + B].ensure(attn_kernel<FP16, C, B>, AT_SMEM);                \
+    if (e == cudaSuccess) {                                                   \
+      attn_kernel<FP16, C, B><<<grid, AT_THREADS, AT_SMEM, s>>>(P);           \
+      e = cudaGetLastError();                                                 \
+    }                                                                         \
+  } while (0)
+  if (cap && bias)
+    QV_ATTN(true, true);
+  else if (cap)
+    QV_ATTN(true, false);
+  else if (bias)
+    QV_ATTN(false, true);
+  else
+    QV_ATTN(false, false);
+#undef QV_ATTN
+  return e;
+}
+
+}  // namespace qv
