@@ -15,16 +15,19 @@ constexpr int AT_TILE = 128;                          // rows of a query tile, k
 constexpr int AT_STAGES = 5;                          // key / value tiles in flight
 constexpr int AT_TILE_BYTES = AT_TILE * D * 2;        // 32 KB: two 128-byte-swizzled halves of 64 channels
 constexpr int AT_HALF_BYTES = AT_TILE_BYTES / 2;
-constexpr int AT_THREADS = 384;                       // two softmax warpgroups, one of helper warps
+constexpr int AT_SOFT = 16;                           // softmax warps: eight per slot, four for each half of the columns
+constexpr int AT_THREADS = (AT_SOFT + 2) * 32;        // a TMA warp and an MMA warp (96 registers a thread)
+constexpr int AT_W_LOAD = AT_SOFT, AT_W_MMA = AT_SOFT + 1;
+constexpr int AT_COLS = AT_TILE / 2;                  // columns of S, and channels of O, per softmax thread
 constexpr int AT_OFF_KV = 2 * AT_TILE_BYTES;
-constexpr int AT_OFF_ML = AT_OFF_KV + AT_STAGES * AT_TILE_BYTES;   // [2][128] fp32: slot 1's m and l
-constexpr int AT_OFF_BAR = AT_OFF_ML + 2 * AT_TILE * 4;
-constexpr int AT_NBAR = 3 * AT_STAGES + 2 + 6;
+constexpr int AT_OFF_X = AT_OFF_KV + AT_STAGES * AT_TILE_BYTES;    // [2 slots][2 halves][128] fp32 exchange
+constexpr int AT_OFF_M = AT_OFF_X + 4 * AT_TILE * 4;               // [128] fp32: slot 1's maxima
+constexpr int AT_OFF_BAR = AT_OFF_M + AT_TILE * 4;
+constexpr int AT_NBAR = 2 * AT_STAGES + 2 + 6;
 constexpr int AT_OFF_MISC = AT_OFF_BAR + AT_NBAR * 8;              // tmem address, flags
-constexpr int AT_SMEM = 1024 + AT_OFF_MISC + 4 * (2 + 2 * AT_STAGES + 2);
+constexpr int AT_SMEM = AT_OFF_MISC + 16;
 static_assert(AT_SMEM <= 232448, "one CTA per SM");
-// launch: 384 threads x 168 registers; softmax warps take 216, helper warps give down to 72
-static_assert(256 * 216 + 128 * 72 <= 384 * 168, "register split");
+constexpr int AT_BAR_ALL = 1, AT_BAR_PAIR = 2;        // named barriers (pairs: 2 .. 9)
 
 struct AttnArgs {
   CUtensorMap tq, tk, tv;      // queries and own keys of each sequence
@@ -156,18 +159,24 @@ __device__ __forceinline__ bool attn_row(const AttnArgs &P, const AttnItem &I, i
   return tok < P.tpt && i < I.ql;
 }
 
-// Bounded wait on an mbarrier phase: as mbar_wait with a limit of 4 s, since a slot that recomputes rows on
-// the CUDA cores (attn_exact_rows) holds the others up for longer than the 200 ms of the other kernels.
+// Bounded wait on an mbarrier phase.  The limit is about 4 s (8e9 SM cycles), longer than the 200 ms of the other
+// kernels' waits, since a slot that recomputes rows on the CUDA cores (attn_exact_rows) holds the others up.  The
+// SM's own clock is read, and only now and then: a first read of the global timer costs more than a tile's wait.
 __device__ __forceinline__ bool attn_wait(uint64_t *bar, uint32_t parity, int *status) {
   if (mbar_try_wait(bar, parity)) return true;
-  const uint64_t t0 = globaltimer_ns();
+  const long long t0 = clock64();
   for (uint32_t it = 0;; ++it) {
     if (mbar_try_wait(bar, parity)) return true;
-    if ((it & 255u) == 255u && globaltimer_ns() - t0 > 4000000000ull) {
+    if ((it & 255u) == 255u && clock64() - t0 > 8000000000ll) {
       atomicOr(status, QV_ERR_TIMEOUT);
       return false;
     }
   }
+}
+
+// The same by a whole warp, one answer for all its lanes.
+__device__ __forceinline__ bool attn_wait_warp(uint64_t *bar, uint32_t parity, int *status) {
+  return __all_sync(0xffffffffu, attn_wait(bar, parity, status));
 }
 
 // ----------------------------------------------------------------------------- tensor memory and products
@@ -180,12 +189,44 @@ __device__ __forceinline__ void tma_load_4d_at(uint32_t dst, const CUtensorMap *
       "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(smem_u32(bar))
       : "memory");
 }
-// D (+)= A B with A in tensor memory
-__device__ __forceinline__ void tc_mma_ta(uint32_t tmem, uint32_t ta, uint64_t db, uint32_t idesc, uint32_t accumulate) {
+// The eight products (16 deep each) of one 128 x 128 x 128 tile, issued by one elected lane of a converged warp:
+// descriptors stay in uniform registers, where a lane-0 branch needs a vector-to-uniform move for every operand of
+// every instruction (about 80 cycles per product, more than the 64 that the tensor pipe takes).
+// S = Q K^T: both operands in shared memory, 64-channel halves 16 KB apart (descriptor units of 16 bytes).
+__device__ __forceinline__ void tc_mma_tile_ss(uint32_t tmem, uint64_t da, uint64_t db, uint32_t idesc) {
   asm volatile(
-      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
-      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}" ::"r"(tmem),
+      "{\n .reg .pred e, f, t;\n .reg .b64 a, b;\n elect.sync _|e, 0xffffffff;\n setp.ne.b32 f, 0, 0;\n setp.eq.b32 t, 0, 0;\n"
+      " @e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, f;\n"
+      " add.s64 a, %1, 2;\n add.s64 b, %2, 2;\n @e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, t;\n"
+      " add.s64 a, %1, 4;\n add.s64 b, %2, 4;\n @e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, t;\n"
+      " add.s64 a, %1, 6;\n add.s64 b, %2, 6;\n @e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, t;\n"
+      " add.s64 a, %1, 1024;\n add.s64 b, %2, 1024;\n @e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, t;\n"
+      " add.s64 a, %1, 1026;\n add.s64 b, %2, 1026;\n @e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, t;\n"
+      " add.s64 a, %1, 1028;\n add.s64 b, %2, 1028;\n @e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, t;\n"
+      " add.s64 a, %1, 1030;\n add.s64 b, %2, 1030;\n @e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, t;\n}" ::"r"(tmem),
+      "l"(da), "l"(db), "r"(idesc)
+      : "memory");
+}
+// O (+)= P V: P in tensor memory (8 columns per 16 keys; keys 64 .. 127 from column 64 on), 16 keys of V 2048 bytes apart
+__device__ __forceinline__ void tc_mma_tile_ts(uint32_t tmem, uint32_t ta, uint64_t db, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n .reg .pred e, f, t;\n .reg .b64 b;\n .reg .b32 a;\n elect.sync _|e, 0xffffffff;\n setp.ne.b32 f, %4, 0;\n setp.eq.b32 t, 0, 0;\n"
+      " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, f;\n"
+      " add.s32 a, %1, 8;\n add.s64 b, %2, 128;\n @e tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, t;\n"
+      " add.s32 a, %1, 16;\n add.s64 b, %2, 256;\n @e tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, t;\n"
+      " add.s32 a, %1, 24;\n add.s64 b, %2, 384;\n @e tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, t;\n"
+      " add.s32 a, %1, 64;\n add.s64 b, %2, 512;\n @e tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, t;\n"
+      " add.s32 a, %1, 72;\n add.s64 b, %2, 640;\n @e tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, t;\n"
+      " add.s32 a, %1, 80;\n add.s64 b, %2, 768;\n @e tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, t;\n"
+      " add.s32 a, %1, 88;\n add.s64 b, %2, 896;\n @e tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, t;\n}" ::"r"(tmem),
       "r"(ta), "l"(db), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+// tcgen05.commit by the same elected lane
+__device__ __forceinline__ void tc_commit_elect(uint64_t *bar) {
+  asm volatile(
+      "{\n .reg .pred e;\n elect.sync _|e, 0xffffffff;\n"
+      " @e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}" ::"r"(smem_u32(bar))
       : "memory");
 }
 // shared-memory descriptor of a value tile: [128 keys][64 channels] halves, channels contiguous (the N side of
@@ -205,6 +246,17 @@ __device__ __forceinline__ uint64_t umma_desc_v(uint32_t saddr) {
       "=r"((r)[(o) + 10]), "=r"((r)[(o) + 11]), "=r"((r)[(o) + 12]), "=r"((r)[(o) + 13]), "=r"((r)[(o) + 14]),        \
       "=r"((r)[(o) + 15])
 
+__device__ __forceinline__ void tmem_ld16(uint32_t addr, uint32_t *r) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : QV_W16(r, 0)
+      : "r"(addr));
+}
+__device__ __forceinline__ void tmem_st8(uint32_t addr, const uint32_t *r) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%8], {%0,%1,%2,%3,%4,%5,%6,%7};" ::"r"(r[0]), "r"(r[1]), "r"(r[2]),
+               "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(addr)
+               : "memory");
+}
 // 32 columns of this thread's lane; the caller waits (tmem_wait_ld) before it uses them
 __device__ __forceinline__ void tmem_ld32(uint32_t addr, uint32_t *r) {
   asm volatile(
@@ -244,6 +296,33 @@ __device__ __forceinline__ float2 unpack2(uint32_t v) {
 }
 
 // ----------------------------------------------------------------------------- rows with values that are not finite
+
+// The keys of tile t that not every row of the item sees: their values that are not finite become 0 in shared memory,
+// thread `who` of 256 taking half a key's channels.  Whether one of them is seen by some row.
+template <bool FP16>
+__device__ __forceinline__ bool attn_clean_values(const AttnItem &I, int t, uint8_t *v, int who) {
+  const int k = who >> 1, key = t * AT_TILE + k;
+  if (key >= I.clean_lo && key < I.clean_hi) return false;
+  constexpr uint32_t E = FP16 ? 0x7C00u : 0x7F80u;
+  uint32_t *p = reinterpret_cast<uint32_t *>(v + (who & 1) * AT_HALF_BYTES + k * 128);
+  bool found = false;
+#pragma unroll 2
+  for (int c = 0; c < 8; ++c) {
+    uint32_t *pc = p + ((c + k) & 7) * 4;   // neighbours start in other banks
+    const uint4 x = lds128(pc);
+    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const bool lo = (w[q] & E) == E, hi = (w[q] & (E << 16)) == (E << 16);
+      if (lo | hi) {
+        pc[q] = (lo ? 0u : w[q] & 0xFFFFu) | (hi ? 0u : w[q] & 0xFFFF0000u);
+        found = true;
+      }
+    }
+  }
+  if (found) fence_proxy_async();   // the product reads shared memory through the async proxy
+  return found && key >= I.key_lo && key < I.key_hi;
+}
 
 // The rows of one warp of a slot recomputed on the CUDA cores, every visible key of the item's own tiles in
 // turn and no masked value touched.  Reached when a value that some row of the item sees and another does not is an infinity or
@@ -326,11 +405,10 @@ __device__ __forceinline__ void attn_exact_rows(const AttnArgs &P, const AttnIte
 
 // ----------------------------------------------------------------------------- the kernel
 
-// One persistent CTA per SM.  Two softmax warpgroups (slots), each thread owning one row of its slot's
-// 128-row tile, and four helper warps: TMA loads, MMA issue, and two that look for values that are not
-// finite in partly masked tiles.  Rows of a tile are (token, query head of the group), so the group's heads share every key
+// One persistent CTA per SM.  Two slots of eight softmax warps, a thread owning one row and half of the columns
+// of its slot's 128-row tile, a TMA warp and an MMA warp.  Rows of a tile are (token, query head of the group), so the group's heads share every key
 // tile.  Tensor memory: S of slot s at columns 128 s, overwritten in place by the probabilities (16-bit, the A operand of
-// P V), O of slot s at 256 + 128 s.  The tensor pipe alternates between the slots: while slot 0 turns
+// P V; each half of the keys over its own half of S), O of slot s at 256 + 128 s.  The tensor pipe alternates between the slots: while slot 0 turns
 // S into P, it runs slot 1's products.
 // Key tiles are taken from the last to the first, so a causal row meets its diagonal, and a distance bias its largest
 // logits, first.  The running max moves only when a row's max has grown by more than 2^8 (then the warp rescales its
@@ -338,28 +416,31 @@ __device__ __forceinline__ void attn_exact_rows(const AttnArgs &P, const AttnIte
 // Every wait is bounded; the TMEM columns are released on every path.
 template <bool FP16, bool CAP, bool BIAS>
 __global__ void __launch_bounds__(AT_THREADS, 1) attn_kernel(const __grid_constant__ AttnArgs P) {
-  extern __shared__ uint8_t at_smem_raw[];
-  uint8_t *sm = at_smem_raw + ((1024 - (smem_u32(at_smem_raw) & 1023)) & 1023);   // swizzle atoms: 1024-aligned
+  extern __shared__ __align__(1024) uint8_t sm[];   // swizzle atoms: 1024-aligned
   uint64_t *bars = reinterpret_cast<uint64_t *>(sm + AT_OFF_BAR);
-  uint64_t *full = bars, *empty = full + AT_STAGES, *gfull = empty + AT_STAGES;
-  uint64_t *qfull = gfull + AT_STAGES, *qempty = qfull + 1;
+  uint64_t *full = bars, *empty = full + AT_STAGES, *qfull = empty + AT_STAGES, *qempty = qfull + 1;
   uint64_t *sfull = qempty + 1, *pfull = sfull + 2, *ofull = pfull + 2;
   uint32_t *misc = reinterpret_cast<uint32_t *>(sm + AT_OFF_MISC);
   uint32_t *tmem_slot = misc;
-  volatile uint32_t *badstage = misc + 2, *badslot = badstage + 2 * AT_STAGES;
-  float *ml = reinterpret_cast<float *>(sm + AT_OFF_ML);
+  volatile int *bad_item = reinterpret_cast<int *>(misc + 2);   // [item parity]: 1 + the item with values to recompute
+  float *xch = reinterpret_cast<float *>(sm + AT_OFF_X), *m_slot1 = reinterpret_cast<float *>(sm + AT_OFF_M);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   int *status = P.status;
+  if (smem_u32(sm) & 1023) {   // cannot be swizzled: nothing runs
+    if (threadIdx.x == 0) atomicOr(status, QV_ERR_STATE);
+    return;
+  }
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < AT_NBAR; ++i) {
       const uint64_t *p = &bars[i];
-      const bool four = p >= pfull && p < pfull + 2, two = p >= ofull && p < ofull + 2;
-      mbar_init(&bars[i], four ? 4 : two ? 2 : 1);
+      const bool soft = p >= pfull && p < pfull + 2, two = p >= ofull && p < ofull + 2;
+      mbar_init(&bars[i], soft ? AT_SOFT / 2 : two ? 2 : 1);
     }
     fence_mbar_init();
+    bad_item[0] = bad_item[1] = 0;
   }
-  if (warp == 9) {
+  if (warp == AT_W_MMA) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)), "r"(512)
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
@@ -369,13 +450,12 @@ __global__ void __launch_bounds__(AT_THREADS, 1) attn_kernel(const __grid_consta
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
 
-  if (warp >= 8) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
-    if (warp == 8) {
+  if (warp >= AT_SOFT) {
+    if (warp == AT_W_LOAD) {
       if (lane == 0) {   // ---- TMA loads
         const uint32_t qbytes = (uint32_t)(P.G * P.tpt) * 128u;   // half of a query tile
         const uint32_t qpbytes = (uint32_t)(P.G * P.s_q * P.nb) * 128u;
-        uint32_t c = 0, qc = 0, gc = 0;
+        uint32_t c = 0, qc = 0;
         bool ok = true;
         for (int it = blockIdx.x; ok && it < P.items; it += gridDim.x) {
           const AttnItem I = attn_item(P, it);
@@ -395,27 +475,24 @@ __global__ void __launch_bounds__(AT_THREADS, 1) attn_kernel(const __grid_consta
             tma_load_4d_at(dst + AT_HALF_BYTES, mq, 64, I.g * P.G, tok, bb, qfull);
           }
           ++qc;
-          auto load = [&](const CUtensorMap *map, int j, int bb, bool value) {
+          auto load = [&](const CUtensorMap *map, int j, int bb) {
             const uint32_t st = c % AT_STAGES;
             if (!ok || !(ok = attn_wait(&empty[st], ((c / AT_STAGES) & 1) ^ 1, status))) return;
             const uint32_t dst = smem_u32(sm) + AT_OFF_KV + st * AT_TILE_BYTES;
             const int t = I.t_hi - 1 - j;
-            // values of a partly masked tile reach the checking warps first, which then fill the stage's barrier
-            uint64_t *bar = &full[st];
-            if (value && attn_mixed(I, t)) bar = &gfull[gc++ % AT_STAGES];
-            mbar_arrive_expect_tx(bar, AT_TILE_BYTES);
-            tma_load_4d_at(dst, map, 0, I.g, t * AT_TILE, bb, bar);
-            tma_load_4d_at(dst + AT_HALF_BYTES, map, 64, I.g, t * AT_TILE, bb, bar);
+            mbar_arrive_expect_tx(&full[st], AT_TILE_BYTES);
+            tma_load_4d_at(dst, map, 0, I.g, t * AT_TILE, bb, &full[st]);
+            tma_load_4d_at(dst + AT_HALF_BYTES, map, 64, I.g, t * AT_TILE, bb, &full[st]);
             ++c;
           };
           const int bk = I.b * P.mul_k, bv = I.b * P.mul_v;
           // in the order of their last use: K0 V0 K1 V1 .. for a pair; K0 K1 V0 K2 V1 K3 .. otherwise
-          load(mk, 0, bk, false);
-          if (!I.pair && I.n > 1) load(mk, 1, bk, false);
+          load(mk, 0, bk);
+          if (!I.pair && I.n > 1) load(mk, 1, bk);
           for (int j = 0; ok && j < I.n; ++j) {
-            load(mv, j, bv, true);
+            load(mv, j, bv);
             const int jk = j + (I.pair ? 1 : 2);
-            if (jk < I.n) load(mk, jk, bk, false);
+            if (jk < I.n) load(mk, jk, bk);
           }
         }
         // copies still in flight land before the CTA leaves
@@ -423,8 +500,8 @@ __global__ void __launch_bounds__(AT_THREADS, 1) attn_kernel(const __grid_consta
           attn_wait(&full[i % AT_STAGES], (i / AT_STAGES) & 1, status);
         if (qc) attn_wait(qfull, (qc - 1) & 1, status);
       }
-    } else if (warp == 9) {
-      if (lane == 0) {   // ---- MMA issue
+    } else if (warp == AT_W_MMA) {
+      {   // ---- MMA issue, the whole warp in step
         constexpr uint32_t ab = FP16 ? 0u : 1u;
         constexpr uint32_t ID_S = (1u << 4) | (ab << 7) | (ab << 10) | ((uint32_t)(AT_TILE >> 3) << 17) |
                                   ((uint32_t)(AT_TILE >> 4) << 24);
@@ -435,50 +512,41 @@ __global__ void __launch_bounds__(AT_THREADS, 1) attn_kernel(const __grid_consta
           const AttnItem I = attn_item(P, it);
           if (I.n == 0) continue;
           const int n = I.n, ns[2] = {I.pair ? n : (n + 1) >> 1, I.pair ? n : n >> 1};
-          uint32_t bad = 0;
-          if (!(ok = attn_wait(qfull, qc & 1, status))) break;
+          if (!(ok = attn_wait_warp(qfull, qc & 1, status))) break;
           ++qc;
           auto issue_s = [&](int s, int i) {
             const int j = I.pair ? i : 2 * i + s;
             const uint32_t cc = base + (I.pair ? 2 * j : j < 2 ? j : 2 * j - 1), st = cc % AT_STAGES;
-            if (!ok || !(ok = attn_wait(&full[st], (cc / AT_STAGES) & 1, status))) return;
+            if (!ok || !(ok = attn_wait_warp(&full[st], (cc / AT_STAGES) & 1, status))) return;
             tc_fence_after();
             const uint32_t a0 = smem_u32(sm) + (I.pair ? s * AT_TILE_BYTES : 0);
             const uint32_t b0 = smem_u32(sm) + AT_OFF_KV + st * AT_TILE_BYTES;
-#pragma unroll
-            for (int kk = 0; kk < D / 16; ++kk) {
-              const uint32_t off = (kk >> 2) * AT_HALF_BYTES + (kk & 3) * 32;
-              tc_mma(tmem + 128 * s, umma_desc(a0 + off), umma_desc(b0 + off), ID_S, kk > 0 ? 1u : 0u);
-            }
-            tc_commit(&sfull[s]);
-            if (!I.pair || s == 1) tc_commit(&empty[st]);
+            tc_mma_tile_ss(tmem + 128 * s, umma_desc(a0), umma_desc(b0), ID_S);
+            tc_commit_elect(&sfull[s]);
+            if (!I.pair || s == 1) tc_commit_elect(&empty[st]);
           };
           issue_s(0, 0);
           if (ns[1]) issue_s(1, 0);
-          if (ns[0] == 1) tc_commit(qempty);
+          if (ns[0] == 1) tc_commit_elect(qempty);
           for (int i = 0; ok && i < ns[0]; ++i) {
             for (int s = 0; ok && s < 2; ++s) {
               if (i >= ns[s]) continue;
-              const int j = I.pair ? i : 2 * i + s, t = I.t_hi - 1 - j;
+              const int j = I.pair ? i : 2 * i + s;
               const uint32_t cc = base + (I.pair ? 2 * j + 1 : j + min(n, j + 2)), st = cc % AT_STAGES;
-              if (!(ok = attn_wait(&full[st], (cc / AT_STAGES) & 1, status))) break;
-              if (attn_mixed(I, t)) bad |= badstage[2 * st] | badstage[2 * st + 1];
-              if (!(ok = attn_wait(&pfull[s], pc[s] & 1, status))) break;
+              if (!(ok = attn_wait_warp(&full[st], (cc / AT_STAGES) & 1, status))) break;
+              if (!(ok = attn_wait_warp(&pfull[s], pc[s] & 1, status))) break;
               ++pc[s];
               tc_fence_after();
               const uint32_t v0 = smem_u32(sm) + AT_OFF_KV + st * AT_TILE_BYTES;
-#pragma unroll
-              for (int kk = 0; kk < AT_TILE / 16; ++kk)
-                tc_mma_ta(tmem + 256 + 128 * s, tmem + 128 * s + 8 * kk, umma_desc_v(v0 + kk * 2048), ID_O,
-                          (i > 0 || kk > 0) ? 1u : 0u);
-              if (!I.pair || s == 1) tc_commit(&empty[st]);
+              tc_mma_tile_ts(tmem + 256 + 128 * s, tmem + 128 * s, umma_desc_v(v0), ID_O, i > 0);
+              if (!I.pair || s == 1) tc_commit_elect(&empty[st]);
               if (i + 1 < ns[s]) {
                 issue_s(s, i + 1);
-                if (i + 1 == ns[0] - 1 && (s == 1 || ns[1] < ns[0])) tc_commit(qempty);
+                if (i + 1 == ns[0] - 1 && (s == 1 || ns[1] < ns[0])) tc_commit_elect(qempty);
               } else {
-                badslot[s] = bad;
-                tc_commit(&ofull[s]);
-                mbar_arrive(&ofull[s]);   // the thread's own arrival orders badslot before the reader
+                tc_commit_elect(&ofull[s]);
+                if (lane == 0) mbar_arrive(&ofull[s]);   // orders what the slots wrote (bad_item) before the reader
+                __syncwarp();
               }
             }
           }
@@ -486,64 +554,23 @@ __global__ void __launch_bounds__(AT_THREADS, 1) attn_kernel(const __grid_consta
         }
         // every MMA issued above has completed before the CTA leaves: the softmax warps wait for ofull
       }
-    } else {   // ---- two warps that look over the values of partly masked tiles
-      const int w = warp - 10;
-      uint32_t base = 0, gc = 0;
-      bool ok = true;
-      for (int it = blockIdx.x; it < P.items; it += gridDim.x) {
-        const AttnItem I = attn_item(P, it);
-        for (int j = 0; j < I.n; ++j) {
-          const int t = I.t_hi - 1 - j;
-          if (!attn_mixed(I, t)) continue;
-          const uint32_t st = (base + (I.pair ? 2 * j + 1 : j + min(I.n, j + 2))) % AT_STAGES;
-          if (ok) ok = attn_wait(&gfull[gc % AT_STAGES], (gc / AT_STAGES) & 1, status);
-          ++gc;
-          uint8_t *v = sm + AT_OFF_KV + st * AT_TILE_BYTES;
-          bool bad = false, dirty = false;
-          for (int k = w * 4 + (lane >> 3); k < AT_TILE; k += 8) {   // eight lanes per key and half
-            const int key = t * AT_TILE + k;
-            if (key >= I.clean_lo && key < I.clean_hi) continue;
-#pragma unroll
-            for (int hf = 0; hf < 2; ++hf) {
-              uint32_t *p = reinterpret_cast<uint32_t *>(v + hf * AT_HALF_BYTES + k * 128 + (lane & 7) * 16);
-              const uint4 x = lds128(p);
-              const uint32_t wv[4] = {x.x, x.y, x.z, x.w};
-              constexpr uint32_t E = FP16 ? 0x7C00u : 0x7F80u;
-#pragma unroll
-              for (int q = 0; q < 4; ++q) {
-                const bool lo = (wv[q] & E) == E, hi = (wv[q] & (E << 16)) == (E << 16);
-                if (lo | hi) {
-                  p[q] = (lo ? 0u : wv[q] & 0xFFFFu) | (hi ? 0u : wv[q] & 0xFFFF0000u);
-                  dirty = true;
-                  bad |= key >= I.key_lo && key < I.key_hi;   // some row sees it
-                }
-              }
-            }
-          }
-          if (dirty) fence_proxy_async();   // the products read shared memory through the async proxy
-          const uint32_t any = __ballot_sync(0xffffffffu, bad);
-          if (lane == 0) badstage[2 * st + w] = any != 0;
-          asm volatile("bar.sync 3, 64;" ::: "memory");
-          if (w == 0 && lane == 0) mbar_arrive(&full[st]);
-          __syncwarp();
-        }
-        base += 2 * I.n;
-      }
     }
-  } else {   // ---- softmax: slot = warpgroup, thread = row
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
-    const int slot = warp >> 2, wq = warp & 3, row = wq * 32 + lane;
+  } else {   // ---- softmax: thread = one row of the slot's tile, one half of its columns
+    const int slot = warp >> 3, half = (warp >> 2) & 1, wq = warp & 3, row = wq * 32 + lane;
     const uint32_t lane_base = tmem + ((uint32_t)(wq * 32) << 16);
-    const uint32_t ts = lane_base + 128 * slot, to = lane_base + 256 + 128 * slot;
-    uint32_t sc = 0, oc = 0;
-    bool ok = true;   // after a wait that ran out the loops go on without waiting, so both slots meet at every barrier
+    const uint32_t ts = lane_base + 128 * slot + AT_COLS * half;   // S, and its half of P
+    const uint32_t to = lane_base + 256 + 128 * slot + AT_COLS * half;
+    float *x_own = xch + (2 * slot + half) * AT_TILE + row, *x_other = xch + (2 * slot + (half ^ 1)) * AT_TILE + row;
+    const int pair_bar = AT_BAR_PAIR + 4 * slot + wq;   // the two warps that share these rows
+    uint32_t sc = 0, oc = 0, base = 0, seq = 0;
+    bool ok = true;   // after a wait that ran out the loops go on without waiting, so all warps meet at every barrier
     for (int it = blockIdx.x; it < P.items; it += gridDim.x) {
       const AttnItem I = attn_item(P, it);
       const int n_s = I.pair ? I.n : (I.n + 1 - slot) >> 1;
-      int b, i, h;
-      const bool valid = attn_row(P, I, slot, row, b, i, h);
+      int b, i, h, it_again = it;
+      bool valid = attn_row(P, I, slot, row, b, i, h);
       const bool any_row = __any_sync(0xffffffffu, valid);
-      int lo = 0, hi = 0;
+      int lo = 0, hi = 1 << 30;   // padding rows take no masks: nothing reads what they compute
       float pos = 0.f, slope = 0.f;
       if (valid) {
         if (I.prefix) {
@@ -557,117 +584,147 @@ __global__ void __launch_bounds__(AT_THREADS, 1) attn_kernel(const __grid_consta
         }
         if (BIAS) slope = P.slopes[h] * 1.4426950408889634f;
       }
-      // x = value * scale2 + off: the products themselves, or with BIAS the finished logit
+      // x = value * scale2: the products themselves, or with BIAS the finished logit
       const float scale2 = BIAS ? 1.f : CAP ? 2.f * P.cap_log2 : P.scale_log2;
       float m = -INFINITY, l = 0.f;
       for (int k = 0; k < n_s; ++k) {
-        const int t = I.t_hi - 1 - (I.pair ? k : 2 * k + slot), c0 = t * AT_TILE;
+        const int t = I.t_hi - 1 - (I.pair ? k : 2 * k + slot), c0 = t * AT_TILE + half * AT_COLS;
         if (ok) ok = attn_wait(&sfull[slot], sc & 1, status);
         ++sc;
         __syncwarp();
         tc_fence_after();
         if (any_row) {
-          uint32_t raw[AT_TILE];
-          float *v = reinterpret_cast<float *>(raw);
-#pragma unroll
-          for (int q = 0; q < 4; ++q) tmem_ld32(ts + 32 * q, raw + 32 * q);
-          tmem_wait_ld();
-          if (CAP) {   // cap tanh(s / cap) = cap (1 + 2 r), r = -1 / (1 + 2^(2 log2e s / cap))
-#pragma unroll
-            for (int j = 0; j < AT_TILE; ++j) v[j] = rcp_approx(-1.f - ex2(v[j] * P.cap_in));
-          }
-          if (BIAS) {
-            const float d0 = pos - (float)c0;
-#pragma unroll
-            for (int j = 0; j < AT_TILE; ++j)
-              v[j] = fmaf(-slope, fabsf(d0 - (float)j), CAP ? fmaf(v[j], 2.f * P.cap_log2, 0.f) : v[j] * P.scale_log2);
-          }
+          // Two passes over S, which stays in tensor memory: the maximum first, then the probabilities 16 columns at a
+          // time.  Holding the 64 values of a row in registers between them spills at 96 registers a thread.
+          float x0 = -INFINITY, x1 = -INFINITY;
           const int a = lo - c0, z = hi - c0;   // the row sees columns [a, z)
-          if (__any_sync(0xffffffffu, a > 0 || z < AT_TILE)) {
+          const bool masked = __any_sync(0xffffffffu, a > 0 || z < AT_COLS);
 #pragma unroll
-            for (int j = 0; j < AT_TILE; ++j)
-              if (j < a || j >= z) v[j] = -INFINITY;
-          }
-          float x0 = v[0], x1 = v[1];
+          for (int q = 0; q < 2; ++q) {
+            uint32_t raw[32];
+            float *v = reinterpret_cast<float *>(raw);
+            tmem_ld32(ts + 32 * q, raw);
+            tmem_wait_ld();
+            if (CAP) {   // cap tanh(s / cap) = cap (1 + 2 r), r = -1 / (1 + 2^(2 log2e s / cap))
 #pragma unroll
-          for (int j = 2; j < AT_TILE - 2; j += 4) {
-            x0 = max3(x0, v[j], v[j + 1]);
-            x1 = max3(x1, v[j + 2], v[j + 3]);
+              for (int j = 0; j < 32; ++j) v[j] = rcp_approx(-1.f - ex2(v[j] * P.cap_in));
+            }
+            if (BIAS) {
+              const float d0 = pos - (float)(c0 + 32 * q), sl = CAP ? 2.f * P.cap_log2 : P.scale_log2;
+#pragma unroll
+              for (int j = 0; j < 32; ++j) v[j] = fmaf(-slope, fabsf(d0 - (float)j), v[j] * sl);
+            }
+            if (masked) {
+#pragma unroll
+              for (int j = 0; j < 32; ++j)
+                if (32 * q + j < a || 32 * q + j >= z) v[j] = -INFINITY;
+            }
+            if (CAP || BIAS || masked) {   // the second pass reads the finished logits
+              tmem_st16(ts + 32 * q, raw);
+              tmem_st16(ts + 32 * q + 16, raw + 16);
+            }
+#pragma unroll
+            for (int j = 0; j < 32; j += 4) {
+              x0 = max3(x0, v[j], v[j + 1]);
+              x1 = max3(x1, v[j + 2], v[j + 3]);
+            }
           }
-          x0 = max3(x0, v[AT_TILE - 2], v[AT_TILE - 1]);
+          if (CAP || BIAS || masked) tmem_wait_st();
           const float mx = fmaxf(x0, x1) * scale2;
           const bool grow = mx > m + 8.f;   // also the first finite max (m = -inf)
-          if (__any_sync(0xffffffffu, grow)) {
-            const float mn = fmaxf(m, mx), f = m == -INFINITY ? 0.f : ex2(m - mn);
-            m = mn;
+          int any;   // one barrier of the two warps: whether a row of either has grown
+          asm volatile(
+              "{\n .reg .pred p, q;\n setp.ne.s32 p, %1, 0;\n barrier.cta.red.or.aligned.pred q, %2, 64, p;\n selp.s32 %0, 1, 0, q;\n}"
+              : "=r"(any)
+              : "r"((int)grow), "r"(pair_bar)
+              : "memory");
+          if (any) {
+            *x_own = mx;
+            asm volatile("bar.sync %0, 64;" ::"r"(pair_bar) : "memory");
+            const float both = fmaxf(mx, *x_other);
+            float f = 1.f;
+            if (both > m + 8.f) {
+              f = m == -INFINITY ? 0.f : ex2(m - both);
+              m = both;
+            }
             l *= f;
             if (k > 0) {
 #pragma unroll
               for (int q = 0; q < 4; ++q) {
-                uint32_t o[32];
-                tmem_ld32(to + 32 * q, o);
+                uint32_t o[16];
+                tmem_ld16(to + 16 * q, o);
                 tmem_wait_ld();
 #pragma unroll
-                for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
-                tmem_st16(to + 32 * q, o);
-                tmem_st16(to + 32 * q + 16, o + 16);
+                for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
+                tmem_st16(to + 16 * q, o);
               }
             }
           }
           const float mu = m == -INFINITY ? 0.f : m;
           float a0 = 0.f, a1 = 0.f, a2 = 0.f, a3 = 0.f;
+          uint32_t buf[2][16];
+          tmem_ld16(ts, buf[0]);
 #pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            uint32_t pk[16];
+          for (int q = 0; q < 4; ++q) {   // the next 16 columns are on their way while these are worked on
+            const float *v = reinterpret_cast<const float *>(buf[q & 1]);
+            tmem_wait_ld();
+            if (q < 3) tmem_ld16(ts + 16 * (q + 1), buf[(q + 1) & 1]);
+            uint32_t pk[8];
 #pragma unroll
-            for (int j = 0; j < 32; j += 4) {
-              const int jj = 32 * q + j;
+            for (int j = 0; j < 16; j += 4) {
               float e0, e1, e2, e3;
-              fma2(e0, e1, v[jj], v[jj + 1], scale2, scale2, -mu, -mu);
-              fma2(e2, e3, v[jj + 2], v[jj + 3], scale2, scale2, -mu, -mu);
+              fma2(e0, e1, v[j], v[j + 1], scale2, scale2, -mu, -mu);
+              fma2(e2, e3, v[j + 2], v[j + 3], scale2, scale2, -mu, -mu);
               e0 = ex2(e0), e1 = ex2(e1), e2 = ex2(e2), e3 = ex2(e3);
               add2(a0, a1, e0, e1);
               add2(a2, a3, e2, e3);
               pk[j / 2] = pack2<FP16>(e0, e1);
               pk[j / 2 + 1] = pack2<FP16>(e2, e3);
             }
-            tmem_st16(ts + 16 * q, pk);
+            tmem_st8(ts + 8 * q, pk);   // over columns already read
           }
           l += (a0 + a1) + (a2 + a3);
           tmem_wait_st();
+        }
+        if (attn_mixed(I, t) && (!I.pair || slot == 0)) {   // slot 1's product comes after slot 0's
+          const int j = I.pair ? k : 2 * k + slot;
+          const uint32_t cc = base + (I.pair ? 2 * j + 1 : j + min(I.n, j + 2)), st = cc % AT_STAGES;
+          if (ok) ok = attn_wait(&full[st], (cc / AT_STAGES) & 1, status);
+          if (attn_clean_values<FP16>(I, t, sm + AT_OFF_KV + st * AT_TILE_BYTES, threadIdx.x & 255)) bad_item[seq & 1] = it + 1;
         }
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&pfull[slot]);
       }
-      // ---- the item's rows are done
+      // ---- the item's rows are done (what the loop does not need is worked out again: it would only fill registers)
+      asm volatile("" : "+r"(it_again));
+      const AttnItem E = attn_item(P, it_again);
+      valid = attn_row(P, E, slot, row, b, i, h);
       const float off = CAP ? P.cap_log2 : 0.f;   // of the base-2 logits
-      const int split = I.prefix ? P.ns + I.sp : I.sp;
-      bool bad = false;
-      if (n_s > 0) {
-        if (ok) ok = attn_wait(&ofull[slot], oc & 1, status);
-        ++oc;
-        bad = badslot[slot] != 0;
-        __syncwarp();
-        tc_fence_after();
-      }
+      const int split = E.prefix ? P.ns + E.sp : E.sp;
       // a single row tile: slot 0 joins its rows with slot 1's, which stand in the same lanes
       const bool join = !I.pair && I.n > 1;
       const bool writes = I.pair || slot == 0;
+      bool bad = false;
       float m1 = -INFINITY, l1 = 0.f;
-      if (join) {
-        if (slot == 1) {
-          ml[row] = m;
-          ml[AT_TILE + row] = l;
-        }
+      if (n_s > 0) {
+        if (ok) ok = attn_wait(&ofull[slot], oc & 1, status);
+        ++oc;
+        *x_own = l;
+        if (slot == 1 && half == 0) m_slot1[row] = m;
         tc_fence_before();
-        asm volatile("bar.sync 1, 256;" ::: "memory");
+        __syncwarp();
+        if (join)
+          asm volatile("bar.sync %0, %1;" ::"r"(AT_BAR_ALL), "r"(AT_SOFT * 32) : "memory");
+        else
+          asm volatile("bar.sync %0, 64;" ::"r"(pair_bar) : "memory");
         tc_fence_after();
-        if (slot == 0) {
-          m1 = ml[row];
-          l1 = ml[AT_TILE + row];
-          bad |= badslot[1] != 0;
+        l = xch[2 * slot * AT_TILE + row] + xch[(2 * slot + 1) * AT_TILE + row];
+        if (join && slot == 0) {
+          m1 = m_slot1[row];
+          l1 = xch[2 * AT_TILE + row] + xch[3 * AT_TILE + row];
         }
+        bad = bad_item[seq & 1] == it + 1;
       }
       if (writes && any_row) {
         const float mm = fmaxf(m, m1), mu = mm == -INFINITY ? 0.f : mm;
@@ -677,51 +734,55 @@ __global__ void __launch_bounds__(AT_THREADS, 1) attn_kernel(const __grid_consta
         const float lse2 = lt == 0.f ? -INFINITY : mu + off + log2f(lt);
         const int64_t prow = ((int64_t)b * P.s_q + i) * P.h_q + h;
         if (!bad) {
-          if (valid) {
+          if (valid && half == 0) {
             if (P.part_o)
               P.part_l[split * P.rows + prow] = lse2;
             else if (P.lse)
               P.lse[prow] = lse2 * 0.69314718055994531f;
           }
           const bool have0 = n_s > 0;
+          const float f0 = w0 * inv, f1 = w1 * inv;
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
-            uint32_t o[32];
+            uint32_t o[16];
             float *of = reinterpret_cast<float *>(o);
             __syncwarp();
             if (have0) {
-              tmem_ld32(to + 32 * q, o);
+              tmem_ld16(to + 16 * q, o);
               if (join) {
-                uint32_t o1[32];
-                tmem_ld32(to + 128 + 32 * q, o1);
+                uint32_t o1[16];
+                tmem_ld16(to + 128 + 16 * q, o1);
                 tmem_wait_ld();
 #pragma unroll
-                for (int j = 0; j < 32; ++j) of[j] = of[j] * w0 + __uint_as_float(o1[j]) * w1;
+                for (int j = 0; j < 16; ++j) of[j] = of[j] * f0 + __uint_as_float(o1[j]) * f1;
               } else {
                 tmem_wait_ld();
+#pragma unroll
+                for (int j = 0; j < 16; ++j) of[j] = of[j] * f0;
               }
             }
-            const float sc_o = join ? inv : inv * w0;
+            if (!have0 || inv == 0.f) {
 #pragma unroll
-            for (int j = 0; j < 32; ++j) of[j] = have0 && inv != 0.f ? of[j] * sc_o : 0.f;
+              for (int j = 0; j < 16; ++j) of[j] = 0.f;
+            }
             if (valid) {
               if (P.part_o) {
-                float4 *dst = reinterpret_cast<float4 *>(P.part_o + (split * P.rows + prow) * D + 32 * q);
+                float4 *dst = reinterpret_cast<float4 *>(P.part_o + (split * P.rows + prow) * D + AT_COLS * half + 16 * q);
                 if (lse2 != -INFINITY)
 #pragma unroll
-                  for (int j = 0; j < 8; ++j) dst[j] = make_float4(of[4 * j], of[4 * j + 1], of[4 * j + 2], of[4 * j + 3]);
+                  for (int j = 0; j < 4; ++j) dst[j] = make_float4(of[4 * j], of[4 * j + 1], of[4 * j + 2], of[4 * j + 3]);
               } else {
                 uint4 *dst = reinterpret_cast<uint4 *>(static_cast<uint16_t *>(P.out) + b * P.so[0] + i * P.so[1] +
-                                                       h * P.so[2] + 32 * q);
+                                                       h * P.so[2] + AT_COLS * half + 16 * q);
 #pragma unroll
-                for (int j = 0; j < 4; ++j)
+                for (int j = 0; j < 2; ++j)
                   dst[j] = make_uint4(pack2<FP16>(of[8 * j], of[8 * j + 1]), pack2<FP16>(of[8 * j + 2], of[8 * j + 3]),
                                       pack2<FP16>(of[8 * j + 4], of[8 * j + 5]), pack2<FP16>(of[8 * j + 6], of[8 * j + 7]));
               }
             }
           }
-        } else {
-          attn_exact_rows<FP16>(P, I, slot, wq, lane, CAP,
+        } else if (half == 0) {
+          attn_exact_rows<FP16>(P, E, slot, wq, lane, CAP,
                                 [&](int, int rb, int ri, int rh, const float (&acc)[4], float rm, float rl) {
             const int64_t pr = ((int64_t)rb * P.s_q + ri) * P.h_q + rh;
             const float ri_l = rl == 0.f ? 0.f : 1.f / rl;
@@ -741,14 +802,17 @@ __global__ void __launch_bounds__(AT_THREADS, 1) attn_kernel(const __grid_consta
       }
       if (join) {
         tc_fence_before();
-        asm volatile("bar.sync 1, 256;" ::: "memory");   // slot 1 keeps its O until slot 0 has read it
+        __syncwarp();
+        asm volatile("bar.sync %0, %1;" ::"r"(AT_BAR_ALL), "r"(AT_SOFT * 32) : "memory");   // slot 1 keeps its O until it has been read
         tc_fence_after();
       }
+      base += 2 * I.n;
+      ++seq;
     }
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == 9) {
+  if (warp == AT_W_MMA) {
     tc_fence_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512) : "memory");
   }
