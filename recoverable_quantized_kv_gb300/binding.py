@@ -407,33 +407,54 @@ def _tensor(t, where, name, shape, dtype, device, dense=False):
         _need(t.shape[-1] == 1 or t.stride(-1) == 1, where, f"{name}'s channels must be contiguous")
 
 
-class _on:
-    """The device and stream of a call: makes the device current, and tells the allocator about tensors that
-    are used on a stream other than the device's current one."""
-
-    def __init__(self, device, stream, tensors=()):
-        import torch
-        self.guard = torch.cuda.device(device)
-        self.device, self.stream, self.tensors = device, stream, tensors
-
-    def __enter__(self):
-        import torch
-        self.guard.__enter__()
-        cur = torch.cuda.current_stream(self.device)
-        if self.stream is None or self.stream == cur:
-            return cur.cuda_stream
-        for t in self.tensors:
+def _enter(device_index, stream, tensors):
+    """The raw stream of a call on a device, and the device to make current for it (None: it is).  Tensors used on
+    another stream than the device's current one are made known to the allocator."""
+    import torch
+    other = None if torch.cuda.current_device() == device_index else torch.device("cuda", device_index)
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(device_index), other
+    if stream != torch.cuda.current_stream(device_index):
+        for t in tensors:
             if t is not None:
-                t.record_stream(self.stream)
-        return self.stream.cuda_stream
+                t.record_stream(stream)
+    return stream.cuda_stream, other
 
-    def __exit__(self, *exc):
-        return self.guard.__exit__(*exc)
+
+def _call(name, other, args):
+    """One C call, with the call's device current."""
+    if other is None:
+        st = getattr(load(), name)(*args)
+    else:
+        import torch
+        with torch.cuda.device(other):
+            st = getattr(load(), name)(*args)
+    if st != OK:
+        _check(st, name)
+
+
+def _torch():
+    import torch
+    return torch
+
+
+def _array(where, name, t, shape, dtype, index):
+    """Address of a dense device array of this shape and dtype; None stays None."""
+    if t is None:
+        return None
+    if not (t.dtype is dtype and t.get_device() == index and t.shape == shape and t.is_contiguous()):
+        _tensor(t, where, name, shape, dtype, _torch().device("cuda", index), dense=True)
+    return t.data_ptr()
+
+
+def _fits(t, shape, dtype, index):
+    """Fast form of _tensor's checks for the common case: true when they all hold."""
+    return t.dtype is dtype and t.get_device() == index and t.shape == shape and t.stride(-1) == 1
 
 
 def _ops_status(word, where, stream):
-    with _on(word.device, stream) as s:
-        _check(load().qevict_ops_status(_ptr(word), None, s), where)
+    s, other = _enter(word.get_device(), stream, (word,))
+    _call("qevict_ops_status", other, (word.data_ptr(), None, s))
 
 
 def _rope_config(rot_dim, base, scaling, factor, orig_len, low, high):
@@ -458,13 +479,15 @@ def rope_table(rows, rot_dim=128, base=10000.0, scaling="none", factor=1.0, orig
     cfg = _rope_config(rot_dim, base, scaling, factor, orig_len, low, high)
     rows = int(rows)
     _need(rows >= 1 and cfg.rot_dim >= 2 and cfg.rot_dim % 2 == 0, "rope_table", "rows and an even rot_dim of at least 2")
+    shape = (rows, cfg.rot_dim // 2, 2)
     if out is None:
         rope_angles(rot_dim, base, scaling, factor, orig_len, low, high)   # refuses before anything is allocated
         with torch.cuda.device(device), torch.cuda.stream(stream):
-            out = torch.empty(rows, cfg.rot_dim // 2, 2, dtype=torch.float32, device=device)
-    _tensor(out, "rope_table", "out", (rows, cfg.rot_dim // 2, 2), torch.float32, out.device, dense=True)
-    with _on(out.device, stream, (out,)) as s:
-        _check(load().qevict_rope_table(ctypes.byref(cfg), int(first), rows, _ptr(out), s), "qevict_rope_table")
+            out = torch.empty(shape, dtype=torch.float32, device=device)
+    if not (out.is_cuda and out.dtype is torch.float32 and out.shape == shape and out.is_contiguous()):
+        _tensor(out, "rope_table", "out", shape, torch.float32, out.device, dense=True)
+    s, other = _enter(out.get_device(), stream, (out,))
+    _call("qevict_rope_table", other, (ctypes.byref(cfg), int(first), rows, out.data_ptr(), s))
     return out
 
 
@@ -477,7 +500,9 @@ class Rope:
         _need(table.dim() == 3 and table.shape[2] == 2, "Rope", "table must have shape [rows][rot_dim / 2][2]")
         _tensor(table, "Rope", "table", table.shape, torch.float32, table.device, dense=True)
         self.table = table
+        self.index = table.get_device()
         self.status = torch.zeros(1, dtype=torch.int32, device=table.device)
+        self._table_ptr, self._status_ptr, self._descs = table.data_ptr(), self.status.data_ptr(), {}
 
     def apply(self, q, k=None, positions=None, pos0=0, interleaved=False, inverse=False, factor=1.0, q_out=None,
               k_out=None, stream=None):
@@ -485,35 +510,59 @@ class Rope:
         (q_out=q rotates in place).  positions: int32 [batch][seq], default pos0 + t.  inverse=True rotates back
         and, with the same factor, is the gradient of the forward call.  Tokens whose position is outside the
         table are not written; check() reports them."""
+        index = self.index
+        if k is None:
+            _need(k_out is None, "Rope.apply", "k_out without k")
+        if q_out is None or (k_out is None and k is not None):
+            q_out, k_out = self._outputs(q, k, q_out, k_out, stream)
+        key = (q.dtype, q.shape, q.stride(), q_out.stride(), interleaved, inverse, factor, pos0) if k is None else \
+            (q.dtype, q.shape, q.stride(), q_out.stride(), interleaved, inverse, factor, pos0, k.shape, k.stride(),
+             k_out.stride())
+        desc = self._descs.get(key)
+        if desc is None:
+            desc = self._desc(key, q, k, q_out, k_out, interleaved, inverse, factor, pos0)
+        dt, shape = q.dtype, q.shape
+        if not (q.get_device() == index and _fits(q_out, shape, dt, index)):
+            _tensor(q, "Rope.apply", "q", shape, dt, self.table.device)
+            _tensor(q_out, "Rope.apply", "q_out", shape, dt, self.table.device)
+        if k is not None and not (_fits(k, k.shape, dt, index) and _fits(k_out, k.shape, dt, index)):
+            _tensor(k, "Rope.apply", "k", k.shape, dt, self.table.device)
+            _tensor(k_out, "Rope.apply", "k_out", k.shape, dt, self.table.device)
+        if positions is not None:
+            _array("Rope.apply", "positions", positions, shape[:2], _torch().int32, index)
+        st, other = _enter(index, stream, (q, k, q_out, k_out, positions, self.table, self.status))
+        _call("qevict_rope_apply", other,
+              (desc, self._table_ptr, None if positions is None else positions.data_ptr(), q.data_ptr(), q_out.data_ptr(),
+               None if k is None else k.data_ptr(), None if k is None else k_out.data_ptr(), self._status_ptr, st))
+        return q_out, k_out
+
+    def _outputs(self, q, k, q_out, k_out, stream):
         import torch
-        where = "Rope.apply"
-        dev = self.table.device
+        with torch.cuda.device(self.table.device), torch.cuda.stream(stream):
+            if q_out is None:
+                q_out = torch.empty(q.shape, dtype=q.dtype, device=self.table.device)
+            if k is not None and k_out is None:
+                k_out = torch.empty(k.shape, dtype=k.dtype, device=self.table.device)
+        return q_out, k_out
+
+    def _desc(self, key, q, k, q_out, k_out, interleaved, inverse, factor, pos0):
+        """Descriptor of calls with these shapes and strides, kept for the next one."""
+        where, dev = "Rope.apply", self.table.device
         _need(q.dim() == 4 and (k is None or k.dim() == 4), where, "q and k must be [batch][seq][heads][d]")
         b, s, hq, d = q.shape
         _tensor(q, where, "q", q.shape, q.dtype, dev)
-        if k is not None:
-            _tensor(k, where, "k", (b, s, k.shape[2], d), q.dtype, dev)
-        if positions is not None:
-            _tensor(positions, where, "positions", (b, s), torch.int32, dev, dense=True)
-        _need(k is not None or k_out is None, where, "k_out without k")
-        outs = []
-        for name, x, o in (("q_out", q, q_out), ("k_out", k, k_out)):
-            if o is None and x is not None:
-                with torch.cuda.device(dev), torch.cuda.stream(stream):
-                    o = torch.empty(x.shape, dtype=x.dtype, device=dev)
-            if o is not None:
-                _tensor(o, where, name, x.shape, x.dtype, dev)
-            outs.append(o)
+        _tensor(q_out, where, "q_out", q.shape, q.dtype, dev)
         desc = RopeDesc(_dtype_code(q.dtype, where, (0, 1, 2)), b, s, hq, 0 if k is None else k.shape[2], d,
                         2 * self.table.shape[1], int(bool(interleaved)), int(bool(inverse)), float(factor),
-                        self.table.shape[0], int(pos0), _Stride3(*q.stride()[:3]), _Stride3(*outs[0].stride()[:3]))
+                        self.table.shape[0], int(pos0), _Stride3(*q.stride()[:3]), _Stride3(*q_out.stride()[:3]))
         if k is not None:
-            desc.k_in, desc.k_out = _Stride3(*k.stride()[:3]), _Stride3(*outs[1].stride()[:3])
-        with _on(dev, stream, (q, k, positions, self.table, self.status, *outs)) as st:
-            _check(load().qevict_rope_apply(ctypes.byref(desc), _ptr(self.table), _ptr(positions), _ptr(q),
-                                            _ptr(outs[0]), _ptr(k), _ptr(outs[1]), _ptr(self.status), st),
-                   "qevict_rope_apply")
-        return outs[0], outs[1]
+            _tensor(k, where, "k", (b, s, k.shape[2], d), q.dtype, dev)
+            _tensor(k_out, where, "k_out", k.shape, q.dtype, dev)
+            desc.k_in, desc.k_out = _Stride3(*k.stride()[:3]), _Stride3(*k_out.stride()[:3])
+        if len(self._descs) > 64:
+            self._descs.clear()
+        self._descs[key] = ctypes.byref(desc)
+        return self._descs[key]
 
     def check(self, stream=None):
         """Raises EDEVICE if a call since the last check met a position outside the table (synchronises)."""
@@ -541,29 +590,40 @@ class _AttnPlan:
         import torch
         self.work = torch.empty(nbytes, dtype=torch.uint8, device=self.device)
         self.work[:256].zero_()
-
-    def _tensors(self, where, q, k, v, out, lse, stream):
-        import torch
         d = self.desc
-        q_shape, kv_shape = (d.batch, d.s_q, d.h_q, 128), (d.batch, d.s_kv, d.h_kv, 128)
-        _tensor(q, where, "q", q_shape, self.dtype, self.device)
-        _tensor(k, where, "k", kv_shape, self.dtype, self.device)
-        _tensor(v, where, "v", kv_shape, self.dtype, self.device)
-        with torch.cuda.device(self.device), torch.cuda.stream(stream):
-            if out is None:
-                out = torch.empty(q_shape, dtype=self.dtype, device=self.device)
-            if lse is None:
-                lse = torch.empty(q_shape[:3], dtype=torch.float32, device=self.device)
-        _tensor(out, where, "out", q_shape, self.dtype, self.device)
-        _tensor(lse, where, "lse", q_shape[:3], torch.float32, self.device, dense=True)
-        desc = type(d).from_buffer_copy(d)   # a call's strides are its own
-        desc.q, desc.k, desc.v, desc.o = (_Stride3(*t.stride()[:3]) for t in (q, k, v, out))
+        self.index, self._descs = self.work.get_device(), {}
+        self._work = (self.work.data_ptr(), nbytes)
+        self.q_shape, self.kv_shape = (d.batch, d.s_q, d.h_q, 128), (d.batch, d.s_kv, d.h_kv, 128)
+
+    def _tensors(self, where, q, k, v, out, lse, stream, strides=()):
+        """Checks a call's tensors, makes the outputs that were not given; the descriptor with the call's strides (kept for
+        the next call of the same strides)."""
+        dt, i = self.dtype, self.index
+        if out is None or lse is None:
+            import torch
+            with torch.cuda.device(self.device), torch.cuda.stream(stream):
+                if out is None:
+                    out = torch.empty(self.q_shape, dtype=dt, device=self.device)
+                if lse is None:
+                    lse = torch.empty(self.q_shape[:3], dtype=torch.float32, device=self.device)
+        if not (_fits(q, self.q_shape, dt, i) and _fits(k, self.kv_shape, dt, i) and _fits(v, self.kv_shape, dt, i) and
+                _fits(out, self.q_shape, dt, i)):
+            for name, t, shape in (("q", q, self.q_shape), ("k", k, self.kv_shape), ("v", v, self.kv_shape),
+                                   ("out", out, self.q_shape)):
+                _tensor(t, where, name, shape, dt, self.device)
+        _array(where, "lse", lse, self.q_shape[:3], _torch().float32, i)
+        key = (q.stride(), k.stride(), v.stride(), out.stride()) + strides
+        desc = self._descs.get(key)
+        if desc is None:
+            if len(self._descs) > 64:
+                self._descs.clear()
+            desc = self._descs[key] = ctypes.byref(self._with_strides(key))
         return desc, out, lse
 
-    def _array(self, where, name, t, shape, dtype):
-        if t is not None:
-            _tensor(t, where, name, shape, dtype, self.device, dense=True)
-        return t
+    def _with_strides(self, key):
+        desc = AttnDesc.from_buffer_copy(self.desc)
+        desc.q, desc.k, desc.v, desc.o = (_Stride3(*st[:3]) for st in key[:4])
+        return desc
 
     def check(self, stream=None):
         """Raises EDEVICE if a call since the last check recorded a fault: a length outside its range (clamped), or
@@ -587,17 +647,19 @@ class Attention(_AttnPlan):
             stream=None):
         """q [batch][s_q][h_q][128], k, v [batch][s_kv][h_kv][128], any strides that are multiples of 8 elements;
         returns (out, lse), new tensors unless given.  Rows behind q_len[b] are not written."""
-        import torch
-        where, d = "Attention.run", self.desc
-        desc, out, lse = self._tensors(where, q, k, v, out, lse, stream)
-        arrays = [self._array(where, "slopes", slopes, (d.h_q,), torch.float32)]
-        for name, t in (("q_len", q_len), ("kv_len", kv_len), ("prefix_len", prefix_len)):
-            arrays.append(self._array(where, name, t, (d.batch,), torch.int32))
-        arrays.append(self._array(where, "doc_ids", doc_ids, (d.batch, d.s_kv), torch.int32))
-        mask = AttnMask(*(_ptr(t) for t in arrays))
-        with _on(self.device, stream, (q, k, v, out, lse, self.work, *arrays)) as s:
-            _check(load().qevict_attn(ctypes.byref(desc), ctypes.byref(mask), _ptr(q), _ptr(k), _ptr(v), _ptr(out),
-                                      _ptr(lse), _ptr(self.work), self.work.numel(), s), "qevict_attn")
+        desc, out, lse = self._tensors("Attention.run", q, k, v, out, lse, stream)
+        d, i, mask = self.desc, self.index, None
+        if not (slopes is None and q_len is None and kv_len is None and prefix_len is None and doc_ids is None):
+            f32, i32, where = _torch().float32, _torch().int32, "Attention.run"
+            batch = self.q_shape[:1]
+            mask = ctypes.byref(AttnMask(_array(where, "slopes", slopes, (d.h_q,), f32, i),
+                                         _array(where, "q_len", q_len, batch, i32, i),
+                                         _array(where, "kv_len", kv_len, batch, i32, i),
+                                         _array(where, "prefix_len", prefix_len, batch, i32, i),
+                                         _array(where, "doc_ids", doc_ids, (d.batch, d.s_kv), i32, i)))
+        s, other = _enter(i, stream, (q, k, v, out, lse, slopes, q_len, kv_len, prefix_len, doc_ids, self.work))
+        _call("qevict_attn", other, (desc, mask, q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), lse.data_ptr(),
+                                     *self._work, s))
         return out, lse
 
 
@@ -608,7 +670,7 @@ class PrefixAttention(_AttnPlan):
     def __init__(self, batch, s_q, s_prefix, s_kv, h_q, h_kv, dtype=None, softcap=0.0, scale=0.0, device="cuda"):
         import torch
         self._setup("PrefixAttention", batch, s_q, s_kv, h_q, h_kv, dtype or torch.bfloat16, True, softcap, scale, device)
-        self.s_prefix = int(s_prefix)
+        self.s_prefix, self.prefix_shape = int(s_prefix), (int(s_prefix), int(h_kv), 128)
         n = ctypes.c_size_t()
         st = _Stride2(self.desc.h_kv * 128, 128)
         pd = PrefixAttnDesc(self.desc, self.s_prefix, st, st)
@@ -619,16 +681,17 @@ class PrefixAttention(_AttnPlan):
     def run(self, q, k_prefix, v_prefix, k, v, out=None, lse=None, slopes=None, kv_len=None, stream=None):
         """q [batch][s_q][h_q][128], k_prefix, v_prefix [s_prefix][h_kv][128], k, v [batch][s_kv][h_kv][128];
         returns (out, lse), new tensors unless given."""
-        import torch
-        where, d = "PrefixAttention.run", self.desc
-        desc, out, lse = self._tensors(where, q, k, v, out, lse, stream)
-        for name, t in (("k_prefix", k_prefix), ("v_prefix", v_prefix)):
-            _tensor(t, where, name, (self.s_prefix, d.h_kv, 128), self.dtype, self.device)
-        self._array(where, "slopes", slopes, (d.h_q,), torch.float32)
-        self._array(where, "kv_len", kv_len, (d.batch,), torch.int32)
-        pd = PrefixAttnDesc(desc, self.s_prefix, _Stride2(*k_prefix.stride()[:2]), _Stride2(*v_prefix.stride()[:2]))
-        with _on(self.device, stream, (q, k_prefix, v_prefix, k, v, out, lse, slopes, kv_len, self.work)) as s:
-            _check(load().qevict_prefix_attn(ctypes.byref(pd), _ptr(slopes), _ptr(kv_len), _ptr(q), _ptr(k_prefix),
-                                             _ptr(v_prefix), _ptr(k), _ptr(v), _ptr(out), _ptr(lse), _ptr(self.work),
-                                             self.work.numel(), s), "qevict_prefix_attn")
+        where, d, i = "PrefixAttention.run", self.desc, self.index
+        desc, out, lse = self._tensors(where, q, k, v, out, lse, stream, (k_prefix.stride(), v_prefix.stride()))
+        if not (_fits(k_prefix, self.prefix_shape, self.dtype, i) and _fits(v_prefix, self.prefix_shape, self.dtype, i)):
+            for name, t in (("k_prefix", k_prefix), ("v_prefix", v_prefix)):
+                _tensor(t, where, name, self.prefix_shape, self.dtype, self.device)
+        s, other = _enter(i, stream, (q, k_prefix, v_prefix, k, v, out, lse, slopes, kv_len, self.work))
+        _call("qevict_prefix_attn", other,
+              (desc, _array(where, "slopes", slopes, (d.h_q,), _torch().float32, i),
+               _array(where, "kv_len", kv_len, self.q_shape[:1], _torch().int32, i), q.data_ptr(), k_prefix.data_ptr(),
+               v_prefix.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), lse.data_ptr(), *self._work, s))
         return out, lse
+
+    def _with_strides(self, key):
+        return PrefixAttnDesc(super()._with_strides(key), self.s_prefix, _Stride2(*key[4][:2]), _Stride2(*key[5][:2]))

@@ -4,6 +4,7 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <atomic>
 #include <cmath>
 #include <cstdint>
 
@@ -54,41 +55,66 @@ __global__ void __launch_bounds__(RUN_THREADS) doc_runs_kernel(const int *ids, i
   }
 }
 
-struct CombineArgs {
-  const float *part_o, *part_l;
-  void *out;
-  float *lse;
-  const int *q_len;
-  int64_t so[3], rows;
-  int n, batch, s_q, h_q;
-};
-
-// One warp per row (sequence, query, head): out = sum_s 2^(lse_s - L) out_s, L the log2-sum-exp over the
-// splits; 512 bytes per split and row, read once.
+// One warp per row (sequence, query, head): out = sum_s 2^(lse_s - L) out_s over the parts of the row's units, L their
+// log2-sum-exp; 512 bytes per part and row, read once.  Which parts a row has is worked out as the attention kernel did,
+// before that kernel is waited for.  128 threads of 32 registers fit beside the attention kernel's CTA.
 template <bool FP16>
-__global__ void __launch_bounds__(256) attn_combine_kernel(const CombineArgs A) {
-  const int64_t row = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
+__global__ void __launch_bounds__(128) attn_combine_kernel(const __grid_constant__ AttnArgs P, int ctas) {
+  const int64_t row = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);
   const int lane = threadIdx.x & 31;
-  if (row >= A.rows) return;
-  const int h = (int)(row % A.h_q);
-  const int64_t x = row / A.h_q;
-  const int i = (int)(x % A.s_q), b = (int)(x / A.s_q);
-  if (A.q_len && i >= A.q_len[b]) return;
+  const int64_t x = row / P.h_q;
+  const int h = (int)(row - x * P.h_q), b = (int)(x / P.s_q), i = (int)(x - (int64_t)b * P.s_q);
+  if (b >= P.batch) return;
+  const int g = h / P.G, hr = h - g * P.G, pr = i / (2 * P.tpt), gi = pr * P.batch + b;
+  const AttnGroup A = attn_group(P, gi);
+  if (i >= A.ql) return;
+  const int tp = P.pre ? (P.pre + AT_TILE - 1) / AT_TILE : 0, wp = attn_places(tp), all_p = P.pre ? P.n_prp * P.h_kv * wp : 0;
+  int all = 0, before = 0;   // places of all groups, and of those before this one
+#pragma unroll 2
+  for (int j = lane; j < P.n_pr * P.batch; j += 32) {
+    const AttnGroup B = attn_group(P, j);
+    const int w = attn_places(B.t_hi - B.t_lo);
+    all += w;
+    if (j < gi) before += w;
+  }
+  all = __reduce_add_sync(0xffffffffu, all);
+  before = __reduce_add_sync(0xffffffffu, before);
+  const int share = attn_share(all_p + all * P.h_kv, ctas, P.min_tiles);
+  const int t = A.t_hi - A.t_lo, u0 = all_p + before * P.h_kv + g * attn_places(t);
+  // own parts: the CTAs whose shares hold tiles u0 .. u0 + t - 1
+  const int c_own = u0 / share, n_own = t ? (u0 + t - 1) / share - c_own + 1 : 0;
+  if (!P.pre && n_own == 1) return;   // the unit was not cut: the row is written
+  const int64_t own_row = (int64_t)(c_own + gi * P.h_kv + g) * P.part_rows + (int64_t)(i - pr * 2 * P.tpt) * P.G + hr;
+  int n_pre = 0;
+  int64_t pre_row = 0;
+  if (P.pre) {
+    const int prp = b / (2 * P.nb), u = prp * P.h_kv + g, c0 = u * wp / share;
+    n_pre = (u * wp + tp - 1) / share - c0 + 1;
+    pre_row = (int64_t)(c0 + u) * P.pre_rows + (int64_t)((b - prp * 2 * P.nb) * P.s_q + i) * P.G + hr;
+  }
+  const int n = n_pre + n_own;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  auto lse_of = [&](int s) {
+    return s < n_pre ? P.pre_l[pre_row + (int64_t)s * P.pre_rows] : P.part_l[own_row + (int64_t)(s - n_pre) * P.part_rows];
+  };
   float mx = -INFINITY;
-  for (int s = lane; s < A.n; s += 32) mx = fmaxf(mx, A.part_l[s * A.rows + row]);
+  for (int s = lane; s < n; s += 32) mx = fmaxf(mx, lse_of(s));
   for (int o = 16; o; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
   const float mu = mx == -INFINITY ? 0.f : mx;
   float l = 0.f;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int s0 = 0; s0 < A.n; s0 += 32) {
-    const float w = s0 + lane < A.n ? ex2(A.part_l[(s0 + lane) * A.rows + row] - mu) : 0.f;
+  for (int s0 = 0; s0 < n; s0 += 32) {
+    const float w = s0 + lane < n ? ex2(lse_of(s0 + lane) - mu) : 0.f;
     l += w;
-    const int m = min(32, A.n - s0);
+    const int m = min(32, n - s0);
 #pragma unroll 4
     for (int s = 0; s < m; ++s) {
       const float ws = __shfl_sync(0xffffffffu, w, s);
-      if (ws != 0.f) {   // a split without keys for the row wrote no output (NaN weights go on)
-        const float4 o = *reinterpret_cast<const float4 *>(A.part_o + ((s0 + s) * A.rows + row) * D + 4 * lane);
+      if (ws != 0.f) {   // a part without keys for the row wrote no output (NaN weights go on)
+        const int ss = s0 + s;
+        const float *src = ss < n_pre ? P.pre_o + (pre_row + (int64_t)ss * P.pre_rows) * D
+                                      : P.part_o + (own_row + (int64_t)(ss - n_pre) * P.part_rows) * D;
+        const float4 o = *reinterpret_cast<const float4 *>(src + 4 * lane);
         acc.x = fmaf(ws, o.x, acc.x);
         acc.y = fmaf(ws, o.y, acc.y);
         acc.z = fmaf(ws, o.z, acc.z);
@@ -98,23 +124,27 @@ __global__ void __launch_bounds__(256) attn_combine_kernel(const CombineArgs A) 
   }
   for (int o = 16; o; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
   const float inv = l == 0.f ? 0.f : 1.f / l;
-  *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(A.out) + b * A.so[0] + i * A.so[1] + h * A.so[2] + 4 * lane) =
+  *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(P.out) + b * P.so[0] + i * P.so[1] + h * P.so[2] + 4 * lane) =
       make_uint2(pack2<FP16>(acc.x * inv, acc.y * inv), pack2<FP16>(acc.z * inv, acc.w * inv));
-  if (lane == 0 && A.lse) A.lse[row] = l == 0.f ? -INFINITY : (mu + log2f(l)) * 0.69314718055994531f;
+  if (lane == 0 && P.lse) P.lse[row] = l == 0.f ? -INFINITY : (mu + log2f(l)) * 0.69314718055994531f;
 }
 
 namespace {
 
 int64_t align256(int64_t x) { return (x + 255) & ~int64_t(255); }
 
-int sm_count() {
+int sm_count() {   // of the current device
+  static std::atomic<int> known[64];
   int dev = 0, n = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess ||
-      n <= 0) {
-    cudaGetLastError();
-    return 152;
+  if (cudaGetDevice(&dev) == cudaSuccess && dev >= 0 && dev < 64) {
+    if ((n = known[dev].load(std::memory_order_relaxed)) > 0) return n;
+    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) == cudaSuccess && n > 0) {
+      known[dev].store(n, std::memory_order_relaxed);
+      return n;
+    }
   }
-  return n;
+  cudaGetLastError();
+  return 152;
 }
 
 // [tokens][heads][128] tensors of `batch` sequences as a 4-D tensor map; a box is 64 channels x `bh` heads x
@@ -135,10 +165,14 @@ bool dense_map(CUtensorMap *map, bool fp16, const void *base, int64_t heads, int
 }
 
 struct AttnPlan {
-  int G, tpt, n_pr, ns, items;
-  int pre, nb, n_prp, nsp, items_p;
-  int64_t rows, off_runs, off_l, off_o, bytes;
+  int G, tpt, n_pr, stream, grid;
+  int pre, nb, n_prp;
+  int part_rows, pre_rows;
+  int64_t rows, off_runs, off_l, off_o, off_pl, off_po, bytes;
 };
+
+// Key tiles that a CTA takes at least, where the stream is cut finer than its CTAs would need
+constexpr int MIN_TILES = 2;
 
 bool stride_ok(int64_t st, int64_t size, bool zero) {
   if (size <= 1) return true;
@@ -164,38 +198,46 @@ qevict_status attn_plan(const qevict_attn_desc *d, int s_prefix, AttnPlan *p) {
   p->tpt = AT_TILE / p->G;
   p->rows = (int64_t)d->batch * d->s_q * d->h_q;
   const int64_t sms = sm_count();
-  const int64_t n_qt = (d->s_q + p->tpt - 1) / p->tpt, n_pr = (n_qt + 1) / 2;
-  const int64_t base = (int64_t)d->batch * d->h_kv * n_pr, tiles = (d->s_kv + AT_TILE - 1) / AT_TILE;
-  if (base > (1 << 24) || p->rows > (1ll << 40)) return QEVICT_EINVAL;
-  // Splits of the keys while the items leave SMs idle, each split with at least four key tiles (two per slot)
-  const int64_t min_tiles = 4;
-  const int64_t ns = std::max<int64_t>(1, std::min(sms / base, tiles / min_tiles));
+  const int64_t n_qt = (d->s_q + p->tpt - 1) / p->tpt, n_pr = (n_qt + 1) / 2, groups = n_pr * d->batch;
+  const int64_t units = groups * d->h_kv, tiles = (d->s_kv + AT_TILE - 1) / AT_TILE;
+  if (units > (1 << 24) || p->rows > (1ll << 38)) return QEVICT_EINVAL;
+  int64_t total = units * (tiles + AT_UNIT_COST);   // places of the stream, at most
   p->n_pr = (int)n_pr;
-  p->ns = (int)ns;
-  int64_t items_p = 0;
   if (s_prefix) {
     if (!d->causal || (int64_t)d->s_q * p->G > AT_TILE) return QEVICT_EINVAL;
     p->pre = s_prefix;
     p->nb = std::min(p->tpt / d->s_q, 256);
-    const int64_t n_qtp = (d->batch + p->nb - 1) / p->nb, n_prp = (n_qtp + 1) / 2;
-    const int64_t base_p = d->h_kv * n_prp, tiles_p = (s_prefix + AT_TILE - 1) / AT_TILE;
-    p->n_prp = (int)n_prp;
-    p->nsp = (int)std::max<int64_t>(1, std::min(sms / base_p, tiles_p / min_tiles));
-    items_p = base_p * p->nsp;
+    const int64_t n_qtp = (d->batch + p->nb - 1) / p->nb;
+    p->n_prp = (int)((n_qtp + 1) / 2);
+    total += (int64_t)p->n_prp * d->h_kv * ((s_prefix + AT_TILE - 1) / AT_TILE + AT_UNIT_COST);
   }
-  if (base * ns + items_p > (1 << 28)) return QEVICT_EINVAL;
-  p->items_p = (int)items_p;
-  p->items = (int)(base * ns + items_p);
+  // One stream of key tiles cut into equal shares, or whole units in turn.  The stream evens out caches of different
+  // lengths and fills the SMs when there are few units, at the price of parts that are merged afterwards: for units of one
+  // row tile (few rows to merge) always but when none would be cut, for larger ones while they leave SMs without work.
+  p->stream = s_prefix || (n_qt == 1 ? tiles > MIN_TILES : units < sms && tiles > MIN_TILES);
+  if (total > (1 << 30) && p->stream) {
+    if (s_prefix) return QEVICT_EINVAL;
+    p->stream = 0;
+  }
+  p->grid = (int)std::min(sms, p->stream ? (total + MIN_TILES - 1) / MIN_TILES : units);
   int64_t off = 256;
-  p->off_runs = off;
-  if (!s_prefix) off += align256((int64_t)d->batch * d->s_kv * 8);
-  const int64_t parts = p->ns + p->nsp;
-  p->off_l = off;
-  p->off_o = off;
-  if (parts > 1) {
-    off += align256(parts * p->rows * 4);
-    p->off_o = off;
-    off += align256(parts * p->rows * D * 4);
+  auto take = [&](int64_t n) {
+    const int64_t o = off;
+    off += align256(n);
+    return o;
+  };
+  if (!s_prefix) p->off_runs = take((int64_t)d->batch * d->s_kv * 8);
+  if (p->stream) {
+    p->part_rows = std::min(d->s_q, 2 * p->tpt) * p->G;
+    const int64_t parts = p->grid + units;
+    p->off_l = take(parts * p->part_rows * 4);
+    p->off_o = take(parts * p->part_rows * D * 4);
+  }
+  if (s_prefix) {
+    p->pre_rows = std::min(d->batch, 2 * p->nb) * d->s_q * p->G;
+    const int64_t parts = p->grid + (int64_t)p->n_prp * d->h_kv;
+    p->off_pl = take(parts * p->pre_rows * 4);
+    p->off_po = take(parts * p->pre_rows * D * 4);
   }
   p->bytes = off;
   return QEVICT_OK;
@@ -235,14 +277,16 @@ qevict_status attn_launch(const qevict_attn_desc *d, const AttnPlan &pl, const q
   A.status = reinterpret_cast<int *>(w);
   A.slopes = m.slopes, A.q_len = m.q_len, A.kv_len = m.kv_len, A.prefix_len = m.prefix_len;
   for (int i = 0; i < 3; ++i) A.sq[i] = d->q[i], A.sk[i] = d->k[i], A.sv[i] = d->v[i], A.so[i] = d->o[i];
-  A.rows = pl.rows;
   A.batch = d->batch, A.s_q = d->s_q, A.s_kv = d->s_kv, A.h_q = d->h_q, A.h_kv = d->h_kv, A.G = pl.G, A.causal = d->causal;
   A.mul_q = d->batch > 1 && d->q[0] ? 1 : 0;
   A.mul_k = d->batch > 1 && d->k[0] ? 1 : 0;
   A.mul_v = d->batch > 1 && d->v[0] ? 1 : 0;
-  A.tpt = pl.tpt, A.n_pr = pl.n_pr, A.ns = pl.ns;
-  A.pre = pl.pre, A.nb = pl.nb, A.n_prp = pl.n_prp, A.nsp = pl.nsp;
-  A.items = pl.items, A.items_p = pl.items_p;
+  A.tpt = pl.tpt, A.n_pr = pl.n_pr;
+  A.pre = pl.pre, A.nb = std::max(1, pl.nb), A.n_prp = pl.n_prp;
+  A.part_rows = pl.part_rows, A.pre_rows = pl.pre_rows;
+  A.stream = pl.stream, A.min_tiles = MIN_TILES;
+  A.wide_out = ((uintptr_t)out & 31) == 0 && (d->batch == 1 || d->o[0] % 16 == 0) && (d->s_q == 1 || d->o[1] % 16 == 0) &&
+               (d->h_q == 1 || d->o[2] % 16 == 0);
   const float scale = d->scale > 0.f ? d->scale : 1.f / std::sqrt((float)D), log2e = 1.4426950408889634f;
   A.scale_log2 = scale * log2e;
   if (d->softcap > 0.f) {
@@ -266,28 +310,26 @@ qevict_status attn_launch(const qevict_attn_desc *d, const AttnPlan &pl, const q
     doc_runs_kernel<<<d->batch, RUN_THREADS, 0, s>>>(m.doc_ids, d->s_kv, const_cast<int2 *>(A.runs));
     if (cudaGetLastError() != cudaSuccess) return QEVICT_ECUDA;
   }
-  const int parts = pl.ns + pl.nsp;
-  if (parts > 1) {
+  if (pl.stream) {
     A.part_l = reinterpret_cast<float *>(w + pl.off_l);
     A.part_o = reinterpret_cast<float *>(w + pl.off_o);
+    A.pre_l = reinterpret_cast<float *>(w + pl.off_pl);
+    A.pre_o = reinterpret_cast<float *>(w + pl.off_po);
   }
-  const int grid = std::min(pl.items, sm_count());
-  if ((fp16 ? launch_attn_fp16 : launch_attn_bf16)(A, grid, d->softcap > 0.f, m.slopes != nullptr, s) != cudaSuccess)
+  if ((fp16 ? launch_attn_fp16 : launch_attn_bf16)(A, pl.grid, d->softcap > 0.f, m.slopes != nullptr, s) != cudaSuccess)
     return QEVICT_ECUDA;
-  if (parts > 1) {
-    CombineArgs C = {};
-    C.part_o = A.part_o, C.part_l = A.part_l;
-    C.out = out, C.lse = lse;
-    C.q_len = m.q_len;
-    for (int i = 0; i < 3; ++i) C.so[i] = d->o[i];
-    C.rows = pl.rows;
-    C.n = parts, C.batch = d->batch, C.s_q = d->s_q, C.h_q = d->h_q;
-    const unsigned blocks = (unsigned)((pl.rows + 7) / 8);
-    if (fp16)
-      attn_combine_kernel<true><<<blocks, 256, 0, s>>>(C);
-    else
-      attn_combine_kernel<false><<<blocks, 256, 0, s>>>(C);
-    if (cudaGetLastError() != cudaSuccess) return QEVICT_ECUDA;
+  if (pl.stream) {
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.gridDim = dim3((unsigned)((pl.rows + 3) / 4));
+    cfg.blockDim = dim3(128);
+    cfg.stream = s;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (cudaLaunchKernelEx(&cfg, fp16 ? attn_combine_kernel<true> : attn_combine_kernel<false>, A, pl.grid) != cudaSuccess)
+      return QEVICT_ECUDA;
   }
   return QEVICT_OK;
 }

@@ -16,16 +16,18 @@ constexpr int AT_STAGES = 5;                          // key / value tiles in fl
 constexpr int AT_TILE_BYTES = AT_TILE * D * 2;        // 32 KB: two 128-byte-swizzled halves of 64 channels
 constexpr int AT_HALF_BYTES = AT_TILE_BYTES / 2;
 constexpr int AT_SOFT = 16;                           // softmax warps: eight per slot, four for each half of the columns
-constexpr int AT_THREADS = (AT_SOFT + 2) * 32;        // a TMA warp and an MMA warp (96 registers a thread)
-constexpr int AT_W_LOAD = AT_SOFT, AT_W_MMA = AT_SOFT + 1;
+constexpr int AT_W_LOAD = AT_SOFT, AT_W_MMA = AT_SOFT + 1, AT_W_PLAN = AT_SOFT + 2;   // TMA, MMA, work items
+constexpr int AT_THREADS = (AT_SOFT + 3) * 32;        // five warps on an SM sub-partition: 96 registers a thread
 constexpr int AT_COLS = AT_TILE / 2;                  // columns of S, and channels of O, per softmax thread
+constexpr int AT_ITEMS = 4;                           // work items described ahead
 constexpr int AT_OFF_KV = 2 * AT_TILE_BYTES;
 constexpr int AT_OFF_X = AT_OFF_KV + AT_STAGES * AT_TILE_BYTES;    // [2 slots][2 halves][128] fp32 exchange
 constexpr int AT_OFF_M = AT_OFF_X + 4 * AT_TILE * 4;               // [128] fp32: slot 1's maxima
 constexpr int AT_OFF_BAR = AT_OFF_M + AT_TILE * 4;
-constexpr int AT_NBAR = 2 * AT_STAGES + 2 + 6;
+constexpr int AT_NBAR = 2 * AT_STAGES + 4 + 6 + 2 * AT_ITEMS;
 constexpr int AT_OFF_MISC = AT_OFF_BAR + AT_NBAR * 8;              // tmem address, flags
-constexpr int AT_SMEM = AT_OFF_MISC + 16;
+constexpr int AT_OFF_ITEM = AT_OFF_MISC + 16;                     // work item ring
+constexpr int AT_SMEM = AT_OFF_ITEM + AT_ITEMS * 64;
 static_assert(AT_SMEM <= 232448, "one CTA per SM");
 constexpr int AT_BAR_ALL = 1, AT_BAR_PAIR = 2;        // named barriers (pairs: 2 .. 9)
 
@@ -35,43 +37,39 @@ struct AttnArgs {
   const void *k, *v, *q, *kp, *vp;
   void *out;
   float *lse;
-  float *part_o, *part_l;      // [split][row][128], [split][row] (log2 domain); NULL: written directly
+  float *part_o, *part_l;      // own keys: [part][row][128], [part][row] (log2 domain)
+  float *pre_o, *pre_l;        // the same of the prefix
   int *status;
   const float *slopes;
   const int *q_len, *kv_len, *prefix_len;
   const int2 *runs;            // [batch][s_kv]: first and past-the-last position of every position's document
   int64_t sq[3], sk[3], sv[3], so[3], skp[2], svp[2];
-  int64_t rows;                // batch * s_q * h_q
   int batch, s_q, s_kv, h_q, h_kv, G, causal;
   int mul_q, mul_k, mul_v;     // batch coordinate of the tensor maps: 0 for a batch stride of 0
-  int tpt, n_pr, ns;           // own keys: tokens per row tile, pairs of row tiles, splits
-  int pre, nb, n_prp, nsp;     // prefix: keys, sequences per row tile, pairs of row tiles, splits
-  int items_p, items;          // prefix items, all items
+  int wide_out;                // rows of out are 32-byte aligned
+  int tpt, n_pr;               // own keys: tokens per row tile, pairs of row tiles
+  int pre, nb, n_prp;          // prefix: keys, sequences per row tile, pairs of row tiles
+  int part_rows, pre_rows;     // rows of a part
+  int stream, min_tiles;       // the key tiles of all units as one stream, cut into equal shares of at least min_tiles
   float scale_log2;            // logit scale * log2 e
   float cap_in, cap_log2;      // softcap: 2 log2 e * scale / cap, cap * log2 e
 };
 
-// A work item: one or two row tiles of one KV head against one split of a key range.  pair: slot 0 and 1
-// hold two row tiles and both see every key tile.  Otherwise one row tile in both slots, slot s taking
-// every second key tile.
-struct AttnItem {
-  bool prefix, pair;
-  int b, g, tile0, sp;
-  int kl, ql;                  // keys and queries of the sequence
-  int n, t_hi;                 // key tiles t_hi - 1, t_hi - 2, ... (n of them)
-  int clean_lo, clean_hi;      // keys that every row of the item sees
-  int key_lo, key_hi;          // keys that some row sees
-};
-
 __device__ __forceinline__ int clampi(int x, int lo, int hi) { return x < lo ? lo : x > hi ? hi : x; }
 
+// A unit of work is one KV head's pair of row tiles against the keys it sees; the units of a pair of row tiles (a
+// group) differ in the KV head only and have the same key tiles.  Group gi = pair * batch + sequence.
+struct AttnGroup {
+  int b, tile0;
+  int kl, ql, pfx;             // keys, queries, prefix mask of the sequence
+  int clean_lo, clean_hi;      // keys that every row sees
+  int key_lo, key_hi;          // keys that some row sees
+  int t_lo, t_hi;              // key tiles
+};
+
 // Visible keys [x, y) of position p.  Both ends grow with p.
-__device__ __forceinline__ int2 attn_interval(const AttnArgs &P, int b, int p, int kl) {
-  int lo = 0, hi = kl;
-  if (P.causal) {
-    const int pre = P.prefix_len ? clampi(P.prefix_len[b], 0, kl) : 0;
-    hi = min(max(p + 1, pre), kl);
-  }
+__device__ __forceinline__ int2 attn_interval(const AttnArgs &P, int b, int p, int kl, int pfx) {
+  int lo = 0, hi = P.causal ? min(max(p + 1, pfx), kl) : kl;
   if (P.runs) {
     if (p < 0) return make_int2(0, 0);
     const int2 r = P.runs[(size_t)b * P.s_kv + p];
@@ -81,62 +79,54 @@ __device__ __forceinline__ int2 attn_interval(const AttnArgs &P, int b, int p, i
   return make_int2(lo, max(hi, lo));
 }
 
-__device__ __forceinline__ AttnItem attn_item(const AttnArgs &P, int it) {
-  AttnItem I;
-  int lo, hi;
-  if (it < P.items_p) {
-    I.prefix = true;
-    I.g = it % P.h_kv;
-    const int x = it / P.h_kv;
-    I.sp = x % P.nsp;
-    I.tile0 = 2 * (x / P.nsp);
-    I.b = 0;
-    I.kl = P.pre;
-    I.ql = P.s_q;
-    I.pair = (I.tile0 + 1) * P.nb < P.batch;
-    I.clean_lo = I.key_lo = 0;
-    I.clean_hi = I.key_hi = P.pre;
-    lo = 0;
-    hi = (P.pre + AT_TILE - 1) / AT_TILE;
-    const int per = (hi + P.nsp - 1) / P.nsp;
-    lo = I.sp * per;
-    hi = min(hi, lo + per);
-  } else {
-    it -= P.items_p;
-    I.prefix = false;
-    I.g = it % P.h_kv;
-    int x = it / P.h_kv;
-    I.b = x % P.batch;
-    x /= P.batch;
-    I.sp = x % P.ns;
-    const int pr = P.n_pr - 1 - x / P.ns;   // causal: the longest rows first
-    I.tile0 = 2 * pr;
-    I.kl = P.kv_len ? clampi(P.kv_len[I.b], 0, P.s_kv) : P.s_kv;
-    I.ql = P.q_len ? clampi(P.q_len[I.b], 0, P.s_q) : P.s_q;
-    const int i0 = I.tile0 * P.tpt, i1 = min(I.ql, i0 + 2 * P.tpt);
-    I.pair = i0 + P.tpt < I.ql;
-    I.clean_lo = I.clean_hi = I.key_lo = I.key_hi = 0;
-    lo = hi = 0;
-    if (i0 < i1) {
-      const int p0 = I.kl - I.ql + i0;
-      const int2 a = attn_interval(P, I.b, p0, I.kl), z = attn_interval(P, I.b, p0 + (i1 - 1 - i0), I.kl);
-      I.key_lo = a.x;
-      I.key_hi = z.y;
-      I.clean_lo = z.x;
-      I.clean_hi = a.y;
-      if (I.key_hi > I.key_lo) {
-        lo = I.key_lo / AT_TILE;
-        hi = (I.key_hi + AT_TILE - 1) / AT_TILE;
-      }
+__device__ __forceinline__ AttnGroup attn_group(const AttnArgs &P, int gi) {
+  AttnGroup A;
+  const int pr = P.n_pr == 1 ? 0 : gi / P.batch;
+  A.b = gi - pr * P.batch;
+  A.tile0 = 2 * pr;
+  A.kl = P.kv_len ? clampi(P.kv_len[A.b], 0, P.s_kv) : P.s_kv;
+  A.ql = P.q_len ? clampi(P.q_len[A.b], 0, P.s_q) : P.s_q;
+  A.pfx = P.prefix_len ? clampi(P.prefix_len[A.b], 0, A.kl) : 0;
+  const int i0 = A.tile0 * P.tpt, i1 = min(A.ql, i0 + 2 * P.tpt);
+  A.clean_lo = A.clean_hi = A.key_lo = A.key_hi = A.t_lo = A.t_hi = 0;
+  if (i0 < i1) {
+    const int p0 = A.kl - A.ql + i0;
+    const int2 a = attn_interval(P, A.b, p0, A.kl, A.pfx), z = attn_interval(P, A.b, p0 + (i1 - 1 - i0), A.kl, A.pfx);
+    A.key_lo = a.x;
+    A.key_hi = z.y;
+    A.clean_lo = z.x;
+    A.clean_hi = a.y;
+    if (A.key_hi > A.key_lo) {
+      A.t_lo = A.key_lo / AT_TILE;
+      A.t_hi = (A.key_hi + AT_TILE - 1) / AT_TILE;
     }
-    const int per = (hi - lo + P.ns - 1) / P.ns;
-    lo += I.sp * per;
-    hi = min(hi, lo + per);
   }
-  I.n = max(0, hi - lo);
-  I.t_hi = hi;
-  return I;
+  return A;
 }
+
+// Places that a unit of t key tiles takes in the stream: its tiles, and behind them the cost of beginning and ending
+// a unit in tiles, so that a CTA with many short units gets fewer tiles.
+constexpr int AT_UNIT_COST = 4;
+__device__ __forceinline__ int attn_places(int t) { return t ? t + AT_UNIT_COST : 0; }
+// Share of the stream that each of `ctas` CTAs takes.
+__device__ __forceinline__ int attn_share(int total, int ctas, int min_tiles) {
+  return max((total + ctas - 1) / ctas, min_tiles);
+}
+
+// A work item: a unit, or the part of it that falls into a CTA's share.  pair: slot 0 and 1 hold two row tiles and
+// both see every key tile.  Otherwise one row tile in both slots, slot s taking every second key tile.
+struct AttnItem {
+  int kind;                    // bit 0 prefix, bit 1 pair, bit 2 written as a part; -1: no more items
+  int b, g, tile0, kl, ql, pfx;
+  int n, t_hi;                 // key tiles t_hi - 1, t_hi - 2, ... (n of them)
+  int clean_lo, clean_hi, key_lo, key_hi;
+  int part;
+  int pad[2];
+  __device__ __forceinline__ bool prefix() const { return kind & 1; }
+  __device__ __forceinline__ bool pair() const { return kind & 2; }
+  __device__ __forceinline__ bool parts() const { return kind & 4; }
+};
+static_assert(sizeof(AttnItem) == 64, "item ring");
 
 // Whether some row of the item does not see some key of tile t: only there can a value that is not finite
 // stand in a masked place (a masked probability is 0, and 0 * NaN is not).
@@ -144,19 +134,35 @@ __device__ __forceinline__ bool attn_mixed(const AttnItem &I, int t) {
   return t * AT_TILE < I.clean_lo || (t + 1) * AT_TILE > I.clean_hi;
 }
 
-// Row r of the slot's tile: sequence b, query i (false: the row is padding).
-__device__ __forceinline__ bool attn_row(const AttnArgs &P, const AttnItem &I, int slot, int r, int &b, int &i, int &h) {
-  const int tile = I.tile0 + (I.pair ? slot : 0), tok = r / P.G;
-  h = I.g * P.G + (r - tok * P.G);
-  if (I.prefix) {
-    const int bl = tok / P.s_q;
-    b = tile * P.nb + bl;
-    i = tok - bl * P.s_q;
-    return bl < P.nb && b < P.batch;
+// What row r of a slot's tile is, in every item: token r / G of the tile and query head r % G of the group.
+struct AttnRow {
+  int tok, hr, bl, ip;         // in a prefix item the token is query ip of the tile's sequence bl
+};
+__device__ __forceinline__ AttnRow attn_row_of(const AttnArgs &P, int r) {
+  AttnRow R;
+  R.tok = r / P.G;
+  R.hr = r - R.tok * P.G;
+  R.bl = R.tok / P.s_q;
+  R.ip = R.tok - R.bl * P.s_q;
+  return R;
+}
+// Sequence b, query i and head h of the row; its row of a part.  False: the row is padding.
+__device__ __forceinline__ bool attn_row(const AttnArgs &P, const AttnItem &I, int slot, const AttnRow &R, int &b, int &i,
+                                         int &h, int &prow) {
+  const int second = I.pair() ? slot : 0;
+  h = I.g * P.G + R.hr;
+  if (I.prefix()) {
+    const int bt = second * P.nb + R.bl;
+    b = I.tile0 * P.nb + bt;
+    i = R.ip;
+    prow = (bt * P.s_q + i) * P.G + R.hr;
+    return R.bl < P.nb && b < P.batch;
   }
   b = I.b;
-  i = tile * P.tpt + tok;
-  return tok < P.tpt && i < I.ql;
+  const int il = second * P.tpt + R.tok;
+  i = I.tile0 * P.tpt + il;
+  prow = il * P.G + R.hr;
+  return R.tok < P.tpt && i < I.ql;
 }
 
 // Bounded wait on an mbarrier phase.  The limit is about 4 s (8e9 SM cycles), longer than the 200 ms of the other
@@ -275,6 +281,11 @@ __device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t *r) {
 }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
+__device__ __forceinline__ void st_global_v8(void *p, const uint32_t *r) {   // 32 bytes, 32-byte aligned
+  asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]),
+               "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
+}
 __device__ __forceinline__ float rcp_approx(float x) {   // relative error about 2^-23
   float y;
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -298,11 +309,12 @@ __device__ __forceinline__ float2 unpack2(uint32_t v) {
 // ----------------------------------------------------------------------------- rows with values that are not finite
 
 // The keys of tile t that not every row of the item sees: their values that are not finite become 0 in shared memory,
-// thread `who` of 256 taking half a key's channels.  Whether one of them is seen by some row.
+// thread `who` of 256 taking half a key's channels.  If some row sees such a key, *flag = mark is set first: a slot that
+// meets the 0 of the other slot also meets its flag.
 template <bool FP16>
-__device__ __forceinline__ bool attn_clean_values(const AttnItem &I, int t, uint8_t *v, int who) {
+__device__ __forceinline__ void attn_clean_values(const AttnItem &I, int t, uint8_t *v, int who, volatile int *flag, int mark) {
   const int k = who >> 1, key = t * AT_TILE + k;
-  if (key >= I.clean_lo && key < I.clean_hi) return false;
+  if (key >= I.clean_lo && key < I.clean_hi) return;
   constexpr uint32_t E = FP16 ? 0x7C00u : 0x7F80u;
   uint32_t *p = reinterpret_cast<uint32_t *>(v + (who & 1) * AT_HALF_BYTES + k * 128);
   bool found = false;
@@ -315,25 +327,28 @@ __device__ __forceinline__ bool attn_clean_values(const AttnItem &I, int t, uint
     for (int q = 0; q < 4; ++q) {
       const bool lo = (w[q] & E) == E, hi = (w[q] & (E << 16)) == (E << 16);
       if (lo | hi) {
+        if (!found && key >= I.key_lo && key < I.key_hi) {
+          *flag = mark;
+          __threadfence_block();
+        }
         pc[q] = (lo ? 0u : w[q] & 0xFFFFu) | (hi ? 0u : w[q] & 0xFFFF0000u);
         found = true;
       }
     }
   }
   if (found) fence_proxy_async();   // the product reads shared memory through the async proxy
-  return found && key >= I.key_lo && key < I.key_hi;
 }
 
 // The rows of one warp of a slot recomputed on the CUDA cores, every visible key of the item's own tiles in
 // turn and no masked value touched.  Reached when a value that some row of the item sees and another does not is an infinity or
 // NaN: the tensor-core product then ran with that value as 0.  Writes O (unnormalised), m, l of row r
-// through `emit(r, acc, m, l)`, the warp's lanes holding four channels each.
+// through `emit`, the warp's lanes holding four channels each.
 template <bool FP16, typename Emit>
 __device__ __forceinline__ void attn_exact_rows(const AttnArgs &P, const AttnItem &I, int slot, int warp, int lane, bool cap,
                                                 const Emit &emit) {
   const uint16_t *kb, *vb;
   int64_t kst, vst;
-  if (I.prefix) {
+  if (I.prefix()) {
     kb = static_cast<const uint16_t *>(P.kp) + I.g * P.skp[1];
     vb = static_cast<const uint16_t *>(P.vp) + I.g * P.svp[1];
     kst = P.skp[0], vst = P.svp[0];
@@ -343,18 +358,17 @@ __device__ __forceinline__ void attn_exact_rows(const AttnArgs &P, const AttnIte
     kst = P.sk[1], vst = P.sv[1];
   }
   for (int rr = 0; rr < 32; ++rr) {
-    const int r = warp * 32 + rr;
-    int b, i, h;
-    if (!attn_row(P, I, slot, r, b, i, h)) continue;
+    int b, i, h, prow;
+    if (!attn_row(P, I, slot, attn_row_of(P, warp * 32 + rr), b, i, h, prow)) continue;
     const uint16_t *q = static_cast<const uint16_t *>(P.q) + b * P.sq[0] + i * P.sq[1] + h * P.sq[2];
     int p, lo, hi;
-    if (I.prefix) {
+    if (I.prefix()) {
       const int kl = P.kv_len ? clampi(P.kv_len[b], 0, P.s_kv) : P.s_kv;
       p = P.pre + kl - P.s_q + i;
       lo = 0, hi = P.pre;
     } else {
       p = I.kl - I.ql + i;
-      const int2 v = attn_interval(P, b, p, I.kl);
+      const int2 v = attn_interval(P, b, p, I.kl, I.pfx);
       lo = v.x, hi = v.y;
     }
     const float slope = P.slopes ? P.slopes[h] * 1.4426950408889634f : 0.f;
@@ -399,30 +413,31 @@ __device__ __forceinline__ void attn_exact_rows(const AttnArgs &P, const AttnIte
         }
       }
     }
-    emit(r, b, i, h, acc, m, l);
+    emit(b, i, h, prow, acc, m, l);
   }
 }
 
 // ----------------------------------------------------------------------------- the kernel
 
-// One persistent CTA per SM.  Two slots of eight softmax warps, a thread owning one row and half of the columns
-// of its slot's 128-row tile, a TMA warp and an MMA warp.  Rows of a tile are (token, query head of the group), so the group's heads share every key
-// tile.  Tensor memory: S of slot s at columns 128 s, overwritten in place by the probabilities (16-bit, the A operand of
-// P V; each half of the keys over its own half of S), O of slot s at 256 + 128 s.  The tensor pipe alternates between the slots: while slot 0 turns
-// S into P, it runs slot 1's products.
+// One persistent CTA per SM: two slots of eight softmax warps, a thread owning one row and half of the columns
+// of its slot's 128-row tile; a TMA warp; an MMA warp; a warp that lays out the work items ahead of the others.  Rows of a tile are (token, query head of the
+// group), so the group's heads share every key tile.  Tensor memory: S of slot s at columns 128 s, overwritten in place by
+// the probabilities (16-bit, the A operand of P V; each half of the keys over its own half of S), O of slot s at 256 + 128 s.  The
+// tensor pipe alternates between the slots: while slot 0 turns S into P, it runs slot 1's products.
 // Key tiles are taken from the last to the first, so a causal row meets its diagonal, and a distance bias its largest
-// logits, first.  The running max moves only when a row's max has grown by more than 2^8 (then the warp rescales its
+// logits, first.  The running max moves only when a row's max has grown by more than 2^8 (then the warps rescale their
 // rows of O in tensor memory): until then p reaches at most 2^8, which fp32 sums and 16-bit probabilities hold as well.
 // Every wait is bounded; the TMEM columns are released on every path.
 template <bool FP16, bool CAP, bool BIAS>
 __global__ void __launch_bounds__(AT_THREADS, 1) attn_kernel(const __grid_constant__ AttnArgs P) {
   extern __shared__ __align__(1024) uint8_t sm[];   // swizzle atoms: 1024-aligned
   uint64_t *bars = reinterpret_cast<uint64_t *>(sm + AT_OFF_BAR);
-  uint64_t *full = bars, *empty = full + AT_STAGES, *qfull = empty + AT_STAGES, *qempty = qfull + 1;
-  uint64_t *sfull = qempty + 1, *pfull = sfull + 2, *ofull = pfull + 2;
+  uint64_t *full = bars, *empty = full + AT_STAGES, *qfull = empty + AT_STAGES, *qempty = qfull + 2;
+  uint64_t *sfull = qempty + 2, *pfull = sfull + 2, *ofull = pfull + 2, *ifull = ofull + 2, *iempty = ifull + AT_ITEMS;
   uint32_t *misc = reinterpret_cast<uint32_t *>(sm + AT_OFF_MISC);
   uint32_t *tmem_slot = misc;
   volatile int *bad_item = reinterpret_cast<int *>(misc + 2);   // [item parity]: 1 + the item with values to recompute
+  AttnItem *items = reinterpret_cast<AttnItem *>(sm + AT_OFF_ITEM);
   float *xch = reinterpret_cast<float *>(sm + AT_OFF_X), *m_slot1 = reinterpret_cast<float *>(sm + AT_OFF_M);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   int *status = P.status;
@@ -431,154 +446,313 @@ __global__ void __launch_bounds__(AT_THREADS, 1) attn_kernel(const __grid_consta
     return;
   }
 
-  if (threadIdx.x == 0) {
-    for (int i = 0; i < AT_NBAR; ++i) {
-      const uint64_t *p = &bars[i];
-      const bool soft = p >= pfull && p < pfull + 2, two = p >= ofull && p < ofull + 2;
-      mbar_init(&bars[i], soft ? AT_SOFT / 2 : two ? 2 : 1);
-    }
-    fence_mbar_init();
-    bad_item[0] = bad_item[1] = 0;
-  }
   if (warp == AT_W_MMA) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)), "r"(512)
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  } else if (threadIdx.x < AT_NBAR) {
+    const uint64_t *p = &bars[threadIdx.x];
+    const int n = p < pfull ? 1 : p < ofull ? AT_SOFT / 2 :
+                  p < ifull ? 2 : p < iempty ? 1 : AT_SOFT + 2;
+    mbar_init(&bars[threadIdx.x], n);
+    fence_mbar_init();
+    if (threadIdx.x < 2) bad_item[threadIdx.x] = 0;
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
-  if (warp >= AT_SOFT) {
-    if (warp == AT_W_LOAD) {
-      if (lane == 0) {   // ---- TMA loads
-        const uint32_t qbytes = (uint32_t)(P.G * P.tpt) * 128u;   // half of a query tile
-        const uint32_t qpbytes = (uint32_t)(P.G * P.s_q * P.nb) * 128u;
-        uint32_t c = 0, qc = 0;
-        bool ok = true;
-        for (int it = blockIdx.x; ok && it < P.items; it += gridDim.x) {
-          const AttnItem I = attn_item(P, it);
-          if (!I.prefix && ((P.kv_len && (P.kv_len[I.b] < 0 || P.kv_len[I.b] > P.s_kv)) ||
-                            (P.q_len && (P.q_len[I.b] < 0 || P.q_len[I.b] > P.s_q))))
-            atomicOr(status, QV_ERR_BOUNDS);
-          if (I.n == 0) continue;
-          const CUtensorMap *mq = I.prefix ? &P.tqp : &P.tq, *mk = I.prefix ? &P.tkp : &P.tk,
-                            *mv = I.prefix ? &P.tvp : &P.tv;
-          if (!(ok = attn_wait(qempty, (qc & 1) ^ 1, status))) break;
-          const uint32_t qb = I.prefix ? qpbytes : qbytes;
-          mbar_arrive_expect_tx(qfull, qb * (I.pair ? 4 : 2));
-          for (int s = 0; s < (I.pair ? 2 : 1); ++s) {
-            const uint32_t dst = smem_u32(sm) + s * AT_TILE_BYTES;
-            const int tok = I.prefix ? 0 : (I.tile0 + s) * P.tpt, bb = I.prefix ? (I.tile0 + s) * P.nb : I.b * P.mul_q;
-            tma_load_4d_at(dst, mq, 0, I.g * P.G, tok, bb, qfull);
-            tma_load_4d_at(dst + AT_HALF_BYTES, mq, 64, I.g * P.G, tok, bb, qfull);
-          }
-          ++qc;
-          auto load = [&](const CUtensorMap *map, int j, int bb) {
-            const uint32_t st = c % AT_STAGES;
-            if (!ok || !(ok = attn_wait(&empty[st], ((c / AT_STAGES) & 1) ^ 1, status))) return;
-            const uint32_t dst = smem_u32(sm) + AT_OFF_KV + st * AT_TILE_BYTES;
-            const int t = I.t_hi - 1 - j;
-            mbar_arrive_expect_tx(&full[st], AT_TILE_BYTES);
-            tma_load_4d_at(dst, map, 0, I.g, t * AT_TILE, bb, &full[st]);
-            tma_load_4d_at(dst + AT_HALF_BYTES, map, 64, I.g, t * AT_TILE, bb, &full[st]);
-            ++c;
-          };
-          const int bk = I.b * P.mul_k, bv = I.b * P.mul_v;
-          // in the order of their last use: K0 V0 K1 V1 .. for a pair; K0 K1 V0 K2 V1 K3 .. otherwise
-          load(mk, 0, bk);
-          if (!I.pair && I.n > 1) load(mk, 1, bk);
-          for (int j = 0; ok && j < I.n; ++j) {
-            load(mv, j, bv);
-            const int jk = j + (I.pair ? 1 : 2);
-            if (jk < I.n) load(mk, jk, bk);
-          }
-        }
-        // copies still in flight land before the CTA leaves
-        for (uint32_t i = c > AT_STAGES ? c - AT_STAGES : 0; i < c; ++i)
-          attn_wait(&full[i % AT_STAGES], (i / AT_STAGES) & 1, status);
-        if (qc) attn_wait(qfull, (qc - 1) & 1, status);
+  // Next work item of a role: waits for its description, copies what the role keeps and hands the ring place back.
+  uint32_t seq = 0;
+  auto next_item = [&](AttnItem &I) {
+    const uint32_t e = seq % AT_ITEMS;
+    bool ok = attn_wait_warp(&ifull[e], (seq / AT_ITEMS) & 1, status);
+    I.kind = -1;
+    if (ok) {
+      I = items[e];
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&iempty[e]);
+      ++seq;
+    }
+    return ok;
+  };
+
+  if (warp == AT_W_PLAN) {
+    // ---- work items, in order.  Every lane works everything out, lane 0 writes.
+    bool ok = true;
+    auto put = [&](const AttnItem &I) {
+      const uint32_t e = seq % AT_ITEMS;
+      if (!ok || !(ok = attn_wait_warp(&iempty[e], ((seq / AT_ITEMS) & 1) ^ 1, status))) return;
+      if (lane == 0) {
+        items[e] = I;
+        mbar_arrive(&ifull[e]);
       }
-    } else if (warp == AT_W_MMA) {
-      {   // ---- MMA issue, the whole warp in step
-        constexpr uint32_t ab = FP16 ? 0u : 1u;
-        constexpr uint32_t ID_S = (1u << 4) | (ab << 7) | (ab << 10) | ((uint32_t)(AT_TILE >> 3) << 17) |
-                                  ((uint32_t)(AT_TILE >> 4) << 24);
-        constexpr uint32_t ID_O = ID_S | (1u << 16);   // B (values) with its N side contiguous
-        uint32_t base = 0, qc = 0, pc[2] = {0, 0};
-        bool ok = true;
-        for (int it = blockIdx.x; ok && it < P.items; it += gridDim.x) {
-          const AttnItem I = attn_item(P, it);
-          if (I.n == 0) continue;
-          const int n = I.n, ns[2] = {I.pair ? n : (n + 1) >> 1, I.pair ? n : n >> 1};
-          if (!(ok = attn_wait_warp(qfull, qc & 1, status))) break;
-          ++qc;
-          auto issue_s = [&](int s, int i) {
-            const int j = I.pair ? i : 2 * i + s;
-            const uint32_t cc = base + (I.pair ? 2 * j : j < 2 ? j : 2 * j - 1), st = cc % AT_STAGES;
-            if (!ok || !(ok = attn_wait_warp(&full[st], (cc / AT_STAGES) & 1, status))) return;
-            tc_fence_after();
-            const uint32_t a0 = smem_u32(sm) + (I.pair ? s * AT_TILE_BYTES : 0);
-            const uint32_t b0 = smem_u32(sm) + AT_OFF_KV + st * AT_TILE_BYTES;
-            tc_mma_tile_ss(tmem + 128 * s, umma_desc(a0), umma_desc(b0), ID_S);
-            tc_commit_elect(&sfull[s]);
-            if (!I.pair || s == 1) tc_commit_elect(&empty[st]);
-          };
-          issue_s(0, 0);
-          if (ns[1]) issue_s(1, 0);
-          if (ns[0] == 1) tc_commit_elect(qempty);
-          for (int i = 0; ok && i < ns[0]; ++i) {
-            for (int s = 0; ok && s < 2; ++s) {
-              if (i >= ns[s]) continue;
-              const int j = I.pair ? i : 2 * i + s;
-              const uint32_t cc = base + (I.pair ? 2 * j + 1 : j + min(n, j + 2)), st = cc % AT_STAGES;
-              if (!(ok = attn_wait_warp(&full[st], (cc / AT_STAGES) & 1, status))) break;
-              if (!(ok = attn_wait_warp(&pfull[s], pc[s] & 1, status))) break;
-              ++pc[s];
-              tc_fence_after();
-              const uint32_t v0 = smem_u32(sm) + AT_OFF_KV + st * AT_TILE_BYTES;
-              tc_mma_tile_ts(tmem + 256 + 128 * s, tmem + 128 * s, umma_desc_v(v0), ID_O, i > 0);
-              if (!I.pair || s == 1) tc_commit_elect(&empty[st]);
-              if (i + 1 < ns[s]) {
-                issue_s(s, i + 1);
-                if (i + 1 == ns[0] - 1 && (s == 1 || ns[1] < ns[0])) tc_commit_elect(qempty);
-              } else {
-                tc_commit_elect(&ofull[s]);
-                if (lane == 0) mbar_arrive(&ofull[s]);   // orders what the slots wrote (bad_item) before the reader
-                __syncwarp();
-              }
-            }
+      ++seq;
+    };
+    auto own_item = [&](const AttnGroup &A, int g) {
+      AttnItem I;
+      I.kind = A.tile0 * P.tpt + P.tpt < A.ql ? 2 : 0;
+      I.b = A.b, I.g = g, I.tile0 = A.tile0, I.kl = A.kl, I.ql = A.ql, I.pfx = A.pfx;
+      I.n = A.t_hi - A.t_lo;
+      I.t_hi = A.t_hi;
+      I.clean_lo = A.clean_lo, I.clean_hi = A.clean_hi, I.key_lo = A.key_lo, I.key_hi = A.key_hi;
+      I.part = 0;
+      return I;
+    };
+    const int groups = P.n_pr * P.batch;
+    if (blockIdx.x == 0)   // lengths out of range are clamped everywhere; here they are reported
+      for (int b = lane; b < P.batch; b += 32)
+        if ((P.kv_len && (P.kv_len[b] < 0 || P.kv_len[b] > P.s_kv)) || (P.q_len && (P.q_len[b] < 0 || P.q_len[b] > P.s_q)))
+          atomicOr(status, QV_ERR_BOUNDS);
+    if (!P.stream) {
+      // whole units, the longest (last rows of causal prompts) first, every second round in reverse so that the CTAs'
+      // sums come out even
+      const int units = groups * P.h_kv;
+      for (int r = 0; r * (int)gridDim.x < units; ++r) {
+        const int u = r * gridDim.x + ((r & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
+        if (u >= units) continue;
+        const int x = u / P.h_kv, pr = x / P.batch;
+        put(own_item(attn_group(P, (P.n_pr - 1 - pr) * P.batch + (x - pr * P.batch)), u - x * P.h_kv));
+      }
+    } else {
+      // The key tiles of all units, prefix first, as one stream; CTA c takes tiles [c share, (c + 1) share).  A unit cut by a
+      // share's end is written as parts, numbered CTA + unit: the numbers of a unit's parts are consecutive, and none is
+      // used twice, since both terms only grow along the stream.
+      const int tp = P.pre ? (P.pre + AT_TILE - 1) / AT_TILE : 0, wp = attn_places(tp), all_p = P.pre ? P.n_prp * P.h_kv * wp : 0;
+      int pos = 0, end = 0, share = 1;
+      AttnGroup A;
+      int done = 0;   // stream position of the groups at hand
+      for (int pass = 0; ok && pass < 2; ++pass) {   // the sum of all places, then the items
+        done = pass ? all_p : 0;
+        for (int g0 = 0; ok && g0 < groups; g0 += 32) {
+          if (pass == 0 || groups > 32) A = attn_group(P, min(g0 + lane, groups - 1));
+          const int t = g0 + lane < groups ? A.t_hi - A.t_lo : 0;
+          const int total = __reduce_add_sync(0xffffffffu, attn_places(t)) * P.h_kv;
+          if (pass == 0 || done + total <= pos || pos >= end) {
+            done += total;
+            continue;
           }
-          base += 2 * n;
+#pragma unroll 1
+          for (int q = 0; ok && pos < end && q < 32; ++q) {
+            const int tq = __shfl_sync(0xffffffffu, t, q), wq = attn_places(tq);
+            if (done + wq * P.h_kv <= pos) {
+              done += wq * P.h_kv;
+              continue;
+            }
+            AttnGroup B;
+            B.b = __shfl_sync(0xffffffffu, A.b, q), B.tile0 = __shfl_sync(0xffffffffu, A.tile0, q);
+            B.kl = __shfl_sync(0xffffffffu, A.kl, q), B.ql = __shfl_sync(0xffffffffu, A.ql, q);
+            B.pfx = __shfl_sync(0xffffffffu, A.pfx, q);
+            B.clean_lo = __shfl_sync(0xffffffffu, A.clean_lo, q), B.clean_hi = __shfl_sync(0xffffffffu, A.clean_hi, q);
+            B.key_lo = __shfl_sync(0xffffffffu, A.key_lo, q), B.key_hi = __shfl_sync(0xffffffffu, A.key_hi, q);
+            B.t_lo = __shfl_sync(0xffffffffu, A.t_lo, q), B.t_hi = __shfl_sync(0xffffffffu, A.t_hi, q);
+            while (ok && pos < min(end, done + wq * P.h_kv)) {
+              const int g = (pos - done) / wq, u0 = done + g * wq, o = pos - u0;
+              if (o < tq) {
+                AttnItem I = own_item(B, g);
+                I.n = min(tq - o, end - pos);
+                I.t_hi -= o;
+                I.part = blockIdx.x + (g0 + q) * P.h_kv + g;
+                if (P.pre || u0 / share != (u0 + tq - 1) / share) I.kind |= 4;
+                put(I);
+              }
+              pos = u0 + wq;
+            }
+            done += wq * P.h_kv;
+          }
         }
-        // every MMA issued above has completed before the CTA leaves: the softmax warps wait for ofull
+        if (pass == 0) {
+          const int64_t total = (int64_t)all_p + done;
+          share = attn_share((int)total, gridDim.x, P.min_tiles);
+          pos = (int)min((int64_t)blockIdx.x * share, total);
+          end = (int)min((int64_t)pos + share, total);
+          while (ok && pos < min(end, all_p)) {
+            const int u = pos / wp, o = pos - u * wp, pr = u / P.h_kv;
+            if (o < tp) {
+              AttnItem I;
+              I.tile0 = 2 * pr;
+              I.kind = 1 | 4 | ((I.tile0 + 1) * P.nb < P.batch ? 2 : 0);
+              I.b = 0, I.g = u - pr * P.h_kv, I.kl = P.pre, I.ql = P.s_q, I.pfx = 0;
+              I.n = min(tp - o, end - pos);
+              I.t_hi = tp - o;
+              I.clean_lo = I.key_lo = 0;
+              I.clean_hi = I.key_hi = P.pre;
+              I.part = blockIdx.x + u;
+              put(I);
+            }
+            pos = (u + 1) * wp;
+          }
+          if (pos >= end) break;
+        }
       }
     }
-  } else {   // ---- softmax: thread = one row of the slot's tile, one half of its columns
+    AttnItem I = {};
+    I.kind = -1;
+    put(I);
+  } else if (warp == AT_W_LOAD) {
+    // ---- TMA loads
+    const uint32_t qbytes = (uint32_t)(P.G * P.tpt) * 256u, qpbytes = (uint32_t)(P.G * P.s_q * P.nb) * 256u;
+    uint32_t c = 0, qn = 0;
+    bool ok = true;
+    AttnItem I;
+    while (ok && next_item(I) && I.kind >= 0) {
+      if (I.n == 0) continue;
+      if (lane == 0) {
+        const CUtensorMap *mq = I.prefix() ? &P.tqp : &P.tq, *mk = I.prefix() ? &P.tkp : &P.tk,
+                          *mv = I.prefix() ? &P.tvp : &P.tv;
+        const bool pair = I.pair();
+        auto load = [&](const CUtensorMap *map, int j, int bb) {
+          const uint32_t st = c % AT_STAGES;
+          if (!ok || !(ok = attn_wait(&empty[st], ((c / AT_STAGES) & 1) ^ 1, status))) return;
+          const uint32_t dst = smem_u32(sm) + AT_OFF_KV + st * AT_TILE_BYTES;
+          const int t = I.t_hi - 1 - j;
+          mbar_arrive_expect_tx(&full[st], AT_TILE_BYTES);
+          tma_load_4d_at(dst, map, 0, I.g, t * AT_TILE, bb, &full[st]);
+          tma_load_4d_at(dst + AT_HALF_BYTES, map, 64, I.g, t * AT_TILE, bb, &full[st]);
+          ++c;
+        };
+        for (int s = 0; ok && s < (pair ? 2 : 1); ++s) {
+          const uint32_t qb = qn & 1, dst = smem_u32(sm) + qb * AT_TILE_BYTES;
+          if (!(ok = attn_wait(&qempty[qb], ((qn >> 1) & 1) ^ 1, status))) break;
+          mbar_arrive_expect_tx(&qfull[qb], I.prefix() ? qpbytes : qbytes);
+          const int tok = I.prefix() ? 0 : (I.tile0 + s) * P.tpt, bb = I.prefix() ? (I.tile0 + s) * P.nb : I.b * P.mul_q;
+          tma_load_4d_at(dst, mq, 0, I.g * P.G, tok, bb, &qfull[qb]);
+          tma_load_4d_at(dst + AT_HALF_BYTES, mq, 64, I.g * P.G, tok, bb, &qfull[qb]);
+          ++qn;
+        }
+        const int bk = I.b * P.mul_k, bv = I.b * P.mul_v;
+        // in the order of their last use: K0 V0 K1 V1 .. for a pair; K0 K1 V0 K2 V1 K3 .. otherwise
+        load(mk, 0, bk);
+        if (!pair && I.n > 1) load(mk, 1, bk);
+        for (int j = 0; ok && j < I.n; ++j) {
+          load(mv, j, bv);
+          const int jk = j + (pair ? 1 : 2);
+          if (jk < I.n) load(mk, jk, bk);
+        }
+      }
+      ok = __shfl_sync(0xffffffffu, (int)ok, 0);
+    }
+    if (lane == 0) {   // copies still in flight land before the CTA leaves
+      for (uint32_t i = c > AT_STAGES ? c - AT_STAGES : 0; i < c; ++i)
+        attn_wait(&full[i % AT_STAGES], (i / AT_STAGES) & 1, status);
+      for (uint32_t i = qn > 2 ? qn - 2 : 0; i < qn; ++i) attn_wait(&qfull[i & 1], (i >> 1) & 1, status);
+    }
+    __syncwarp();
+  } else if (warp == AT_W_MMA) {
+    // ---- MMA issue, the whole warp in step, slot after slot: P V and the next S of slot 0, then of slot 1.  (A warp per
+    // slot lets the products of both slots interleave, so each finishes as late as both, and the slots fall into step
+    // instead of alternating: 6.99 ms against 5.6 for a 32K prompt of 32 heads.)  A slot's S(i + 1) overwrites P(i) after P V(i):
+    // the tensor pipe runs in the order of issue.  The warp meets the ring's tiles in order, so a phase parity is enough.
+    constexpr uint32_t ab = FP16 ? 0u : 1u;
+    constexpr uint32_t ID_S = (1u << 4) | (ab << 7) | (ab << 10) | ((uint32_t)(AT_TILE >> 3) << 17) |
+                              ((uint32_t)(AT_TILE >> 4) << 24);
+    constexpr uint32_t ID_O = ID_S | (1u << 16);   // B (values) with its N side contiguous
+    const uint64_t dq0 = umma_desc(smem_u32(sm)), dk0 = umma_desc(smem_u32(sm) + AT_OFF_KV),
+                   dv0 = umma_desc_v(smem_u32(sm) + AT_OFF_KV);
+    uint32_t base = 0, qn = 0, pc0 = 0, pc1 = 0;
+    bool ok = true;
+    AttnItem I;
+    auto issue_s = [&](int s, uint32_t kpos, uint32_t qb, bool last) {
+      const uint32_t st = kpos % AT_STAGES;
+      ok = attn_wait_warp(&full[st], (kpos / AT_STAGES) & 1, status);
+      tc_fence_after();
+      tc_mma_tile_ss(tmem + 128 * s, dq0 + qb * (AT_TILE_BYTES >> 4), dk0 + st * (AT_TILE_BYTES >> 4), ID_S);
+      tc_commit_elect(&sfull[s]);
+      if (last) tc_commit_elect(&empty[st]);
+    };
+    auto issue_pv = [&](int s, uint32_t vpos, uint32_t pph, bool first, bool final, bool last) {
+      const uint32_t st = vpos % AT_STAGES;
+      attn_wait(&full[st], (vpos / AT_STAGES) & 1, status);
+      ok = attn_wait_warp(&pfull[s], pph, status);
+      tc_fence_after();
+      tc_mma_tile_ts(tmem + 256 + 128 * s, tmem + 128 * s, dv0 + st * (AT_TILE_BYTES >> 4), ID_O, !first);
+      if (last) tc_commit_elect(&empty[st]);
+      if (final) {
+        tc_commit_elect(&ofull[s]);
+        if (lane == 0) mbar_arrive(&ofull[s]);   // orders what the slots wrote (bad_item) before the reader
+        __syncwarp();
+      }
+    };
+    while (ok && next_item(I) && I.kind >= 0) {
+      const int n = I.n;
+      if (n == 0) continue;
+      const bool pair = I.pair();
+      const uint32_t q0 = qn & 1, q1 = pair ? (qn + 1) & 1 : q0;
+      ok = attn_wait_warp(&qfull[q0], (qn >> 1) & 1, status);
+      if (pair) ok = ok && attn_wait_warp(&qfull[q1], ((qn + 1) >> 1) & 1, status);
+      qn += pair ? 2 : 1;
+      if (ok && pair) {
+        issue_s(0, base, q0, false);
+        if (ok) issue_s(1, base, q1, true);
+        for (int i = 0; ok && i < n; ++i) {
+          const bool end = i == n - 1;
+          if (end) {   // every S of the item has been issued
+            tc_commit_elect(&qempty[q0]);
+            tc_commit_elect(&qempty[q1]);
+          }
+          issue_pv(0, base + 1, pc0++ & 1, i == 0, end, false);
+          if (ok && !end) issue_s(0, base + 2, q0, false);
+          if (ok) issue_pv(1, base + 1, pc1++ & 1, i == 0, end, true);
+          if (ok && !end) issue_s(1, base + 2, q1, true);
+          base += 2;
+        }
+      } else if (ok) {
+        const int n0 = (n + 1) >> 1, n1 = n >> 1;
+        auto kpos = [&](int j) { return base + (j < 2 ? j : 2 * j - 1); };
+        auto vpos = [&](int j) { return base + (j + min(n, j + 2)); };
+        issue_s(0, base, q0, true);
+        if (ok && n1) issue_s(1, base + 1, q0, true);
+        for (int i = 0; ok && i < n0; ++i) {
+          if (i == n0 - 1) tc_commit_elect(&qempty[q0]);
+          issue_pv(0, vpos(2 * i), pc0++ & 1, i == 0, i == n0 - 1, true);
+          if (ok && i + 1 < n0) issue_s(0, kpos(2 * i + 2), q0, true);
+          if (ok && i < n1) {
+            issue_pv(1, vpos(2 * i + 1), pc1++ & 1, i == 0, i == n1 - 1, true);
+            if (ok && i + 1 < n1) issue_s(1, kpos(2 * i + 3), q0, true);
+          }
+        }
+        base += 2 * n;
+      }
+    }
+    // every product issued above has completed before the CTA leaves: the softmax warps wait for ofull
+  } else {
+    // ---- softmax: thread = one row of the slot's tile, one half of its columns
     const int slot = warp >> 3, half = (warp >> 2) & 1, wq = warp & 3, row = wq * 32 + lane;
     const uint32_t lane_base = tmem + ((uint32_t)(wq * 32) << 16);
     const uint32_t ts = lane_base + 128 * slot + AT_COLS * half;   // S, and its half of P
     const uint32_t to = lane_base + 256 + 128 * slot + AT_COLS * half;
     float *x_own = xch + (2 * slot + half) * AT_TILE + row, *x_other = xch + (2 * slot + (half ^ 1)) * AT_TILE + row;
     const int pair_bar = AT_BAR_PAIR + 4 * slot + wq;   // the two warps that share these rows
-    uint32_t sc = 0, oc = 0, base = 0, seq = 0;
+    const AttnRow R = attn_row_of(P, row);
+    uint32_t sc = 0, oc = 0, base = 0;
     bool ok = true;   // after a wait that ran out the loops go on without waiting, so all warps meet at every barrier
-    for (int it = blockIdx.x; it < P.items; it += gridDim.x) {
-      const AttnItem I = attn_item(P, it);
-      const int n_s = I.pair ? I.n : (I.n + 1 - slot) >> 1;
-      int b, i, h, it_again = it;
-      bool valid = attn_row(P, I, slot, row, b, i, h);
+    for (;;) {
+      AttnItem I;
+      const bool got = next_item(I);
+      // all softmax warps go on together or stop together: none is left alone at a barrier
+      int stop;
+      asm volatile(
+          "{\n .reg .pred p, q;\n setp.ne.s32 p, %1, 0;\n barrier.cta.red.or.aligned.pred q, %2, %3, p;\n selp.s32 %0, 1, 0, q;\n}"
+          : "=r"(stop)
+          : "r"((int)(!got || I.kind < 0)), "r"(AT_BAR_ALL), "r"(AT_SOFT * 32)
+          : "memory");
+      if (stop) break;
+      const bool pair = I.pair();
+      const int n_s = pair ? I.n : (I.n + 1 - slot) >> 1;
+      int b, i, h, prow;
+      const bool valid = attn_row(P, I, slot, R, b, i, h, prow);
       const bool any_row = __any_sync(0xffffffffu, valid);
       int lo = 0, hi = 1 << 30;   // padding rows take no masks: nothing reads what they compute
       float pos = 0.f, slope = 0.f;
       if (valid) {
-        if (I.prefix) {
+        if (I.prefix()) {
           hi = P.pre;
           if (BIAS) pos = (float)(P.pre + (P.kv_len ? clampi(P.kv_len[b], 0, P.s_kv) : P.s_kv) - P.s_q + i);
         } else {
           const int p = I.kl - I.ql + i;
-          const int2 v = attn_interval(P, b, p, I.kl);
+          const int2 v = attn_interval(P, b, p, I.kl, I.pfx);
           lo = v.x, hi = v.y;
           if (BIAS) pos = (float)p;
         }
@@ -588,7 +762,7 @@ __global__ void __launch_bounds__(AT_THREADS, 1) attn_kernel(const __grid_consta
       const float scale2 = BIAS ? 1.f : CAP ? 2.f * P.cap_log2 : P.scale_log2;
       float m = -INFINITY, l = 0.f;
       for (int k = 0; k < n_s; ++k) {
-        const int t = I.t_hi - 1 - (I.pair ? k : 2 * k + slot), c0 = t * AT_TILE + half * AT_COLS;
+        const int t = I.t_hi - 1 - (pair ? k : 2 * k + slot), c0 = t * AT_TILE + half * AT_COLS;
         if (ok) ok = attn_wait(&sfull[slot], sc & 1, status);
         ++sc;
         __syncwarp();
@@ -599,7 +773,7 @@ __global__ void __launch_bounds__(AT_THREADS, 1) attn_kernel(const __grid_consta
           float x0 = -INFINITY, x1 = -INFINITY;
           const int a = lo - c0, z = hi - c0;   // the row sees columns [a, z)
           const bool masked = __any_sync(0xffffffffu, a > 0 || z < AT_COLS);
-#pragma unroll
+#pragma unroll 1
           for (int q = 0; q < 2; ++q) {
             uint32_t raw[32];
             float *v = reinterpret_cast<float *>(raw);
@@ -615,9 +789,10 @@ __global__ void __launch_bounds__(AT_THREADS, 1) attn_kernel(const __grid_consta
               for (int j = 0; j < 32; ++j) v[j] = fmaf(-slope, fabsf(d0 - (float)j), v[j] * sl);
             }
             if (masked) {
+              const int aq = a - 32 * q, zq = z - 32 * q;
 #pragma unroll
               for (int j = 0; j < 32; ++j)
-                if (32 * q + j < a || 32 * q + j >= z) v[j] = -INFINITY;
+                if (j < aq || j >= zq) v[j] = -INFINITY;
             }
             if (CAP || BIAS || masked) {   // the second pass reads the finished logits
               tmem_st16(ts + 32 * q, raw);
@@ -649,7 +824,7 @@ __global__ void __launch_bounds__(AT_THREADS, 1) attn_kernel(const __grid_consta
             }
             l *= f;
             if (k > 0) {
-#pragma unroll
+#pragma unroll 1
               for (int q = 0; q < 4; ++q) {
                 uint32_t o[16];
                 tmem_ld16(to + 16 * q, o);
@@ -662,13 +837,10 @@ __global__ void __launch_bounds__(AT_THREADS, 1) attn_kernel(const __grid_consta
           }
           const float mu = m == -INFINITY ? 0.f : m;
           float a0 = 0.f, a1 = 0.f, a2 = 0.f, a3 = 0.f;
-          uint32_t buf[2][16];
-          tmem_ld16(ts, buf[0]);
-#pragma unroll
-          for (int q = 0; q < 4; ++q) {   // the next 16 columns are on their way while these are worked on
-            const float *v = reinterpret_cast<const float *>(buf[q & 1]);
-            tmem_wait_ld();
-            if (q < 3) tmem_ld16(ts + 16 * (q + 1), buf[(q + 1) & 1]);
+          // 16 columns at a time, the next 16 on their way while these are worked on; the loop is kept short, since
+          // instructions that are met for the first time cost about ten cycles each
+          auto probs = [&](const uint32_t (&raw)[16], uint32_t at) {
+            const float *v = reinterpret_cast<const float *>(raw);
             uint32_t pk[8];
 #pragma unroll
             for (int j = 0; j < 16; j += 4) {
@@ -681,30 +853,37 @@ __global__ void __launch_bounds__(AT_THREADS, 1) attn_kernel(const __grid_consta
               pk[j / 2] = pack2<FP16>(e0, e1);
               pk[j / 2 + 1] = pack2<FP16>(e2, e3);
             }
-            tmem_st8(ts + 8 * q, pk);   // over columns already read
+            tmem_st8(at, pk);   // over columns already read
+          };
+          uint32_t buf0[16], buf1[16];
+          tmem_ld16(ts, buf0);
+#pragma unroll 1
+          for (int q = 0; q < 2; ++q) {
+            tmem_wait_ld();
+            tmem_ld16(ts + 32 * q + 16, buf1);
+            probs(buf0, ts + 16 * q);
+            tmem_wait_ld();
+            if (q == 0) tmem_ld16(ts + 32, buf0);
+            probs(buf1, ts + 16 * q + 8);
           }
           l += (a0 + a1) + (a2 + a3);
           tmem_wait_st();
         }
-        if (attn_mixed(I, t) && (!I.pair || slot == 0)) {   // slot 1's product comes after slot 0's
-          const int j = I.pair ? k : 2 * k + slot;
-          const uint32_t cc = base + (I.pair ? 2 * j + 1 : j + min(I.n, j + 2)), st = cc % AT_STAGES;
-          if (ok) ok = attn_wait(&full[st], (cc / AT_STAGES) & 1, status);
-          if (attn_clean_values<FP16>(I, t, sm + AT_OFF_KV + st * AT_TILE_BYTES, threadIdx.x & 255)) bad_item[seq & 1] = it + 1;
+        if (attn_mixed(I, t)) {
+          const int j = pair ? k : 2 * k + slot;
+          const uint32_t vpos = base + (pair ? 2 * j + 1 : j + min(I.n, j + 2)), st = vpos % AT_STAGES;
+          if (ok) ok = attn_wait(&full[st], (vpos / AT_STAGES) & 1, status);
+          attn_clean_values<FP16>(I, t, sm + AT_OFF_KV + st * AT_TILE_BYTES, threadIdx.x & 255, &bad_item[seq & 1], seq);
         }
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&pfull[slot]);
       }
-      // ---- the item's rows are done (what the loop does not need is worked out again: it would only fill registers)
-      asm volatile("" : "+r"(it_again));
-      const AttnItem E = attn_item(P, it_again);
-      valid = attn_row(P, E, slot, row, b, i, h);
+      // ---- the item's rows are done
       const float off = CAP ? P.cap_log2 : 0.f;   // of the base-2 logits
-      const int split = E.prefix ? P.ns + E.sp : E.sp;
       // a single row tile: slot 0 joins its rows with slot 1's, which stand in the same lanes
-      const bool join = !I.pair && I.n > 1;
-      const bool writes = I.pair || slot == 0;
+      const bool join = !pair && I.n > 1;
+      const bool writes = pair || slot == 0;
       bool bad = false;
       float m1 = -INFINITY, l1 = 0.f;
       if (n_s > 0) {
@@ -724,25 +903,26 @@ __global__ void __launch_bounds__(AT_THREADS, 1) attn_kernel(const __grid_consta
           m1 = m_slot1[row];
           l1 = xch[2 * AT_TILE + row] + xch[3 * AT_TILE + row];
         }
-        bad = bad_item[seq & 1] == it + 1;
+        bad = bad_item[seq & 1] == (int)seq;
       }
       if (writes && any_row) {
+        float *part_o = I.prefix() ? P.pre_o : P.part_o, *part_l = I.prefix() ? P.pre_l : P.part_l;
+        const int64_t part_row = (int64_t)I.part * (I.prefix() ? P.pre_rows : P.part_rows);
         const float mm = fmaxf(m, m1), mu = mm == -INFINITY ? 0.f : mm;
         const float w0 = ex2(m - mu), w1 = ex2(m1 - mu);
         const float lt = l * w0 + l1 * w1;
         const float inv = lt == 0.f ? 0.f : 1.f / lt;   // an empty row is 0
         const float lse2 = lt == 0.f ? -INFINITY : mu + off + log2f(lt);
-        const int64_t prow = ((int64_t)b * P.s_q + i) * P.h_q + h;
         if (!bad) {
           if (valid && half == 0) {
-            if (P.part_o)
-              P.part_l[split * P.rows + prow] = lse2;
+            if (I.parts())
+              part_l[part_row + prow] = lse2;
             else if (P.lse)
-              P.lse[prow] = lse2 * 0.69314718055994531f;
+              P.lse[((int64_t)b * P.s_q + i) * P.h_q + h] = lse2 * 0.69314718055994531f;
           }
           const bool have0 = n_s > 0;
           const float f0 = w0 * inv, f1 = w1 * inv;
-#pragma unroll
+#pragma unroll 1
           for (int q = 0; q < 4; ++q) {
             uint32_t o[16];
             float *of = reinterpret_cast<float *>(o);
@@ -766,34 +946,39 @@ __global__ void __launch_bounds__(AT_THREADS, 1) attn_kernel(const __grid_consta
               for (int j = 0; j < 16; ++j) of[j] = 0.f;
             }
             if (valid) {
-              if (P.part_o) {
-                float4 *dst = reinterpret_cast<float4 *>(P.part_o + (split * P.rows + prow) * D + AT_COLS * half + 16 * q);
-                if (lse2 != -INFINITY)
-#pragma unroll
-                  for (int j = 0; j < 4; ++j) dst[j] = make_float4(of[4 * j], of[4 * j + 1], of[4 * j + 2], of[4 * j + 3]);
+              if (I.parts()) {
+                float *dst = part_o + (part_row + prow) * D + AT_COLS * half + 16 * q;
+                if (lse2 != -INFINITY) {
+                  st_global_v8(dst, o);
+                  st_global_v8(dst + 8, o + 8);
+                }
               } else {
-                uint4 *dst = reinterpret_cast<uint4 *>(static_cast<uint16_t *>(P.out) + b * P.so[0] + i * P.so[1] +
-                                                       h * P.so[2] + AT_COLS * half + 16 * q);
+                uint32_t pk[8];
 #pragma unroll
-                for (int j = 0; j < 2; ++j)
-                  dst[j] = make_uint4(pack2<FP16>(of[8 * j], of[8 * j + 1]), pack2<FP16>(of[8 * j + 2], of[8 * j + 3]),
-                                      pack2<FP16>(of[8 * j + 4], of[8 * j + 5]), pack2<FP16>(of[8 * j + 6], of[8 * j + 7]));
+                for (int j = 0; j < 8; ++j) pk[j] = pack2<FP16>(of[2 * j], of[2 * j + 1]);
+                uint16_t *dst = static_cast<uint16_t *>(P.out) + b * P.so[0] + i * P.so[1] + h * P.so[2] + AT_COLS * half +
+                                16 * q;
+                if (P.wide_out) {
+                  st_global_v8(dst, pk);
+                } else {
+                  reinterpret_cast<uint4 *>(dst)[0] = make_uint4(pk[0], pk[1], pk[2], pk[3]);
+                  reinterpret_cast<uint4 *>(dst)[1] = make_uint4(pk[4], pk[5], pk[6], pk[7]);
+                }
               }
             }
           }
         } else if (half == 0) {
-          attn_exact_rows<FP16>(P, E, slot, wq, lane, CAP,
-                                [&](int, int rb, int ri, int rh, const float (&acc)[4], float rm, float rl) {
-            const int64_t pr = ((int64_t)rb * P.s_q + ri) * P.h_q + rh;
+          attn_exact_rows<FP16>(P, I, slot, wq, lane, CAP,
+                                [&](int rb, int ri, int rh, int rp, const float (&acc)[4], float rm, float rl) {
             const float ri_l = rl == 0.f ? 0.f : 1.f / rl;
             const float ls = rl == 0.f ? -INFINITY : rm + log2f(rl);
             const float o0 = rl == 0.f ? 0.f : acc[0] * ri_l, o1 = rl == 0.f ? 0.f : acc[1] * ri_l;
             const float o2 = rl == 0.f ? 0.f : acc[2] * ri_l, o3 = rl == 0.f ? 0.f : acc[3] * ri_l;
-            if (P.part_o) {
-              if (lane == 0) P.part_l[split * P.rows + pr] = ls;
-              *reinterpret_cast<float4 *>(P.part_o + (split * P.rows + pr) * D + 4 * lane) = make_float4(o0, o1, o2, o3);
+            if (I.parts()) {
+              if (lane == 0) part_l[part_row + rp] = ls;
+              *reinterpret_cast<float4 *>(part_o + (part_row + rp) * D + 4 * lane) = make_float4(o0, o1, o2, o3);
             } else {
-              if (lane == 0 && P.lse) P.lse[pr] = ls * 0.69314718055994531f;
+              if (lane == 0 && P.lse) P.lse[((int64_t)rb * P.s_q + ri) * P.h_q + rh] = ls * 0.69314718055994531f;
               *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(P.out) + rb * P.so[0] + ri * P.so[1] + rh * P.so[2] +
                                          4 * lane) = make_uint2(pack2<FP16>(o0, o1), pack2<FP16>(o2, o3));
             }
@@ -807,7 +992,6 @@ __global__ void __launch_bounds__(AT_THREADS, 1) attn_kernel(const __grid_consta
         tc_fence_after();
       }
       base += 2 * I.n;
-      ++seq;
     }
   }
   tc_fence_before();

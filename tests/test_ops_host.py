@@ -165,9 +165,9 @@ def test_prefix_attention_pointers(lib, i):
 def test_workspace_sizes(lib):
     """256 bytes of status, the document runs, and the split results when the keys are split."""
     n = ctypes.c_size_t()
-    big = attn_desc(batch=64, s_q=1, s_kv=1024, h_q=32, h_kv=8)
-    assert lib.qevict_attn_bytes(ctypes.byref(big), ctypes.byref(n)) == B.OK
-    assert n.value == 256 + 64 * 1024 * 8
+    short = attn_desc(batch=64, s_q=1, s_kv=256, h_q=32, h_kv=8)
+    assert lib.qevict_attn_bytes(ctypes.byref(short), ctypes.byref(n)) == B.OK
+    assert n.value == 256 + 64 * 256 * 8
     one = attn_desc(batch=1, s_q=1, s_kv=32768, h_q=32, h_kv=8)
     assert lib.qevict_attn_bytes(ctypes.byref(one), ctypes.byref(n)) == B.OK
     assert n.value > 256 + 32768 * 8
