@@ -12,8 +12,10 @@
 #include "qevict.h"
 
 namespace qv {
-cudaError_t launch_attn_bf16(const AttnArgs &P, int grid, bool cap, bool bias, cudaStream_t s);
-cudaError_t launch_attn_fp16(const AttnArgs &P, int grid, bool cap, bool bias, cudaStream_t s);
+cudaError_t launch_attn_bf16(const AttnArgs &P, int grid, bool bias, cudaStream_t s);
+cudaError_t launch_attn_fp16(const AttnArgs &P, int grid, bool bias, cudaStream_t s);
+cudaError_t launch_attn_bf16_cap(const AttnArgs &P, int grid, bool bias, cudaStream_t s);
+cudaError_t launch_attn_fp16_cap(const AttnArgs &P, int grid, bool bias, cudaStream_t s);
 
 // First and past-the-last position of every position's run of equal ids.  One CTA per sequence; thread i
 // takes the i-th of 1024 consecutive pieces, finds the first and last run start in it, and two block
@@ -285,8 +287,6 @@ qevict_status attn_launch(const qevict_attn_desc *d, const AttnPlan &pl, const q
   A.pre = pl.pre, A.nb = std::max(1, pl.nb), A.n_prp = pl.n_prp;
   A.part_rows = pl.part_rows, A.pre_rows = pl.pre_rows;
   A.stream = pl.stream, A.min_tiles = MIN_TILES;
-  A.wide_out = ((uintptr_t)out & 31) == 0 && (d->batch == 1 || d->o[0] % 16 == 0) && (d->s_q == 1 || d->o[1] % 16 == 0) &&
-               (d->h_q == 1 || d->o[2] % 16 == 0);
   const float scale = d->scale > 0.f ? d->scale : 1.f / std::sqrt((float)D), log2e = 1.4426950408889634f;
   A.scale_log2 = scale * log2e;
   if (d->softcap > 0.f) {
@@ -316,8 +316,9 @@ qevict_status attn_launch(const qevict_attn_desc *d, const AttnPlan &pl, const q
     A.pre_l = reinterpret_cast<float *>(w + pl.off_pl);
     A.pre_o = reinterpret_cast<float *>(w + pl.off_po);
   }
-  if ((fp16 ? launch_attn_fp16 : launch_attn_bf16)(A, pl.grid, d->softcap > 0.f, m.slopes != nullptr, s) != cudaSuccess)
-    return QEVICT_ECUDA;
+  const auto launch = d->softcap > 0.f ? (fp16 ? launch_attn_fp16_cap : launch_attn_bf16_cap)
+                                       : (fp16 ? launch_attn_fp16 : launch_attn_bf16);
+  if (launch(A, pl.grid, m.slopes != nullptr, s) != cudaSuccess) return QEVICT_ECUDA;
   if (pl.stream) {
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[1];

@@ -1,8 +1,8 @@
-// The attention kernel for bf16 inputs.
+// The attention kernel for bf16 inputs, plain and biased scores.
 #include "attn_dev.cuh"
 
 namespace qv {
-cudaError_t launch_attn_bf16(const AttnArgs &P, int grid, bool cap, bool bias, cudaStream_t s) {
-  return launch_attn_type<false>(P, grid, cap, bias, s);
+cudaError_t launch_attn_bf16(const AttnArgs &P, int grid, bool bias, cudaStream_t s) {
+  return bias ? launch_attn_variant<false, false, true>(P, grid, s) : launch_attn_variant<false, false, false>(P, grid, s);
 }
 }  // namespace qv

@@ -46,7 +46,6 @@ struct AttnArgs {
   int64_t sq[3], sk[3], sv[3], so[3], skp[2], svp[2];
   int batch, s_q, s_kv, h_q, h_kv, G, causal;
   int mul_q, mul_k, mul_v;     // batch coordinate of the tensor maps: 0 for a batch stride of 0
-  int wide_out;                // rows of out are 32-byte aligned
   int tpt, n_pr;               // own keys: tokens per row tile, pairs of row tiles
   int pre, nb, n_prp;          // prefix: keys, sequences per row tile, pairs of row tiles
   int part_rows, pre_rows;     // rows of a part
@@ -147,11 +146,12 @@ __device__ __forceinline__ AttnRow attn_row_of(const AttnArgs &P, int r) {
   return R;
 }
 // Sequence b, query i and head h of the row; its row of a part.  False: the row is padding.
+template <bool STREAM>
 __device__ __forceinline__ bool attn_row(const AttnArgs &P, const AttnItem &I, int slot, const AttnRow &R, int &b, int &i,
                                          int &h, int &prow) {
-  const int second = I.pair() ? slot : 0;
+  const int second = !STREAM || I.pair() ? slot : 0;
   h = I.g * P.G + R.hr;
-  if (I.prefix()) {
+  if (STREAM && I.prefix()) {
     const int bt = second * P.nb + R.bl;
     b = I.tile0 * P.nb + bt;
     i = R.ip;
@@ -315,28 +315,28 @@ template <bool FP16>
 __device__ __forceinline__ void attn_clean_values(const AttnItem &I, int t, uint8_t *v, int who, volatile int *flag, int mark) {
   const int k = who >> 1, key = t * AT_TILE + k;
   if (key >= I.clean_lo && key < I.clean_hi) return;
-  constexpr uint32_t E = FP16 ? 0x7C00u : 0x7F80u;
+  constexpr uint32_t E = FP16 ? 0x7C00u : 0x7F80u, E2 = E | (E << 16);   // all exponent bits set: infinity or NaN
   uint32_t *p = reinterpret_cast<uint32_t *>(v + (who & 1) * AT_HALF_BYTES + k * 128);
-  bool found = false;
-#pragma unroll 2
-  for (int c = 0; c < 8; ++c) {
-    uint32_t *pc = p + ((c + k) & 7) * 4;   // neighbours start in other banks
-    const uint4 x = lds128(pc);
-    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+  // ~w & E2 has an empty half exactly where the half is not finite; taking 1 from both halves then sets its top bit
+  uint32_t hit = 0;
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      const bool lo = (w[q] & E) == E, hi = (w[q] & (E << 16)) == (E << 16);
-      if (lo | hi) {
-        if (!found && key >= I.key_lo && key < I.key_hi) {
-          *flag = mark;
-          __threadfence_block();
-        }
-        pc[q] = (lo ? 0u : w[q] & 0xFFFFu) | (hi ? 0u : w[q] & 0xFFFF0000u);
-        found = true;
-      }
-    }
+  for (int c = 0; c < 8; ++c) {
+    const uint4 x = lds128(p + ((c + k) & 7) * 4);   // neighbours start in other banks
+    hit |= ((~x.x & E2) - 0x00010001u) | ((~x.y & E2) - 0x00010001u) | ((~x.z & E2) - 0x00010001u) | ((~x.w & E2) - 0x00010001u);
   }
-  if (found) fence_proxy_async();   // the product reads shared memory through the async proxy
+  if (hit & 0x80008000u) {
+    if (key >= I.key_lo && key < I.key_hi) {
+      *flag = mark;
+      __threadfence_block();
+    }
+#pragma unroll 1
+    for (int c = 0; c < 32; ++c) {
+      const uint32_t w = p[c];
+      const bool lo = (w & E) == E, hi = (w & (E << 16)) == (E << 16);
+      if (lo | hi) p[c] = (lo ? 0u : w & 0xFFFFu) | (hi ? 0u : w & 0xFFFF0000u);
+    }
+    fence_proxy_async();   // the product reads shared memory through the async proxy
+  }
 }
 
 // The rows of one warp of a slot recomputed on the CUDA cores, every visible key of the item's own tiles in
@@ -359,7 +359,7 @@ __device__ __forceinline__ void attn_exact_rows(const AttnArgs &P, const AttnIte
   }
   for (int rr = 0; rr < 32; ++rr) {
     int b, i, h, prow;
-    if (!attn_row(P, I, slot, attn_row_of(P, warp * 32 + rr), b, i, h, prow)) continue;
+    if (!attn_row<true>(P, I, slot, attn_row_of(P, warp * 32 + rr), b, i, h, prow)) continue;
     const uint16_t *q = static_cast<const uint16_t *>(P.q) + b * P.sq[0] + i * P.sq[1] + h * P.sq[2];
     int p, lo, hi;
     if (I.prefix()) {
@@ -428,7 +428,8 @@ __device__ __forceinline__ void attn_exact_rows(const AttnArgs &P, const AttnIte
 // logits, first.  The running max moves only when a row's max has grown by more than 2^8 (then the warps rescale their
 // rows of O in tensor memory): until then p reaches at most 2^8, which fp32 sums and 16-bit probabilities hold as well.
 // Every wait is bounded; the TMEM columns are released on every path.
-template <bool FP16, bool CAP, bool BIAS>
+// STREAM = false: whole units, always as pairs (of a last odd row tile the second is empty).
+template <bool FP16, bool CAP, bool BIAS, bool STREAM>
 __global__ void __launch_bounds__(AT_THREADS, 1) attn_kernel(const __grid_constant__ AttnArgs P) {
   extern __shared__ __align__(1024) uint8_t sm[];   // swizzle atoms: 1024-aligned
   uint64_t *bars = reinterpret_cast<uint64_t *>(sm + AT_OFF_BAR);
@@ -493,7 +494,7 @@ __global__ void __launch_bounds__(AT_THREADS, 1) attn_kernel(const __grid_consta
     };
     auto own_item = [&](const AttnGroup &A, int g) {
       AttnItem I;
-      I.kind = A.tile0 * P.tpt + P.tpt < A.ql ? 2 : 0;
+      I.kind = !STREAM || A.tile0 * P.tpt + P.tpt < A.ql ? 2 : 0;
       I.b = A.b, I.g = g, I.tile0 = A.tile0, I.kl = A.kl, I.ql = A.ql, I.pfx = A.pfx;
       I.n = A.t_hi - A.t_lo;
       I.t_hi = A.t_hi;
@@ -506,7 +507,7 @@ __global__ void __launch_bounds__(AT_THREADS, 1) attn_kernel(const __grid_consta
       for (int b = lane; b < P.batch; b += 32)
         if ((P.kv_len && (P.kv_len[b] < 0 || P.kv_len[b] > P.s_kv)) || (P.q_len && (P.q_len[b] < 0 || P.q_len[b] > P.s_q)))
           atomicOr(status, QV_ERR_BOUNDS);
-    if (!P.stream) {
+    if (!STREAM) {
       // whole units, the longest (last rows of causal prompts) first, every second round in reverse so that the CTAs'
       // sums come out even
       const int units = groups * P.h_kv;
@@ -600,9 +601,8 @@ __global__ void __launch_bounds__(AT_THREADS, 1) attn_kernel(const __grid_consta
     while (ok && next_item(I) && I.kind >= 0) {
       if (I.n == 0) continue;
       if (lane == 0) {
-        const CUtensorMap *mq = I.prefix() ? &P.tqp : &P.tq, *mk = I.prefix() ? &P.tkp : &P.tk,
-                          *mv = I.prefix() ? &P.tvp : &P.tv;
-        const bool pair = I.pair();
+        const bool prefix = STREAM && I.prefix(), pair = !STREAM || I.pair();
+        const CUtensorMap *mq = prefix ? &P.tqp : &P.tq, *mk = prefix ? &P.tkp : &P.tk, *mv = prefix ? &P.tvp : &P.tv;
         auto load = [&](const CUtensorMap *map, int j, int bb) {
           const uint32_t st = c % AT_STAGES;
           if (!ok || !(ok = attn_wait(&empty[st], ((c / AT_STAGES) & 1) ^ 1, status))) return;
@@ -616,8 +616,8 @@ __global__ void __launch_bounds__(AT_THREADS, 1) attn_kernel(const __grid_consta
         for (int s = 0; ok && s < (pair ? 2 : 1); ++s) {
           const uint32_t qb = qn & 1, dst = smem_u32(sm) + qb * AT_TILE_BYTES;
           if (!(ok = attn_wait(&qempty[qb], ((qn >> 1) & 1) ^ 1, status))) break;
-          mbar_arrive_expect_tx(&qfull[qb], I.prefix() ? qpbytes : qbytes);
-          const int tok = I.prefix() ? 0 : (I.tile0 + s) * P.tpt, bb = I.prefix() ? (I.tile0 + s) * P.nb : I.b * P.mul_q;
+          mbar_arrive_expect_tx(&qfull[qb], prefix ? qpbytes : qbytes);
+          const int tok = prefix ? 0 : (I.tile0 + s) * P.tpt, bb = prefix ? (I.tile0 + s) * P.nb : I.b * P.mul_q;
           tma_load_4d_at(dst, mq, 0, I.g * P.G, tok, bb, &qfull[qb]);
           tma_load_4d_at(dst + AT_HALF_BYTES, mq, 64, I.g * P.G, tok, bb, &qfull[qb]);
           ++qn;
@@ -678,7 +678,7 @@ __global__ void __launch_bounds__(AT_THREADS, 1) attn_kernel(const __grid_consta
     while (ok && next_item(I) && I.kind >= 0) {
       const int n = I.n;
       if (n == 0) continue;
-      const bool pair = I.pair();
+      const bool pair = !STREAM || I.pair();
       const uint32_t q0 = qn & 1, q1 = pair ? (qn + 1) & 1 : q0;
       ok = attn_wait_warp(&qfull[q0], (qn >> 1) & 1, status);
       if (pair) ok = ok && attn_wait_warp(&qfull[q1], ((qn + 1) >> 1) & 1, status);
@@ -739,15 +739,15 @@ __global__ void __launch_bounds__(AT_THREADS, 1) attn_kernel(const __grid_consta
           : "r"((int)(!got || I.kind < 0)), "r"(AT_BAR_ALL), "r"(AT_SOFT * 32)
           : "memory");
       if (stop) break;
-      const bool pair = I.pair();
+      const bool prefix = STREAM && I.prefix(), pair = !STREAM || I.pair(), parts = STREAM && I.parts();
       const int n_s = pair ? I.n : (I.n + 1 - slot) >> 1;
       int b, i, h, prow;
-      const bool valid = attn_row(P, I, slot, R, b, i, h, prow);
+      const bool valid = attn_row<STREAM>(P, I, slot, R, b, i, h, prow);
       const bool any_row = __any_sync(0xffffffffu, valid);
       int lo = 0, hi = 1 << 30;   // padding rows take no masks: nothing reads what they compute
       float pos = 0.f, slope = 0.f;
       if (valid) {
-        if (I.prefix()) {
+        if (prefix) {
           hi = P.pre;
           if (BIAS) pos = (float)(P.pre + (P.kv_len ? clampi(P.kv_len[b], 0, P.s_kv) : P.s_kv) - P.s_q + i);
         } else {
@@ -763,8 +763,20 @@ __global__ void __launch_bounds__(AT_THREADS, 1) attn_kernel(const __grid_consta
       float m = -INFINITY, l = 0.f;
       for (int k = 0; k < n_s; ++k) {
         const int t = I.t_hi - 1 - (pair ? k : 2 * k + slot), c0 = t * AT_TILE + half * AT_COLS;
+        // Values of a partly masked tile are looked over while S is on its way.  The stage's previous tile has been used by
+        // this slot's last S, so its phase cannot be mistaken; in a single row tile only once this S has come, since
+        // the other slot's tiles stand between.
+        auto look = [&]() {
+          const int j = pair ? k : 2 * k + slot;
+          const uint32_t vpos = base + (pair ? 2 * j + 1 : j + min(I.n, j + 2)), st = vpos % AT_STAGES;
+          if (ok) ok = attn_wait(&full[st], (vpos / AT_STAGES) & 1, status);
+          attn_clean_values<FP16>(I, t, sm + AT_OFF_KV + st * AT_TILE_BYTES, threadIdx.x & 255, &bad_item[seq & 1], seq);
+        };
+        const bool mixed = attn_mixed(I, t);
+        if (mixed && pair) look();
         if (ok) ok = attn_wait(&sfull[slot], sc & 1, status);
         ++sc;
+        if (STREAM && mixed && !pair) look();
         __syncwarp();
         tc_fence_after();
         if (any_row) {
@@ -773,7 +785,7 @@ __global__ void __launch_bounds__(AT_THREADS, 1) attn_kernel(const __grid_consta
           float x0 = -INFINITY, x1 = -INFINITY;
           const int a = lo - c0, z = hi - c0;   // the row sees columns [a, z)
           const bool masked = __any_sync(0xffffffffu, a > 0 || z < AT_COLS);
-#pragma unroll 1
+#pragma unroll STREAM ? 1 : 2
           for (int q = 0; q < 2; ++q) {
             uint32_t raw[32];
             float *v = reinterpret_cast<float *>(raw);
@@ -789,10 +801,11 @@ __global__ void __launch_bounds__(AT_THREADS, 1) attn_kernel(const __grid_consta
               for (int j = 0; j < 32; ++j) v[j] = fmaf(-slope, fabsf(d0 - (float)j), v[j] * sl);
             }
             if (masked) {
-              const int aq = a - 32 * q, zq = z - 32 * q;
+              const int aq = clampi(a - 32 * q, 0, 32), zq = clampi(z - 32 * q, 0, 32);
+              const uint32_t see = (zq == 32 ? ~0u : (1u << zq) - 1u) & (aq == 32 ? 0u : ~0u << aq);
 #pragma unroll
               for (int j = 0; j < 32; ++j)
-                if (j < aq || j >= zq) v[j] = -INFINITY;
+                if (!(see & (1u << j))) v[j] = -INFINITY;
             }
             if (CAP || BIAS || masked) {   // the second pass reads the finished logits
               tmem_st16(ts + 32 * q, raw);
@@ -837,8 +850,9 @@ __global__ void __launch_bounds__(AT_THREADS, 1) attn_kernel(const __grid_consta
           }
           const float mu = m == -INFINITY ? 0.f : m;
           float a0 = 0.f, a1 = 0.f, a2 = 0.f, a3 = 0.f;
-          // 16 columns at a time, the next 16 on their way while these are worked on; the loop is kept short, since
-          // instructions that are met for the first time cost about ten cycles each
+          // 16 columns at a time, the next 16 on their way while these are worked on; the stream kernel's
+          // loops stay rolled: its calls are short, and instructions that are met for the first time cost about ten cycles
+          // each (a token against 1K keys takes 12.7 us, unrolled 15.2; a 32K prompt the other way round, 6.0 ms and 5.8)
           auto probs = [&](const uint32_t (&raw)[16], uint32_t at) {
             const float *v = reinterpret_cast<const float *>(raw);
             uint32_t pk[8];
@@ -857,7 +871,7 @@ __global__ void __launch_bounds__(AT_THREADS, 1) attn_kernel(const __grid_consta
           };
           uint32_t buf0[16], buf1[16];
           tmem_ld16(ts, buf0);
-#pragma unroll 1
+#pragma unroll STREAM ? 1 : 2
           for (int q = 0; q < 2; ++q) {
             tmem_wait_ld();
             tmem_ld16(ts + 32 * q + 16, buf1);
@@ -868,12 +882,6 @@ __global__ void __launch_bounds__(AT_THREADS, 1) attn_kernel(const __grid_consta
           }
           l += (a0 + a1) + (a2 + a3);
           tmem_wait_st();
-        }
-        if (attn_mixed(I, t)) {
-          const int j = pair ? k : 2 * k + slot;
-          const uint32_t vpos = base + (pair ? 2 * j + 1 : j + min(I.n, j + 2)), st = vpos % AT_STAGES;
-          if (ok) ok = attn_wait(&full[st], (vpos / AT_STAGES) & 1, status);
-          attn_clean_values<FP16>(I, t, sm + AT_OFF_KV + st * AT_TILE_BYTES, threadIdx.x & 255, &bad_item[seq & 1], seq);
         }
         tc_fence_before();
         __syncwarp();
@@ -906,8 +914,8 @@ __global__ void __launch_bounds__(AT_THREADS, 1) attn_kernel(const __grid_consta
         bad = bad_item[seq & 1] == (int)seq;
       }
       if (writes && any_row) {
-        float *part_o = I.prefix() ? P.pre_o : P.part_o, *part_l = I.prefix() ? P.pre_l : P.part_l;
-        const int64_t part_row = (int64_t)I.part * (I.prefix() ? P.pre_rows : P.part_rows);
+        float *part_o = prefix ? P.pre_o : P.part_o, *part_l = prefix ? P.pre_l : P.part_l;
+        const int64_t part_row = (int64_t)I.part * (prefix ? P.pre_rows : P.part_rows);
         const float mm = fmaxf(m, m1), mu = mm == -INFINITY ? 0.f : mm;
         const float w0 = ex2(m - mu), w1 = ex2(m1 - mu);
         const float lt = l * w0 + l1 * w1;
@@ -915,21 +923,20 @@ __global__ void __launch_bounds__(AT_THREADS, 1) attn_kernel(const __grid_consta
         const float lse2 = lt == 0.f ? -INFINITY : mu + off + log2f(lt);
         if (!bad) {
           if (valid && half == 0) {
-            if (I.parts())
+            if (parts)
               part_l[part_row + prow] = lse2;
             else if (P.lse)
               P.lse[((int64_t)b * P.s_q + i) * P.h_q + h] = lse2 * 0.69314718055994531f;
           }
           const bool have0 = n_s > 0;
           const float f0 = w0 * inv, f1 = w1 * inv;
-#pragma unroll 1
-          for (int q = 0; q < 4; ++q) {
-            uint32_t o[16];
+          // 16 channels of the row, scaled, as fp32
+          auto take = [&](int q, uint32_t (&o)[16]) {
             float *of = reinterpret_cast<float *>(o);
             __syncwarp();
             if (have0) {
               tmem_ld16(to + 16 * q, o);
-              if (join) {
+              if (STREAM && join) {
                 uint32_t o1[16];
                 tmem_ld16(to + 128 + 16 * q, o1);
                 tmem_wait_ld();
@@ -945,26 +952,57 @@ __global__ void __launch_bounds__(AT_THREADS, 1) attn_kernel(const __grid_consta
 #pragma unroll
               for (int j = 0; j < 16; ++j) of[j] = 0.f;
             }
-            if (valid) {
-              if (I.parts()) {
-                float *dst = part_o + (part_row + prow) * D + AT_COLS * half + 16 * q;
-                if (lse2 != -INFINITY) {
-                  st_global_v8(dst, o);
-                  st_global_v8(dst + 8, o + 8);
-                }
-              } else {
-                uint32_t pk[8];
-#pragma unroll
-                for (int j = 0; j < 8; ++j) pk[j] = pack2<FP16>(of[2 * j], of[2 * j + 1]);
-                uint16_t *dst = static_cast<uint16_t *>(P.out) + b * P.so[0] + i * P.so[1] + h * P.so[2] + AT_COLS * half +
-                                16 * q;
-                if (P.wide_out) {
-                  st_global_v8(dst, pk);
-                } else {
-                  reinterpret_cast<uint4 *>(dst)[0] = make_uint4(pk[0], pk[1], pk[2], pk[3]);
-                  reinterpret_cast<uint4 *>(dst)[1] = make_uint4(pk[4], pk[5], pk[6], pk[7]);
-                }
+          };
+          if (STREAM && parts) {
+#pragma unroll 1
+            for (int q = 0; q < 4; ++q) {
+              uint32_t o[16];
+              take(q, o);
+              float *dst = part_o + (part_row + prow) * D + AT_COLS * half + 16 * q;
+              if (valid && lse2 != -INFINITY) {
+                st_global_v8(dst, o);
+                st_global_v8(dst + 8, o + 8);
               }
+            }
+          } else {
+            // Eight lanes turn their eight rows of 128 bytes around, 16 bytes at a time, so that each store of a warp writes
+            // four whole rows.  Rows stored by their own lanes touch 32 lines an instruction: 6000 cycles an item, not 1500.
+            uint4 u[8];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              uint32_t o[16];
+              take(q, o);
+              const float *of = reinterpret_cast<const float *>(o);
+#pragma unroll
+              for (int c = 0; c < 2; ++c)
+                u[2 * q + c] = make_uint4(pack2<FP16>(of[8 * c], of[8 * c + 1]), pack2<FP16>(of[8 * c + 2], of[8 * c + 3]),
+                                          pack2<FP16>(of[8 * c + 4], of[8 * c + 5]), pack2<FP16>(of[8 * c + 6], of[8 * c + 7]));
+            }
+#pragma unroll
+            for (int d = 4; d; d >>= 1) {
+              const bool up = lane & d;
+#pragma unroll
+              for (int c = 0; c < 8; ++c) {
+                if (c & d) continue;
+                uint4 send = up ? u[c] : u[c | d];
+                send.x = __shfl_xor_sync(0xffffffffu, send.x, d);
+                send.y = __shfl_xor_sync(0xffffffffu, send.y, d);
+                send.z = __shfl_xor_sync(0xffffffffu, send.z, d);
+                send.w = __shfl_xor_sync(0xffffffffu, send.w, d);
+                if (up)
+                  u[c] = send;
+                else
+                  u[c | d] = send;
+              }
+            }
+            const int64_t at = b * P.so[0] + i * P.so[1] + h * P.so[2] + AT_COLS * half;
+            const uint32_t rows = __ballot_sync(0xffffffffu, valid);
+#pragma unroll
+            for (int c = 0; c < 8; ++c) {
+              const int r = (lane & 24) + c;
+              const int64_t o = __shfl_sync(0xffffffffu, at, r);
+              if (rows >> r & 1)
+                *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(P.out) + o + 8 * (lane & 7)) = u[c];
             }
           }
         } else if (half == 0) {
@@ -974,7 +1012,7 @@ __global__ void __launch_bounds__(AT_THREADS, 1) attn_kernel(const __grid_consta
             const float ls = rl == 0.f ? -INFINITY : rm + log2f(rl);
             const float o0 = rl == 0.f ? 0.f : acc[0] * ri_l, o1 = rl == 0.f ? 0.f : acc[1] * ri_l;
             const float o2 = rl == 0.f ? 0.f : acc[2] * ri_l, o3 = rl == 0.f ? 0.f : acc[3] * ri_l;
-            if (I.parts()) {
+            if (parts) {
               if (lane == 0) part_l[part_row + rp] = ls;
               *reinterpret_cast<float4 *>(part_o + (part_row + rp) * D + 4 * lane) = make_float4(o0, o1, o2, o3);
             } else {
@@ -1002,28 +1040,18 @@ __global__ void __launch_bounds__(AT_THREADS, 1) attn_kernel(const __grid_consta
   }
 }
 
-template <bool FP16>
-cudaError_t launch_attn_type(const AttnArgs &P, int grid, bool cap, bool bias, cudaStream_t s) {
-  static SmemOptIn o[4];
+template <bool FP16, bool CAP, bool BIAS>
+cudaError_t launch_attn_variant(const AttnArgs &P, int grid, cudaStream_t s) {
+  static SmemOptIn units, stream;
   cudaError_t e;
-#define QV_ATTN(C, B)                                                         \
-  do {                                                                        \
-    e = o[2 * C + B].ensure(attn_kernel<FP16, C, B>, AT_SMEM);                \
-    if (e == cudaSuccess) {                                                   \
-      attn_kernel<FP16, C, B><<<grid, AT_THREADS, AT_SMEM, s>>>(P);           \
-      e = cudaGetLastError();                                                 \
-    }                                                                         \
-  } while (0)
-  if (cap && bias)
-    QV_ATTN(true, true);
-  else if (cap)
-    QV_ATTN(true, false);
-  else if (bias)
-    QV_ATTN(false, true);
-  else
-    QV_ATTN(false, false);
-#undef QV_ATTN
-  return e;
+  if (P.stream) {
+    e = stream.ensure(attn_kernel<FP16, CAP, BIAS, true>, AT_SMEM);
+    if (e == cudaSuccess) attn_kernel<FP16, CAP, BIAS, true><<<grid, AT_THREADS, AT_SMEM, s>>>(P);
+  } else {
+    e = units.ensure(attn_kernel<FP16, CAP, BIAS, false>, AT_SMEM);
+    if (e == cudaSuccess) attn_kernel<FP16, CAP, BIAS, false><<<grid, AT_THREADS, AT_SMEM, s>>>(P);
+  }
+  return e == cudaSuccess ? cudaGetLastError() : e;
 }
 
 }  // namespace qv

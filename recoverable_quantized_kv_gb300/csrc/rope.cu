@@ -7,7 +7,9 @@
 // rot on pass unchanged.  The table is the one qevict_set_rope_table takes for rot = 128.
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <cmath>
+#include <cstdlib>
 #include <cstdint>
 
 #include "common.cuh"
@@ -22,48 +24,71 @@ constexpr int MAX_PAIRS = 256;
 // theta_i / (2 pi) as a 64-bit fraction of a turn, one per pair
 struct TableArgs {
   uint64_t turn[MAX_PAIRS];
-  int pairs;
+  int pairs, step;             // rows between a thread's entries
   int64_t first, rows;
   float2 *out;
 };
 
-// One thread per (row, pair).  The angle in turns is p * turn[i] mod 2^64: whole turns fall away in
-// the integer product, exactly, so a position of 2^31 still has an angle to 2^-33 turns, and no
-// fp64 is needed (whose rate bounds this kernel at ten times its write time).  The eighth of a turn
-// around the nearest quadrant goes to fp32 in two parts, hi and lo, and the Taylor polynomials of
-// sine and cosine on [-pi/4, pi/4] (first terms left out: x^11/11! < 2e-9, x^12/12! < 2e-10) take
-// hi with a first-order correction for lo.
+// cos and sin of the angle ph * 2^-64 turns.  The eighth of a turn around the nearest quadrant goes to fp32 in two parts
+// and from turns to radians with the product's error kept, x + d; the Taylor polynomials of sine and cosine on
+// [-pi/4, pi/4] (first terms left out: x^11/11! < 2e-9, x^12/12! < 2e-10) take x, with a first-order correction for d.
+__device__ __forceinline__ float2 cos_sin_turns(uint64_t ph) {
+  const uint64_t sh = ph + (1ull << 61);            // nearest quadrant: add an eighth of a turn
+  const int quad = (int)(sh >> 62);
+  const int64_t r = (int64_t)((sh & ((1ull << 62) - 1)) - (1ull << 61));   // in [-1/8, 1/8) turn, times 2^64
+  const float rh = (float)(int)(r >> 38), rl = (float)(uint32_t)((uint64_t)(r & ((1ll << 38) - 1)) >> 6);
+  // 2 pi = C + C2; units of rh are 2^-26 turns, of rl 2^-58
+  constexpr float C = 6.28318548202514648437f, C2 = -1.74845553146e-07f;
+  const float ah = rh * 1.490116119384765625e-8f, al0 = rl * 3.4694469519536141888e-18f;
+  const float p = ah * C;
+  const float e = fmaf(ah, C, -p) + fmaf(ah, C2, al0 * C);
+  const float x = p + e, d = e - (x - p);
+  const float z = x * x;
+  float sn = fmaf(z, 2.75573192e-6f, -1.98412698e-4f);
+  sn = fmaf(z, sn, 8.33333333e-3f);
+  sn = fmaf(z, sn, -1.66666667e-1f);
+  sn = fmaf(x * z, sn, x);
+  float cs = fmaf(z, -2.75573192e-7f, 2.48015873e-5f);
+  cs = fmaf(z, cs, -1.38888889e-3f);
+  cs = fmaf(z, cs, 4.16666667e-2f);
+  cs = fmaf(z, cs, -0.5f);
+  cs = fmaf(z, cs, 1.0f);
+  const float s0 = fmaf(d, cs, sn), c0 = fmaf(-d, sn, cs);
+  float c = (quad & 1) ? s0 : c0, s = (quad & 1) ? c0 : s0;
+  if (quad == 1 || quad == 2) c = -c;
+  if (quad >= 2) s = -s;
+  return make_float2(c, s);
+}
+
+// A thread owns N neighbouring pairs (N = 2: 16-byte stores) and walks down the rows.  The angle in turns is p * turn[i] mod 2^64:
+// whole turns fall away in the integer product, exactly, so a position of 2^31 still has an angle to 2^-33 turns, and no
+// fp64 is needed (whose rate would bound this kernel at ten times its write time); a step down adds step * turn[i].
+// Bound by its arithmetic, about 40 operations for 8 bytes.
+template <int N>
 __global__ void __launch_bounds__(256) rope_table_kernel(const __grid_constant__ TableArgs A) {
-  const int64_t n = A.rows * A.pairs;
-  for (int64_t idx = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; idx < n; idx += (int64_t)gridDim.x * blockDim.x) {
-    const int64_t row = idx / A.pairs;
-    const int i = (int)(idx - row * A.pairs);
-    const uint64_t ph = (uint64_t)(A.first + row) * A.turn[i];
-    const uint64_t sh = ph + (1ull << 61);            // nearest quadrant: add an eighth of a turn
-    const int quad = (int)(sh >> 62);
-    const int64_t r = (int64_t)((sh & ((1ull << 62) - 1)) - (1ull << 61));   // in [-1/8, 1/8) turn, times 2^64
-    const float rh = (float)(int)(r >> 38), rl = (float)(uint32_t)((uint64_t)(r & ((1ll << 38) - 1)) >> 6);
-    // turns -> radians: 2 pi = C + C2; units of rh are 2^-26 turns, of rl 2^-58
-    constexpr float C = 6.28318548202514648437f, C2 = -1.74845553146e-07f;
-    const float ah = rh * 1.490116119384765625e-8f, al0 = rl * 3.4694469519536141888e-18f;
-    const float p = ah * C;
-    const float e = fmaf(ah, C, -p) + fmaf(ah, C2, al0 * C);
-    const float x = p + e, d = e - (x - p);
-    const float z = x * x;
-    float sn = fmaf(z, 2.75573192e-6f, -1.98412698e-4f);
-    sn = fmaf(z, sn, 8.33333333e-3f);
-    sn = fmaf(z, sn, -1.66666667e-1f);
-    sn = fmaf(x * z, sn, x);
-    float cs = fmaf(z, -2.75573192e-7f, 2.48015873e-5f);
-    cs = fmaf(z, cs, -1.38888889e-3f);
-    cs = fmaf(z, cs, 4.16666667e-2f);
-    cs = fmaf(z, cs, -0.5f);
-    cs = fmaf(z, cs, 1.0f);
-    const float s0 = fmaf(d, cs, sn), c0 = fmaf(-d, sn, cs);
-    float c = (quad & 1) ? s0 : c0, s = (quad & 1) ? c0 : s0;
-    if (quad == 1 || quad == 2) c = -c;
-    if (quad >= 2) s = -s;
-    A.out[idx] = make_float2(c, s);
+  const int groups = A.pairs / N;
+  const uint32_t id = blockIdx.x * 256u + threadIdx.x;
+  const uint32_t row0 = id / groups, i = (id - row0 * groups) * N;
+  if (row0 >= (uint32_t)A.step) return;
+  uint64_t ph[N], inc[N];
+#pragma unroll
+  for (int j = 0; j < N; ++j) {
+    ph[j] = (uint64_t)(A.first + row0) * A.turn[i + j];
+    inc[j] = (uint64_t)A.step * A.turn[i + j];
+  }
+  float2 *out = A.out + (int64_t)row0 * A.pairs + i;
+  const int64_t hop = (int64_t)A.step * A.pairs;
+  for (int64_t row = row0; row < A.rows; row += A.step, out += hop) {
+    float2 cs[N];
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+      cs[j] = cos_sin_turns(ph[j]);
+      ph[j] += inc[j];
+    }
+    if (N == 2)
+      *reinterpret_cast<float4 *>(out) = make_float4(cs[0].x, cs[0].y, cs[N - 1].x, cs[N - 1].y);
+    else
+      *out = cs[0];
   }
 }
 
@@ -78,10 +103,10 @@ struct RopeArgs {
   int64_t rows, pos0;
   int64_t qi[3], qo_[3], ki[3], ko_[3];   // strides in elements: batch, token, head
   int64_t tokens;                         // batch * seq
-  int seq, h_q, heads;                    // heads: queries and keys together
+  int seq, h_q, h_k;
+  int groups_q;                           // of the groups of neighbouring heads, those of queries
   int half;                               // rotated pairs
-  int units, pair_units;                  // vectors of work per head, those of them that rotate
-  int lanes;                              // heads in flight per token
+  int pair_units;                         // of a head's vectors of work (blockDim.x), those that rotate
   float f, fs;                            // magnitude factor; fs = -f for the inverse
 };
 
@@ -103,28 +128,76 @@ struct alignas(sizeof(T) * VEC) Pack {
   T v[VEC];
 };
 
-// A thread owns one unit (VEC pairs of the half layout, VEC / 2 pairs of the interleaved one, or VEC
-// channels that pass) of one token and walks over `lanes`-strided heads with the unit's cosines and
-// sines in registers, so the table row is read once per unit and token however many heads there are.
-// VEC fills 16 bytes where sizes, strides and alignment allow, else 1.  Rounded once, at the store.
-template <typename T, int VEC, bool INTER>
-__global__ void __launch_bounds__(256) rope_apply_kernel(const __grid_constant__ RopeArgs A) {
-  constexpr int NP = INTER ? (VEC > 1 ? VEC / 2 : 1) : VEC;   // pairs of a rotating unit
-  const int per_tok = A.units * A.lanes;
-  const int64_t id = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
-  const int64_t tok = id / per_tok;
-  if (tok >= A.tokens) return;
-  const int rest = (int)(id - tok * per_tok), u = rest % A.units, lane = rest / A.units;
-  const int64_t b = tok / A.seq, t = tok - b * A.seq;
+// Who holds the two channels of a pair: one thread, from two places of the half layout (any size and alignment), one
+// thread in the interleaved layout, or two lanes of a warp, each with 16 bytes of the half layout, that swap them.  The last
+// keeps every load and store of a warp on whole heads.
+enum : int { ROPE_TWO_PLACES = 0, ROPE_INTERLEAVED = 1, ROPE_SWAP = 2 };
+
+// Two neighbouring channels as fp32 and back, rounded once
+template <typename T>
+__device__ __forceinline__ float2 two(const T *p) {
+  return make_float2(to_f(p[0]), to_f(p[1]));
+}
+template <>
+__device__ __forceinline__ float2 two(const __nv_bfloat16 *p) {
+  const uint32_t w = *reinterpret_cast<const uint32_t *>(p);
+  return make_float2(bf16_lo(w), bf16_hi(w));
+}
+template <>
+__device__ __forceinline__ float2 two(const __half *p) {
+  return __half22float2(*reinterpret_cast<const __half2 *>(p));
+}
+__device__ __forceinline__ void put_two(float *p, float a, float b) { p[0] = a, p[1] = b; }
+__device__ __forceinline__ void put_two(__nv_bfloat16 *p, float a, float b) { *reinterpret_cast<uint32_t *>(p) = pack_bf16(a, b); }
+__device__ __forceinline__ void put_two(__half *p, float a, float b) { *reinterpret_cast<__half2 *>(p) = __floats2half2_rn(a, b); }
+
+// A thread owns one unit of one token (VEC channels; with ROPE_TWO_PLACES VEC pairs) in HPT heads, blockDim.y apart,
+// with the unit's cosines and sines in registers, so the table row is read once per unit for all of them; the heads'
+// loads are issued before the position is looked at.  Block: (units, heads side by side); grid: (tokens, groups of
+// HPT * blockDim.y neighbouring heads, queries' before keys').  VEC fills 16 bytes where sizes, strides and
+// alignment allow, else 1.  Rounded once, at the store.  Memory bound.
+template <typename T, int VEC, int MODE, int HPT>
+__global__ void __launch_bounds__(VEC > 1 ? 256 : 1024) rope_apply_kernel(const __grid_constant__ RopeArgs A) {
+  constexpr int NP = MODE == ROPE_INTERLEAVED ? (VEC > 1 ? VEC / 2 : 1) : VEC;   // pairs of a rotating unit
+  constexpr int NV = MODE == ROPE_INTERLEAVED && VEC == 1 ? 2 : VEC;             // elements loaded at one place
+  const int64_t tok = blockIdx.x;   // fewer than 2^31
+  const uint32_t b = blockIdx.x / (uint32_t)A.seq, t = blockIdx.x - b * (uint32_t)A.seq;
   const int64_t pos = A.pos ? (int64_t)A.pos[tok] : A.pos0 + t;
+  const int u = threadIdx.x;
+  const bool rotates = u < A.pair_units;
+  const int hu = A.pair_units / 2;                         // ROPE_SWAP: units of first channels
+  const bool second = MODE == ROPE_SWAP && u >= hu;
+  // first channel of the unit
+  const int ch = MODE == ROPE_SWAP ? u * VEC
+                 : rotates         ? u * NP * (MODE == ROPE_INTERLEAVED ? 2 : 1)
+                                   : 2 * A.half + (u - A.pair_units) * VEC;
+  const int group = blockIdx.y;
+  const bool is_q = group < A.groups_q;
+  const int h0 = (is_q ? group : group - A.groups_q) * blockDim.y * HPT + threadIdx.y, heads = is_q ? A.h_q : A.h_k;
+  const int64_t s0 = is_q ? A.qi[0] : A.ki[0], s1 = is_q ? A.qi[1] : A.ki[1], s2 = is_q ? A.qi[2] : A.ki[2];
+  const T *src = static_cast<const T *>(is_q ? A.q : A.k) + b * s0 + t * s1 + h0 * s2 + ch;
+  const int64_t shop = s2 * blockDim.y;
+  using V = Pack<T, NV>;
+  V x[HPT], y[MODE == ROPE_TWO_PLACES ? HPT : 1];
+#pragma unroll
+  for (int k = 0; k < HPT; ++k, src += shop) {
+    if (h0 + k * (int)blockDim.y < heads) {
+      if (NV == VEC) {
+        x[k] = *reinterpret_cast<const V *>(src);
+      } else {   // one pair (or passing channel) at any alignment
+        x[k].v[0] = src[0];
+        if (rotates) x[k].v[NV - 1] = src[1];
+      }
+      if (MODE == ROPE_TWO_PLACES && rotates) y[k] = *reinterpret_cast<const V *>(src + A.half);
+    }
+  }
   if (pos < 0 || pos >= A.rows) {   // no such table row: the token's heads are not written
-    if (rest == 0) atomicOr(A.status, QV_ERR_BOUNDS);
+    if (u == 0 && threadIdx.y == 0) atomicOr(A.status, QV_ERR_BOUNDS);
     return;
   }
-  const bool rotates = u < A.pair_units;
   float c[NP], s[NP];
   if (rotates) {
-    const float2 *row = A.table + pos * A.half + (int64_t)u * NP;
+    const float2 *row = A.table + pos * A.half + (int64_t)(second ? u - hu : u) * NP;
 #pragma unroll
     for (int j = 0; j < NP; ++j) {
       float2 cs;
@@ -135,64 +208,99 @@ __global__ void __launch_bounds__(256) rope_apply_kernel(const __grid_constant__
         cs = row[j];
       }
       c[j] = cs.x * A.f;
-      s[j] = cs.y * A.fs;
+      s[j] = cs.y * (MODE == ROPE_SWAP && !second ? -A.fs : A.fs);   // swapped: y = own c +- other s
     }
   }
-  // channels of the unit: half layout ch and ch + half; interleaved ch .. ; passing ch ..
-  const int ch = rotates ? (INTER ? u * NP * 2 : u * NP) : 2 * A.half + (u - A.pair_units) * VEC;
-  for (int h = lane; h < A.heads; h += A.lanes) {
-    const bool is_q = h < A.h_q;
-    const int hh = is_q ? h : h - A.h_q;
-    const int64_t *si = is_q ? A.qi : A.ki, *so = is_q ? A.qo_ : A.ko_;
-    const T *src = reinterpret_cast<const T *>(is_q ? A.q : A.k) + b * si[0] + t * si[1] + hh * si[2] + ch;
-    T *dst = reinterpret_cast<T *>(is_q ? A.qo : A.ko) + b * so[0] + t * so[1] + hh * so[2] + ch;
-    if (!rotates) {
-      if (src != dst) *reinterpret_cast<Pack<T, VEC> *>(dst) = *reinterpret_cast<const Pack<T, VEC> *>(src);
-    } else if (INTER) {
-      constexpr int N = VEC > 1 ? VEC : 2;
-      T x[N];
-      if (VEC > 1) {
-        *reinterpret_cast<Pack<T, VEC> *>(x) = *reinterpret_cast<const Pack<T, VEC> *>(src);
-      } else {
-        x[0] = src[0];
-        x[1] = src[1];
-      }
+  const int64_t d0 = is_q ? A.qo_[0] : A.ko_[0], d1 = is_q ? A.qo_[1] : A.ko_[1], d2 = is_q ? A.qo_[2] : A.ko_[2];
+  T *dst = static_cast<T *>(is_q ? A.qo : A.ko) + b * d0 + t * d1 + h0 * d2 + ch;
+  const int64_t dhop = d2 * blockDim.y;
 #pragma unroll
-      for (int j = 0; j < NP; ++j) {
-        const float x1 = to_f(x[2 * j]), x2 = to_f(x[2 * j + 1]);
-        x[2 * j] = from_f<T>(fmaf(x1, c[j], -x2 * s[j]));
-        x[2 * j + 1] = from_f<T>(fmaf(x2, c[j], x1 * s[j]));
+  for (int k = 0; k < HPT; ++k, dst += dhop) {
+    if (h0 + k * (int)blockDim.y >= heads) break;
+    if (MODE == ROPE_SWAP) {   // the head's lanes are together here
+      const int lane = (threadIdx.x + blockDim.x * threadIdx.y) & 31;
+      const int n = blockDim.x;   // lanes of a head: a power of two up to 32
+      const uint32_t mates = (n == 32 ? ~0u : (1u << n) - 1u) << (lane & ~(n - 1));
+      const int from = rotates ? (second ? lane - hu : lane + hu) : lane;
+      uint4 w = *reinterpret_cast<uint4 *>(&x[k]);
+      w.x = __shfl_sync(mates, w.x, from);
+      w.y = __shfl_sync(mates, w.y, from);
+      w.z = __shfl_sync(mates, w.z, from);
+      w.w = __shfl_sync(mates, w.w, from);
+      if (rotates) {
+        const V o = *reinterpret_cast<V *>(&w);
+#pragma unroll
+        for (int j = 0; j + 1 < VEC; j += 2) {
+          const float2 a = two(x[k].v + j), q = two(o.v + j);
+          put_two(x[k].v + j, fmaf(a.x, c[j], q.x * s[j]), fmaf(a.y, c[j + 1], q.y * s[j + 1]));
+        }
       }
-      if (VEC > 1) {
-        *reinterpret_cast<Pack<T, VEC> *>(dst) = *reinterpret_cast<const Pack<T, VEC> *>(x);
+      *reinterpret_cast<V *>(dst) = x[k];   // passing channels in place: what stands there
+    } else if (!rotates) {
+      if (NV == VEC)
+        *reinterpret_cast<V *>(dst) = x[k];
+      else
+        dst[0] = x[k].v[0];
+    } else if (MODE == ROPE_INTERLEAVED) {
+      if (NV == VEC) {
+#pragma unroll
+        for (int j = 0; j < NP; ++j) {
+          const float2 a = two(x[k].v + 2 * j);
+          put_two(x[k].v + 2 * j, fmaf(a.x, c[j], -a.y * s[j]), fmaf(a.y, c[j], a.x * s[j]));
+        }
+        *reinterpret_cast<V *>(dst) = x[k];
       } else {
-        dst[0] = x[0];
-        dst[1] = x[1];
+        const float x1 = to_f(x[k].v[0]), x2 = to_f(x[k].v[NV - 1]);
+        dst[0] = from_f<T>(fmaf(x1, c[0], -x2 * s[0]));
+        dst[1] = from_f<T>(fmaf(x2, c[0], x1 * s[0]));
       }
     } else {
-      Pack<T, VEC> x = *reinterpret_cast<const Pack<T, VEC> *>(src);
-      Pack<T, VEC> y = *reinterpret_cast<const Pack<T, VEC> *>(src + A.half);
 #pragma unroll
       for (int j = 0; j < VEC; ++j) {
-        const float x1 = to_f(x.v[j]), x2 = to_f(y.v[j]);
-        x.v[j] = from_f<T>(fmaf(x1, c[j], -x2 * s[j]));
-        y.v[j] = from_f<T>(fmaf(x2, c[j], x1 * s[j]));
+        const float x1 = to_f(x[k].v[j]), x2 = to_f(y[k].v[j]);
+        x[k].v[j] = from_f<T>(fmaf(x1, c[j], -x2 * s[j]));
+        y[k].v[j] = from_f<T>(fmaf(x2, c[j], x1 * s[j]));
       }
-      *reinterpret_cast<Pack<T, VEC> *>(dst) = x;
-      *reinterpret_cast<Pack<T, VEC> *>(dst + A.half) = y;
+      *reinterpret_cast<V *>(dst) = x[k];
+      *reinterpret_cast<V *>(dst + A.half) = y[k];
     }
   }
 }
 
 namespace {
 
-template <typename T, bool INTER>
-void launch_apply(const RopeArgs &A, int vec, int64_t blocks, int threads, cudaStream_t s) {
-  constexpr int V = 16 / (int)sizeof(T);
-  if (vec > 1)
-    rope_apply_kernel<T, V, INTER><<<(unsigned)blocks, threads, 0, s>>>(A);
+// Block and grid for `units` vectors a head: a warp a block, four neighbouring heads a thread, so that a warp has 2 KB of
+// one place in flight, unless there are so few tokens that one head a thread does not fill the GPU.  A 32K prompt of 32 + 8
+// heads takes 110 us (6.2 TB/s, 92% of a plain copy); two heads a thread 167, eight 110, five warps a block 113.
+template <typename T, int VEC, int MODE>
+bool launch_apply(RopeArgs &A, int units, cudaStream_t s) {
+  const bool one = MODE == ROPE_TWO_PLACES || A.tokens * units * (A.h_q + A.h_k) <= 152 * 2048;
+  const int ny = std::max(1, 32 / units), per = ny * (one ? 1 : 4);
+  A.groups_q = (A.h_q + per - 1) / per;
+  const int64_t gx = A.tokens, gy = A.groups_q + (A.h_k + per - 1) / per;
+  if (gx > 0x7fffffffll || gy > 65535) return false;
+  const dim3 grid((unsigned)gx, (unsigned)gy), block(units, ny);
+  if (one)
+    rope_apply_kernel<T, VEC, MODE, 1><<<grid, block, 0, s>>>(A);
   else
-    rope_apply_kernel<T, 1, INTER><<<(unsigned)blocks, threads, 0, s>>>(A);
+    rope_apply_kernel<T, VEC, MODE, MODE == ROPE_TWO_PLACES ? 1 : 4><<<grid, block, 0, s>>>(A);
+  return true;
+}
+template <typename T>
+bool launch_apply_type(RopeArgs &A, bool vec, bool inter, int d_head, cudaStream_t s) {
+  constexpr int V = 16 / (int)sizeof(T);
+  const int pass = d_head - 2 * A.half;
+  if (inter) {
+    A.pair_units = vec ? 2 * A.half / V : A.half;
+    return vec ? launch_apply<T, V, ROPE_INTERLEAVED>(A, d_head / V, s) : launch_apply<T, 1, ROPE_INTERLEAVED>(A, A.half + pass, s);
+  }
+  if (vec && 32 % (d_head / V) == 0 && d_head % V == 0) {   // a head's lanes in one warp
+    A.pair_units = 2 * A.half / V;
+    return launch_apply<T, V, ROPE_SWAP>(A, d_head / V, s);
+  }
+  A.pair_units = vec ? A.half / V : A.half;
+  return vec ? launch_apply<T, V, ROPE_TWO_PLACES>(A, A.half / V + pass / V, s)
+             : launch_apply<T, 1, ROPE_TWO_PLACES>(A, A.half + pass, s);
 }
 
 // The strides of a written tensor put no two elements in one place: by ascending stride, every
@@ -271,9 +379,17 @@ qevict_status qevict_rope_table(const qevict_rope_config *cfg, int64_t first, in
     const double hi = std::floor(std::ldexp(turns, 32)), lo = std::ldexp(turns, 32) - hi;
     A.turn[i] = ((uint64_t)hi << 32) + (uint64_t)std::floor(std::ldexp(lo, 32));
   }
-  const int64_t blocks = (rows * A.pairs + 255) / 256;
-  qv::rope_table_kernel<<<(unsigned)(blocks < 152 * 32 ? blocks : 152 * 32), 256, 0,
-                          reinterpret_cast<cudaStream_t>(stream)>>>(A);
+  const bool two = A.pairs % 2 == 0 && ((uintptr_t)d_table & 15) == 0;
+  const int groups = two ? A.pairs / 2 : A.pairs;
+  // rows side by side: all of a short table's, else as many as fill the GPU's 152 x 2048 threads
+  const int64_t fill = (152 * 2048 + groups - 1) / groups;
+  A.step = (int)(rows < fill ? rows : fill);
+  const unsigned blocks = (unsigned)(((int64_t)A.step * groups + 255) / 256);
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  if (two)
+    qv::rope_table_kernel<2><<<blocks, 256, 0, s>>>(A);
+  else
+    qv::rope_table_kernel<1><<<blocks, 256, 0, s>>>(A);
   return cudaGetLastError() == cudaSuccess ? QEVICT_OK : QEVICT_ECUDA;
 }
 
@@ -329,7 +445,7 @@ qevict_status qevict_rope_apply(const qevict_rope_desc *d, const float *d_table,
   A.seq = d->seq;
   A.tokens = (int64_t)d->batch * d->seq;
   A.h_q = d->h_q;
-  A.heads = d->h_q + d->h_k;
+  A.h_k = d->h_k;
   A.half = d->rot_dim / 2;
   A.f = d->factor;
   A.fs = d->inverse ? -d->factor : d->factor;
@@ -337,24 +453,11 @@ qevict_status qevict_rope_apply(const qevict_rope_desc *d, const float *d_table,
   const int np = d->interleaved ? V / 2 : V;   // pairs of a full vector
   // full vectors need every start on 16 bytes, table rows (8 bytes a pair) included
   const bool vec = align == 0 && A.half % np == 0 && pass % V == 0 && (A.half % 2 == 0 || np == 1);
-  A.pair_units = vec ? A.half / np : A.half;
-  A.units = A.pair_units + (vec ? pass / V : pass);
-  // heads in flight: all of them for few tokens (latency), else about three heads a thread, which
-  // reads each table row a third as often
-  const int64_t all = A.tokens * A.units * A.heads;
-  A.lanes = all <= 152 * 2048 ? A.heads : (A.heads + 2) / 3;
-  const int64_t n = A.tokens * A.units * A.lanes;
-  const int64_t blocks = (n + 255) / 256;
-  if (blocks > 0x7fffffffll) return QEVICT_EINVAL;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-#define QV_ROPE(T) (d->interleaved ? launch_apply<T, true>(A, vec ? V : 1, blocks, 256, s) : launch_apply<T, false>(A, vec ? V : 1, blocks, 256, s))
-  if (d->dtype == QEVICT_BF16)
-    QV_ROPE(__nv_bfloat16);
-  else if (d->dtype == QEVICT_FP16)
-    QV_ROPE(__half);
-  else
-    QV_ROPE(float);
-#undef QV_ROPE
+  const bool ok = d->dtype == QEVICT_BF16   ? launch_apply_type<__nv_bfloat16>(A, vec, d->interleaved, d->d_head, s)
+                  : d->dtype == QEVICT_FP16 ? launch_apply_type<__half>(A, vec, d->interleaved, d->d_head, s)
+                                            : launch_apply_type<float>(A, vec, d->interleaved, d->d_head, s);
+  if (!ok) return QEVICT_EINVAL;
   return cudaGetLastError() == cudaSuccess ? QEVICT_OK : QEVICT_ECUDA;
 }
 
