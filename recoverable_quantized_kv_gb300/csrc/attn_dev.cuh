@@ -15,21 +15,20 @@ constexpr int AT_TILE = 128;                          // rows of a query tile, k
 constexpr int AT_STAGES = 5;                          // key / value tiles in flight
 constexpr int AT_TILE_BYTES = AT_TILE * D * 2;        // 32 KB: two 128-byte-swizzled halves of 64 channels
 constexpr int AT_HALF_BYTES = AT_TILE_BYTES / 2;
-constexpr int AT_SOFT = 16;                           // softmax warps: eight per slot, four for each half of the columns
+constexpr int AT_SOFT = 16;                           // softmax warps: four for each quarter of the columns
 constexpr int AT_W_LOAD = AT_SOFT, AT_W_MMA = AT_SOFT + 1, AT_W_PLAN = AT_SOFT + 2;   // TMA, MMA, work items
 constexpr int AT_THREADS = (AT_SOFT + 3) * 32;        // five warps on an SM sub-partition: 96 registers a thread
-constexpr int AT_COLS = AT_TILE / 2;                  // columns of S, and channels of O, per softmax thread
+constexpr int AT_COLS = AT_TILE / 4;                  // columns of S, and channels of O, per softmax thread
 constexpr int AT_ITEMS = 4;                           // work items described ahead
 constexpr int AT_OFF_KV = 2 * AT_TILE_BYTES;
-constexpr int AT_OFF_X = AT_OFF_KV + AT_STAGES * AT_TILE_BYTES;    // [2 slots][2 halves][128] fp32 exchange
-constexpr int AT_OFF_M = AT_OFF_X + 4 * AT_TILE * 4;               // [128] fp32: slot 1's maxima
-constexpr int AT_OFF_BAR = AT_OFF_M + AT_TILE * 4;
+constexpr int AT_OFF_X = AT_OFF_KV + AT_STAGES * AT_TILE_BYTES;    // [4 quarters][128] fp32 exchange
+constexpr int AT_OFF_BAR = AT_OFF_X + 4 * AT_TILE * 4;
 constexpr int AT_NBAR = 2 * AT_STAGES + 4 + 6 + 2 * AT_ITEMS;
 constexpr int AT_OFF_MISC = AT_OFF_BAR + AT_NBAR * 8;              // tmem address, flags
 constexpr int AT_OFF_ITEM = AT_OFF_MISC + 16;                     // work item ring
 constexpr int AT_SMEM = AT_OFF_ITEM + AT_ITEMS * 64;
 static_assert(AT_SMEM <= 232448, "one CTA per SM");
-constexpr int AT_BAR_ALL = 1, AT_BAR_PAIR = 2;        // named barriers (pairs: 2 .. 9)
+constexpr int AT_BAR_ALL = 1, AT_BAR_ROWS = 2;        // named barriers (of the four warps that share rows: 2 .. 5)
 
 struct AttnArgs {
   CUtensorMap tq, tk, tv;      // queries and own keys of each sequence
@@ -213,18 +212,19 @@ __device__ __forceinline__ void tc_mma_tile_ss(uint32_t tmem, uint64_t da, uint6
       "l"(da), "l"(db), "r"(idesc)
       : "memory");
 }
-// O (+)= P V: P in tensor memory (8 columns per 16 keys; keys 64 .. 127 from column 64 on), 16 keys of V 2048 bytes apart
+// O (+)= P V: P in tensor memory (8 columns per 16 keys, 32 keys at the start of each 32 columns), 16 keys of V 2048 bytes
+// apart
 __device__ __forceinline__ void tc_mma_tile_ts(uint32_t tmem, uint32_t ta, uint64_t db, uint32_t idesc, uint32_t accumulate) {
   asm volatile(
       "{\n .reg .pred e, f, t;\n .reg .b64 b;\n .reg .b32 a;\n elect.sync _|e, 0xffffffff;\n setp.ne.b32 f, %4, 0;\n setp.eq.b32 t, 0, 0;\n"
       " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, f;\n"
       " add.s32 a, %1, 8;\n add.s64 b, %2, 128;\n @e tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, t;\n"
-      " add.s32 a, %1, 16;\n add.s64 b, %2, 256;\n @e tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, t;\n"
-      " add.s32 a, %1, 24;\n add.s64 b, %2, 384;\n @e tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, t;\n"
+      " add.s32 a, %1, 32;\n add.s64 b, %2, 256;\n @e tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, t;\n"
+      " add.s32 a, %1, 40;\n add.s64 b, %2, 384;\n @e tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, t;\n"
       " add.s32 a, %1, 64;\n add.s64 b, %2, 512;\n @e tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, t;\n"
       " add.s32 a, %1, 72;\n add.s64 b, %2, 640;\n @e tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, t;\n"
-      " add.s32 a, %1, 80;\n add.s64 b, %2, 768;\n @e tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, t;\n"
-      " add.s32 a, %1, 88;\n add.s64 b, %2, 896;\n @e tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, t;\n}" ::"r"(tmem),
+      " add.s32 a, %1, 96;\n add.s64 b, %2, 768;\n @e tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, t;\n"
+      " add.s32 a, %1, 104;\n add.s64 b, %2, 896;\n @e tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, t;\n}" ::"r"(tmem),
       "r"(ta), "l"(db), "r"(idesc), "r"(accumulate)
       : "memory");
 }
@@ -286,6 +286,23 @@ __device__ __forceinline__ void st_global_v8(void *p, const uint32_t *r) {   // 
                "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
                : "memory");
 }
+// Packed fp32 pairs as 64-bit values: what stays the same over a loop is packed once
+__device__ __forceinline__ uint64_t pack_f2(float x, float y) {
+  uint64_t d;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(x), "f"(y));
+  return d;
+}
+__device__ __forceinline__ void unpack_f2(float &x, float &y, uint64_t v) { asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(v)); }
+__device__ __forceinline__ uint64_t fma_f2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ uint64_t add_f2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
 __device__ __forceinline__ float rcp_approx(float x) {   // relative error about 2^-23
   float y;
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -309,28 +326,24 @@ __device__ __forceinline__ float2 unpack2(uint32_t v) {
 // ----------------------------------------------------------------------------- rows with values that are not finite
 
 // The keys of tile t that not every row of the item sees: their values that are not finite become 0 in shared memory,
-// thread `who` of 256 taking half a key's channels.  If some row sees such a key, *flag = mark is set first: a slot that
-// meets the 0 of the other slot also meets its flag.
+// thread `who` of 512 taking a quarter of a key's channels.  If some row sees such a key, *flag = mark.
 template <bool FP16>
 __device__ __forceinline__ void attn_clean_values(const AttnItem &I, int t, uint8_t *v, int who, volatile int *flag, int mark) {
-  const int k = who >> 1, key = t * AT_TILE + k;
+  const int k = who >> 2, key = t * AT_TILE + k;
   if (key >= I.clean_lo && key < I.clean_hi) return;
   constexpr uint32_t E = FP16 ? 0x7C00u : 0x7F80u, E2 = E | (E << 16);   // all exponent bits set: infinity or NaN
-  uint32_t *p = reinterpret_cast<uint32_t *>(v + (who & 1) * AT_HALF_BYTES + k * 128);
+  uint32_t *p = reinterpret_cast<uint32_t *>(v + (who >> 1 & 1) * AT_HALF_BYTES + k * 128 + (who & 1) * 64);
   // ~w & E2 has an empty half exactly where the half is not finite; taking 1 from both halves then sets its top bit
   uint32_t hit = 0;
 #pragma unroll
-  for (int c = 0; c < 8; ++c) {
-    const uint4 x = lds128(p + ((c + k) & 7) * 4);   // neighbours start in other banks
+  for (int c = 0; c < 4; ++c) {
+    const uint4 x = lds128(p + ((c + k) & 3) * 4);   // neighbours start in other banks
     hit |= ((~x.x & E2) - 0x00010001u) | ((~x.y & E2) - 0x00010001u) | ((~x.z & E2) - 0x00010001u) | ((~x.w & E2) - 0x00010001u);
   }
   if (hit & 0x80008000u) {
-    if (key >= I.key_lo && key < I.key_hi) {
-      *flag = mark;
-      __threadfence_block();
-    }
+    if (key >= I.key_lo && key < I.key_hi) *flag = mark;
 #pragma unroll 1
-    for (int c = 0; c < 32; ++c) {
+    for (int c = 0; c < 16; ++c) {
       const uint32_t w = p[c];
       const bool lo = (w & E) == E, hi = (w & (E << 16)) == (E << 16);
       if (lo | hi) p[c] = (lo ? 0u : w & 0xFFFFu) | (hi ? 0u : w & 0xFFFF0000u);
@@ -419,11 +432,13 @@ __device__ __forceinline__ void attn_exact_rows(const AttnArgs &P, const AttnIte
 
 // ----------------------------------------------------------------------------- the kernel
 
-// One persistent CTA per SM: two slots of eight softmax warps, a thread owning one row and half of the columns
-// of its slot's 128-row tile; a TMA warp; an MMA warp; a warp that lays out the work items ahead of the others.  Rows of a tile are (token, query head of the
+// One persistent CTA per SM: sixteen softmax warps, a thread owning one row and a quarter of the columns of the 128-row tile
+// at hand; a TMA warp; an MMA warp; a warp that lays out the work items ahead of the others.  Rows of a tile are (token, query head of the
 // group), so the group's heads share every key tile.  Tensor memory: S of slot s at columns 128 s, overwritten in place by
-// the probabilities (16-bit, the A operand of P V; each half of the keys over its own half of S), O of slot s at 256 + 128 s.  The
-// tensor pipe alternates between the slots: while slot 0 turns S into P, it runs slot 1's products.
+// the probabilities (16-bit, the A operand of P V; each quarter of the keys over its own quarter of S), O of slot s at 256 + 128 s.  The
+// softmax warps and the tensor pipe alternate between the slots: while all warps turn slot 0's S into P, the pipe runs slot 1's
+// products.  (With eight warps a slot a tile's S takes 1600 cycles to become P instead of 900, and a slot's round of softmax and
+// products, which nothing shortens, sets the pace: 5.5 ms against 4.9 for a 32K prompt of 32 heads.)
 // Key tiles are taken from the last to the first, so a causal row meets its diagonal, and a distance bias its largest
 // logits, first.  The running max moves only when a row's max has grown by more than 2^8 (then the warps rescale their
 // rows of O in tensor memory): until then p reaches at most 2^8, which fp32 sums and 16-bit probabilities hold as well.
@@ -439,7 +454,7 @@ __global__ void __launch_bounds__(AT_THREADS, 1) attn_kernel(const __grid_consta
   uint32_t *tmem_slot = misc;
   volatile int *bad_item = reinterpret_cast<int *>(misc + 2);   // [item parity]: 1 + the item with values to recompute
   AttnItem *items = reinterpret_cast<AttnItem *>(sm + AT_OFF_ITEM);
-  float *xch = reinterpret_cast<float *>(sm + AT_OFF_X), *m_slot1 = reinterpret_cast<float *>(sm + AT_OFF_M);
+  float *xch = reinterpret_cast<float *>(sm + AT_OFF_X);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   int *status = P.status;
   if (smem_u32(sm) & 1023) {   // cannot be swizzled: nothing runs
@@ -453,7 +468,7 @@ __global__ void __launch_bounds__(AT_THREADS, 1) attn_kernel(const __grid_consta
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   } else if (threadIdx.x < AT_NBAR) {
     const uint64_t *p = &bars[threadIdx.x];
-    const int n = p < pfull ? 1 : p < ofull ? AT_SOFT / 2 :
+    const int n = p < pfull ? 1 : p < ofull ? AT_SOFT :
                   p < ifull ? 2 : p < iempty ? 1 : AT_SOFT + 2;
     mbar_init(&bars[threadIdx.x], n);
     fence_mbar_init();
@@ -718,15 +733,13 @@ __global__ void __launch_bounds__(AT_THREADS, 1) attn_kernel(const __grid_consta
     }
     // every product issued above has completed before the CTA leaves: the softmax warps wait for ofull
   } else {
-    // ---- softmax: thread = one row of the slot's tile, one half of its columns
-    const int slot = warp >> 3, half = (warp >> 2) & 1, wq = warp & 3, row = wq * 32 + lane;
-    const uint32_t lane_base = tmem + ((uint32_t)(wq * 32) << 16);
-    const uint32_t ts = lane_base + 128 * slot + AT_COLS * half;   // S, and its half of P
-    const uint32_t to = lane_base + 256 + 128 * slot + AT_COLS * half;
-    float *x_own = xch + (2 * slot + half) * AT_TILE + row, *x_other = xch + (2 * slot + (half ^ 1)) * AT_TILE + row;
-    const int pair_bar = AT_BAR_PAIR + 4 * slot + wq;   // the two warps that share these rows
+    // ---- softmax: thread = one row of a tile, one quarter of its columns, slot after slot
+    const int quarter = warp >> 2, wq = warp & 3, row = wq * 32 + lane;
+    const uint32_t lane_base = tmem + ((uint32_t)(wq * 32) << 16) + AT_COLS * quarter;   // S, P and O (+ 256) of slot 0
+    float *x_own = xch + quarter * AT_TILE + row;
+    const int row_bar = AT_BAR_ROWS + wq;   // the four warps that share these rows
     const AttnRow R = attn_row_of(P, row);
-    uint32_t sc = 0, oc = 0, base = 0;
+    uint32_t sc0 = 0, sc1 = 0, oc0 = 0, oc1 = 0, base = 0;
     bool ok = true;   // after a wait that ran out the loops go on without waiting, so all warps meet at every barrier
     for (;;) {
       AttnItem I;
@@ -740,195 +753,196 @@ __global__ void __launch_bounds__(AT_THREADS, 1) attn_kernel(const __grid_consta
           : "memory");
       if (stop) break;
       const bool prefix = STREAM && I.prefix(), pair = !STREAM || I.pair(), parts = STREAM && I.parts();
-      const int n_s = pair ? I.n : (I.n + 1 - slot) >> 1;
-      int b, i, h, prow;
-      const bool valid = attn_row<STREAM>(P, I, slot, R, b, i, h, prow);
-      const bool any_row = __any_sync(0xffffffffu, valid);
-      int lo = 0, hi = 1 << 30;   // padding rows take no masks: nothing reads what they compute
-      float pos = 0.f, slope = 0.f;
-      if (valid) {
-        if (prefix) {
-          hi = P.pre;
-          if (BIAS) pos = (float)(P.pre + (P.kv_len ? clampi(P.kv_len[b], 0, P.s_kv) : P.s_kv) - P.s_q + i);
-        } else {
-          const int p = I.kl - I.ql + i;
-          const int2 v = attn_interval(P, b, p, I.kl, I.pfx);
-          lo = v.x, hi = v.y;
-          if (BIAS) pos = (float)p;
+      // what a thread keeps of its row in each slot (in a single row tile both are the same row)
+      struct Slot {
+        float m, l, pos;
+        int lo, hi;
+        bool any;
+      } S0, S1;
+      float slope = 0.f;
+      auto setup = [&](int slot, Slot &S) {
+        int b, i, h, prow;
+        const bool valid = attn_row<STREAM>(P, I, slot, R, b, i, h, prow);
+        S.any = __any_sync(0xffffffffu, valid);
+        S.lo = 0, S.hi = 1 << 30;   // padding rows take no masks: nothing reads what they compute
+        S.m = -INFINITY, S.l = 0.f, S.pos = 0.f;
+        if (valid) {
+          if (prefix) {
+            S.hi = P.pre;
+            if (BIAS) S.pos = (float)(P.pre + (P.kv_len ? clampi(P.kv_len[b], 0, P.s_kv) : P.s_kv) - P.s_q + i);
+          } else {
+            const int p = I.kl - I.ql + i;
+            const int2 v = attn_interval(P, b, p, I.kl, I.pfx);
+            S.lo = v.x, S.hi = v.y;
+            if (BIAS) S.pos = (float)p;
+          }
+          if (BIAS) slope = P.slopes[h] * 1.4426950408889634f;
         }
-        if (BIAS) slope = P.slopes[h] * 1.4426950408889634f;
-      }
+      };
+      setup(0, S0);
+      if (pair)
+        setup(1, S1);
+      else
+        S1 = S0;
       // x = value * scale2: the products themselves, or with BIAS the finished logit
       const float scale2 = BIAS ? 1.f : CAP ? 2.f * P.cap_log2 : P.scale_log2;
-      float m = -INFINITY, l = 0.f;
-      for (int k = 0; k < n_s; ++k) {
-        const int t = I.t_hi - 1 - (pair ? k : 2 * k + slot), c0 = t * AT_TILE + half * AT_COLS;
-        // Values of a partly masked tile are looked over while S is on its way.  The stage's previous tile has been used by
-        // this slot's last S, so its phase cannot be mistaken; in a single row tile only once this S has come, since
-        // the other slot's tiles stand between.
+      const uint64_t scale22 = pack_f2(scale2, scale2);
+      const int clean_lo = (I.clean_lo + AT_TILE - 1) / AT_TILE, clean_hi = I.clean_hi / AT_TILE;   // tiles that every row sees whole
+      // One slot's S of key tile j (from the last) into probabilities; first: the slot's first tile
+      auto step = [&](const int slot, Slot &S, uint32_t &sc, int j, bool first) {
+        const int t = I.t_hi - 1 - j;
+        const uint32_t ts = lane_base + 128 * slot;
+        const bool mixed = t < clean_lo || t >= clean_hi;
+        // Values of a partly masked tile are looked over while S is on its way, once for both slots of a pair.  The stage's
+        // previous tile has been used by an S that came before, so its phase cannot be mistaken; in a single row tile only
+        // once this S has come, since the other slot's tiles stand between.
         auto look = [&]() {
-          const int j = pair ? k : 2 * k + slot;
           const uint32_t vpos = base + (pair ? 2 * j + 1 : j + min(I.n, j + 2)), st = vpos % AT_STAGES;
           if (ok) ok = attn_wait(&full[st], (vpos / AT_STAGES) & 1, status);
-          attn_clean_values<FP16>(I, t, sm + AT_OFF_KV + st * AT_TILE_BYTES, threadIdx.x & 255, &bad_item[seq & 1], seq);
+          attn_clean_values<FP16>(I, t, sm + AT_OFF_KV + st * AT_TILE_BYTES, threadIdx.x, &bad_item[seq & 1], seq);
         };
-        const bool mixed = attn_mixed(I, t);
-        if (mixed && pair) look();
+        if (mixed && pair && slot == 0) look();
         if (ok) ok = attn_wait(&sfull[slot], sc & 1, status);
         ++sc;
         if (STREAM && mixed && !pair) look();
         __syncwarp();
         tc_fence_after();
-        if (any_row) {
-          // Two passes over S, which stays in tensor memory: the maximum first, then the probabilities 16 columns at a
-          // time.  Holding the 64 values of a row in registers between them spills at 96 registers a thread.
-          float x0 = -INFINITY, x1 = -INFINITY;
-          const int a = lo - c0, z = hi - c0;   // the row sees columns [a, z)
-          const bool masked = __any_sync(0xffffffffu, a > 0 || z < AT_COLS);
-#pragma unroll STREAM ? 1 : 2
-          for (int q = 0; q < 2; ++q) {
-            uint32_t raw[32];
-            float *v = reinterpret_cast<float *>(raw);
-            tmem_ld32(ts + 32 * q, raw);
-            tmem_wait_ld();
-            if (CAP) {   // cap tanh(s / cap) = cap (1 + 2 r), r = -1 / (1 + 2^(2 log2e s / cap))
+        if (S.any) {
+          uint32_t raw[AT_COLS];
+          float *v = reinterpret_cast<float *>(raw);
+          tmem_ld32(ts, raw);
+          tmem_wait_ld();
+          if (CAP) {   // cap tanh(s / cap) = cap (1 + 2 r), r = -1 / (1 + 2^(2 log2e s / cap))
 #pragma unroll
-              for (int j = 0; j < 32; ++j) v[j] = rcp_approx(-1.f - ex2(v[j] * P.cap_in));
-            }
+            for (int c = 0; c < AT_COLS; ++c) v[c] = rcp_approx(-1.f - ex2(v[c] * P.cap_in));
+          }
+          if (BIAS || mixed) {
+            const int c0 = t * AT_TILE + quarter * AT_COLS;
             if (BIAS) {
-              const float d0 = pos - (float)(c0 + 32 * q), sl = CAP ? 2.f * P.cap_log2 : P.scale_log2;
+              const float d0 = S.pos - (float)c0, sl = CAP ? 2.f * P.cap_log2 : P.scale_log2;
 #pragma unroll
-              for (int j = 0; j < 32; ++j) v[j] = fmaf(-slope, fabsf(d0 - (float)j), v[j] * sl);
+              for (int c = 0; c < AT_COLS; ++c) v[c] = fmaf(-slope, fabsf(d0 - (float)c), v[c] * sl);
             }
-            if (masked) {
-              const int aq = clampi(a - 32 * q, 0, 32), zq = clampi(z - 32 * q, 0, 32);
-              const uint32_t see = (zq == 32 ? ~0u : (1u << zq) - 1u) & (aq == 32 ? 0u : ~0u << aq);
+            if (mixed) {   // the row sees keys [lo, hi)
+              const int a = clampi(S.lo - c0, 0, 32), z = clampi(S.hi - c0, 0, 32);
+              const uint32_t see = (z == 32 ? ~0u : (1u << z) - 1u) & (a == 32 ? 0u : ~0u << a);
 #pragma unroll
-              for (int j = 0; j < 32; ++j)
-                if (!(see & (1u << j))) v[j] = -INFINITY;
-            }
-            if (CAP || BIAS || masked) {   // the second pass reads the finished logits
-              tmem_st16(ts + 32 * q, raw);
-              tmem_st16(ts + 32 * q + 16, raw + 16);
-            }
-#pragma unroll
-            for (int j = 0; j < 32; j += 4) {
-              x0 = max3(x0, v[j], v[j + 1]);
-              x1 = max3(x1, v[j + 2], v[j + 3]);
+              for (int c = 0; c < AT_COLS; ++c)
+                if (!(see & (1u << c))) v[c] = -INFINITY;
             }
           }
-          if (CAP || BIAS || masked) tmem_wait_st();
+          float x0 = v[0], x1 = v[1];
+#pragma unroll
+          for (int c = 2; c < AT_COLS - 2; c += 4) {
+            x0 = max3(x0, v[c], v[c + 1]);
+            x1 = max3(x1, v[c + 2], v[c + 3]);
+          }
+          x0 = max3(x0, v[AT_COLS - 2], v[AT_COLS - 1]);
           const float mx = fmaxf(x0, x1) * scale2;
-          const bool grow = mx > m + 8.f;   // also the first finite max (m = -inf)
-          int any;   // one barrier of the two warps: whether a row of either has grown
+          const bool grow = mx > S.m + 8.f;   // also the first finite max (m = -inf)
+          int any;   // one barrier of the four warps: whether a row has grown in one of them
           asm volatile(
-              "{\n .reg .pred p, q;\n setp.ne.s32 p, %1, 0;\n barrier.cta.red.or.aligned.pred q, %2, 64, p;\n selp.s32 %0, 1, 0, q;\n}"
+              "{\n .reg .pred p, q;\n setp.ne.s32 p, %1, 0;\n barrier.cta.red.or.aligned.pred q, %2, 128, p;\n selp.s32 %0, 1, 0, q;\n}"
               : "=r"(any)
-              : "r"((int)grow), "r"(pair_bar)
+              : "r"((int)grow), "r"(row_bar)
               : "memory");
           if (any) {
             *x_own = mx;
-            asm volatile("bar.sync %0, 64;" ::"r"(pair_bar) : "memory");
-            const float both = fmaxf(mx, *x_other);
+            asm volatile("bar.sync %0, 128;" ::"r"(row_bar) : "memory");
+            const float all = fmaxf(fmaxf(xch[row], xch[AT_TILE + row]), fmaxf(xch[2 * AT_TILE + row], xch[3 * AT_TILE + row]));
             float f = 1.f;
-            if (both > m + 8.f) {
-              f = m == -INFINITY ? 0.f : ex2(m - both);
-              m = both;
+            if (all > S.m + 8.f) {
+              f = S.m == -INFINITY ? 0.f : ex2(S.m - all);
+              S.m = all;
             }
-            l *= f;
-            if (k > 0) {
+            S.l *= f;
+            if (!first) {
 #pragma unroll 1
-              for (int q = 0; q < 4; ++q) {
+              for (int q = 0; q < 2; ++q) {
                 uint32_t o[16];
-                tmem_ld16(to + 16 * q, o);
+                tmem_ld16(ts + 256 + 16 * q, o);
                 tmem_wait_ld();
 #pragma unroll
-                for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
-                tmem_st16(to + 16 * q, o);
+                for (int c = 0; c < 16; ++c) o[c] = __float_as_uint(__uint_as_float(o[c]) * f);
+                tmem_st16(ts + 256 + 16 * q, o);
               }
             }
           }
-          const float mu = m == -INFINITY ? 0.f : m;
-          float a0 = 0.f, a1 = 0.f, a2 = 0.f, a3 = 0.f;
-          // 16 columns at a time, the next 16 on their way while these are worked on; the stream kernel's
-          // loops stay rolled: its calls are short, and instructions that are met for the first time cost about ten cycles
-          // each (a token against 1K keys takes 12.7 us, unrolled 15.2; a 32K prompt the other way round, 6.0 ms and 5.8)
-          auto probs = [&](const uint32_t (&raw)[16], uint32_t at) {
-            const float *v = reinterpret_cast<const float *>(raw);
-            uint32_t pk[8];
+          const float mu = S.m == -INFINITY ? 0.f : S.m;
+          const uint64_t mu2 = pack_f2(-mu, -mu);
+          uint64_t sa = 0, sb = 0;
+          uint32_t pk[16];
 #pragma unroll
-            for (int j = 0; j < 16; j += 4) {
-              float e0, e1, e2, e3;
-              fma2(e0, e1, v[j], v[j + 1], scale2, scale2, -mu, -mu);
-              fma2(e2, e3, v[j + 2], v[j + 3], scale2, scale2, -mu, -mu);
-              e0 = ex2(e0), e1 = ex2(e1), e2 = ex2(e2), e3 = ex2(e3);
-              add2(a0, a1, e0, e1);
-              add2(a2, a3, e2, e3);
-              pk[j / 2] = pack2<FP16>(e0, e1);
-              pk[j / 2 + 1] = pack2<FP16>(e2, e3);
-            }
-            tmem_st8(at, pk);   // over columns already read
-          };
-          uint32_t buf0[16], buf1[16];
-          tmem_ld16(ts, buf0);
-#pragma unroll STREAM ? 1 : 2
-          for (int q = 0; q < 2; ++q) {
-            tmem_wait_ld();
-            tmem_ld16(ts + 32 * q + 16, buf1);
-            probs(buf0, ts + 16 * q);
-            tmem_wait_ld();
-            if (q == 0) tmem_ld16(ts + 32, buf0);
-            probs(buf1, ts + 16 * q + 8);
+          for (int c = 0; c < AT_COLS; c += 4) {
+            float e0, e1, e2, e3;
+            unpack_f2(e0, e1, fma_f2(pack_f2(v[c], v[c + 1]), scale22, mu2));
+            unpack_f2(e2, e3, fma_f2(pack_f2(v[c + 2], v[c + 3]), scale22, mu2));
+            e0 = ex2(e0), e1 = ex2(e1), e2 = ex2(e2), e3 = ex2(e3);
+            sa = add_f2(sa, pack_f2(e0, e1));
+            sb = add_f2(sb, pack_f2(e2, e3));
+            pk[c / 2] = pack2<FP16>(e0, e1);
+            pk[c / 2 + 1] = pack2<FP16>(e2, e3);
           }
-          l += (a0 + a1) + (a2 + a3);
+          tmem_st16(ts, pk);   // over this quarter of S
+          unpack_f2(x0, x1, add_f2(sa, sb));
+          S.l += x0 + x1;
           tmem_wait_st();
         }
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&pfull[slot]);
+      };
+      if (pair) {
+        for (int j = 0; j < I.n; ++j) {
+          step(0, S0, sc0, j, j == 0);
+          step(1, S1, sc1, j, j == 0);
+        }
+      } else if (STREAM) {
+        for (int j = 0; j < I.n; j += 2) {
+          step(0, S0, sc0, j, j == 0);
+          if (j + 1 < I.n) step(1, S1, sc1, j + 1, j == 0);
+        }
       }
-      // ---- the item's rows are done
+      // ---- the item's rows are done: the sums over the quarters, and the outputs
       const float off = CAP ? P.cap_log2 : 0.f;   // of the base-2 logits
-      // a single row tile: slot 0 joins its rows with slot 1's, which stand in the same lanes
-      const bool join = !pair && I.n > 1;
-      const bool writes = pair || slot == 0;
-      bool bad = false;
-      float m1 = -INFINITY, l1 = 0.f;
-      if (n_s > 0) {
+      const bool join = STREAM && !pair && I.n > 1;   // a single row tile: slot 1 holds the same rows' other key tiles
+      const int slots = I.n == 0 ? 0 : pair || join ? 2 : 1;
+      auto whole_row = [&](const int slot, Slot &S, uint32_t &oc) {
         if (ok) ok = attn_wait(&ofull[slot], oc & 1, status);
         ++oc;
-        *x_own = l;
-        if (slot == 1 && half == 0) m_slot1[row] = m;
-        tc_fence_before();
-        __syncwarp();
-        if (join)
-          asm volatile("bar.sync %0, %1;" ::"r"(AT_BAR_ALL), "r"(AT_SOFT * 32) : "memory");
-        else
-          asm volatile("bar.sync %0, 64;" ::"r"(pair_bar) : "memory");
-        tc_fence_after();
-        l = xch[2 * slot * AT_TILE + row] + xch[(2 * slot + 1) * AT_TILE + row];
-        if (join && slot == 0) {
-          m1 = m_slot1[row];
-          l1 = xch[2 * AT_TILE + row] + xch[3 * AT_TILE + row];
-        }
-        bad = bad_item[seq & 1] == (int)seq;
-      }
-      if (writes && any_row) {
-        float *part_o = prefix ? P.pre_o : P.part_o, *part_l = prefix ? P.pre_l : P.part_l;
-        const int64_t part_row = (int64_t)I.part * (prefix ? P.pre_rows : P.part_rows);
-        const float mm = fmaxf(m, m1), mu = mm == -INFINITY ? 0.f : mm;
-        const float w0 = ex2(m - mu), w1 = ex2(m1 - mu);
-        const float lt = l * w0 + l1 * w1;
+        *x_own = S.l;
+        asm volatile("bar.sync %0, 128;" ::"r"(row_bar) : "memory");
+        S.l = (xch[row] + xch[AT_TILE + row]) + (xch[2 * AT_TILE + row] + xch[3 * AT_TILE + row]);
+        asm volatile("bar.sync %0, 128;" ::"r"(row_bar) : "memory");
+      };
+      if (slots > 0) whole_row(0, S0, oc0);
+      if (slots > 1) whole_row(1, S1, oc1);
+      __syncwarp();
+      tc_fence_after();
+      const bool bad = I.n > 0 && bad_item[seq & 1] == (int)seq;
+      float *part_o = prefix ? P.pre_o : P.part_o, *part_l = prefix ? P.pre_l : P.part_l;
+      const int64_t part_row = (int64_t)I.part * (prefix ? P.pre_rows : P.part_rows);
+#pragma unroll 1
+      for (int slot = 0; slot < (pair ? 2 : 1); ++slot) {
+        const float m0 = slot ? S1.m : S0.m, l0 = slot ? S1.l : S0.l, m1 = join ? S1.m : -INFINITY, l1 = join ? S1.l : 0.f;
+        const bool any_row = slot ? S1.any : S0.any;
+        const uint32_t to = lane_base + 256 + 128 * slot;
+        int b, i, h, prow;
+        const bool valid = attn_row<STREAM>(P, I, slot, R, b, i, h, prow);
+        if (!any_row) continue;
+        const float mm = fmaxf(m0, m1), mu = mm == -INFINITY ? 0.f : mm;
+        const float w0 = ex2(m0 - mu), w1 = ex2(m1 - mu);
+        const float lt = l0 * w0 + l1 * w1;
         const float inv = lt == 0.f ? 0.f : 1.f / lt;   // an empty row is 0
         const float lse2 = lt == 0.f ? -INFINITY : mu + off + log2f(lt);
         if (!bad) {
-          if (valid && half == 0) {
+          if (valid && quarter == 0) {
             if (parts)
               part_l[part_row + prow] = lse2;
             else if (P.lse)
               P.lse[((int64_t)b * P.s_q + i) * P.h_q + h] = lse2 * 0.69314718055994531f;
           }
-          const bool have0 = n_s > 0;
+          const bool have0 = I.n > 0;
           const float f0 = w0 * inv, f1 = w1 * inv;
           // 16 channels of the row, scaled, as fp32
           auto take = [&](int q, uint32_t (&o)[16]) {
@@ -936,40 +950,40 @@ __global__ void __launch_bounds__(AT_THREADS, 1) attn_kernel(const __grid_consta
             __syncwarp();
             if (have0) {
               tmem_ld16(to + 16 * q, o);
-              if (STREAM && join) {
+              if (join) {
                 uint32_t o1[16];
                 tmem_ld16(to + 128 + 16 * q, o1);
                 tmem_wait_ld();
 #pragma unroll
-                for (int j = 0; j < 16; ++j) of[j] = of[j] * f0 + __uint_as_float(o1[j]) * f1;
+                for (int c = 0; c < 16; ++c) of[c] = of[c] * f0 + __uint_as_float(o1[c]) * f1;
               } else {
                 tmem_wait_ld();
 #pragma unroll
-                for (int j = 0; j < 16; ++j) of[j] = of[j] * f0;
+                for (int c = 0; c < 16; ++c) of[c] = of[c] * f0;
               }
             }
             if (!have0 || inv == 0.f) {
 #pragma unroll
-              for (int j = 0; j < 16; ++j) of[j] = 0.f;
+              for (int c = 0; c < 16; ++c) of[c] = 0.f;
             }
           };
-          if (STREAM && parts) {
+          if (parts) {
 #pragma unroll 1
-            for (int q = 0; q < 4; ++q) {
+            for (int q = 0; q < 2; ++q) {
               uint32_t o[16];
               take(q, o);
-              float *dst = part_o + (part_row + prow) * D + AT_COLS * half + 16 * q;
+              float *dst = part_o + (part_row + prow) * D + AT_COLS * quarter + 16 * q;
               if (valid && lse2 != -INFINITY) {
                 st_global_v8(dst, o);
                 st_global_v8(dst + 8, o + 8);
               }
             }
           } else {
-            // Eight lanes turn their eight rows of 128 bytes around, 16 bytes at a time, so that each store of a warp writes
-            // four whole rows.  Rows stored by their own lanes touch 32 lines an instruction: 6000 cycles an item, not 1500.
-            uint4 u[8];
+            // Four lanes turn their four rows of 64 bytes around, 16 bytes at a time, so that each store of a warp writes 64
+            // bytes of eight rows.  Rows stored by their own lanes touch 32 lines an instruction.
+            uint4 u[4];
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
+            for (int q = 0; q < 2; ++q) {
               uint32_t o[16];
               take(q, o);
               const float *of = reinterpret_cast<const float *>(o);
@@ -979,10 +993,10 @@ __global__ void __launch_bounds__(AT_THREADS, 1) attn_kernel(const __grid_consta
                                           pack2<FP16>(of[8 * c + 4], of[8 * c + 5]), pack2<FP16>(of[8 * c + 6], of[8 * c + 7]));
             }
 #pragma unroll
-            for (int d = 4; d; d >>= 1) {
+            for (int d = 2; d; d >>= 1) {
               const bool up = lane & d;
 #pragma unroll
-              for (int c = 0; c < 8; ++c) {
+              for (int c = 0; c < 4; ++c) {
                 if (c & d) continue;
                 uint4 send = up ? u[c] : u[c | d];
                 send.x = __shfl_xor_sync(0xffffffffu, send.x, d);
@@ -995,17 +1009,17 @@ __global__ void __launch_bounds__(AT_THREADS, 1) attn_kernel(const __grid_consta
                   u[c | d] = send;
               }
             }
-            const int64_t at = b * P.so[0] + i * P.so[1] + h * P.so[2] + AT_COLS * half;
+            const int64_t at = b * P.so[0] + i * P.so[1] + h * P.so[2] + AT_COLS * quarter;
             const uint32_t rows = __ballot_sync(0xffffffffu, valid);
 #pragma unroll
-            for (int c = 0; c < 8; ++c) {
-              const int r = (lane & 24) + c;
+            for (int c = 0; c < 4; ++c) {
+              const int r = (lane & 28) + c;
               const int64_t o = __shfl_sync(0xffffffffu, at, r);
               if (rows >> r & 1)
-                *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(P.out) + o + 8 * (lane & 7)) = u[c];
+                *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(P.out) + o + 8 * (lane & 3)) = u[c];
             }
           }
-        } else if (half == 0) {
+        } else if (quarter == 0) {
           attn_exact_rows<FP16>(P, I, slot, wq, lane, CAP,
                                 [&](int rb, int ri, int rh, int rp, const float (&acc)[4], float rm, float rl) {
             const float ri_l = rl == 0.f ? 0.f : 1.f / rl;
@@ -1022,12 +1036,6 @@ __global__ void __launch_bounds__(AT_THREADS, 1) attn_kernel(const __grid_consta
             }
           });
         }
-      }
-      if (join) {
-        tc_fence_before();
-        __syncwarp();
-        asm volatile("bar.sync %0, %1;" ::"r"(AT_BAR_ALL), "r"(AT_SOFT * 32) : "memory");   // slot 1 keeps its O until it has been read
-        tc_fence_after();
       }
       base += 2 * I.n;
     }
