@@ -57,13 +57,13 @@ __global__ void __launch_bounds__(RUN_THREADS) doc_runs_kernel(const int *ids, i
   }
 }
 
-// One warp per row (sequence, query, head): out = sum_s 2^(lse_s - L) out_s over the parts of the row's units, L their
-// log2-sum-exp; 512 bytes per part and row, read once.  Which parts a row has is worked out as the attention kernel did,
-// before that kernel is waited for.  128 threads of 32 registers fit beside the attention kernel's CTA.
-template <bool FP16>
+// WARPS warps per row (sequence, query, head): out = sum_s 2^(lse_s - L) out_s over the parts of the row's units, L their
+// log2-sum-exp; 512 bytes per part and row, read once, eight loads of a warp at a time.  Which parts a row has is worked out
+// as the attention kernel did, before that kernel is waited for.  Four warps a row where rows are few: latency.
+template <bool FP16, int WARPS>
 __global__ void __launch_bounds__(128) attn_combine_kernel(const __grid_constant__ AttnArgs P, int ctas) {
-  const int64_t row = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);
-  const int lane = threadIdx.x & 31;
+  const int lane = threadIdx.x & 31, warp = WARPS == 1 ? 0 : threadIdx.x >> 5;
+  const int64_t row = WARPS == 1 ? (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5) : blockIdx.x;
   const int64_t x = row / P.h_q;
   const int h = (int)(row - x * P.h_q), b = (int)(x / P.s_q), i = (int)(x - (int64_t)b * P.s_q);
   if (b >= P.batch) return;
@@ -105,26 +105,43 @@ __global__ void __launch_bounds__(128) attn_combine_kernel(const __grid_constant
   const float mu = mx == -INFINITY ? 0.f : mx;
   float l = 0.f;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int s0 = 0; s0 < n; s0 += 32) {
-    const float w = s0 + lane < n ? ex2(lse_of(s0 + lane) - mu) : 0.f;
+  for (int s0 = 0; s0 < n; s0 += 8 * WARPS) {   // every warp knows the weights of these parts, and reads its eight
+    const float w = lane < 8 * WARPS && s0 + lane < n ? ex2(lse_of(s0 + lane) - mu) : 0.f;
     l += w;
-    const int m = min(32, n - s0);
-#pragma unroll 4
-    for (int s = 0; s < m; ++s) {
-      const float ws = __shfl_sync(0xffffffffu, w, s);
-      if (ws != 0.f) {   // a part without keys for the row wrote no output (NaN weights go on)
-        const int ss = s0 + s;
-        const float *src = ss < n_pre ? P.pre_o + (pre_row + (int64_t)ss * P.pre_rows) * D
-                                      : P.part_o + (own_row + (int64_t)(ss - n_pre) * P.part_rows) * D;
-        const float4 o = *reinterpret_cast<const float4 *>(src + 4 * lane);
-        acc.x = fmaf(ws, o.x, acc.x);
-        acc.y = fmaf(ws, o.y, acc.y);
-        acc.z = fmaf(ws, o.z, acc.z);
-        acc.w = fmaf(ws, o.w, acc.w);
+    float4 o[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const int s = s0 + WARPS * k + warp;
+      const float *src = s < n_pre ? P.pre_o + (pre_row + (int64_t)s * P.pre_rows) * D
+                                   : P.part_o + (own_row + (int64_t)(s - n_pre) * P.part_rows) * D;
+      if (s < n) o[k] = *reinterpret_cast<const float4 *>(src + 4 * lane);
+    }
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const float ws = __shfl_sync(0xffffffffu, w, WARPS * k + warp);
+      if (s0 + WARPS * k + warp < n && ws != 0.f) {   // a part without keys for the row wrote no output (NaN weights go on)
+        acc.x = fmaf(ws, o[k].x, acc.x);
+        acc.y = fmaf(ws, o[k].y, acc.y);
+        acc.z = fmaf(ws, o[k].z, acc.z);
+        acc.w = fmaf(ws, o[k].w, acc.w);
       }
     }
   }
   for (int o = 16; o; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+  if (WARPS > 1) {
+    __shared__ float4 sums[WARPS][32];
+    sums[warp][lane] = acc;
+    __syncthreads();
+    if (warp) return;
+#pragma unroll
+    for (int k = 1; k < WARPS; ++k) {
+      const float4 o = sums[k][lane];
+      acc.x += o.x;
+      acc.y += o.y;
+      acc.z += o.z;
+      acc.w += o.w;
+    }
+  }
   const float inv = l == 0.f ? 0.f : 1.f / l;
   *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(P.out) + b * P.so[0] + i * P.so[1] + h * P.so[2] + 4 * lane) =
       make_uint2(pack2<FP16>(acc.x * inv, acc.y * inv), pack2<FP16>(acc.z * inv, acc.w * inv));
@@ -173,8 +190,12 @@ struct AttnPlan {
   int64_t rows, off_runs, off_l, off_o, off_pl, off_po, bytes;
 };
 
-// Key tiles that a CTA takes at least, where the stream is cut finer than its CTAs would need
+// Key tiles that a CTA takes at least: a token of 8 heads against 16K keys takes 12 us with 2, 13.6 with 1, 13.2 with 6;
+// against 1K keys 10, 9.6 and 13 us.
 constexpr int MIN_TILES = 2;
+// Row tiles against up to this many key tiles are not cut where there are half as many of them as SMs: 16 tokens of 32 heads
+// against 1K keys take 16 us whole, 19 as parts; 64 of different lengths up to 1K 42 and 48 us.
+constexpr int WHOLE_TILES = 8;
 
 bool stride_ok(int64_t st, int64_t size, bool zero) {
   if (size <= 1) return true;
@@ -216,8 +237,8 @@ qevict_status attn_plan(const qevict_attn_desc *d, int s_prefix, AttnPlan *p) {
   // One stream of key tiles cut into equal shares, or whole units in turn.  The stream evens out caches of different
   // lengths and fills the SMs when there are few units, at the price of parts that are merged afterwards: for units of one
   // row tile (few rows to merge) always but when none would be cut, for larger ones while they leave SMs without work.
-  p->stream = s_prefix || (n_qt == 1 ? tiles > MIN_TILES : units < sms && tiles > MIN_TILES);
-  if (total > (1 << 30) && p->stream) {
+  p->stream = s_prefix || (tiles > MIN_TILES && (n_qt == 1 ? tiles > WHOLE_TILES || 2 * units < sms : units < sms));
+  if ((total > (1 << 30) || p->rows > (1ll << 32)) && p->stream) {
     if (s_prefix) return QEVICT_EINVAL;
     p->stream = 0;
   }
@@ -324,13 +345,15 @@ qevict_status attn_launch(const qevict_attn_desc *d, const AttnPlan &pl, const q
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.gridDim = dim3((unsigned)((pl.rows + 3) / 4));
+    const bool few = pl.rows <= 1024;
+    cfg.gridDim = dim3((unsigned)(few ? pl.rows : (pl.rows + 3) / 4));
     cfg.blockDim = dim3(128);
     cfg.stream = s;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    if (cudaLaunchKernelEx(&cfg, fp16 ? attn_combine_kernel<true> : attn_combine_kernel<false>, A, pl.grid) != cudaSuccess)
-      return QEVICT_ECUDA;
+    const auto combine = few ? (fp16 ? attn_combine_kernel<true, 4> : attn_combine_kernel<false, 4>)
+                             : (fp16 ? attn_combine_kernel<true, 1> : attn_combine_kernel<false, 1>);
+    if (cudaLaunchKernelEx(&cfg, combine, A, pl.grid) != cudaSuccess) return QEVICT_ECUDA;
   }
   return QEVICT_OK;
 }

@@ -286,6 +286,12 @@ __device__ __forceinline__ void st_global_v8(void *p, const uint32_t *r) {   // 
                "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
                : "memory");
 }
+__device__ __forceinline__ float min_nan(float x, float y) {   // NaN if one is
+  float d;
+  asm("min.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(x), "f"(y));
+  return d;
+}
+
 // Packed fp32 pairs as 64-bit values: what stays the same over a loop is packed once
 __device__ __forceinline__ uint64_t pack_f2(float x, float y) {
   uint64_t d;
@@ -474,11 +480,25 @@ __global__ void __launch_bounds__(AT_THREADS, 1) attn_kernel(const __grid_consta
     fence_mbar_init();
     if (threadIdx.x < 2) bad_item[threadIdx.x] = 0;
   }
+  // The launch may overlap the previous kernel's end: nothing is read from device memory before this wait, and the next
+  // kernel is let in only after it, so whatever starts early still finds the kernel two launches back complete.
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  AttnGroup plan_a;        // the plan warp's lane: its group of the first 32, worked out while the others set up
+  int plan_places = 0;     // and the places of all groups
+  if (warp == AT_W_PLAN && STREAM) {
+    const int groups = P.n_pr * P.batch;
+#pragma unroll 1
+    for (int g0 = 0; g0 < groups; g0 += 32) {
+      const AttnGroup A = attn_group(P, min(g0 + lane, groups - 1));
+      if (g0 == 0) plan_a = A;
+      plan_places += __reduce_add_sync(0xffffffffu, g0 + lane < groups ? attn_places(A.t_hi - A.t_lo) : 0) * P.h_kv;
+    }
+  }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
   // Next work item of a role: waits for its description, copies what the role keeps and hands the ring place back.
   uint32_t seq = 0;
@@ -518,10 +538,6 @@ __global__ void __launch_bounds__(AT_THREADS, 1) attn_kernel(const __grid_consta
       return I;
     };
     const int groups = P.n_pr * P.batch;
-    if (blockIdx.x == 0)   // lengths out of range are clamped everywhere; here they are reported
-      for (int b = lane; b < P.batch; b += 32)
-        if ((P.kv_len && (P.kv_len[b] < 0 || P.kv_len[b] > P.s_kv)) || (P.q_len && (P.q_len[b] < 0 || P.q_len[b] > P.s_q)))
-          atomicOr(status, QV_ERR_BOUNDS);
     if (!STREAM) {
       // whole units, the longest (last rows of causal prompts) first, every second round in reverse so that the CTAs'
       // sums come out even
@@ -537,76 +553,73 @@ __global__ void __launch_bounds__(AT_THREADS, 1) attn_kernel(const __grid_consta
       // share's end is written as parts, numbered CTA + unit: the numbers of a unit's parts are consecutive, and none is
       // used twice, since both terms only grow along the stream.
       const int tp = P.pre ? (P.pre + AT_TILE - 1) / AT_TILE : 0, wp = attn_places(tp), all_p = P.pre ? P.n_prp * P.h_kv * wp : 0;
-      int pos = 0, end = 0, share = 1;
-      AttnGroup A;
-      int done = 0;   // stream position of the groups at hand
-      for (int pass = 0; ok && pass < 2; ++pass) {   // the sum of all places, then the items
-        done = pass ? all_p : 0;
-        for (int g0 = 0; ok && g0 < groups; g0 += 32) {
-          if (pass == 0 || groups > 32) A = attn_group(P, min(g0 + lane, groups - 1));
-          const int t = g0 + lane < groups ? A.t_hi - A.t_lo : 0;
-          const int total = __reduce_add_sync(0xffffffffu, attn_places(t)) * P.h_kv;
-          if (pass == 0 || done + total <= pos || pos >= end) {
-            done += total;
+      const int64_t total = (int64_t)all_p + plan_places;
+      const int share = attn_share((int)total, gridDim.x, P.min_tiles);
+      const int begin = (int)min((int64_t)blockIdx.x * share, total), end = (int)min((int64_t)begin + share, total);
+      int pos = begin;
+      while (ok && pos < min(end, all_p)) {
+        const int u = pos / wp, o = pos - u * wp, pr = u / P.h_kv;
+        if (o < tp) {
+          AttnItem I;
+          I.tile0 = 2 * pr;
+          I.kind = 1 | 4 | ((I.tile0 + 1) * P.nb < P.batch ? 2 : 0);
+          I.b = 0, I.g = u - pr * P.h_kv, I.kl = P.pre, I.ql = P.s_q, I.pfx = 0;
+          I.n = min(tp - o, end - pos);
+          I.t_hi = tp - o;
+          I.clean_lo = I.key_lo = 0;
+          I.clean_hi = I.key_hi = P.pre;
+          I.part = blockIdx.x + u;
+          put(I);
+        }
+        pos = (u + 1) * wp;
+      }
+      int done = all_p;   // stream position of the groups at hand
+#pragma unroll 1
+      for (int g0 = 0; ok && pos < end && g0 < groups; g0 += 32) {
+        const AttnGroup A = g0 == 0 ? plan_a : attn_group(P, min(g0 + lane, groups - 1));
+        const int t = g0 + lane < groups ? A.t_hi - A.t_lo : 0;
+        const int here = __reduce_add_sync(0xffffffffu, attn_places(t)) * P.h_kv;
+        if (done + here <= pos) {
+          done += here;
+          continue;
+        }
+#pragma unroll 1
+        for (int q = 0; ok && pos < end && q < 32; ++q) {
+          const int tq = __shfl_sync(0xffffffffu, t, q), wq = attn_places(tq);
+          if (done + wq * P.h_kv <= pos) {
+            done += wq * P.h_kv;
             continue;
           }
-#pragma unroll 1
-          for (int q = 0; ok && pos < end && q < 32; ++q) {
-            const int tq = __shfl_sync(0xffffffffu, t, q), wq = attn_places(tq);
-            if (done + wq * P.h_kv <= pos) {
-              done += wq * P.h_kv;
-              continue;
-            }
-            AttnGroup B;
-            B.b = __shfl_sync(0xffffffffu, A.b, q), B.tile0 = __shfl_sync(0xffffffffu, A.tile0, q);
-            B.kl = __shfl_sync(0xffffffffu, A.kl, q), B.ql = __shfl_sync(0xffffffffu, A.ql, q);
-            B.pfx = __shfl_sync(0xffffffffu, A.pfx, q);
-            B.clean_lo = __shfl_sync(0xffffffffu, A.clean_lo, q), B.clean_hi = __shfl_sync(0xffffffffu, A.clean_hi, q);
-            B.key_lo = __shfl_sync(0xffffffffu, A.key_lo, q), B.key_hi = __shfl_sync(0xffffffffu, A.key_hi, q);
-            B.t_lo = __shfl_sync(0xffffffffu, A.t_lo, q), B.t_hi = __shfl_sync(0xffffffffu, A.t_hi, q);
-            while (ok && pos < min(end, done + wq * P.h_kv)) {
-              const int g = (pos - done) / wq, u0 = done + g * wq, o = pos - u0;
-              if (o < tq) {
-                AttnItem I = own_item(B, g);
-                I.n = min(tq - o, end - pos);
-                I.t_hi -= o;
-                I.part = blockIdx.x + (g0 + q) * P.h_kv + g;
-                if (P.pre || u0 / share != (u0 + tq - 1) / share) I.kind |= 4;
-                put(I);
-              }
-              pos = u0 + wq;
-            }
-            done += wq * P.h_kv;
-          }
-        }
-        if (pass == 0) {
-          const int64_t total = (int64_t)all_p + done;
-          share = attn_share((int)total, gridDim.x, P.min_tiles);
-          pos = (int)min((int64_t)blockIdx.x * share, total);
-          end = (int)min((int64_t)pos + share, total);
-          while (ok && pos < min(end, all_p)) {
-            const int u = pos / wp, o = pos - u * wp, pr = u / P.h_kv;
-            if (o < tp) {
-              AttnItem I;
-              I.tile0 = 2 * pr;
-              I.kind = 1 | 4 | ((I.tile0 + 1) * P.nb < P.batch ? 2 : 0);
-              I.b = 0, I.g = u - pr * P.h_kv, I.kl = P.pre, I.ql = P.s_q, I.pfx = 0;
-              I.n = min(tp - o, end - pos);
-              I.t_hi = tp - o;
-              I.clean_lo = I.key_lo = 0;
-              I.clean_hi = I.key_hi = P.pre;
-              I.part = blockIdx.x + u;
+          AttnGroup B;
+          B.b = __shfl_sync(0xffffffffu, A.b, q), B.tile0 = __shfl_sync(0xffffffffu, A.tile0, q);
+          B.kl = __shfl_sync(0xffffffffu, A.kl, q), B.ql = __shfl_sync(0xffffffffu, A.ql, q);
+          B.pfx = __shfl_sync(0xffffffffu, A.pfx, q);
+          B.clean_lo = __shfl_sync(0xffffffffu, A.clean_lo, q), B.clean_hi = __shfl_sync(0xffffffffu, A.clean_hi, q);
+          B.key_lo = __shfl_sync(0xffffffffu, A.key_lo, q), B.key_hi = __shfl_sync(0xffffffffu, A.key_hi, q);
+          B.t_lo = __shfl_sync(0xffffffffu, A.t_lo, q), B.t_hi = __shfl_sync(0xffffffffu, A.t_hi, q);
+          while (ok && pos < min(end, done + wq * P.h_kv)) {
+            const int g = (pos - done) / wq, u0 = done + g * wq, o = pos - u0;
+            if (o < tq) {
+              AttnItem I = own_item(B, g);
+              I.n = min(tq - o, end - pos);
+              I.t_hi -= o;
+              I.part = blockIdx.x + (g0 + q) * P.h_kv + g;
+              if (P.pre || u0 < begin || u0 + tq > begin + share) I.kind |= 4;   // not all in this share
               put(I);
             }
-            pos = (u + 1) * wp;
+            pos = u0 + wq;
           }
-          if (pos >= end) break;
+          done += wq * P.h_kv;
         }
       }
     }
     AttnItem I = {};
     I.kind = -1;
     put(I);
+    if (blockIdx.x == 0)   // lengths out of range are clamped everywhere; here they are reported
+      for (int b = lane; b < P.batch; b += 32)
+        if ((P.kv_len && (P.kv_len[b] < 0 || P.kv_len[b] > P.s_kv)) || (P.q_len && (P.q_len[b] < 0 || P.q_len[b] > P.s_q)))
+          atomicOr(status, QV_ERR_BOUNDS);
   } else if (warp == AT_W_LOAD) {
     // ---- TMA loads
     const uint32_t qbytes = (uint32_t)(P.G * P.tpt) * 256u, qpbytes = (uint32_t)(P.G * P.s_q * P.nb) * 256u;
@@ -812,24 +825,35 @@ __global__ void __launch_bounds__(AT_THREADS, 1) attn_kernel(const __grid_consta
           float *v = reinterpret_cast<float *>(raw);
           tmem_ld32(ts, raw);
           tmem_wait_ld();
-          if (CAP) {   // cap tanh(s / cap) = cap (1 + 2 r), r = -1 / (1 + 2^(2 log2e s / cap))
-#pragma unroll
-            for (int c = 0; c < AT_COLS; ++c) v[c] = rcp_approx(-1.f - ex2(v[c] * P.cap_in));
+          const int c0 = t * AT_TILE + quarter * AT_COLS;
+          uint32_t see = ~0u;
+          if (mixed) {   // the row sees keys [lo, hi)
+            const int a = clampi(S.lo - c0, 0, 32), z = clampi(S.hi - c0, 0, 32);
+            see = (z == 32 ? ~0u : (1u << z) - 1u) & (a == 32 ? 0u : ~0u << a);
           }
-          if (BIAS || mixed) {
-            const int c0 = t * AT_TILE + quarter * AT_COLS;
-            if (BIAS) {
-              const float d0 = S.pos - (float)c0, sl = CAP ? 2.f * P.cap_log2 : P.scale_log2;
-#pragma unroll
-              for (int c = 0; c < AT_COLS; ++c) v[c] = fmaf(-slope, fabsf(d0 - (float)c), v[c] * sl);
-            }
-            if (mixed) {   // the row sees keys [lo, hi)
-              const int a = clampi(S.lo - c0, 0, 32), z = clampi(S.hi - c0, 0, 32);
-              const uint32_t see = (z == 32 ? ~0u : (1u << z) - 1u) & (a == 32 ? 0u : ~0u << a);
+          if (CAP) {   // cap tanh(s / cap) = cap (1 + 2 r), r = -1 / (1 + 2^(2 log2e s / cap))
+            if (mixed) {   // a NaN in a masked place stays out of its neighbour's reciprocal
 #pragma unroll
               for (int c = 0; c < AT_COLS; ++c)
-                if (!(see & (1u << c))) v[c] = -INFINITY;
+                if (!(see & (1u << c))) v[c] = 0.f;
             }
+#pragma unroll
+            for (int c = 0; c < AT_COLS; c += 2) {   // one reciprocal for two: 1 / a = b / (a b), with |a|, |b| <= 1 + 2^60
+              const float a = -1.f - ex2(min_nan(v[c] * P.cap_in, 60.f)), b = -1.f - ex2(min_nan(v[c + 1] * P.cap_in, 60.f));
+              const float r = rcp_approx(a * b);
+              v[c] = b * r;
+              v[c + 1] = a * r;
+            }
+          }
+          if (BIAS) {
+            const float d0 = S.pos - (float)c0, sl = CAP ? 2.f * P.cap_log2 : P.scale_log2;
+#pragma unroll
+            for (int c = 0; c < AT_COLS; ++c) v[c] = fmaf(-slope, fabsf(d0 - (float)c), v[c] * sl);
+          }
+          if (mixed) {
+#pragma unroll
+            for (int c = 0; c < AT_COLS; ++c)
+              if (!(see & (1u << c))) v[c] = -INFINITY;
           }
           float x0 = v[0], x1 = v[1];
 #pragma unroll
@@ -916,7 +940,7 @@ __global__ void __launch_bounds__(AT_THREADS, 1) attn_kernel(const __grid_consta
         asm volatile("bar.sync %0, 128;" ::"r"(row_bar) : "memory");
       };
       if (slots > 0) whole_row(0, S0, oc0);
-      if (slots > 1) whole_row(1, S1, oc1);
+      if (STREAM && slots > 1) whole_row(1, S1, oc1);
       __syncwarp();
       tc_fence_after();
       const bool bad = I.n > 0 && bad_item[seq & 1] == (int)seq;
@@ -924,6 +948,11 @@ __global__ void __launch_bounds__(AT_THREADS, 1) attn_kernel(const __grid_consta
       const int64_t part_row = (int64_t)I.part * (prefix ? P.pre_rows : P.part_rows);
 #pragma unroll 1
       for (int slot = 0; slot < (pair ? 2 : 1); ++slot) {
+        if (!STREAM && slot && I.n > 0) {   // whole units finish slot 0 while slot 1's last product runs
+          whole_row(1, S1, oc1);
+          __syncwarp();
+          tc_fence_after();
+        }
         const float m0 = slot ? S1.m : S0.m, l0 = slot ? S1.l : S0.l, m1 = join ? S1.m : -INFINITY, l1 = join ? S1.l : 0.f;
         const bool any_row = slot ? S1.any : S0.any;
         const uint32_t to = lane_base + 256 + 128 * slot;
@@ -933,7 +962,7 @@ __global__ void __launch_bounds__(AT_THREADS, 1) attn_kernel(const __grid_consta
         const float mm = fmaxf(m0, m1), mu = mm == -INFINITY ? 0.f : mm;
         const float w0 = ex2(m0 - mu), w1 = ex2(m1 - mu);
         const float lt = l0 * w0 + l1 * w1;
-        const float inv = lt == 0.f ? 0.f : 1.f / lt;   // an empty row is 0
+        const float inv = lt == 0.f ? 0.f : rcp_approx(lt);   // an empty row is 0
         const float lse2 = lt == 0.f ? -INFINITY : mu + off + log2f(lt);
         if (!bad) {
           if (valid && quarter == 0) {
@@ -962,7 +991,7 @@ __global__ void __launch_bounds__(AT_THREADS, 1) attn_kernel(const __grid_consta
                 for (int c = 0; c < 16; ++c) of[c] = of[c] * f0;
               }
             }
-            if (!have0 || inv == 0.f) {
+            else {
 #pragma unroll
               for (int c = 0; c < 16; ++c) of[c] = 0.f;
             }
@@ -1048,18 +1077,30 @@ __global__ void __launch_bounds__(AT_THREADS, 1) attn_kernel(const __grid_consta
   }
 }
 
+// (Programmatic launch: the kernel's setup overlaps the end of the one before.)
+template <typename Kernel>
+cudaError_t launch_attn_kernel(Kernel kern, const AttnArgs &P, int grid, cudaStream_t s) {
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.gridDim = dim3((unsigned)grid);
+  cfg.blockDim = dim3(AT_THREADS);
+  cfg.dynamicSmemBytes = AT_SMEM;
+  cfg.stream = s;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, P);
+}
+
 template <bool FP16, bool CAP, bool BIAS>
 cudaError_t launch_attn_variant(const AttnArgs &P, int grid, cudaStream_t s) {
   static SmemOptIn units, stream;
-  cudaError_t e;
-  if (P.stream) {
-    e = stream.ensure(attn_kernel<FP16, CAP, BIAS, true>, AT_SMEM);
-    if (e == cudaSuccess) attn_kernel<FP16, CAP, BIAS, true><<<grid, AT_THREADS, AT_SMEM, s>>>(P);
-  } else {
-    e = units.ensure(attn_kernel<FP16, CAP, BIAS, false>, AT_SMEM);
-    if (e == cudaSuccess) attn_kernel<FP16, CAP, BIAS, false><<<grid, AT_THREADS, AT_SMEM, s>>>(P);
-  }
-  return e == cudaSuccess ? cudaGetLastError() : e;
+  cudaError_t e = P.stream ? stream.ensure(attn_kernel<FP16, CAP, BIAS, true>, AT_SMEM)
+                           : units.ensure(attn_kernel<FP16, CAP, BIAS, false>, AT_SMEM);
+  if (e != cudaSuccess) return e;
+  return P.stream ? launch_attn_kernel(attn_kernel<FP16, CAP, BIAS, true>, P, grid, s)
+                  : launch_attn_kernel(attn_kernel<FP16, CAP, BIAS, false>, P, grid, s);
 }
 
 }  // namespace qv

@@ -162,10 +162,34 @@ def test_masked_places_may_hold_anything(lib, dtype, bad):
     one.check()
 
 
-def test_visible_nan_scores_propagate(lib):
+@pytest.mark.parametrize("slopes", [False, True])
+def test_masked_places_with_capped_scores(lib, slopes):
+    """Keys behind the end and of later tokens hold NaN next to visible ones; infinite scores reach the cap."""
+    B, s = 2, 260
+    q, k, v = rnd(B, s, 4, 128), rnd(B, s, 2, 128, seed=2), rnd(B, s, 2, 128, seed=3)
+    k[0, 131:], v[0, 131:] = math.nan, math.inf
+    k[1, 201], v[1, 201] = math.nan, -math.inf
+    q[1, 7] = 1e38       # products overflow to infinities of both signs
+    sl = torch.tensor([0.5, 0.25, 0.125, 0.0], device="cuda") if slopes else None
+    plan = binding.Attention(B, s, s, 4, 2, softcap=25.0)
+    out, lse = plan.run(q, k, v, slopes=sl, kv_len=i32([131, 201]), q_len=i32([131, 201]))
+    plan.check()
+    assert torch.isfinite(out[0, :131].float()).all() and torch.isfinite(lse[1, :201]).all()
+    qq = q.clone()
+    qq[1, 7] = 0
+    ref = R.attention(qq, k, v, slopes=sl, cap=25.0, kv_len=[131, 201], q_len=[131, 201])
+    keep = [i for i in range(201) if i != 7]
+    for (b, h), (o, ls, eo, el) in ref.items():
+        rows = torch.tensor(keep if b else range(131), device="cuda")
+        assert torch.all((out[b, rows, h].double() - o[rows]).abs() <= eo[rows])
+        assert torch.all((lse[b, rows, h].double() - ls[rows]).abs() <= el[rows] if torch.is_tensor(el) else el)
+
+
+@pytest.mark.parametrize("cap", [0.0, 20.0])
+def test_visible_nan_scores_propagate(lib, cap):
     q, k, v = rnd(1, 4, 2, 128), rnd(1, 300, 1, 128, seed=2), rnd(1, 300, 1, 128, seed=3)
     q[0, 1, 0] = math.nan
-    plan = binding.Attention(1, 4, 300, 2, 1)
+    plan = binding.Attention(1, 4, 300, 2, 1, softcap=cap)
     out, lse = plan.run(q, k, v)
     assert torch.isnan(out[0, 1, 0]).all() and torch.isnan(lse[0, 1, 0])
     keep = [0, 2, 3]
