@@ -235,9 +235,11 @@ qevict_status attn_plan(const qevict_attn_desc *d, int s_prefix, AttnPlan *p) {
     total += (int64_t)p->n_prp * d->h_kv * ((s_prefix + AT_TILE - 1) / AT_TILE + AT_UNIT_COST);
   }
   // One stream of key tiles cut into equal shares, or whole units in turn.  The stream evens out caches of different
-  // lengths and fills the SMs when there are few units, at the price of parts that are merged afterwards: for units of one
-  // row tile (few rows to merge) always but when none would be cut, for larger ones while they leave SMs without work.
-  p->stream = s_prefix || (tiles > MIN_TILES && (n_qt == 1 ? tiles > WHOLE_TILES || 2 * units < sms : units < sms));
+  // lengths and fills the SMs when there are few units, at the price of parts that are merged afterwards.  Units of one row tile
+  // have few rows to merge.  Pairs have 256, which costs as much as about 16 key tiles: prompts of 512 and 1024 tokens take 29 and 43 us
+  // as a stream, 13 and 17 as units; the last 256 tokens of 32K 114 us as a stream.
+  p->stream = s_prefix || (tiles > MIN_TILES && (n_qt == 1 ? tiles > WHOLE_TILES || 2 * units < sms
+                                                           : tiles * (sms - std::min(units, sms)) >= 16 * sms));
   if ((total > (1 << 30) || p->rows > (1ll << 32)) && p->stream) {
     if (s_prefix) return QEVICT_EINVAL;
     p->stream = 0;
@@ -311,8 +313,12 @@ qevict_status attn_launch(const qevict_attn_desc *d, const AttnPlan &pl, const q
   const float scale = d->scale > 0.f ? d->scale : 1.f / std::sqrt((float)D), log2e = 1.4426950408889634f;
   A.scale_log2 = scale * log2e;
   if (d->softcap > 0.f) {
-    A.cap_in = 2.f * log2e * scale / d->softcap;
-    A.cap_log2 = d->softcap * log2e;
+    A.cap_u = scale / d->softcap;
+    A.cap_s = d->softcap / scale;
+    const double q[5] = {0.9999999403953552, -0.33332324028015137, 0.13310357928276062, -0.052109625190496445,
+                         0.01548669021576643};
+    const double u = A.cap_u;
+    for (int i = 0; i < 5; ++i) A.cap_q[i] = (float)(q[i] * std::pow(u, 2 * i));
   }
   const bool fp16 = d->dtype == QEVICT_FP16;
   const int qb = A.mul_q ? d->batch : 1, kb = A.mul_k ? d->batch : 1, vb = A.mul_v ? d->batch : 1;

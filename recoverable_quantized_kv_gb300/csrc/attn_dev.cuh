@@ -50,7 +50,8 @@ struct AttnArgs {
   int part_rows, pre_rows;     // rows of a part
   int stream, min_tiles;       // the key tiles of all units as one stream, cut into equal shares of at least min_tiles
   float scale_log2;            // logit scale * log2 e
-  float cap_in, cap_log2;      // softcap: 2 log2 e * scale / cap, cap * log2 e
+  float cap_u, cap_s;          // softcap: scale / cap, cap / scale
+  float cap_q[5];              // tanh(u) / u in powers of the product's square, u = product * cap_u
 };
 
 __device__ __forceinline__ int clampi(int x, int lo, int hi) { return x < lo ? lo : x > hi ? hi : x; }
@@ -304,6 +305,11 @@ __device__ __forceinline__ uint64_t fma_f2(uint64_t a, uint64_t b, uint64_t c) {
   asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
   return d;
 }
+__device__ __forceinline__ uint64_t mul_f2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
 __device__ __forceinline__ uint64_t add_f2(uint64_t a, uint64_t b) {
   uint64_t d;
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
@@ -408,7 +414,7 @@ __device__ __forceinline__ void attn_exact_rows(const AttnArgs &P, const AttnIte
             s = fmaf(a.x, c.x, s);
             s = fmaf(a.y, c.y, s);
           }
-          x = cap ? P.cap_log2 * (1.f - 2.f * rcp_approx(1.f + ex2(s * P.cap_in))) : s * P.scale_log2;
+          x = (cap ? P.cap_s * tanhf(s * P.cap_u) : s) * P.scale_log2;
           x -= slope * fabsf((float)(p - key));
         }
         float mx = x;
@@ -798,9 +804,41 @@ __global__ void __launch_bounds__(AT_THREADS, 1) attn_kernel(const __grid_consta
       else
         S1 = S0;
       // x = value * scale2: the products themselves, or with BIAS the finished logit
-      const float scale2 = BIAS ? 1.f : CAP ? 2.f * P.cap_log2 : P.scale_log2;
+      const float scale2 = BIAS ? 1.f : P.scale_log2;
       const uint64_t scale22 = pack_f2(scale2, scale2);
       const int clean_lo = (I.clean_lo + AT_TILE - 1) / AT_TILE, clean_hi = I.clean_hi / AT_TILE;   // tiles that every row sees whole
+      // Capped products: y with y scale = cap tanh(v scale / cap).  Where no |v scale / cap| of the warp's rows exceeds 0.6, the
+      // usual case, tanh(u) = u Q(u^2) with Q of degree 4, fitted at Chebyshev nodes on [0, 0.36] (error 7e-8 of tanh in fp32), its
+      // coefficients scaled to take v: six packed operations for two.  Else 1 - 2 / (1 + 2^(2 log2e u)) with one
+      // reciprocal for two, 1 / a = b / (a b), where 2^60 bounds the exponentials so that the product stays finite.
+      auto capped = [&](float *v) {
+        float x0 = 0.f, x1 = 0.f;
+#pragma unroll
+        for (int c = 0; c < AT_COLS; c += 4) {
+          x0 = max3(x0, fabsf(v[c]), fabsf(v[c + 1]));
+          x1 = max3(x1, fabsf(v[c + 2]), fabsf(v[c + 3]));
+        }
+        if (__all_sync(0xffffffffu, fmaxf(x0, x1) * P.cap_u <= 0.6f)) {
+          const uint64_t q0 = pack_f2(P.cap_q[0], P.cap_q[0]), q1 = pack_f2(P.cap_q[1], P.cap_q[1]),
+                         q2 = pack_f2(P.cap_q[2], P.cap_q[2]), q3 = pack_f2(P.cap_q[3], P.cap_q[3]),
+                         q4 = pack_f2(P.cap_q[4], P.cap_q[4]);
+#pragma unroll
+          for (int c = 0; c < AT_COLS; c += 2) {
+            const uint64_t v2 = pack_f2(v[c], v[c + 1]), z = mul_f2(v2, v2);
+            const uint64_t q = fma_f2(z, fma_f2(z, fma_f2(z, fma_f2(z, q4, q3), q2), q1), q0);
+            unpack_f2(v[c], v[c + 1], mul_f2(v2, q));
+          }
+        } else {
+          const float in = P.cap_u * 2.8853900817779268f;   // 2 log2 e
+#pragma unroll
+          for (int c = 0; c < AT_COLS; c += 2) {
+            const float a = 1.f + ex2(min_nan(v[c] * in, 60.f)), b = 1.f + ex2(min_nan(v[c + 1] * in, 60.f));
+            const float r = rcp_approx(a * b) * (-2.f * P.cap_s);
+            v[c] = fmaf(b, r, P.cap_s);
+            v[c + 1] = fmaf(a, r, P.cap_s);
+          }
+        }
+      };
       // One slot's S of key tile j (from the last) into probabilities; first: the slot's first tile
       auto step = [&](const int slot, Slot &S, uint32_t &sc, int j, bool first) {
         const int t = I.t_hi - 1 - j;
@@ -831,24 +869,31 @@ __global__ void __launch_bounds__(AT_THREADS, 1) attn_kernel(const __grid_consta
             const int a = clampi(S.lo - c0, 0, 32), z = clampi(S.hi - c0, 0, 32);
             see = (z == 32 ? ~0u : (1u << z) - 1u) & (a == 32 ? 0u : ~0u << a);
           }
-          if (CAP) {   // cap tanh(s / cap) = cap (1 + 2 r), r = -1 / (1 + 2^(2 log2e s / cap))
-            if (mixed) {   // a NaN in a masked place stays out of its neighbour's reciprocal
+          float base2 = 0.f;       // of every logit of the row in this tile
+          if (CAP) {
+            if (mixed) {           // a NaN in a masked place stays out of its neighbours
 #pragma unroll
               for (int c = 0; c < AT_COLS; ++c)
                 if (!(see & (1u << c))) v[c] = 0.f;
             }
-#pragma unroll
-            for (int c = 0; c < AT_COLS; c += 2) {   // one reciprocal for two: 1 / a = b / (a b), with |a|, |b| <= 1 + 2^60
-              const float a = -1.f - ex2(min_nan(v[c] * P.cap_in, 60.f)), b = -1.f - ex2(min_nan(v[c + 1] * P.cap_in, 60.f));
-              const float r = rcp_approx(a * b);
-              v[c] = b * r;
-              v[c + 1] = a * r;
-            }
+            capped(v);
           }
           if (BIAS) {
-            const float d0 = S.pos - (float)c0, sl = CAP ? 2.f * P.cap_log2 : P.scale_log2;
+            const float sl = P.scale_log2, d0 = S.pos - (float)c0;
+            if ((P.causal && !P.prefix_len) || __all_sync(0xffffffffu, d0 >= (float)(AT_COLS - 1))) {
+              // no key behind the row's position is seen: -slope |p - j| = -slope (p - c0) + slope (j - c0)
+              const uint64_t sl2 = pack_f2(sl, sl), hop = pack_f2(2.f * slope, 2.f * slope);
+              uint64_t b2 = pack_f2(0.f, slope);
 #pragma unroll
-            for (int c = 0; c < AT_COLS; ++c) v[c] = fmaf(-slope, fabsf(d0 - (float)c), v[c] * sl);
+              for (int c = 0; c < AT_COLS; c += 2) {
+                unpack_f2(v[c], v[c + 1], fma_f2(pack_f2(v[c], v[c + 1]), sl2, b2));
+                b2 = add_f2(b2, hop);
+              }
+              base2 = -slope * d0;
+            } else {
+#pragma unroll
+              for (int c = 0; c < AT_COLS; ++c) v[c] = fmaf(-slope, fabsf(d0 - (float)c), v[c] * sl);
+            }
           }
           if (mixed) {
 #pragma unroll
@@ -862,7 +907,7 @@ __global__ void __launch_bounds__(AT_THREADS, 1) attn_kernel(const __grid_consta
             x1 = max3(x1, v[c + 2], v[c + 3]);
           }
           x0 = max3(x0, v[AT_COLS - 2], v[AT_COLS - 1]);
-          const float mx = fmaxf(x0, x1) * scale2;
+          const float mx = fmaf(fmaxf(x0, x1), scale2, base2);
           const bool grow = mx > S.m + 8.f;   // also the first finite max (m = -inf)
           int any;   // one barrier of the four warps: whether a row has grown in one of them
           asm volatile(
@@ -893,7 +938,7 @@ __global__ void __launch_bounds__(AT_THREADS, 1) attn_kernel(const __grid_consta
             }
           }
           const float mu = S.m == -INFINITY ? 0.f : S.m;
-          const uint64_t mu2 = pack_f2(-mu, -mu);
+          const uint64_t mu2 = pack_f2(base2 - mu, base2 - mu);
           uint64_t sa = 0, sb = 0;
           uint32_t pk[16];
 #pragma unroll
@@ -928,7 +973,6 @@ __global__ void __launch_bounds__(AT_THREADS, 1) attn_kernel(const __grid_consta
         }
       }
       // ---- the item's rows are done: the sums over the quarters, and the outputs
-      const float off = CAP ? P.cap_log2 : 0.f;   // of the base-2 logits
       const bool join = STREAM && !pair && I.n > 1;   // a single row tile: slot 1 holds the same rows' other key tiles
       const int slots = I.n == 0 ? 0 : pair || join ? 2 : 1;
       auto whole_row = [&](const int slot, Slot &S, uint32_t &oc) {
@@ -963,7 +1007,7 @@ __global__ void __launch_bounds__(AT_THREADS, 1) attn_kernel(const __grid_consta
         const float w0 = ex2(m0 - mu), w1 = ex2(m1 - mu);
         const float lt = l0 * w0 + l1 * w1;
         const float inv = lt == 0.f ? 0.f : rcp_approx(lt);   // an empty row is 0
-        const float lse2 = lt == 0.f ? -INFINITY : mu + off + log2f(lt);
+        const float lse2 = lt == 0.f ? -INFINITY : mu + log2f(lt);
         if (!bad) {
           if (valid && quarter == 0) {
             if (parts)
