@@ -18,15 +18,15 @@ cudaError_t launch_attn_bf16_cap(const AttnArgs &P, int grid, bool bias, cudaStr
 cudaError_t launch_attn_fp16_cap(const AttnArgs &P, int grid, bool bias, cudaStream_t s);
 
 // First and past-the-last position of every position's run of equal ids.  One CTA per sequence; thread i
-// takes the i-th of 1024 consecutive pieces, finds the first and last run start in it, and two block
-// scans carry the last start before and the first start after each piece.
+// takes the i-th of 1024 consecutive pieces, finds the first and last run start in it, and scans over the warp and then
+// over the warps carry the last start before and the first start after each piece.
 constexpr int RUN_THREADS = 1024;
 __global__ void __launch_bounds__(RUN_THREADS) doc_runs_kernel(const int *ids, int s_kv, int2 *runs) {
-  __shared__ int last[RUN_THREADS], first[RUN_THREADS];
+  __shared__ int w_last[32], w_first[32];
   const int *id = ids + (size_t)blockIdx.x * s_kv;
   int2 *out = runs + (size_t)blockIdx.x * s_kv;
-  const int piece = (s_kv + RUN_THREADS - 1) / RUN_THREADS, t = threadIdx.x;
-  const int lo = min(s_kv, t * piece), hi = min(s_kv, lo + piece);
+  const int piece = (s_kv + RUN_THREADS - 1) / RUN_THREADS, t = threadIdx.x, lane = t & 31, warp = t >> 5;
+  const int lo = min((int64_t)s_kv, (int64_t)t * piece), hi = min(s_kv, lo + piece);
   auto starts = [&](int p) { return p == 0 || id[p] != id[p - 1]; };
   int f = s_kv, l = -1;
   for (int p = lo; p < hi; ++p)
@@ -34,24 +34,39 @@ __global__ void __launch_bounds__(RUN_THREADS) doc_runs_kernel(const int *ids, i
       if (f == s_kv) f = p;
       l = p;
     }
-  last[t] = l;
-  first[t] = f;
+  auto scan = [&](int &a, int &b) {   // inclusive over the lanes: maximum from the left, minimum from the right
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int x = __shfl_up_sync(0xffffffffu, a, o), y = __shfl_down_sync(0xffffffffu, b, o);
+      if (lane >= o) a = max(a, x);
+      if (lane + o < 32) b = min(b, y);
+    }
+  };
+  int wl = l, wf = f;
+  scan(wl, wf);
+  if (lane == 31) w_last[warp] = wl;
+  if (lane == 0) w_first[warp] = wf;
   __syncthreads();
-  for (int o = 1; o < RUN_THREADS; o <<= 1) {   // inclusive scans: max from the left, min from the right
-    const int a = t >= o ? last[t - o] : -1, b = t + o < RUN_THREADS ? first[t + o] : s_kv;
-    __syncthreads();
-    last[t] = max(last[t], a);
-    first[t] = min(first[t], b);
-    __syncthreads();
+  if (warp == 0) {
+    int a = w_last[lane], b = w_first[lane];
+    scan(a, b);
+    w_last[lane] = a;
+    w_first[lane] = b;
   }
-  int begin = t ? last[t - 1] : 0;
-  int end = 0;   // past the current run, found when a run starts
+  __syncthreads();
+  // last start before this thread's piece, first start behind it
+  int before = __shfl_up_sync(0xffffffffu, wl, 1), after = __shfl_down_sync(0xffffffffu, wf, 1);
+  if (lane == 0) before = -1;
+  if (lane == 31) after = s_kv;
+  if (warp > 0) before = max(before, w_last[warp - 1]);
+  if (warp < 31) after = min(after, w_first[warp + 1]);
+  int begin = max(before, 0), end = 0;   // of the run at hand
   for (int p = lo; p < hi; ++p) {
     if (p == lo || starts(p)) {
       if (starts(p)) begin = p;
       end = p + 1;
       while (end < hi && !starts(end)) ++end;
-      if (end == hi) end = t + 1 < RUN_THREADS ? first[t + 1] : s_kv;
+      if (end == hi) end = after;
     }
     out[p] = make_int2(begin, end);
   }

@@ -287,6 +287,11 @@ __device__ __forceinline__ void st_global_v8(void *p, const uint32_t *r) {   // 
                "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
                : "memory");
 }
+__device__ __forceinline__ float lg2_approx(float x) {   // absolute error 2^-22 around 1, relative 2^-22 elsewhere
+  float y;
+  asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
 __device__ __forceinline__ float min_nan(float x, float y) {   // NaN if one is
   float d;
   asm("min.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(x), "f"(y));
@@ -1004,10 +1009,10 @@ __global__ void __launch_bounds__(AT_THREADS, 1) attn_kernel(const __grid_consta
         const bool valid = attn_row<STREAM>(P, I, slot, R, b, i, h, prow);
         if (!any_row) continue;
         const float mm = fmaxf(m0, m1), mu = mm == -INFINITY ? 0.f : mm;
-        const float w0 = ex2(m0 - mu), w1 = ex2(m1 - mu);
-        const float lt = l0 * w0 + l1 * w1;
+        const float w0 = join ? ex2(m0 - mu) : 1.f, w1 = join ? ex2(m1 - mu) : 0.f;
+        const float lt = join ? l0 * w0 + l1 * w1 : l0;
         const float inv = lt == 0.f ? 0.f : rcp_approx(lt);   // an empty row is 0
-        const float lse2 = lt == 0.f ? -INFINITY : mu + log2f(lt);
+        const float lse2 = lt == 0.f ? -INFINITY : mu + lg2_approx(lt);
         if (!bad) {
           if (valid && quarter == 0) {
             if (parts)
