@@ -92,6 +92,29 @@ def test_ragged_lengths_and_rows_behind_them(lib, sq):
     assert torch.all(out[3, :ql[3]] == 0) and torch.all(lse[3, :ql[3]] == -math.inf)
 
 
+def test_many_sequences_of_all_lengths(lib):
+    """More sequences than a warp has lanes, empty and short ones between long ones, so that shares of the key tiles begin and
+    end anywhere; and more units of work than SMs."""
+    g = torch.Generator().manual_seed(5)
+    B, skv = 70, 1500
+    kv = [int(x) for x in torch.randint(0, skv + 1, (B,), generator=g)]
+    kv[0], kv[33], kv[34], kv[69] = 0, 0, 1, skv
+    q, k, v = rnd(B, 1, 8, 128), rnd(B, skv, 2, 128, seed=2), rnd(B, skv, 2, 128, seed=3)
+    plan = binding.Attention(B, 1, skv, 8, 2)
+    out, lse = plan.run(q, k, v, kv_len=i32(kv))
+    plan.check()
+    R.compare(out, lse, R.attention(q, k, v, kv_len=kv))
+    assert torch.all(out[0] == 0) and torch.all(lse[33] == -math.inf)
+    run_case(40, 70, 200, 16, 8, FP)          # 320 units of one pair of row tiles each
+
+
+@pytest.mark.parametrize("sq,skv", [(200, 9000), (33, 20000), (300, 40000)])
+def test_last_chunk_of_a_long_context(lib, sq, skv):
+    """Few rows against many keys: pairs of row tiles, and an odd last one, cut into parts."""
+    run_case(1, sq, skv, 8, 2, BF)
+    run_case(2, sq, skv, 4, 4, FP, kv_len=i32([skv - 77, sq]), cap=15.0)
+
+
 def test_more_queries_than_keys(lib):
     """Causal queries before position 0 see nothing."""
     B, sq, skv = 2, 70, 90
@@ -160,6 +183,30 @@ def test_masked_places_may_hold_anything(lib, dtype, bad):
     R.compare(out, lse, R.attention(q[:, :1], k, v, kv_len=[250, 150]), "single tokens")
     plan.check()
     one.check()
+
+
+def test_a_later_nan_in_a_long_prompt(lib):
+    """The rows that share a tile with a later value that is not finite are worked out again over all their keys."""
+    s, at = 8192, 7000
+    q, k, v = rnd(1, s, 4, 128), rnd(1, s, 2, 128, seed=2), rnd(1, s, 2, 128, seed=3)
+    clean = binding.Attention(1, s, s, 4, 2)
+    want, want_lse = clean.run(q, k, v)
+    v[0, at, 1, 17] = math.nan
+    plan = binding.Attention(1, s, s, 4, 2)
+    out, lse = plan.run(q, k, v)
+    plan.check()
+    assert torch.equal(out[:, :, :2], want[:, :, :2])            # the other KV head
+    assert torch.isnan(out[0, at:, 2:, 17]).all()
+    keep = [c for c in range(128) if c != 17]
+    rows = torch.arange(at - 130, at + 130, device="cuda")
+    for h in (2, 3):
+        ok = R.visible(rows, s)
+        vv = v[0, :, 1].clone()
+        vv[at, 17] = 0
+        o, ls, eo, el = R.attention_rows(q[0, rows, h], k[0, :, 1], vv, ok, rows, torch.arange(s, device="cuda"), 1 / math.sqrt(128))
+        assert torch.all((out[0, rows, h].double() - o).abs()[:, keep] <= eo[:, keep])
+        assert torch.all((out[0, rows, h].double() - o).abs()[:130] <= eo[:130])
+        assert torch.all((lse[0, rows, h].double() - ls).abs() <= el)
 
 
 @pytest.mark.parametrize("slopes", [False, True])
@@ -266,6 +313,31 @@ def test_lengths_out_of_range_are_clamped_and_reported(lib):
     assert e.value.status == binding.EDEVICE
     plan.check()                                  # reported once
     R.compare(out, lse, R.attention(q, k, v, kv_len=[100, 0]))
+
+
+def test_a_stream_given_by_the_caller(lib):
+    """Inputs made on the current stream, the call on another that waits for it, new outputs read after a wait back."""
+    side = torch.cuda.Stream()
+    q, k, v = rnd(2, 40, 8, 128), rnd(2, 3000, 2, 128, seed=2), rnd(2, 3000, 2, 128, seed=3)
+    plan = binding.Attention(2, 40, 3000, 8, 2)
+    side.wait_stream(torch.cuda.current_stream())
+    out, lse = plan.run(q, k, v, stream=side)
+    torch.cuda.current_stream().wait_stream(side)
+    R.compare(out, lse, R.attention(q, k, v))
+    plan.check(stream=side)
+
+
+def test_plans_of_one_workspace_size_do_not_share(lib):
+    """Calls of different shapes in turn on one stream, each plan with its own workspace, results unchanged."""
+    plans = []
+    for sq, skv in ((1, 5000), (600, 600), (1, 700), (100, 9000)):
+        q, k, v = rnd(2, sq, 8, 128), rnd(2, skv, 2, 128, seed=2), rnd(2, skv, 2, 128, seed=3)
+        plan = binding.Attention(2, sq, skv, 8, 2)
+        plans.append((plan, q, k, v, plan.run(q, k, v)))
+    again = [p.run(q, k, v) for p, q, k, v, _ in plans for _ in range(2)]
+    for n, (p, q, k, v, first) in enumerate(plans):
+        for a in again[2 * n:2 * n + 2]:
+            assert torch.equal(a[0], first[0]) and torch.equal(a[1], first[1])
 
 
 def test_graph_replay_and_another_stream(lib):
