@@ -410,7 +410,7 @@ def _tensor(t, where, name, shape, dtype, device, dense=False):
 def _enter(device_index, stream, tensors):
     """The raw stream of a call on a device, and the device to make current for it (None: it is).  Tensors used on
     another stream than the device's current one are made known to the allocator."""
-    import torch
+    torch = _torch()
     other = None if torch.cuda.current_device() == device_index else torch.device("cuda", device_index)
     if stream is None:
         return torch._C._cuda_getCurrentRawStream(device_index), other
@@ -423,19 +423,25 @@ def _enter(device_index, stream, tensors):
 
 def _call(name, other, args):
     """One C call, with the call's device current."""
+    fn = getattr(_lib or load(), name)
     if other is None:
-        st = getattr(load(), name)(*args)
+        st = fn(*args)
     else:
-        import torch
-        with torch.cuda.device(other):
-            st = getattr(load(), name)(*args)
+        with _torch().cuda.device(other):
+            st = fn(*args)
     if st != OK:
         _check(st, name)
 
 
+_torch_module = None
+
+
 def _torch():
-    import torch
-    return torch
+    global _torch_module
+    if _torch_module is None:
+        import torch
+        _torch_module = torch
+    return _torch_module
 
 
 def _array(where, name, t, shape, dtype, index):
@@ -448,8 +454,8 @@ def _array(where, name, t, shape, dtype, index):
 
 
 def _fits(t, shape, dtype, index):
-    """Fast form of _tensor's checks for the common case: true when they all hold."""
-    return t.dtype is dtype and t.get_device() == index and t.shape == shape and t.stride(-1) == 1
+    """Fast form of _tensor's checks but for the strides (a descriptor made for them has passed): true when all hold."""
+    return t.shape == shape and t.dtype is dtype and t.get_device() == index
 
 
 def _ops_status(word, where, stream):
@@ -515,17 +521,17 @@ class Rope:
             _need(k_out is None, "Rope.apply", "k_out without k")
         if q_out is None or (k_out is None and k is not None):
             q_out, k_out = self._outputs(q, k, q_out, k_out, stream)
-        key = (q.dtype, q.shape, q.stride(), q_out.stride(), interleaved, inverse, factor, pos0) if k is None else \
-            (q.dtype, q.shape, q.stride(), q_out.stride(), interleaved, inverse, factor, pos0, k.shape, k.stride(),
-             k_out.stride())
+        dt, shape = q.dtype, q.shape
+        key = (dt, shape, q.stride(), q_out.stride(), interleaved, inverse, factor, pos0)
+        if k is not None:
+            key += (k.shape, k.stride(), k_out.stride())
         desc = self._descs.get(key)
         if desc is None:
             desc = self._desc(key, q, k, q_out, k_out, interleaved, inverse, factor, pos0)
-        dt, shape = q.dtype, q.shape
         if not (q.get_device() == index and _fits(q_out, shape, dt, index)):
             _tensor(q, "Rope.apply", "q", shape, dt, self.table.device)
             _tensor(q_out, "Rope.apply", "q_out", shape, dt, self.table.device)
-        if k is not None and not (_fits(k, k.shape, dt, index) and _fits(k_out, k.shape, dt, index)):
+        if k is not None and not (k.dtype is dt and k.get_device() == index and _fits(k_out, k.shape, dt, index)):
             _tensor(k, "Rope.apply", "k", k.shape, dt, self.table.device)
             _tensor(k_out, "Rope.apply", "k_out", k.shape, dt, self.table.device)
         if positions is not None:
@@ -615,6 +621,7 @@ class _AttnPlan:
         key = (q.stride(), k.stride(), v.stride(), out.stride()) + strides
         desc = self._descs.get(key)
         if desc is None:
+            _need(all(st[-1] == 1 for st in key), where, "the channels of every tensor must be contiguous")
             if len(self._descs) > 64:
                 self._descs.clear()
             desc = self._descs[key] = ctypes.byref(self._with_strides(key))

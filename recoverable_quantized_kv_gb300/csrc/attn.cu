@@ -78,9 +78,9 @@ __global__ void __launch_bounds__(RUN_THREADS) doc_runs_kernel(const int *ids, i
 template <bool FP16, int WARPS>
 __global__ void __launch_bounds__(128) attn_combine_kernel(const __grid_constant__ AttnArgs P, int ctas) {
   const int lane = threadIdx.x & 31, warp = WARPS == 1 ? 0 : threadIdx.x >> 5;
-  const int64_t row = WARPS == 1 ? (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5) : blockIdx.x;
-  const int64_t x = row / P.h_q;
-  const int h = (int)(row - x * P.h_q), b = (int)(x / P.s_q), i = (int)(x - (int64_t)b * P.s_q);
+  const uint32_t row = WARPS == 1 ? blockIdx.x * 4 + (threadIdx.x >> 5) : blockIdx.x;   // fewer than 2^31
+  const uint32_t x = row / (uint32_t)P.h_q;
+  const int h = (int)(row - x * P.h_q), b = (int)(x / (uint32_t)P.s_q), i = (int)(x - (uint32_t)b * P.s_q);
   if (b >= P.batch) return;
   const int g = h / P.G, hr = h - g * P.G, pr = i / (2 * P.tpt), gi = pr * P.batch + b;
   const AttnGroup A = attn_group(P, gi);
@@ -255,7 +255,7 @@ qevict_status attn_plan(const qevict_attn_desc *d, int s_prefix, AttnPlan *p) {
   // as a stream, 13 and 17 as units; the last 256 tokens of 32K 114 us as a stream.
   p->stream = s_prefix || (tiles > MIN_TILES && (n_qt == 1 ? tiles > WHOLE_TILES || 2 * units < sms
                                                            : tiles * (sms - std::min(units, sms)) >= 16 * sms));
-  if ((total > (1 << 30) || p->rows > (1ll << 32)) && p->stream) {
+  if ((total > (1 << 30) || p->rows > (1ll << 30)) && p->stream) {
     if (s_prefix) return QEVICT_EINVAL;
     p->stream = 0;
   }
