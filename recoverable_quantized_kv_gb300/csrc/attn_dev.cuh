@@ -340,6 +340,35 @@ __device__ __forceinline__ float2 unpack2(uint32_t v) {
   return make_float2(bf16_lo(v), bf16_hi(v));
 }
 
+// 64 bytes of every lane's row (at element `at` of out; rows: the lanes that have one).  Four lanes turn their four rows
+// around, 16 bytes at a time, so that each store of the warp writes 64 bytes of eight rows; rows stored by their own lanes
+// touch 32 lines an instruction.
+__device__ __forceinline__ void attn_store_rows(uint16_t *out, int64_t at, uint32_t rows, int lane, uint4 (&u)[4]) {
+#pragma unroll
+  for (int d = 2; d; d >>= 1) {
+    const bool up = lane & d;
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      if (c & d) continue;
+      uint4 send = up ? u[c] : u[c | d];
+      send.x = __shfl_xor_sync(0xffffffffu, send.x, d);
+      send.y = __shfl_xor_sync(0xffffffffu, send.y, d);
+      send.z = __shfl_xor_sync(0xffffffffu, send.z, d);
+      send.w = __shfl_xor_sync(0xffffffffu, send.w, d);
+      if (up)
+        u[c] = send;
+      else
+        u[c | d] = send;
+    }
+  }
+#pragma unroll
+  for (int c = 0; c < 4; ++c) {
+    const int r = (lane & 28) + c;
+    const int64_t to_row = __shfl_sync(0xffffffffu, at, r);
+    if (rows >> r & 1) *reinterpret_cast<uint4 *>(out + to_row + 8 * (lane & 3)) = u[c];
+  }
+}
+
 // ----------------------------------------------------------------------------- rows with values that are not finite
 
 // The keys of tile t that not every row of the item sees: their values that are not finite become 0 in shared memory,
@@ -373,7 +402,7 @@ __device__ __forceinline__ void attn_clean_values(const AttnItem &I, int t, uint
 // turn and no masked value touched.  Reached when a value that some row of the item sees and another does not is an infinity or
 // NaN: the tensor-core product then ran with that value as 0.  Writes O (unnormalised), m, l of row r
 // through `emit`, the warp's lanes holding four channels each.
-template <bool FP16, typename Emit>
+template <bool FP16, bool STREAM, typename Emit>
 __device__ __forceinline__ void attn_exact_rows(const AttnArgs &P, const AttnItem &I, int slot, int warp, int lane, bool cap,
                                                 const Emit &emit) {
   const uint16_t *kb, *vb;
@@ -389,7 +418,7 @@ __device__ __forceinline__ void attn_exact_rows(const AttnArgs &P, const AttnIte
   }
   for (int rr = 0; rr < 32; ++rr) {
     int b, i, h, prow;
-    if (!attn_row<true>(P, I, slot, attn_row_of(P, warp * 32 + rr), b, i, h, prow)) continue;
+    if (!attn_row<STREAM>(P, I, slot, attn_row_of(P, warp * 32 + rr), b, i, h, prow)) continue;
     const uint16_t *q = static_cast<const uint16_t *>(P.q) + b * P.sq[0] + i * P.sq[1] + h * P.sq[2];
     int p, lo, hi;
     if (I.prefix()) {
@@ -977,6 +1006,71 @@ __global__ void __launch_bounds__(AT_THREADS, 1) attn_kernel(const __grid_consta
         }
       }
       // ---- the item's rows are done: the sums over the quarters, and the outputs
+      if (!STREAM) {
+        // Whole units: two quarters of the warps finish each slot, half of its columns a thread, so that what a row costs is
+        // paid once.  The sums change hands while the last products run.
+        const int slot = quarter >> 1, side = quarter & 1;
+        float l = 0.f;
+        bool bad = false;
+        if (I.n > 0) {
+          auto row_sum = [&](float x) {
+            asm volatile("bar.sync %0, 128;" ::"r"(row_bar) : "memory");   // what stood in xch has been read
+            *x_own = x;
+            asm volatile("bar.sync %0, 128;" ::"r"(row_bar) : "memory");
+            return (xch[row] + xch[AT_TILE + row]) + (xch[2 * AT_TILE + row] + xch[3 * AT_TILE + row]);
+          };
+          const float l0 = row_sum(S0.l), l1 = row_sum(S1.l);
+          l = slot ? l1 : l0;
+          if (ok) ok = attn_wait(&ofull[slot], oc0 & 1, status);
+          ++oc0;
+          __syncwarp();
+          tc_fence_after();
+          bad = bad_item[seq & 1] == (int)seq;
+        }
+        const uint32_t to = tmem + ((uint32_t)(wq * 32) << 16) + 256 + 128 * slot + 64 * side;
+        const bool any_row = slot ? S1.any : S0.any;
+        int b, i, h, prow;
+        const bool valid = attn_row<false>(P, I, slot, R, b, i, h, prow);
+        if (any_row && !bad) {
+          const float inv = l == 0.f ? 0.f : rcp_approx(l);   // an empty row is 0
+          if (valid && side == 0 && P.lse)
+            P.lse[((int64_t)b * P.s_q + i) * P.h_q + h] =
+                l == 0.f ? -INFINITY : ((slot ? S1.m : S0.m) + lg2_approx(l)) * 0.69314718055994531f;
+          const int64_t at = b * P.so[0] + i * P.so[1] + h * P.so[2] + 64 * side;
+          const uint32_t rows = __ballot_sync(0xffffffffu, valid);
+#pragma unroll 1
+          for (int part = 0; part < 2; ++part) {
+            uint32_t o[32];
+            const float *of = reinterpret_cast<const float *>(o);
+            if (I.n > 0) {
+              tmem_ld32(to + 32 * part, o);
+              tmem_wait_ld();
+            } else {
+#pragma unroll
+              for (int c = 0; c < 32; ++c) o[c] = 0;
+            }
+            uint4 u[4];
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+              u[c] = make_uint4(pack2<FP16>(of[8 * c] * inv, of[8 * c + 1] * inv), pack2<FP16>(of[8 * c + 2] * inv, of[8 * c + 3] * inv),
+                                pack2<FP16>(of[8 * c + 4] * inv, of[8 * c + 5] * inv),
+                                pack2<FP16>(of[8 * c + 6] * inv, of[8 * c + 7] * inv));
+            attn_store_rows(static_cast<uint16_t *>(P.out) + 32 * part, at, rows, lane, u);
+            __syncwarp();
+          }
+        } else if (any_row && side == 0) {
+          attn_exact_rows<FP16, false>(P, I, slot, wq, lane, CAP,
+                                       [&](int rb, int ri, int rh, int, const float (&acc)[4], float rm, float rl) {
+            const float f = rl == 0.f ? 0.f : 1.f / rl;
+            if (lane == 0 && P.lse)
+              P.lse[((int64_t)rb * P.s_q + ri) * P.h_q + rh] = rl == 0.f ? -INFINITY : (rm + log2f(rl)) * 0.69314718055994531f;
+            *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(P.out) + rb * P.so[0] + ri * P.so[1] + rh * P.so[2] + 4 * lane) =
+                rl == 0.f ? make_uint2(0, 0) : make_uint2(pack2<FP16>(acc[0] * f, acc[1] * f), pack2<FP16>(acc[2] * f, acc[3] * f));
+          });
+        }
+        base += 2 * I.n;
+        continue;
+      }
       const bool join = STREAM && !pair && I.n > 1;   // a single row tile: slot 1 holds the same rows' other key tiles
       const int slots = I.n == 0 ? 0 : pair || join ? 2 : 1;
       auto whole_row = [&](const int slot, Slot &S, uint32_t &oc) {
@@ -988,7 +1082,7 @@ __global__ void __launch_bounds__(AT_THREADS, 1) attn_kernel(const __grid_consta
         asm volatile("bar.sync %0, 128;" ::"r"(row_bar) : "memory");
       };
       if (slots > 0) whole_row(0, S0, oc0);
-      if (STREAM && slots > 1) whole_row(1, S1, oc1);
+      if (slots > 1) whole_row(1, S1, oc1);
       __syncwarp();
       tc_fence_after();
       const bool bad = I.n > 0 && bad_item[seq & 1] == (int)seq;
@@ -996,11 +1090,6 @@ __global__ void __launch_bounds__(AT_THREADS, 1) attn_kernel(const __grid_consta
       const int64_t part_row = (int64_t)I.part * (prefix ? P.pre_rows : P.part_rows);
 #pragma unroll 1
       for (int slot = 0; slot < (pair ? 2 : 1); ++slot) {
-        if (!STREAM && slot && I.n > 0) {   // whole units finish slot 0 while slot 1's last product runs
-          whole_row(1, S1, oc1);
-          __syncwarp();
-          tc_fence_after();
-        }
         const float m0 = slot ? S1.m : S0.m, l0 = slot ? S1.l : S0.l, m1 = join ? S1.m : -INFINITY, l1 = join ? S1.l : 0.f;
         const bool any_row = slot ? S1.any : S0.any;
         const uint32_t to = lane_base + 256 + 128 * slot;
@@ -1056,8 +1145,6 @@ __global__ void __launch_bounds__(AT_THREADS, 1) attn_kernel(const __grid_consta
               }
             }
           } else {
-            // Four lanes turn their four rows of 64 bytes around, 16 bytes at a time, so that each store of a warp writes 64
-            // bytes of eight rows.  Rows stored by their own lanes touch 32 lines an instruction.
             uint4 u[4];
 #pragma unroll
             for (int q = 0; q < 2; ++q) {
@@ -1069,35 +1156,11 @@ __global__ void __launch_bounds__(AT_THREADS, 1) attn_kernel(const __grid_consta
                 u[2 * q + c] = make_uint4(pack2<FP16>(of[8 * c], of[8 * c + 1]), pack2<FP16>(of[8 * c + 2], of[8 * c + 3]),
                                           pack2<FP16>(of[8 * c + 4], of[8 * c + 5]), pack2<FP16>(of[8 * c + 6], of[8 * c + 7]));
             }
-#pragma unroll
-            for (int d = 2; d; d >>= 1) {
-              const bool up = lane & d;
-#pragma unroll
-              for (int c = 0; c < 4; ++c) {
-                if (c & d) continue;
-                uint4 send = up ? u[c] : u[c | d];
-                send.x = __shfl_xor_sync(0xffffffffu, send.x, d);
-                send.y = __shfl_xor_sync(0xffffffffu, send.y, d);
-                send.z = __shfl_xor_sync(0xffffffffu, send.z, d);
-                send.w = __shfl_xor_sync(0xffffffffu, send.w, d);
-                if (up)
-                  u[c] = send;
-                else
-                  u[c | d] = send;
-              }
-            }
-            const int64_t at = b * P.so[0] + i * P.so[1] + h * P.so[2] + AT_COLS * quarter;
-            const uint32_t rows = __ballot_sync(0xffffffffu, valid);
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-              const int r = (lane & 28) + c;
-              const int64_t o = __shfl_sync(0xffffffffu, at, r);
-              if (rows >> r & 1)
-                *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(P.out) + o + 8 * (lane & 3)) = u[c];
-            }
+            attn_store_rows(static_cast<uint16_t *>(P.out), b * P.so[0] + i * P.so[1] + h * P.so[2] + AT_COLS * quarter,
+                            __ballot_sync(0xffffffffu, valid), lane, u);
           }
         } else if (quarter == 0) {
-          attn_exact_rows<FP16>(P, I, slot, wq, lane, CAP,
+          attn_exact_rows<FP16, true>(P, I, slot, wq, lane, CAP,
                                 [&](int rb, int ri, int rh, int rp, const float (&acc)[4], float rm, float rl) {
             const float ri_l = rl == 0.f ? 0.f : 1.f / rl;
             const float ls = rl == 0.f ? -INFINITY : rm + log2f(rl);
