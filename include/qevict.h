@@ -428,7 +428,7 @@ typedef struct {
 } qevict_rope_desc;
 /* d_table: fp32 [table_rows][rot_dim / 2][2], 16-byte aligned.  d_positions: int32 [batch][seq], or NULL
  * for pos0 + t.  A tensor may be rotated in place (same pointer and strides); any other overlap of a
- * tensor's input and output is QEVICT_EINVAL, as are positions past the table when d_positions is NULL.  A token whose
+ * tensor's input and output is QEVICT_EINVAL (queries and keys may lie between one another, as in a fused projection), as are positions past the table when d_positions is NULL.  A token whose
  * d_positions entry lies outside [0, table_rows) is not written and sets bit 8 of *d_status, a device
  * word that the caller clears. */
 qevict_status qevict_rope_apply(const qevict_rope_desc *desc, const float *d_table, const int32_t *d_positions,
@@ -446,7 +446,7 @@ qevict_status qevict_rope_apply(const qevict_rope_desc *desc, const float *d_tab
  * invisible keys and values (infinities, NaN) does not reach a row; visible ones propagate.  Rows behind
  * q_len[b] are not written.  Softmax statistics and sums are fp32; the probabilities are rounded to the
  * input type for the product with the values, and the output once.
- * Results do not change from run to run. */
+ * Results do not change from run to run.  out and lse may share no bytes with the inputs. */
 typedef struct {
   int32_t dtype;                           /* QEVICT_BF16 or QEVICT_FP16, of q, k, v and out */
   int32_t batch, s_q, s_kv, h_q, h_kv;     /* s_kv: keys the cache has room for; h_q / h_kv whole, at most 128 */

@@ -90,14 +90,14 @@ __global__ void __launch_bounds__(128) attn_combine_kernel(const __grid_constant
 #pragma unroll 2
   for (int j = lane; j < P.n_pr * P.batch; j += 32) {
     const AttnGroup B = attn_group(P, j);
-    const int w = attn_places(B.t_hi - B.t_lo);
+    const int w = attn_places(B.tiles);
     all += w;
     if (j < gi) before += w;
   }
   all = __reduce_add_sync(0xffffffffu, all);
   before = __reduce_add_sync(0xffffffffu, before);
   const int share = attn_share(all_p + all * P.h_kv, ctas, P.min_tiles);
-  const int t = A.t_hi - A.t_lo, u0 = all_p + before * P.h_kv + g * attn_places(t);
+  const int t = A.tiles, u0 = all_p + before * P.h_kv + g * attn_places(t);
   // own parts: the CTAs whose shares hold tiles u0 .. u0 + t - 1
   const int c_own = u0 / share, n_own = t ? (u0 + t - 1) / share - c_own + 1 : 0;
   if (!P.pre && n_own == 1) return;   // the unit was not cut: the row is written

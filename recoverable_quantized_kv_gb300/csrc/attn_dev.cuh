@@ -63,7 +63,7 @@ struct AttnGroup {
   int kl, ql, pfx;             // keys, queries, prefix mask of the sequence
   int clean_lo, clean_hi;      // keys that every row sees
   int key_lo, key_hi;          // keys that some row sees
-  int t_lo, t_hi;              // key tiles
+  int tiles;                   // key tiles from key_lo on
 };
 
 // Visible keys [x, y) of position p.  Both ends grow with p.
@@ -87,7 +87,7 @@ __device__ __forceinline__ AttnGroup attn_group(const AttnArgs &P, int gi) {
   A.ql = P.q_len ? clampi(P.q_len[A.b], 0, P.s_q) : P.s_q;
   A.pfx = P.prefix_len ? clampi(P.prefix_len[A.b], 0, A.kl) : 0;
   const int i0 = A.tile0 * P.tpt, i1 = min(A.ql, i0 + 2 * P.tpt);
-  A.clean_lo = A.clean_hi = A.key_lo = A.key_hi = A.t_lo = A.t_hi = 0;
+  A.clean_lo = A.clean_hi = A.key_lo = A.key_hi = A.tiles = 0;
   if (i0 < i1) {
     const int p0 = A.kl - A.ql + i0;
     const int2 a = attn_interval(P, A.b, p0, A.kl, A.pfx), z = attn_interval(P, A.b, p0 + (i1 - 1 - i0), A.kl, A.pfx);
@@ -95,10 +95,7 @@ __device__ __forceinline__ AttnGroup attn_group(const AttnArgs &P, int gi) {
     A.key_hi = z.y;
     A.clean_lo = z.x;
     A.clean_hi = a.y;
-    if (A.key_hi > A.key_lo) {
-      A.t_lo = A.key_lo / AT_TILE;
-      A.t_hi = (A.key_hi + AT_TILE - 1) / AT_TILE;
-    }
+    A.tiles = (A.key_hi - A.key_lo + AT_TILE - 1) / AT_TILE;   // (a document's units share its tiles)
   }
   return A;
 }
@@ -117,8 +114,9 @@ __device__ __forceinline__ int attn_share(int total, int ctas, int min_tiles) {
 struct AttnItem {
   int kind;                    // bit 0 prefix, bit 1 pair, bit 2 written as a part; -1: no more items
   int b, g, tile0, kl, ql, pfx;
-  int n, t_hi;                 // key tiles t_hi - 1, t_hi - 2, ... (n of them)
-  int clean_lo, clean_hi, key_lo, key_hi;
+  int n, t_hi;                 // key tiles t_hi - 1, t_hi - 2, ... (n of them), tile t from key k0 + 128 t on
+  int k0;
+  int clean_lo, clean_hi, key_hi;   // counted from k0
   int part;
   int pad[2];
   __device__ __forceinline__ bool prefix() const { return kind & 1; }
@@ -387,7 +385,7 @@ __device__ __forceinline__ void attn_clean_values(const AttnItem &I, int t, uint
     hit |= ((~x.x & E2) - 0x00010001u) | ((~x.y & E2) - 0x00010001u) | ((~x.z & E2) - 0x00010001u) | ((~x.w & E2) - 0x00010001u);
   }
   if (hit & 0x80008000u) {
-    if (key >= I.key_lo && key < I.key_hi) *flag = mark;
+    if (key < I.key_hi) *flag = mark;   // key 0 is the first that some row sees
 #pragma unroll 1
     for (int c = 0; c < 16; ++c) {
       const uint32_t w = p[c];
@@ -433,8 +431,8 @@ __device__ __forceinline__ void attn_exact_rows(const AttnArgs &P, const AttnIte
     const float slope = P.slopes ? P.slopes[h] * 1.4426950408889634f : 0.f;
     float m = -INFINITY, l = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};
     for (int j = 0; j < I.n; ++j) {
-      const int t = I.t_hi - 1 - j;
-      for (int c0 = t * AT_TILE; c0 < (t + 1) * AT_TILE; c0 += 32) {
+      const int k0 = I.k0 + (I.t_hi - 1 - j) * AT_TILE;
+      for (int c0 = k0; c0 < k0 + AT_TILE; c0 += 32) {
         if (c0 + 32 <= lo || c0 >= hi) continue;
         const int key = c0 + lane;
         const bool seen = key >= lo && key < hi;
@@ -531,7 +529,7 @@ __global__ void __launch_bounds__(AT_THREADS, 1) attn_kernel(const __grid_consta
     for (int g0 = 0; g0 < groups; g0 += 32) {
       const AttnGroup A = attn_group(P, min(g0 + lane, groups - 1));
       if (g0 == 0) plan_a = A;
-      plan_places += __reduce_add_sync(0xffffffffu, g0 + lane < groups ? attn_places(A.t_hi - A.t_lo) : 0) * P.h_kv;
+      plan_places += __reduce_add_sync(0xffffffffu, g0 + lane < groups ? attn_places(A.tiles) : 0) * P.h_kv;
     }
   }
   tc_fence_before();
@@ -570,9 +568,10 @@ __global__ void __launch_bounds__(AT_THREADS, 1) attn_kernel(const __grid_consta
       AttnItem I;
       I.kind = !STREAM || A.tile0 * P.tpt + P.tpt < A.ql ? 2 : 0;
       I.b = A.b, I.g = g, I.tile0 = A.tile0, I.kl = A.kl, I.ql = A.ql, I.pfx = A.pfx;
-      I.n = A.t_hi - A.t_lo;
-      I.t_hi = A.t_hi;
-      I.clean_lo = A.clean_lo, I.clean_hi = A.clean_hi, I.key_lo = A.key_lo, I.key_hi = A.key_hi;
+      I.n = A.tiles;
+      I.t_hi = A.tiles;
+      I.k0 = A.key_lo;
+      I.clean_lo = A.clean_lo - I.k0, I.clean_hi = A.clean_hi - I.k0, I.key_hi = A.key_hi - I.k0;
       I.part = 0;
       return I;
     };
@@ -605,7 +604,7 @@ __global__ void __launch_bounds__(AT_THREADS, 1) attn_kernel(const __grid_consta
           I.b = 0, I.g = u - pr * P.h_kv, I.kl = P.pre, I.ql = P.s_q, I.pfx = 0;
           I.n = min(tp - o, end - pos);
           I.t_hi = tp - o;
-          I.clean_lo = I.key_lo = 0;
+          I.k0 = I.clean_lo = 0;
           I.clean_hi = I.key_hi = P.pre;
           I.part = blockIdx.x + u;
           put(I);
@@ -616,7 +615,7 @@ __global__ void __launch_bounds__(AT_THREADS, 1) attn_kernel(const __grid_consta
 #pragma unroll 1
       for (int g0 = 0; ok && pos < end && g0 < groups; g0 += 32) {
         const AttnGroup A = g0 == 0 ? plan_a : attn_group(P, min(g0 + lane, groups - 1));
-        const int t = g0 + lane < groups ? A.t_hi - A.t_lo : 0;
+        const int t = g0 + lane < groups ? A.tiles : 0;
         const int here = __reduce_add_sync(0xffffffffu, attn_places(t)) * P.h_kv;
         if (done + here <= pos) {
           done += here;
@@ -635,7 +634,7 @@ __global__ void __launch_bounds__(AT_THREADS, 1) attn_kernel(const __grid_consta
           B.pfx = __shfl_sync(0xffffffffu, A.pfx, q);
           B.clean_lo = __shfl_sync(0xffffffffu, A.clean_lo, q), B.clean_hi = __shfl_sync(0xffffffffu, A.clean_hi, q);
           B.key_lo = __shfl_sync(0xffffffffu, A.key_lo, q), B.key_hi = __shfl_sync(0xffffffffu, A.key_hi, q);
-          B.t_lo = __shfl_sync(0xffffffffu, A.t_lo, q), B.t_hi = __shfl_sync(0xffffffffu, A.t_hi, q);
+          B.tiles = tq;
           while (ok && pos < min(end, done + wq * P.h_kv)) {
             const int g = (pos - done) / wq, u0 = done + g * wq, o = pos - u0;
             if (o < tq) {
@@ -676,8 +675,8 @@ __global__ void __launch_bounds__(AT_THREADS, 1) attn_kernel(const __grid_consta
           const uint32_t dst = smem_u32(sm) + AT_OFF_KV + st * AT_TILE_BYTES;
           const int t = I.t_hi - 1 - j;
           mbar_arrive_expect_tx(&full[st], AT_TILE_BYTES);
-          tma_load_4d_at(dst, map, 0, I.g, t * AT_TILE, bb, &full[st]);
-          tma_load_4d_at(dst + AT_HALF_BYTES, map, 64, I.g, t * AT_TILE, bb, &full[st]);
+          tma_load_4d_at(dst, map, 0, I.g, I.k0 + t * AT_TILE, bb, &full[st]);
+          tma_load_4d_at(dst + AT_HALF_BYTES, map, 64, I.g, I.k0 + t * AT_TILE, bb, &full[st]);
           ++c;
         };
         for (int s = 0; ok && s < (pair ? 2 : 1); ++s) {
@@ -825,8 +824,8 @@ __global__ void __launch_bounds__(AT_THREADS, 1) attn_kernel(const __grid_consta
           } else {
             const int p = I.kl - I.ql + i;
             const int2 v = attn_interval(P, b, p, I.kl, I.pfx);
-            S.lo = v.x, S.hi = v.y;
-            if (BIAS) S.pos = (float)p;
+            S.lo = v.x - I.k0, S.hi = v.y - I.k0;   // counted from k0, as the tiles are
+            if (BIAS) S.pos = (float)(p - I.k0);
           }
           if (BIAS) slope = P.slopes[h] * 1.4426950408889634f;
         }
