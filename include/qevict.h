@@ -468,7 +468,7 @@ typedef struct {
   const int32_t *doc_ids;      /* [batch][s_kv] */
 } qevict_attn_mask;
 /* Bytes of device workspace of a call (a bound for every mask).  The workspace is 256-byte aligned; its first 256 bytes
- * hold the status word and must be cleared once before its first use.  Calls that may overlap on the
+ * hold the status word and a count, and must be cleared once before its first use.  Calls that may overlap on the
  * GPU (two streams, two replayed graphs) need workspaces of their own. */
 qevict_status qevict_attn_bytes(const qevict_attn_desc *desc, size_t *bytes);
 /* q [batch][s_q][h_q][128], k, v [batch][s_kv][h_kv][128], out like q (16-byte aligned); lse fp32

@@ -315,6 +315,7 @@ qevict_status attn_launch(const qevict_attn_desc *d, const AttnPlan &pl, const q
   A.out = out;
   A.lse = lse;
   A.status = reinterpret_cast<int *>(w);
+  A.drawn = A.status + 32;
   A.slopes = m.slopes, A.q_len = m.q_len, A.kv_len = m.kv_len, A.prefix_len = m.prefix_len;
   for (int i = 0; i < 3; ++i) A.sq[i] = d->q[i], A.sk[i] = d->k[i], A.sv[i] = d->v[i], A.so[i] = d->o[i];
   A.batch = d->batch, A.s_q = d->s_q, A.s_kv = d->s_kv, A.h_q = d->h_q, A.h_kv = d->h_kv, A.G = pl.G, A.causal = d->causal;

@@ -23,7 +23,7 @@ constexpr int AT_ITEMS = 4;                           // work items described ah
 constexpr int AT_OFF_KV = 2 * AT_TILE_BYTES;
 constexpr int AT_OFF_X = AT_OFF_KV + AT_STAGES * AT_TILE_BYTES;    // [4 quarters][128] fp32 exchange
 constexpr int AT_OFF_BAR = AT_OFF_X + 4 * AT_TILE * 4;
-constexpr int AT_NBAR = 2 * AT_STAGES + 4 + 6 + 2 * AT_ITEMS;
+constexpr int AT_NBAR = 2 * AT_STAGES + 4 + 6 + 2 * AT_ITEMS + 2;   // (one unused: 16-byte steps)
 constexpr int AT_OFF_MISC = AT_OFF_BAR + AT_NBAR * 8;              // tmem address, flags
 constexpr int AT_OFF_ITEM = AT_OFF_MISC + 16;                     // work item ring
 constexpr int AT_SMEM = AT_OFF_ITEM + AT_ITEMS * 64;
@@ -38,7 +38,7 @@ struct AttnArgs {
   float *lse;
   float *part_o, *part_l;      // own keys: [part][row][128], [part][row] (log2 domain)
   float *pre_o, *pre_l;        // the same of the prefix
-  int *status;
+  int *status, *drawn;         // status word; units given out (whole units)
   const float *slopes;
   const int *q_len, *kv_len, *prefix_len;
   const int2 *runs;            // [batch][s_kv]: first and past-the-last position of every position's document
@@ -493,6 +493,7 @@ __global__ void __launch_bounds__(AT_THREADS, 1) attn_kernel(const __grid_consta
   uint64_t *bars = reinterpret_cast<uint64_t *>(sm + AT_OFF_BAR);
   uint64_t *full = bars, *empty = full + AT_STAGES, *qfull = empty + AT_STAGES, *qempty = qfull + 2;
   uint64_t *sfull = qempty + 2, *pfull = sfull + 2, *ofull = pfull + 2, *ifull = ofull + 2, *iempty = ifull + AT_ITEMS;
+  uint64_t *loaded = iempty + AT_ITEMS;
   uint32_t *misc = reinterpret_cast<uint32_t *>(sm + AT_OFF_MISC);
   uint32_t *tmem_slot = misc;
   volatile int *bad_item = reinterpret_cast<int *>(misc + 2);   // [item parity]: 1 + the item with values to recompute
@@ -512,7 +513,7 @@ __global__ void __launch_bounds__(AT_THREADS, 1) attn_kernel(const __grid_consta
   } else if (threadIdx.x < AT_NBAR) {
     const uint64_t *p = &bars[threadIdx.x];
     const int n = p < pfull ? 1 : p < ofull ? AT_SOFT :
-                  p < ifull ? 2 : p < iempty ? 1 : AT_SOFT + 2;
+                  p < ifull ? 2 : p < iempty ? 1 : p < loaded ? AT_SOFT + 2 : 1;
     mbar_init(&bars[threadIdx.x], n);
     fence_mbar_init();
     if (threadIdx.x < 2) bad_item[threadIdx.x] = 0;
@@ -577,14 +578,23 @@ __global__ void __launch_bounds__(AT_THREADS, 1) attn_kernel(const __grid_consta
     };
     const int groups = P.n_pr * P.batch;
     if (!STREAM) {
-      // whole units, the longest (last rows of causal prompts) first, every second round in reverse so that the CTAs'
-      // sums come out even
+      // Whole units, the longest (last rows of causal prompts) first, each to the CTA that is ready next: lengths and documents
+      // make units differ, and a fixed turn leaves some CTAs twice the mean.  A CTA's first unit is its own number; it draws the next
+      // when its TMA warp has asked for the last one's tiles, two or three tiles before it needs it.  Every CTA draws once past the
+      // end, so the draw that takes the count to the number of units is the last, and starts it again for the next call.
       const int units = groups * P.h_kv;
-      for (int r = 0; r * (int)gridDim.x < units; ++r) {
-        const int u = r * gridDim.x + ((r & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
-        if (u >= units) continue;
+      int u = blockIdx.x;
+      uint32_t drawn = 0;
+      while (u < units) {
         const int x = u / P.h_kv, pr = x / P.batch;
         put(own_item(attn_group(P, (P.n_pr - 1 - pr) * P.batch + (x - pr * P.batch)), u - x * P.h_kv));
+        if (ok) ok = attn_wait_warp(loaded, drawn++ & 1, status);
+        int n = 0;
+        if (lane == 0) {
+          n = atomicAdd(P.drawn, 1);
+          if (n == units - 1) *P.drawn = 0;
+        }
+        u = gridDim.x + __shfl_sync(0xffffffffu, n, 0);
       }
     } else {
       // The key tiles of all units, prefix first, as one stream; CTA c takes tiles [c share, (c + 1) share).  A unit cut by a
@@ -665,8 +675,7 @@ __global__ void __launch_bounds__(AT_THREADS, 1) attn_kernel(const __grid_consta
     bool ok = true;
     AttnItem I;
     while (ok && next_item(I) && I.kind >= 0) {
-      if (I.n == 0) continue;
-      if (lane == 0) {
+      if (I.n > 0 && lane == 0) {
         const bool prefix = STREAM && I.prefix(), pair = !STREAM || I.pair();
         const CUtensorMap *mq = prefix ? &P.tqp : &P.tq, *mk = prefix ? &P.tkp : &P.tk, *mv = prefix ? &P.tvp : &P.tv;
         auto load = [&](const CUtensorMap *map, int j, int bb) {
@@ -699,6 +708,7 @@ __global__ void __launch_bounds__(AT_THREADS, 1) attn_kernel(const __grid_consta
         }
       }
       ok = __shfl_sync(0xffffffffu, (int)ok, 0);
+      if (!STREAM && lane == 0) mbar_arrive(loaded);
     }
     if (lane == 0) {   // copies still in flight land before the CTA leaves
       for (uint32_t i = c > AT_STAGES ? c - AT_STAGES : 0; i < c; ++i)
