@@ -333,8 +333,10 @@ qevict_status attn_launch(const qevict_attn_desc *d, const AttnPlan &pl, const q
     A.cap_s = d->softcap / scale;
     const double q[5] = {0.9999999403953552, -0.33332324028015137, 0.13310357928276062, -0.052109625190496445,
                          0.01548669021576643};
+    const double r[3] = {0.9999995827674866, -0.3332192897796631, 0.12841935455799103};
     const double u = A.cap_u;
     for (int i = 0; i < 5; ++i) A.cap_q[i] = (float)(q[i] * std::pow(u, 2 * i));
+    for (int i = 0; i < 3; ++i) A.cap_r[i] = (float)(r[i] * std::pow(u, 2 * i));
   }
   const bool fp16 = d->dtype == QEVICT_FP16;
   const int qb = A.mul_q ? d->batch : 1, kb = A.mul_k ? d->batch : 1, vb = A.mul_v ? d->batch : 1;

@@ -51,7 +51,7 @@ struct AttnArgs {
   int stream, min_tiles;       // the key tiles of all units as one stream, cut into equal shares of at least min_tiles
   float scale_log2;            // logit scale * log2 e
   float cap_u, cap_s;          // softcap: scale / cap, cap / scale
-  float cap_q[5];              // tanh(u) / u in powers of the product's square, u = product * cap_u
+  float cap_q[5], cap_r[3];    // tanh(u) / u in powers of the product's square, u = product * cap_u: to 0.6, to 0.25
 };
 
 __device__ __forceinline__ int clampi(int x, int lo, int hi) { return x < lo ? lo : x > hi ? hi : x; }
@@ -849,10 +849,11 @@ __global__ void __launch_bounds__(AT_THREADS, 1) attn_kernel(const __grid_consta
       const float scale2 = BIAS ? 1.f : P.scale_log2;
       const uint64_t scale22 = pack_f2(scale2, scale2);
       const int clean_lo = (I.clean_lo + AT_TILE - 1) / AT_TILE, clean_hi = I.clean_hi / AT_TILE;   // tiles that every row sees whole
-      // Capped products: y with y scale = cap tanh(v scale / cap).  Where no |v scale / cap| of the warp's rows exceeds 0.6, the
-      // usual case, tanh(u) = u Q(u^2) with Q of degree 4, fitted at Chebyshev nodes on [0, 0.36] (error 7e-8 of tanh in fp32), its
-      // coefficients scaled to take v: six packed operations for two.  Else 1 - 2 / (1 + 2^(2 log2e u)) with one
-      // reciprocal for two, 1 / a = b / (a b), where 2^60 bounds the exponentials so that the product stays finite.
+      // Capped products: y with y scale = cap tanh(v scale / cap), tanh(u) = u Q(u^2) with Q fitted at Chebyshev nodes, its
+      // coefficients scaled to take v: of degree 2 where no |u| of the warp's rows exceeds 0.25, the usual case, of degree 4 up to
+      // 0.6 (errors 1e-7 and 7e-8 of tanh in fp32).  Beyond, 1 - 2 / (1 + 2^(2 log2e u)) with one reciprocal for two, 1 / a =
+      // b / (a b), where 2^60 bounds the exponentials so that the product stays finite.  A 4K prompt of 32 heads takes 100 us
+      // without a cap, 139 with one, bound by the FMA pipe's share of each step (158 with degree 4, 173 by exponentials).
       auto capped = [&](float *v) {
         float x0 = 0.f, x1 = 0.f;
 #pragma unroll
@@ -860,7 +861,16 @@ __global__ void __launch_bounds__(AT_THREADS, 1) attn_kernel(const __grid_consta
           x0 = max3(x0, fabsf(v[c]), fabsf(v[c + 1]));
           x1 = max3(x1, fabsf(v[c + 2]), fabsf(v[c + 3]));
         }
-        if (__all_sync(0xffffffffu, fmaxf(x0, x1) * P.cap_u <= 0.6f)) {
+        const float most = fmaxf(x0, x1) * P.cap_u;
+        if (__all_sync(0xffffffffu, most <= 0.25f)) {
+          const uint64_t q0 = pack_f2(P.cap_r[0], P.cap_r[0]), q1 = pack_f2(P.cap_r[1], P.cap_r[1]),
+                         q2 = pack_f2(P.cap_r[2], P.cap_r[2]);
+#pragma unroll
+          for (int c = 0; c < AT_COLS; c += 2) {
+            const uint64_t v2 = pack_f2(v[c], v[c + 1]), z = mul_f2(v2, v2);
+            unpack_f2(v[c], v[c + 1], mul_f2(v2, fma_f2(z, fma_f2(z, q2, q1), q0)));
+          }
+        } else if (__all_sync(0xffffffffu, most <= 0.6f)) {
           const uint64_t q0 = pack_f2(P.cap_q[0], P.cap_q[0]), q1 = pack_f2(P.cap_q[1], P.cap_q[1]),
                          q2 = pack_f2(P.cap_q[2], P.cap_q[2]), q3 = pack_f2(P.cap_q[3], P.cap_q[3]),
                          q4 = pack_f2(P.cap_q[4], P.cap_q[4]);

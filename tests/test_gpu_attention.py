@@ -54,6 +54,14 @@ def test_scores_capped_biased_scaled(lib, dtype, cap, slopes, causal, scale, sq,
     run_case(2, sq, skv, 8, 2, dtype, causal=causal, cap=cap, slopes=slopes, scale=scale)
 
 
+@pytest.mark.parametrize("cap", [100.0, 24.0, 14.0, 8.0, 2.0])
+@pytest.mark.parametrize("sq,skv", [(300, 300), (1, 700)])
+def test_caps_from_barely_felt_to_tight(lib, cap, sq, skv):
+    """Logits of deviation 1.5, about 5 at most among the 1024 of a warp's step: the caps put them on either side of 0.25 and 0.6
+    of the cap, or on both within one row."""
+    run_case(1, sq, skv, 4, 2, cap=cap, seed=13)
+
+
 def test_capped_scores_far_beyond_the_cap(lib):
     """Logits of hundreds against a cap of 3: tanh at its ends, both signs."""
     run_case(1, 130, 260, 4, 2, BF, cap=3.0, gain=300.0)
