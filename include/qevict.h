@@ -428,7 +428,9 @@ typedef struct {
 } qevict_rope_desc;
 /* d_table: fp32 [table_rows][rot_dim / 2][2], 16-byte aligned.  d_positions: int32 [batch][seq], or NULL
  * for pos0 + t.  A tensor may be rotated in place (same pointer and strides); any other overlap of a
- * tensor's input and output is QEVICT_EINVAL (queries and keys may lie between one another, as in a fused projection), as are positions past the table when d_positions is NULL.  A token whose
+ * tensor's input and output is QEVICT_EINVAL.  Queries and keys may lie between one another, as in a fused
+ * projection, but an element written for one may not belong to the other (QEVICT_EINVAL where they start
+ * together).  Positions past the table are QEVICT_EINVAL when d_positions is NULL; a token whose
  * d_positions entry lies outside [0, table_rows) is not written and sets bit 8 of *d_status, a device
  * word that the caller clears. */
 qevict_status qevict_rope_apply(const qevict_rope_desc *desc, const float *d_table, const int32_t *d_positions,
@@ -453,7 +455,7 @@ typedef struct {
   int32_t d_head;                          /* 128 */
   int32_t causal;
   float scale;                             /* > 0; 0 = 1 / sqrt(d_head) */
-  float softcap;                           /* >= 0; 0 = none */
+  float softcap;                           /* 0 = none; otherwise 2^-14 to 2^100 times the scale */
   /* strides in elements, {batch, token, head}, channels contiguous: multiples of 8; a batch stride of q, k, v may be
    * 0 (one cache for all); out's may not put two elements in one place */
   int64_t q[3], k[3], v[3], o[3];
@@ -468,8 +470,9 @@ typedef struct {
   const int32_t *doc_ids;      /* [batch][s_kv] */
 } qevict_attn_mask;
 /* Bytes of device workspace of a call (a bound for every mask).  The workspace is 256-byte aligned; its first 256 bytes
- * hold the status word and a count, and must be cleared once before its first use.  Calls that may overlap on the
- * GPU (two streams, two replayed graphs) need workspaces of their own. */
+ * hold the status word and a count, and must be cleared once before its first use, and again after a wait ran
+ * out (bit 1 of the status word).  Calls that may overlap on the GPU (two streams, two replayed graphs) need
+ * workspaces of their own. */
 qevict_status qevict_attn_bytes(const qevict_attn_desc *desc, size_t *bytes);
 /* q [batch][s_q][h_q][128], k, v [batch][s_kv][h_kv][128], out like q (16-byte aligned); lse fp32
  * [batch][s_q][h_q] or NULL. */

@@ -414,6 +414,7 @@ def _enter(device_index, stream, tensors):
     other = None if torch.cuda.current_device() == device_index else torch.device("cuda", device_index)
     if stream is None:
         return torch._C._cuda_getCurrentRawStream(device_index), other
+    _need(stream.device.index == device_index, "stream", f"the stream is on {stream.device}, the tensors on cuda:{device_index}")
     if stream != torch.cuda.current_stream(device_index):
         for t in tensors:
             if t is not None:
@@ -456,6 +457,16 @@ def _array(where, name, t, shape, dtype, index):
 def _fits(t, shape, dtype, index):
     """Fast form of _tensor's checks but for the strides (a descriptor made for them has passed): true when all hold."""
     return t.shape == shape and t.dtype is dtype and t.get_device() == index
+
+
+def _settled(t):
+    """Waits until what the current stream has written to a new tensor is there, so that any stream may use it (in a
+    capture the writes are the graph's)."""
+    torch = _torch()
+    if t.is_cuda:
+        with torch.cuda.device(t.device):
+            if not torch.cuda.is_current_stream_capturing():
+                torch.cuda.current_stream().synchronize()
 
 
 def _ops_status(word, where, stream):
@@ -508,6 +519,7 @@ class Rope:
         self.table = table
         self.index = table.get_device()
         self.status = torch.zeros(1, dtype=torch.int32, device=table.device)
+        _settled(self.status)
         self._table_ptr, self._status_ptr, self._descs = table.data_ptr(), self.status.data_ptr(), {}
 
     def apply(self, q, k=None, positions=None, pos0=0, interleaved=False, inverse=False, factor=1.0, q_out=None,
@@ -596,6 +608,7 @@ class _AttnPlan:
         import torch
         self.work = torch.empty(nbytes, dtype=torch.uint8, device=self.device)
         self.work[:256].zero_()
+        _settled(self.work)
         d = self.desc
         self.index, self._descs = self.work.get_device(), {}
         self._work = (self.work.data_ptr(), nbytes)
@@ -635,7 +648,12 @@ class _AttnPlan:
     def check(self, stream=None):
         """Raises EDEVICE if a call since the last check recorded a fault: a length outside its range (clamped), or
         a wait that ran out (synchronises)."""
-        _ops_status(self.work, type(self).__name__ + ".check", stream)
+        try:
+            _ops_status(self.work, type(self).__name__ + ".check", stream)
+        except QEvictError:
+            self.work[:256].zero_()   # a wait that ran out leaves the count behind it undone
+            _settled(self.work)
+            raise
 
 
 class Attention(_AttnPlan):

@@ -74,17 +74,18 @@ __global__ void __launch_bounds__(RUN_THREADS) doc_runs_kernel(const int *ids, i
 
 // WARPS warps per row (sequence, query, head): out = sum_s 2^(lse_s - L) out_s over the parts of the row's units, L their
 // log2-sum-exp; 512 bytes per part and row, read once, eight loads of a warp at a time.  Which parts a row has is worked out
-// as the attention kernel did, before that kernel is waited for.  Four warps a row where rows are few: latency.
+// as the attention kernel did, before that kernel is waited for.  Four warps a row where rows are few: latency.  A thread
+// without work waits too: what follows in the stream is ordered behind this kernel, and through it behind that one.
 template <bool FP16, int WARPS>
 __global__ void __launch_bounds__(128) attn_combine_kernel(const __grid_constant__ AttnArgs P, int ctas) {
   const int lane = threadIdx.x & 31, warp = WARPS == 1 ? 0 : threadIdx.x >> 5;
   const uint32_t row = WARPS == 1 ? blockIdx.x * 4 + (threadIdx.x >> 5) : blockIdx.x;   // fewer than 2^31
   const uint32_t x = row / (uint32_t)P.h_q;
   const int h = (int)(row - x * P.h_q), b = (int)(x / (uint32_t)P.s_q), i = (int)(x - (uint32_t)b * P.s_q);
-  if (b >= P.batch) return;
+  if (b >= P.batch) return attn_wait_previous();
   const int g = h / P.G, hr = h - g * P.G, pr = i / (2 * P.tpt), gi = pr * P.batch + b;
   const AttnGroup A = attn_group(P, gi);
-  if (i >= A.ql) return;
+  if (i >= A.ql) return attn_wait_previous();
   const int tp = P.pre ? (P.pre + AT_TILE - 1) / AT_TILE : 0, wp = attn_places(tp), all_p = P.pre ? P.n_prp * P.h_kv * wp : 0;
   int all = 0, before = 0;   // places of all groups, and of those before this one
 #pragma unroll 2
@@ -100,7 +101,7 @@ __global__ void __launch_bounds__(128) attn_combine_kernel(const __grid_constant
   const int t = A.tiles, u0 = all_p + before * P.h_kv + g * attn_places(t);
   // own parts: the CTAs whose shares hold tiles u0 .. u0 + t - 1
   const int c_own = u0 / share, n_own = t ? (u0 + t - 1) / share - c_own + 1 : 0;
-  if (!P.pre && n_own == 1) return;   // the unit was not cut: the row is written
+  if (!P.pre && n_own == 1) return attn_wait_previous();   // the unit was not cut: the row is written
   const int64_t own_row = (int64_t)(c_own + gi * P.h_kv + g) * P.part_rows + (int64_t)(i - pr * 2 * P.tpt) * P.G + hr;
   int n_pre = 0;
   int64_t pre_row = 0;
@@ -110,7 +111,7 @@ __global__ void __launch_bounds__(128) attn_combine_kernel(const __grid_constant
     pre_row = (int64_t)(c0 + u) * P.pre_rows + (int64_t)((b - prp * 2 * P.nb) * P.s_q + i) * P.G + hr;
   }
   const int n = n_pre + n_own;
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  attn_wait_previous();
   auto lse_of = [&](int s) {
     return s < n_pre ? P.pre_l[pre_row + (int64_t)s * P.pre_rows] : P.part_l[own_row + (int64_t)(s - n_pre) * P.part_rows];
   };
@@ -217,11 +218,17 @@ bool stride_ok(int64_t st, int64_t size, bool zero) {
   return st % 8 == 0 && st < (1ll << 38) && (st > 0 || (zero && st == 0));
 }
 
+float logit_scale(const qevict_attn_desc *d) { return d->scale > 0.f ? d->scale : 1.f / std::sqrt((float)D); }
+
 qevict_status attn_plan(const qevict_attn_desc *d, int s_prefix, AttnPlan *p) {
   if (!d || d->dtype < 0 || d->dtype > 1 || d->batch < 1 || d->s_q < 1 || d->s_kv < 1 || d->h_kv < 1 || d->h_q < d->h_kv ||
       d->h_q % d->h_kv || d->h_q / d->h_kv > AT_TILE || d->d_head != D || d->causal < 0 || d->causal > 1 ||
       !(d->scale >= 0.f) || !std::isfinite(d->scale) || !(d->softcap >= 0.f) || !std::isfinite(d->softcap))
     return QEVICT_EINVAL;
+  if (d->softcap > 0.f) {   // scale / cap to its eighth power, and cap / scale, stay finite in fp32
+    const double cap = (double)d->softcap / logit_scale(d);
+    if (cap < 0x1p-14 || cap > 0x1p100) return QEVICT_EINVAL;
+  }
   if (d->s_q > (1 << 30) || d->s_kv > (1 << 30) || s_prefix < 0 || s_prefix > (1 << 30)) return QEVICT_EINVAL;
   for (int n = 0; n < 3; ++n) {
     const int64_t *st = n == 0 ? d->q : n == 1 ? d->k : d->v;
@@ -251,8 +258,9 @@ qevict_status attn_plan(const qevict_attn_desc *d, int s_prefix, AttnPlan *p) {
   }
   // One stream of key tiles cut into equal shares, or whole units in turn.  The stream evens out caches of different
   // lengths and fills the SMs when there are few units, at the price of parts that are merged afterwards.  Units of one row tile
-  // have few rows to merge.  Pairs have 256, which costs as much as about 16 key tiles: prompts of 512 and 1024 tokens take 29 and 43 us
-  // as a stream, 13 and 17 as units; the last 256 tokens of 32K 114 us as a stream.
+  // have few rows to merge.  Pairs have 256, which costs as much as about 16 key tiles: prompts of 512 and 1024 tokens
+  // of 32 heads take 29 and 43 us as a stream, 13 and 19 as units; the last 256 tokens of 32K, which would fill 32 of the
+  // SMs as units, 111 us as a stream.
   p->stream = s_prefix || (tiles > MIN_TILES && (n_qt == 1 ? tiles > WHOLE_TILES || 2 * units < sms
                                                            : tiles * (sms - std::min(units, sms)) >= 16 * sms));
   if ((total > (1 << 30) || p->rows > (1ll << 30)) && p->stream) {
@@ -326,7 +334,7 @@ qevict_status attn_launch(const qevict_attn_desc *d, const AttnPlan &pl, const q
   A.pre = pl.pre, A.nb = std::max(1, pl.nb), A.n_prp = pl.n_prp;
   A.part_rows = pl.part_rows, A.pre_rows = pl.pre_rows;
   A.stream = pl.stream, A.min_tiles = MIN_TILES;
-  const float scale = d->scale > 0.f ? d->scale : 1.f / std::sqrt((float)D), log2e = 1.4426950408889634f;
+  const float scale = logit_scale(d), log2e = 1.4426950408889634f;
   A.scale_log2 = scale * log2e;
   if (d->softcap > 0.f) {
     A.cap_u = scale / d->softcap;

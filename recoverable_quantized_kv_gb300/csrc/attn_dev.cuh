@@ -125,12 +125,6 @@ struct AttnItem {
 };
 static_assert(sizeof(AttnItem) == 64, "item ring");
 
-// Whether some row of the item does not see some key of tile t: only there can a value that is not finite
-// stand in a masked place (a masked probability is 0, and 0 * NaN is not).
-__device__ __forceinline__ bool attn_mixed(const AttnItem &I, int t) {
-  return t * AT_TILE < I.clean_lo || (t + 1) * AT_TILE > I.clean_hi;
-}
-
 // What row r of a slot's tile is, in every item: token r / G of the tile and query head r % G of the group.
 struct AttnRow {
   int tok, hr, bl, ip;         // in a prefix item the token is query ip of the tile's sequence bl
@@ -162,6 +156,9 @@ __device__ __forceinline__ bool attn_row(const AttnArgs &P, const AttnItem &I, i
   prow = il * P.G + R.hr;
   return R.tok < P.tpt && i < I.ql;
 }
+
+// Until the kernel before, which may still run, has ended and its writes are visible.
+__device__ __forceinline__ void attn_wait_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
 // Bounded wait on an mbarrier phase.  The limit is about 4 s (8e9 SM cycles), longer than the 200 ms of the other
 // kernels' waits, since a slot that recomputes rows on the CUDA cores (attn_exact_rows) holds the others up.  The
@@ -256,11 +253,6 @@ __device__ __forceinline__ void tmem_ld16(uint32_t addr, uint32_t *r) {
       "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
       : QV_W16(r, 0)
       : "r"(addr));
-}
-__device__ __forceinline__ void tmem_st8(uint32_t addr, const uint32_t *r) {
-  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%8], {%0,%1,%2,%3,%4,%5,%6,%7};" ::"r"(r[0]), "r"(r[1]), "r"(r[2]),
-               "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(addr)
-               : "memory");
 }
 // 32 columns of this thread's lane; the caller waits (tmem_wait_ld) before it uses them
 __device__ __forceinline__ void tmem_ld32(uint32_t addr, uint32_t *r) {
@@ -502,6 +494,7 @@ __global__ void __launch_bounds__(AT_THREADS, 1) attn_kernel(const __grid_consta
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   int *status = P.status;
   if (smem_u32(sm) & 1023) {   // cannot be swizzled: nothing runs
+    attn_wait_previous();
     if (threadIdx.x == 0) atomicOr(status, QV_ERR_STATE);
     return;
   }
@@ -520,7 +513,7 @@ __global__ void __launch_bounds__(AT_THREADS, 1) attn_kernel(const __grid_consta
   }
   // The launch may overlap the previous kernel's end: nothing is read from device memory before this wait, and the next
   // kernel is let in only after it, so whatever starts early still finds the kernel two launches back complete.
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  attn_wait_previous();
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   AttnGroup plan_a;        // the plan warp's lane: its group of the first 32, worked out while the others set up
   int plan_places = 0;     // and the places of all groups
@@ -816,8 +809,8 @@ __global__ void __launch_bounds__(AT_THREADS, 1) attn_kernel(const __grid_consta
       const bool prefix = STREAM && I.prefix(), pair = !STREAM || I.pair(), parts = STREAM && I.parts();
       // what a thread keeps of its row in each slot (in a single row tile both are the same row)
       struct Slot {
-        float m, l, pos;
-        int lo, hi;
+        float m, l;
+        int lo, hi, pos;   // pos: an integer, as positions past 2^24 are not all fp32 numbers
         bool any;
       } S0, S1;
       float slope = 0.f;
@@ -826,16 +819,16 @@ __global__ void __launch_bounds__(AT_THREADS, 1) attn_kernel(const __grid_consta
         const bool valid = attn_row<STREAM>(P, I, slot, R, b, i, h, prow);
         S.any = __any_sync(0xffffffffu, valid);
         S.lo = 0, S.hi = 1 << 30;   // padding rows take no masks: nothing reads what they compute
-        S.m = -INFINITY, S.l = 0.f, S.pos = 0.f;
+        S.m = -INFINITY, S.l = 0.f, S.pos = 0;
         if (valid) {
           if (prefix) {
             S.hi = P.pre;
-            if (BIAS) S.pos = (float)(P.pre + (P.kv_len ? clampi(P.kv_len[b], 0, P.s_kv) : P.s_kv) - P.s_q + i);
+            if (BIAS) S.pos = P.pre + ((P.kv_len ? clampi(P.kv_len[b], 0, P.s_kv) : P.s_kv) - P.s_q + i);
           } else {
             const int p = I.kl - I.ql + i;
             const int2 v = attn_interval(P, b, p, I.kl, I.pfx);
             S.lo = v.x - I.k0, S.hi = v.y - I.k0;   // counted from k0, as the tiles are
-            if (BIAS) S.pos = (float)(p - I.k0);
+            if (BIAS) S.pos = p - I.k0;
           }
           if (BIAS) slope = P.slopes[h] * 1.4426950408889634f;
         }
@@ -931,7 +924,7 @@ __global__ void __launch_bounds__(AT_THREADS, 1) attn_kernel(const __grid_consta
             capped(v);
           }
           if (BIAS) {
-            const float sl = P.scale_log2, d0 = S.pos - (float)c0;
+            const float sl = P.scale_log2, d0 = (float)(S.pos - c0);
             if ((P.causal && !P.prefix_len) || __all_sync(0xffffffffu, d0 >= (float)(AT_COLS - 1))) {
               // no key behind the row's position is seen: -slope |p - j| = -slope (p - c0) + slope (j - c0)
               const uint64_t sl2 = pack_f2(sl, sl), hop = pack_f2(2.f * slope, 2.f * slope);

@@ -434,6 +434,8 @@ qevict_status qevict_rope_apply(const qevict_rope_desc *d, const float *d_table,
     const char *o1 = o0 + extent(so, d->batch, d->seq, heads, d->d_head) * size;
     if (!same && i0 < o1 && o0 < i1) return QEVICT_EINVAL;
   }
+  // queries and keys may lie between one another, but what is written of one may not be the other
+  if (d->h_q && d->h_k && (q_out == k_out || q_out == k_in || k_out == q_in)) return QEVICT_EINVAL;
   RopeArgs A = {};
   A.q = q_in, A.k = k_in, A.qo = q_out, A.ko = k_out;
   A.table = reinterpret_cast<const float2 *>(d_table);

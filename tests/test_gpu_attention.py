@@ -335,6 +335,74 @@ def test_a_stream_given_by_the_caller(lib):
     plan.check(stream=side)
 
 
+@pytest.mark.parametrize("sq", [1, 600])
+def test_a_plan_made_while_its_stream_is_busy(lib, sq):
+    """A plan made behind queued work, in memory that holds other bits, and used at once on a stream that waits for nothing."""
+    side = torch.cuda.Stream()
+    q, k, v = rnd(2, sq, 8, 128), rnd(2, 600, 2, 128, seed=2), rnd(2, 600, 2, 128, seed=3)
+    torch.cuda.synchronize()
+    torch.full((binding.Attention(2, sq, 600, 8, 2).work.numel(),), 255, dtype=torch.uint8, device="cuda")
+    big = torch.ones(1 << 28, device="cuda")
+    for _ in range(20):
+        big.mul_(1.0)
+    plan = binding.Attention(2, sq, 600, 8, 2)
+    out, lse = plan.run(q, k, v, stream=side)
+    plan.check(stream=side)
+    R.compare(out, lse, R.attention(q, k, v))
+
+
+def test_an_error_leaves_a_usable_plan(lib):
+    """The count of units given out starts anew after a reported error."""
+    q, k, v = rnd(2, 600, 8, 128), rnd(2, 600, 2, 128, seed=2), rnd(2, 600, 2, 128, seed=3)
+    plan = binding.Attention(2, 600, 600, 8, 2)
+    plan.run(q, k, v)
+    plan.work[:4] = torch.tensor([1, 0, 0, 0], dtype=torch.uint8)        # a wait that ran out
+    plan.work[128:132] = torch.tensor([3, 0, 0, 0], dtype=torch.uint8)   # and left a count
+    with pytest.raises(binding.QEvictError):
+        plan.check()
+    assert not plan.work[:256].any()
+    R.compare(*plan.run(q, k, v), R.attention(q, k, v))
+    plan.check()
+
+
+def test_captured_plan_made_in_the_capture(lib):
+    q, k, v = rnd(2, 300, 8, 128), rnd(2, 300, 2, 128, seed=2), rnd(2, 300, 2, 128, seed=3)
+    binding.Attention(2, 300, 300, 8, 2).run(q, k, v)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        plan = binding.Attention(2, 300, 300, 8, 2)
+        out, lse = plan.run(q, k, v)
+    for _ in range(3):
+        graph.replay()
+    R.compare(out, lse, R.attention(q, k, v))
+    plan.check()
+
+
+def test_zero_logits_under_the_smallest_cap(lib):
+    """tanh(0) stays 0 where the powers of scale / cap are largest: a mean of the visible values."""
+    q, k, v = torch.zeros(1, 200, 4, 128, dtype=BF, device="cuda"), rnd(1, 200, 2, 128, seed=2), rnd(1, 200, 2, 128, seed=3)
+    for cap in (2.0 ** -14, 2.0 ** 99):
+        plan = binding.Attention(1, 200, 200, 4, 2, softcap=cap, scale=1.0)
+        out, lse = plan.run(q, k, v)
+        plan.check()
+        R.compare(out, lse, R.attention(q, k, v, scale=1.0, cap=cap))
+
+
+def test_bias_at_positions_past_fp32_integers(lib):
+    """A token at position 2^24 + 4097 and zero keys: the logits are -slope |p - j|, lse = -log(1 - exp(-slope)) up to
+    exp(-slope 2^24).  A distance that was off by one key would move lse by the slope, 0.5."""
+    n, slope = 2 ** 24 + 4098, 0.5
+    kv = torch.zeros(1, n, 1, 128, dtype=BF, device="cuda")
+    plan = binding.Attention(1, 1, n, 1, 1)
+    out, lse = plan.run(rnd(1, 1, 1, 128), kv, kv, slopes=torch.tensor([slope], device="cuda"))
+    plan.check()
+    assert not out.any()
+    # Terms of 32 keys at a time stay below 32 in log2 units, whose half step is 2^-20: 16 sums of the bias along the keys,
+    # four more roundings, and the exponential's and logarithm's 2^-22 each: less than 21 * 2^-20.
+    assert abs(lse.item() + math.log(1 - math.exp(-slope))) <= 21 * 2.0 ** -20
+
+
 def test_plans_of_one_workspace_size_do_not_share(lib):
     """Calls of different shapes in turn on one stream, each plan with its own workspace, results unchanged."""
     plans = []

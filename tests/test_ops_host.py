@@ -88,6 +88,12 @@ def test_rope_pointers(lib, kw):
     assert rope_call(lib, rope_desc(), **kw) == B.EINVAL
 
 
+@pytest.mark.parametrize("kw", [dict(qo=PTR + (2 << 30)), dict(ko=PTR), dict(qo=PTR + (3 << 30))])
+def test_rope_outputs_over_the_other_tensor(lib, kw):
+    """Queries written over the keys, keys over the queries, both to one place."""
+    assert rope_call(lib, rope_desc(), **kw) == B.EINVAL
+
+
 def test_rope_positions_past_the_table_without_a_list(lib):
     assert rope_call(lib, rope_desc(pos0=98), pos=0) == B.EINVAL
     assert rope_call(lib, rope_desc(pos0=2 ** 62), pos=0) == B.EINVAL
@@ -113,6 +119,16 @@ def test_attention_descriptors(lib, kw):
     n = ctypes.c_size_t()
     assert lib.qevict_attn_bytes(ctypes.byref(attn_desc(**kw)), ctypes.byref(n)) == B.EINVAL
     assert lib.qevict_attn(ctypes.byref(attn_desc(**kw)), None, PTR, PTR, PTR, PTR, None, PTR, 1 << 40, None) == B.EINVAL
+
+
+@pytest.mark.parametrize("scale,lo,hi", [(0.0, 2.0 ** -14 / math.sqrt(128), 2.0 ** 100 / math.sqrt(128)),
+                                         (0.25, 2.0 ** -16, 2.0 ** 98)])
+def test_attention_caps(lib, scale, lo, hi):
+    """A cap far below or above the scale leaves fp32's range in its powers."""
+    n = ctypes.c_size_t()
+    for cap, want in ((lo * 1.001, B.OK), (hi * 0.999, B.OK), (lo * 0.99, B.EINVAL), (hi * 1.01, B.EINVAL)):
+        assert lib.qevict_attn_bytes(ctypes.byref(attn_desc(scale=scale, softcap=cap)), ctypes.byref(n)) == want
+        assert lib.qevict_prefix_attn_bytes(ctypes.byref(prefix_desc(scale=scale, softcap=cap)), ctypes.byref(n)) == want
 
 
 @pytest.mark.parametrize("i", range(9))
