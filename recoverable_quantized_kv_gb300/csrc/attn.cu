@@ -330,6 +330,8 @@ qevict_status attn_launch(const qevict_attn_desc *d, const AttnPlan &pl, const q
   A.mul_q = d->batch > 1 && d->q[0] ? 1 : 0;
   A.mul_k = d->batch > 1 && d->k[0] ? 1 : 0;
   A.mul_v = d->batch > 1 && d->v[0] ? 1 : 0;
+  A.wide_out = ((uintptr_t)out & 31) == 0 && (d->batch == 1 || d->o[0] % 16 == 0) && (d->s_q == 1 || d->o[1] % 16 == 0) &&
+               (d->h_q == 1 || d->o[2] % 16 == 0);
   A.tpt = pl.tpt, A.n_pr = pl.n_pr;
   A.pre = pl.pre, A.nb = std::max(1, pl.nb), A.n_prp = pl.n_prp;
   A.part_rows = pl.part_rows, A.pre_rows = pl.pre_rows;

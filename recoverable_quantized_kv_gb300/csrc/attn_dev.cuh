@@ -6,6 +6,8 @@
 // out = O / l, lse = (m + log2 l) ln 2.
 #pragma once
 
+#include <type_traits>
+
 #include "smem_optin.h"
 #include "tc_dev.cuh"
 
@@ -48,6 +50,7 @@ struct AttnArgs {
   int tpt, n_pr;               // own keys: tokens per row tile, pairs of row tiles
   int pre, nb, n_prp;          // prefix: keys, sequences per row tile, pairs of row tiles
   int part_rows, pre_rows;     // rows of a part
+  int wide_out;                // rows of out start on 32 bytes
   int stream, min_tiles;       // the key tiles of all units as one stream, cut into equal shares of at least min_tiles
   float scale_log2;            // logit scale * log2 e
   float cap_u, cap_s;          // softcap: scale / cap, cap / scale
@@ -330,32 +333,30 @@ __device__ __forceinline__ float2 unpack2(uint32_t v) {
   return make_float2(bf16_lo(v), bf16_hi(v));
 }
 
-// 64 bytes of every lane's row (at element `at` of out; rows: the lanes that have one).  Four lanes turn their four rows
-// around, 16 bytes at a time, so that each store of the warp writes 64 bytes of eight rows; rows stored by their own lanes
-// touch 32 lines an instruction.
-__device__ __forceinline__ void attn_store_rows(uint16_t *out, int64_t at, uint32_t rows, int lane, uint4 (&u)[4]) {
+// 64 bytes of every lane's row (at element `at` of out; rows: the lanes that have one).  Lanes trade 32 bytes with their
+// neighbour, so that each store of the warp writes 64 bytes of 16 rows, 32 of them a lane where the rows allow (`wide`);
+// rows stored by their own lanes touch 32 lines an instruction.
+__device__ __forceinline__ void attn_store_rows(uint16_t *out, int64_t at, uint32_t rows, int lane, bool wide, uint32_t (&w)[16]) {
+  const bool odd = lane & 1;
 #pragma unroll
-  for (int d = 2; d; d >>= 1) {
-    const bool up = lane & d;
-#pragma unroll
-    for (int c = 0; c < 4; ++c) {
-      if (c & d) continue;
-      uint4 send = up ? u[c] : u[c | d];
-      send.x = __shfl_xor_sync(0xffffffffu, send.x, d);
-      send.y = __shfl_xor_sync(0xffffffffu, send.y, d);
-      send.z = __shfl_xor_sync(0xffffffffu, send.z, d);
-      send.w = __shfl_xor_sync(0xffffffffu, send.w, d);
-      if (up)
-        u[c] = send;
-      else
-        u[c | d] = send;
-    }
+  for (int c = 0; c < 8; ++c) {
+    const uint32_t x = __shfl_xor_sync(0xffffffffu, odd ? w[c] : w[c + 8], 1);
+    if (odd)
+      w[c] = x;
+    else
+      w[c + 8] = x;
   }
+  const int64_t mate = __shfl_xor_sync(0xffffffffu, at, 1);
 #pragma unroll
-  for (int c = 0; c < 4; ++c) {
-    const int r = (lane & 28) + c;
-    const int64_t to_row = __shfl_sync(0xffffffffu, at, r);
-    if (rows >> r & 1) *reinterpret_cast<uint4 *>(out + to_row + 8 * (lane & 3)) = u[c];
+  for (int r = 0; r < 2; ++r) {   // the pair's rows
+    if (!(rows >> ((lane & 30) + r) & 1)) continue;
+    uint16_t *dst = out + (odd == (r == 1) ? at : mate) + (odd ? 16 : 0);
+    if (wide) {
+      st_global_v8(dst, w + 8 * r);
+    } else {
+      reinterpret_cast<uint4 *>(dst)[0] = make_uint4(w[8 * r], w[8 * r + 1], w[8 * r + 2], w[8 * r + 3]);
+      reinterpret_cast<uint4 *>(dst)[1] = make_uint4(w[8 * r + 4], w[8 * r + 5], w[8 * r + 6], w[8 * r + 7]);
+    }
   }
 }
 
@@ -826,8 +827,13 @@ __global__ void __launch_bounds__(AT_THREADS, 1) attn_kernel(const __grid_consta
             if (BIAS) S.pos = P.pre + ((P.kv_len ? clampi(P.kv_len[b], 0, P.s_kv) : P.s_kv) - P.s_q + i);
           } else {
             const int p = I.kl - I.ql + i;
-            const int2 v = attn_interval(P, b, p, I.kl, I.pfx);
-            S.lo = v.x - I.k0, S.hi = v.y - I.k0;   // counted from k0, as the tiles are
+            if (I.clean_lo > 0) {
+              const int2 v = attn_interval(P, b, p, I.kl, I.pfx);
+              S.lo = v.x - I.k0, S.hi = v.y - I.k0;   // counted from k0, as the tiles are
+            } else {   // one document: the rows' first key is k0, their last the item's or their own
+              S.hi = P.causal ? min(max(p + 1, I.pfx) - I.k0, I.key_hi) : I.key_hi;
+              if (S.hi < 0 || (P.runs && p < 0)) S.hi = 0;
+            }
             if (BIAS) S.pos = p - I.k0;
           }
           if (BIAS) slope = P.slopes[h] * 1.4426950408889634f;
@@ -847,7 +853,7 @@ __global__ void __launch_bounds__(AT_THREADS, 1) attn_kernel(const __grid_consta
       // 0.6 (errors 1e-7 and 7e-8 of tanh in fp32).  Beyond, 1 - 2 / (1 + 2^(2 log2e u)) with one reciprocal for two, 1 / a =
       // b / (a b), where 2^60 bounds the exponentials so that the product stays finite.  A 4K prompt of 32 heads takes 100 us
       // without a cap, 139 with one, bound by the FMA pipe's share of each step (158 with degree 4, 173 by exponentials).
-      auto capped = [&](float *v) {
+      auto capped = [&](float *v, uint32_t see) {
         float x0 = 0.f, x1 = 0.f;
 #pragma unroll
         for (int c = 0; c < AT_COLS; c += 4) {
@@ -875,6 +881,11 @@ __global__ void __launch_bounds__(AT_THREADS, 1) attn_kernel(const __grid_consta
           }
         } else {
           const float in = P.cap_u * 2.8853900817779268f;   // 2 log2 e
+          if (see != ~0u) {   // a NaN in a masked place stays out of its neighbour
+#pragma unroll
+            for (int c = 0; c < AT_COLS; ++c)
+              if (!(see & (1u << c))) v[c] = 0.f;
+          }
 #pragma unroll
           for (int c = 0; c < AT_COLS; c += 2) {
             const float a = 1.f + ex2(min_nan(v[c] * in, 60.f)), b = 1.f + ex2(min_nan(v[c + 1] * in, 60.f));
@@ -885,22 +896,19 @@ __global__ void __launch_bounds__(AT_THREADS, 1) attn_kernel(const __grid_consta
         }
       };
       // One slot's S of key tile j (from the last) into probabilities; first: the slot's first tile
-      auto step = [&](const int slot, Slot &S, uint32_t &sc, int j, bool first) {
+      auto step_of = [&](auto masks, const int slot, Slot &S, uint32_t &sc, int j, bool first) {
+        constexpr bool mixed = decltype(masks)::value;   // some row does not see some key of the tile
         const int t = I.t_hi - 1 - j;
         const uint32_t ts = lane_base + 128 * slot;
-        const bool mixed = t < clean_lo || t >= clean_hi;
-        // Values of a partly masked tile are looked over while S is on its way, once for both slots of a pair.  The stage's
-        // previous tile has been used by an S that came before, so its phase cannot be mistaken; in a single row tile only
-        // once this S has come, since the other slot's tiles stand between.
+        // Values of a partly masked tile are looked over before P V may run, once for both slots of a pair.  This S, and so
+        // every tile of the ring before its keys, has come: the stage's phase cannot be mistaken for the one before.
         auto look = [&]() {
           const uint32_t vpos = base + (pair ? 2 * j + 1 : j + min(I.n, j + 2)), st = vpos % AT_STAGES;
           if (ok) ok = attn_wait(&full[st], (vpos / AT_STAGES) & 1, status);
           attn_clean_values<FP16>(I, t, sm + AT_OFF_KV + st * AT_TILE_BYTES, threadIdx.x, &bad_item[seq & 1], seq);
         };
-        if (mixed && pair && slot == 0) look();
         if (ok) ok = attn_wait(&sfull[slot], sc & 1, status);
         ++sc;
-        if (STREAM && mixed && !pair) look();
         __syncwarp();
         tc_fence_after();
         if (S.any) {
@@ -910,19 +918,17 @@ __global__ void __launch_bounds__(AT_THREADS, 1) attn_kernel(const __grid_consta
           tmem_wait_ld();
           const int c0 = t * AT_TILE + quarter * AT_COLS;
           uint32_t see = ~0u;
+          bool none = false, part = false;   // of the warp's rows and columns none is visible, not all are
           if (mixed) {   // the row sees keys [lo, hi)
             const int a = clampi(S.lo - c0, 0, 32), z = clampi(S.hi - c0, 0, 32);
             see = (z == 32 ? ~0u : (1u << z) - 1u) & (a == 32 ? 0u : ~0u << a);
+            none = __all_sync(0xffffffffu, see == 0u);
+            part = !__all_sync(0xffffffffu, see == ~0u);
           }
           float base2 = 0.f;       // of every logit of the row in this tile
-          if (CAP) {
-            if (mixed) {           // a NaN in a masked place stays out of its neighbours
-#pragma unroll
-              for (int c = 0; c < AT_COLS; ++c)
-                if (!(see & (1u << c))) v[c] = 0.f;
-            }
-            capped(v);
-          }
+          float x0 = -INFINITY, x1;
+          if (!none) {
+          if (CAP) capped(v, see);
           if (BIAS) {
             const float sl = P.scale_log2, d0 = (float)(S.pos - c0);
             if ((P.causal && !P.prefix_len) || __all_sync(0xffffffffu, d0 >= (float)(AT_COLS - 1))) {
@@ -940,19 +946,20 @@ __global__ void __launch_bounds__(AT_THREADS, 1) attn_kernel(const __grid_consta
               for (int c = 0; c < AT_COLS; ++c) v[c] = fmaf(-slope, fabsf(d0 - (float)c), v[c] * sl);
             }
           }
-          if (mixed) {
+          if (part) {
 #pragma unroll
             for (int c = 0; c < AT_COLS; ++c)
               if (!(see & (1u << c))) v[c] = -INFINITY;
           }
-          float x0 = v[0], x1 = v[1];
+          x0 = v[0], x1 = v[1];
 #pragma unroll
           for (int c = 2; c < AT_COLS - 2; c += 4) {
             x0 = max3(x0, v[c], v[c + 1]);
             x1 = max3(x1, v[c + 2], v[c + 3]);
           }
-          x0 = max3(x0, v[AT_COLS - 2], v[AT_COLS - 1]);
-          const float mx = fmaf(fmaxf(x0, x1), scale2, base2);
+          x0 = fmaxf(max3(x0, v[AT_COLS - 2], v[AT_COLS - 1]), x1);
+          }
+          const float mx = fmaf(x0, scale2, base2);
           const bool grow = mx > S.m + 8.f;   // also the first finite max (m = -inf)
           int any;   // one barrier of the four warps: whether a row has grown in one of them
           asm volatile(
@@ -986,6 +993,11 @@ __global__ void __launch_bounds__(AT_THREADS, 1) attn_kernel(const __grid_consta
           const uint64_t mu2 = pack_f2(base2 - mu, base2 - mu);
           uint64_t sa = 0, sb = 0;
           uint32_t pk[16];
+          if (none) {
+#pragma unroll
+            for (int c = 0; c < 16; ++c) pk[c] = 0;
+            tmem_st16(ts, pk);
+          } else {
 #pragma unroll
           for (int c = 0; c < AT_COLS; c += 4) {
             float e0, e1, e2, e3;
@@ -1000,11 +1012,20 @@ __global__ void __launch_bounds__(AT_THREADS, 1) attn_kernel(const __grid_consta
           tmem_st16(ts, pk);   // over this quarter of S
           unpack_f2(x0, x1, add_f2(sa, sb));
           S.l += x0 + x1;
+          }
           tmem_wait_st();
         }
+        if (mixed && (slot == 0 || !pair)) look();
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&pfull[slot]);
+      };
+      auto step = [&](const int slot, Slot &S, uint32_t &sc, int j, bool first) {
+        const int t = I.t_hi - 1 - j;
+        if (__builtin_expect(t < clean_lo || t >= clean_hi, 0))
+          step_of(std::true_type(), slot, S, sc, j, first);
+        else
+          step_of(std::false_type(), slot, S, sc, j, first);
       };
       if (pair) {
         for (int j = 0; j < I.n; ++j) {
@@ -1061,13 +1082,10 @@ __global__ void __launch_bounds__(AT_THREADS, 1) attn_kernel(const __grid_consta
 #pragma unroll
               for (int c = 0; c < 32; ++c) o[c] = 0;
             }
-            uint4 u[4];
+            uint32_t w[16];
 #pragma unroll
-            for (int c = 0; c < 4; ++c)
-              u[c] = make_uint4(pack2<FP16>(of[8 * c] * inv, of[8 * c + 1] * inv), pack2<FP16>(of[8 * c + 2] * inv, of[8 * c + 3] * inv),
-                                pack2<FP16>(of[8 * c + 4] * inv, of[8 * c + 5] * inv),
-                                pack2<FP16>(of[8 * c + 6] * inv, of[8 * c + 7] * inv));
-            attn_store_rows(static_cast<uint16_t *>(P.out) + 32 * part, at, rows, lane, u);
+            for (int c = 0; c < 16; ++c) w[c] = pack2<FP16>(of[2 * c] * inv, of[2 * c + 1] * inv);
+            attn_store_rows(static_cast<uint16_t *>(P.out) + 32 * part, at, rows, lane, P.wide_out, w);
             __syncwarp();
           }
         } else if (any_row && side == 0) {
@@ -1157,19 +1175,17 @@ __global__ void __launch_bounds__(AT_THREADS, 1) attn_kernel(const __grid_consta
               }
             }
           } else {
-            uint4 u[4];
+            uint32_t w[16];
 #pragma unroll
             for (int q = 0; q < 2; ++q) {
               uint32_t o[16];
               take(q, o);
               const float *of = reinterpret_cast<const float *>(o);
 #pragma unroll
-              for (int c = 0; c < 2; ++c)
-                u[2 * q + c] = make_uint4(pack2<FP16>(of[8 * c], of[8 * c + 1]), pack2<FP16>(of[8 * c + 2], of[8 * c + 3]),
-                                          pack2<FP16>(of[8 * c + 4], of[8 * c + 5]), pack2<FP16>(of[8 * c + 6], of[8 * c + 7]));
+              for (int c = 0; c < 8; ++c) w[8 * q + c] = pack2<FP16>(of[2 * c], of[2 * c + 1]);
             }
             attn_store_rows(static_cast<uint16_t *>(P.out), b * P.so[0] + i * P.so[1] + h * P.so[2] + AT_COLS * quarter,
-                            __ballot_sync(0xffffffffu, valid), lane, u);
+                            __ballot_sync(0xffffffffu, valid), lane, P.wide_out, w);
           }
         } else if (quarter == 0) {
           attn_exact_rows<FP16, true>(P, I, slot, wq, lane, CAP,
