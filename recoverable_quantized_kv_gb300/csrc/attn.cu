@@ -23,6 +23,7 @@ cudaError_t launch_attn_fp16_cap(const AttnArgs &P, int grid, bool bias, cudaStr
 constexpr int RUN_THREADS = 1024;
 __global__ void __launch_bounds__(RUN_THREADS) doc_runs_kernel(const int *ids, int s_kv, int2 *runs) {
   __shared__ int w_last[32], w_first[32];
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");   // the attention kernel waits for this one to end
   const int *id = ids + (size_t)blockIdx.x * s_kv;
   int2 *out = runs + (size_t)blockIdx.x * s_kv;
   const int piece = (s_kv + RUN_THREADS - 1) / RUN_THREADS, t = threadIdx.x, lane = t & 31, warp = t >> 5;

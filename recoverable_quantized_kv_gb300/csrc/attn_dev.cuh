@@ -1029,8 +1029,22 @@ __global__ void __launch_bounds__(AT_THREADS, 1) attn_kernel(const __grid_consta
       };
       if (pair) {
         for (int j = 0; j < I.n; ++j) {
-          step(0, S0, sc0, j, j == 0);
-          step(1, S1, sc1, j, j == 0);
+          const int t = I.t_hi - 1 - j;
+          if (__builtin_expect(t < clean_lo || t >= clean_hi, 0)) {
+#pragma unroll 1
+            for (int s = 0; s < 2; ++s) {   // one copy of the code: it is run once or twice a unit
+              Slot S = s ? S1 : S0;
+              uint32_t sc = s ? sc1 : sc0;
+              step_of(std::true_type(), s, S, sc, j, j == 0);
+              if (s)
+                S1 = S, sc1 = sc;
+              else
+                S0 = S, sc0 = sc;
+            }
+          } else {
+            step_of(std::false_type(), 0, S0, sc0, j, j == 0);
+            step_of(std::false_type(), 1, S1, sc1, j, j == 0);
+          }
         }
       } else if (STREAM) {
         for (int j = 0; j < I.n; j += 2) {
