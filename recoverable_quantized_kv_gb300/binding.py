@@ -414,7 +414,7 @@ def _enter(device_index, stream, tensors):
     other = None if torch.cuda.current_device() == device_index else torch.device("cuda", device_index)
     if stream is None:
         return torch._C._cuda_getCurrentRawStream(device_index), other
-    _need(stream.device.index == device_index, "stream", f"the stream is on {stream.device}, the tensors on cuda:{device_index}")
+    _need(stream.device.index == device_index, "stream", f"{stream} is not on the tensors' device cuda:{device_index}")
     if stream != torch.cuda.current_stream(device_index):
         for t in tensors:
             if t is not None:

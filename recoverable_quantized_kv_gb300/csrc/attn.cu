@@ -17,9 +17,9 @@ cudaError_t launch_attn_fp16(const AttnArgs &P, int grid, bool bias, cudaStream_
 cudaError_t launch_attn_bf16_cap(const AttnArgs &P, int grid, bool bias, cudaStream_t s);
 cudaError_t launch_attn_fp16_cap(const AttnArgs &P, int grid, bool bias, cudaStream_t s);
 
-// First and past-the-last position of every position's run of equal ids.  One CTA per sequence; thread i
-// takes the i-th of 1024 consecutive pieces, finds the first and last run start in it, and scans over the warp and then
-// over the warps carry the last start before and the first start after each piece.
+// First and past-the-last position of every position's run of equal ids.  One CTA per sequence; thread i takes the i-th of
+// 1024 consecutive pieces, finds the first and last run start in it, and scans over the warp and then over the warps carry
+// the last start before and the first start after each piece.  Bound by latency: reads 4 bytes and writes 8 a position.
 constexpr int RUN_THREADS = 1024;
 __global__ void __launch_bounds__(RUN_THREADS) doc_runs_kernel(const int *ids, int s_kv, int2 *runs) {
   __shared__ int w_last[32], w_first[32];
@@ -87,7 +87,8 @@ __global__ void __launch_bounds__(128) attn_combine_kernel(const __grid_constant
   const int g = h / P.G, hr = h - g * P.G, pr = i / (2 * P.tpt), gi = pr * P.batch + b;
   const AttnGroup A = attn_group(P, gi);
   if (i >= A.ql) return attn_wait_previous();
-  const int tp = P.pre ? (P.pre + AT_TILE - 1) / AT_TILE : 0, wp = attn_places(tp), all_p = P.pre ? P.n_prp * P.h_kv * wp : 0;
+  const int tp = P.pre ? (P.pre + AT_TILE - 1) / AT_TILE : 0, wp = attn_places(tp);
+  const int all_p = P.pre ? P.n_prp * P.h_kv * wp : 0;
   int all = 0, before = 0;   // places of all groups, and of those before this one
 #pragma unroll 2
   for (int j = lane; j < P.n_pr * P.batch; j += 32) {
@@ -258,10 +259,10 @@ qevict_status attn_plan(const qevict_attn_desc *d, int s_prefix, AttnPlan *p) {
     total += (int64_t)p->n_prp * d->h_kv * ((s_prefix + AT_TILE - 1) / AT_TILE + AT_UNIT_COST);
   }
   // One stream of key tiles cut into equal shares, or whole units in turn.  The stream evens out caches of different
-  // lengths and fills the SMs when there are few units, at the price of parts that are merged afterwards.  Units of one row tile
-  // have few rows to merge.  Pairs have 256, which costs as much as about 16 key tiles: prompts of 512 and 1024 tokens
-  // of 32 heads take 29 and 43 us as a stream, 13 and 19 as units; the last 256 tokens of 32K, which would fill 32 of the
-  // SMs as units, 111 us as a stream.
+  // lengths and fills the SMs when there are few units, at the price of parts that are merged afterwards.  Units of one
+  // row tile have few rows to merge.  Pairs have 256, which costs as much as about 16 key tiles: prompts of 512 and 1024
+  // tokens of 32 heads take 29 and 43 us as a stream, 12.5 and 19 as units; the last 256 tokens of 32K, which would fill
+  // 32 of the SMs as units, 113 us as a stream.
   p->stream = s_prefix || (tiles > MIN_TILES && (n_qt == 1 ? tiles > WHOLE_TILES || 2 * units < sms
                                                            : tiles * (sms - std::min(units, sms)) >= 16 * sms));
   if ((total > (1 << 30) || p->rows > (1ll << 30)) && p->stream) {

@@ -215,7 +215,8 @@ __device__ __forceinline__ void tc_mma_tile_ss(uint32_t tmem, uint64_t da, uint6
 // apart
 __device__ __forceinline__ void tc_mma_tile_ts(uint32_t tmem, uint32_t ta, uint64_t db, uint32_t idesc, uint32_t accumulate) {
   asm volatile(
-      "{\n .reg .pred e, f, t;\n .reg .b64 b;\n .reg .b32 a;\n elect.sync _|e, 0xffffffff;\n setp.ne.b32 f, %4, 0;\n setp.eq.b32 t, 0, 0;\n"
+      "{\n .reg .pred e, f, t;\n .reg .b64 b;\n .reg .b32 a;\n elect.sync _|e, 0xffffffff;\n"
+      " setp.ne.b32 f, %4, 0;\n setp.eq.b32 t, 0, 0;\n"
       " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, f;\n"
       " add.s32 a, %1, 8;\n add.s64 b, %2, 128;\n @e tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, t;\n"
       " add.s32 a, %1, 32;\n add.s64 b, %2, 256;\n @e tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, t;\n"
@@ -297,7 +298,9 @@ __device__ __forceinline__ uint64_t pack_f2(float x, float y) {
   asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(x), "f"(y));
   return d;
 }
-__device__ __forceinline__ void unpack_f2(float &x, float &y, uint64_t v) { asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(v)); }
+__device__ __forceinline__ void unpack_f2(float &x, float &y, uint64_t v) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(v));
+}
 __device__ __forceinline__ uint64_t fma_f2(uint64_t a, uint64_t b, uint64_t c) {
   uint64_t d;
   asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
@@ -336,7 +339,8 @@ __device__ __forceinline__ float2 unpack2(uint32_t v) {
 // 64 bytes of every lane's row (at element `at` of out; rows: the lanes that have one).  Lanes trade 32 bytes with their
 // neighbour, so that each store of the warp writes 64 bytes of 16 rows, 32 of them a lane where the rows allow (`wide`);
 // rows stored by their own lanes touch 32 lines an instruction.
-__device__ __forceinline__ void attn_store_rows(uint16_t *out, int64_t at, uint32_t rows, int lane, bool wide, uint32_t (&w)[16]) {
+__device__ __forceinline__ void attn_store_rows(uint16_t *out, int64_t at, uint32_t rows, int lane, bool wide,
+                                                uint32_t (&w)[16]) {
   const bool odd = lane & 1;
 #pragma unroll
   for (int c = 0; c < 8; ++c) {
@@ -375,7 +379,8 @@ __device__ __forceinline__ void attn_clean_values(const AttnItem &I, int t, uint
 #pragma unroll
   for (int c = 0; c < 4; ++c) {
     const uint4 x = lds128(p + ((c + k) & 3) * 4);   // neighbours start in other banks
-    hit |= ((~x.x & E2) - 0x00010001u) | ((~x.y & E2) - 0x00010001u) | ((~x.z & E2) - 0x00010001u) | ((~x.w & E2) - 0x00010001u);
+    hit |= ((~x.x & E2) - 0x00010001u) | ((~x.y & E2) - 0x00010001u) | ((~x.z & E2) - 0x00010001u) |
+           ((~x.w & E2) - 0x00010001u);
   }
   if (hit & 0x80008000u) {
     if (key < I.key_hi) *flag = mark;   // key 0 is the first that some row sees
@@ -389,10 +394,10 @@ __device__ __forceinline__ void attn_clean_values(const AttnItem &I, int t, uint
   }
 }
 
-// The rows of one warp of a slot recomputed on the CUDA cores, every visible key of the item's own tiles in
-// turn and no masked value touched.  Reached when a value that some row of the item sees and another does not is an infinity or
-// NaN: the tensor-core product then ran with that value as 0.  Writes O (unnormalised), m, l of row r
-// through `emit`, the warp's lanes holding four channels each.
+// The rows of one warp of a slot recomputed on the CUDA cores, every visible key of the item's own tiles in turn and no
+// masked value touched.  Reached when a value that some row of the item sees and another does not is an infinity or NaN:
+// the tensor-core product then ran with that value as 0.  Writes O (unnormalised), m, l of row r through `emit`, the
+// warp's lanes holding four channels each.
 template <bool FP16, bool STREAM, typename Emit>
 __device__ __forceinline__ void attn_exact_rows(const AttnArgs &P, const AttnItem &I, int slot, int warp, int lane, bool cap,
                                                 const Emit &emit) {
@@ -469,12 +474,17 @@ __device__ __forceinline__ void attn_exact_rows(const AttnArgs &P, const AttnIte
 
 // ----------------------------------------------------------------------------- the kernel
 
-// One persistent CTA per SM: sixteen softmax warps, a thread owning one row and a quarter of the columns of the 128-row tile
-// at hand; a TMA warp; an MMA warp; a warp that lays out the work items ahead of the others.  Rows of a tile are (token, query head of the
-// group), so the group's heads share every key tile.  Tensor memory: S of slot s at columns 128 s, overwritten in place by
-// the probabilities (16-bit, the A operand of P V; each quarter of the keys over its own quarter of S), O of slot s at 256 + 128 s.  The
-// softmax warps and the tensor pipe alternate between the slots: while all warps turn slot 0's S into P, the pipe runs slot 1's
-// products.  (With eight warps a slot, a half row a thread, a 32K prompt of 32 heads takes 5.45 ms instead of 5.16.)
+// One persistent CTA per SM: sixteen softmax warps, a thread owning one row and a quarter of the columns of the 128-row
+// tile at hand; a TMA warp; an MMA warp; a warp that lays out the work items ahead of the others.  Rows of a tile are
+// (token, query head of the group), so the group's heads share every key tile.  Tensor memory: S of slot s at columns
+// 128 s, overwritten in place by the probabilities (each quarter of the keys over its own quarter of S), O of slot s at
+// 256 + 128 s.  The probabilities are rounded to the input type, which the product takes as its A operand; the row sums
+// take them unrounded.  The softmax warps and the tensor pipe alternate between the slots: while all warps turn slot 0's
+// S into P, the pipe runs slot 1's products.  (With eight warps a slot, a half row a thread, a 32K prompt of 32 heads
+// takes 5.45 ms instead of 5.16.)
+// What bounds it: prompts by a step's chain of S load, row maximum, exponentials and P store, which takes the softmax
+// warps about 1450 cycles where the tensor pipe needs 1180 (32K prompt of 32 heads: 5.16 ms, 1.70 PFLOP/s; 4.25 ms with
+// the softmax left out); single tokens by memory (16 of 32 heads against caches of 33K keys: 211 us, 6.7 TB/s).
 // Key tiles are taken from the last to the first, so a causal row meets its diagonal, and a distance bias its largest
 // logits, first.  The running max moves only when a row's max has grown by more than 2^8 (then the warps rescale their
 // rows of O in tensor memory): until then p reaches at most 2^8, which fp32 sums and 16-bit probabilities hold as well.
@@ -572,17 +582,21 @@ __global__ void __launch_bounds__(AT_THREADS, 1) attn_kernel(const __grid_consta
     };
     const int groups = P.n_pr * P.batch;
     if (!STREAM) {
-      // Whole units, the longest (last rows of causal prompts) first, each to the CTA that is ready next: lengths and documents
-      // make units differ, and a fixed turn leaves some CTAs twice the mean.  A CTA's first unit is its own number; it draws the next
-      // when its TMA warp has asked for the last one's tiles, two or three tiles before it needs it.  Every CTA draws once past the
-      // end, so the draw that takes the count to the number of units is the last, and starts it again for the next call.
+      // Whole units, the longest (last rows of causal prompts) first, each to the CTA that is ready next: lengths and
+      // documents make units differ, and a fixed turn leaves some CTAs twice the mean (a padded batch of prefix-mask
+      // prompts 54 us, drawn 31).  A CTA's first unit is its own number; it draws the next when its TMA warp has asked
+      // for the last one's tiles, two or three tiles before it needs it.  Every CTA draws once past the end, so the draw
+      // that takes the count to the number of units is the last, and starts it again for the next call.
       const int units = groups * P.h_kv;
       int u = blockIdx.x;
       uint32_t drawn = 0;
       while (u < units) {
         const int x = u / P.h_kv, pr = x / P.batch;
-        put(own_item(attn_group(P, (P.n_pr - 1 - pr) * P.batch + (x - pr * P.batch)), u - x * P.h_kv));
-        if (ok) ok = attn_wait_warp(loaded, drawn++ & 1, status);
+        const AttnGroup A = attn_group(P, (P.n_pr - 1 - pr) * P.batch + (x - pr * P.batch));
+        if (A.tile0 * P.tpt < A.ql) {   // the padding of a shorter sequence has no rows to write
+          put(own_item(A, u - x * P.h_kv));
+          if (ok) ok = attn_wait_warp(loaded, drawn++ & 1, status);
+        }
         int n = 0;
         if (lane == 0) {
           n = atomicAdd(P.drawn, 1);
@@ -591,10 +605,11 @@ __global__ void __launch_bounds__(AT_THREADS, 1) attn_kernel(const __grid_consta
         u = gridDim.x + __shfl_sync(0xffffffffu, n, 0);
       }
     } else {
-      // The key tiles of all units, prefix first, as one stream; CTA c takes tiles [c share, (c + 1) share).  A unit cut by a
-      // share's end is written as parts, numbered CTA + unit: the numbers of a unit's parts are consecutive, and none is
-      // used twice, since both terms only grow along the stream.
-      const int tp = P.pre ? (P.pre + AT_TILE - 1) / AT_TILE : 0, wp = attn_places(tp), all_p = P.pre ? P.n_prp * P.h_kv * wp : 0;
+      // The key tiles of all units, prefix first, as one stream; CTA c takes tiles [c share, (c + 1) share).  A unit cut
+      // by a share's end is written as parts, numbered CTA + unit: the numbers of a unit's parts are consecutive, and
+      // none is used twice, since both terms only grow along the stream.
+      const int tp = P.pre ? (P.pre + AT_TILE - 1) / AT_TILE : 0, wp = attn_places(tp);
+      const int all_p = P.pre ? P.n_prp * P.h_kv * wp : 0;
       const int64_t total = (int64_t)all_p + plan_places;
       const int share = attn_share((int)total, gridDim.x, P.min_tiles);
       const int begin = (int)min((int64_t)blockIdx.x * share, total), end = (int)min((int64_t)begin + share, total);
@@ -713,8 +728,9 @@ __global__ void __launch_bounds__(AT_THREADS, 1) attn_kernel(const __grid_consta
   } else if (warp == AT_W_MMA) {
     // ---- MMA issue, the whole warp in step, slot after slot: P V and the next S of slot 0, then of slot 1.  (A warp per
     // slot lets the products of both slots interleave, so each finishes as late as both, and the slots fall into step
-    // instead of alternating: 6.99 ms against 5.6 for a 32K prompt of 32 heads.)  A slot's S(i + 1) overwrites P(i) after P V(i):
-    // the tensor pipe runs in the order of issue.  The warp meets the ring's tiles in order, so a phase parity is enough.
+    // instead of alternating: 6.99 ms against 5.6 for a 32K prompt of 32 heads.)  A slot's S(i + 1) overwrites P(i) after
+    // P V(i): the tensor pipe runs in the order of issue.  The warp meets the ring's tiles in order, so a phase parity is
+    // enough.
     constexpr uint32_t ab = FP16 ? 0u : 1u;
     constexpr uint32_t ID_S = (1u << 4) | (ab << 7) | (ab << 10) | ((uint32_t)(AT_TILE >> 3) << 17) |
                               ((uint32_t)(AT_TILE >> 4) << 24);
@@ -802,7 +818,8 @@ __global__ void __launch_bounds__(AT_THREADS, 1) attn_kernel(const __grid_consta
       // all softmax warps go on together or stop together: none is left alone at a barrier
       int stop;
       asm volatile(
-          "{\n .reg .pred p, q;\n setp.ne.s32 p, %1, 0;\n barrier.cta.red.or.aligned.pred q, %2, %3, p;\n selp.s32 %0, 1, 0, q;\n}"
+          "{\n .reg .pred p, q;\n setp.ne.s32 p, %1, 0;\n barrier.cta.red.or.aligned.pred q, %2, %3, p;\n"
+          " selp.s32 %0, 1, 0, q;\n}"
           : "=r"(stop)
           : "r"((int)(!got || I.kind < 0)), "r"(AT_BAR_ALL), "r"(AT_SOFT * 32)
           : "memory");
@@ -847,12 +864,14 @@ __global__ void __launch_bounds__(AT_THREADS, 1) attn_kernel(const __grid_consta
       // x = value * scale2: the products themselves, or with BIAS the finished logit
       const float scale2 = BIAS ? 1.f : P.scale_log2;
       const uint64_t scale22 = pack_f2(scale2, scale2);
-      const int clean_lo = (I.clean_lo + AT_TILE - 1) / AT_TILE, clean_hi = I.clean_hi / AT_TILE;   // tiles that every row sees whole
+      // tiles that every row sees whole
+      const int clean_lo = (I.clean_lo + AT_TILE - 1) / AT_TILE, clean_hi = I.clean_hi / AT_TILE;
       // Capped products: y with y scale = cap tanh(v scale / cap), tanh(u) = u Q(u^2) with Q fitted at Chebyshev nodes, its
-      // coefficients scaled to take v: of degree 2 where no |u| of the warp's rows exceeds 0.25, the usual case, of degree 4 up to
-      // 0.6 (errors 1e-7 and 7e-8 of tanh in fp32).  Beyond, 1 - 2 / (1 + 2^(2 log2e u)) with one reciprocal for two, 1 / a =
-      // b / (a b), where 2^60 bounds the exponentials so that the product stays finite.  A 4K prompt of 32 heads takes 100 us
-      // without a cap, 139 with one, bound by the FMA pipe's share of each step (158 with degree 4, 173 by exponentials).
+      // coefficients scaled to take v: of degree 2 where no |u| of the warp's rows exceeds 0.25, the usual case, of degree
+      // 4 up to 0.6 (errors 1e-7 and 7e-8 of tanh in fp32).  Beyond, 1 - 2 / (1 + 2^(2 log2e u)) with one reciprocal for
+      // two, 1 / a = b / (a b), where 2^60 bounds the exponentials so that the product stays finite.  A 4K prompt of 32
+      // heads takes 99 us without a cap, 139 with one, bound by the FMA pipe's share of each step (158 with degree 4
+      // alone, 173 by exponentials).
       auto capped = [&](float *v, uint32_t see) {
         float x0 = 0.f, x1 = 0.f;
 #pragma unroll
@@ -897,7 +916,9 @@ __global__ void __launch_bounds__(AT_THREADS, 1) attn_kernel(const __grid_consta
       };
       // One slot's S of key tile j (from the last) into probabilities; first: the slot's first tile
       auto step_of = [&](auto masks, const int slot, Slot &S, uint32_t &sc, int j, bool first) {
-        constexpr bool mixed = decltype(masks)::value;   // some row does not see some key of the tile
+        // Some row does not see some key of the tile: a body of its own, since its branches in the common one cost a
+        // prompt of 8192 tokens 5%.
+        constexpr bool mixed = decltype(masks)::value;
         const int t = I.t_hi - 1 - j;
         const uint32_t ts = lane_base + 128 * slot;
         // Values of a partly masked tile are looked over before P V may run, once for both slots of a pair.  This S, and so
@@ -928,42 +949,43 @@ __global__ void __launch_bounds__(AT_THREADS, 1) attn_kernel(const __grid_consta
           float base2 = 0.f;       // of every logit of the row in this tile
           float x0 = -INFINITY, x1;
           if (!none) {
-          if (CAP) capped(v, see);
-          if (BIAS) {
-            const float sl = P.scale_log2, d0 = (float)(S.pos - c0);
-            if ((P.causal && !P.prefix_len) || __all_sync(0xffffffffu, d0 >= (float)(AT_COLS - 1))) {
-              // no key behind the row's position is seen: -slope |p - j| = -slope (p - c0) + slope (j - c0)
-              const uint64_t sl2 = pack_f2(sl, sl), hop = pack_f2(2.f * slope, 2.f * slope);
-              uint64_t b2 = pack_f2(0.f, slope);
+            if (CAP) capped(v, see);
+            if (BIAS) {
+              const float sl = P.scale_log2, d0 = (float)(S.pos - c0);
+              if ((P.causal && !P.prefix_len) || __all_sync(0xffffffffu, d0 >= (float)(AT_COLS - 1))) {
+                // no key behind the row's position is seen: -slope |p - j| = -slope (p - c0) + slope (j - c0)
+                const uint64_t sl2 = pack_f2(sl, sl), hop = pack_f2(2.f * slope, 2.f * slope);
+                uint64_t b2 = pack_f2(0.f, slope);
 #pragma unroll
-              for (int c = 0; c < AT_COLS; c += 2) {
-                unpack_f2(v[c], v[c + 1], fma_f2(pack_f2(v[c], v[c + 1]), sl2, b2));
-                b2 = add_f2(b2, hop);
+                for (int c = 0; c < AT_COLS; c += 2) {
+                  unpack_f2(v[c], v[c + 1], fma_f2(pack_f2(v[c], v[c + 1]), sl2, b2));
+                  b2 = add_f2(b2, hop);
+                }
+                base2 = -slope * d0;
+              } else {
+#pragma unroll
+                for (int c = 0; c < AT_COLS; ++c) v[c] = fmaf(-slope, fabsf(d0 - (float)c), v[c] * sl);
               }
-              base2 = -slope * d0;
-            } else {
-#pragma unroll
-              for (int c = 0; c < AT_COLS; ++c) v[c] = fmaf(-slope, fabsf(d0 - (float)c), v[c] * sl);
             }
-          }
-          if (part) {
+            if (part) {
 #pragma unroll
-            for (int c = 0; c < AT_COLS; ++c)
-              if (!(see & (1u << c))) v[c] = -INFINITY;
-          }
-          x0 = v[0], x1 = v[1];
+              for (int c = 0; c < AT_COLS; ++c)
+                if (!(see & (1u << c))) v[c] = -INFINITY;
+            }
+            x0 = v[0], x1 = v[1];
 #pragma unroll
-          for (int c = 2; c < AT_COLS - 2; c += 4) {
-            x0 = max3(x0, v[c], v[c + 1]);
-            x1 = max3(x1, v[c + 2], v[c + 3]);
-          }
-          x0 = fmaxf(max3(x0, v[AT_COLS - 2], v[AT_COLS - 1]), x1);
+            for (int c = 2; c < AT_COLS - 2; c += 4) {
+              x0 = max3(x0, v[c], v[c + 1]);
+              x1 = max3(x1, v[c + 2], v[c + 3]);
+            }
+            x0 = fmaxf(max3(x0, v[AT_COLS - 2], v[AT_COLS - 1]), x1);
           }
           const float mx = fmaf(x0, scale2, base2);
           const bool grow = mx > S.m + 8.f;   // also the first finite max (m = -inf)
           int any;   // one barrier of the four warps: whether a row has grown in one of them
           asm volatile(
-              "{\n .reg .pred p, q;\n setp.ne.s32 p, %1, 0;\n barrier.cta.red.or.aligned.pred q, %2, 128, p;\n selp.s32 %0, 1, 0, q;\n}"
+              "{\n .reg .pred p, q;\n setp.ne.s32 p, %1, 0;\n barrier.cta.red.or.aligned.pred q, %2, 128, p;\n"
+              " selp.s32 %0, 1, 0, q;\n}"
               : "=r"(any)
               : "r"((int)grow), "r"(row_bar)
               : "memory");
@@ -999,19 +1021,19 @@ __global__ void __launch_bounds__(AT_THREADS, 1) attn_kernel(const __grid_consta
             tmem_st16(ts, pk);
           } else {
 #pragma unroll
-          for (int c = 0; c < AT_COLS; c += 4) {
-            float e0, e1, e2, e3;
-            unpack_f2(e0, e1, fma_f2(pack_f2(v[c], v[c + 1]), scale22, mu2));
-            unpack_f2(e2, e3, fma_f2(pack_f2(v[c + 2], v[c + 3]), scale22, mu2));
-            e0 = ex2(e0), e1 = ex2(e1), e2 = ex2(e2), e3 = ex2(e3);
-            sa = add_f2(sa, pack_f2(e0, e1));
-            sb = add_f2(sb, pack_f2(e2, e3));
-            pk[c / 2] = pack2<FP16>(e0, e1);
-            pk[c / 2 + 1] = pack2<FP16>(e2, e3);
-          }
-          tmem_st16(ts, pk);   // over this quarter of S
-          unpack_f2(x0, x1, add_f2(sa, sb));
-          S.l += x0 + x1;
+            for (int c = 0; c < AT_COLS; c += 4) {
+              float e0, e1, e2, e3;
+              unpack_f2(e0, e1, fma_f2(pack_f2(v[c], v[c + 1]), scale22, mu2));
+              unpack_f2(e2, e3, fma_f2(pack_f2(v[c + 2], v[c + 3]), scale22, mu2));
+              e0 = ex2(e0), e1 = ex2(e1), e2 = ex2(e2), e3 = ex2(e3);
+              sa = add_f2(sa, pack_f2(e0, e1));
+              sb = add_f2(sb, pack_f2(e2, e3));
+              pk[c / 2] = pack2<FP16>(e0, e1);
+              pk[c / 2 + 1] = pack2<FP16>(e2, e3);
+            }
+            tmem_st16(ts, pk);   // over this quarter of S
+            unpack_f2(x0, x1, add_f2(sa, sb));
+            S.l += x0 + x1;
           }
           tmem_wait_st();
         }
@@ -1054,8 +1076,8 @@ __global__ void __launch_bounds__(AT_THREADS, 1) attn_kernel(const __grid_consta
       }
       // ---- the item's rows are done: the sums over the quarters, and the outputs
       if (!STREAM) {
-        // Whole units: two quarters of the warps finish each slot, half of its columns a thread, so that what a row costs is
-        // paid once.  The sums change hands while the last products run.
+        // Whole units: two quarters of the warps finish each slot, half of its columns a thread, so that what a row costs
+        // is paid once.  The sums change hands while the last products run.
         const int slot = quarter >> 1, side = quarter & 1;
         float l = 0.f;
         bool bad = false;

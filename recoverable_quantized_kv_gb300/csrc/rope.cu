@@ -60,10 +60,11 @@ __device__ __forceinline__ float2 cos_sin_turns(uint64_t ph) {
   return make_float2(c, s);
 }
 
-// A thread owns N neighbouring pairs (N = 2: 16-byte stores) and walks down the rows.  The angle in turns is p * turn[i] mod 2^64:
-// whole turns fall away in the integer product, exactly, so a position of 2^31 still has an angle to 2^-33 turns, and no
-// fp64 is needed (whose rate would bound this kernel at ten times its write time); a step down adds step * turn[i].
-// Bound by its arithmetic, about 40 operations for 8 bytes.
+// A thread owns N neighbouring pairs (N = 2: 16-byte stores) and walks down the rows.  The angle in turns is
+// p * turn[i] mod 2^64: whole turns fall away in the integer product, exactly, so a position of 2^31 still has an angle to
+// 2^-33 turns, and no fp64 is needed (whose rate would bound this kernel at ten times its write time); a step down adds
+// step * turn[i].  Bound by its arithmetic, 52 instructions for 8 bytes: 131072 rows of 64 pairs take 16.5 us, 71% of the
+// issue slots; writing them alone would take 9.9.
 template <int N>
 __global__ void __launch_bounds__(256) rope_table_kernel(const __grid_constant__ TableArgs A) {
   const int groups = A.pairs / N;
@@ -129,8 +130,8 @@ struct alignas(sizeof(T) * VEC) Pack {
 };
 
 // Who holds the two channels of a pair: one thread, from two places of the half layout (any size and alignment), one
-// thread in the interleaved layout, or two lanes of a warp, each with 16 bytes of the half layout, that swap them.  The last
-// keeps every load and store of a warp on whole heads.
+// thread in the interleaved layout, or two lanes of a warp, each with 16 bytes of the half layout, that swap them.  The
+// last keeps every load and store of a warp on whole heads.
 enum : int { ROPE_TWO_PLACES = 0, ROPE_INTERLEAVED = 1, ROPE_SWAP = 2 };
 
 // Two neighbouring channels as fp32 and back, rounded once
@@ -270,8 +271,8 @@ __global__ void __launch_bounds__(VEC > 1 ? 256 : 1024) rope_apply_kernel(const 
 namespace {
 
 // Block and grid for `units` vectors a head: a warp a block, four neighbouring heads a thread, so that a warp has 2 KB of
-// one place in flight, unless there are so few tokens that one head a thread does not fill the GPU.  A 32K prompt of 32 + 8
-// heads takes 110 us (6.2 TB/s, 92% of a plain copy); two heads a thread 167, eight 110, five warps a block 113.
+// one place in flight, unless there are so few tokens that one head a thread does not fill the GPU.  A 32K prompt of
+// 32 + 8 heads takes 111 us (6.2 TB/s, 91% of a plain copy); two heads a thread 167, eight 110, five warps a block 113.
 template <typename T, int VEC, int MODE>
 bool launch_apply(RopeArgs &A, int units, cudaStream_t s) {
   const bool one = MODE == ROPE_TWO_PLACES || A.tokens * units * (A.h_q + A.h_k) <= 152 * 2048;
@@ -292,7 +293,8 @@ bool launch_apply_type(RopeArgs &A, bool vec, bool inter, int d_head, cudaStream
   const int pass = d_head - 2 * A.half;
   if (inter) {
     A.pair_units = vec ? 2 * A.half / V : A.half;
-    return vec ? launch_apply<T, V, ROPE_INTERLEAVED>(A, d_head / V, s) : launch_apply<T, 1, ROPE_INTERLEAVED>(A, A.half + pass, s);
+    return vec ? launch_apply<T, V, ROPE_INTERLEAVED>(A, d_head / V, s)
+               : launch_apply<T, 1, ROPE_INTERLEAVED>(A, A.half + pass, s);
   }
   if (vec && 32 % (d_head / V) == 0 && d_head % V == 0) {   // a head's lanes in one warp
     A.pair_units = 2 * A.half / V;
