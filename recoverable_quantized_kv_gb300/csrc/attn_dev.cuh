@@ -1142,10 +1142,10 @@ __global__ void __launch_bounds__(AT_THREADS, 1) attn_kernel(const __grid_consta
       auto whole_row = [&](const int slot, Slot &S, uint32_t &oc) {
         if (ok) ok = attn_wait(&ofull[slot], oc & 1, status);
         ++oc;
+        asm volatile("bar.sync %0, 128;" ::"r"(row_bar) : "memory");   // what stood in xch has been read
         *x_own = S.l;
         asm volatile("bar.sync %0, 128;" ::"r"(row_bar) : "memory");
         S.l = (xch[row] + xch[AT_TILE + row]) + (xch[2 * AT_TILE + row] + xch[3 * AT_TILE + row]);
-        asm volatile("bar.sync %0, 128;" ::"r"(row_bar) : "memory");
       };
       if (slots > 0) whole_row(0, S0, oc0);
       if (slots > 1) whole_row(1, S1, oc1);
