@@ -160,6 +160,11 @@ __device__ __forceinline__ bool attn_row(const AttnArgs &P, const AttnItem &I, i
   return R.tok < P.tpt && i < I.ql;
 }
 
+// Position of query i of sequence b behind the prefix.
+__device__ __forceinline__ int attn_prefix_pos(const AttnArgs &P, int b, int i) {
+  return P.pre + ((P.kv_len ? clampi(P.kv_len[b], 0, P.s_kv) : P.s_kv) - P.s_q + i);
+}
+
 // Until the kernel before, which may still run, has ended and its writes are visible.
 __device__ __forceinline__ void attn_wait_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
@@ -418,9 +423,8 @@ __device__ __forceinline__ void attn_exact_rows(const AttnArgs &P, const AttnIte
     const uint16_t *q = static_cast<const uint16_t *>(P.q) + b * P.sq[0] + i * P.sq[1] + h * P.sq[2];
     int p, lo, hi;
     if (I.prefix()) {
-      const int kl = P.kv_len ? clampi(P.kv_len[b], 0, P.s_kv) : P.s_kv;
-      p = P.pre + kl - P.s_q + i;
-      lo = 0, hi = P.pre;
+      p = attn_prefix_pos(P, b, i);
+      lo = 0, hi = clampi(p + 1, 0, P.pre);
     } else {
       p = I.kl - I.ql + i;
       const int2 v = attn_interval(P, b, p, I.kl, I.pfx);
@@ -624,7 +628,9 @@ __global__ void __launch_bounds__(AT_THREADS, 1) attn_kernel(const __grid_consta
           I.n = min(tp - o, end - pos);
           I.t_hi = tp - o;
           I.k0 = I.clean_lo = 0;
-          I.clean_hi = I.key_hi = P.pre;
+          I.key_hi = P.pre;
+          // a sequence with fewer own keys than queries has rows that sit inside the prefix
+          I.clean_hi = max(0, P.pre - max(0, P.s_q - 1 - (P.kv_len ? 0 : P.s_kv)));
           I.part = blockIdx.x + u;
           put(I);
         }
@@ -840,8 +846,9 @@ __global__ void __launch_bounds__(AT_THREADS, 1) attn_kernel(const __grid_consta
         S.m = -INFINITY, S.l = 0.f, S.pos = 0;
         if (valid) {
           if (prefix) {
-            S.hi = P.pre;
-            if (BIAS) S.pos = P.pre + ((P.kv_len ? clampi(P.kv_len[b], 0, P.s_kv) : P.s_kv) - P.s_q + i);
+            const int p = attn_prefix_pos(P, b, i);
+            S.hi = clampi(p + 1, 0, P.pre);
+            if (BIAS) S.pos = p;
           } else {
             const int p = I.kl - I.ql + i;
             if (I.clean_lo > 0) {

@@ -13,7 +13,7 @@ def visible(pos, n, causal=True, prefix=0, ids=None):
     p = pos[:, None]
     ok = (key <= p) | (key < prefix) if causal else torch.ones(len(pos), n, dtype=torch.bool, device=pos.device)
     if ids is not None:
-        run = torch.cat([torch.zeros(1, dtype=torch.long, device=pos.device), (ids[1:n] != ids[:n - 1]).long().cumsum(0)])
+        run = torch.cat([torch.zeros(1, dtype=torch.long, device=pos.device), (ids[1:n] != ids[:max(n, 1) - 1]).long().cumsum(0)])
         ok = ok & (p >= 0) & (run[pos.clamp(0)][:, None] == run[None, :n])
     return ok
 

@@ -484,6 +484,26 @@ def test_shared_prefix_at_decode_size(lib):
     run_prefix(4, 1, 2000, 8, 8, 2, lens=[0, 1, 8, 0])
 
 
+@pytest.mark.parametrize("sq,pre", [(2, 4000), (5, 256), (30, 20), (32, 1), (16, 129)])
+@pytest.mark.parametrize("cap,slopes", [(0.0, False), (30.0, True)])
+def test_shared_prefix_queries_inside_the_prefix(lib, sq, pre, cap, slopes):
+    """Fewer own keys than queries: the first queries sit inside the prefix, or before it, and see it up to themselves."""
+    run_prefix(4, sq, pre, 40, 8, 2, cap=cap, slopes=slopes, lens=[0, 1, sq - 1, sq])
+    run_prefix(3, sq, pre, 1, 8, 2, cap=cap, slopes=slopes)
+
+
+def test_shared_prefix_values_seen_by_some_queries(lib):
+    """Infinities in the prefix's last keys, which only the later queries see."""
+    q, kp, vp = rnd(2, 6, 8, 128), rnd(300, 2, 128, seed=2), rnd(300, 2, 128, seed=3)
+    k, v = rnd(2, 10, 2, 128, seed=4), rnd(2, 10, 2, 128, seed=5)
+    vp[297, 0, 5] = math.inf
+    kp[299, 1, 7] = math.nan
+    plan = binding.PrefixAttention(2, 6, 300, 10, 8, 2)
+    out, lse = plan.run(q, kp, vp, k, v, kv_len=i32([1, 10]))
+    plan.check()
+    R.compare(out, lse, R.attention(q, k, v, kv_len=[1, 10], k_prefix=kp, v_prefix=vp))
+
+
 def test_shared_prefix_garbage_behind_own_keys(lib):
     B, pre, skv = 3, 200, 64
     q, kp, vp = rnd(B, 1, 8, 128), rnd(pre, 2, 128, seed=2), rnd(pre, 2, 128, seed=3)
