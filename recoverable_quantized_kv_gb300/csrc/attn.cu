@@ -124,8 +124,16 @@ __global__ void __launch_bounds__(128) attn_combine_kernel(const __grid_constant
   float l = 0.f;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
   for (int s0 = 0; s0 < n; s0 += 8 * WARPS) {   // every warp knows the weights of these parts, and reads its eight
-    const float w = lane < 8 * WARPS && s0 + lane < n ? ex2(lse_of(s0 + lane) - mu) : 0.f;
-    l += w;
+    // -1: no such part, or one without keys for the row, which wrote no output.  A weight that underflows to 0 counts: what
+    // is infinite or NaN in a visible value stays so.
+    float w = -1.f;
+    if (lane < 8 * WARPS && s0 + lane < n) {
+      const float x = lse_of(s0 + lane);
+      if (x != -INFINITY) {
+        w = ex2(x - mu);
+        l += w;
+      }
+    }
     float4 o[8];
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
@@ -137,7 +145,7 @@ __global__ void __launch_bounds__(128) attn_combine_kernel(const __grid_constant
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
       const float ws = __shfl_sync(0xffffffffu, w, WARPS * k + warp);
-      if (s0 + WARPS * k + warp < n && ws != 0.f) {   // a part without keys for the row wrote no output (NaN weights go on)
+      if (!(ws < 0.f)) {   // a NaN weight goes on
         acc.x = fmaf(ws, o[k].x, acc.x);
         acc.y = fmaf(ws, o[k].y, acc.y);
         acc.z = fmaf(ws, o[k].z, acc.z);

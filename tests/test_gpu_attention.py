@@ -240,6 +240,20 @@ def test_masked_places_with_capped_scores(lib, slopes):
         assert torch.all((lse[b, rows, h].double() - ls[rows]).abs() <= el[rows] if torch.is_tensor(el) else el)
 
 
+@pytest.mark.parametrize("bad", [math.nan, math.inf])
+def test_visible_values_of_vanishing_weight_propagate(lib, bad):
+    """A bias of 1 a key leaves keys 3000 back a weight of 0 in fp32; 0 times an infinity is NaN, in whichever part it lies."""
+    for sq, skv, at in ((1, 6000, 10), (1, 6000, 2990), (3, 700, 5)):
+        q, k, v = rnd(2, sq, 4, 128), rnd(2, skv, 2, 128, seed=2), rnd(2, skv, 2, 128, seed=3)
+        v[1, at, 0, 9] = bad
+        sl = torch.ones(4, device="cuda")
+        plan = binding.Attention(2, sq, skv, 4, 2)
+        out, lse = plan.run(q, k, v, slopes=sl)
+        plan.check()
+        assert not torch.isfinite(out[1, :, :2, 9]).any()
+        R.compare(out, lse, R.attention(q, k, v, slopes=sl))
+
+
 @pytest.mark.parametrize("cap", [0.0, 20.0])
 def test_visible_nan_scores_propagate(lib, cap):
     q, k, v = rnd(1, 4, 2, 128), rnd(1, 300, 1, 128, seed=2), rnd(1, 300, 1, 128, seed=3)
