@@ -268,7 +268,70 @@ __global__ void __launch_bounds__(VEC > 1 ? 256 : 1024) rope_apply_kernel(const 
   }
 }
 
+// Rotations whose pairs do not fall on whole vectors (37 pairs of a head, say) where heads still start on 16 bytes: a block
+// takes up to hc heads of one token through shared memory, in and out 16 bytes a thread, and turns them there pair by pair,
+// a lane's cosine and sine serving all the heads of its warp.  8192 tokens of 32 + 8 bf16 heads, 37 pairs: half layout 40 us
+// (167 by single loads and stores), interleaved 40 (51); fp32 65 (167) and 66 (55), so interleaved fp32, whose pairs are
+// 8 bytes each, is left to single loads.  24.7 and 49.4 at the rate of a copy.
+template <typename T>
+__global__ void __launch_bounds__(128) rope_staged_kernel(const __grid_constant__ RopeArgs A, int d, int hc, bool inter) {
+  extern __shared__ uint4 staged[];
+  constexpr int V = 16 / (int)sizeof(T);
+  const int64_t tok = blockIdx.x;
+  const uint32_t b = blockIdx.x / (uint32_t)A.seq, t = blockIdx.x - b * (uint32_t)A.seq;
+  const int64_t pos = A.pos ? (int64_t)A.pos[tok] : A.pos0 + t;
+  if (pos < 0 || pos >= A.rows) {   // no such table row: the token's heads are not written
+    if (threadIdx.x == 0) atomicOr(A.status, QV_ERR_BOUNDS);
+    return;
+  }
+  const int group = blockIdx.y;
+  const bool is_q = group < A.groups_q;
+  const int h0 = (is_q ? group : group - A.groups_q) * hc, n = min(hc, (is_q ? A.h_q : A.h_k) - h0);
+  const int64_t s2 = is_q ? A.qi[2] : A.ki[2], d2 = is_q ? A.qo_[2] : A.ko_[2];
+  const T *src = static_cast<const T *>(is_q ? A.q : A.k) + b * (is_q ? A.qi[0] : A.ki[0]) + t * (is_q ? A.qi[1] : A.ki[1]) +
+                 h0 * s2;
+  T *dst = static_cast<T *>(is_q ? A.qo : A.ko) + b * (is_q ? A.qo_[0] : A.ko_[0]) + t * (is_q ? A.qo_[1] : A.ko_[1]) + h0 * d2;
+  const int nu = d / V, h_first = threadIdx.x / nu, u_first = threadIdx.x - h_first * nu;
+  const int dh = blockDim.x / nu, du = blockDim.x - dh * nu;   // a block's step in heads and vectors
+  for (int h = h_first, u = u_first; h < n;) {
+    staged[h * nu + u] = *reinterpret_cast<const uint4 *>(src + h * s2 + u * V);
+    h += dh, u += du;
+    if (u >= nu) u -= nu, ++h;
+  }
+  __syncthreads();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  for (int i = lane; i < A.half; i += 32) {
+    const float2 cs = A.table[pos * A.half + i];
+    const float c = cs.x * A.f, s = cs.y * A.fs;
+    T *p = reinterpret_cast<T *>(staged) + warp * d + (inter ? 2 * i : i);
+    const int other = inter ? 1 : A.half;
+    for (int h = warp; h < n; h += 4, p += 4 * d) {
+      const float x1 = to_f(p[0]), x2 = to_f(p[other]);
+      p[0] = from_f<T>(fmaf(x1, c, -x2 * s));
+      p[other] = from_f<T>(fmaf(x2, c, x1 * s));
+    }
+  }
+  __syncthreads();
+  for (int h = h_first, u = u_first; h < n;) {
+    *reinterpret_cast<uint4 *>(dst + h * d2 + u * V) = staged[h * nu + u];
+    h += dh, u += du;
+    if (u >= nu) u -= nu, ++h;
+  }
+}
+
 namespace {
+
+template <typename T>
+bool launch_staged(RopeArgs &A, bool inter, int d_head, cudaStream_t s) {
+  const int bytes = d_head * (int)sizeof(T);
+  int hc = std::min(std::max(1, 8192 / bytes), std::max(A.h_q, A.h_k));
+  while (hc > 4 && A.tokens * ((A.h_q + A.h_k + hc - 1) / hc) < 304) hc = (hc + 1) / 2;   // few tokens: two blocks an SM
+  A.groups_q = (A.h_q + hc - 1) / hc;
+  const int64_t gy = A.groups_q + (A.h_k + hc - 1) / hc;
+  if (A.tokens > 0x7fffffffll || gy > 65535) return false;
+  rope_staged_kernel<T><<<dim3((unsigned)A.tokens, (unsigned)gy), 128, hc * bytes, s>>>(A, d_head, hc, inter);
+  return true;
+}
 
 // Block and grid for `units` vectors a head: a warp a block, four neighbouring heads a thread, so that a warp has 2 KB of
 // one place in flight, unless there are so few tokens that one head a thread does not fill the GPU.  A 32K prompt of
@@ -288,8 +351,9 @@ bool launch_apply(RopeArgs &A, int units, cudaStream_t s) {
   return true;
 }
 template <typename T>
-bool launch_apply_type(RopeArgs &A, bool vec, bool inter, int d_head, cudaStream_t s) {
+bool launch_apply_type(RopeArgs &A, bool vec, bool wide, bool inter, int d_head, cudaStream_t s) {
   constexpr int V = 16 / (int)sizeof(T);
+  if (!vec && wide && (!inter || sizeof(T) == 2)) return launch_staged<T>(A, inter, d_head, s);
   const int pass = d_head - 2 * A.half;
   if (inter) {
     A.pair_units = vec ? 2 * A.half / V : A.half;
@@ -457,10 +521,11 @@ qevict_status qevict_rope_apply(const qevict_rope_desc *d, const float *d_table,
   const int np = d->interleaved ? V / 2 : V;   // pairs of a full vector
   // full vectors need every start on 16 bytes, table rows (8 bytes a pair) included
   const bool vec = align == 0 && A.half % np == 0 && pass % V == 0 && (A.half % 2 == 0 || np == 1);
+  const bool wide = align == 0 && d->d_head % V == 0;   // heads, at least, are whole vectors
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  const bool ok = d->dtype == QEVICT_BF16   ? launch_apply_type<__nv_bfloat16>(A, vec, d->interleaved, d->d_head, s)
-                  : d->dtype == QEVICT_FP16 ? launch_apply_type<__half>(A, vec, d->interleaved, d->d_head, s)
-                                            : launch_apply_type<float>(A, vec, d->interleaved, d->d_head, s);
+  const bool ok = d->dtype == QEVICT_BF16   ? launch_apply_type<__nv_bfloat16>(A, vec, wide, d->interleaved, d->d_head, s)
+                  : d->dtype == QEVICT_FP16 ? launch_apply_type<__half>(A, vec, wide, d->interleaved, d->d_head, s)
+                                            : launch_apply_type<float>(A, vec, wide, d->interleaved, d->d_head, s);
   if (!ok) return QEVICT_EINVAL;
   return cudaGetLastError() == cudaSuccess ? QEVICT_OK : QEVICT_ECUDA;
 }

@@ -125,6 +125,30 @@ def test_strides_and_in_place(lib):
     assert torch.all((rope.apply(one)[0].double() - w).abs() <= tol)
 
 
+@pytest.mark.parametrize("dtype", [BF, FP, F32])
+@pytest.mark.parametrize("inter", [False, True])
+@pytest.mark.parametrize("rot,d,tokens,hq", [(74, 128, 3, 40), (10, 1024, 2, 9), (2, 8, 5, 3), (126, 128, 400, 7)])
+def test_pairs_off_the_vectors(lib, dtype, inter, rot, d, tokens, hq):
+    """Heads on 16 bytes whose pairs are not: head-major in, in place, a position outside the table, a head count that is
+    no multiple of a block's."""
+    rope = binding.Rope(binding.rope_table(500, rot_dim=rot))
+    g = torch.Generator(device="cuda").manual_seed(rot + tokens)
+    q = torch.randn(2, hq, tokens, d, generator=g, device="cuda").to(dtype).transpose(1, 2)
+    k = torch.randn(2, tokens, 2, d, generator=g, device="cuda").to(dtype)
+    pos = torch.randint(0, 500, (2, tokens), generator=g, device="cuda", dtype=torch.int32)
+    wants = [apply_ref(x, rope.table, pos, inter, False, 0.75) for x in (q, k)]
+    outs = rope.apply(q, k, positions=pos, interleaved=inter, factor=0.75)
+    for got, x, (want, tol) in zip(outs, (q, k), wants):
+        assert torch.all((got.double() - want).abs() <= tol) and torch.equal(got[..., rot:], x[..., rot:])
+    pos[1, 1] = 500
+    before = q.clone(), k.clone()
+    rope.apply(q, k, positions=pos, interleaved=inter, factor=0.75, q_out=q, k_out=k)
+    for x, b, got in zip((q, k), before, outs):
+        assert torch.equal(x[1, 1], b[1, 1]) and torch.equal(x[0], got[0]) and torch.equal(x[1, 2:], got[1, 2:])
+    with pytest.raises(binding.QEvictError):
+        rope.check()
+
+
 def test_positions_outside_the_table(lib):
     """The token is not written and the status word says so; the other tokens are."""
     rope = binding.Rope(binding.rope_table(16))
