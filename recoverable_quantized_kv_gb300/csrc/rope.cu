@@ -63,7 +63,7 @@ __device__ __forceinline__ float2 cos_sin_turns(uint64_t ph) {
 // A thread owns N neighbouring pairs (N = 2: 16-byte stores) and walks down the rows.  The angle in turns is
 // p * turn[i] mod 2^64: whole turns fall away in the integer product, exactly, so a position of 2^31 still has an angle to
 // 2^-33 turns, and no fp64 is needed (whose rate would bound this kernel at ten times its write time); a step down adds
-// step * turn[i].  Bound by its arithmetic, 52 instructions for 8 bytes: 131072 rows of 64 pairs take 16.5 us, 71% of the
+// step * turn[i].  Bound by its arithmetic, 52 instructions for 8 bytes: 131200 rows of 64 pairs take 16.5 us, 71% of the
 // issue slots; writing them alone would take 9.9.
 template <int N>
 __global__ void __launch_bounds__(256) rope_table_kernel(const __grid_constant__ TableArgs A) {
