@@ -30,6 +30,7 @@ constexpr int AT_OFF_MISC = AT_OFF_BAR + AT_NBAR * 8;              // tmem addre
 constexpr int AT_OFF_ITEM = AT_OFF_MISC + 16;                     // work item ring
 constexpr int AT_SMEM = AT_OFF_ITEM + AT_ITEMS * 64;
 static_assert(AT_SMEM <= 232448, "one CTA per SM");
+constexpr int AT_PADDING = 0x7fffffff;                // end of the visible keys of a row that is none (others: up to 2^30)
 constexpr int AT_BAR_ALL = 1, AT_BAR_ROWS = 2;        // named barriers (of the four warps that share rows: 2 .. 5)
 
 struct AttnArgs {
@@ -842,7 +843,7 @@ __global__ void __launch_bounds__(AT_THREADS, 1) attn_kernel(const __grid_consta
         int b, i, h, prow;
         const bool valid = attn_row<STREAM>(P, I, slot, R, b, i, h, prow);
         S.any = __any_sync(0xffffffffu, valid);
-        S.lo = 0, S.hi = 1 << 30;   // padding rows take no masks: nothing reads what they compute
+        S.lo = 0, S.hi = AT_PADDING;   // padding rows take no masks: nothing reads what they compute
         S.m = -INFINITY, S.l = 0.f, S.pos = 0;
         if (valid) {
           if (prefix) {
@@ -874,20 +875,33 @@ __global__ void __launch_bounds__(AT_THREADS, 1) attn_kernel(const __grid_consta
       // tiles that every row sees whole
       const int clean_lo = (I.clean_lo + AT_TILE - 1) / AT_TILE, clean_hi = I.clean_hi / AT_TILE;
       // Capped products: y with y scale = cap tanh(v scale / cap), tanh(u) = u Q(u^2) with Q fitted at Chebyshev nodes, its
-      // coefficients scaled to take v: of degree 2 where no |u| of the warp's rows exceeds 0.25, the usual case, of degree
+      // coefficients scaled to take v: of degree 2 where no |u| of the warp's rows exceeds 0.25, of degree
       // 4 up to 0.6 (errors 1e-7 and 7e-8 of tanh in fp32).  Beyond, 1 - 2 / (1 + 2^(2 log2e u)) with one reciprocal for
       // two, 1 / a = b / (a b), where 2^60 bounds the exponentials so that the product stays finite.  A 4K prompt of 32
       // heads takes 99 us without a cap, 139 with one, bound by the FMA pipe's share of each step (158 with degree 4
       // alone, 173 by exponentials).
-      auto capped = [&](float *v, uint32_t see) {
-        float x0 = 0.f, x1 = 0.f;
+      // Which form a row takes depends on what it sees alone: in a partly masked tile each row goes by its visible keys; in the
+      // others, whose keys every row sees, the warp's rows agree, padding rows (whose queries may be anything) having no say.
+      auto capped = [&](auto masks, float *v, uint32_t see, bool valid) {
+        constexpr bool mixed = decltype(masks)::value;
+        auto largest = [&]() {   // |u| of the row's columns; a NaN is passed over, and propagates in every form
+          float x0 = 0.f, x1 = 0.f;
 #pragma unroll
-        for (int c = 0; c < AT_COLS; c += 4) {
-          x0 = max3(x0, fabsf(v[c]), fabsf(v[c + 1]));
-          x1 = max3(x1, fabsf(v[c + 2]), fabsf(v[c + 3]));
+          for (int c = 0; c < AT_COLS; c += 4) {
+            x0 = max3(x0, fabsf(v[c]), fabsf(v[c + 1]));
+            x1 = max3(x1, fabsf(v[c + 2]), fabsf(v[c + 3]));
+          }
+          return valid ? fmaxf(x0, x1) * P.cap_u : 0.f;
+        };
+        float most = largest();
+        if (mixed && see != ~0u && !(most <= 0.25f)) {   // without the hidden keys
+#pragma unroll
+          for (int c = 0; c < AT_COLS; ++c)
+            if (!(see & (1u << c))) v[c] = 0.f;
+          most = largest();
         }
-        const float most = fmaxf(x0, x1) * P.cap_u;
-        if (__all_sync(0xffffffffu, most <= 0.25f)) {
+        auto agreed = [&](bool x) { return mixed ? x : (bool)__all_sync(0xffffffffu, x); };
+        if (agreed(most <= 0.25f)) {
           const uint64_t q0 = pack_f2(P.cap_r[0], P.cap_r[0]), q1 = pack_f2(P.cap_r[1], P.cap_r[1]),
                          q2 = pack_f2(P.cap_r[2], P.cap_r[2]);
 #pragma unroll
@@ -895,7 +909,7 @@ __global__ void __launch_bounds__(AT_THREADS, 1) attn_kernel(const __grid_consta
             const uint64_t v2 = pack_f2(v[c], v[c + 1]), z = mul_f2(v2, v2);
             unpack_f2(v[c], v[c + 1], mul_f2(v2, fma_f2(z, fma_f2(z, q2, q1), q0)));
           }
-        } else if (__all_sync(0xffffffffu, most <= 0.6f)) {
+        } else if (!mixed && agreed(most <= 0.6f)) {   // (rows that differ in their form take turns: two forms are enough)
           const uint64_t q0 = pack_f2(P.cap_q[0], P.cap_q[0]), q1 = pack_f2(P.cap_q[1], P.cap_q[1]),
                          q2 = pack_f2(P.cap_q[2], P.cap_q[2]), q3 = pack_f2(P.cap_q[3], P.cap_q[3]),
                          q4 = pack_f2(P.cap_q[4], P.cap_q[4]);
@@ -907,13 +921,8 @@ __global__ void __launch_bounds__(AT_THREADS, 1) attn_kernel(const __grid_consta
           }
         } else {
           const float in = P.cap_u * 2.8853900817779268f;   // 2 log2 e
-          if (see != ~0u) {   // a NaN in a masked place stays out of its neighbour
 #pragma unroll
-            for (int c = 0; c < AT_COLS; ++c)
-              if (!(see & (1u << c))) v[c] = 0.f;
-          }
-#pragma unroll
-          for (int c = 0; c < AT_COLS; c += 2) {
+          for (int c = 0; c < AT_COLS; c += 2) {   // (hidden keys are 0 here, so no NaN of theirs reaches a neighbour)
             const float a = 1.f + ex2(min_nan(v[c] * in, 60.f)), b = 1.f + ex2(min_nan(v[c + 1] * in, 60.f));
             const float r = rcp_approx(a * b) * (-2.f * P.cap_s);
             v[c] = fmaf(b, r, P.cap_s);
@@ -956,7 +965,7 @@ __global__ void __launch_bounds__(AT_THREADS, 1) attn_kernel(const __grid_consta
           float base2 = 0.f;       // of every logit of the row in this tile
           float x0 = -INFINITY, x1;
           if (!none) {
-            if (CAP) capped(v, see);
+            if (CAP) capped(masks, v, see, S.hi != AT_PADDING);
             if (BIAS) {
               const float sl = P.scale_log2, d0 = (float)(S.pos - c0);
               if ((P.causal && !P.prefix_len) || __all_sync(0xffffffffu, d0 >= (float)(AT_COLS - 1))) {
