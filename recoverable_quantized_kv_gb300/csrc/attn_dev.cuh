@@ -30,6 +30,7 @@ constexpr int AT_OFF_MISC = AT_OFF_BAR + AT_NBAR * 8;              // tmem addre
 constexpr int AT_OFF_ITEM = AT_OFF_MISC + 16;                     // work item ring
 constexpr int AT_SMEM = AT_OFF_ITEM + AT_ITEMS * 64;
 static_assert(AT_SMEM <= 232448, "one CTA per SM");
+constexpr float AT_BIG = 8388608.f;                   // 2^23: fp32 numbers beyond are whole
 constexpr int AT_PADDING = 0x7fffffff;                // end of the visible keys of a row that is none (others: up to 2^30)
 constexpr int AT_BAR_ALL = 1, AT_BAR_ROWS = 2;        // named barriers (of the four warps that share rows: 2 .. 5)
 
@@ -401,9 +402,9 @@ __device__ __forceinline__ void attn_clean_values(const AttnItem &I, int t, uint
 }
 
 // The rows of one warp of a slot recomputed on the CUDA cores, every visible key of the item's own tiles in turn and no
-// masked value touched.  Reached when a value that some row of the item sees and another does not is an infinity or NaN:
-// the tensor-core product then ran with that value as 0.  Writes O (unnormalised), m, l of row r through `emit`, the
-// warp's lanes holding four channels each.
+// masked value touched.  Reached when a value that some row of the item sees and another does not is an infinity or NaN
+// (the tensor-core product then ran with that value as 0), and when the maximum of one of the rows is beyond AT_BIG.  Writes
+// O (unnormalised), m, l of row r through `emit`, the warp's lanes holding four channels each.
 template <bool FP16, bool STREAM, typename Emit>
 __device__ __forceinline__ void attn_exact_rows(const AttnArgs &P, const AttnItem &I, int slot, int warp, int lane, bool cap,
                                                 const Emit &emit) {
@@ -844,7 +845,7 @@ __global__ void __launch_bounds__(AT_THREADS, 1) attn_kernel(const __grid_consta
         const bool valid = attn_row<STREAM>(P, I, slot, R, b, i, h, prow);
         S.any = __any_sync(0xffffffffu, valid);
         S.lo = 0, S.hi = AT_PADDING;   // padding rows take no masks: nothing reads what they compute
-        S.m = -INFINITY, S.l = 0.f, S.pos = 0;
+        S.m = -AT_BIG, S.l = 0.f, S.pos = 0;
         if (valid) {
           if (prefix) {
             const int p = attn_prefix_pos(P, b, i);
@@ -930,6 +931,14 @@ __global__ void __launch_bounds__(AT_THREADS, 1) attn_kernel(const __grid_consta
           }
         }
       };
+      // The exponents are taken from unrounded logits, the maximum is rounded: beyond 2^24 the row's largest may come out as 2^-30
+      // or 2^30, or further.  Running maxima start at -AT_BIG, so that logits far below weigh nothing, and the warp's rows are
+      // recomputed from rounded logits when one has ended above AT_BIG, or sees keys and holds a sum l of 0.  (Rounding the
+      // logits as they come costs a prompt 6%.)  The four warps that share the rows hold the same maxima and sums.
+      auto far_out = [&](const Slot &S, float l) {
+        const bool sees = max(S.lo, (I.t_hi - I.n) * AT_TILE) < min(S.hi, I.t_hi * AT_TILE);
+        return (bool)__any_sync(0xffffffffu, S.hi != AT_PADDING && ((S.m > AT_BIG && S.m < INFINITY) || (l == 0.f && sees)));
+      };
       // One slot's S of key tile j (from the last) into probabilities; first: the slot's first tile
       auto step_of = [&](auto masks, const int slot, Slot &S, uint32_t &sc, int j, bool first) {
         // Some row does not see some key of the tile: a body of its own, since its branches in the common one cost a
@@ -997,7 +1006,7 @@ __global__ void __launch_bounds__(AT_THREADS, 1) attn_kernel(const __grid_consta
             x0 = fmaxf(max3(x0, v[AT_COLS - 2], v[AT_COLS - 1]), x1);
           }
           const float mx = fmaf(x0, scale2, base2);
-          const bool grow = mx > S.m + 8.f;   // also the first finite max (m = -inf)
+          const bool grow = mx > S.m + 8.f;   // also the first max
           int any;   // one barrier of the four warps: whether a row has grown in one of them
           asm volatile(
               "{\n .reg .pred p, q;\n setp.ne.s32 p, %1, 0;\n barrier.cta.red.or.aligned.pred q, %2, 128, p;\n"
@@ -1011,7 +1020,7 @@ __global__ void __launch_bounds__(AT_THREADS, 1) attn_kernel(const __grid_consta
             const float all = fmaxf(fmaxf(xch[row], xch[AT_TILE + row]), fmaxf(xch[2 * AT_TILE + row], xch[3 * AT_TILE + row]));
             float f = 1.f;
             if (all > S.m + 8.f) {
-              f = S.m == -INFINITY ? 0.f : ex2(S.m - all);
+              f = ex2(S.m - all);
               S.m = all;
             }
             S.l *= f;
@@ -1027,8 +1036,7 @@ __global__ void __launch_bounds__(AT_THREADS, 1) attn_kernel(const __grid_consta
               }
             }
           }
-          const float mu = S.m == -INFINITY ? 0.f : S.m;
-          const uint64_t mu2 = pack_f2(base2 - mu, base2 - mu);
+          const uint64_t mu2 = pack_f2(base2 - S.m, base2 - S.m);
           uint64_t sa = 0, sb = 0;
           uint32_t pk[16];
           if (none) {
@@ -1110,7 +1118,7 @@ __global__ void __launch_bounds__(AT_THREADS, 1) attn_kernel(const __grid_consta
           ++oc0;
           __syncwarp();
           tc_fence_after();
-          bad = bad_item[seq & 1] == (int)seq;
+          bad = bad_item[seq & 1] == (int)seq || far_out(slot ? S1 : S0, l);
         }
         const uint32_t to = tmem + ((uint32_t)(wq * 32) << 16) + 256 + 128 * slot + 64 * side;
         const bool any_row = slot ? S1.any : S0.any;
@@ -1167,23 +1175,25 @@ __global__ void __launch_bounds__(AT_THREADS, 1) attn_kernel(const __grid_consta
       if (slots > 1) whole_row(1, S1, oc1);
       __syncwarp();
       tc_fence_after();
-      const bool bad = I.n > 0 && bad_item[seq & 1] == (int)seq;
+      const bool bad_values = I.n > 0 && bad_item[seq & 1] == (int)seq;
       float *part_o = prefix ? P.pre_o : P.part_o, *part_l = prefix ? P.pre_l : P.part_l;
       const int64_t part_row = (int64_t)I.part * (prefix ? P.pre_rows : P.part_rows);
 #pragma unroll 1
       for (int slot = 0; slot < (pair ? 2 : 1); ++slot) {
-        const float m0 = slot ? S1.m : S0.m, l0 = slot ? S1.l : S0.l, m1 = join ? S1.m : -INFINITY, l1 = join ? S1.l : 0.f;
+        const float m0 = slot ? S1.m : S0.m, l0 = slot ? S1.l : S0.l, m1 = join ? S1.m : -AT_BIG, l1 = join ? S1.l : 0.f;
         const bool any_row = slot ? S1.any : S0.any;
         const uint32_t to = lane_base + 256 + 128 * slot;
         int b, i, h, prow;
         const bool valid = attn_row<STREAM>(P, I, slot, R, b, i, h, prow);
         if (!any_row) continue;
-        const float mm = fmaxf(m0, m1), mu = mm == -INFINITY ? 0.f : mm;
+        const float mu = fmaxf(m0, m1);
         const float w0 = join ? ex2(m0 - mu) : 1.f, w1 = join ? ex2(m1 - mu) : 0.f;
         const float lt = join ? l0 * w0 + l1 * w1 : l0;
         const float inv = lt == 0.f ? 0.f : rcp_approx(lt);   // an empty row is 0
         const float lse2 = lt == 0.f ? -INFINITY : mu + lg2_approx(lt);
-        if (!bad) {
+        Slot Sm = slot ? S1 : S0;
+        Sm.m = mu;
+        if (!bad_values && !(I.n > 0 && far_out(Sm, lt))) {
           if (valid && quarter == 0) {
             if (parts)
               part_l[part_row + prow] = lse2;

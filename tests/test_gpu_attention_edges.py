@@ -106,3 +106,58 @@ def test_capped_rows_do_not_feel_what_ran_before(lib, cap):
     step.check()
     for g in got[1:]:
         assert all(same_bits(x, y) for x, y in zip(g, got[0]))
+
+
+@pytest.mark.parametrize("dtype,size", [(FP, 1000), (FP, 5000), (FP, 6001), (FP, 12004), (FP, 60000), (BF, 8064), (BF, 20096), (BF, 24064),
+                                        (BF, 1e15)])
+@pytest.mark.parametrize("sq,skv", [(1, 500), (300, 300), (20, 9000)])
+@pytest.mark.parametrize("slopes", [False, True])
+def test_logits_whose_last_digit_is_large(lib, dtype, size, sq, skv, slopes):
+    """One key's logit is 10^7 and more, where fp32 numbers lie whole powers of two apart: the row is that key's value."""
+    q, k, v = rnd(1, sq, 4, 128, dtype=dtype), rnd(1, skv, 2, 128, seed=2, dtype=dtype), rnd(1, skv, 2, 128, seed=3, dtype=dtype)
+    q.fill_(size)
+    k.mul_(1e-3)
+    k[0, 0] = size
+    sl = torch.tensor([0.5, 0.25, 0.125, 0.0], device="cuda") if slopes else None
+    plan = binding.Attention(1, sq, skv, 4, 2, dtype=dtype)
+    out, lse = plan.run(q, k, v, slopes=sl)
+    plan.check()
+    assert torch.equal(out[0].view(sq, 2, 2, 128), v[0, 0][None, :, None].expand(sq, 2, 2, 128))
+    want = 128 * q[0, 0, 0, 0].double() ** 2 / math.sqrt(128)
+    # the product's running sum (128 roundings), its scale (2), the exponent's base and the logarithm's way back (3)
+    assert ((lse.double() - want).abs() <= 133 * 2.0 ** -24 * want + (0 if sl is None else 0.5 * skv)).all()
+
+
+@pytest.mark.parametrize("dtype", [BF, FP])
+def test_large_logits_of_both_signs(lib, dtype):
+    """Rows of every magnitude from 1 to 10^10 in one tile, with equal keys at the top: the mean of their values."""
+    s = 200
+    q, k, v = rnd(1, s, 2, 128, dtype=dtype), rnd(1, s, 1, 128, seed=2, dtype=dtype), rnd(1, s, 1, 128, seed=3, dtype=dtype)
+    q[0] = (torch.logspace(0, 4.5, s, device="cuda")[:, None, None] * torch.ones(2, 128, device="cuda")).to(dtype)
+    k[:] = -300.0
+    k[0, 0:9:4] = 300.0
+    plan = binding.Attention(1, s, s, 2, 1, dtype=dtype)
+    out, lse = plan.run(q, k, v)
+    plan.check()
+    for i in range(s):
+        top = v[0, 0:min(i, 8) + 1:4, 0].double()
+        # weights of 1 / 1, 1 / 2 or 1 / 3, rounded once each, and the output once
+        assert ((out[0, i].double() - top.mean(0)).abs() <= S.HALF[dtype] * (top.abs().mean(0) + top.mean(0).abs()) + 2.0 ** -22).all()
+
+
+def test_logits_from_far_below_to_far_above(lib):
+    """Tiles of logits of -10^9, 10^9, -10^7, 0 in every order along the keys: the largest that a row sees decides."""
+    s, size = 640, 10000.0
+    for dtype in (BF, FP):
+        q, k, v = rnd(1, s, 2, 128, dtype=dtype), rnd(1, s, 1, 128, seed=2, dtype=dtype), rnd(1, s, 1, 128, seed=3, dtype=dtype)
+        q.fill_(size)
+        for order in ((0, 1, 2, 3, 2), (1, 0, 3, 2, 0), (2, 0, 2, 0, 3), (3, 2, 0, 2, 1), (0, 2, 0, 2, 0)):
+            level = torch.tensor([-1e4, 1e4, -1e2, 0.0], device="cuda")[torch.tensor(order, device="cuda").repeat_interleave(128)]
+            k[0, :, 0] = level[:, None].to(dtype)
+            plan = binding.Attention(1, s, s, 2, 1, dtype=dtype)
+            out, lse = plan.run(q, k, v)
+            plan.check()
+            for i in range(0, s, 61):
+                vv = v[0, :i + 1, 0][level[:i + 1] == level[:i + 1].max()].double()
+                tol = S.HALF[dtype] * (vv.abs().mean(0) + vv.mean(0).abs()) + (len(vv) + 64) * 2.0 ** -24 * vv.abs().mean(0) + 2.0 ** -24
+                assert ((out[0, i].double() - vv.mean(0)).abs() <= tol).all(), (order, i)
