@@ -73,8 +73,8 @@ __global__ void __launch_bounds__(RUN_THREADS) doc_runs_kernel(const int *ids, i
   }
 }
 
-// WARPS warps per row (sequence, query, head): out = sum_s 2^(lse_s - L) out_s over the parts of the row's units, L their
-// log2-sum-exp; 512 bytes per part and row, read once, eight loads of a warp at a time.  Which parts a row has is worked out
+// WARPS warps per row (sequence, query, head): out = sum_s w_s out_s / sum_s w_s over the parts of the row's units, with
+// w_s = l_s 2^(m_s - max m); 520 bytes per part and row, read once, eight loads of a warp at a time.  Which parts a row has is worked out
 // as the attention kernel did, before that kernel is waited for.  Four warps a row where rows are few: latency.  A thread
 // without work waits too: what follows in the stream is ordered behind this kernel, and through it behind that one.
 template <bool FP16, int WARPS>
@@ -114,11 +114,14 @@ __global__ void __launch_bounds__(128) attn_combine_kernel(const __grid_constant
   }
   const int n = n_pre + n_own;
   attn_wait_previous();
-  auto lse_of = [&](int s) {
+  auto sum_of = [&](int s) {   // (m, l)
     return s < n_pre ? P.pre_l[pre_row + (int64_t)s * P.pre_rows] : P.part_l[own_row + (int64_t)(s - n_pre) * P.part_rows];
   };
   float mx = -INFINITY;
-  for (int s = lane; s < n; s += 32) mx = fmaxf(mx, lse_of(s));
+  for (int s = lane; s < n; s += 32) {
+    const float2 ml = sum_of(s);
+    if (ml.y != 0.f) mx = fmaxf(mx, ml.x);
+  }
   for (int o = 16; o; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
   const float mu = mx == -INFINITY ? 0.f : mx;
   float l = 0.f;
@@ -128,9 +131,9 @@ __global__ void __launch_bounds__(128) attn_combine_kernel(const __grid_constant
     // is infinite or NaN in a visible value stays so.
     float w = -1.f;
     if (lane < 8 * WARPS && s0 + lane < n) {
-      const float x = lse_of(s0 + lane);
-      if (x != -INFINITY) {
-        w = ex2(x - mu);
+      const float2 ml = sum_of(s0 + lane);
+      if (ml.y != 0.f) {
+        w = ml.y * ex2(ml.x - mu);
         l += w;
       }
     }
@@ -288,13 +291,13 @@ qevict_status attn_plan(const qevict_attn_desc *d, int s_prefix, AttnPlan *p) {
   if (p->stream) {
     p->part_rows = std::min(d->s_q, 2 * p->tpt) * p->G;
     const int64_t parts = p->grid + units;
-    p->off_l = take(parts * p->part_rows * 4);
+    p->off_l = take(parts * p->part_rows * 8);
     p->off_o = take(parts * p->part_rows * D * 4);
   }
   if (s_prefix) {
     p->pre_rows = std::min(d->batch, 2 * p->nb) * d->s_q * p->G;
     const int64_t parts = p->grid + (int64_t)p->n_prp * d->h_kv;
-    p->off_pl = take(parts * p->pre_rows * 4);
+    p->off_pl = take(parts * p->pre_rows * 8);
     p->off_po = take(parts * p->pre_rows * D * 4);
   }
   p->bytes = off;
@@ -376,9 +379,9 @@ qevict_status attn_launch(const qevict_attn_desc *d, const AttnPlan &pl, const q
     if (cudaGetLastError() != cudaSuccess) return QEVICT_ECUDA;
   }
   if (pl.stream) {
-    A.part_l = reinterpret_cast<float *>(w + pl.off_l);
+    A.part_l = reinterpret_cast<float2 *>(w + pl.off_l);
     A.part_o = reinterpret_cast<float *>(w + pl.off_o);
-    A.pre_l = reinterpret_cast<float *>(w + pl.off_pl);
+    A.pre_l = reinterpret_cast<float2 *>(w + pl.off_pl);
     A.pre_o = reinterpret_cast<float *>(w + pl.off_po);
   }
   const auto launch = d->softcap > 0.f ? (fp16 ? launch_attn_fp16_cap : launch_attn_bf16_cap)

@@ -40,8 +40,12 @@ struct AttnArgs {
   const void *k, *v, *q, *kp, *vp;
   void *out;
   float *lse;
-  float *part_o, *part_l;      // own keys: [part][row][128], [part][row] (log2 domain)
-  float *pre_o, *pre_l;        // the same of the prefix
+  // Own keys, [part][row]: output [128], and (m, l) with maximum m (log2 domain) and sum l of 2^(x - m), 0 where the row sees no
+  // key.  One number m + log2 l would lose l behind a maximum of 10^6.
+  float *part_o;
+  float2 *part_l;
+  float *pre_o;                // the same of the prefix
+  float2 *pre_l;
   int *status, *drawn;         // status word; units given out (whole units)
   const float *slopes;
   const int *q_len, *kv_len, *prefix_len;
@@ -1176,7 +1180,8 @@ __global__ void __launch_bounds__(AT_THREADS, 1) attn_kernel(const __grid_consta
       __syncwarp();
       tc_fence_after();
       const bool bad_values = I.n > 0 && bad_item[seq & 1] == (int)seq;
-      float *part_o = prefix ? P.pre_o : P.part_o, *part_l = prefix ? P.pre_l : P.part_l;
+      float *part_o = prefix ? P.pre_o : P.part_o;
+      float2 *part_l = prefix ? P.pre_l : P.part_l;
       const int64_t part_row = (int64_t)I.part * (prefix ? P.pre_rows : P.part_rows);
 #pragma unroll 1
       for (int slot = 0; slot < (pair ? 2 : 1); ++slot) {
@@ -1190,15 +1195,15 @@ __global__ void __launch_bounds__(AT_THREADS, 1) attn_kernel(const __grid_consta
         const float w0 = join ? ex2(m0 - mu) : 1.f, w1 = join ? ex2(m1 - mu) : 0.f;
         const float lt = join ? l0 * w0 + l1 * w1 : l0;
         const float inv = lt == 0.f ? 0.f : rcp_approx(lt);   // an empty row is 0
-        const float lse2 = lt == 0.f ? -INFINITY : mu + lg2_approx(lt);
         Slot Sm = slot ? S1 : S0;
         Sm.m = mu;
         if (!bad_values && !(I.n > 0 && far_out(Sm, lt))) {
           if (valid && quarter == 0) {
             if (parts)
-              part_l[part_row + prow] = lse2;
+              part_l[part_row + prow] = make_float2(mu, lt);
             else if (P.lse)
-              P.lse[((int64_t)b * P.s_q + i) * P.h_q + h] = lse2 * 0.69314718055994531f;
+              P.lse[((int64_t)b * P.s_q + i) * P.h_q + h] =
+                  lt == 0.f ? -INFINITY : (mu + lg2_approx(lt)) * 0.69314718055994531f;
           }
           const bool have0 = I.n > 0;
           const float f0 = w0 * inv, f1 = w1 * inv;
@@ -1231,7 +1236,7 @@ __global__ void __launch_bounds__(AT_THREADS, 1) attn_kernel(const __grid_consta
               uint32_t o[16];
               take(q, o);
               float *dst = part_o + (part_row + prow) * D + AT_COLS * quarter + 16 * q;
-              if (valid && lse2 != -INFINITY) {
+              if (valid && lt != 0.f) {
                 st_global_v8(dst, o);
                 st_global_v8(dst + 8, o + 8);
               }
@@ -1253,14 +1258,14 @@ __global__ void __launch_bounds__(AT_THREADS, 1) attn_kernel(const __grid_consta
           attn_exact_rows<FP16, true>(P, I, slot, wq, lane, CAP,
                                 [&](int rb, int ri, int rh, int rp, const float (&acc)[4], float rm, float rl) {
             const float ri_l = rl == 0.f ? 0.f : 1.f / rl;
-            const float ls = rl == 0.f ? -INFINITY : rm + log2f(rl);
             const float o0 = rl == 0.f ? 0.f : acc[0] * ri_l, o1 = rl == 0.f ? 0.f : acc[1] * ri_l;
             const float o2 = rl == 0.f ? 0.f : acc[2] * ri_l, o3 = rl == 0.f ? 0.f : acc[3] * ri_l;
             if (parts) {
-              if (lane == 0) part_l[part_row + rp] = ls;
+              if (lane == 0) part_l[part_row + rp] = make_float2(rm, rl);
               *reinterpret_cast<float4 *>(part_o + (part_row + rp) * D + 4 * lane) = make_float4(o0, o1, o2, o3);
             } else {
-              if (lane == 0 && P.lse) P.lse[((int64_t)rb * P.s_q + ri) * P.h_q + rh] = ls * 0.69314718055994531f;
+              if (lane == 0 && P.lse)
+                P.lse[((int64_t)rb * P.s_q + ri) * P.h_q + rh] = rl == 0.f ? -INFINITY : (rm + log2f(rl)) * 0.69314718055994531f;
               *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(P.out) + rb * P.so[0] + ri * P.so[1] + rh * P.so[2] +
                                          4 * lane) = make_uint2(pack2<FP16>(o0, o1), pack2<FP16>(o2, o3));
             }

@@ -161,3 +161,32 @@ def test_logits_from_far_below_to_far_above(lib):
                 vv = v[0, :i + 1, 0][level[:i + 1] == level[:i + 1].max()].double()
                 tol = S.HALF[dtype] * (vv.abs().mean(0) + vv.mean(0).abs()) + (len(vv) + 64) * 2.0 ** -24 * vv.abs().mean(0) + 2.0 ** -24
                 assert ((out[0, i].double() - vv.mean(0)).abs() <= tol).all(), (order, i)
+
+
+@pytest.mark.parametrize("dtype,size", [(FP, 300), (FP, 1000), (FP, 6001), (FP, 60000), (BF, 300), (BF, 20096), (BF, 1e15)])
+@pytest.mark.parametrize("sq,skv", [(1, 300), (300, 300), (7, 9000), (200, 9000)])
+@pytest.mark.parametrize("one", [None, 0, -1])
+def test_logits_far_below_zero(lib, dtype, size, sq, skv, one):
+    """Every key's logit is -10^6 and less: the mean of the visible values; one key of logit 0 among them: that key's value."""
+    q, k, v = rnd(1, sq, 4, 128, dtype=dtype), rnd(1, skv, 2, 128, seed=2, dtype=dtype), rnd(1, skv, 2, 128, seed=3, dtype=dtype)
+    q.fill_(size)
+    k.fill_(-size)
+    if one is not None:
+        k[0, one] = 0
+    plan = binding.Attention(1, sq, skv, 4, 2, dtype=dtype)
+    out, lse = plan.run(q, k, v)
+    plan.check()
+    want = -128 * q[0, 0, 0, 0].double() ** 2 / math.sqrt(128)
+    for i in sorted({0, sq // 2, sq - 1}):
+        n = skv - sq + i + 1
+        hit = one is not None and (one == 0 or i == sq - 1)
+        for h in range(4):
+            vv = v[0, one if one == 0 else skv - 1, h // 2][None].double() if hit else v[0, :n, h // 2].double()
+            # equal weights, each rounded by half a step, and the output; n sums; parts' sums of weights, log2 n of them lost
+            # behind a maximum of -10^6 and less are not: parts of equal maxima weigh by their sums
+            tol = S.HALF[dtype] * (vv.abs().mean(0) + vv.mean(0).abs()) + (n + 64) * 2.0 ** -24 * vv.abs().mean(0) + 2.0 ** -24
+            assert ((out[0, i, h].double() - vv.mean(0)).abs() <= tol).all(), (i, h)
+            if hit:
+                assert abs(lse[0, i, h].item()) <= 2.0 ** -20
+            else:
+                assert abs(lse[0, i, h].item() - want.item() - math.log(n)) <= 140 * 2.0 ** -24 * abs(want.item())
