@@ -447,7 +447,8 @@ qevict_status qevict_rope_apply(const qevict_rope_desc *desc, const float *d_tab
  * position 0 then sees nothing).  A row that sees nothing gets out = 0, lse = -inf.  What stands in
  * invisible keys and values (infinities, NaN) does not reach a row; visible ones propagate.  Rows behind
  * q_len[b] are not written.  Softmax statistics and sums are fp32; the probabilities are rounded to the
- * input type for the product with the values, and the output once.
+ * input type for the product with the values (fp16 ones hold weights down to 2^-32 of a row's largest), and
+ * the output once.
  * Results do not change from run to run.  out and lse may share no bytes with the inputs. */
 typedef struct {
   int32_t dtype;                           /* QEVICT_BF16 or QEVICT_FP16, of q, k, v and out */

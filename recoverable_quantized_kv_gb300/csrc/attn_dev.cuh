@@ -497,7 +497,8 @@ __device__ __forceinline__ void attn_exact_rows(const AttnArgs &P, const AttnIte
 // the softmax left out); single tokens by memory (16 of 32 heads against caches of 33K keys: 211 us, 6.7 TB/s).
 // Key tiles are taken from the last to the first, so a causal row meets its diagonal, and a distance bias its largest
 // logits, first.  The running max moves only when a row's max has grown by more than 2^8 (then the warps rescale their
-// rows of O in tensor memory): until then p reaches at most 2^8, which fp32 sums and 16-bit probabilities hold as well.
+// rows of O in tensor memory): until then p reaches at most 2^8 of its scale, which fp32 sums and 16-bit probabilities hold
+// as well.
 // Every wait is bounded; the TMEM columns are released on every path.
 // STREAM = false: whole units, always as pairs (of a last odd row tile the second is empty).
 template <bool FP16, bool CAP, bool BIAS, bool STREAM>
@@ -939,6 +940,9 @@ __global__ void __launch_bounds__(AT_THREADS, 1) attn_kernel(const __grid_consta
       // or 2^30, or further.  Running maxima start at -AT_BIG, so that logits far below weigh nothing, and the warp's rows are
       // recomputed from rounded logits when one has ended above AT_BIG, or sees keys and holds a sum l of 0.  (Rounding the
       // logits as they come costs a prompt 6%.)  The four warps that share the rows hold the same maxima and sums.
+      // fp16 holds 2^-24 to 2^15 of a power of two: the reference m is the maximum less 7, so that a row's largest probability
+      // lies between 2^7 and 2^15, and what is lost below 2^-25 is below 2^-32 of it.  (bf16 has fp32's exponents.)
+      constexpr float LIFT = FP16 ? 7.f : 0.f, RISE = 8.f + LIFT;
       auto far_out = [&](const Slot &S, float l) {
         const bool sees = max(S.lo, (I.t_hi - I.n) * AT_TILE) < min(S.hi, I.t_hi * AT_TILE);
         return (bool)__any_sync(0xffffffffu, S.hi != AT_PADDING && ((S.m > AT_BIG && S.m < INFINITY) || (l == 0.f && sees)));
@@ -1010,7 +1014,7 @@ __global__ void __launch_bounds__(AT_THREADS, 1) attn_kernel(const __grid_consta
             x0 = fmaxf(max3(x0, v[AT_COLS - 2], v[AT_COLS - 1]), x1);
           }
           const float mx = fmaf(x0, scale2, base2);
-          const bool grow = mx > S.m + 8.f;   // also the first max
+          const bool grow = mx > S.m + RISE;   // also the first max
           int any;   // one barrier of the four warps: whether a row has grown in one of them
           asm volatile(
               "{\n .reg .pred p, q;\n setp.ne.s32 p, %1, 0;\n barrier.cta.red.or.aligned.pred q, %2, 128, p;\n"
@@ -1023,9 +1027,9 @@ __global__ void __launch_bounds__(AT_THREADS, 1) attn_kernel(const __grid_consta
             asm volatile("bar.sync %0, 128;" ::"r"(row_bar) : "memory");
             const float all = fmaxf(fmaxf(xch[row], xch[AT_TILE + row]), fmaxf(xch[2 * AT_TILE + row], xch[3 * AT_TILE + row]));
             float f = 1.f;
-            if (all > S.m + 8.f) {
-              f = ex2(S.m - all);
-              S.m = all;
+            if (all > S.m + RISE) {
+              f = ex2(S.m - (all - LIFT));
+              S.m = all - LIFT;
             }
             S.l *= f;
             if (!first) {

@@ -190,3 +190,40 @@ def test_logits_far_below_zero(lib, dtype, size, sq, skv, one):
                 assert abs(lse[0, i, h].item()) <= 2.0 ** -20
             else:
                 assert abs(lse[0, i, h].item() - want.item() - math.log(n)) <= 140 * 2.0 ** -24 * abs(want.item())
+
+
+# ------------------------------------------------------------------------------------------------ weights far below the largest
+
+def sink(dtype, skv, hkv, bits, at):
+    """Keys whose logit is 0 and one, at `at`, whose logit is bits * ln 2 and whose value is 0; the other values near 1."""
+    k, v = torch.zeros(1, skv, hkv, 128, dtype=dtype, device="cuda"), 1 + rnd(1, skv, hkv, 128, seed=3, dtype=dtype, gain=0.25)
+    k[0, at, :, 0] = bits * math.log(2)
+    v[0, at] = 0
+    return k, v
+
+
+@pytest.mark.parametrize("dtype", [BF, FP])
+@pytest.mark.parametrize("bits", [20.0, 24.5, 25.5, 28.0])
+@pytest.mark.parametrize("sq,skv", [(1, 60000), (1, 900), (300, 4096), (20, 60000)])
+def test_many_small_weights_beside_a_large_one(lib, dtype, bits, sq, skv):
+    """The last tokens see one key of weight 1 and thousands of weight 2^-bits, which together make the output."""
+    q = torch.zeros(1, sq, 4, 128, dtype=dtype, device="cuda")
+    q[..., 0] = 1.0
+    k, v = sink(dtype, skv, 2, bits, skv - sq)
+    plan = binding.Attention(1, sq, skv, 4, 2, dtype=dtype, scale=1.0)
+    out, lse = plan.run(q, k, v)
+    plan.check()
+    S.check(out, lse, q, k, v, scale=1.0, rows=sorted({0, sq // 2, sq - 1}))
+    assert (out[0, -1].float() > 0).all()
+
+
+@pytest.mark.parametrize("bits", [20.0, 25.5])
+def test_many_small_weights_behind_a_shared_prefix(lib, bits):
+    q = torch.zeros(3, 1, 4, 128, dtype=FP, device="cuda")
+    q[..., 0] = 1.0
+    kp, vp = (x[0] for x in sink(FP, 20000, 2, bits, 19990))
+    k, v = torch.zeros(3, 8, 2, 128, dtype=FP, device="cuda"), torch.ones(3, 8, 2, 128, dtype=FP, device="cuda")
+    plan = binding.PrefixAttention(3, 1, 20000, 8, 4, 2, dtype=FP, scale=1.0)
+    out, lse = plan.run(q, kp, vp, k, v)
+    plan.check()
+    S.check(out, lse, q, k, v, scale=1.0, k_prefix=kp, v_prefix=vp)
