@@ -16,7 +16,7 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 SOURCES = ["api.cu", "decode.cu", "route.cu", "scores.cu", "noalloc.cu", "diag.cu", "rope.cu", "attn.cu", "attn_bf16.cu",
-           "attn_bf16_cap.cu", "attn_fp16.cu", "attn_fp16_cap.cu"]
+           "attn_bf16_cap.cu", "attn_bf16_wide.cu", "attn_fp16.cu", "attn_fp16_cap.cu", "attn_fp16_wide.cu"]
 LIB = os.path.join(HERE, "libqevict.so")
 # the checked build: every index read from device data is tested before use (-DQEVICT_CHECK); an index
 # outside its buffer sets a bit of the device status word instead of being used

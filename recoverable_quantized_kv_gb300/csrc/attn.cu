@@ -16,6 +16,8 @@ cudaError_t launch_attn_bf16(const AttnArgs &P, int grid, bool bias, cudaStream_
 cudaError_t launch_attn_fp16(const AttnArgs &P, int grid, bool bias, cudaStream_t s);
 cudaError_t launch_attn_bf16_cap(const AttnArgs &P, int grid, bool bias, cudaStream_t s);
 cudaError_t launch_attn_fp16_cap(const AttnArgs &P, int grid, bool bias, cudaStream_t s);
+cudaError_t launch_attn_bf16_wide(const AttnArgs &P, int grid, bool bias, cudaStream_t s);
+cudaError_t launch_attn_fp16_wide(const AttnArgs &P, int grid, bool bias, cudaStream_t s);
 
 // First and past-the-last position of every position's run of equal ids.  One CTA per sequence; thread i takes the i-th of
 // 1024 consecutive pieces, finds the first and last run start in it, and scans over the warp and then over the warps carry
@@ -226,6 +228,10 @@ constexpr int MIN_TILES = 2;
 // against 1K keys take 16 us whole, 19 as parts; 64 of different lengths up to 1K 42 and 48 us.
 constexpr int WHOLE_TILES = 8;
 
+// Caps from here on take the instances that keep small logits exact beside large ones: the others' error of 2^-22 of the cap
+// is 2^-16 of a weight at 64.
+constexpr float WIDE_CAP = 64.f;
+
 bool stride_ok(int64_t st, int64_t size, bool zero) {
   if (size <= 1) return true;
   return st % 8 == 0 && st < (1ll << 38) && (st > 0 || (zero && st == 0));
@@ -354,12 +360,15 @@ qevict_status attn_launch(const qevict_attn_desc *d, const AttnPlan &pl, const q
   if (d->softcap > 0.f) {
     A.cap_u = scale / d->softcap;
     A.cap_s = d->softcap / scale;
-    const double q[5] = {0.9999999403953552, -0.33332324028015137, 0.13310357928276062, -0.052109625190496445,
-                         0.01548669021576643};
+    const double q[5] = {TANH_0, TANH_1, TANH_2, TANH_3, TANH_4};
     const double r[3] = {0.9999995827674866, -0.3332192897796631, 0.12841935455799103};
     const double u = A.cap_u;
     for (int i = 0; i < 5; ++i) A.cap_q[i] = (float)(q[i] * std::pow(u, 2 * i));
     for (int i = 0; i < 3; ++i) A.cap_r[i] = (float)(r[i] * std::pow(u, 2 * i));
+    // squares of products up to 0.6 of the cap stay finite below 2^62; the coefficients of higher powers may vanish there
+    const bool squares = A.cap_s <= 0x1p62f;
+    A.cap_near = squares ? 0.25f : -1.f;
+    A.cap_mid = squares ? 0.6f : -1.f;
   }
   const bool fp16 = d->dtype == QEVICT_FP16;
   const int qb = A.mul_q ? d->batch : 1, kb = A.mul_k ? d->batch : 1, vb = A.mul_v ? d->batch : 1;
@@ -384,8 +393,9 @@ qevict_status attn_launch(const qevict_attn_desc *d, const AttnPlan &pl, const q
     A.pre_l = reinterpret_cast<float2 *>(w + pl.off_pl);
     A.pre_o = reinterpret_cast<float *>(w + pl.off_po);
   }
-  const auto launch = d->softcap > 0.f ? (fp16 ? launch_attn_fp16_cap : launch_attn_bf16_cap)
-                                       : (fp16 ? launch_attn_fp16 : launch_attn_bf16);
+  const auto launch = d->softcap > WIDE_CAP ? (fp16 ? launch_attn_fp16_wide : launch_attn_bf16_wide)
+                      : d->softcap > 0.f    ? (fp16 ? launch_attn_fp16_cap : launch_attn_bf16_cap)
+                                            : (fp16 ? launch_attn_fp16 : launch_attn_bf16);
   if (launch(A, pl.grid, m.slopes != nullptr, s) != cudaSuccess) return QEVICT_ECUDA;
   if (pl.stream) {
     cudaLaunchConfig_t cfg = {};

@@ -3,6 +3,6 @@
 
 namespace qv {
 cudaError_t launch_attn_bf16_cap(const AttnArgs &P, int grid, bool bias, cudaStream_t s) {
-  return bias ? launch_attn_variant<false, true, true>(P, grid, s) : launch_attn_variant<false, true, false>(P, grid, s);
+  return bias ? launch_attn_variant<false, 1, true>(P, grid, s) : launch_attn_variant<false, 1, false>(P, grid, s);
 }
 }  // namespace qv

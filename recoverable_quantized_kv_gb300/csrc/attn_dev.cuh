@@ -30,6 +30,9 @@ constexpr int AT_OFF_MISC = AT_OFF_BAR + AT_NBAR * 8;              // tmem addre
 constexpr int AT_OFF_ITEM = AT_OFF_MISC + 16;                     // work item ring
 constexpr int AT_SMEM = AT_OFF_ITEM + AT_ITEMS * 64;
 static_assert(AT_SMEM <= 232448, "one CTA per SM");
+// tanh(u) / u in powers of u^2 up to |u| = 0.6
+constexpr double TANH_0 = 0.9999999403953552, TANH_1 = -0.33332324028015137, TANH_2 = 0.13310357928276062,
+                 TANH_3 = -0.052109625190496445, TANH_4 = 0.01548669021576643;
 constexpr float AT_BIG = 8388608.f;                   // 2^23: fp32 numbers beyond are whole
 constexpr int AT_PADDING = 0x7fffffff;                // end of the visible keys of a row that is none (others: up to 2^30)
 constexpr int AT_BAR_ALL = 1, AT_BAR_ROWS = 2;        // named barriers (of the four warps that share rows: 2 .. 5)
@@ -61,6 +64,7 @@ struct AttnArgs {
   float scale_log2;            // logit scale * log2 e
   float cap_u, cap_s;          // softcap: scale / cap, cap / scale
   float cap_q[5], cap_r[3];    // tanh(u) / u in powers of the product's square, u = product * cap_u: to 0.6, to 0.25
+  float cap_near, cap_mid;     // the |u| up to which they serve: 0.25 and 0.6, or below 0 (never)
 };
 
 __device__ __forceinline__ int clampi(int x, int lo, int hi) { return x < lo ? lo : x > hi ? hi : x; }
@@ -500,8 +504,9 @@ __device__ __forceinline__ void attn_exact_rows(const AttnArgs &P, const AttnIte
 // rows of O in tensor memory): until then p reaches at most 2^8 of its scale, which fp32 sums and 16-bit probabilities hold
 // as well.
 // Every wait is bounded; the TMEM columns are released on every path.
-// STREAM = false: whole units, always as pairs (of a last odd row tile the second is empty).
-template <bool FP16, bool CAP, bool BIAS, bool STREAM>
+// STREAM = false: whole units, always as pairs (of a last odd row tile the second is empty).  CAP: 0 none, 1 up to 64, 2 wider
+// (instances of their own: its code in the others costs capped prompts 2%).
+template <bool FP16, int CAP, bool BIAS, bool STREAM>
 __global__ void __launch_bounds__(AT_THREADS, 1) attn_kernel(const __grid_constant__ AttnArgs P) {
   extern __shared__ __align__(1024) uint8_t sm[];   // swizzle atoms: 1024-aligned
   uint64_t *bars = reinterpret_cast<uint64_t *>(sm + AT_OFF_BAR);
@@ -900,14 +905,14 @@ __global__ void __launch_bounds__(AT_THREADS, 1) attn_kernel(const __grid_consta
           return valid ? fmaxf(x0, x1) * P.cap_u : 0.f;
         };
         float most = largest();
-        if (mixed && see != ~0u && !(most <= 0.25f)) {   // without the hidden keys
+        if (mixed && see != ~0u && !(most <= P.cap_near)) {   // without the hidden keys
 #pragma unroll
           for (int c = 0; c < AT_COLS; ++c)
             if (!(see & (1u << c))) v[c] = 0.f;
           most = largest();
         }
         auto agreed = [&](bool x) { return mixed ? x : (bool)__all_sync(0xffffffffu, x); };
-        if (agreed(most <= 0.25f)) {
+        if (agreed(most <= P.cap_near)) {
           const uint64_t q0 = pack_f2(P.cap_r[0], P.cap_r[0]), q1 = pack_f2(P.cap_r[1], P.cap_r[1]),
                          q2 = pack_f2(P.cap_r[2], P.cap_r[2]);
 #pragma unroll
@@ -915,7 +920,7 @@ __global__ void __launch_bounds__(AT_THREADS, 1) attn_kernel(const __grid_consta
             const uint64_t v2 = pack_f2(v[c], v[c + 1]), z = mul_f2(v2, v2);
             unpack_f2(v[c], v[c + 1], mul_f2(v2, fma_f2(z, fma_f2(z, q2, q1), q0)));
           }
-        } else if (!mixed && agreed(most <= 0.6f)) {   // (rows that differ in their form take turns: two forms are enough)
+        } else if (!mixed && agreed(most <= P.cap_mid)) {   // (rows that differ in their form take turns: two forms are enough)
           const uint64_t q0 = pack_f2(P.cap_q[0], P.cap_q[0]), q1 = pack_f2(P.cap_q[1], P.cap_q[1]),
                          q2 = pack_f2(P.cap_q[2], P.cap_q[2]), q3 = pack_f2(P.cap_q[3], P.cap_q[3]),
                          q4 = pack_f2(P.cap_q[4], P.cap_q[4]);
@@ -927,22 +932,43 @@ __global__ void __launch_bounds__(AT_THREADS, 1) attn_kernel(const __grid_consta
           }
         } else {
           const float in = P.cap_u * 2.8853900817779268f;   // 2 log2 e
-#pragma unroll
-          for (int c = 0; c < AT_COLS; c += 2) {   // (hidden keys are 0 here, so no NaN of theirs reaches a neighbour)
-            const float a = 1.f + ex2(min_nan(v[c] * in, 60.f)), b = 1.f + ex2(min_nan(v[c + 1] * in, 60.f));
+          auto pair_of = [&](float &x, float &y) {   // (hidden keys are 0 here, so no NaN of theirs reaches a neighbour)
+            const float a = 1.f + ex2(min_nan(x * in, 60.f)), b = 1.f + ex2(min_nan(y * in, 60.f));
             const float r = rcp_approx(a * b) * (-2.f * P.cap_s);
-            v[c] = fmaf(b, r, P.cap_s);
-            v[c + 1] = fmaf(a, r, P.cap_s);
+            x = fmaf(b, r, P.cap_s);
+            y = fmaf(a, r, P.cap_s);
+          };
+          if (CAP == 2) {
+            // The difference from cap_s is off by about 2^-22 of the cap, which small logits of a wide cap would feel: up to
+            // 0.6 the polynomial of u itself.
+            auto near = [&](float x, float far) {
+              const float u = x * P.cap_u, z = u * u;
+              float y = fmaf(z, (float)TANH_4, (float)TANH_3);
+              y = fmaf(z, y, (float)TANH_2);
+              y = fmaf(z, y, (float)TANH_1);
+              y = fmaf(z, y, (float)TANH_0);
+              return fabsf(u) <= 0.6f ? u * y * P.cap_s : far;
+            };
+#pragma unroll
+            for (int c = 0; c < AT_COLS; c += 2) {
+              float x = v[c], y = v[c + 1];
+              pair_of(x, y);
+              v[c] = near(v[c], x);
+              v[c + 1] = near(v[c + 1], y);
+            }
+          } else {
+#pragma unroll
+            for (int c = 0; c < AT_COLS; c += 2) pair_of(v[c], v[c + 1]);
           }
         }
       };
+      // fp16 holds 2^-24 to 2^15 of a power of two: the reference m is the maximum less 7, so that a row's largest probability
+      // lies between 2^7 and 2^15, and what is lost below 2^-25 is below 2^-32 of it.  (bf16 has fp32's exponents.)
+      constexpr float LIFT = FP16 ? 7.f : 0.f, RISE = 8.f + LIFT;
       // The exponents are taken from unrounded logits, the maximum is rounded: beyond 2^24 the row's largest may come out as 2^-30
       // or 2^30, or further.  Running maxima start at -AT_BIG, so that logits far below weigh nothing, and the warp's rows are
       // recomputed from rounded logits when one has ended above AT_BIG, or sees keys and holds a sum l of 0.  (Rounding the
       // logits as they come costs a prompt 6%.)  The four warps that share the rows hold the same maxima and sums.
-      // fp16 holds 2^-24 to 2^15 of a power of two: the reference m is the maximum less 7, so that a row's largest probability
-      // lies between 2^7 and 2^15, and what is lost below 2^-25 is below 2^-32 of it.  (bf16 has fp32's exponents.)
-      constexpr float LIFT = FP16 ? 7.f : 0.f, RISE = 8.f + LIFT;
       auto far_out = [&](const Slot &S, float l) {
         const bool sees = max(S.lo, (I.t_hi - I.n) * AT_TILE) < min(S.hi, I.t_hi * AT_TILE);
         return (bool)__any_sync(0xffffffffu, S.hi != AT_PADDING && ((S.m > AT_BIG && S.m < INFINITY) || (l == 0.f && sees)));
@@ -1303,7 +1329,7 @@ cudaError_t launch_attn_kernel(Kernel kern, const AttnArgs &P, int grid, cudaStr
   return cudaLaunchKernelEx(&cfg, kern, P);
 }
 
-template <bool FP16, bool CAP, bool BIAS>
+template <bool FP16, int CAP, bool BIAS>
 cudaError_t launch_attn_variant(const AttnArgs &P, int grid, cudaStream_t s) {
   static SmemOptIn units, stream;
   cudaError_t e = P.stream ? stream.ensure(attn_kernel<FP16, CAP, BIAS, true>, AT_SMEM)

@@ -3,6 +3,6 @@
 
 namespace qv {
 cudaError_t launch_attn_fp16_cap(const AttnArgs &P, int grid, bool bias, cudaStream_t s) {
-  return bias ? launch_attn_variant<true, true, true>(P, grid, s) : launch_attn_variant<true, true, false>(P, grid, s);
+  return bias ? launch_attn_variant<true, 1, true>(P, grid, s) : launch_attn_variant<true, 1, false>(P, grid, s);
 }
 }  // namespace qv

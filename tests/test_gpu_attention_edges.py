@@ -108,6 +108,35 @@ def test_capped_rows_do_not_feel_what_ran_before(lib, cap):
         assert all(same_bits(x, y) for x, y in zip(g, got[0]))
 
 
+@pytest.mark.parametrize("dtype", [BF, FP])
+@pytest.mark.parametrize("cap", [64.0, 1000.0, 1e5])
+@pytest.mark.parametrize("sq,skv", [(1, 700), (200, 200)])
+def test_large_caps_keep_small_logits(lib, dtype, cap, sq, skv):
+    """Heads whose logits reach past the cap beside heads of ordinary ones, in one tile: the ordinary ones keep their digits."""
+    q, k, v = rnd(1, sq, 4, 128, dtype=dtype), rnd(1, skv, 1, 128, seed=2, dtype=dtype), rnd(1, skv, 1, 128, seed=3, dtype=dtype)
+    q *= 0.1
+    q[:, :, 0] *= cap / 4.5      # logits of deviation 11.3 * 0.1, and a quarter of the cap
+    plan = binding.Attention(1, sq, skv, 4, 1, dtype=dtype, softcap=cap, scale=1.0)
+    out, lse = plan.run(q, k, v)
+    plan.check()
+    S.check(out, lse, q, k, v, cap=cap, scale=1.0, rows=[0] if sq == 1 else [0, 1, 31, 32, 63, 100, 199])
+
+
+@pytest.mark.parametrize("top", [2.0 ** 20, 2.0 ** 33, 2.0 ** 40])
+@pytest.mark.parametrize("cap", [2.0 ** 61, 2.0 ** 70, 2.0 ** 90, 2.0 ** 99])
+@pytest.mark.parametrize("sq", [1, 300])
+def test_caps_near_the_largest(lib, top, cap, sq):
+    """One key of every row's product is 128 top^2, far above the others: the row is that key's value."""
+    q, k, v = rnd(1, sq, 4, 128), rnd(1, 300, 2, 128, seed=2), rnd(1, 300, 2, 128, seed=3)
+    q.fill_(top)
+    k[0, 0] = top
+    plan = binding.Attention(1, sq, 300, 4, 2, softcap=cap, scale=1.0)
+    out, lse = plan.run(q, k, v)
+    plan.check()
+    S.check(out, lse, q, k, v, cap=cap, scale=1.0, rows=range(0, sq, 37))
+    assert torch.equal(out[0, -1].view(2, 2, 128), v[0, 0][:, None].expand(2, 2, 128))
+
+
 @pytest.mark.parametrize("dtype,size", [(FP, 1000), (FP, 5000), (FP, 6001), (FP, 12004), (FP, 60000), (BF, 8064), (BF, 20096), (BF, 24064),
                                         (BF, 1e15)])
 @pytest.mark.parametrize("sq,skv", [(1, 500), (300, 300), (20, 9000)])
