@@ -406,7 +406,8 @@ typedef struct {
 /* theta_i of every pair, host fp64 [rot_dim / 2].  Host only. */
 qevict_status qevict_rope_angles(const qevict_rope_config *cfg, double *theta);
 /* d_table: fp32 [rows][rot_dim / 2][2], row r = (cos, sin) of position first + r, each within 2^-23 of the
- * exact value of position * theta_i.  With rot_dim = 128 and first = 0 it is the table of qevict_set_rope_table.
+ * exact value of position * theta_i, for every position and theta_i (as qevict_rope_angles gives it) up to 2^40.
+ * With rot_dim = 128 and first = 0 it is the table of qevict_set_rope_table.
  * 8-byte aligned; 0 <= first, 1 <= rows, first + rows <= 2^31. */
 qevict_status qevict_rope_table(const qevict_rope_config *cfg, int64_t first, int64_t rows, float *d_table,
                                 qevict_stream_t stream);

@@ -438,12 +438,12 @@ qevict_status qevict_rope_table(const qevict_rope_config *cfg, int64_t first, in
   A.first = first;
   A.rows = rows;
   A.out = reinterpret_cast<float2 *>(d_table);
-  const double two_pi = 6.283185307179586476925286766559;
+  // theta / (2 pi) in two doubles, off by about 2^-104 of it: up to theta = 2^40 the 64-bit fraction is off by one at most
+  const double inv = 0.15915494309189535, inv_low = -9.839338337591243e-18;   // 1 / (2 pi) = inv + inv_low
   for (int i = 0; i < A.pairs; ++i) {
-    const double turns = std::fmod(theta[i] / two_pi, 1.0);   // whole turns per position change nothing
-    // split so that the product below 2^64 stays exact in a double
-    const double hi = std::floor(std::ldexp(turns, 32)), lo = std::ldexp(turns, 32) - hi;
-    A.turn[i] = ((uint64_t)hi << 32) + (uint64_t)std::floor(std::ldexp(lo, 32));
+    const double hi = theta[i] * inv, lo = std::fma(theta[i], inv, -hi) + theta[i] * inv_low;
+    // whole turns per position change nothing and fall away exactly; lo may be negative, its low bit is dropped
+    A.turn[i] = (uint64_t)std::ldexp(hi - std::floor(hi), 64) + ((uint64_t)std::llround(std::ldexp(lo - std::rint(lo), 63)) << 1);
   }
   const bool two = A.pairs % 2 == 0 && ((uintptr_t)d_table & 15) == 0;
   const int groups = two ? A.pairs / 2 : A.pairs;
