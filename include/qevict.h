@@ -499,7 +499,8 @@ qevict_status qevict_prefix_attn(const qevict_prefix_attn_desc *desc, const floa
                                  qevict_stream_t stream);
 
 /* The status word at d_status (the one of qevict_rope_apply, or the start of an attention workspace):
- * synchronises `stream`, copies the word to *host_word (may be NULL) and clears it.  QEVICT_EDEVICE if it was set. */
+ * synchronises `stream`, the one that the calls ran on, copies the word to *host_word (may be NULL) and clears it if it
+ * was set, which is QEVICT_EDEVICE. */
 qevict_status qevict_ops_status(void *d_status, int32_t *host_word, qevict_stream_t stream);
 
 /* Frees the host handle (the arena stays the caller's). */

@@ -19,6 +19,8 @@ COUNTER_NAMES = ("promotions", "demotions", "first_quant", "reactivations", "evi
 
 
 class QEvictError(RuntimeError):
+    word = 0   # of a status check that found bits set: those bits
+
     def __init__(self, status: int, where: str, msg: str):
         super().__init__(f"{where}: {msg} (status {status})")
         self.status = status
@@ -469,9 +471,18 @@ def _settled(t):
                 torch.cuda.current_stream().synchronize()
 
 
-def _ops_status(word, where, stream):
+_TIMEOUT = 1   # bit of a status word: a wait ran out
+
+
+def _ops_status(word, stream):
+    """Synchronises the stream and raises if the status word was set (cleared then); the error has it as `word`."""
     s, other = _enter(word.get_device(), stream, (word,))
-    _call("qevict_ops_status", other, (word.data_ptr(), None, s))
+    bits = ctypes.c_int32()
+    try:
+        _call("qevict_ops_status", other, (word.data_ptr(), ctypes.byref(bits), s))
+    except QEvictError as e:
+        e.word = bits.value
+        raise
 
 
 def _rope_config(rot_dim, base, scaling, factor, orig_len, low, high):
@@ -583,8 +594,9 @@ class Rope:
         return self._descs[key]
 
     def check(self, stream=None):
-        """Raises EDEVICE if a call since the last check met a position outside the table (synchronises)."""
-        _ops_status(self.status, "Rope.check", stream)
+        """Raises EDEVICE if a call since the last check met a position outside the table.  Synchronises `stream` (the
+        current one unless given): the one that the calls ran on."""
+        _ops_status(self.status, stream)
 
 
 class _AttnPlan:
@@ -647,12 +659,14 @@ class _AttnPlan:
 
     def check(self, stream=None):
         """Raises EDEVICE if a call since the last check recorded a fault: a length outside its range (clamped), or
-        a wait that ran out (synchronises)."""
+        a wait that ran out.  Synchronises `stream` (the current one unless given): the one that the calls ran on."""
         try:
-            _ops_status(self.work, type(self).__name__ + ".check", stream)
-        except QEvictError:
-            self.work[:256].zero_()   # a wait that ran out leaves the count behind it undone
-            _settled(self.work)
+            _ops_status(self.work, stream)
+        except QEvictError as e:
+            if e.word & _TIMEOUT:   # which leaves the count of units undone; no call is under way now
+                with _torch().cuda.stream(stream):
+                    self.work[:256].zero_()
+                    _settled(self.work)
             raise
 
 

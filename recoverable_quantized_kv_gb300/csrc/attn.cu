@@ -474,7 +474,10 @@ qevict_status qevict_ops_status(void *d_status, int32_t *host_word, qevict_strea
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   int word = 0;
   if (cudaMemcpyAsync(&word, d_status, sizeof(int), cudaMemcpyDeviceToHost, s) != cudaSuccess ||
-      cudaMemsetAsync(d_status, 0, sizeof(int), s) != cudaSuccess || cudaStreamSynchronize(s) != cudaSuccess)
+      cudaStreamSynchronize(s) != cudaSuccess)
+    return QEVICT_ECUDA;
+  // cleared only where it was set: a bit that another stream's call sets after a clean read stays for the next one
+  if (word && (cudaMemsetAsync(d_status, 0, sizeof(int), s) != cudaSuccess || cudaStreamSynchronize(s) != cudaSuccess))
     return QEVICT_ECUDA;
   if (host_word) *host_word = word;
   return word ? QEVICT_EDEVICE : QEVICT_OK;

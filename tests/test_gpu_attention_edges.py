@@ -256,3 +256,31 @@ def test_many_small_weights_behind_a_shared_prefix(lib, bits):
     out, lse = plan.run(q, kp, vp, k, v)
     plan.check()
     S.check(out, lse, q, k, v, scale=1.0, k_prefix=kp, v_prefix=vp)
+
+
+# ------------------------------------------------------------------------------------------------ plans
+
+def test_a_report_leaves_the_count_of_units_alone(lib):
+    """Only a wait that ran out leaves the count undone.  A clamped length does not, and a call on another stream may be drawing
+    from the count while the word is read."""
+    q, k, v = rnd(2, 600, 8, 128), rnd(2, 600, 2, 128, seed=2), rnd(2, 600, 2, 128, seed=3)
+    plan = binding.Attention(2, 600, 600, 8, 2)
+    plan.run(q, k, v, kv_len=i32([601, 600]))
+    plan.work[128:132] = torch.tensor([3, 0, 0, 0], dtype=torch.uint8)   # as if a call were under way
+    with pytest.raises(binding.QEvictError) as e:
+        plan.check()
+    assert e.value.status == binding.EDEVICE
+    assert e.value.word == 8 and plan.work[128].item() == 3 and not plan.work[:4].any()
+
+
+def test_a_status_is_reported_once(lib):
+    """Reported once, then clean."""
+    plan = binding.Attention(1, 1, 100, 4, 2)
+    rope = binding.Rope(binding.rope_table(16))
+    for word, check in ((plan.work[:4], plan.check), (rope.status.view(torch.uint8)[:4], rope.check)):
+        check()
+        word[0] = 8
+        with pytest.raises(binding.QEvictError):
+            check()
+        assert not word.any()
+        check()
