@@ -409,19 +409,32 @@ def _tensor(t, where, name, shape, dtype, device, dense=False):
         _need(t.shape[-1] == 1 or t.stride(-1) == 1, where, f"{name}'s channels must be contiguous")
 
 
-def _enter(device_index, stream, tensors):
+def _enter(device_index, stream, tensors, home=None, own=()):
     """The raw stream of a call on a device, and the device to make current for it (None: it is).  Tensors used on
-    another stream than the device's current one are made known to the allocator."""
+    another stream than the device's current one are made known to the allocator, and so are the operator's `own`, which
+    its caller does not see, on any stream but the one they were made on, `home`."""
     torch = _torch()
     other = None if torch.cuda.current_device() == device_index else torch.device("cuda", device_index)
     if stream is None:
-        return torch._C._cuda_getCurrentRawStream(device_index), other
+        raw = torch._C._cuda_getCurrentRawStream(device_index)
+        if own and raw != home:
+            for t in own:
+                t.record_stream(torch.cuda.current_stream(device_index))
+        return raw, other
     _need(stream.device.index == device_index, "stream", f"{stream} is not on the tensors' device cuda:{device_index}")
     if stream != torch.cuda.current_stream(device_index):
         for t in tensors:
             if t is not None:
                 t.record_stream(stream)
+    if stream.cuda_stream != home:
+        for t in own:
+            t.record_stream(stream)
     return stream.cuda_stream, other
+
+
+def _home(index):
+    """The raw stream that new tensors of a device belong to."""
+    return _torch()._C._cuda_getCurrentRawStream(index)
 
 
 def _call(name, other, args):
@@ -531,6 +544,8 @@ class Rope:
         self.index = table.get_device()
         self.status = torch.zeros(1, dtype=torch.int32, device=table.device)
         _settled(self.status)
+        self._home, self._own = _home(self.index), (table, self.status)
+        table.record_stream(torch.cuda.current_stream(self.index))   # it may have been made on another
         self._table_ptr, self._status_ptr, self._descs = table.data_ptr(), self.status.data_ptr(), {}
 
     def apply(self, q, k=None, positions=None, pos0=0, interleaved=False, inverse=False, factor=1.0, q_out=None,
@@ -559,7 +574,7 @@ class Rope:
             _tensor(k_out, "Rope.apply", "k_out", k.shape, dt, self.table.device)
         if positions is not None:
             _array("Rope.apply", "positions", positions, shape[:2], _torch().int32, index)
-        st, other = _enter(index, stream, (q, k, q_out, k_out, positions, self.table, self.status))
+        st, other = _enter(index, stream, (q, k, q_out, k_out, positions), self._home, self._own)
         _call("qevict_rope_apply", other,
               (desc, self._table_ptr, None if positions is None else positions.data_ptr(), q.data_ptr(), q_out.data_ptr(),
                None if k is None else k.data_ptr(), None if k is None else k_out.data_ptr(), self._status_ptr, st))
@@ -623,6 +638,7 @@ class _AttnPlan:
         _settled(self.work)
         d = self.desc
         self.index, self._descs = self.work.get_device(), {}
+        self._home, self._own = _home(self.index), (self.work,)
         self._work = (self.work.data_ptr(), nbytes)
         self.q_shape, self.kv_shape = (d.batch, d.s_q, d.h_q, 128), (d.batch, d.s_kv, d.h_kv, 128)
 
@@ -696,7 +712,7 @@ class Attention(_AttnPlan):
                                          _array(where, "kv_len", kv_len, batch, i32, i),
                                          _array(where, "prefix_len", prefix_len, batch, i32, i),
                                          _array(where, "doc_ids", doc_ids, (d.batch, d.s_kv), i32, i)))
-        s, other = _enter(i, stream, (q, k, v, out, lse, slopes, q_len, kv_len, prefix_len, doc_ids, self.work))
+        s, other = _enter(i, stream, (q, k, v, out, lse, slopes, q_len, kv_len, prefix_len, doc_ids), self._home, self._own)
         _call("qevict_attn", other, (desc, mask, q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), lse.data_ptr(),
                                      *self._work, s))
         return out, lse
@@ -725,7 +741,7 @@ class PrefixAttention(_AttnPlan):
         if not (_fits(k_prefix, self.prefix_shape, self.dtype, i) and _fits(v_prefix, self.prefix_shape, self.dtype, i)):
             for name, t in (("k_prefix", k_prefix), ("v_prefix", v_prefix)):
                 _tensor(t, where, name, self.prefix_shape, self.dtype, self.device)
-        s, other = _enter(i, stream, (q, k_prefix, v_prefix, k, v, out, lse, slopes, kv_len, self.work))
+        s, other = _enter(i, stream, (q, k_prefix, v_prefix, k, v, out, lse, slopes, kv_len), self._home, self._own)
         _call("qevict_prefix_attn", other,
               (desc, _array(where, "slopes", slopes, (d.h_q,), _torch().float32, i),
                _array(where, "kv_len", kv_len, self.q_shape[:1], _torch().int32, i), q.data_ptr(), k_prefix.data_ptr(),

@@ -284,3 +284,28 @@ def test_a_status_is_reported_once(lib):
             check()
         assert not word.any()
         check()
+
+
+@pytest.mark.parametrize("given", [False, True])
+def test_a_plan_dropped_while_its_call_runs(lib, given):
+    """A plan made on one stream and used on another, as the current one or by name: its workspace is not handed to the first
+    stream while the call runs."""
+    side = torch.cuda.Stream()
+    q, k, v = rnd(2, 1, 8, 128), rnd(2, 3000, 2, 128, seed=2), rnd(2, 3000, 2, 128, seed=3)
+    table = binding.rope_table(4000)
+    torch.cuda.synchronize()
+    for make in (lambda: binding.Attention(2, 1, 3000, 8, 2), lambda: binding.PrefixAttention(2, 1, 3000, 3000, 8, 2),
+                 lambda: binding.Rope(table)):
+        plan = make()
+        own = plan.status if isinstance(plan, binding.Rope) else plan.work
+        at, size = own.data_ptr(), own.numel() * own.element_size()
+        args = {"Attention": (q, k, v), "PrefixAttention": (q, k[0], v[0], k, v), "Rope": (q, k[:, :1])}[type(plan).__name__]
+        with torch.cuda.stream(side):
+            torch.cuda._sleep(200_000_000)   # about 0.1 s
+            outs = plan.run(*args, stream=side if given else None) if hasattr(plan, "run") else \
+                plan.apply(*args, stream=side if given else None)
+        del plan, own
+        others = [torch.empty(size, dtype=torch.uint8, device="cuda") for _ in range(4)]
+        assert at not in [x.data_ptr() for x in others]
+        torch.cuda.synchronize()
+        del outs, others
