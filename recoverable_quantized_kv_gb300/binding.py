@@ -469,6 +469,13 @@ def _array(where, name, t, shape, dtype, index):
     return t.data_ptr()
 
 
+def _no_graph(where, tensors):
+    """Refuses inputs that ask for a gradient: no graph is recorded, and the outputs would silently have none."""
+    for t in tensors:
+        if t is not None and t.requires_grad and _torch().is_grad_enabled():
+            raise QEvictError(EINVAL, where, "no gradient is recorded: call under torch.no_grad(), or with detached tensors")
+
+
 def _fits(t, shape, dtype, index):
     """Fast form of _tensor's checks but for the strides (a descriptor made for them has passed): true when all hold."""
     return t.shape == shape and t.dtype is dtype and t.get_device() == index
@@ -553,8 +560,10 @@ class Rope:
         """Rotates q [batch][seq][heads][d] and, if given, k; returns (q_out, k_out), new tensors unless given
         (q_out=q rotates in place).  positions: int32 [batch][seq], default pos0 + t.  inverse=True rotates back
         and, with the same factor, is the gradient of the forward call.  Tokens whose position is outside the
-        table are not written; check() reports them."""
+        table are not written; check() reports them.  Nothing is recorded for autograd: q and k that require a gradient
+        are refused unless gradients are off."""
         index = self.index
+        _no_graph("Rope.apply", (q, k))
         if k is None:
             _need(k_out is None, "Rope.apply", "k_out without k")
         if q_out is None or (k_out is None and k is not None):
@@ -701,7 +710,9 @@ class Attention(_AttnPlan):
     def run(self, q, k, v, out=None, lse=None, slopes=None, q_len=None, kv_len=None, prefix_len=None, doc_ids=None,
             stream=None):
         """q [batch][s_q][h_q][128], k, v [batch][s_kv][h_kv][128], any strides that are multiples of 8 elements;
-        returns (out, lse), new tensors unless given.  Rows behind q_len[b] are not written."""
+        returns (out, lse), new tensors unless given.  Rows behind q_len[b] are not written.  There is no backward pass:
+        inputs that require a gradient are refused unless gradients are off."""
+        _no_graph("Attention.run", (q, k, v, slopes))
         desc, out, lse = self._tensors("Attention.run", q, k, v, out, lse, stream)
         d, i, mask = self.desc, self.index, None
         if not (slopes is None and q_len is None and kv_len is None and prefix_len is None and doc_ids is None):
@@ -735,8 +746,10 @@ class PrefixAttention(_AttnPlan):
 
     def run(self, q, k_prefix, v_prefix, k, v, out=None, lse=None, slopes=None, kv_len=None, stream=None):
         """q [batch][s_q][h_q][128], k_prefix, v_prefix [s_prefix][h_kv][128], k, v [batch][s_kv][h_kv][128];
-        returns (out, lse), new tensors unless given."""
+        returns (out, lse), new tensors unless given.  Inputs that require a gradient are refused unless gradients are
+        off."""
         where, d, i = "PrefixAttention.run", self.desc, self.index
+        _no_graph(where, (q, k_prefix, v_prefix, k, v, slopes))
         desc, out, lse = self._tensors(where, q, k, v, out, lse, stream, (k_prefix.stride(), v_prefix.stride()))
         if not (_fits(k_prefix, self.prefix_shape, self.dtype, i) and _fits(v_prefix, self.prefix_shape, self.dtype, i)):
             for name, t in (("k_prefix", k_prefix), ("v_prefix", v_prefix)):

@@ -309,3 +309,24 @@ def test_a_plan_dropped_while_its_call_runs(lib, given):
         assert at not in [x.data_ptr() for x in others]
         torch.cuda.synchronize()
         del outs, others
+
+
+def test_gradients_are_refused(lib):
+    """No graph is recorded, so tensors that ask for one are refused; under no_grad, and detached, they are taken."""
+    q, k, v = rnd(1, 2, 4, 128), rnd(1, 9, 2, 128, seed=2), rnd(1, 9, 2, 128, seed=3)
+    plan, step = binding.Attention(1, 2, 9, 4, 2), binding.PrefixAttention(1, 2, 9, 9, 4, 2)
+    rope = binding.Rope(binding.rope_table(16))
+    sl = torch.ones(4, device="cuda")
+    calls = {"q": lambda: plan.run(q, k, v), "k": lambda: plan.run(q, k, v), "v": lambda: step.run(q, k[0], v[0], k, v),
+             "slopes": lambda: plan.run(q, k, v, slopes=sl), "rope": lambda: rope.apply(q, k[:, :2])}
+    for name, call in calls.items():
+        t = {"q": q, "k": k, "v": v, "slopes": sl, "rope": k}[name]
+        want = call()
+        t.requires_grad_()
+        with pytest.raises(binding.QEvictError) as e:
+            call()
+        assert e.value.status == binding.EINVAL
+        with torch.no_grad():
+            got = call()
+        t.requires_grad_(False)
+        assert all(torch.equal(x, y) for x, y in zip(want, got))
