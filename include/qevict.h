@@ -415,7 +415,8 @@ qevict_status qevict_rope_table(const qevict_rope_config *cfg, int64_t first, in
 enum { QEVICT_BF16 = 0, QEVICT_FP16 = 1, QEVICT_FP32 = 2 };
 /* Rotates the heads of h_q queries and h_k keys per token (either may be 0, its pointers then NULL).
  * Strides are in elements, {batch, token, head}, channels contiguous; input strides may be 0 or in any
- * order, output strides may not put two elements in one place. */
+ * order, output strides may not put two elements in one place.  Refused (QEVICT_EINVAL): batch * seq from 2^31, strides
+ * above 2^40, a tensor that reaches 2^48 elements, more than 65535 groups of heads (h_q + h_k up to 65535 always pass). */
 typedef struct {
   int32_t dtype;        /* QEVICT_BF16, QEVICT_FP16, QEVICT_FP32 */
   int32_t batch, seq, h_q, h_k;
@@ -459,7 +460,9 @@ typedef struct {
   float scale;                             /* > 0; 0 = 1 / sqrt(d_head) */
   float softcap;                           /* 0 = none; otherwise 2^-14 to 2^100 times the scale */
   /* strides in elements, {batch, token, head}, channels contiguous: multiples of 8; a batch stride of q, k, v may be
-   * 0 (one cache for all); out's may not put two elements in one place */
+   * 0 (one cache for all); out's may not put two elements in one place.  Refused (QEVICT_EINVAL): s_q, s_kv above 2^30,
+   * strides from 2^38, a tensor that reaches 2^48 elements, and more than 2^24 units of work: batch * h_kv times
+   * the pairs of row tiles, ceil(ceil(s_q / floor(128 / (h_q / h_kv))) / 2) */
   int64_t q[3], k[3], v[3], o[3];
 } qevict_attn_desc;
 /* Optional device arrays, NULL = absent: kv_len absent = s_kv, q_len absent = s_q.  Lengths outside
@@ -485,7 +488,8 @@ qevict_status qevict_attn(const qevict_attn_desc *desc, const qevict_attn_mask *
  * prefix's keys are read once for all sequences.  Sequence b sees the s_prefix shared keys and its own
  * kv_len[b] keys, which follow them (key j at position s_prefix + j; the newest tokens' keys are among
  * them), causally: query i sits at position s_prefix + kv_len[b] - s_q + i.  Equal to qevict_attn over
- * the joined keys.  s_q * h_q / h_kv <= 128.  desc: s_kv is the room for own keys, causal must be 1. */
+ * the joined keys.  s_q * h_q / h_kv <= 128; s_prefix up to 2^30, at most 2^30 rows, and 2^30 key tiles of 128 over
+ * all units.  desc: s_kv is the room for own keys, causal must be 1. */
 typedef struct {
   qevict_attn_desc attn;
   int32_t s_prefix;            /* >= 1 */

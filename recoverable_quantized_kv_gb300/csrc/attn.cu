@@ -234,7 +234,7 @@ constexpr float WIDE_CAP = 64.f;
 
 bool stride_ok(int64_t st, int64_t size, bool zero) {
   if (size <= 1) return true;
-  return st % 8 == 0 && st < (1ll << 38) && (st > 0 || (zero && st == 0));
+  return st % 8 == 0 && st < (1ll << 38) && st <= (1ll << 48) / (size - 1) && (st > 0 || (zero && st == 0));
 }
 
 float logit_scale(const qevict_attn_desc *d) { return d->scale > 0.f ? d->scale : 1.f / std::sqrt((float)D); }
@@ -260,11 +260,11 @@ qevict_status attn_plan(const qevict_attn_desc *d, int s_prefix, AttnPlan *p) {
   *p = AttnPlan();
   p->G = d->h_q / d->h_kv;
   p->tpt = AT_TILE / p->G;
-  p->rows = (int64_t)d->batch * d->s_q * d->h_q;
   const int64_t sms = sm_count();
   const int64_t n_qt = (d->s_q + p->tpt - 1) / p->tpt, n_pr = (n_qt + 1) / 2, groups = n_pr * d->batch;
+  if (groups > (1 << 24) || groups * d->h_kv > (1 << 24)) return QEVICT_EINVAL;   // each factor first: no product wraps
   const int64_t units = groups * d->h_kv, tiles = (d->s_kv + AT_TILE - 1) / AT_TILE;
-  if (units > (1 << 24) || p->rows > (1ll << 38)) return QEVICT_EINVAL;
+  p->rows = (int64_t)d->batch * d->s_q * d->h_q;   // at most 256 a unit
   int64_t total = units * (tiles + AT_UNIT_COST);   // places of the stream, at most
   p->n_pr = (int)n_pr;
   if (s_prefix) {

@@ -328,7 +328,7 @@ bool launch_staged(RopeArgs &A, bool inter, int d_head, cudaStream_t s) {
   while (hc > 4 && A.tokens * ((A.h_q + A.h_k + hc - 1) / hc) < 304) hc = (hc + 1) / 2;   // few tokens: two blocks an SM
   A.groups_q = (A.h_q + hc - 1) / hc;
   const int64_t gy = A.groups_q + (A.h_k + hc - 1) / hc;
-  if (A.tokens > 0x7fffffffll || gy > 65535) return false;
+  if (gy > 65535) return false;
   rope_staged_kernel<T><<<dim3((unsigned)A.tokens, (unsigned)gy), 128, hc * bytes, s>>>(A, d_head, hc, inter);
   return true;
 }
@@ -342,7 +342,7 @@ bool launch_apply(RopeArgs &A, int units, cudaStream_t s) {
   const int ny = std::max(1, 32 / units), per = ny * (one ? 1 : 4);
   A.groups_q = (A.h_q + per - 1) / per;
   const int64_t gx = A.tokens, gy = A.groups_q + (A.h_k + per - 1) / per;
-  if (gx > 0x7fffffffll || gy > 65535) return false;
+  if (gy > 65535) return false;
   const dim3 grid((unsigned)gx, (unsigned)gy), block(units, ny);
   if (one)
     rope_apply_kernel<T, VEC, MODE, 1><<<grid, block, 0, s>>>(A);
@@ -469,7 +469,7 @@ qevict_status qevict_rope_apply(const qevict_rope_desc *d, const float *d_table,
   if (d->dtype < 0 || d->dtype > 2 || d->batch < 1 || d->seq < 1 || d->h_q < 0 || d->h_k < 0 || d->h_q + (int64_t)d->h_k < 1 ||
       d->d_head < 2 || d->d_head > 1024 || d->rot_dim < 2 || d->rot_dim > d->d_head || d->rot_dim % 2 ||
       d->rot_dim > 2 * MAX_PAIRS || d->interleaved < 0 || d->interleaved > 1 || d->inverse < 0 || d->inverse > 1 ||
-      d->h_q > (1 << 20) || d->h_k > (1 << 20) || !std::isfinite(d->factor) || d->table_rows < 1 || d->pos0 < 0)
+      d->h_q > (1 << 20) || d->h_k > (1 << 20) || (int64_t)d->batch * d->seq > 0x7fffffffll || !std::isfinite(d->factor) || d->table_rows < 1 || d->pos0 < 0)
     return QEVICT_EINVAL;
   if (!d_positions && (d->pos0 > d->table_rows || d->seq > d->table_rows - d->pos0)) return QEVICT_EINVAL;
   if ((d->h_q > 0) != (q_in != nullptr && q_out != nullptr) || (d->h_k > 0) != (k_in != nullptr && k_out != nullptr))
@@ -488,6 +488,7 @@ qevict_status qevict_rope_apply(const qevict_rope_desc *d, const float *d_table,
     for (int i = 0; i < 3; ++i) {
       if (si[i] < 0 || so[i] < 0 || si[i] > (1ll << 40) || so[i] > (1ll << 40)) return QEVICT_EINVAL;
       if (dim[i] > 1) {
+        if (std::max(si[i], so[i]) > (1ll << 48) / (dim[i] - 1)) return QEVICT_EINVAL;
         align |= (si[i] | so[i]) % V;
         same = same && si[i] == so[i];
       }
