@@ -330,3 +330,54 @@ def test_gradients_are_refused(lib):
             got = call()
         t.requires_grad_(False)
         assert all(torch.equal(x, y) for x, y in zip(want, got))
+
+
+# ------------------------------------------------------------------------------------------------ infinities and NaN that some rows see
+
+@pytest.mark.parametrize("dtype", [BF, FP])
+@pytest.mark.parametrize("bad", [math.nan, math.inf, -math.inf])
+@pytest.mark.parametrize("cap,slopes", [(0.0, False), (20.0, False), (0.0, True), (2.0, True)])
+def test_keys_that_some_rows_see(lib, dtype, bad, cap, slopes):
+    """A later token's key, one of another document and one behind the end hold infinities or NaN: the rows that do not see it
+    keep their bounds."""
+    s, n = 300, [270, 300]
+    q, k, v = rnd(2, s, 4, 128, dtype=dtype), rnd(2, s, 2, 128, seed=2, dtype=dtype), rnd(2, s, 2, 128, seed=3, dtype=dtype)
+    k[0, 200, 0, 3], k[1, 129, 1, 77], k[0, 270:], v[0, 270:] = bad, bad, bad, bad
+    sl = torch.tensor([0.5, 0.25, 0.125, 0.0], device="cuda") if slopes else None
+    arrays = dict(slopes=sl, kv_len=i32(n), q_len=i32(n))
+    plan = binding.Attention(2, s, s, 4, 2, dtype=dtype, softcap=cap)
+    some = [0, 1, 63, 127, 128, 129, 130, 199, 200, 201, 269]
+    out, lse = plan.run(q, k, v, **arrays)
+    S.check(out, lse, q, k, v, "later", rows=some, cap=cap, **arrays)
+    ids = torch.zeros(2, s, dtype=torch.int32, device="cuda")
+    ids[0, 150:], ids[1, 130:] = 1, 2
+    out, lse = plan.run(q, k, v, doc_ids=ids, **arrays)
+    S.check(out, lse, q, k, v, "documents", rows=some, cap=cap, doc_ids=ids, **arrays)
+    pl = i32([250, 40])
+    out, lse = plan.run(q, k, v, prefix_len=pl, **arrays)
+    S.check(out, lse, q, k, v, "prefix", rows=some, cap=cap, prefix_len=pl, **arrays)
+    full = binding.Attention(2, 7, s, 4, 2, dtype=dtype, causal=False, softcap=cap)
+    out, lse = full.run(q[:, :7], k, v, slopes=sl, kv_len=i32([200, 129]))
+    S.check(out, lse, q[:, :7], k, v, "not causal", causal=False, cap=cap, slopes=sl, kv_len=[200, 129])
+    plan.check()
+    full.check()
+
+
+@pytest.mark.parametrize("dtype", [BF, FP])
+@pytest.mark.parametrize("cap,slopes", [(0.0, False), (20.0, False), (0.0, True)])
+def test_shared_prefix_keys_and_values_that_some_queries_see(lib, dtype, cap, slopes):
+    """The prefix's last keys and values, and own ones of later drafted tokens, hold infinities or NaN."""
+    q, kp, vp = rnd(2, 6, 8, 128, dtype=dtype), rnd(300, 2, 128, seed=2, dtype=dtype), rnd(300, 2, 128, seed=3, dtype=dtype)
+    k, v = rnd(2, 10, 2, 128, seed=4, dtype=dtype), rnd(2, 10, 2, 128, seed=5, dtype=dtype)
+    vp[297, 0, 5] = math.inf
+    kp[299, 1, 7] = math.nan
+    sl = torch.tensor([2.0 ** -h for h in range(8)], device="cuda") if slopes else None
+    plan = binding.PrefixAttention(2, 6, 300, 10, 8, 2, dtype=dtype, softcap=cap)
+    for lens in ([1, 10], [0, 3]):
+        out, lse = plan.run(q, kp, vp, k, v, slopes=sl, kv_len=i32(lens))
+        S.check(out, lse, q, k, v, str(lens), cap=cap, slopes=sl, kv_len=lens, k_prefix=kp, v_prefix=vp)
+    kp, vp = rnd(300, 2, 128, seed=2, dtype=dtype), rnd(300, 2, 128, seed=3, dtype=dtype)
+    k[1, 7, 0, 9], v[0, 9, 1, 3] = -math.inf, math.nan
+    out, lse = plan.run(q, kp, vp, k, v, slopes=sl)
+    S.check(out, lse, q, k, v, "own", cap=cap, slopes=sl, k_prefix=kp, v_prefix=vp)
+    plan.check()
