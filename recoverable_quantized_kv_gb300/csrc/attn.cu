@@ -365,10 +365,10 @@ qevict_status attn_launch(const qevict_attn_desc *d, const AttnPlan &pl, const q
     const double u = A.cap_u;
     for (int i = 0; i < 5; ++i) A.cap_q[i] = (float)(q[i] * std::pow(u, 2 * i));
     for (int i = 0; i < 3; ++i) A.cap_r[i] = (float)(r[i] * std::pow(u, 2 * i));
-    // squares of products up to 0.6 of the cap stay finite below 2^62; the coefficients of higher powers may vanish there
-    const bool squares = A.cap_s <= 0x1p62f;
-    A.cap_near = squares ? 0.25f : -1.f;
-    A.cap_mid = squares ? 0.6f : -1.f;
+    // where the last coefficients are normal numbers: 0.128 u^4 and 0.0155 u^8 above 2^-126 (and so the squares of products up
+    // to the cap below 2^128)
+    A.cap_near = A.cap_s <= 0x1p30f ? 0.25f : -1.f;
+    A.cap_mid = A.cap_s <= 0x1p15f ? 0.6f : -1.f;
   }
   const bool fp16 = d->dtype == QEVICT_FP16;
   const int qb = A.mul_q ? d->batch : 1, kb = A.mul_k ? d->batch : 1, vb = A.mul_v ? d->batch : 1;

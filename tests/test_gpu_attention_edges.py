@@ -137,6 +137,31 @@ def test_caps_near_the_largest(lib, top, cap, sq):
     assert torch.equal(out[0, -1].view(2, 2, 128), v[0, 0][:, None].expand(2, 2, 128))
 
 
+@pytest.mark.parametrize("cap,scale", [(20.0, 0.0), (64.0, 0.0), (2000.0, 0.0), (3e4, 0.05), (1e6, 0.0), (1e9, 0.0), (2.0 ** 40, 1.0), (2.0 ** 99, 1.0),
+                                       (50.0, 1e-4), (50.0, 1e-9), (2.0 ** -13, 1.0)])
+@pytest.mark.parametrize("skv", [1, 200])
+def test_capped_logits_over_the_whole_range_of_caps(lib, cap, scale, skv):
+    """Rows of products from -1.5 to 1.5 times cap / scale against one key (behind it keys of the same rows that none sees): lse is
+    the capped logit."""
+    n, real = 1000, scale or 1 / math.sqrt(128)
+    top = cap / real
+    q, k = torch.zeros(1, n, 1, 128, dtype=BF, device="cuda"), torch.zeros(1, skv, 1, 128, dtype=BF, device="cuda")
+    b = 2.0 ** round(math.log2(top) / 2)
+    q[0, :, 0, 5] = (torch.linspace(-1.5, 1.5, n, device="cuda", dtype=torch.float64) * (top / b)).to(BF)
+    k[..., 5] = b
+    plan = binding.Attention(1, n, skv, 1, 1, causal=False, softcap=cap, scale=scale)
+    out, lse = plan.run(q, k, torch.ones_like(k), kv_len=i32([1]))
+    plan.check()
+    want = cap * torch.tanh(q[0, :, 0, 5].double() * b * (torch.tensor(scale or 0.0, dtype=torch.float32).double().item() or real) / cap)
+    # scale / cap, its product and the logarithm's two conversions are rounded (2^-22), tanh is off by up to 2^-20 of itself or, up
+    # to a cap of 64, by 8 * 2^-22 of the cap
+    tol = 2.0 ** -19 * want.abs() + 8 * 2.0 ** -22 * min(cap, 64.0)
+    assert ((lse[0, :, 0].double() - want).abs() <= tol).all()
+    # the one weight is 2^e, e the rounding of a maximum up to 10^6 (2^-4 there): rounded to bf16 against an unrounded sum, and
+    # the output once, half a step each
+    assert ((out.float() - 1).abs() <= 2 * S.HALF[BF]).all()
+
+
 @pytest.mark.parametrize("dtype,size", [(FP, 1000), (FP, 5000), (FP, 6001), (FP, 12004), (FP, 60000), (BF, 8064), (BF, 20096), (BF, 24064),
                                         (BF, 1e15)])
 @pytest.mark.parametrize("sq,skv", [(1, 500), (300, 300), (20, 9000)])
