@@ -886,11 +886,10 @@ __global__ void __launch_bounds__(AT_THREADS, 1) attn_kernel(const __grid_consta
       // tiles that every row sees whole
       const int clean_lo = (I.clean_lo + AT_TILE - 1) / AT_TILE, clean_hi = I.clean_hi / AT_TILE;
       // Capped products: y with y scale = cap tanh(v scale / cap), tanh(u) = u Q(u^2) with Q fitted at Chebyshev nodes, its
-      // coefficients scaled to take v: of degree 2 where no |u| of the warp's rows exceeds 0.25, of degree
-      // 4 up to 0.6 (errors 1e-7 and 7e-8 of tanh in fp32).  Beyond, 1 - 2 / (1 + 2^(2 log2e u)) with one reciprocal for
+      // coefficients scaled to take v: of degree 2 where no |u| of the warp's rows exceeds 0.25, of degree 4 up to 0.6 (errors 1e-7 and 7e-8 of tanh in fp32).  Beyond, 1 - 2 / (1 + 2^(2 log2e u)) with one reciprocal for
       // two, 1 / a = b / (a b), where 2^60 bounds the exponentials so that the product stays finite.  A 4K prompt of 32
-      // heads takes 99 us without a cap, 139 with one, bound by the FMA pipe's share of each step (158 with degree 4
-      // alone, 173 by exponentials).
+      // heads takes 99 us without a cap, 137 with one that no logit reaches a quarter of, 153, 175 and 192 with logits two, four
+      // and twelve times as large: bound by the FMA pipe's share of each step.
       // Which form a row takes depends on what it sees alone: in a partly masked tile each row goes by its visible keys; in the
       // others, whose keys every row sees, the warp's rows agree, padding rows (whose queries may be anything) having no say.
       auto capped = [&](auto masks, float *v, uint32_t see, bool valid) {
