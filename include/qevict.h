@@ -451,8 +451,8 @@ qevict_status qevict_rope_apply(const qevict_rope_desc *desc, const float *d_tab
  * q_len[b] are not written.  Softmax statistics and sums are fp32; the probabilities are rounded to the
  * input type for the product with the values (fp16 ones hold weights down to 2^-32 of a row's largest), and
  * the output once.
- * Results do not change from run to run, nor with what stands in places that a row does not see.  out and lse may
- * share no bytes with the inputs.
+ * Results do not change from run to run, nor, outside the slow cases below, with what stands in places that a row
+ * does not see.  out and lse may share no bytes with the inputs.
  * Slow, by a factor of hundreds for the rows concerned: values that are not finite and that some rows of a tile see and
  * others do not, and rows whose largest logit is beyond 5.8e6 or all of whose logits are below -5.8e6.  Such rows take
  * about 10 us a key for every 256; over some 400000 keys of a prompt the kernel's waits run out (bit 1 of the status word). */

@@ -76,9 +76,9 @@ __global__ void __launch_bounds__(RUN_THREADS) doc_runs_kernel(const int *ids, i
 }
 
 // WARPS warps per row (sequence, query, head): out = sum_s w_s out_s / sum_s w_s over the parts of the row's units, with
-// w_s = l_s 2^(m_s - max m); 520 bytes per part and row, read once, eight loads of a warp at a time.  Which parts a row has is worked out
-// as the attention kernel did, before that kernel is waited for.  Four warps a row where rows are few: latency.  A thread
-// without work waits too: what follows in the stream is ordered behind this kernel, and through it behind that one.
+// w_s = l_s 2^(m_s - max m); 520 bytes per part and row, read once, eight loads of a warp at a time.  Which parts a row has
+// is worked out as the attention kernel did, before that kernel is waited for.  Four warps a row where rows are few: latency.
+// A thread without work waits too: what follows in the stream is ordered behind this kernel, and through it behind that one.
 template <bool FP16, int WARPS>
 __global__ void __launch_bounds__(128) attn_combine_kernel(const __grid_constant__ AttnArgs P, int ctas) {
   const int lane = threadIdx.x & 31, warp = WARPS == 1 ? 0 : threadIdx.x >> 5;

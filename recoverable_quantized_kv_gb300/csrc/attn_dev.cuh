@@ -43,8 +43,8 @@ struct AttnArgs {
   const void *k, *v, *q, *kp, *vp;
   void *out;
   float *lse;
-  // Own keys, [part][row]: output [128], and (m, l) with maximum m (log2 domain) and sum l of 2^(x - m), 0 where the row sees no
-  // key.  One number m + log2 l would lose l behind a maximum of 10^6.
+  // Own keys, [part][row]: output [128], and (m, l) with maximum m (log2 domain) and sum l of 2^(x - m), 0 where the row sees
+  // no key.  One number m + log2 l would lose l behind a maximum of 10^6.
   float *part_o;
   float2 *part_l;
   float *pre_o;                // the same of the prefix
@@ -886,10 +886,11 @@ __global__ void __launch_bounds__(AT_THREADS, 1) attn_kernel(const __grid_consta
       // tiles that every row sees whole
       const int clean_lo = (I.clean_lo + AT_TILE - 1) / AT_TILE, clean_hi = I.clean_hi / AT_TILE;
       // Capped products: y with y scale = cap tanh(v scale / cap), tanh(u) = u Q(u^2) with Q fitted at Chebyshev nodes, its
-      // coefficients scaled to take v: of degree 2 where no |u| of the warp's rows exceeds 0.25, of degree 4 up to 0.6 (errors 1e-7 and 7e-8 of tanh in fp32).  Beyond, 1 - 2 / (1 + 2^(2 log2e u)) with one reciprocal for
-      // two, 1 / a = b / (a b), where 2^60 bounds the exponentials so that the product stays finite.  A 4K prompt of 32
-      // heads takes 99 us without a cap, 137 with one that no logit reaches a quarter of, 153, 175 and 192 with logits two, four
-      // and twelve times as large: bound by the FMA pipe's share of each step.
+      // coefficients scaled to take v: of degree 2 where no |u| of the warp's rows exceeds 0.25, of degree 4 up to 0.6 (errors
+      // 1e-7 and 7e-8 of tanh in fp32).  Beyond, 1 - 2 / (1 + 2^(2 log2e u)) with one reciprocal for two, 1 / a = b / (a b),
+      // where 2^60 bounds the exponentials so that the product stays finite.  A 4K prompt of 32 heads takes 99 us without a
+      // cap, 137 with one that no logit reaches a quarter of, 153, 175 and 192 with logits two, four and twelve times as
+      // large: bound by the FMA pipe's share of each step.
       // Which form a row takes depends on what it sees alone: in a partly masked tile each row goes by its visible keys; in the
       // others, whose keys every row sees, the warp's rows agree, padding rows (whose queries may be anything) having no say.
       auto capped = [&](auto masks, float *v, uint32_t see, bool valid) {
@@ -919,7 +920,7 @@ __global__ void __launch_bounds__(AT_THREADS, 1) attn_kernel(const __grid_consta
             const uint64_t v2 = pack_f2(v[c], v[c + 1]), z = mul_f2(v2, v2);
             unpack_f2(v[c], v[c + 1], mul_f2(v2, fma_f2(z, fma_f2(z, q2, q1), q0)));
           }
-        } else if (!mixed && agreed(most <= P.cap_mid)) {   // (rows that differ in their form take turns: two forms are enough)
+        } else if (!mixed && agreed(most <= P.cap_mid)) {   // (rows that differ take turns: two forms are enough there)
           const uint64_t q0 = pack_f2(P.cap_q[0], P.cap_q[0]), q1 = pack_f2(P.cap_q[1], P.cap_q[1]),
                          q2 = pack_f2(P.cap_q[2], P.cap_q[2]), q3 = pack_f2(P.cap_q[3], P.cap_q[3]),
                          q4 = pack_f2(P.cap_q[4], P.cap_q[4]);
@@ -963,9 +964,9 @@ __global__ void __launch_bounds__(AT_THREADS, 1) attn_kernel(const __grid_consta
       };
       // fp16 holds 2^-24 to 2^15 of a power of two: the reference m is the maximum less 7, so that a row's largest probability
       // lies between 2^7 and 2^15, and what is lost below 2^-25 is below 2^-32 of it.  (bf16 has fp32's exponents.)
-      constexpr float LIFT = FP16 ? 7.f : 0.f, RISE = 8.f + LIFT;
-      // The exponents are taken from unrounded logits, the maximum is rounded: beyond 2^24 the row's largest may come out as 2^-30
-      // or 2^30, or further.  Running maxima start at -AT_BIG, so that logits far below weigh nothing, and the warp's rows are
+      constexpr float LIFT = FP16 ? 7.f : 0.f, RISE = 8.f + LIFT, DROP = FP16 ? 0.0078125f : 1.f;   // DROP = 2^-LIFT
+      // The exponents are taken from unrounded logits, the maximum is rounded: beyond 2^24 the row's largest may come out as
+      // 2^-30 or 2^30, or further.  Running maxima start at -AT_BIG, so that logits far below weigh nothing, and the warp's rows are
       // recomputed from rounded logits when one has ended above AT_BIG, or sees keys and holds a sum l of 0.  (Rounding the
       // logits as they come costs a prompt 6%.)  The four warps that share the rows hold the same maxima and sums.
       auto far_out = [&](const Slot &S, float l) {
@@ -1161,7 +1162,7 @@ __global__ void __launch_bounds__(AT_THREADS, 1) attn_kernel(const __grid_consta
           const float inv = l == 0.f ? 0.f : rcp_approx(l);   // an empty row is 0
           if (valid && side == 0 && P.lse)
             P.lse[((int64_t)b * P.s_q + i) * P.h_q + h] =
-                l == 0.f ? -INFINITY : ((slot ? S1.m : S0.m) + lg2_approx(l)) * 0.69314718055994531f;
+                l == 0.f ? -INFINITY : ((slot ? S1.m : S0.m) + LIFT + lg2_approx(l * DROP)) * 0.69314718055994531f;
           const int64_t at = b * P.so[0] + i * P.so[1] + h * P.so[2] + 64 * side;
           const uint32_t rows = __ballot_sync(0xffffffffu, valid);
 #pragma unroll 1
@@ -1232,7 +1233,7 @@ __global__ void __launch_bounds__(AT_THREADS, 1) attn_kernel(const __grid_consta
               part_l[part_row + prow] = make_float2(mu, lt);
             else if (P.lse)
               P.lse[((int64_t)b * P.s_q + i) * P.h_q + h] =
-                  lt == 0.f ? -INFINITY : (mu + lg2_approx(lt)) * 0.69314718055994531f;
+                  lt == 0.f ? -INFINITY : (mu + LIFT + lg2_approx(lt * DROP)) * 0.69314718055994531f;
           }
           const bool have0 = I.n > 0;
           const float f0 = w0 * inv, f1 = w1 * inv;
@@ -1294,7 +1295,8 @@ __global__ void __launch_bounds__(AT_THREADS, 1) attn_kernel(const __grid_consta
               *reinterpret_cast<float4 *>(part_o + (part_row + rp) * D + 4 * lane) = make_float4(o0, o1, o2, o3);
             } else {
               if (lane == 0 && P.lse)
-                P.lse[((int64_t)rb * P.s_q + ri) * P.h_q + rh] = rl == 0.f ? -INFINITY : (rm + log2f(rl)) * 0.69314718055994531f;
+                P.lse[((int64_t)rb * P.s_q + ri) * P.h_q + rh] =
+                    rl == 0.f ? -INFINITY : (rm + log2f(rl)) * 0.69314718055994531f;
               *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(P.out) + rb * P.so[0] + ri * P.so[1] + rh * P.so[2] +
                                          4 * lane) = make_uint2(pack2<FP16>(o0, o1), pack2<FP16>(o2, o3));
             }

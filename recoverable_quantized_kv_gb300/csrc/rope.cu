@@ -443,7 +443,8 @@ qevict_status qevict_rope_table(const qevict_rope_config *cfg, int64_t first, in
   for (int i = 0; i < A.pairs; ++i) {
     const double hi = theta[i] * inv, lo = std::fma(theta[i], inv, -hi) + theta[i] * inv_low;
     // whole turns per position change nothing and fall away exactly; lo may be negative, its low bit is dropped
-    A.turn[i] = (uint64_t)std::ldexp(hi - std::floor(hi), 64) + ((uint64_t)std::llround(std::ldexp(lo - std::rint(lo), 63)) << 1);
+    const uint64_t low = (uint64_t)std::llround(std::ldexp(lo - std::rint(lo), 63));
+    A.turn[i] = (uint64_t)std::ldexp(hi - std::floor(hi), 64) + (low << 1);
   }
   const bool two = A.pairs % 2 == 0 && ((uintptr_t)d_table & 15) == 0;
   const int groups = two ? A.pairs / 2 : A.pairs;
@@ -469,7 +470,8 @@ qevict_status qevict_rope_apply(const qevict_rope_desc *d, const float *d_table,
   if (d->dtype < 0 || d->dtype > 2 || d->batch < 1 || d->seq < 1 || d->h_q < 0 || d->h_k < 0 || d->h_q + (int64_t)d->h_k < 1 ||
       d->d_head < 2 || d->d_head > 1024 || d->rot_dim < 2 || d->rot_dim > d->d_head || d->rot_dim % 2 ||
       d->rot_dim > 2 * MAX_PAIRS || d->interleaved < 0 || d->interleaved > 1 || d->inverse < 0 || d->inverse > 1 ||
-      d->h_q > (1 << 20) || d->h_k > (1 << 20) || (int64_t)d->batch * d->seq > 0x7fffffffll || !std::isfinite(d->factor) || d->table_rows < 1 || d->pos0 < 0)
+      d->h_q > (1 << 20) || d->h_k > (1 << 20) || (int64_t)d->batch * d->seq > 0x7fffffffll || !std::isfinite(d->factor) ||
+      d->table_rows < 1 || d->pos0 < 0)
     return QEVICT_EINVAL;
   if (!d_positions && (d->pos0 > d->table_rows || d->seq > d->table_rows - d->pos0)) return QEVICT_EINVAL;
   if ((d->h_q > 0) != (q_in != nullptr && q_out != nullptr) || (d->h_k > 0) != (k_in != nullptr && k_out != nullptr))

@@ -137,8 +137,8 @@ def test_caps_near_the_largest(lib, top, cap, sq):
     assert torch.equal(out[0, -1].view(2, 2, 128), v[0, 0][:, None].expand(2, 2, 128))
 
 
-@pytest.mark.parametrize("cap,scale", [(20.0, 0.0), (64.0, 0.0), (2000.0, 0.0), (3e4, 0.05), (1e6, 0.0), (1e9, 0.0), (2.0 ** 40, 1.0), (2.0 ** 99, 1.0),
-                                       (50.0, 1e-4), (50.0, 1e-9), (2.0 ** -13, 1.0)])
+@pytest.mark.parametrize("cap,scale", [(20.0, 0.0), (64.0, 0.0), (2000.0, 0.0), (3e4, 0.05), (1e6, 0.0), (1e9, 0.0),
+                                       (2.0 ** 40, 1.0), (2.0 ** 99, 1.0), (50.0, 1e-4), (50.0, 1e-9), (2.0 ** -13, 1.0)])
 @pytest.mark.parametrize("skv", [1, 200])
 def test_capped_logits_over_the_whole_range_of_caps(lib, cap, scale, skv):
     """Rows of products from -1.5 to 1.5 times cap / scale against one key (behind it keys of the same rows that none sees): lse is
