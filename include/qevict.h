@@ -506,7 +506,109 @@ qevict_status qevict_prefix_attn(const qevict_prefix_attn_desc *desc, const floa
                                  const void *v, void *out, float *lse, void *d_work, size_t bytes,
                                  qevict_stream_t stream);
 
-/* The status word at d_status (the one of qevict_rope_apply, or the start of an attention workspace):
+/* ---- A KV cache in pages, for caches whose sequences share prompts, branch and end at different times.
+ * Pool: k, v [layers][pages][page][h_kv][128], 16-bit elements.  Sequence b holds length[b] tokens; token t of it stands
+ * in row t % page of page table[b][t / page], in every layer.  held[b] pages are in its table, -1 behind them: enough
+ * for its length, and what qevict_pages_reserve has added.  refs counts the table entries of every page; a page
+ * may stand in several sequences, at the same place of each.  Only pages that one sequence holds alone are written to.
+ * All bookkeeping lives in one int32 device buffer of the caller, d_state (256-byte aligned): copied together with the
+ * pool it is a snapshot.  Its arrays, in int32 elements from its start (qevict_pages_get_layout): the status word
+ * (qevict_ops_status), the number of free pages, length [batch], held [batch], table [batch][max_pages], refs [pages], one bit per
+ * free page.  They may be read any time behind the calls in the stream; of them length alone may be written, to a value within
+ * the pages held (an undo of tokens, say).
+ * The calls of one cache run one after the other (one stream, or ordered by events).  Nothing is synchronised.
+ * Faults set bits of the status word: 2 too few free pages, 4 a table that cannot be (qevict_pages_load), 8 an argument or index
+ * out of range.  A sequence that sets bit 8 is left as it was, unless stated; the others are served. */
+typedef struct {
+  int32_t layers;              /* 1..32767 */
+  int32_t pages;               /* of the pool, 1..2^24 */
+  int32_t page;                /* tokens of a page: 16, 32, 64 or 128 */
+  int32_t h_kv, d_head;        /* 1..4096, 128 */
+  int32_t batch, max_pages;    /* sequences, 1..1024; table entries of each; max_pages * page and batch * max_pages up to 2^30 */
+  int32_t reserved0;           /* 0 */
+  int64_t k[4], v[4];          /* strides in elements {layer, page, token, head}, channels contiguous: multiples of 8, no two
+                                * elements in one place; k and v may lie between one another */
+} qevict_pages_desc;
+typedef struct {
+  int64_t status, n_free, length, held, table, refs, free_bits;   /* offsets */
+  int64_t ints;                /* of the whole buffer */
+} qevict_pages_layout;
+qevict_status qevict_pages_get_layout(const qevict_pages_desc *desc, qevict_pages_layout *layout);
+/* Starts the bookkeeping: from d_table [batch][max_pages] and d_length [batch], or empty (both NULL).  The entries of a sequence
+ * up to the first that is not a page of the pool are its pages (entries other than -1 there set bit 8), a length past them or below 0
+ * is clamped (bit 8).  A page at two different places of the tables sets bit 4.  Clears the status word first. */
+qevict_status qevict_pages_load(const qevict_pages_desc *desc, void *d_state, const int32_t *d_table,
+                                const int32_t *d_length, qevict_stream_t stream);
+/* Makes rows length[b] .. length[b] + new - 1 of every sequence writable; new = d_new[b], or n_new where d_new is NULL.
+ * Missing pages are taken from the free ones, the lowest number first, sequence after sequence.  Where the row of the
+ * next token stands in a page that other sequences hold too, the sequence gets a page of its own with a copy of its rows
+ * (all layers); of several sequences that hold it and reserve in one call, the first keeps it if no other holds it.  A
+ * sequence with new = 0 is left as it is.  If the free pages do not suffice (bit 2), or a sequence would pass max_pages
+ * (bit 8, also for new < 0), nothing changes for any sequence. */
+qevict_status qevict_pages_reserve(const qevict_pages_desc *desc, void *k, void *v, void *d_state, const int32_t *d_new,
+                                   int32_t n_new, qevict_stream_t stream);
+/* Writes rows length[b] + i, i < n[b], of layers [layer, layer + layers) from k_new, v_new
+ * [layers][batch][n][h_kv][128]; n[b] = d_n[b] (at most n), or n where d_n is NULL.  Lengths stay: the rows count once
+ * qevict_pages_accept takes them.  Rows whose page is missing or shared are not written (bit 8). */
+typedef struct {
+  int32_t layer, layers, n, reserved0;   /* layers 1.., n 1.., reserved0 0 */
+  int64_t k[4], v[4];                    /* strides {layer, sequence, token, head}: multiples of 8, 0 allowed */
+} qevict_pages_rows;
+qevict_status qevict_pages_append(const qevict_pages_desc *desc, const qevict_pages_rows *rows, void *k, void *v,
+                                  void *d_state, const void *k_new, const void *v_new, const int32_t *d_n,
+                                  qevict_stream_t stream);
+/* The first d_count[b] rows behind every sequence's length become part of it; with d_path [batch][max_path], row
+ * length[b] + path[b][j] moves to length[b] + j first, in all layers (the accepted nodes of a tree of drafts:
+ * strictly ascending).  0 <= count[b], with a path at most max_path (1..256). */
+qevict_status qevict_pages_accept(const qevict_pages_desc *desc, void *k, void *v, void *d_state, const int32_t *d_count,
+                                  const int32_t *d_path, int32_t max_path, qevict_stream_t stream);
+/* All at once, sequence b becomes what sequence d_src[b] was: it holds the same pages, as far as they hold tokens, and the
+ * same length.  d_src[b] = b: it stays as it is; -1: it ends, its pages are given back.  This forks a sequence, reorders beams and
+ * frees.  No rows are copied: qevict_pages_reserve does, where it must.  Other values: bit 8, the sequence stays. */
+qevict_status qevict_pages_select(const qevict_pages_desc *desc, void *d_state, const int32_t *d_src,
+                                  qevict_stream_t stream);
+/* Sequences keep their first min(length[b], d_length[b]) tokens; pages behind them, reserved ones too, are given back.
+ * A negative d_length[b] leaves the sequence as it is. */
+qevict_status qevict_pages_trim(const qevict_pages_desc *desc, void *d_state, const int32_t *d_length,
+                                qevict_stream_t stream);
+/* Moves pages so that those in use are the first ones: the used pages from number n on, n being how many are in use, move to
+ * the free ones below n, both in ascending order.  Tables follow. */
+qevict_status qevict_pages_compact(const qevict_pages_desc *desc, void *k, void *v, void *d_state, qevict_stream_t stream);
+
+/* ---- Attention of the newest tokens of every sequence over a cache in pages: single tokens, chains of them (a
+ * prompt's chunk) and trees of drafts.  Sequence b has length[b] tokens in its pages and q_len[b] new ones, whose keys and
+ * values stand in rows length[b] + i already (qevict_pages_append).  Query i sees the length[b] tokens, itself and
+ *   without parents: new tokens j < i; its position is length[b] + i;
+ *   with parents: its ancestors; parents[i] < i is the node that it follows, -1 the last of the length[b] tokens; its
+ *     position is length[b] + the number of its ancestors.
+ * Scores, out and lse as for qevict_attn with causal = 1; the bias goes by these positions.  s_q up to 64 with parents. */
+typedef struct {
+  int32_t dtype;                           /* QEVICT_BF16 or QEVICT_FP16 */
+  int32_t batch, s_q, h_q, h_kv, d_head;   /* as for qevict_attn */
+  float scale, softcap;
+  int32_t pages, page, max_pages;          /* as for the cache; max_pages * page up to 2^30 */
+  int32_t reserved0;                       /* 0 */
+  int64_t q[3], o[3];                      /* strides {batch, token, head} as for qevict_attn */
+  int64_t k[3], v[3];                      /* of one layer's pool: {page, token, head} */
+} qevict_paged_attn_desc;
+/* Optional device arrays, NULL = absent: q_len absent = s_q.  Lengths out of range (q_len outside [0, s_q], length
+ * outside [0, max_pages * page - q_len]) are clamped, parents outside [-1, i) count as -1, and pages outside the pool are read
+ * as page 0; each sets bit 8 of the status word. */
+typedef struct {
+  const float *slopes;         /* [h_q] fp32 */
+  const int32_t *q_len;        /* [batch] */
+  const int32_t *parents;      /* [batch][s_q], or [s_q] for all sequences (one_tree = 1) */
+  int32_t one_tree;
+} qevict_paged_attn_mask;
+/* Workspace as for qevict_attn. */
+qevict_status qevict_paged_attn_bytes(const qevict_paged_attn_desc *desc, size_t *bytes);
+/* q [batch][s_q][h_q][128], out like q; k, v [pages][page][h_kv][128]; d_table int32 [batch][max_pages], d_length int32
+ * [batch] (the cache's); lse fp32 [batch][s_q][h_q] or NULL. */
+qevict_status qevict_paged_attn(const qevict_paged_attn_desc *desc, const qevict_paged_attn_mask *mask, const void *q,
+                                const void *k, const void *v, const int32_t *d_table, const int32_t *d_length, void *out,
+                                float *lse, void *d_work, size_t bytes, qevict_stream_t stream);
+
+/* The status word at d_status (the one of qevict_rope_apply, or the start of an attention workspace or of a paged cache's state):
  * synchronises `stream`, the one that the calls ran on, copies the word to *host_word (may be NULL) and clears it if it
  * was set, which is QEVICT_EDEVICE. */
 qevict_status qevict_ops_status(void *d_status, int32_t *host_word, qevict_stream_t stream);

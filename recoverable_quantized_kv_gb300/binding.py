@@ -77,6 +77,7 @@ class RopeConfig(ctypes.Structure):
 
 _Stride3 = ctypes.c_int64 * 3
 _Stride2 = ctypes.c_int64 * 2
+_Stride4 = ctypes.c_int64 * 4
 
 
 class RopeDesc(ctypes.Structure):
@@ -97,6 +98,31 @@ class AttnMask(ctypes.Structure):
 
 class PrefixAttnDesc(ctypes.Structure):
     _fields_ = [("attn", AttnDesc), ("s_prefix", ctypes.c_int32), ("k_prefix", _Stride2), ("v_prefix", _Stride2)]
+
+
+class PagesDesc(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("layers", "pages", "page", "h_kv", "d_head", "batch", "max_pages",
+                                             "reserved0")] + [("k", _Stride4), ("v", _Stride4)]
+
+
+class PagesLayout(ctypes.Structure):
+    """Offsets of the bookkeeping's arrays, in int32 elements (qevict_pages_layout)."""
+    _fields_ = [(n, ctypes.c_int64) for n in ("status", "n_free", "length", "held", "table", "refs", "free_bits", "ints")]
+
+
+class PagesRows(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("layer", "layers", "n", "reserved0")] + [("k", _Stride4), ("v", _Stride4)]
+
+
+class PagedAttnDesc(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("dtype", "batch", "s_q", "h_q", "h_kv", "d_head")] + \
+               [("scale", ctypes.c_float), ("softcap", ctypes.c_float)] + \
+               [(n, ctypes.c_int32) for n in ("pages", "page", "max_pages", "reserved0")] + \
+               [(n, _Stride3) for n in ("q", "o", "k", "v")]
+
+
+class PagedAttnMask(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("slopes", "q_len", "parents")] + [("one_tree", ctypes.c_int32)]
 
 
 _lib = None
@@ -147,6 +173,17 @@ def load() -> ctypes.CDLL:
         "qevict_prefix_attn_bytes": [ctypes.POINTER(PrefixAttnDesc), ctypes.POINTER(ctypes.c_size_t)],
         "qevict_prefix_attn": [ctypes.POINTER(PrefixAttnDesc)] + [P] * 10 + [ctypes.c_size_t, P],
         "qevict_ops_status": [P, ctypes.POINTER(I32), P],
+        "qevict_pages_get_layout": [ctypes.POINTER(PagesDesc), ctypes.POINTER(PagesLayout)],
+        "qevict_pages_load": [ctypes.POINTER(PagesDesc), P, P, P, P],
+        "qevict_pages_reserve": [ctypes.POINTER(PagesDesc), P, P, P, P, I32, P],
+        "qevict_pages_append": [ctypes.POINTER(PagesDesc), ctypes.POINTER(PagesRows)] + [P] * 7,
+        "qevict_pages_accept": [ctypes.POINTER(PagesDesc), P, P, P, P, P, I32, P],
+        "qevict_pages_select": [ctypes.POINTER(PagesDesc), P, P, P],
+        "qevict_pages_trim": [ctypes.POINTER(PagesDesc), P, P, P],
+        "qevict_pages_compact": [ctypes.POINTER(PagesDesc), P, P, P, P],
+        "qevict_paged_attn_bytes": [ctypes.POINTER(PagedAttnDesc), ctypes.POINTER(ctypes.c_size_t)],
+        "qevict_paged_attn": [ctypes.POINTER(PagedAttnDesc), ctypes.POINTER(PagedAttnMask)] + [P] * 8 +
+                             [ctypes.c_size_t, P],
     }
     for name, args in sig.items():
         fn = getattr(lib, name)
@@ -168,7 +205,10 @@ def exported_symbols():
             "qevict_diag_init", "qevict_diag_route", "qevict_diag_read", "qevict_diag_destroy",
             "qevict_selftest_wait", "qevict_prefill_scores_noalloc_status", "qevict_debug_cap_free_slots",
             "qevict_read_status", "qevict_rope_angles", "qevict_rope_table", "qevict_rope_apply", "qevict_attn_bytes",
-            "qevict_attn", "qevict_prefix_attn_bytes", "qevict_prefix_attn", "qevict_ops_status"]
+            "qevict_attn", "qevict_prefix_attn_bytes", "qevict_prefix_attn", "qevict_ops_status",
+            "qevict_pages_get_layout", "qevict_pages_load", "qevict_pages_reserve", "qevict_pages_append",
+            "qevict_pages_accept", "qevict_pages_select", "qevict_pages_trim", "qevict_pages_compact",
+            "qevict_paged_attn_bytes", "qevict_paged_attn"]
 
 
 def _check(status: int, where: str):
@@ -379,7 +419,7 @@ class Diagnostics:
 
 
 # ---------------------------------------------------------------------------------------------- operators
-# Rotary positions and attention over dense tensors (no cache handle).  Tensors keep their strides; a call
+# Rotary positions, attention over dense tensors and over a cache in pages (no cache handle).  Tensors keep their strides; a call
 # runs on the device of its first tensor, on `stream` or that device's current stream.
 
 _ROPE_SCALING = {"none": 0, "linear": 1, "ntk": 2, "parts": 3}
@@ -763,3 +803,182 @@ class PrefixAttention(_AttnPlan):
 
     def _with_strides(self, key):
         return PrefixAttnDesc(super()._with_strides(key), self.s_prefix, _Stride2(*key[4][:2]), _Stride2(*key[5][:2]))
+
+
+class PagedCache:
+    """A KV cache in pages: the pool k, v [layers][pages][page][h_kv][128], and which pages hold the tokens of each of
+    `batch` sequences (at most max_pages each).  A step: reserve() room, append() each layer's new rows, attend
+    (PagedAttention), accept() what counts.  select() forks, reorders and frees; trim() shortens; compact() gathers the pages in
+    use at the pool's beginning.  See qevict_pages_* for what each does.
+
+    length, held [batch], table [batch][max_pages], refs [pages] and n_free are views of `state`, one int32 tensor: with copies
+    of it and the pool a cache is saved and restored.  Calls of a cache run in order: one stream, or ordered by the caller."""
+
+    def __init__(self, layers, pages, page, h_kv, batch, max_pages, dtype=None, device="cuda", k=None, v=None):
+        import torch
+        where = "PagedCache"
+        self.dtype = dtype or torch.bfloat16
+        _dtype_code(self.dtype, where, (0, 1))
+        _need((k is None) == (v is None), where, "k and v are given together")
+        self.device = torch.device(device) if k is None else k.device
+        _need(self.device.type == "cuda", where, "the pool must be on a CUDA device")
+        if self.device.index is None:
+            self.device = torch.device("cuda", torch.cuda.current_device())
+        shape = tuple(int(n) for n in (layers, pages, page, h_kv, 128))
+        step = [shape[1] * shape[2] * shape[3] * 128, shape[2] * shape[3] * 128, shape[3] * 128, 128]
+        if k is not None:
+            for name, t in (("k", k), ("v", v)):
+                _tensor(t, where, name, shape, self.dtype, self.device)
+            _no_graph(where, (k, v))
+        desc = PagesDesc(shape[0], shape[1], shape[2], shape[3], 128, int(batch), int(max_pages), 0,
+                         _Stride4(*(step if k is None else k.stride()[:4])),
+                         _Stride4(*(step if v is None else v.stride()[:4])))
+        self.layout = PagesLayout()
+        _check(load().qevict_pages_get_layout(ctypes.byref(desc), ctypes.byref(self.layout)), "qevict_pages_get_layout")
+        if k is None:
+            k = torch.empty(shape, dtype=self.dtype, device=self.device)
+            v = torch.empty(shape, dtype=self.dtype, device=self.device)
+        self.k, self.v, self.shape, self.batch = k, v, shape, int(batch)
+        self.state = torch.empty(self.layout.ints, dtype=torch.int32, device=self.device)
+        part = lambda off, n: self.state[off:off + n]   # noqa: E731
+        lay = self.layout
+        self.n_free = part(lay.n_free, 1)
+        self.length, self.held, self.refs = part(lay.length, desc.batch), part(lay.held, desc.batch), part(lay.refs, desc.pages)
+        self.table = part(lay.table, desc.batch * desc.max_pages).view(desc.batch, desc.max_pages)
+        self.index = self.state.get_device()
+        self._home, self._own = _home(self.index), (self.state, k, v)
+        self._desc, self._state, self._pool, self._rows = ctypes.byref(desc), self.state.data_ptr(), \
+            (k.data_ptr(), v.data_ptr()), {}
+        self.load()
+        _settled(self.state)
+
+    def _ints(self, where, name, t, shape):
+        return _array(where, name, t, shape, _torch().int32, self.index)
+
+    def _run(self, name, stream, tensors, *args):
+        s, other = _enter(self.index, stream, tensors, self._home, self._own)
+        _call(name, other, (self._desc, *args, s))
+
+    def load(self, table=None, length=None, stream=None):
+        """Starts the bookkeeping from a table int32 [batch][max_pages] (-1: no page) and lengths int32 [batch], or empty."""
+        where = "PagedCache.load"
+        _need((table is None) == (length is None), where, "table and length are given together")
+        self._run("qevict_pages_load", stream, (table, length), self._state,
+                  self._ints(where, "table", table, self.table.shape), self._ints(where, "length", length, self.length.shape))
+
+    def reserve(self, new, stream=None):
+        """Makes `new` rows behind every sequence writable: an int, or an int32 tensor [batch]."""
+        if isinstance(new, int):
+            self._run("qevict_pages_reserve", stream, (), *self._pool, self._state, None, new)
+        else:
+            self._run("qevict_pages_reserve", stream, (new,), *self._pool, self._state,
+                      self._ints("PagedCache.reserve", "new", new, self.length.shape), 0)
+
+    def append(self, k, v, layer=None, n=None, stream=None):
+        """Writes rows behind every sequence's length: k, v [batch][n][h_kv][128] of one layer, or [layers][batch][n][h_kv][128]
+        of all.  n: int32 [batch], the rows of each sequence (default all).  Inputs that require a gradient are refused
+        unless gradients are off."""
+        where = "PagedCache.append"
+        _no_graph(where, (k, v))
+        key = (k.shape, k.stride(), v.shape, v.stride(), layer)
+        rows = self._rows.get(key)
+        if rows is None:
+            rows = self._rows_of(where, key, k, v, layer)
+        i, dt = self.index, self.dtype
+        if not (k.dtype is dt and v.dtype is dt and k.get_device() == i and v.get_device() == i):
+            for name, t in (("k", k), ("v", v)):
+                _tensor(t, where, name, t.shape, dt, self.device)
+        self._run("qevict_pages_append", stream, (k, v, n), rows, *self._pool, self._state, k.data_ptr(), v.data_ptr(),
+                  self._ints(where, "n", n, self.length.shape))
+
+    def _rows_of(self, where, key, k, v, layer):
+        """Descriptor of rows with these shapes and strides, kept for the next call."""
+        layers, _, _, h_kv, d = self.shape
+        _need(k.dim() == (5 if layer is None else 4), where, "k and v must be [layers][batch][n][h_kv][128], or without layers")
+        lead = (layers, self.batch) if layer is None else (self.batch,)
+        shape = lead + (k.shape[-3], h_kv, d)
+        for name, t in (("k", k), ("v", v)):
+            _tensor(t, where, name, shape, self.dtype, self.device)
+        st = [(0,) * (4 - len(shape) + 1) + tuple(t.stride()[:-1]) for t in (k, v)]
+        if layer is not None:
+            _need(0 <= layer < layers, where, f"layer must be in [0, {layers}), is {layer}")
+        rows = PagesRows(0 if layer is None else int(layer), layers if layer is None else 1, shape[-3], 0, _Stride4(*st[0]),
+                         _Stride4(*st[1]))
+        if len(self._rows) > 256:
+            self._rows.clear()
+        self._rows[key] = ctypes.byref(rows)
+        return self._rows[key]
+
+    def accept(self, count, path=None, stream=None):
+        """The first count[b] rows behind each length count from now on; with path int32 [batch][max_path], rows path[b][j]
+        (strictly ascending) move there first."""
+        where, most = "PagedCache.accept", 0
+        if path is not None:
+            _need(path.dim() == 2, where, "path must be [batch][max_path]")
+            most = path.shape[1]
+            path_at = self._ints(where, "path", path, (self.batch, most))
+        self._run("qevict_pages_accept", stream, (count, path), *self._pool, self._state,
+                  self._ints(where, "count", count, self.length.shape), None if path is None else path_at, most)
+
+    def select(self, src, stream=None):
+        """Sequence b becomes a copy of what sequence src[b] (int32 [batch]) was, or ends (-1); pages are shared, no rows copied."""
+        self._run("qevict_pages_select", stream, (src,), self._state,
+                  self._ints("PagedCache.select", "src", src, self.length.shape))
+
+    def trim(self, length, stream=None):
+        """Cuts sequences to their first length[b] tokens (int32 [batch]; negative: as it is) and gives pages behind back."""
+        self._run("qevict_pages_trim", stream, (length,), self._state,
+                  self._ints("PagedCache.trim", "length", length, self.length.shape))
+
+    def compact(self, stream=None):
+        """Moves the pages in use to the beginning of the pool."""
+        self._run("qevict_pages_compact", stream, (), *self._pool, self._state)
+
+    def check(self, stream=None):
+        """Raises EDEVICE if a call since the last check recorded a fault: too few free pages, an argument or index out of
+        range, a table that cannot be.  Synchronises `stream` (the current one unless given): the one that the calls ran on."""
+        _ops_status(self.state, stream)
+
+
+class PagedAttention(_AttnPlan):
+    """Attention of the newest tokens of every sequence over a cache in pages: single tokens (s_q = 1), chunks of a prompt,
+    trees of drafts.  See qevict_paged_attn."""
+
+    def __init__(self, batch, s_q, pages, page, max_pages, h_q, h_kv, dtype=None, softcap=0.0, scale=0.0, device="cuda"):
+        import torch
+        self._setup("PagedAttention", batch, s_q, 1, h_q, h_kv, dtype or torch.bfloat16, True, softcap, scale, device)
+        self.pool_shape, self.table_shape = (int(pages), int(page), int(h_kv), 128), (int(batch), int(max_pages))
+        h, n, d = int(h_kv), ctypes.c_size_t(), self.desc
+        pool, q = (int(page) * h * 128, h * 128, 128), tuple(d.q)
+        with torch.cuda.device(self.device):
+            _check(load().qevict_paged_attn_bytes(ctypes.byref(self._with_strides((q, pool, pool, q))), ctypes.byref(n)),
+                   "qevict_paged_attn_bytes")
+        self._workspace(n.value)
+        self.kv_shape = self.pool_shape
+
+    def run(self, q, k, v, table, length, out=None, lse=None, parents=None, q_len=None, slopes=None, stream=None):
+        """q [batch][s_q][h_q][128], k, v [pages][page][h_kv][128] (one layer's pool), table int32 [batch][max_pages], length
+        int32 [batch]: the tokens before the queries, whose own keys and values stand behind them.  parents: int32
+        [batch][s_q], or [s_q] for all.  Returns (out, lse), new tensors unless given; rows behind q_len[b] are not
+        written.  Inputs that require a gradient are refused unless gradients are off."""
+        where, d, i, i32 = "PagedAttention.run", self.desc, self.index, _torch().int32
+        _no_graph(where, (q, k, v, slopes))
+        desc, out, lse = self._tensors(where, q, k, v, out, lse, stream)
+        batch, mask = self.q_shape[:1], None
+        if not (slopes is None and q_len is None and parents is None):
+            one = parents is not None and parents.dim() == 1
+            mask = ctypes.byref(PagedAttnMask(_array(where, "slopes", slopes, (d.h_q,), _torch().float32, i),
+                                              _array(where, "q_len", q_len, batch, i32, i),
+                                              _array(where, "parents", parents, self.q_shape[1:2] if one else self.q_shape[:2],
+                                                     i32, i), int(one)))
+        _need(table is not None and length is not None, where, "table and length are needed")
+        s, other = _enter(i, stream, (q, k, v, table, length, out, lse, parents, q_len, slopes), self._home, self._own)
+        _call("qevict_paged_attn", other,
+              (desc, mask, q.data_ptr(), k.data_ptr(), v.data_ptr(), _array(where, "table", table, self.table_shape, i32, i),
+               _array(where, "length", length, batch, i32, i), out.data_ptr(), lse.data_ptr(), *self._work, s))
+        return out, lse
+
+    def _with_strides(self, key):
+        d, (pages, page, h_kv, _) = self.desc, self.pool_shape
+        return PagedAttnDesc(d.dtype, d.batch, d.s_q, d.h_q, h_kv, 128, d.scale, d.softcap, pages, page, self.table_shape[1], 0,
+                             *(_Stride3(*key[n][:3]) for n in (0, 3, 1, 2)))

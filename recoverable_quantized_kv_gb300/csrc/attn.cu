@@ -1,4 +1,4 @@
-// Attention over a dense KV cache and of a batch behind a shared prefix: argument checks, split rules,
+// Attention over a dense KV cache, over one in pages and of a batch behind a shared prefix: argument checks, split rules,
 // workspace layout, the document scan and the merge of split results.  The attention kernel itself is in
 // attn_dev.cuh.
 #include <cuda_runtime.h>
@@ -18,6 +18,10 @@ cudaError_t launch_attn_bf16_cap(const AttnArgs &P, int grid, bool bias, cudaStr
 cudaError_t launch_attn_fp16_cap(const AttnArgs &P, int grid, bool bias, cudaStream_t s);
 cudaError_t launch_attn_bf16_wide(const AttnArgs &P, int grid, bool bias, cudaStream_t s);
 cudaError_t launch_attn_fp16_wide(const AttnArgs &P, int grid, bool bias, cudaStream_t s);
+cudaError_t launch_attn_bf16_paged(const AttnArgs &P, int grid, bool bias, cudaStream_t s);
+cudaError_t launch_attn_fp16_paged(const AttnArgs &P, int grid, bool bias, cudaStream_t s);
+cudaError_t launch_attn_bf16_paged_cap(const AttnArgs &P, int grid, bool bias, cudaStream_t s);
+cudaError_t launch_attn_fp16_paged_cap(const AttnArgs &P, int grid, bool bias, cudaStream_t s);
 
 // First and past-the-last position of every position's run of equal ids.  One CTA per sequence; thread i takes the i-th of
 // 1024 consecutive pieces, finds the first and last run start in it, and scans over the warp and then over the warps carry
@@ -239,7 +243,7 @@ bool stride_ok(int64_t st, int64_t size, bool zero) {
 
 float logit_scale(const qevict_attn_desc *d) { return d->scale > 0.f ? d->scale : 1.f / std::sqrt((float)D); }
 
-qevict_status attn_plan(const qevict_attn_desc *d, int s_prefix, AttnPlan *p) {
+qevict_status attn_plan(const qevict_attn_desc *d, int s_prefix, AttnPlan *p, bool paged = false) {
   if (!d || d->dtype < 0 || d->dtype > 1 || d->batch < 1 || d->s_q < 1 || d->s_kv < 1 || d->h_kv < 1 || d->h_q < d->h_kv ||
       d->h_q % d->h_kv || d->h_q / d->h_kv > AT_TILE || d->d_head != D || d->causal < 0 || d->causal > 1 ||
       !(d->scale >= 0.f) || !std::isfinite(d->scale) || !(d->softcap >= 0.f) || !std::isfinite(d->softcap))
@@ -293,7 +297,7 @@ qevict_status attn_plan(const qevict_attn_desc *d, int s_prefix, AttnPlan *p) {
     off += align256(n);
     return o;
   };
-  if (!s_prefix) p->off_runs = take((int64_t)d->batch * d->s_kv * 8);
+  if (!s_prefix && !paged) p->off_runs = take((int64_t)d->batch * d->s_kv * 8);
   if (p->stream) {
     p->part_rows = std::min(d->s_q, 2 * p->tpt) * p->G;
     const int64_t parts = p->grid + units;
@@ -324,8 +328,15 @@ bool o_disjoint(const qevict_attn_desc *d) {
   return true;
 }
 
+// The cache in pages of a call, and the tree of its queries.
+struct PagedArgs {
+  const qevict_paged_attn_desc *desc;
+  const int32_t *table, *length, *parents;
+  bool one_tree;
+};
+
 qevict_status attn_launch(const qevict_attn_desc *d, const AttnPlan &pl, const qevict_attn_mask *mask,
-                          const qevict_prefix_attn_desc *pd, const void *q, const void *kp, const void *vp, const void *k,
+                          const qevict_prefix_attn_desc *pd, const PagedArgs *pg, const void *q, const void *kp, const void *vp, const void *k,
                           const void *v, void *out, float *lse, void *d_work, size_t bytes, cudaStream_t s) {
   if (!q || !k || !v || !out || !d_work || (((uintptr_t)q | (uintptr_t)k | (uintptr_t)v | (uintptr_t)out) & 15) ||
       ((uintptr_t)lse & 3) || ((uintptr_t)d_work & 255) || !o_disjoint(d))
@@ -372,9 +383,20 @@ qevict_status attn_launch(const qevict_attn_desc *d, const AttnPlan &pl, const q
   }
   const bool fp16 = d->dtype == QEVICT_FP16;
   const int qb = A.mul_q ? d->batch : 1, kb = A.mul_k ? d->batch : 1, vb = A.mul_v ? d->batch : 1;
-  bool ok = dense_map(&A.tq, fp16, q, d->h_q, d->s_q, qb, d->q[2], d->q[1], d->q[0], pl.G, pl.tpt, 1) &&
-            dense_map(&A.tk, fp16, k, d->h_kv, d->s_kv, kb, d->k[2], d->k[1], d->k[0], 1, AT_TILE, 1) &&
-            dense_map(&A.tv, fp16, v, d->h_kv, d->s_kv, vb, d->v[2], d->v[1], d->v[0], 1, AT_TILE, 1);
+  bool ok = dense_map(&A.tq, fp16, q, d->h_q, d->s_q, qb, d->q[2], d->q[1], d->q[0], pl.G, pl.tpt, 1);
+  if (pg) {
+    const qevict_paged_attn_desc &c = *pg->desc;
+    A.table = pg->table, A.ctx_len = pg->length, A.parents = pg->parents;
+    A.parents_step = pg->one_tree ? 0 : d->s_q;
+    A.pages = c.pages, A.max_pages = c.max_pages;
+    while (1 << A.page_lg < c.page) ++A.page_lg;
+    for (int i = 0; i < 3; ++i) A.sk[i] = c.k[i], A.sv[i] = c.v[i];
+    ok = ok && dense_map(&A.tk, fp16, k, d->h_kv, c.page, c.pages, c.k[2], c.k[1], c.k[0], 1, c.page, 1) &&
+         dense_map(&A.tv, fp16, v, d->h_kv, c.page, c.pages, c.v[2], c.v[1], c.v[0], 1, c.page, 1);
+  } else {
+    ok = ok && dense_map(&A.tk, fp16, k, d->h_kv, d->s_kv, kb, d->k[2], d->k[1], d->k[0], 1, AT_TILE, 1) &&
+         dense_map(&A.tv, fp16, v, d->h_kv, d->s_kv, vb, d->v[2], d->v[1], d->v[0], 1, AT_TILE, 1);
+  }
   if (pd) {
     A.skp[0] = pd->k_prefix[0], A.skp[1] = pd->k_prefix[1], A.svp[0] = pd->v_prefix[0], A.svp[1] = pd->v_prefix[1];
     ok = ok && dense_map(&A.tqp, fp16, q, d->h_q, d->s_q, d->batch, d->q[2], d->q[1], d->q[0], pl.G, d->s_q, pl.nb) &&
@@ -393,7 +415,10 @@ qevict_status attn_launch(const qevict_attn_desc *d, const AttnPlan &pl, const q
     A.pre_l = reinterpret_cast<float2 *>(w + pl.off_pl);
     A.pre_o = reinterpret_cast<float *>(w + pl.off_po);
   }
-  const auto launch = d->softcap > WIDE_CAP ? (fp16 ? launch_attn_fp16_wide : launch_attn_bf16_wide)
+  // (over pages one kind of capped instances: the narrow caps' saves 2% of a long prompt, nothing of a decode step)
+  const auto launch = pg ? (d->softcap > 0.f ? (fp16 ? launch_attn_fp16_paged_cap : launch_attn_bf16_paged_cap)
+                                             : (fp16 ? launch_attn_fp16_paged : launch_attn_bf16_paged))
+                      : d->softcap > WIDE_CAP ? (fp16 ? launch_attn_fp16_wide : launch_attn_bf16_wide)
                       : d->softcap > 0.f    ? (fp16 ? launch_attn_fp16_cap : launch_attn_bf16_cap)
                                             : (fp16 ? launch_attn_fp16 : launch_attn_bf16);
   if (launch(A, pl.grid, m.slopes != nullptr, s) != cudaSuccess) return QEVICT_ECUDA;
@@ -433,7 +458,7 @@ qevict_status qevict_attn(const qevict_attn_desc *desc, const qevict_attn_mask *
   qv::AttnPlan p;
   const qevict_status st = qv::attn_plan(desc, 0, &p);
   if (st != QEVICT_OK) return st;
-  return qv::attn_launch(desc, p, mask, nullptr, q, nullptr, nullptr, k, v, out, lse, d_work, bytes,
+  return qv::attn_launch(desc, p, mask, nullptr, nullptr, q, nullptr, nullptr, k, v, out, lse, d_work, bytes,
                          reinterpret_cast<cudaStream_t>(stream));
 }
 
@@ -465,7 +490,52 @@ qevict_status qevict_prefix_attn(const qevict_prefix_attn_desc *desc, const floa
   qevict_attn_mask m = {};
   m.slopes = slopes;
   m.kv_len = kv_len;
-  return qv::attn_launch(&desc->attn, p, &m, desc, q, k_prefix, v_prefix, k, v, out, lse, d_work, bytes,
+  return qv::attn_launch(&desc->attn, p, &m, desc, nullptr, q, k_prefix, v_prefix, k, v, out, lse, d_work, bytes,
+                         reinterpret_cast<cudaStream_t>(stream));
+}
+
+static qevict_status paged_plan(const qevict_paged_attn_desc *d, qevict_attn_desc *a, qv::AttnPlan *p) {
+  if (!d || d->pages < 1 || d->pages > (1 << 24) || (d->page != 16 && d->page != 32 && d->page != 64 && d->page != 128) ||
+      d->max_pages < 1 || d->max_pages > (1 << 30) / d->page || d->s_q > d->max_pages * d->page || d->reserved0 ||
+      (int64_t)d->batch * d->max_pages > (1 << 30))
+    return QEVICT_EINVAL;
+  if (!qv::stride_ok(d->k[0], d->pages, false) || !qv::stride_ok(d->v[0], d->pages, false) ||
+      !qv::stride_ok(d->k[1], d->page, false) || !qv::stride_ok(d->v[1], d->page, false) ||
+      !qv::stride_ok(d->k[2], d->h_kv, false) || !qv::stride_ok(d->v[2], d->h_kv, false))
+    return QEVICT_EINVAL;
+  *a = qevict_attn_desc();
+  a->dtype = d->dtype, a->batch = d->batch, a->s_q = d->s_q, a->s_kv = d->max_pages * d->page;
+  a->h_q = d->h_q, a->h_kv = d->h_kv, a->d_head = d->d_head, a->causal = 1, a->scale = d->scale, a->softcap = d->softcap;
+  for (int i = 0; i < 3; ++i) a->q[i] = d->q[i], a->o[i] = d->o[i], a->k[i] = a->v[i] = i ? 8 : 0;   // (the pool has its own)
+  return qv::attn_plan(a, 0, p, true);
+}
+
+qevict_status qevict_paged_attn_bytes(const qevict_paged_attn_desc *desc, size_t *bytes) {
+  qv::AttnPlan p;
+  qevict_attn_desc a;
+  if (!bytes) return QEVICT_EINVAL;
+  const qevict_status st = paged_plan(desc, &a, &p);
+  if (st == QEVICT_OK) *bytes = (size_t)p.bytes;
+  return st;
+}
+
+qevict_status qevict_paged_attn(const qevict_paged_attn_desc *desc, const qevict_paged_attn_mask *mask, const void *q,
+                                const void *k, const void *v, const int32_t *d_table, const int32_t *d_length, void *out,
+                                float *lse, void *d_work, size_t bytes, qevict_stream_t stream) {
+  qv::AttnPlan p;
+  qevict_attn_desc a;
+  const qevict_status st = paged_plan(desc, &a, &p);
+  if (st != QEVICT_OK) return st;
+  qevict_attn_mask m = {};
+  qv::PagedArgs pg = {desc, d_table, d_length, nullptr, false};
+  if (mask) {
+    m.slopes = mask->slopes, m.q_len = mask->q_len;
+    pg.parents = mask->parents, pg.one_tree = mask->one_tree != 0;
+  }
+  if (!d_table || !d_length || (((uintptr_t)d_table | (uintptr_t)d_length | (uintptr_t)pg.parents) & 3) ||
+      (pg.parents && desc->s_q > 64))
+    return QEVICT_EINVAL;
+  return qv::attn_launch(&a, p, &m, nullptr, &pg, q, nullptr, nullptr, k, v, out, lse, d_work, bytes,
                          reinterpret_cast<cudaStream_t>(stream));
 }
 

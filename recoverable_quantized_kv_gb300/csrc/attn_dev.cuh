@@ -53,6 +53,11 @@ struct AttnArgs {
   const float *slopes;
   const int *q_len, *kv_len, *prefix_len;
   const int2 *runs;            // [batch][s_kv]: first and past-the-last position of every position's document
+  // A cache in pages (PAGED instances): tk, tv are [pages][page][h_kv][128], s_kv the room of a sequence's table.
+  const int *table, *ctx_len;  // [batch][max_pages]; keys before the queries' own
+  const int *parents;          // NULL: query i sees the queries before it; else its ancestors
+  int64_t parents_step;        // between sequences: s_q, or 0
+  int pages, max_pages, page_lg;
   int64_t sq[3], sk[3], sv[3], so[3], skp[2], svp[2];
   int batch, s_q, s_kv, h_q, h_kv, G, causal;
   int mul_q, mul_k, mul_v;     // batch coordinate of the tensor maps: 0 for a batch stride of 0
@@ -79,6 +84,34 @@ struct AttnGroup {
   int tiles;                   // key tiles from key_lo on
 };
 
+// Page number of entry e of sequence b's table, whatever stands there; one outside the pool is reported and read as page 0.
+__device__ __forceinline__ int attn_page(const AttnArgs &P, int b, int e) {
+  const int p = P.table[(int64_t)b * P.max_pages + e];
+  if ((unsigned)p < (unsigned)P.pages) return p;
+  atomicOr(P.status, QV_ERR_BOUNDS);
+  return 0;
+}
+// Nodes that node i < 64 of sequence b's tree sees, itself and its ancestors, as bits.  Parents come before their children,
+// so the walk ends; what does not is reported and ends it.
+__device__ __forceinline__ uint64_t attn_line(const AttnArgs &P, int b, int i) {
+  const int *parents = P.parents + b * P.parents_step;
+  uint64_t line = 0;
+  while (i >= 0) {
+    line |= 1ull << i;
+    const int up = parents[i];
+    if (up >= i || up < -1) {
+      atomicOr(P.status, QV_ERR_BOUNDS);
+      break;
+    }
+    i = up;
+  }
+  return line;
+}
+// Of 32 keys from node d on (d < 0: from -d keys before the tree) those in `line`.
+__device__ __forceinline__ uint32_t attn_line_bits(uint64_t line, int d) {
+  return d >= 64 || d <= -32 ? 0u : (uint32_t)(d >= 0 ? line >> d : line << -d);
+}
+
 // Visible keys [x, y) of position p.  Both ends grow with p.
 __device__ __forceinline__ int2 attn_interval(const AttnArgs &P, int b, int p, int kl, int pfx) {
   int lo = 0, hi = P.causal ? min(max(p + 1, pfx), kl) : kl;
@@ -98,6 +131,7 @@ __device__ __forceinline__ AttnGroup attn_group(const AttnArgs &P, int gi) {
   A.tile0 = 2 * pr;
   A.kl = P.kv_len ? clampi(P.kv_len[A.b], 0, P.s_kv) : P.s_kv;
   A.ql = P.q_len ? clampi(P.q_len[A.b], 0, P.s_q) : P.s_q;
+  if (P.ctx_len) A.kl = clampi(P.ctx_len[A.b], 0, P.s_kv - A.ql) + A.ql;
   A.pfx = P.prefix_len ? clampi(P.prefix_len[A.b], 0, A.kl) : 0;
   const int i0 = A.tile0 * P.tpt, i1 = min(A.ql, i0 + 2 * P.tpt);
   A.clean_lo = A.clean_hi = A.key_lo = A.key_hi = A.tiles = 0;
@@ -107,7 +141,7 @@ __device__ __forceinline__ AttnGroup attn_group(const AttnArgs &P, int gi) {
     A.key_lo = a.x;
     A.key_hi = z.y;
     A.clean_lo = z.x;
-    A.clean_hi = a.y;
+    A.clean_hi = P.parents ? min(a.y, A.kl - A.ql) : a.y;
     A.tiles = (A.key_hi - A.key_lo + AT_TILE - 1) / AT_TILE;   // (a document's units share its tiles)
   }
   return A;
@@ -205,6 +239,16 @@ __device__ __forceinline__ void tma_load_4d_at(uint32_t dst, const CUtensorMap *
   asm volatile(
       "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], "
       "[%6];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(smem_u32(bar))
+      : "memory");
+}
+// The same by one elected lane of a converged warp.
+__device__ __forceinline__ void tma_load_4d_elect(uint32_t dst, const CUtensorMap *map, int x, int y, int z, int w,
+                                                  uint64_t *bar) {
+  asm volatile(
+      "{\n .reg .pred e;\n elect.sync _|e, 0xffffffff;\n"
+      " @e cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], "
+      "[%6];\n}" ::"r"(dst),
       "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(smem_u32(bar))
       : "memory");
 }
@@ -413,7 +457,7 @@ __device__ __forceinline__ void attn_clean_values(const AttnItem &I, int t, uint
 // masked value touched.  Reached when a value that some row of the item sees and another does not is an infinity or NaN
 // (the tensor-core product then ran with that value as 0), and when the maximum of one of the rows is beyond AT_BIG.  Writes
 // O (unnormalised), m, l of row r through `emit`, the warp's lanes holding four channels each.
-template <bool FP16, bool STREAM, typename Emit>
+template <bool FP16, bool STREAM, bool PAGED, typename Emit>
 __device__ __forceinline__ void attn_exact_rows(const AttnArgs &P, const AttnItem &I, int slot, int warp, int lane, bool cap,
                                                 const Emit &emit) {
   const uint16_t *kb, *vb;
@@ -423,34 +467,44 @@ __device__ __forceinline__ void attn_exact_rows(const AttnArgs &P, const AttnIte
     vb = static_cast<const uint16_t *>(P.vp) + I.g * P.svp[1];
     kst = P.skp[0], vst = P.svp[0];
   } else {
-    kb = static_cast<const uint16_t *>(P.k) + I.b * P.sk[0] + I.g * P.sk[2];
-    vb = static_cast<const uint16_t *>(P.v) + I.b * P.sv[0] + I.g * P.sv[2];
+    kb = static_cast<const uint16_t *>(P.k) + (PAGED ? 0 : I.b * P.sk[0]) + I.g * P.sk[2];
+    vb = static_cast<const uint16_t *>(P.v) + (PAGED ? 0 : I.b * P.sv[0]) + I.g * P.sv[2];
     kst = P.sk[1], vst = P.sv[1];
   }
+  auto row_at = [&](const uint16_t *base, int64_t page_st, int64_t st, int key) {
+    if (!PAGED) return base + (int64_t)key * st;
+    return base + attn_page(P, I.b, key >> P.page_lg) * page_st + (key & ((1 << P.page_lg) - 1)) * st;
+  };
   for (int rr = 0; rr < 32; ++rr) {
     int b, i, h, prow;
     if (!attn_row<STREAM>(P, I, slot, attn_row_of(P, warp * 32 + rr), b, i, h, prow)) continue;
     const uint16_t *q = static_cast<const uint16_t *>(P.q) + b * P.sq[0] + i * P.sq[1] + h * P.sq[2];
-    int p, lo, hi;
+    int p, lo, hi, end;          // keys [lo, hi), and the row's line of the tree between hi and end
+    uint64_t line = 0;
     if (I.prefix()) {
       p = attn_prefix_pos(P, b, i);
-      lo = 0, hi = clampi(p + 1, 0, P.pre);
+      lo = 0, hi = end = clampi(p + 1, 0, P.pre);
+    } else if (PAGED && P.parents) {
+      line = attn_line(P, b, i);
+      lo = 0, hi = I.kl - I.ql, end = hi + i + 1;
+      p = hi + __popcll(line) - 1;
     } else {
       p = I.kl - I.ql + i;
       const int2 v = attn_interval(P, b, p, I.kl, I.pfx);
-      lo = v.x, hi = v.y;
+      lo = v.x, hi = end = v.y;
     }
     const float slope = P.slopes ? P.slopes[h] * 1.4426950408889634f : 0.f;
     float m = -INFINITY, l = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};
     for (int j = 0; j < I.n; ++j) {
       const int k0 = I.k0 + (I.t_hi - 1 - j) * AT_TILE;
       for (int c0 = k0; c0 < k0 + AT_TILE; c0 += 32) {
-        if (c0 + 32 <= lo || c0 >= hi) continue;
+        if (c0 + 32 <= lo || c0 >= end) continue;
         const int key = c0 + lane;
-        const bool seen = key >= lo && key < hi;
+        bool seen = key >= lo && key < hi;
+        if (PAGED) seen |= attn_line_bits(line, c0 - hi) >> lane & 1;
         float x = -INFINITY;
         if (seen) {
-          const uint32_t *kr = reinterpret_cast<const uint32_t *>(kb + (int64_t)key * kst);
+          const uint32_t *kr = reinterpret_cast<const uint32_t *>(row_at(kb, P.sk[0], kst, key));
           const uint32_t *qr = reinterpret_cast<const uint32_t *>(q);
           float s = 0.f;
           for (int d = 0; d < D / 2; ++d) {
@@ -459,7 +513,7 @@ __device__ __forceinline__ void attn_exact_rows(const AttnArgs &P, const AttnIte
             s = fmaf(a.y, c.y, s);
           }
           x = (cap ? P.cap_s * tanhf(s * P.cap_u) : s) * P.scale_log2;
-          x -= slope * fabsf((float)(p - key));
+          x -= slope * fabsf((float)(PAGED && key >= hi ? __popcll(line >> (key - hi)) - 1 : p - key));
         }
         float mx = x;
         for (int o = 16; o; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
@@ -471,9 +525,11 @@ __device__ __forceinline__ void attn_exact_rows(const AttnArgs &P, const AttnIte
         float ps = pr;
         for (int o = 16; o; o >>= 1) ps += __shfl_xor_sync(0xffffffffu, ps, o);
         l += ps;
-        for (int k = max(0, lo - c0); k < min(32, hi - c0); ++k) {   // visible keys only
+        const uint32_t see = PAGED ? __ballot_sync(0xffffffffu, seen) : ~0u;
+        for (int k = max(0, lo - c0); k < min(32, end - c0); ++k) {   // visible keys only
+          if (PAGED && !(see >> k & 1)) continue;
           const float pk = __shfl_sync(0xffffffffu, pr, k);
-          const uint2 w = *reinterpret_cast<const uint2 *>(vb + (int64_t)(c0 + k) * vst + lane * 4);
+          const uint2 w = *reinterpret_cast<const uint2 *>(row_at(vb, P.sv[0], vst, c0 + k) + lane * 4);
           const float2 a = unpack2<FP16>(w.x), c = unpack2<FP16>(w.y);
           acc[0] = fmaf(pk, a.x, acc[0]);
           acc[1] = fmaf(pk, a.y, acc[1]);
@@ -506,7 +562,10 @@ __device__ __forceinline__ void attn_exact_rows(const AttnArgs &P, const AttnIte
 // Every wait is bounded; the TMEM columns are released on every path.
 // STREAM = false: whole units, always as pairs (of a last odd row tile the second is empty).  CAP: 0 none, 1 up to 64, 2 wider
 // (instances of their own: its code in the others costs capped prompts 2%).
-template <bool FP16, int CAP, bool BIAS, bool STREAM>
+// PAGED: keys and values in pages of 16 to 128 tokens, a copy a page and half instead of one a tile and half, the page numbers
+// held 64 a time in the copying warp's registers, the next 32 on their way while the last are used.  A row of a tree of drafts
+// sees the keys before the tree and a line of up to 64 nodes, found by a walk while the first keys are on their way.
+template <bool FP16, int CAP, bool BIAS, bool STREAM, bool PAGED = false>
 __global__ void __launch_bounds__(AT_THREADS, 1) attn_kernel(const __grid_constant__ AttnArgs P) {
   extern __shared__ __align__(1024) uint8_t sm[];   // swizzle atoms: 1024-aligned
   uint64_t *bars = reinterpret_cast<uint64_t *>(sm + AT_OFF_BAR);
@@ -695,6 +754,11 @@ __global__ void __launch_bounds__(AT_THREADS, 1) attn_kernel(const __grid_consta
       for (int b = lane; b < P.batch; b += 32)
         if ((P.kv_len && (P.kv_len[b] < 0 || P.kv_len[b] > P.s_kv)) || (P.q_len && (P.q_len[b] < 0 || P.q_len[b] > P.s_q)))
           atomicOr(status, QV_ERR_BOUNDS);
+    if (PAGED && blockIdx.x == 0)
+      for (int b = lane; b < P.batch; b += 32) {
+        const int ql = P.q_len ? clampi(P.q_len[b], 0, P.s_q) : P.s_q;
+        if (P.ctx_len[b] < 0 || P.ctx_len[b] > P.s_kv - ql) atomicOr(status, QV_ERR_BOUNDS);
+      }
   } else if (warp == AT_W_LOAD) {
     // ---- TMA loads
     const uint32_t qbytes = (uint32_t)(P.G * P.tpt) * 256u, qpbytes = (uint32_t)(P.G * P.s_q * P.nb) * 256u;
@@ -702,19 +766,9 @@ __global__ void __launch_bounds__(AT_THREADS, 1) attn_kernel(const __grid_consta
     bool ok = true;
     AttnItem I;
     while (ok && next_item(I) && I.kind >= 0) {
-      if (I.n > 0 && lane == 0) {
-        const bool prefix = STREAM && I.prefix(), pair = !STREAM || I.pair();
-        const CUtensorMap *mq = prefix ? &P.tqp : &P.tq, *mk = prefix ? &P.tkp : &P.tk, *mv = prefix ? &P.tvp : &P.tv;
-        auto load = [&](const CUtensorMap *map, int j, int bb) {
-          const uint32_t st = c % AT_STAGES;
-          if (!ok || !(ok = attn_wait(&empty[st], ((c / AT_STAGES) & 1) ^ 1, status))) return;
-          const uint32_t dst = smem_u32(sm) + AT_OFF_KV + st * AT_TILE_BYTES;
-          const int t = I.t_hi - 1 - j;
-          mbar_arrive_expect_tx(&full[st], AT_TILE_BYTES);
-          tma_load_4d_at(dst, map, 0, I.g, I.k0 + t * AT_TILE, bb, &full[st]);
-          tma_load_4d_at(dst + AT_HALF_BYTES, map, 64, I.g, I.k0 + t * AT_TILE, bb, &full[st]);
-          ++c;
-        };
+      const bool prefix = STREAM && I.prefix(), pair = !STREAM || I.pair();
+      auto queries = [&]() {   // one lane
+        const CUtensorMap *mq = prefix ? &P.tqp : &P.tq;
         for (int s = 0; ok && s < (pair ? 2 : 1); ++s) {
           const uint32_t qb = qn & 1, dst = smem_u32(sm) + qb * AT_TILE_BYTES;
           if (!(ok = attn_wait(&qempty[qb], ((qn >> 1) & 1) ^ 1, status))) break;
@@ -724,8 +778,9 @@ __global__ void __launch_bounds__(AT_THREADS, 1) attn_kernel(const __grid_consta
           tma_load_4d_at(dst + AT_HALF_BYTES, mq, 64, I.g * P.G, tok, bb, &qfull[qb]);
           ++qn;
         }
-        const int bk = I.b * P.mul_k, bv = I.b * P.mul_v;
-        // in the order of their last use: K0 V0 K1 V1 .. for a pair; K0 K1 V0 K2 V1 K3 .. otherwise
+      };
+      // tiles in the order of their last use: K0 V0 K1 V1 .. for a pair; K0 K1 V0 K2 V1 K3 .. otherwise
+      auto in_order = [&](auto load, const CUtensorMap *mk, const CUtensorMap *mv, int bk, int bv) {
         load(mk, 0, bk);
         if (!pair && I.n > 1) load(mk, 1, bk);
         for (int j = 0; ok && j < I.n; ++j) {
@@ -733,6 +788,49 @@ __global__ void __launch_bounds__(AT_THREADS, 1) attn_kernel(const __grid_consta
           const int jk = j + (pair ? 1 : 2);
           if (jk < I.n) load(mk, jk, bk);
         }
+      };
+      if (PAGED && I.n > 0) {   // the whole warp, in step
+        if (lane == 0) queries();
+        ok = __shfl_sync(0xffffffffu, (int)ok, 0);
+        qn = __shfl_sync(0xffffffffu, qn, 0);
+        const int lg = P.page_lg, per = AT_TILE >> lg, used = (I.kl + (1 << lg) - 1) >> lg;   // pages of a tile, of the sequence
+        auto entry = [&](int e) { return e >= 0 && e < used ? attn_page(P, I.b, e) : 0; };
+        int w = ((I.t_hi - 1) * per) & ~31;   // a tile's pages lie in one window of 32: [w, w + 32) or the one below
+        int here = entry(w + lane), below = entry(w - 32 + lane);
+        in_order([&](const CUtensorMap *map, int j, int) {
+          const uint32_t st = c % AT_STAGES;
+          if (!ok || !(ok = attn_wait_warp(&empty[st], ((c / AT_STAGES) & 1) ^ 1, status))) return;
+          const uint32_t dst = smem_u32(sm) + AT_OFF_KV + st * AT_TILE_BYTES;
+          const int first = (I.t_hi - 1 - j) * per, n = min(per, used - first);   // (values lag by two tiles at most)
+          if (first < w - 32) {
+            w -= 32;
+            here = below;
+            below = entry(w - 32 + lane);
+          }
+          const int e = first >= w ? here : below, at = first - (first >= w ? w : w - 32);
+          if (lane == 0) mbar_arrive_expect_tx(&full[st], (uint32_t)n << (lg + 8));   // pages without keys are left out
+          __syncwarp();
+#pragma unroll 1
+          for (int p = 0; p < n; ++p) {
+            const int pg = __shfl_sync(0xffffffffu, e, at + p);
+            const uint32_t d = dst + ((uint32_t)p << (lg + 7));
+            tma_load_4d_elect(d, map, 0, I.g, 0, pg, &full[st]);
+            tma_load_4d_elect(d + AT_HALF_BYTES, map, 64, I.g, 0, pg, &full[st]);
+          }
+          ++c;
+        }, &P.tk, &P.tv, 0, 0);
+      } else if (!PAGED && I.n > 0 && lane == 0) {
+        queries();
+        in_order([&](const CUtensorMap *map, int j, int bb) {
+          const uint32_t st = c % AT_STAGES;
+          if (!ok || !(ok = attn_wait(&empty[st], ((c / AT_STAGES) & 1) ^ 1, status))) return;
+          const uint32_t dst = smem_u32(sm) + AT_OFF_KV + st * AT_TILE_BYTES;
+          const int t = I.t_hi - 1 - j;
+          mbar_arrive_expect_tx(&full[st], AT_TILE_BYTES);
+          tma_load_4d_at(dst, map, 0, I.g, I.k0 + t * AT_TILE, bb, &full[st]);
+          tma_load_4d_at(dst + AT_HALF_BYTES, map, 64, I.g, I.k0 + t * AT_TILE, bb, &full[st]);
+          ++c;
+        }, prefix ? &P.tkp : &P.tk, prefix ? &P.tvp : &P.tv, I.b * P.mul_k, I.b * P.mul_v);
       }
       ok = __shfl_sync(0xffffffffu, (int)ok, 0);
       if (!STREAM && lane == 0) mbar_arrive(loaded);
@@ -847,6 +945,7 @@ __global__ void __launch_bounds__(AT_THREADS, 1) attn_kernel(const __grid_consta
       struct Slot {
         float m, l;
         int lo, hi, pos;   // pos: an integer, as positions past 2^24 are not all fp32 numbers
+        uint64_t line;     // PAGED: nodes that it sees behind hi
         bool any;
       } S0, S1;
       float slope = 0.f;
@@ -855,12 +954,16 @@ __global__ void __launch_bounds__(AT_THREADS, 1) attn_kernel(const __grid_consta
         const bool valid = attn_row<STREAM>(P, I, slot, R, b, i, h, prow);
         S.any = __any_sync(0xffffffffu, valid);
         S.lo = 0, S.hi = AT_PADDING;   // padding rows take no masks: nothing reads what they compute
-        S.m = -AT_BIG, S.l = 0.f, S.pos = 0;
+        S.m = -AT_BIG, S.l = 0.f, S.pos = 0, S.line = 0;
         if (valid) {
           if (prefix) {
             const int p = attn_prefix_pos(P, b, i);
             S.hi = clampi(p + 1, 0, P.pre);
             if (BIAS) S.pos = p;
+          } else if (PAGED && P.parents) {
+            S.hi = I.kl - I.ql;
+            if (BIAS || I.t_hi * AT_TILE > S.hi) S.line = attn_line(P, b, i);
+            if (BIAS) S.pos = S.hi + __popcll(S.line) - 1;
           } else {
             const int p = I.kl - I.ql + i;
             if (I.clean_lo > 0) {
@@ -970,7 +1073,12 @@ __global__ void __launch_bounds__(AT_THREADS, 1) attn_kernel(const __grid_consta
       // recomputed from rounded logits when one has ended above AT_BIG, or sees keys and holds a sum l of 0.  (Rounding the
       // logits as they come costs a prompt 6%.)  The four warps that share the rows hold the same maxima and sums.
       auto far_out = [&](const Slot &S, float l) {
-        const bool sees = max(S.lo, (I.t_hi - I.n) * AT_TILE) < min(S.hi, I.t_hi * AT_TILE);
+        const int first = (I.t_hi - I.n) * AT_TILE;
+        bool sees = max(S.lo, first) < min(S.hi, I.t_hi * AT_TILE);
+        if (PAGED && S.line) {   // nodes [a, z) of the tree are the item's
+          const int a = max(first - S.hi, 0), z = I.t_hi * AT_TILE - S.hi;
+          sees |= z > 0 && a < 64 && ((z < 64 ? S.line & ((1ull << z) - 1) : S.line) >> a) != 0;
+        }
         return (bool)__any_sync(0xffffffffu, S.hi != AT_PADDING && ((S.m > AT_BIG && S.m < INFINITY) || (l == 0.f && sees)));
       };
       // One slot's S of key tile j (from the last) into probabilities; first: the slot's first tile
@@ -1002,6 +1110,7 @@ __global__ void __launch_bounds__(AT_THREADS, 1) attn_kernel(const __grid_consta
           if (mixed) {   // the row sees keys [lo, hi)
             const int a = clampi(S.lo - c0, 0, 32), z = clampi(S.hi - c0, 0, 32);
             see = (z == 32 ? ~0u : (1u << z) - 1u) & (a == 32 ? 0u : ~0u << a);
+            if (PAGED) see |= attn_line_bits(S.line, c0 - (I.kl - I.ql));
             none = __all_sync(0xffffffffu, see == 0u);
             part = !__all_sync(0xffffffffu, see == ~0u);
           }
@@ -1011,7 +1120,16 @@ __global__ void __launch_bounds__(AT_THREADS, 1) attn_kernel(const __grid_consta
             if (CAP) capped(masks, v, see, S.hi != AT_PADDING);
             if (BIAS) {
               const float sl = P.scale_log2, d0 = (float)(S.pos - c0);
-              if ((P.causal && !P.prefix_len) || __all_sync(0xffffffffu, d0 >= (float)(AT_COLS - 1))) {
+              if (PAGED && mixed && P.parents) {
+                // from one key to the next the distance falls by 1 where the row sees the key, by 0 past another branch's node
+                const int d = c0 - (I.kl - I.ql);
+                float far = (float)(d < 0 ? S.pos - c0 : __popcll(S.line >> min(d, 63)) - 1);
+#pragma unroll
+                for (int c = 0; c < AT_COLS; ++c) {
+                  v[c] = fmaf(-slope, far, v[c] * sl);
+                  if (see >> c & 1) far -= 1.f;
+                }
+              } else if ((P.causal && !P.prefix_len) || __all_sync(0xffffffffu, d0 >= (float)(AT_COLS - 1))) {
                 // no key behind the row's position is seen: -slope |p - j| = -slope (p - c0) + slope (j - c0)
                 const uint64_t sl2 = pack_f2(sl, sl), hop = pack_f2(2.f * slope, 2.f * slope);
                 uint64_t b2 = pack_f2(0.f, slope);
@@ -1183,7 +1301,7 @@ __global__ void __launch_bounds__(AT_THREADS, 1) attn_kernel(const __grid_consta
             __syncwarp();
           }
         } else if (any_row && side == 0) {
-          attn_exact_rows<FP16, false>(P, I, slot, wq, lane, CAP,
+          attn_exact_rows<FP16, false, PAGED>(P, I, slot, wq, lane, CAP,
                                        [&](int rb, int ri, int rh, int, const float (&acc)[4], float rm, float rl) {
             const float f = rl == 0.f ? 0.f : 1.f / rl;
             if (lane == 0 && P.lse)
@@ -1285,7 +1403,7 @@ __global__ void __launch_bounds__(AT_THREADS, 1) attn_kernel(const __grid_consta
                             __ballot_sync(0xffffffffu, valid), lane, P.wide_out, w);
           }
         } else if (quarter == 0) {
-          attn_exact_rows<FP16, true>(P, I, slot, wq, lane, CAP,
+          attn_exact_rows<FP16, true, PAGED>(P, I, slot, wq, lane, CAP,
                                 [&](int rb, int ri, int rh, int rp, const float (&acc)[4], float rm, float rl) {
             const float ri_l = rl == 0.f ? 0.f : 1.f / rl;
             const float o0 = rl == 0.f ? 0.f : acc[0] * ri_l, o1 = rl == 0.f ? 0.f : acc[1] * ri_l;
@@ -1330,14 +1448,14 @@ cudaError_t launch_attn_kernel(Kernel kern, const AttnArgs &P, int grid, cudaStr
   return cudaLaunchKernelEx(&cfg, kern, P);
 }
 
-template <bool FP16, int CAP, bool BIAS>
+template <bool FP16, int CAP, bool BIAS, bool PAGED = false>
 cudaError_t launch_attn_variant(const AttnArgs &P, int grid, cudaStream_t s) {
   static SmemOptIn units, stream;
-  cudaError_t e = P.stream ? stream.ensure(attn_kernel<FP16, CAP, BIAS, true>, AT_SMEM)
-                           : units.ensure(attn_kernel<FP16, CAP, BIAS, false>, AT_SMEM);
+  cudaError_t e = P.stream ? stream.ensure(attn_kernel<FP16, CAP, BIAS, true, PAGED>, AT_SMEM)
+                           : units.ensure(attn_kernel<FP16, CAP, BIAS, false, PAGED>, AT_SMEM);
   if (e != cudaSuccess) return e;
-  return P.stream ? launch_attn_kernel(attn_kernel<FP16, CAP, BIAS, true>, P, grid, s)
-                  : launch_attn_kernel(attn_kernel<FP16, CAP, BIAS, false>, P, grid, s);
+  return P.stream ? launch_attn_kernel(attn_kernel<FP16, CAP, BIAS, true, PAGED>, P, grid, s)
+                  : launch_attn_kernel(attn_kernel<FP16, CAP, BIAS, false, PAGED>, P, grid, s);
 }
 
 }  // namespace qv

@@ -1,0 +1,763 @@
+// The paged KV cache: bookkeeping of pages (reserving, forking, giving back, compacting) and the copies of rows that go
+// with it (writing new rows, accepting drafted ones, pages copied on write or moved).
+//
+// The bookkeeping is integer work on a few KB and bound by latency: one CTA, or one per sequence or block of columns,
+// and no value that depends on the order of atomics (counts only; which page goes where follows from prefix sums).  The
+// copies are bound by memory: 16 bytes a thread, eight loads in flight, nothing staged.
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cstdint>
+
+#include "common.cuh"
+#include "qevict.h"
+
+namespace qv {
+namespace {
+
+constexpr int PG_BATCH = 1024;   // sequences of a cache: a thread each where one CTA plans for all
+constexpr int PG_PATH = 256;     // accepted rows of a sequence
+constexpr int PG_HEADER = 64;    // int32 in front of the arrays
+
+struct PagesDev {
+  uint16_t *k, *v;
+  int64_t sk[4], sv[4];          // layer, page, token, head
+  int layers, pages, page, lg, h_kv, batch, max_pages, words;   // lg: log2 page; words: of the free bits, a multiple of 4
+  int *status, *n_free, *moves, *n_copies;
+  int *length, *held, *table, *refs;
+  uint32_t *bits;
+  int *tickets;                  // [batch + 1] CTAs that have read what the last one changes; 0 between calls
+  int4 *copies;                  // [batch] of a reserve: page, its copy, rows to copy
+  int *from, *to, *goes;         // [pages] of a compaction: r-th page that moves, its new place; new place of each
+};
+
+// (Programmatic launches: a kernel's setup overlaps the end of the one before.  Nothing is read before the wait, and the
+// next kernel is let in only behind it.)
+__device__ __forceinline__ void pages_begin() {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
+// Tokens of a sequence, whatever stands in the arrays: within the pages that it holds.
+__device__ __forceinline__ int held_of(const PagesDev &P, int b) { return min(max(P.held[b], 0), P.max_pages); }
+__device__ __forceinline__ int length_of(const PagesDev &P, int b, int held) { return min(max(P.length[b], 0), held << P.lg); }
+__device__ __forceinline__ bool is_page(const PagesDev &P, int p) { return (unsigned)p < (unsigned)P.pages; }
+__device__ __forceinline__ int *row_of(const PagesDev &P, int b) { return P.table + (int64_t)b * P.max_pages; }
+
+// One table entry of page p less.  True: it was the last, and the page is free now.
+__device__ __forceinline__ bool give_back(const PagesDev &P, int p) {
+  if (atomicSub(&P.refs[p], 1) != 1) return false;
+  atomicOr(&P.bits[p >> 5], 1u << (p & 31));
+  return true;
+}
+
+// Exclusive sum over a CTA of 32 warps; `total` for every thread.  Two barriers.
+__device__ __forceinline__ int scan_1024(int x, int *warps, int &total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int s = x;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, s, o);
+    if (lane >= o) s += y;
+  }
+  __syncthreads();   // what stood in warps has been read
+  if (lane == 31) warps[warp] = s;
+  __syncthreads();
+  const int w = warps[lane];
+  const int before = __reduce_add_sync(0xffffffffu, lane < warp ? w : 0);
+  total = __reduce_add_sync(0xffffffffu, w);
+  return before + s - x;
+}
+
+// ----------------------------------------------------------------------------- start
+
+__global__ void pages_clear_kernel(PagesDev P) {
+  pages_begin();
+  const int i = blockIdx.x * blockDim.x + threadIdx.x;
+  if (i < PG_HEADER) P.status[i] = 0;
+  if (i <= P.batch) P.tickets[i] = 0;
+  if (i < P.pages) {
+    P.refs[i] = 0;
+    P.goes[i] = -1;   // here: the place in the tables where the page was first seen
+  }
+}
+
+__global__ void pages_adopt_kernel(PagesDev P, const int *table, const int *length) {
+  __shared__ int first_none;
+  pages_begin();
+  const int b = blockIdx.x;
+  const int *src = table ? table + (int64_t)b * P.max_pages : nullptr;
+  if (threadIdx.x == 0) first_none = P.max_pages;
+  __syncthreads();
+  if (table)
+    for (int c = threadIdx.x; c < P.max_pages; c += blockDim.x)
+      if (!is_page(P, src[c])) {
+        atomicMin(&first_none, c);
+        break;   // this thread's later ones lie behind it
+      }
+  __syncthreads();
+  const int held = table ? first_none : 0;
+  int *dst = row_of(P, b);
+  for (int c = threadIdx.x; c < P.max_pages; c += blockDim.x) {
+    const int p = table ? src[c] : -1;
+    dst[c] = c < held ? p : -1;
+    if (c < held) {
+      atomicAdd(&P.refs[p], 1);
+      const int seen = atomicCAS(&P.goes[p], -1, c);
+      if (seen != -1 && seen != c) atomicOr(P.status, QV_ERR_STATE);
+    } else if (c == held && p != -1) {
+      atomicOr(P.status, QV_ERR_BOUNDS);
+    }
+  }
+  if (threadIdx.x == 0) {
+    const int n = length ? length[b] : 0, fit = min(max(n, 0), held << P.lg);
+    if (n != fit) atomicOr(P.status, QV_ERR_BOUNDS);
+    P.length[b] = fit;
+    P.held[b] = held;
+  }
+}
+
+__global__ void pages_free_bits_kernel(PagesDev P) {
+  pages_begin();
+  const int w = blockIdx.x * blockDim.x + threadIdx.x;
+  uint32_t x = 0;
+  for (int i = 0; i < 32 && w * 32 + i < P.pages; ++i)
+    if (P.refs[w * 32 + i] == 0) x |= 1u << i;
+  if (w < P.words) P.bits[w] = x;
+  const int n = __reduce_add_sync(0xffffffffu, __popc(x));
+  if ((threadIdx.x & 31) == 0 && n) atomicAdd(P.n_free, n);
+}
+
+// ----------------------------------------------------------------------------- rows
+
+// Place of 16-byte piece x, (row, head, 16th of the channels), of a page that starts at `base`.  DENSE: rows follow one another.
+template <bool DENSE>
+__device__ __forceinline__ int64_t piece_at(const int64_t (&st)[4], int64_t base, int h_kv, uint32_t x) {
+  if (DENSE) return base + (int64_t)x * 8;
+  const uint32_t h = x >> 4, r = h / (uint32_t)h_kv;
+  return base + r * st[2] + (h - r * h_kv) * st[3] + (x & 15) * 8;
+}
+
+// A part (of PART_PIECES pieces of 16 bytes) of the first `rows` rows of page a, copied to page z by a CTA of 256 threads.
+constexpr int PART_PIECES = 2048;
+template <bool DENSE>
+__device__ __forceinline__ void copy_part(uint16_t *pool, const int64_t (&st)[4], int layer, int a, int z, int rows, int h_kv,
+                                          int part) {
+  const uint32_t n = (uint32_t)rows * h_kv * 16, x = (uint32_t)part * PART_PIECES + threadIdx.x;
+  const int64_t ba = layer * st[0] + a * st[1], bz = layer * st[0] + z * st[1];
+  uint4 w[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    if (x + i * 256 < n) w[i] = *reinterpret_cast<const uint4 *>(pool + piece_at<DENSE>(st, ba, h_kv, x + i * 256));
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    if (x + i * 256 < n) *reinterpret_cast<uint4 *>(pool + piece_at<DENSE>(st, bz, h_kv, x + i * 256)) = w[i];
+}
+
+// Copies in turn over the grid: unit u is a part of one copy's page in one layer, keys or values.
+template <bool DENSE, typename Copy>
+__device__ __forceinline__ void copy_all(const PagesDev &P, int n, const Copy &copy) {
+  const int parts = (P.page * P.h_kv * 16 + PART_PIECES - 1) / PART_PIECES, per = parts * 2 * P.layers;
+  const int64_t units = (int64_t)n * per;
+  for (int64_t u = blockIdx.x; u < units; u += gridDim.x) {
+    const int r = (int)(u / per), y = (int)(u - (int64_t)r * per), l2 = y / parts, part = y - l2 * parts;
+    const int4 c = copy(r);
+    if (l2 & 1)
+      copy_part<DENSE>(P.v, P.sv, l2 >> 1, c.x, c.y, c.z, P.h_kv, part);
+    else
+      copy_part<DENSE>(P.k, P.sk, l2 >> 1, c.x, c.y, c.z, P.h_kv, part);
+  }
+}
+
+struct RowsDev {
+  const uint16_t *k, *v;
+  int64_t sk[4], sv[4];          // layer, sequence, token, head
+  int layer, layers, n;
+  const int *d_n;
+};
+
+// New rows: a CTA takes 4 pieces a thread of one (layer, sequence), keys and values, so eight loads are in flight.
+constexpr int APPEND_THREADS = 256, APPEND_PIECES = 4;
+__global__ void __launch_bounds__(APPEND_THREADS) pages_append_kernel(const __grid_constant__ PagesDev P,
+                                                                     const __grid_constant__ RowsDev R) {
+  pages_begin();
+  const int b = blockIdx.y, held = held_of(P, b), len = length_of(P, b, held);
+  int n = R.n;
+  if (R.d_n) {
+    const int want = R.d_n[b];
+    n = min(max(want, 0), R.n);
+    if (want != n && threadIdx.x == 0 && blockIdx.x == 0) atomicOr(P.status, QV_ERR_BOUNDS);
+  }
+  const int *row = row_of(P, b);
+  const uint32_t per_row = (uint32_t)P.h_kv * 16, all = (uint32_t)n * per_row;
+  const uint32_t x0 = blockIdx.x * (APPEND_THREADS * APPEND_PIECES) + threadIdx.x;
+  if (x0 >= all) return;
+  for (int l = blockIdx.z; l < R.layers; l += gridDim.z) {
+    uint4 wk[APPEND_PIECES], wv[APPEND_PIECES];
+    int64_t at[APPEND_PIECES][2];
+#pragma unroll
+    for (int i = 0; i < APPEND_PIECES; ++i) {
+      const uint32_t x = x0 + i * APPEND_THREADS;
+      at[i][0] = -1;
+      if (x >= all) continue;
+      const uint32_t t = x / per_row, y = x - t * per_row, h = y >> 4, c = (y & 15) * 8;
+      wk[i] = *reinterpret_cast<const uint4 *>(R.k + l * R.sk[0] + b * R.sk[1] + t * R.sk[2] + h * R.sk[3] + c);
+      wv[i] = *reinterpret_cast<const uint4 *>(R.v + l * R.sv[0] + b * R.sv[1] + t * R.sv[2] + h * R.sv[3] + c);
+      const int64_t pos = (int64_t)len + t;
+      const int pg = pos < (int64_t)held << P.lg ? row[pos >> P.lg] : -1, off = (int)pos & (P.page - 1);
+      if (!is_page(P, pg) || P.refs[pg] != 1) {
+        if (y == 0) atomicOr(P.status, QV_ERR_BOUNDS);
+        continue;
+      }
+      const int64_t ll = R.layer + l;
+      at[i][0] = ll * P.sk[0] + pg * P.sk[1] + off * P.sk[2] + h * P.sk[3] + c;
+      at[i][1] = ll * P.sv[0] + pg * P.sv[1] + off * P.sv[2] + h * P.sv[3] + c;
+    }
+#pragma unroll
+    for (int i = 0; i < APPEND_PIECES; ++i)
+      if (at[i][0] >= 0) {
+        *reinterpret_cast<uint4 *>(P.k + at[i][0]) = wk[i];
+        *reinterpret_cast<uint4 *>(P.v + at[i][1]) = wv[i];
+      }
+  }
+}
+
+// Accepted rows move down their sequence.  A thread owns 16 bytes of every row of one (layer, K or V, head) and moves them in
+// ascending order, eight rows at a time, all loads before the stores: row path[j] >= j, so a row is read before anything
+// lands on it, and no other thread touches these bytes.  The sequence's last CTA to have read its length counts the rows in.
+__global__ void __launch_bounds__(256) pages_accept_kernel(const __grid_constant__ PagesDev P, const int *d_count,
+                                                          const int *d_path, int max_path) {
+  __shared__ int s_from[PG_PATH], s_to[PG_PATH], last;   // page << 7 | row
+  pages_begin();
+  const int b = blockIdx.y, held = held_of(P, b), len = length_of(P, b, held), count = d_count[b];
+  const int *row = row_of(P, b);
+  const int64_t room = (int64_t)held << P.lg;
+  bool ok = count >= 0 && (!d_path || count <= max_path) && (int64_t)len + count <= room;
+  if (ok && d_path) {
+    const int *path = d_path + (int64_t)b * max_path;
+    for (int j = threadIdx.x; j < count; j += blockDim.x) {
+      const int p = path[j];
+      if (p < 0 || (int64_t)len + p >= room || (j && path[j - 1] >= p)) {
+        ok = false;
+        break;
+      }
+      const int src = row[(len + p) >> P.lg], dst = row[(len + j) >> P.lg];
+      if (!is_page(P, src) || !is_page(P, dst) || P.refs[dst] != 1) {
+        ok = false;
+        break;
+      }
+      s_from[j] = p == j ? -1 : src << 7 | ((len + p) & (P.page - 1));
+      s_to[j] = dst << 7 | ((len + j) & (P.page - 1));
+    }
+  } else if (ok) {   // rows that shared pages hold were never written
+    for (int c = (len >> P.lg) + threadIdx.x; (int64_t)c << P.lg < (int64_t)len + count; c += blockDim.x)
+      if (!is_page(P, row[c]) || P.refs[row[c]] != 1) ok = false;
+  }
+  ok = __syncthreads_and(ok);
+  if (threadIdx.x == 0) {
+    last = gridDim.x == 1;
+    if (!last) {
+      __threadfence();
+      last = atomicAdd(&P.tickets[b], 1) == (int)gridDim.x - 1;
+      if (last) P.tickets[b] = 0;
+    }
+    if (last && !ok) atomicOr(P.status, QV_ERR_BOUNDS);
+    if (last && ok) P.length[b] = len + count;
+  }
+  if (!ok || !d_path) return;
+  const uint32_t x = blockIdx.x * blockDim.x + threadIdx.x, h = x >> 4, l2 = h / (uint32_t)P.h_kv;
+  if (l2 >= 2u * P.layers) return;
+  const bool is_v = l2 & 1;
+  uint16_t *pool = is_v ? P.v : P.k;
+  const int64_t st_p = is_v ? P.sv[1] : P.sk[1], st_t = is_v ? P.sv[2] : P.sk[2];
+  pool += (l2 >> 1) * (is_v ? P.sv[0] : P.sk[0]) + (h - l2 * P.h_kv) * (is_v ? P.sv[3] : P.sk[3]) + (x & 15) * 8;
+  auto at = [&](int e) { return reinterpret_cast<uint4 *>(pool + (e >> 7) * st_p + (e & 127) * st_t); };
+  for (int j0 = 0; j0 < count; j0 += 8) {
+    uint4 w[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (j0 + j < count && s_from[j0 + j] >= 0) w[j] = *at(s_from[j0 + j]);
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (j0 + j < count && s_from[j0 + j] >= 0) *at(s_to[j0 + j]) = w[j];
+  }
+}
+
+// ----------------------------------------------------------------------------- pages
+
+// Who needs which pages, a thread a sequence; then the free bits are walked from the lowest page on, 128 a thread at a
+// time, and the r-th free page goes to whom the running sum of needs says.  Nothing is written before it is known to
+// suffice.  Bound by latency: 3 barriers' worth and a scan per 131072 pages.
+__global__ void __launch_bounds__(1024) pages_reserve_kernel(const __grid_constant__ PagesDev P, const int *d_new, int n_new) {
+  __shared__ int s_tail[PG_BATCH], s_start[PG_BATCH], s_len[PG_BATCH], s_held[PG_BATCH], s_copy[PG_BATCH], s_warp[32];
+  pages_begin();
+  const int t = threadIdx.x;
+  int len = 0, held = 0, add = 0, tail = -1, refs = 0;
+  bool bad = false;
+  if (t < P.batch) {
+    held = held_of(P, t);
+    len = length_of(P, t, held);
+    const int64_t n = d_new ? d_new[t] : n_new, want = (len + n + P.page - 1) >> P.lg;
+    bad = n < 0 || want > P.max_pages;
+    if (!bad && n > 0) {
+      add = max((int)want - held, 0);
+      if (len & (P.page - 1)) {
+        tail = row_of(P, t)[len >> P.lg];
+        bad = !is_page(P, tail);
+        if (!bad) refs = P.refs[tail];
+      }
+    }
+    s_tail[t] = tail, s_len[t] = len, s_held[t] = held;
+  }
+  if (t == 0) *P.n_copies = 0;
+  const int n_free = *P.n_free;
+  if (__syncthreads_or(bad)) {
+    if (t == 0) atomicOr(P.status, QV_ERR_BOUNDS);
+    return;
+  }
+  bool copy = false;
+  if (refs > 1) {   // shared: by how many that reserve now, and is this the first of them
+    int same = 0, before = 0;
+    for (int j = 0; j < P.batch; ++j)
+      if (s_tail[j] == tail) {
+        ++same;
+        before += j < t;
+      }
+    copy = same < refs || before > 0;
+  }
+  int total;
+  const int start = scan_1024(add + copy, s_warp, total);
+  int copies;
+  const int c_at = scan_1024(copy, s_warp, copies);
+  if (total > n_free) {
+    if (t == 0) atomicOr(P.status, QV_ERR_SLOT);
+    return;
+  }
+  if (total == 0) return;
+  if (t < P.batch) s_start[t] = start, s_copy[t] = copy ? c_at : -1;
+  if (t == 0) *P.n_copies = copies;
+  __syncthreads();
+  auto assign = [&](int r, int id) {
+    int lo = 0, hi = P.batch - 1;   // the last sequence that starts at r or before: it needs pages
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (s_start[mid] <= r)
+        lo = mid;
+      else
+        hi = mid - 1;
+    }
+    const int k = r - s_start[lo], l = s_len[lo];
+    int *row = row_of(P, lo);
+    if (s_copy[lo] >= 0 && k == 0) {
+      P.copies[s_copy[lo]] = make_int4(s_tail[lo], id, l & (P.page - 1), 0);
+      row[l >> P.lg] = id;
+    } else {
+      row[s_held[lo] + k - (s_copy[lo] >= 0)] = id;
+    }
+    P.refs[id] = 1;
+  };
+  int found = 0;
+  for (int base = 0; base < P.words && found < total; base += 4 * 1024) {
+    const int w = base + 4 * t;
+    uint4 x = make_uint4(0, 0, 0, 0);
+    if (w < P.words) x = *reinterpret_cast<const uint4 *>(P.bits + w);
+    int here;
+    int r = found + scan_1024(__popc(x.x) + __popc(x.y) + __popc(x.z) + __popc(x.w), s_warp, here);
+    uint32_t q[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      uint32_t left = q[i];
+      while (left && r < total) {
+        const int id = (w + i) * 32 + __ffs(left) - 1;
+        left &= left - 1;
+        if (is_page(P, id)) assign(r, id);
+        ++r;
+      }
+      if (left != q[i]) P.bits[w + i] = left;
+    }
+    found += here;
+  }
+  if (copy) atomicSub(&P.refs[tail], 1);
+  if (add) P.held[t] = held + add;
+  if (t == 0) {
+    *P.n_free = n_free - total;
+    if (found < total) {   // the count and the bits disagree: not every copy has a page
+      *P.n_copies = 0;
+      atomicOr(P.status, QV_ERR_STATE);
+    }
+  }
+}
+
+// The rows of the pages that a reserve copied.
+template <bool DENSE>
+__global__ void __launch_bounds__(256) pages_tail_kernel(const __grid_constant__ PagesDev P) {
+  pages_begin();
+  copy_all<DENSE>(P, *P.n_copies, [&](int r) { return P.copies[r]; });
+}
+
+// Tables rearranged.  A CTA takes 8 places of all sequences: it reads them all before it writes any, and since a page stands at
+// one place of the tables, it counts every entry that a page gains before the ones it loses.  The last CTA to have
+// read lengths rearranges those.
+constexpr int SELECT_COLS = 8;
+__global__ void __launch_bounds__(1024) pages_select_kernel(const __grid_constant__ PagesDev P, const int *d_src) {
+  __shared__ int s_old[PG_BATCH * SELECT_COLS], last, given;
+  pages_begin();
+  const int t = threadIdx.x;
+  int src = t, held = 0, len = 0, n_held = 0, n_len = 0;
+  if (t < P.batch) {
+    src = d_src[t];
+    if (src < -1 || src >= P.batch) {
+      if (blockIdx.x == 0) atomicOr(P.status, QV_ERR_BOUNDS);
+      src = t;
+    }
+    held = held_of(P, t), len = length_of(P, t, held);
+    n_held = held, n_len = len;
+    if (src < 0) {
+      n_held = n_len = 0;
+    } else if (src != t) {
+      n_len = length_of(P, src, held_of(P, src));
+      n_held = (n_len + P.page - 1) >> P.lg;
+    }
+  }
+  if (t == 0) given = 0;
+  const int c0 = blockIdx.x * SELECT_COLS;
+  const bool work = __syncthreads_or(src != t && c0 < max(held, n_held));
+  if (work) {
+    const int cells = P.batch * SELECT_COLS;
+    for (int i = t; i < cells; i += 1024) {
+      const int c = c0 + i % SELECT_COLS;
+      s_old[i] = c < P.max_pages ? row_of(P, i / SELECT_COLS)[c] : -1;
+    }
+    __syncthreads();
+    const int n = min(SELECT_COLS, P.max_pages - c0);
+    if (src != t)
+      for (int c = 0; c < n; ++c) {
+        const int p = c0 + c < n_held ? s_old[src * SELECT_COLS + c] : -1;
+        if (is_page(P, p)) atomicAdd(&P.refs[p], 1);
+        row_of(P, t)[c0 + c] = p;
+      }
+    __threadfence();
+    __syncthreads();
+    int free = 0;
+    if (src != t)
+      for (int c = 0; c < n; ++c) {
+        const int p = s_old[t * SELECT_COLS + c];
+        if (c0 + c < held && is_page(P, p)) free += give_back(P, p);
+      }
+    if (free) atomicAdd(&given, free);
+    __syncthreads();
+    if (t == 0 && given) atomicAdd(P.n_free, given);
+  }
+  if (t == 0) {
+    __threadfence();
+    last = atomicAdd(&P.tickets[P.batch], 1) == (int)gridDim.x - 1;
+    if (last) P.tickets[P.batch] = 0;
+  }
+  __syncthreads();
+  if (last && t < P.batch && src != t) {   // every thread has read lengths above, before the barrier
+    P.length[t] = n_len;
+    P.held[t] = n_held;
+  }
+}
+
+__global__ void __launch_bounds__(256) pages_trim_kernel(const __grid_constant__ PagesDev P, const int *d_length) {
+  __shared__ int given;
+  pages_begin();
+  const int b = blockIdx.x, want = d_length[b], held = held_of(P, b), len = min(length_of(P, b, held), want);
+  if (want < 0) return;
+  if (threadIdx.x == 0) given = 0;
+  __syncthreads();   // also: held and length have been read
+  const int keep = (len + P.page - 1) >> P.lg;
+  int *row = row_of(P, b), free = 0;
+  for (int c = keep + threadIdx.x; c < held; c += blockDim.x) {
+    const int p = row[c];
+    row[c] = -1;
+    if (is_page(P, p)) free += give_back(P, p);
+  }
+  if (free) atomicAdd(&given, free);
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    P.length[b] = len;
+    P.held[b] = min(held, keep);
+    if (given) atomicAdd(P.n_free, given);
+  }
+}
+
+// Which pages move where: the r-th used page from n on to the r-th free one below n, n pages being in use.
+__global__ void __launch_bounds__(1024) pages_plan_kernel(const __grid_constant__ PagesDev P) {
+  __shared__ int s_warp[32];
+  pages_begin();
+  const int t = threadIdx.x, n = P.pages - *P.n_free;
+  auto below = [](int edge, int w) {   // bits of word w whose page is below edge
+    const int k = edge - w * 32;
+    return k >= 32 ? ~0u : k <= 0 ? 0u : (1u << k) - 1u;
+  };
+  int from = 0, to = 0;
+  for (int base = 0; base < P.words; base += 4 * 1024) {
+    const int w = base + 4 * t;
+    uint4 x = make_uint4(0, 0, 0, 0);
+    if (w < P.words) x = *reinterpret_cast<const uint4 *>(P.bits + w);
+    const uint32_t q[4] = {x.x, x.y, x.z, x.w};
+    uint32_t hole[4], used[4];
+    int nh = 0, nu = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      hole[i] = q[i] & below(n, w + i);
+      used[i] = ~q[i] & below(P.pages, w + i) & ~below(n, w + i);
+      nh += __popc(hole[i]);
+      nu += __popc(used[i]);
+    }
+    int all_h, all_u;
+    int rh = to + scan_1024(nh, s_warp, all_h), ru = from + scan_1024(nu, s_warp, all_u);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      for (uint32_t y = hole[i]; y; y &= y - 1) P.to[rh++] = (w + i) * 32 + __ffs(y) - 1;
+      for (uint32_t y = used[i]; y; y &= y - 1) P.from[ru++] = (w + i) * 32 + __ffs(y) - 1;
+    }
+    to += all_h, from += all_u;
+  }
+  const bool fits = from == to;   // else the count of free pages and their bits disagree: nothing moves
+  if (t == 0) {
+    *P.moves = fits ? from : 0;
+    if (!fits) atomicOr(P.status, QV_ERR_STATE);
+  }
+  if (!fits || !from) return;
+  __syncthreads();
+  for (int r = t; r < from; r += 1024) {
+    const int a = P.from[r], z = P.to[r];
+    P.refs[z] = P.refs[a];
+    P.refs[a] = 0;
+    P.goes[a] = z;
+  }
+  for (int w = t; w < P.words; w += 1024) P.bits[w] = below(P.pages, w) & ~below(n, w);
+}
+
+// The moves themselves, and the tables.
+template <bool DENSE>
+__global__ void __launch_bounds__(256) pages_move_kernel(const __grid_constant__ PagesDev P) {
+  pages_begin();
+  const int moves = *P.moves, n = P.pages - *P.n_free;
+  if (!moves) return;
+  copy_all<DENSE>(P, moves, [&](int r) { return make_int4(P.from[r], P.to[r], P.page, 0); });
+  const int cells = P.batch * P.max_pages;
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < cells; i += (int64_t)gridDim.x * 256) {
+    const int p = P.table[i];
+    if (p >= n && is_page(P, p)) P.table[i] = P.goes[p];
+  }
+}
+
+// ----------------------------------------------------------------------------- host
+
+bool dims_ok(const int64_t *st, const int64_t *size, int dims, bool zero) {
+  for (int i = 0; i < dims; ++i)
+    if (size[i] > 1 && (st[i] % 8 || st[i] >= (1ll << 40) || st[i] > (1ll << 48) / (size[i] - 1) || st[i] < (zero ? 0 : 8)))
+      return false;
+  return true;
+}
+
+// No two elements in one place: each dimension steps over all that the smaller steps reach.
+bool apart(const int64_t *st, const int64_t *size_in, int dims) {
+  int64_t size[4], reach = D;
+  for (int i = 0; i < dims; ++i) size[i] = size_in[i];
+  for (int n = 0; n < dims; ++n) {
+    int best = -1;
+    for (int i = 0; i < dims; ++i)
+      if (size[i] > 1 && (best < 0 || st[i] < st[best])) best = i;
+    if (best < 0) break;
+    if (st[best] < reach) return false;
+    reach += st[best] * (size[best] - 1);
+    size[best] = 1;
+  }
+  return true;
+}
+
+struct PagesPlan {
+  qevict_pages_layout lay;
+  int64_t tickets, copies, from, to, goes;
+  int words;
+  bool dense;
+};
+
+qevict_status pages_plan(const qevict_pages_desc *d, PagesPlan *p) {
+  if (!d || d->layers < 1 || d->layers > 32767 || d->pages < 1 || d->pages > (1 << 24) ||
+      (d->page != 16 && d->page != 32 && d->page != 64 && d->page != 128) || d->h_kv < 1 || d->h_kv > 4096 || d->d_head != D ||
+      d->batch < 1 || d->batch > PG_BATCH || d->max_pages < 1 || d->max_pages > (1 << 30) / d->page ||
+      (int64_t)d->batch * d->max_pages > (1 << 30) || d->reserved0)
+    return QEVICT_EINVAL;
+  const int64_t size[4] = {d->layers, d->pages, d->page, d->h_kv};
+  if (!dims_ok(d->k, size, 4, false) || !dims_ok(d->v, size, 4, false) || !apart(d->k, size, 4) || !apart(d->v, size, 4))
+    return QEVICT_EINVAL;
+  int64_t off = PG_HEADER;
+  auto take = [&](int64_t n) {
+    const int64_t o = off;
+    off += (n + 63) & ~int64_t(63);   // 256 bytes
+    return o;
+  };
+  p->words = (d->pages + 127) / 128 * 4;
+  p->lay.status = 0;
+  p->lay.n_free = 1;
+  p->lay.length = take(d->batch);
+  p->lay.held = take(d->batch);
+  p->lay.table = take((int64_t)d->batch * d->max_pages);
+  p->lay.refs = take(d->pages);
+  p->lay.free_bits = take(p->words);
+  p->tickets = take(d->batch + 1);
+  p->copies = take((int64_t)d->batch * 4);
+  p->from = take(d->pages);
+  p->to = take(d->pages);
+  p->goes = take(d->pages);
+  p->lay.ints = off;
+  auto rows_follow = [&](const int64_t *st) {
+    return (d->h_kv == 1 || st[3] == D) && st[2] == (int64_t)d->h_kv * D;
+  };
+  p->dense = rows_follow(d->k) && rows_follow(d->v);
+  return QEVICT_OK;
+}
+
+qevict_status pages_args(const qevict_pages_desc *d, bool pool, void *k, void *v, void *d_state, PagesPlan *p, PagesDev *P) {
+  const qevict_status st = pages_plan(d, p);
+  if (st != QEVICT_OK) return st;
+  if (!d_state || ((uintptr_t)d_state & 255) || (pool && (!k || !v || (((uintptr_t)k | (uintptr_t)v) & 15))))
+    return QEVICT_EINVAL;
+  int *s = static_cast<int *>(d_state);
+  *P = PagesDev();
+  P->k = static_cast<uint16_t *>(k), P->v = static_cast<uint16_t *>(v);
+  for (int i = 0; i < 4; ++i) P->sk[i] = d->k[i], P->sv[i] = d->v[i];
+  P->layers = d->layers, P->pages = d->pages, P->page = d->page, P->h_kv = d->h_kv, P->batch = d->batch;
+  P->max_pages = d->max_pages, P->words = p->words;
+  P->lg = d->page == 16 ? 4 : d->page == 32 ? 5 : d->page == 64 ? 6 : 7;
+  P->status = s, P->n_free = s + 1, P->moves = s + 2, P->n_copies = s + 3;
+  P->length = s + p->lay.length, P->held = s + p->lay.held, P->table = s + p->lay.table, P->refs = s + p->lay.refs;
+  P->bits = reinterpret_cast<uint32_t *>(s + p->lay.free_bits);
+  P->tickets = s + p->tickets, P->copies = reinterpret_cast<int4 *>(s + p->copies);
+  P->from = s + p->from, P->to = s + p->to, P->goes = s + p->goes;
+  return QEVICT_OK;
+}
+
+template <typename... Params, typename... Args>
+bool launch(void (*kern)(Params...), dim3 grid, int threads, qevict_stream_t stream, const Args &...args) {
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.stream = reinterpret_cast<cudaStream_t>(stream);
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, args...) == cudaSuccess;
+}
+
+unsigned ceil_div(int64_t x, int64_t y) { return (unsigned)((x + y - 1) / y); }
+// At most `most` pages to copy: no more CTAs than eight on each of 152 SMs.
+dim3 copy_grid(const PagesDev &P, int64_t most) {
+  const int64_t parts = ceil_div((int64_t)P.page * P.h_kv * 16, PART_PIECES);
+  return dim3((unsigned)std::min<int64_t>(most * parts * 2 * P.layers, 152 * 8));
+}
+bool word_ok(const void *p, bool needed) { return !((uintptr_t)p & 3) && (p || !needed); }
+
+}  // namespace
+}  // namespace qv
+
+extern "C" {
+
+qevict_status qevict_pages_get_layout(const qevict_pages_desc *desc, qevict_pages_layout *layout) {
+  qv::PagesPlan p;
+  if (!layout) return QEVICT_EINVAL;
+  const qevict_status st = qv::pages_plan(desc, &p);
+  if (st == QEVICT_OK) *layout = p.lay;
+  return st;
+}
+
+qevict_status qevict_pages_load(const qevict_pages_desc *desc, void *d_state, const int32_t *d_table, const int32_t *d_length,
+                                qevict_stream_t stream) {
+  qv::PagesPlan p;
+  qv::PagesDev P;
+  const qevict_status st = qv::pages_args(desc, false, nullptr, nullptr, d_state, &p, &P);
+  if (st != QEVICT_OK) return st;
+  if (!qv::word_ok(d_table, false) || !qv::word_ok(d_length, false) || !d_table != !d_length) return QEVICT_EINVAL;
+  const int64_t n = std::max<int64_t>(std::max(P.pages, P.batch + 1), qv::PG_HEADER);
+  const bool ok = qv::launch(qv::pages_clear_kernel, dim3(qv::ceil_div(n, 256)), 256, stream, P) &&
+                  qv::launch(qv::pages_adopt_kernel, dim3(P.batch), 256, stream, P, (const int *)d_table, (const int *)d_length) &&
+                  qv::launch(qv::pages_free_bits_kernel, dim3(qv::ceil_div(P.words, 256)), 256, stream, P);
+  return ok ? QEVICT_OK : QEVICT_ECUDA;
+}
+
+qevict_status qevict_pages_reserve(const qevict_pages_desc *desc, void *k, void *v, void *d_state, const int32_t *d_new,
+                                   int32_t n_new, qevict_stream_t stream) {
+  qv::PagesPlan p;
+  qv::PagesDev P;
+  const qevict_status st = qv::pages_args(desc, true, k, v, d_state, &p, &P);
+  if (st != QEVICT_OK) return st;
+  if (!qv::word_ok(d_new, false) || (!d_new && n_new < 0)) return QEVICT_EINVAL;
+  const auto tail = p.dense ? qv::pages_tail_kernel<true> : qv::pages_tail_kernel<false>;
+  const bool ok = qv::launch(qv::pages_reserve_kernel, dim3(1), 1024, stream, P, (const int *)d_new, (int)n_new) &&
+                  qv::launch(tail, qv::copy_grid(P, P.batch), 256, stream, P);
+  return ok ? QEVICT_OK : QEVICT_ECUDA;
+}
+
+qevict_status qevict_pages_append(const qevict_pages_desc *desc, const qevict_pages_rows *rows, void *k, void *v,
+                                  void *d_state, const void *k_new, const void *v_new, const int32_t *d_n,
+                                  qevict_stream_t stream) {
+  qv::PagesPlan p;
+  qv::PagesDev P;
+  const qevict_status st = qv::pages_args(desc, true, k, v, d_state, &p, &P);
+  if (st != QEVICT_OK) return st;
+  if (!rows || rows->layer < 0 || rows->layers < 1 || rows->layer > P.layers - rows->layers || rows->n < 1 || rows->reserved0 ||
+      rows->n > (1 << 30) / (P.h_kv * 16) || !k_new || !v_new || (((uintptr_t)k_new | (uintptr_t)v_new) & 15) ||
+      !qv::word_ok(d_n, false))
+    return QEVICT_EINVAL;
+  const int64_t size[4] = {rows->layers, P.batch, rows->n, P.h_kv};
+  if (!qv::dims_ok(rows->k, size, 4, true) || !qv::dims_ok(rows->v, size, 4, true)) return QEVICT_EINVAL;
+  qv::RowsDev R = {};
+  R.k = static_cast<const uint16_t *>(k_new), R.v = static_cast<const uint16_t *>(v_new);
+  for (int i = 0; i < 4; ++i) R.sk[i] = rows->k[i], R.sv[i] = rows->v[i];
+  R.layer = rows->layer, R.layers = rows->layers, R.n = rows->n, R.d_n = d_n;
+  const dim3 grid(qv::ceil_div((int64_t)R.n * P.h_kv * 16, qv::APPEND_THREADS * qv::APPEND_PIECES), P.batch, R.layers);
+  return qv::launch(qv::pages_append_kernel, grid, qv::APPEND_THREADS, stream, P, R) ? QEVICT_OK : QEVICT_ECUDA;
+}
+
+qevict_status qevict_pages_accept(const qevict_pages_desc *desc, void *k, void *v, void *d_state, const int32_t *d_count,
+                                  const int32_t *d_path, int32_t max_path, qevict_stream_t stream) {
+  qv::PagesPlan p;
+  qv::PagesDev P;
+  const qevict_status st = qv::pages_args(desc, true, k, v, d_state, &p, &P);
+  if (st != QEVICT_OK) return st;
+  if (!qv::word_ok(d_count, true) || !qv::word_ok(d_path, false) || (d_path && (max_path < 1 || max_path > qv::PG_PATH)))
+    return QEVICT_EINVAL;
+  const dim3 grid(d_path ? qv::ceil_div((int64_t)P.layers * 2 * P.h_kv * 16, 256) : 1, P.batch);
+  return qv::launch(qv::pages_accept_kernel, grid, 256, stream, P, (const int *)d_count, (const int *)d_path, (int)max_path)
+             ? QEVICT_OK : QEVICT_ECUDA;
+}
+
+qevict_status qevict_pages_select(const qevict_pages_desc *desc, void *d_state, const int32_t *d_src, qevict_stream_t stream) {
+  qv::PagesPlan p;
+  qv::PagesDev P;
+  const qevict_status st = qv::pages_args(desc, false, nullptr, nullptr, d_state, &p, &P);
+  if (st != QEVICT_OK) return st;
+  if (!qv::word_ok(d_src, true)) return QEVICT_EINVAL;
+  return qv::launch(qv::pages_select_kernel, dim3(qv::ceil_div(P.max_pages, qv::SELECT_COLS)), 1024, stream, P,
+                    (const int *)d_src) ? QEVICT_OK : QEVICT_ECUDA;
+}
+
+qevict_status qevict_pages_trim(const qevict_pages_desc *desc, void *d_state, const int32_t *d_length, qevict_stream_t stream) {
+  qv::PagesPlan p;
+  qv::PagesDev P;
+  const qevict_status st = qv::pages_args(desc, false, nullptr, nullptr, d_state, &p, &P);
+  if (st != QEVICT_OK) return st;
+  if (!qv::word_ok(d_length, true)) return QEVICT_EINVAL;
+  return qv::launch(qv::pages_trim_kernel, dim3(P.batch), 256, stream, P, (const int *)d_length) ? QEVICT_OK : QEVICT_ECUDA;
+}
+
+qevict_status qevict_pages_compact(const qevict_pages_desc *desc, void *k, void *v, void *d_state, qevict_stream_t stream) {
+  qv::PagesPlan p;
+  qv::PagesDev P;
+  const qevict_status st = qv::pages_args(desc, true, k, v, d_state, &p, &P);
+  if (st != QEVICT_OK) return st;
+  const auto move = p.dense ? qv::pages_move_kernel<true> : qv::pages_move_kernel<false>;
+  const bool ok = qv::launch(qv::pages_plan_kernel, dim3(1), 1024, stream, P) &&
+                  qv::launch(move, qv::copy_grid(P, P.pages / 2 + 1), 256, stream, P);
+  return ok ? QEVICT_OK : QEVICT_ECUDA;
+}
+
+}  // extern "C"
