@@ -242,14 +242,31 @@ __device__ __forceinline__ void tma_load_4d_at(uint32_t dst, const CUtensorMap *
       "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(smem_u32(bar))
       : "memory");
 }
-// The same by one elected lane of a converged warp.
-__device__ __forceinline__ void tma_load_4d_elect(uint32_t dst, const CUtensorMap *map, int x, int y, int z, int w,
-                                                  uint64_t *bar) {
+// Two pages of one KV head, both halves of the channels, by one elected lane of a converged warp: the first page's rows go to
+// dst and dst + half a tile, the second's `step` bytes behind.
+__device__ __forceinline__ void tma_load_pages2(uint32_t dst, uint32_t step, const CUtensorMap *map, int head, int p0, int p1,
+                                                uint64_t *bar) {
   asm volatile(
-      "{\n .reg .pred e;\n elect.sync _|e, 0xffffffff;\n"
-      " @e cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], "
-      "[%6];\n}" ::"r"(dst),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(smem_u32(bar))
+      "{\n .reg .pred e;\n .reg .b32 d, z, h;\n elect.sync _|e, 0xffffffff;\n mov.b32 z, 0;\n mov.b32 h, 64;\n"
+      " @e cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {z, %2, z, %3}], [%5];\n"
+      " add.u32 d, %0, %7;\n"
+      " @e cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [d], [%1, {h, %2, z, %3}], [%5];\n"
+      " add.u32 d, %0, %6;\n"
+      " @e cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [d], [%1, {z, %2, z, %4}], [%5];\n"
+      " add.u32 d, d, %7;\n"
+      " @e cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [d], [%1, {h, %2, z, %4}], [%5];\n}" ::"r"(
+          dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(head), "r"(p0), "r"(p1), "r"(smem_u32(bar)), "r"(step), "n"(AT_HALF_BYTES)
+      : "memory");
+}
+__device__ __forceinline__ void tma_load_page(uint32_t dst, const CUtensorMap *map, int head, int p, uint64_t *bar) {
+  asm volatile(
+      "{\n .reg .pred e;\n .reg .b32 d, z, h;\n elect.sync _|e, 0xffffffff;\n mov.b32 z, 0;\n mov.b32 h, 64;\n"
+      " @e cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {z, %2, z, %3}], [%4];\n"
+      " add.u32 d, %0, %5;\n"
+      " @e cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [d], [%1, {h, %2, z, %3}], [%4];\n}" ::"r"(
+          dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(head), "r"(p), "r"(smem_u32(bar)), "n"(AT_HALF_BYTES)
       : "memory");
 }
 // The eight products (16 deep each) of one 128 x 128 x 128 tile, issued by one elected lane of a converged warp:
@@ -810,13 +827,17 @@ __global__ void __launch_bounds__(AT_THREADS, 1) attn_kernel(const __grid_consta
           const int e = first >= w ? here : below, at = first - (first >= w ? w : w - 32);
           if (lane == 0) mbar_arrive_expect_tx(&full[st], (uint32_t)n << (lg + 8));   // pages without keys are left out
           __syncwarp();
+          const uint32_t step = 1u << (lg + 7);
+          int p = 0;
 #pragma unroll 1
-          for (int p = 0; p < n; ++p) {
-            const int pg = __shfl_sync(0xffffffffu, e, at + p);
-            const uint32_t d = dst + ((uint32_t)p << (lg + 7));
-            tma_load_4d_elect(d, map, 0, I.g, 0, pg, &full[st]);
-            tma_load_4d_elect(d + AT_HALF_BYTES, map, 64, I.g, 0, pg, &full[st]);
+          for (; p + 4 <= n; p += 4) {
+            const int p0 = __shfl_sync(0xffffffffu, e, at + p), p1 = __shfl_sync(0xffffffffu, e, at + p + 1);
+            const int p2 = __shfl_sync(0xffffffffu, e, at + p + 2), p3 = __shfl_sync(0xffffffffu, e, at + p + 3);
+            tma_load_pages2(dst + p * step, step, map, I.g, p0, p1, &full[st]);
+            tma_load_pages2(dst + (p + 2) * step, step, map, I.g, p2, p3, &full[st]);
           }
+#pragma unroll 1
+          for (; p < n; ++p) tma_load_page(dst + p * step, map, I.g, __shfl_sync(0xffffffffu, e, at + p), &full[st]);
           ++c;
         }, &P.tk, &P.tv, 0, 0);
       } else if (!PAGED && I.n > 0 && lane == 0) {

@@ -24,6 +24,7 @@ struct PagesDev {
   int64_t sk[4], sv[4];          // layer, page, token, head
   int layers, pages, page, lg, h_kv, batch, max_pages, words;   // lg: log2 page; words: of the free bits, a multiple of 4
   int *status, *n_free, *moves, *n_copies;
+  unsigned long long *drawn;     // units of a copy given out
   int *length, *held, *table, *refs;
   uint32_t *bits;
   int *tickets;                  // [batch + 1] CTAs that have read what the last one changes; 0 between calls
@@ -51,22 +52,28 @@ __device__ __forceinline__ bool give_back(const PagesDev &P, int p) {
   return true;
 }
 
-// Exclusive sum over a CTA of 32 warps; `total` for every thread.  Two barriers.
-__device__ __forceinline__ int scan_1024(int x, int *warps, int &total) {
+// Exclusive sums of x and y over a CTA of 32 warps, and their totals, the same for every thread.  Two barriers.
+struct Sums {
+  int x, y, all_x, all_y;
+};
+__device__ __forceinline__ Sums scan_1024(int x, int y, int2 *warps) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  int s = x;
+  int sx = x, sy = y;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const int y = __shfl_up_sync(0xffffffffu, s, o);
-    if (lane >= o) s += y;
+    const int ux = __shfl_up_sync(0xffffffffu, sx, o), uy = __shfl_up_sync(0xffffffffu, sy, o);
+    if (lane >= o) sx += ux, sy += uy;
   }
   __syncthreads();   // what stood in warps has been read
-  if (lane == 31) warps[warp] = s;
+  if (lane == 31) warps[warp] = make_int2(sx, sy);
   __syncthreads();
-  const int w = warps[lane];
-  const int before = __reduce_add_sync(0xffffffffu, lane < warp ? w : 0);
-  total = __reduce_add_sync(0xffffffffu, w);
-  return before + s - x;
+  const int2 w = warps[lane];
+  Sums S;
+  S.x = __reduce_add_sync(0xffffffffu, lane < warp ? w.x : 0) + sx - x;
+  S.y = __reduce_add_sync(0xffffffffu, lane < warp ? w.y : 0) + sy - y;
+  S.all_x = __reduce_add_sync(0xffffffffu, w.x);
+  S.all_y = __reduce_add_sync(0xffffffffu, w.y);
+  return S;
 }
 
 // ----------------------------------------------------------------------------- start
@@ -130,42 +137,48 @@ __global__ void pages_free_bits_kernel(PagesDev P) {
 
 // ----------------------------------------------------------------------------- rows
 
-// Place of 16-byte piece x, (row, head, 16th of the channels), of a page that starts at `base`.  DENSE: rows follow one another.
-template <bool DENSE>
-__device__ __forceinline__ int64_t piece_at(const int64_t (&st)[4], int64_t base, int h_kv, uint32_t x) {
-  if (DENSE) return base + (int64_t)x * 8;
-  const uint32_t h = x >> 4, r = h / (uint32_t)h_kv;
-  return base + r * st[2] + (h - r * h_kv) * st[3] + (x & 15) * 8;
-}
-
 // A part (of PART_PIECES pieces of 16 bytes) of the first `rows` rows of page a, copied to page z by a CTA of 256 threads.
+// DENSE: rows follow one another, so that one address and eight offsets do.
 constexpr int PART_PIECES = 2048;
 template <bool DENSE>
 __device__ __forceinline__ void copy_part(uint16_t *pool, const int64_t (&st)[4], int layer, int a, int z, int rows, int h_kv,
                                           int part) {
-  const uint32_t n = (uint32_t)rows * h_kv * 16, x = (uint32_t)part * PART_PIECES + threadIdx.x;
-  const int64_t ba = layer * st[0] + a * st[1], bz = layer * st[0] + z * st[1];
+  const int n = rows * h_kv * 16, x = part * PART_PIECES + threadIdx.x;
+  const uint16_t *src = pool + layer * st[0] + a * st[1];
+  uint16_t *dst = pool + layer * st[0] + z * st[1];
+  auto place = [&](auto *page, int i) {   // of piece x + 256 i: (row, head, 16th of the channels)
+    if (DENSE) return page + (int64_t)x * 8 + i * (256 * 8);
+    const uint32_t y = x + i * 256, h = y >> 4, r = h / (uint32_t)h_kv;
+    return page + r * st[2] + (h - r * h_kv) * st[3] + (y & 15) * 8;
+  };
   uint4 w[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i)
-    if (x + i * 256 < n) w[i] = *reinterpret_cast<const uint4 *>(pool + piece_at<DENSE>(st, ba, h_kv, x + i * 256));
+    if (x + i * 256 < n) w[i] = *reinterpret_cast<const uint4 *>(place(src, i));
 #pragma unroll
   for (int i = 0; i < 8; ++i)
-    if (x + i * 256 < n) *reinterpret_cast<uint4 *>(pool + piece_at<DENSE>(st, bz, h_kv, x + i * 256)) = w[i];
+    if (x + i * 256 < n) *reinterpret_cast<uint4 *>(place(dst, i)) = w[i];
 }
 
-// Copies in turn over the grid: unit u is a part of one copy's page in one layer, keys or values.
+// n copies drawn by the CTAs: a unit is a part of one copy's page in one layer, keys or values.  (In fixed turns CTAs
+// far from the memory at hand end last: 64 samples of 4 prompts 84 us, drawn 70.  A unit a CTA does as well, but a grid for the
+// most copies possible costs a step without any 1 us a thousand CTAs.)
 template <bool DENSE, typename Copy>
 __device__ __forceinline__ void copy_all(const PagesDev &P, int n, const Copy &copy) {
+  __shared__ unsigned long long next[2];
   const int parts = (P.page * P.h_kv * 16 + PART_PIECES - 1) / PART_PIECES, per = parts * 2 * P.layers;
-  const int64_t units = (int64_t)n * per;
-  for (int64_t u = blockIdx.x; u < units; u += gridDim.x) {
-    const int r = (int)(u / per), y = (int)(u - (int64_t)r * per), l2 = y / parts, part = y - l2 * parts;
+  const unsigned long long units = (unsigned long long)n * per;
+  int turn = 0;
+  for (unsigned long long u = blockIdx.x; u < units; turn ^= 1) {
+    if (threadIdx.x == 0) next[turn] = gridDim.x + atomicAdd(P.drawn, 1ull);
+    const int r = (int)(u / per), y = (int)(u - (unsigned long long)r * per), l2 = y / parts, part = y - l2 * parts;
     const int4 c = copy(r);
     if (l2 & 1)
       copy_part<DENSE>(P.v, P.sv, l2 >> 1, c.x, c.y, c.z, P.h_kv, part);
     else
       copy_part<DENSE>(P.k, P.sk, l2 >> 1, c.x, c.y, c.z, P.h_kv, part);
+    __syncthreads();
+    u = next[turn];
   }
 }
 
@@ -176,9 +189,10 @@ struct RowsDev {
   const int *d_n;
 };
 
-// New rows: a CTA takes 4 pieces a thread of one (layer, sequence), keys and values, so eight loads are in flight.
+// New rows: a CTA takes 4 pieces a thread of one (layer, sequence), keys and values, so eight loads are in flight.  Bound by
+// memory: 4099 + 3075 rows of 8 heads in 8 layers 71 us (6.6 TB/s; with addresses kept over the loads, 90 registers, 81).
 constexpr int APPEND_THREADS = 256, APPEND_PIECES = 4;
-__global__ void __launch_bounds__(APPEND_THREADS) pages_append_kernel(const __grid_constant__ PagesDev P,
+__global__ void __launch_bounds__(APPEND_THREADS, 4) pages_append_kernel(const __grid_constant__ PagesDev P,
                                                                      const __grid_constant__ RowsDev R) {
   pages_begin();
   const int b = blockIdx.y, held = held_of(P, b), len = length_of(P, b, held);
@@ -194,104 +208,124 @@ __global__ void __launch_bounds__(APPEND_THREADS) pages_append_kernel(const __gr
   if (x0 >= all) return;
   for (int l = blockIdx.z; l < R.layers; l += gridDim.z) {
     uint4 wk[APPEND_PIECES], wv[APPEND_PIECES];
-    int64_t at[APPEND_PIECES][2];
+    int to[APPEND_PIECES];   // page << 7 | row; -1: nowhere
 #pragma unroll
     for (int i = 0; i < APPEND_PIECES; ++i) {
       const uint32_t x = x0 + i * APPEND_THREADS;
-      at[i][0] = -1;
+      to[i] = -1;
       if (x >= all) continue;
       const uint32_t t = x / per_row, y = x - t * per_row, h = y >> 4, c = (y & 15) * 8;
       wk[i] = *reinterpret_cast<const uint4 *>(R.k + l * R.sk[0] + b * R.sk[1] + t * R.sk[2] + h * R.sk[3] + c);
       wv[i] = *reinterpret_cast<const uint4 *>(R.v + l * R.sv[0] + b * R.sv[1] + t * R.sv[2] + h * R.sv[3] + c);
       const int64_t pos = (int64_t)len + t;
-      const int pg = pos < (int64_t)held << P.lg ? row[pos >> P.lg] : -1, off = (int)pos & (P.page - 1);
-      if (!is_page(P, pg) || P.refs[pg] != 1) {
-        if (y == 0) atomicOr(P.status, QV_ERR_BOUNDS);
-        continue;
-      }
-      const int64_t ll = R.layer + l;
-      at[i][0] = ll * P.sk[0] + pg * P.sk[1] + off * P.sk[2] + h * P.sk[3] + c;
-      at[i][1] = ll * P.sv[0] + pg * P.sv[1] + off * P.sv[2] + h * P.sv[3] + c;
+      const int pg = pos < (int64_t)held << P.lg ? row[pos >> P.lg] : -1;
+      if (is_page(P, pg) && P.refs[pg] == 1)
+        to[i] = pg << 7 | ((int)pos & (P.page - 1));
+      else if (y == 0)
+        atomicOr(P.status, QV_ERR_BOUNDS);
     }
+    uint16_t *k = P.k + (R.layer + l) * P.sk[0], *v = P.v + (R.layer + l) * P.sv[0];
 #pragma unroll
-    for (int i = 0; i < APPEND_PIECES; ++i)
-      if (at[i][0] >= 0) {
-        *reinterpret_cast<uint4 *>(P.k + at[i][0]) = wk[i];
-        *reinterpret_cast<uint4 *>(P.v + at[i][1]) = wv[i];
-      }
+    for (int i = 0; i < APPEND_PIECES; ++i) {
+      if (to[i] < 0) continue;
+      const uint32_t y = (x0 + i * APPEND_THREADS) % per_row, h = y >> 4, c = (y & 15) * 8;
+      const int pg = to[i] >> 7, off = to[i] & 127;
+      *reinterpret_cast<uint4 *>(k + pg * P.sk[1] + off * P.sk[2] + h * P.sk[3] + c) = wk[i];
+      *reinterpret_cast<uint4 *>(v + pg * P.sv[1] + off * P.sv[2] + h * P.sv[3] + c) = wv[i];
+    }
   }
 }
 
 // Accepted rows move down their sequence.  A thread owns 16 bytes of every row of one (layer, K or V, head) and moves them in
 // ascending order, eight rows at a time, all loads before the stores: row path[j] >= j, so a row is read before anything
 // lands on it, and no other thread touches these bytes.  The sequence's last CTA to have read its length counts the rows in.
+// Bound by the chain from lengths over path and table to the rows, then by memory; the counts of the pages written to are
+// looked up while the first rows are on their way.
 __global__ void __launch_bounds__(256) pages_accept_kernel(const __grid_constant__ PagesDev P, const int *d_count,
                                                           const int *d_path, int max_path) {
-  __shared__ int s_from[PG_PATH], s_to[PG_PATH], last;   // page << 7 | row
+  __shared__ int s_from[PG_PATH], s_to[PG_PATH], last;   // page << 7 | row; from -1: nothing to move
   pages_begin();
-  const int b = blockIdx.y, held = held_of(P, b), len = length_of(P, b, held), count = d_count[b];
+  const int b = blockIdx.y, j = threadIdx.x, held = held_of(P, b), len = length_of(P, b, held), count = d_count[b];
   const int *row = row_of(P, b);
   const int64_t room = (int64_t)held << P.lg;
-  bool ok = count >= 0 && (!d_path || count <= max_path) && (int64_t)len + count <= room;
-  if (ok && d_path) {
+  int at = -1, before = -1;
+  if (d_path && j < max_path) {
     const int *path = d_path + (int64_t)b * max_path;
-    for (int j = threadIdx.x; j < count; j += blockDim.x) {
-      const int p = path[j];
-      if (p < 0 || (int64_t)len + p >= room || (j && path[j - 1] >= p)) {
-        ok = false;
-        break;
-      }
-      const int src = row[(len + p) >> P.lg], dst = row[(len + j) >> P.lg];
-      if (!is_page(P, src) || !is_page(P, dst) || P.refs[dst] != 1) {
-        ok = false;
-        break;
-      }
-      s_from[j] = p == j ? -1 : src << 7 | ((len + p) & (P.page - 1));
-      s_to[j] = dst << 7 | ((len + j) & (P.page - 1));
-    }
-  } else if (ok) {   // rows that shared pages hold were never written
-    for (int c = (len >> P.lg) + threadIdx.x; (int64_t)c << P.lg < (int64_t)len + count; c += blockDim.x)
+    at = path[j];
+    if (j) before = path[j - 1];
+  }
+  const bool fits = count >= 0 && (!d_path || count <= max_path) && (int64_t)len + count <= room;
+  bool ok = fits;
+  int dst = -1;
+  if (fits && d_path && j < count) {
+    ok = at > before && at >= 0 && (int64_t)len + at < room;
+    const int src = ok ? row[(len + at) >> P.lg] : -1;
+    dst = row[(len + j) >> P.lg];
+    ok = ok && is_page(P, src) && is_page(P, dst);
+    s_from[j] = ok && at != j ? src << 7 | ((len + at) & (P.page - 1)) : -1;
+    s_to[j] = dst << 7 | ((len + j) & (P.page - 1));
+    if (ok) ok = P.refs[dst] == 1;   // rows of shared pages are never written
+  } else if (fits && !d_path) {
+    for (int c = (len >> P.lg) + j; (int64_t)c << P.lg < (int64_t)len + count; c += blockDim.x)
       if (!is_page(P, row[c]) || P.refs[row[c]] != 1) ok = false;
   }
-  ok = __syncthreads_and(ok);
-  if (threadIdx.x == 0) {
-    last = gridDim.x == 1;
-    if (!last) {
-      __threadfence();
-      last = atomicAdd(&P.tickets[b], 1) == (int)gridDim.x - 1;
-      if (last) P.tickets[b] = 0;
+  auto settle = [&]() {   // whether the sequence's rows may move, and what follows for its length
+    ok = __syncthreads_and(ok);
+    if (threadIdx.x == 0) {
+      last = gridDim.x == 1;
+      if (!last) {
+        __threadfence();
+        last = atomicAdd(&P.tickets[b], 1) == (int)gridDim.x - 1;
+        if (last) P.tickets[b] = 0;
+      }
+      if (last && !ok) atomicOr(P.status, QV_ERR_BOUNDS);
+      if (last && ok) P.length[b] = len + count;
     }
-    if (last && !ok) atomicOr(P.status, QV_ERR_BOUNDS);
-    if (last && ok) P.length[b] = len + count;
+    return ok;
+  };
+  if (!fits || !d_path || count == 0) {
+    settle();
+    return;
   }
-  if (!ok || !d_path) return;
-  const uint32_t x = blockIdx.x * blockDim.x + threadIdx.x, h = x >> 4, l2 = h / (uint32_t)P.h_kv;
-  if (l2 >= 2u * P.layers) return;
-  const bool is_v = l2 & 1;
-  uint16_t *pool = is_v ? P.v : P.k;
-  const int64_t st_p = is_v ? P.sv[1] : P.sk[1], st_t = is_v ? P.sv[2] : P.sk[2];
-  pool += (l2 >> 1) * (is_v ? P.sv[0] : P.sk[0]) + (h - l2 * P.h_kv) * (is_v ? P.sv[3] : P.sk[3]) + (x & 15) * 8;
-  auto at = [&](int e) { return reinterpret_cast<uint4 *>(pool + (e >> 7) * st_p + (e & 127) * st_t); };
-  for (int j0 = 0; j0 < count; j0 += 8) {
-    uint4 w[8];
+  __syncthreads();
+  const uint32_t all = 2u * P.layers * P.h_kv * 16;
+  bool settled = false;
+  for (uint32_t x0 = blockIdx.x * 256; x0 < all; x0 += gridDim.x * 256) {
+    const uint32_t x = min(x0 + threadIdx.x, all - 1), h = x >> 4, l2 = h / (uint32_t)P.h_kv;
+    const bool mine = x0 + threadIdx.x < all, is_v = l2 & 1;
+    uint16_t *pool = is_v ? P.v : P.k;
+    const int64_t st_p = is_v ? P.sv[1] : P.sk[1], st_t = is_v ? P.sv[2] : P.sk[2];
+    pool += (l2 >> 1) * (is_v ? P.sv[0] : P.sk[0]) + (h - l2 * P.h_kv) * (is_v ? P.sv[3] : P.sk[3]) + (x & 15) * 8;
+    auto place = [&](int e) { return reinterpret_cast<uint4 *>(pool + (e >> 7) * st_p + (e & 127) * st_t); };
+    for (int j0 = 0; j0 < count; j0 += 8) {
+      uint4 w[8];
 #pragma unroll
-    for (int j = 0; j < 8; ++j)
-      if (j0 + j < count && s_from[j0 + j] >= 0) w[j] = *at(s_from[j0 + j]);
+      for (int i = 0; i < 8; ++i)
+        if (mine && j0 + i < count && s_from[j0 + i] >= 0) w[i] = *place(s_from[j0 + i]);
+      if (!settled && !settle()) return;
+      settled = true;
 #pragma unroll
-    for (int j = 0; j < 8; ++j)
-      if (j0 + j < count && s_from[j0 + j] >= 0) *at(s_to[j0 + j]) = w[j];
+      for (int i = 0; i < 8; ++i)
+        if (mine && j0 + i < count && s_from[j0 + i] >= 0) *place(s_to[j0 + i]) = w[i];
+    }
   }
 }
 
 // ----------------------------------------------------------------------------- pages
 
-// Who needs which pages, a thread a sequence; then the free bits are walked from the lowest page on, 128 a thread at a
-// time, and the r-th free page goes to whom the running sum of needs says.  Nothing is written before it is known to
-// suffice.  Bound by latency: 3 barriers' worth and a scan per 131072 pages.
+// Who needs which pages, a thread a sequence; then the free bits are walked from the lowest page on, a word a thread, and
+// the r-th free page goes to whom the running sum of needs says, a thread a page: it finds word and sequence by their sums.
+// Nothing is written before the pages are known to suffice.  Bound by latency: lengths, table, counts in a chain of
+// loads, then a few barriers for every 32768 pages (a thread that hands out all pages of its 128 bits took 30 us for 64
+// samples of 4 prompts, 6 now).
 __global__ void __launch_bounds__(1024) pages_reserve_kernel(const __grid_constant__ PagesDev P, const int *d_new, int n_new) {
-  __shared__ int s_tail[PG_BATCH], s_start[PG_BATCH], s_len[PG_BATCH], s_held[PG_BATCH], s_copy[PG_BATCH], s_warp[32];
+  __shared__ int s_tail[PG_BATCH], s_start[PG_BATCH], s_len[PG_BATCH], s_held[PG_BATCH], s_copy[PG_BATCH], s_rank[1024];
+  __shared__ uint32_t s_word[1024];
+  __shared__ int2 s_warp[32];
   pages_begin();
   const int t = threadIdx.x;
+  uint32_t word = t < P.words ? P.bits[t] : 0u;
+  const int n_free = *P.n_free;
   int len = 0, held = 0, add = 0, tail = -1, refs = 0;
   bool bad = false;
   if (t < P.batch) {
@@ -307,10 +341,10 @@ __global__ void __launch_bounds__(1024) pages_reserve_kernel(const __grid_consta
         if (!bad) refs = P.refs[tail];
       }
     }
-    s_tail[t] = tail, s_len[t] = len, s_held[t] = held;
+    s_len[t] = len, s_held[t] = held;
   }
-  if (t == 0) *P.n_copies = 0;
-  const int n_free = *P.n_free;
+  s_tail[t] = tail;
+  if (t == 0) *P.n_copies = 0, *P.drawn = 0;
   if (__syncthreads_or(bad)) {
     if (t == 0) atomicOr(P.status, QV_ERR_BOUNDS);
     return;
@@ -318,6 +352,7 @@ __global__ void __launch_bounds__(1024) pages_reserve_kernel(const __grid_consta
   bool copy = false;
   if (refs > 1) {   // shared: by how many that reserve now, and is this the first of them
     int same = 0, before = 0;
+#pragma unroll 8
     for (int j = 0; j < P.batch; ++j)
       if (s_tail[j] == tail) {
         ++same;
@@ -325,18 +360,15 @@ __global__ void __launch_bounds__(1024) pages_reserve_kernel(const __grid_consta
       }
     copy = same < refs || before > 0;
   }
-  int total;
-  const int start = scan_1024(add + copy, s_warp, total);
-  int copies;
-  const int c_at = scan_1024(copy, s_warp, copies);
+  const Sums need = scan_1024(add + copy, copy, s_warp);
+  const int total = need.all_x;
   if (total > n_free) {
     if (t == 0) atomicOr(P.status, QV_ERR_SLOT);
     return;
   }
   if (total == 0) return;
-  if (t < P.batch) s_start[t] = start, s_copy[t] = copy ? c_at : -1;
-  if (t == 0) *P.n_copies = copies;
-  __syncthreads();
+  if (t < P.batch) s_start[t] = need.x, s_copy[t] = copy ? need.y : -1;
+  if (t == 0) *P.n_copies = need.all_y;
   auto assign = [&](int r, int id) {
     int lo = 0, hi = P.batch - 1;   // the last sequence that starts at r or before: it needs pages
     while (lo < hi) {
@@ -357,25 +389,35 @@ __global__ void __launch_bounds__(1024) pages_reserve_kernel(const __grid_consta
     P.refs[id] = 1;
   };
   int found = 0;
-  for (int base = 0; base < P.words && found < total; base += 4 * 1024) {
-    const int w = base + 4 * t;
-    uint4 x = make_uint4(0, 0, 0, 0);
-    if (w < P.words) x = *reinterpret_cast<const uint4 *>(P.bits + w);
-    int here;
-    int r = found + scan_1024(__popc(x.x) + __popc(x.y) + __popc(x.z) + __popc(x.w), s_warp, here);
-    uint32_t q[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      uint32_t left = q[i];
-      while (left && r < total) {
-        const int id = (w + i) * 32 + __ffs(left) - 1;
-        left &= left - 1;
-        if (is_page(P, id)) assign(r, id);
-        ++r;
-      }
-      if (left != q[i]) P.bits[w + i] = left;
+  for (int base = 0; base < P.words && found < total; base += 1024) {
+    const int w = base + t;
+    if (base) word = w < P.words ? P.bits[w] : 0u;
+    const int here = __popc(word);
+    const Sums at = scan_1024(here, 0, s_warp);   // (its barriers also part this round's lists from the last one's readers)
+    s_rank[t] = at.x, s_word[t] = word;
+    const int take = min(here, total - found - at.x);
+    if (take > 0) {
+      uint32_t left = take == here ? 0u : word;
+      if (left)
+        for (int i = 0; i < take; ++i) left &= left - 1;
+      P.bits[w] = left;
     }
-    found += here;
+    __syncthreads();
+    for (int r = t; r < min(at.all_x, total - found); r += 1024) {
+      int lo = 0, hi = 1023;   // the last word whose free pages start at r or before: it has some
+      while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (s_rank[mid] <= r)
+          lo = mid;
+        else
+          hi = mid - 1;
+      }
+      uint32_t x = s_word[lo];
+      for (int i = r - s_rank[lo]; i > 0; --i) x &= x - 1;
+      const int id = (base + lo) * 32 + __ffs(x) - 1;
+      if (is_page(P, id)) assign(found + r, id);
+    }
+    found += at.all_x;
   }
   if (copy) atomicSub(&P.refs[tail], 1);
   if (add) P.held[t] = held + add;
@@ -395,15 +437,22 @@ __global__ void __launch_bounds__(256) pages_tail_kernel(const __grid_constant__
   copy_all<DENSE>(P, *P.n_copies, [&](int r) { return P.copies[r]; });
 }
 
-// Tables rearranged.  A CTA takes 8 places of all sequences: it reads them all before it writes any, and since a page stands at
-// one place of the tables, it counts every entry that a page gains before the ones it loses.  The last CTA to have
-// read lengths rearranges those.
-constexpr int SELECT_COLS = 8;
-__global__ void __launch_bounds__(1024) pages_select_kernel(const __grid_constant__ PagesDev P, const int *d_src) {
-  __shared__ int s_old[PG_BATCH * SELECT_COLS], last, given;
+// Tables rearranged.  A CTA takes the same places of all sequences, up to 8192 entries: it reads them all before it writes
+// any, and since a page stands at one place of the tables, it counts every entry that a page gains before the ones it loses.
+// Lengths change once all CTAs have read them: by the last of them.  Bound by its chain of loads and atomics.
+constexpr int SELECT_CELLS = 8;   // entries of a thread
+__global__ void __launch_bounds__(1024) pages_select_kernel(const __grid_constant__ PagesDev P, const int *d_src, int cols) {
+  __shared__ int s_old[1024 * SELECT_CELLS];
+  __shared__ int s_src[PG_BATCH], s_held[PG_BATCH], s_new[PG_BATCH], s_len[PG_BATCH];   // 48 KB in all
   pages_begin();
-  const int t = threadIdx.x;
-  int src = t, held = 0, len = 0, n_held = 0, n_len = 0;
+  const int t = threadIdx.x, c0 = blockIdx.x * cols, n = min(cols, P.max_pages - c0), cells = P.batch * n;
+  int cell[SELECT_CELLS];
+#pragma unroll
+  for (int k = 0; k < SELECT_CELLS; ++k) {   // all entries, while it is worked out which of them count
+    const int i = t + 1024 * k;
+    if (i < cells) cell[k] = row_of(P, i / n)[c0 + i % n];
+  }
+  int src = t, held = 0, len = 0;
   if (t < P.batch) {
     src = d_src[t];
     if (src < -1 || src >= P.batch) {
@@ -411,50 +460,51 @@ __global__ void __launch_bounds__(1024) pages_select_kernel(const __grid_constan
       src = t;
     }
     held = held_of(P, t), len = length_of(P, t, held);
-    n_held = held, n_len = len;
-    if (src < 0) {
-      n_held = n_len = 0;
-    } else if (src != t) {
-      n_len = length_of(P, src, held_of(P, src));
-      n_held = (n_len + P.page - 1) >> P.lg;
-    }
+    s_held[t] = held, s_len[t] = len, s_src[t] = src;
   }
-  if (t == 0) given = 0;
-  const int c0 = blockIdx.x * SELECT_COLS;
-  const bool work = __syncthreads_or(src != t && c0 < max(held, n_held));
-  if (work) {
-    const int cells = P.batch * SELECT_COLS;
-    for (int i = t; i < cells; i += 1024) {
-      const int c = c0 + i % SELECT_COLS;
-      s_old[i] = c < P.max_pages ? row_of(P, i / SELECT_COLS)[c] : -1;
+#pragma unroll
+  for (int k = 0; k < SELECT_CELLS; ++k)
+    if (t + 1024 * k < cells) s_old[t + 1024 * k] = cell[k];
+  __syncthreads();
+  int n_held = held, n_len = len;
+  if (src != t) {
+    n_len = src < 0 ? 0 : s_len[src];
+    n_held = (n_len + P.page - 1) >> P.lg;
+  }
+  if (t < P.batch) s_new[t] = n_held;
+  if (__syncthreads_or(src != t && c0 < max(held, n_held))) {
+#pragma unroll
+    for (int k = 0; k < SELECT_CELLS; ++k) {
+      const int i = t + 1024 * k;
+      if (i >= cells) break;
+      const int b = i / n, c = i - b * n, from = s_src[b];
+      if (from == b) continue;
+      const int p = c0 + c < s_new[b] ? s_old[from * n + c] : -1;
+      if (is_page(P, p)) atomicAdd(&P.refs[p], 1);
+      if (p != cell[k]) row_of(P, b)[c0 + c] = p;
     }
-    __syncthreads();
-    const int n = min(SELECT_COLS, P.max_pages - c0);
-    if (src != t)
-      for (int c = 0; c < n; ++c) {
-        const int p = c0 + c < n_held ? s_old[src * SELECT_COLS + c] : -1;
-        if (is_page(P, p)) atomicAdd(&P.refs[p], 1);
-        row_of(P, t)[c0 + c] = p;
-      }
-    __threadfence();
     __syncthreads();
     int free = 0;
-    if (src != t)
-      for (int c = 0; c < n; ++c) {
-        const int p = s_old[t * SELECT_COLS + c];
-        if (c0 + c < held && is_page(P, p)) free += give_back(P, p);
-      }
-    if (free) atomicAdd(&given, free);
-    __syncthreads();
-    if (t == 0 && given) atomicAdd(P.n_free, given);
+#pragma unroll
+    for (int k = 0; k < SELECT_CELLS; ++k) {
+      const int i = t + 1024 * k;
+      if (i >= cells) break;
+      const int b = i / n, c = i - b * n;
+      if (s_src[b] != b && c0 + c < s_held[b] && is_page(P, cell[k])) free += give_back(P, cell[k]);
+    }
+    free = __reduce_add_sync(0xffffffffu, free);
+    if (free && (t & 31) == 0) atomicAdd(P.n_free, free);
   }
-  if (t == 0) {
-    __threadfence();
-    last = atomicAdd(&P.tickets[P.batch], 1) == (int)gridDim.x - 1;
-    if (last) P.tickets[P.batch] = 0;
+  if (gridDim.x > 1) {
+    bool last = false;
+    if (t == 0) {
+      __threadfence();
+      last = atomicAdd(&P.tickets[P.batch], 1) == (int)gridDim.x - 1;
+      if (last) P.tickets[P.batch] = 0;
+    }
+    if (!__syncthreads_or(last)) return;
   }
-  __syncthreads();
-  if (last && t < P.batch && src != t) {   // every thread has read lengths above, before the barrier
+  if (t < P.batch && src != t) {   // every thread of every CTA has read lengths
     P.length[t] = n_len;
     P.held[t] = n_held;
   }
@@ -485,7 +535,7 @@ __global__ void __launch_bounds__(256) pages_trim_kernel(const __grid_constant__
 
 // Which pages move where: the r-th used page from n on to the r-th free one below n, n pages being in use.
 __global__ void __launch_bounds__(1024) pages_plan_kernel(const __grid_constant__ PagesDev P) {
-  __shared__ int s_warp[32];
+  __shared__ int2 s_warp[32];
   pages_begin();
   const int t = threadIdx.x, n = P.pages - *P.n_free;
   auto below = [](int edge, int w) {   // bits of word w whose page is below edge
@@ -493,32 +543,20 @@ __global__ void __launch_bounds__(1024) pages_plan_kernel(const __grid_constant_
     return k >= 32 ? ~0u : k <= 0 ? 0u : (1u << k) - 1u;
   };
   int from = 0, to = 0;
-  for (int base = 0; base < P.words; base += 4 * 1024) {
-    const int w = base + 4 * t;
-    uint4 x = make_uint4(0, 0, 0, 0);
-    if (w < P.words) x = *reinterpret_cast<const uint4 *>(P.bits + w);
-    const uint32_t q[4] = {x.x, x.y, x.z, x.w};
-    uint32_t hole[4], used[4];
-    int nh = 0, nu = 0;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      hole[i] = q[i] & below(n, w + i);
-      used[i] = ~q[i] & below(P.pages, w + i) & ~below(n, w + i);
-      nh += __popc(hole[i]);
-      nu += __popc(used[i]);
-    }
-    int all_h, all_u;
-    int rh = to + scan_1024(nh, s_warp, all_h), ru = from + scan_1024(nu, s_warp, all_u);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      for (uint32_t y = hole[i]; y; y &= y - 1) P.to[rh++] = (w + i) * 32 + __ffs(y) - 1;
-      for (uint32_t y = used[i]; y; y &= y - 1) P.from[ru++] = (w + i) * 32 + __ffs(y) - 1;
-    }
-    to += all_h, from += all_u;
+  for (int base = 0; base < P.words; base += 1024) {
+    const int w = base + t;
+    const uint32_t x = w < P.words ? P.bits[w] : 0u;
+    const uint32_t hole = x & below(n, w), used = ~x & below(P.pages, w) & ~below(n, w);
+    const Sums at = scan_1024(__popc(hole), __popc(used), s_warp);
+    int rh = to + at.x, ru = from + at.y;
+    for (uint32_t y = hole; y; y &= y - 1) P.to[rh++] = w * 32 + __ffs(y) - 1;
+    for (uint32_t y = used; y; y &= y - 1) P.from[ru++] = w * 32 + __ffs(y) - 1;
+    to += at.all_x, from += at.all_y;
   }
   const bool fits = from == to;   // else the count of free pages and their bits disagree: nothing moves
   if (t == 0) {
     *P.moves = fits ? from : 0;
+    *P.drawn = 0;
     if (!fits) atomicOr(P.status, QV_ERR_STATE);
   }
   if (!fits || !from) return;
@@ -627,6 +665,7 @@ qevict_status pages_args(const qevict_pages_desc *d, bool pool, void *k, void *v
   P->max_pages = d->max_pages, P->words = p->words;
   P->lg = d->page == 16 ? 4 : d->page == 32 ? 5 : d->page == 64 ? 6 : 7;
   P->status = s, P->n_free = s + 1, P->moves = s + 2, P->n_copies = s + 3;
+  P->drawn = reinterpret_cast<unsigned long long *>(s + 4);
   P->length = s + p->lay.length, P->held = s + p->lay.held, P->table = s + p->lay.table, P->refs = s + p->lay.refs;
   P->bits = reinterpret_cast<uint32_t *>(s + p->lay.free_bits);
   P->tickets = s + p->tickets, P->copies = reinterpret_cast<int4 *>(s + p->copies);
@@ -649,10 +688,10 @@ bool launch(void (*kern)(Params...), dim3 grid, int threads, qevict_stream_t str
 }
 
 unsigned ceil_div(int64_t x, int64_t y) { return (unsigned)((x + y - 1) / y); }
-// At most `most` pages to copy: no more CTAs than eight on each of 152 SMs.
+// At most `most` pages to copy: no more CTAs than fit on 152 SMs at once.
 dim3 copy_grid(const PagesDev &P, int64_t most) {
   const int64_t parts = ceil_div((int64_t)P.page * P.h_kv * 16, PART_PIECES);
-  return dim3((unsigned)std::min<int64_t>(most * parts * 2 * P.layers, 152 * 8));
+  return dim3((unsigned)std::min<int64_t>(most * parts * 2 * P.layers, 152 * 3));
 }
 bool word_ok(const void *p, bool needed) { return !((uintptr_t)p & 3) && (p || !needed); }
 
@@ -725,7 +764,10 @@ qevict_status qevict_pages_accept(const qevict_pages_desc *desc, void *k, void *
   if (st != QEVICT_OK) return st;
   if (!qv::word_ok(d_count, true) || !qv::word_ok(d_path, false) || (d_path && (max_path < 1 || max_path > qv::PG_PATH)))
     return QEVICT_EINVAL;
-  const dim3 grid(d_path ? qv::ceil_div((int64_t)P.layers * 2 * P.h_kv * 16, 256) : 1, P.batch);
+  // CTAs for every 256 columns of 16 bytes, or four on each of 152 SMs over all sequences: the table and path are looked
+  // up once a CTA
+  const unsigned cols = qv::ceil_div((int64_t)P.layers * 2 * P.h_kv * 16, 256);
+  const dim3 grid(d_path ? std::min(cols, std::max(1u, 4u * 152u / P.batch)) : 1, P.batch);
   return qv::launch(qv::pages_accept_kernel, grid, 256, stream, P, (const int *)d_count, (const int *)d_path, (int)max_path)
              ? QEVICT_OK : QEVICT_ECUDA;
 }
@@ -736,8 +778,9 @@ qevict_status qevict_pages_select(const qevict_pages_desc *desc, void *d_state, 
   const qevict_status st = qv::pages_args(desc, false, nullptr, nullptr, d_state, &p, &P);
   if (st != QEVICT_OK) return st;
   if (!qv::word_ok(d_src, true)) return QEVICT_EINVAL;
-  return qv::launch(qv::pages_select_kernel, dim3(qv::ceil_div(P.max_pages, qv::SELECT_COLS)), 1024, stream, P,
-                    (const int *)d_src) ? QEVICT_OK : QEVICT_ECUDA;
+  const int cols = std::min(P.max_pages, 1024 * qv::SELECT_CELLS / P.batch);
+  return qv::launch(qv::pages_select_kernel, dim3(qv::ceil_div(P.max_pages, cols)), 1024, stream, P, (const int *)d_src,
+                    (int)cols) ? QEVICT_OK : QEVICT_ECUDA;
 }
 
 qevict_status qevict_pages_trim(const qevict_pages_desc *desc, void *d_state, const int32_t *d_length, qevict_stream_t stream) {
