@@ -453,8 +453,8 @@ def _enter(device_index, stream, tensors, home=None, own=()):
     """The raw stream of a call on a device, and the device to make current for it (None: it is).  Tensors used on
     another stream than the device's current one are made known to the allocator, and so are the operator's `own`, which
     its caller does not see, on any stream but the one they were made on, `home`."""
-    torch = _torch()
-    other = None if torch.cuda.current_device() == device_index else torch.device("cuda", device_index)
+    torch = _torch_module or _torch()
+    other = None if torch._C._cuda_getDevice() == device_index else torch.device("cuda", device_index)
     if stream is None:
         raw = torch._C._cuda_getCurrentRawStream(device_index)
         if own and raw != home:
@@ -702,12 +702,14 @@ class _AttnPlan:
                     out = torch.empty(self.q_shape, dtype=dt, device=self.device)
                 if lse is None:
                     lse = torch.empty(self.q_shape[:3], dtype=torch.float32, device=self.device)
-        if not (_fits(q, self.q_shape, dt, i) and _fits(k, self.kv_shape, dt, i) and _fits(v, self.kv_shape, dt, i) and
-                _fits(out, self.q_shape, dt, i)):
+        qs, ks = self.q_shape, self.kv_shape
+        if not (q.dtype is dt and k.dtype is dt and v.dtype is dt and out.dtype is dt and q.shape == qs and out.shape == qs and
+                k.shape == ks and v.shape == ks and
+                q.get_device() == k.get_device() == v.get_device() == out.get_device() == i):
             for name, t, shape in (("q", q, self.q_shape), ("k", k, self.kv_shape), ("v", v, self.kv_shape),
                                    ("out", out, self.q_shape)):
                 _tensor(t, where, name, shape, dt, self.device)
-        _array(where, "lse", lse, self.q_shape[:3], _torch().float32, i)
+        _array(where, "lse", lse, qs[:3], _torch().float32, i)
         key = (q.stride(), k.stride(), v.stride(), out.stride()) + strides
         desc = self._descs.get(key)
         if desc is None:
@@ -845,15 +847,18 @@ class PagedCache:
         self.n_free = part(lay.n_free, 1)
         self.length, self.held, self.refs = part(lay.length, desc.batch), part(lay.held, desc.batch), part(lay.refs, desc.pages)
         self.table = part(lay.table, desc.batch * desc.max_pages).view(desc.batch, desc.max_pages)
-        self.index = self.state.get_device()
-        self._home, self._own = _home(self.index), (self.state, k, v)
+        self.index, self._i32 = self.state.get_device(), torch.int32
+        self._seqs, self._home, self._own = self.length.shape, _home(self.index), (self.state, k, v)
         self._desc, self._state, self._pool, self._rows = ctypes.byref(desc), self.state.data_ptr(), \
             (k.data_ptr(), v.data_ptr()), {}
         self.load()
         _settled(self.state)
 
     def _ints(self, where, name, t, shape):
-        return _array(where, name, t, shape, _torch().int32, self.index)
+        """Address of an int32 array of this shape."""
+        if t is not None and t.dtype is self._i32 and t.shape == shape and t.get_device() == self.index and t.is_contiguous():
+            return t.data_ptr()
+        return _array(where, name, t, shape, self._i32, self.index)
 
     def _run(self, name, stream, tensors, *args):
         s, other = _enter(self.index, stream, tensors, self._home, self._own)
@@ -864,7 +869,7 @@ class PagedCache:
         where = "PagedCache.load"
         _need((table is None) == (length is None), where, "table and length are given together")
         self._run("qevict_pages_load", stream, (table, length), self._state,
-                  self._ints(where, "table", table, self.table.shape), self._ints(where, "length", length, self.length.shape))
+                  self._ints(where, "table", table, self.table.shape), self._ints(where, "length", length, self._seqs))
 
     def reserve(self, new, stream=None):
         """Makes `new` rows behind every sequence writable: an int, or an int32 tensor [batch]."""
@@ -872,7 +877,7 @@ class PagedCache:
             self._run("qevict_pages_reserve", stream, (), *self._pool, self._state, None, new)
         else:
             self._run("qevict_pages_reserve", stream, (new,), *self._pool, self._state,
-                      self._ints("PagedCache.reserve", "new", new, self.length.shape), 0)
+                      self._ints("PagedCache.reserve", "new", new, self._seqs), 0)
 
     def append(self, k, v, layer=None, n=None, stream=None):
         """Writes rows behind every sequence's length: k, v [batch][n][h_kv][128] of one layer, or [layers][batch][n][h_kv][128]
@@ -889,7 +894,7 @@ class PagedCache:
             for name, t in (("k", k), ("v", v)):
                 _tensor(t, where, name, t.shape, dt, self.device)
         self._run("qevict_pages_append", stream, (k, v, n), rows, *self._pool, self._state, k.data_ptr(), v.data_ptr(),
-                  self._ints(where, "n", n, self.length.shape))
+                  self._ints(where, "n", n, self._seqs))
 
     def _rows_of(self, where, key, k, v, layer):
         """Descriptor of rows with these shapes and strides, kept for the next call."""
@@ -918,17 +923,17 @@ class PagedCache:
             most = path.shape[1]
             path_at = self._ints(where, "path", path, (self.batch, most))
         self._run("qevict_pages_accept", stream, (count, path), *self._pool, self._state,
-                  self._ints(where, "count", count, self.length.shape), None if path is None else path_at, most)
+                  self._ints(where, "count", count, self._seqs), None if path is None else path_at, most)
 
     def select(self, src, stream=None):
         """Sequence b becomes a copy of what sequence src[b] (int32 [batch]) was, or ends (-1); pages are shared, no rows copied."""
         self._run("qevict_pages_select", stream, (src,), self._state,
-                  self._ints("PagedCache.select", "src", src, self.length.shape))
+                  self._ints("PagedCache.select", "src", src, self._seqs))
 
     def trim(self, length, stream=None):
         """Cuts sequences to their first length[b] tokens (int32 [batch]; negative: as it is) and gives pages behind back."""
         self._run("qevict_pages_trim", stream, (length,), self._state,
-                  self._ints("PagedCache.trim", "length", length, self.length.shape))
+                  self._ints("PagedCache.trim", "length", length, self._seqs))
 
     def compact(self, stream=None):
         """Moves the pages in use to the beginning of the pool."""
@@ -954,28 +959,32 @@ class PagedAttention(_AttnPlan):
             _check(load().qevict_paged_attn_bytes(ctypes.byref(self._with_strides((q, pool, pool, q))), ctypes.byref(n)),
                    "qevict_paged_attn_bytes")
         self._workspace(n.value)
-        self.kv_shape = self.pool_shape
+        self.kv_shape, self._i32 = self.pool_shape, torch.int32
+        self._heads, self._seqs, self._tree, self._trees = (d.h_q,), (d.batch,), (d.s_q,), (d.batch, d.s_q)
+        self._mask = PagedAttnMask()   # (filled by every call that has one)
+        self._mask_ref = ctypes.byref(self._mask)
 
     def run(self, q, k, v, table, length, out=None, lse=None, parents=None, q_len=None, slopes=None, stream=None):
         """q [batch][s_q][h_q][128], k, v [pages][page][h_kv][128] (one layer's pool), table int32 [batch][max_pages], length
         int32 [batch]: the tokens before the queries, whose own keys and values stand behind them.  parents: int32
         [batch][s_q], or [s_q] for all.  Returns (out, lse), new tensors unless given; rows behind q_len[b] are not
         written.  Inputs that require a gradient are refused unless gradients are off."""
-        where, d, i, i32 = "PagedAttention.run", self.desc, self.index, _torch().int32
-        _no_graph(where, (q, k, v, slopes))
+        where, i, i32, mask = "PagedAttention.run", self.index, self._i32, None
+        if q.requires_grad or k.requires_grad or v.requires_grad or slopes is not None:
+            _no_graph(where, (q, k, v, slopes))
         desc, out, lse = self._tensors(where, q, k, v, out, lse, stream)
-        batch, mask = self.q_shape[:1], None
-        if not (slopes is None and q_len is None and parents is None):
-            one = parents is not None and parents.dim() == 1
-            mask = ctypes.byref(PagedAttnMask(_array(where, "slopes", slopes, (d.h_q,), _torch().float32, i),
-                                              _array(where, "q_len", q_len, batch, i32, i),
-                                              _array(where, "parents", parents, self.q_shape[1:2] if one else self.q_shape[:2],
-                                                     i32, i), int(one)))
         _need(table is not None and length is not None, where, "table and length are needed")
+        if not (slopes is None and q_len is None and parents is None):
+            mask, one = self._mask, parents is not None and parents.dim() == 1
+            mask.slopes = _array(where, "slopes", slopes, self._heads, _torch().float32, i)
+            mask.q_len = _array(where, "q_len", q_len, self._seqs, i32, i)
+            mask.parents = _array(where, "parents", parents, self._tree if one else self._trees, i32, i)
+            mask.one_tree = one
+            mask = self._mask_ref
         s, other = _enter(i, stream, (q, k, v, table, length, out, lse, parents, q_len, slopes), self._home, self._own)
         _call("qevict_paged_attn", other,
               (desc, mask, q.data_ptr(), k.data_ptr(), v.data_ptr(), _array(where, "table", table, self.table_shape, i32, i),
-               _array(where, "length", length, batch, i32, i), out.data_ptr(), lse.data_ptr(), *self._work, s))
+               _array(where, "length", length, self._seqs, i32, i), out.data_ptr(), lse.data_ptr(), *self._work, s))
         return out, lse
 
     def _with_strides(self, key):

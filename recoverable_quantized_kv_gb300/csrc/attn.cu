@@ -183,6 +183,92 @@ __global__ void __launch_bounds__(128) attn_combine_kernel(const __grid_constant
   if (lane == 0 && P.lse) P.lse[row] = l == 0.f ? -INFINITY : (mu + log2f(l)) * 0.69314718055994531f;
 }
 
+// The same for the many rows of trees and chunks over pages: a warp takes four rows of a unit, so that what their parts
+// are is worked out once and eight loads are in flight with few parts too.  Lane 4 s + r looks up part s of row r.
+template <bool FP16>
+__global__ void __launch_bounds__(128) attn_combine_rows_kernel(const __grid_constant__ AttnArgs P, int ctas) {
+  const int lane = threadIdx.x & 31, chunks = (P.part_rows + 3) / 4;
+  const uint32_t w = blockIdx.x * 4 + (threadIdx.x >> 5), unit = w / (uint32_t)chunks;   // fewer than 2^31
+  const int r0 = (int)(w - unit * chunks) * 4, gi = (int)(unit / (uint32_t)P.h_kv), g = (int)(unit - (uint32_t)gi * P.h_kv);
+  if (gi >= P.n_pr * P.batch) return attn_wait_previous();
+  const AttnGroup A = attn_group(P, gi);
+  const int first = A.tile0 * P.tpt, rows = (min(A.ql, first + 2 * P.tpt) - first) * P.G;
+  if (r0 >= rows) return attn_wait_previous();
+  int all = 0, before = 0;   // places of all groups, and of those before this one
+#pragma unroll 2
+  for (int j = lane; j < P.n_pr * P.batch; j += 32) {
+    const int places = attn_places(attn_group(P, j).tiles);
+    all += places;
+    if (j < gi) before += places;
+  }
+  all = __reduce_add_sync(0xffffffffu, all);
+  before = __reduce_add_sync(0xffffffffu, before);
+  const int share = attn_share(all * P.h_kv, ctas, P.min_tiles);
+  const int t = A.tiles, u0 = before * P.h_kv + g * attn_places(t), c0 = u0 / share;
+  const int n = t ? (u0 + t - 1) / share - c0 + 1 : 0;   // parts: the CTAs whose shares hold tiles u0 .. u0 + t - 1
+  if (n == 1) return attn_wait_previous();   // the unit was not cut: its rows are written
+  const int64_t at = (int64_t)(c0 + unit) * P.part_rows + r0;
+  attn_wait_previous();
+  const int r = lane & 3;
+  auto sum_of = [&](int s) {   // (m, l)
+    return s < n && r0 + r < rows ? P.part_l[at + (int64_t)s * P.part_rows + r] : make_float2(0.f, 0.f);
+  };
+  float mx = -INFINITY;
+  for (int s = lane >> 2; s < n; s += 8) {
+    const float2 ml = sum_of(s);
+    if (ml.y != 0.f) mx = fmaxf(mx, ml.x);
+  }
+  for (int o = 16; o >= 4; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+  const float mu = mx == -INFINITY ? 0.f : mx;
+  float l = 0.f;
+  float4 acc[4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) acc[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int s0 = 0; s0 < n; s0 += 8) {
+    const float2 ml = sum_of(s0 + (lane >> 2));
+    float weight = -1.f;   // no such part, or one without keys for the row, which wrote no output
+    if (ml.y != 0.f) {
+      weight = ml.y * ex2(ml.x - mu);
+      l += weight;
+    }
+#pragma unroll 1
+    for (int s = 0; s < min(8, n - s0); s += 2) {
+      const float *src = P.part_o + (at + (int64_t)(s0 + s) * P.part_rows) * D + 4 * lane;
+      float4 o[2][4];
+#pragma unroll
+      for (int x = 0; x < 2; ++x)
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          if (s0 + s + x < n && r0 + k < rows)
+            o[x][k] = *reinterpret_cast<const float4 *>(src + (int64_t)x * P.part_rows * D + k * D);
+#pragma unroll
+      for (int x = 0; x < 2; ++x)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const float ws = __shfl_sync(0xffffffffu, weight, (s + x) * 4 + k);   // (of part 7 + 1: lane k, not used)
+          if (s0 + s + x < n && !(ws < 0.f)) {   // a NaN weight goes on
+            acc[k].x = fmaf(ws, o[x][k].x, acc[k].x);
+            acc[k].y = fmaf(ws, o[x][k].y, acc[k].y);
+            acc[k].z = fmaf(ws, o[x][k].z, acc[k].z);
+            acc[k].w = fmaf(ws, o[x][k].w, acc[k].w);
+          }
+        }
+    }
+  }
+  for (int o = 16; o >= 4; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const float lk = __shfl_sync(0xffffffffu, l, k), mk = __shfl_sync(0xffffffffu, mu, k);
+    if (r0 + k >= rows) break;
+    const int token = (r0 + k) / P.G, i = first + token, h = g * P.G + (r0 + k) - token * P.G;
+    const float inv = lk == 0.f ? 0.f : 1.f / lk;
+    *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(P.out) + A.b * P.so[0] + i * P.so[1] + h * P.so[2] + 4 * lane) =
+        make_uint2(pack2<FP16>(acc[k].x * inv, acc[k].y * inv), pack2<FP16>(acc[k].z * inv, acc[k].w * inv));
+    if (lane == 0 && P.lse)
+      P.lse[((int64_t)A.b * P.s_q + i) * P.h_q + h] = lk == 0.f ? -INFINITY : (mk + log2f(lk)) * 0.69314718055994531f;
+  }
+}
+
 namespace {
 
 int64_t align256(int64_t x) { return (x + 255) & ~int64_t(255); }
@@ -235,6 +321,10 @@ constexpr int WHOLE_TILES = 8;
 // Caps from here on take the instances that keep small logits exact beside large ones: the others' error of 2^-22 of the cap
 // is 2^-16 of a weight at 64.
 constexpr float WIDE_CAP = 64.f;
+
+// Rows of trees over pages from which a warp merges four of them: 64 nodes of 1 / 2 / 3 sequences of 32 heads against 8K keys
+// take 29 / 33 / 44 us with a warp a row, 35 / 38 / 43 with four rows, 26 nodes of 16 against 33K 237 and 230.
+constexpr int MANY_ROWS = 6144;
 
 bool stride_ok(int64_t st, int64_t size, bool zero) {
   if (size <= 1) return true;
@@ -427,13 +517,15 @@ qevict_status attn_launch(const qevict_attn_desc *d, const AttnPlan &pl, const q
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
-    const bool few = pl.rows <= 1024;
-    cfg.gridDim = dim3((unsigned)(few ? pl.rows : (pl.rows + 3) / 4));
+    const bool few = pl.rows <= 1024, many = pg && pl.rows > MANY_ROWS;
+    const int64_t fours = ((int64_t)pl.part_rows + 3) / 4 * pl.n_pr * d->batch * d->h_kv;
+    cfg.gridDim = dim3((unsigned)(few ? pl.rows : many ? (fours + 3) / 4 : (pl.rows + 3) / 4));
     cfg.blockDim = dim3(128);
     cfg.stream = s;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     const auto combine = few ? (fp16 ? attn_combine_kernel<true, 4> : attn_combine_kernel<false, 4>)
+                      : many ? (fp16 ? attn_combine_rows_kernel<true> : attn_combine_rows_kernel<false>)
                              : (fp16 ? attn_combine_kernel<true, 1> : attn_combine_kernel<false, 1>);
     if (cudaLaunchKernelEx(&cfg, combine, A, pl.grid) != cudaSuccess) return QEVICT_ECUDA;
   }
