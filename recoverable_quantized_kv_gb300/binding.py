@@ -807,6 +807,13 @@ class PrefixAttention(_AttnPlan):
         return PrefixAttnDesc(super()._with_strides(key), self.s_prefix, _Stride2(*key[4][:2]), _Stride2(*key[5][:2]))
 
 
+def _sizes(where, **sizes):
+    """Sizes as ints of the C interface; one that is larger would be another there."""
+    for name, n in sizes.items():
+        _need(-2 ** 31 <= int(n) < 2 ** 31, where, f"{name} is out of range: {n}")
+    return tuple(int(n) for n in sizes.values())
+
+
 class PagedCache:
     """A KV cache in pages: the pool k, v [layers][pages][page][h_kv][128], and which pages hold the tokens of each of
     `batch` sequences (at most max_pages each).  A step: reserve() room, append() each layer's new rows, attend
@@ -826,13 +833,15 @@ class PagedCache:
         _need(self.device.type == "cuda", where, "the pool must be on a CUDA device")
         if self.device.index is None:
             self.device = torch.device("cuda", torch.cuda.current_device())
-        shape = tuple(int(n) for n in (layers, pages, page, h_kv, 128))
+        layers, pages, page, h_kv, batch, max_pages = _sizes(where, layers=layers, pages=pages, page=page, h_kv=h_kv, batch=batch,
+                                                            max_pages=max_pages)
+        shape = (layers, pages, page, h_kv, 128)
         step = [shape[1] * shape[2] * shape[3] * 128, shape[2] * shape[3] * 128, shape[3] * 128, 128]
         if k is not None:
             for name, t in (("k", k), ("v", v)):
                 _tensor(t, where, name, shape, self.dtype, self.device)
             _no_graph(where, (k, v))
-        desc = PagesDesc(shape[0], shape[1], shape[2], shape[3], 128, int(batch), int(max_pages), 0,
+        desc = PagesDesc(*shape, batch, max_pages, 0,
                          _Stride4(*(step if k is None else k.stride()[:4])),
                          _Stride4(*(step if v is None else v.stride()[:4])))
         self.layout = PagesLayout()
@@ -840,7 +849,7 @@ class PagedCache:
         if k is None:
             k = torch.empty(shape, dtype=self.dtype, device=self.device)
             v = torch.empty(shape, dtype=self.dtype, device=self.device)
-        self.k, self.v, self.shape, self.batch = k, v, shape, int(batch)
+        self.k, self.v, self.shape, self.batch = k, v, shape, batch
         self.state = torch.empty(self.layout.ints, dtype=torch.int32, device=self.device)
         part = lambda off, n: self.state[off:off + n]   # noqa: E731
         lay = self.layout
@@ -873,11 +882,12 @@ class PagedCache:
 
     def reserve(self, new, stream=None):
         """Makes `new` rows behind every sequence writable: an int, or an int32 tensor [batch]."""
-        if isinstance(new, int):
-            self._run("qevict_pages_reserve", stream, (), *self._pool, self._state, None, new)
-        else:
+        where = "PagedCache.reserve"
+        if hasattr(new, "data_ptr"):
             self._run("qevict_pages_reserve", stream, (new,), *self._pool, self._state,
-                      self._ints("PagedCache.reserve", "new", new, self._seqs), 0)
+                      self._ints(where, "new", new, self._seqs), 0)
+        else:
+            self._run("qevict_pages_reserve", stream, (), *self._pool, self._state, None, *_sizes(where, new=new))
 
     def append(self, k, v, layer=None, n=None, stream=None):
         """Writes rows behind every sequence's length: k, v [batch][n][h_kv][128] of one layer, or [layers][batch][n][h_kv][128]
@@ -951,10 +961,12 @@ class PagedAttention(_AttnPlan):
 
     def __init__(self, batch, s_q, pages, page, max_pages, h_q, h_kv, dtype=None, softcap=0.0, scale=0.0, device="cuda"):
         import torch
+        batch, s_q, pages, page, max_pages, h_q, h_kv = _sizes("PagedAttention", batch=batch, s_q=s_q, pages=pages, page=page,
+                                                              max_pages=max_pages, h_q=h_q, h_kv=h_kv)
         self._setup("PagedAttention", batch, s_q, 1, h_q, h_kv, dtype or torch.bfloat16, True, softcap, scale, device)
-        self.pool_shape, self.table_shape = (int(pages), int(page), int(h_kv), 128), (int(batch), int(max_pages))
-        h, n, d = int(h_kv), ctypes.c_size_t(), self.desc
-        pool, q = (int(page) * h * 128, h * 128, 128), tuple(d.q)
+        self.pool_shape, self.table_shape = (pages, page, h_kv, 128), (batch, max_pages)
+        n, d = ctypes.c_size_t(), self.desc
+        pool, q = (page * h_kv * 128, h_kv * 128, 128), tuple(d.q)
         with torch.cuda.device(self.device):
             _check(load().qevict_paged_attn_bytes(ctypes.byref(self._with_strides((q, pool, pool, q))), ctypes.byref(n)),
                    "qevict_paged_attn_bytes")

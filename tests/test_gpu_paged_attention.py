@@ -230,6 +230,19 @@ def test_unseen_places_may_hold_anything(lib, dtype, bad, cap):
     assert torch.isfinite(out[0, ~sees].float()).all()
 
 
+@pytest.mark.parametrize("s_q,n", [(20, 300), (150, 700), (3, 0), (150, 5000)])
+@pytest.mark.parametrize("dtype,bad", [(BF, math.nan), (FP, math.inf)])
+def test_a_later_tokens_value_in_a_chain(lib, s_q, n, dtype, bad):
+    """Rows before the token are unchanged to the bound: whole units and parts of them, over pages."""
+    page, at = 16, n + s_q // 2
+
+    def later(q, k, v, table):
+        v[table[0, at // page].long(), at % page, 1, 70] = bad
+
+    out = run_case([n, 44], s_q, 4, 2, page, dtype, change=later)[1][4]
+    assert torch.isfinite(out[0, :s_q // 2].float()).all() and not torch.isfinite(out[0, s_q // 2:, 2:, 70].float()).any()
+
+
 def test_logits_beyond_whole_numbers(lib):
     """Rows whose largest logit is past 2^23: worked out again over pages and lines of the tree."""
     n, m, page = 200, 10, 16

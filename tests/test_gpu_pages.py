@@ -328,3 +328,21 @@ def test_streams_and_graphs(lib):
         g.replay()
         ref()
         x.same()
+
+
+def test_other_devices_streams_and_refusals(lib):
+    """Arguments on the wrong device, of the wrong shape, type or layout, and sizes that another integer would hold."""
+    c = binding.PagedCache(2, 8, 16, 2, 3, 4)
+    x, n = torch.zeros(3, 5, 2, 128, dtype=BF, device="cuda"), i32([1, 1, 1])
+    for call in (lambda: c.append(x.cpu(), x, layer=0), lambda: c.append(x, x, layer=2), lambda: c.append(x, x, layer=-1),
+                 lambda: c.append(x, x), lambda: c.append(x, x[:, :4], layer=0), lambda: c.append(x.to(FP), x, layer=0),
+                 lambda: c.append(x[..., ::2], x, layer=0), lambda: c.append(x, x, layer=0, n=n.long()),
+                 lambda: c.append(x.clone().requires_grad_(), x, layer=0), lambda: c.accept(n[:2]), lambda: c.accept(None),
+                 lambda: c.accept(n, i32([1, 2, 3])), lambda: c.accept(n, i32([[0, 1]] * 2)), lambda: c.select(n.cpu()),
+                 lambda: c.trim(i32([[1], [1], [1]])), lambda: c.reserve(n.float()), lambda: c.reserve(-1),
+                 lambda: c.reserve(2 ** 32), lambda: c.load(c.table), lambda: c.load(c.table[:, :3], c.length),
+                 lambda: c.load(i32([[0] * 4] * 4)[:3].t(), n)):
+        with pytest.raises(binding.QEvictError):
+            call()
+    c.check()
+    assert int(c.n_free) == 8 and not bool(c.length.any())

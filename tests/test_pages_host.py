@@ -144,3 +144,6 @@ def test_binding_refuses_before_the_library(lib):
         B.PagedCache(1, 4, 16, 2, 1, 4, k=x)
     with pytest.raises(B.QEvictError):
         B.PagedCache(1, 4, 16, 2, 1, 4, dtype=torch.float32)
+    for kw in (dict(pages=2 ** 32 + 4), dict(max_pages=2 ** 32 + 4), dict(batch=-2 ** 33)):
+        with pytest.raises(B.QEvictError):
+            B._sizes("PagedCache", **kw)
