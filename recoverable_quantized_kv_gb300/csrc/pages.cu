@@ -193,7 +193,7 @@ struct RowsDev {
 // memory: 4099 + 3075 rows of 8 heads in 8 layers 71 us (6.6 TB/s; with addresses kept over the loads, 90 registers, 81).
 constexpr int APPEND_THREADS = 256, APPEND_PIECES = 4;
 __global__ void __launch_bounds__(APPEND_THREADS, 4) pages_append_kernel(const __grid_constant__ PagesDev P,
-                                                                     const __grid_constant__ RowsDev R) {
+                                                                        const __grid_constant__ RowsDev R) {
   pages_begin();
   const int b = blockIdx.y, held = held_of(P, b), len = length_of(P, b, held);
   int n = R.n;
@@ -239,11 +239,14 @@ __global__ void __launch_bounds__(APPEND_THREADS, 4) pages_append_kernel(const _
 // Accepted rows move down their sequence.  A thread owns 16 bytes of every row of one (layer, K or V, head) and moves them in
 // ascending order, eight rows at a time, all loads before the stores: row path[j] >= j, so a row is read before anything
 // lands on it, and no other thread touches these bytes.  The sequence's last CTA to have read its length counts the rows in.
-// Bound by the chain from lengths over path and table to the rows, then by memory; the counts of the pages written to are
-// looked up while the first rows are on their way.
+// Bound by the chain from lengths over path and table to the rows (4 sequences in 32 layers 3 us), then by memory in
+// pieces of a row: 256 sequences in 8 layers 14 us, 4.2 TB/s (17 with places worked out by every thread; 16 with keys and
+// values by one thread, sixteen loads in flight).  The counts of the pages written to are looked up while the first rows
+// are on their way.
 __global__ void __launch_bounds__(256) pages_accept_kernel(const __grid_constant__ PagesDev P, const int *d_count,
                                                           const int *d_path, int max_path) {
-  __shared__ int s_from[PG_PATH], s_to[PG_PATH], last;   // page << 7 | row; from -1: nothing to move
+  __shared__ int64_t s_from[2][PG_PATH], s_to[2][PG_PATH];   // places of the rows that move, keys and values
+  __shared__ int s_moved[8], last;
   pages_begin();
   const int b = blockIdx.y, j = threadIdx.x, held = held_of(P, b), len = length_of(P, b, held), count = d_count[b];
   const int *row = row_of(P, b);
@@ -255,15 +258,14 @@ __global__ void __launch_bounds__(256) pages_accept_kernel(const __grid_constant
     if (j) before = path[j - 1];
   }
   const bool fits = count >= 0 && (!d_path || count <= max_path) && (int64_t)len + count <= room;
-  bool ok = fits;
-  int dst = -1;
+  bool ok = fits, moves = false;
+  int src = -1, dst = -1;
   if (fits && d_path && j < count) {
     ok = at > before && at >= 0 && (int64_t)len + at < room;
-    const int src = ok ? row[(len + at) >> P.lg] : -1;
+    src = ok ? row[(len + at) >> P.lg] : -1;
     dst = row[(len + j) >> P.lg];
     ok = ok && is_page(P, src) && is_page(P, dst);
-    s_from[j] = ok && at != j ? src << 7 | ((len + at) & (P.page - 1)) : -1;
-    s_to[j] = dst << 7 | ((len + j) & (P.page - 1));
+    moves = ok && at != j;
     if (ok) ok = P.refs[dst] == 1;   // rows of shared pages are never written
   } else if (fits && !d_path) {
     for (int c = (len >> P.lg) + j; (int64_t)c << P.lg < (int64_t)len + count; c += blockDim.x)
@@ -283,30 +285,42 @@ __global__ void __launch_bounds__(256) pages_accept_kernel(const __grid_constant
     }
     return ok;
   };
-  if (!fits || !d_path || count == 0) {
+  const uint32_t here = __ballot_sync(0xffffffffu, moves);
+  if ((j & 31) == 0) s_moved[j >> 5] = __popc(here);
+  __syncthreads();
+  int n = 0, mine = __popc(here & ((1u << (j & 31)) - 1));   // rows that move, and those in front of this one
+#pragma unroll
+  for (int w = 0; w < 8; ++w) {
+    if (w < j >> 5) mine += s_moved[w];
+    n += s_moved[w];
+  }
+  if (n == 0) {
     settle();
     return;
+  }
+  if (moves) {
+    const int a = (len + at) & (P.page - 1), z = (len + j) & (P.page - 1);
+    s_from[0][mine] = src * P.sk[1] + a * P.sk[2], s_from[1][mine] = src * P.sv[1] + a * P.sv[2];
+    s_to[0][mine] = dst * P.sk[1] + z * P.sk[2], s_to[1][mine] = dst * P.sv[1] + z * P.sv[2];
   }
   __syncthreads();
   const uint32_t all = 2u * P.layers * P.h_kv * 16;
   bool settled = false;
   for (uint32_t x0 = blockIdx.x * 256; x0 < all; x0 += gridDim.x * 256) {
-    const uint32_t x = min(x0 + threadIdx.x, all - 1), h = x >> 4, l2 = h / (uint32_t)P.h_kv;
-    const bool mine = x0 + threadIdx.x < all, is_v = l2 & 1;
+    const uint32_t x = min(x0 + threadIdx.x, all - 1), h = x >> 4, l2 = h / (uint32_t)P.h_kv, is_v = l2 & 1;
+    const bool in = x0 + threadIdx.x < all;
     uint16_t *pool = is_v ? P.v : P.k;
-    const int64_t st_p = is_v ? P.sv[1] : P.sk[1], st_t = is_v ? P.sv[2] : P.sk[2];
     pool += (l2 >> 1) * (is_v ? P.sv[0] : P.sk[0]) + (h - l2 * P.h_kv) * (is_v ? P.sv[3] : P.sk[3]) + (x & 15) * 8;
-    auto place = [&](int e) { return reinterpret_cast<uint4 *>(pool + (e >> 7) * st_p + (e & 127) * st_t); };
-    for (int j0 = 0; j0 < count; j0 += 8) {
+    for (int i0 = 0; i0 < n; i0 += 8) {
       uint4 w[8];
 #pragma unroll
       for (int i = 0; i < 8; ++i)
-        if (mine && j0 + i < count && s_from[j0 + i] >= 0) w[i] = *place(s_from[j0 + i]);
+        if (in && i0 + i < n) w[i] = *reinterpret_cast<const uint4 *>(pool + s_from[is_v][i0 + i]);
       if (!settled && !settle()) return;
       settled = true;
 #pragma unroll
       for (int i = 0; i < 8; ++i)
-        if (mine && j0 + i < count && s_from[j0 + i] >= 0) *place(s_to[j0 + i]) = w[i];
+        if (in && i0 + i < n) *reinterpret_cast<uint4 *>(pool + s_to[is_v][i0 + i]) = w[i];
     }
   }
 }
@@ -316,8 +330,8 @@ __global__ void __launch_bounds__(256) pages_accept_kernel(const __grid_constant
 // Who needs which pages, a thread a sequence; then the free bits are walked from the lowest page on, a word a thread, and
 // the r-th free page goes to whom the running sum of needs says, a thread a page: it finds word and sequence by their sums.
 // Nothing is written before the pages are known to suffice.  Bound by latency: lengths, table, counts in a chain of
-// loads, then a few barriers for every 32768 pages (a thread that hands out all pages of its 128 bits took 30 us for 64
-// samples of 4 prompts, 6 now).
+// loads, then a few barriers for every 32768 pages: 2.5 us with the copying kernel where nothing is needed, 5 for 16
+// sequences of 33K tokens that grow.  (A thread that hands out all pages of its 128 bits took 30 us for 64 samples of 4 prompts.)
 __global__ void __launch_bounds__(1024) pages_reserve_kernel(const __grid_constant__ PagesDev P, const int *d_new, int n_new) {
   __shared__ int s_tail[PG_BATCH], s_start[PG_BATCH], s_len[PG_BATCH], s_held[PG_BATCH], s_copy[PG_BATCH], s_rank[1024];
   __shared__ uint32_t s_word[1024];
@@ -350,15 +364,28 @@ __global__ void __launch_bounds__(1024) pages_reserve_kernel(const __grid_consta
     return;
   }
   bool copy = false;
-  if (refs > 1) {   // shared: by how many that reserve now, and is this the first of them
+  // Shared pages: how many that reserve now hold each, and is this the first of them.  A look at every other sequence costs
+  // 8 of them 0.6 us less than counts in memory, 256 the same, 1024 30 us more.
+  if (P.batch <= 256) {
     int same = 0, before = 0;
+    if (refs > 1) {
 #pragma unroll 8
-    for (int j = 0; j < P.batch; ++j)
-      if (s_tail[j] == tail) {
-        ++same;
-        before += j < t;
-      }
-    copy = same < refs || before > 0;
+      for (int j = 0; j < P.batch; ++j)
+        if (s_tail[j] == tail) {
+          ++same;
+          before += j < t;
+        }
+      copy = same < refs || before > 0;
+    }
+  } else if (__syncthreads_or(refs > 1)) {
+    if (refs > 1) P.goes[tail] = P.batch, P.to[tail] = 0;   // (scratch of a compaction)
+    __syncthreads();
+    if (refs > 1) {
+      atomicMin(&P.goes[tail], t);
+      atomicAdd(&P.to[tail], 1);
+    }
+    __syncthreads();
+    if (refs > 1) copy = __ldcg(&P.to[tail]) < refs || __ldcg(&P.goes[tail]) < t;
   }
   const Sums need = scan_1024(add + copy, copy, s_warp);
   const int total = need.all_x;
@@ -430,7 +457,8 @@ __global__ void __launch_bounds__(1024) pages_reserve_kernel(const __grid_consta
   }
 }
 
-// The rows of the pages that a reserve copied.
+// The rows of the pages that a reserve copied.  Bound by memory: 60 copies of 4 pages in 16 layers, 24 MB read and 356 written,
+// 62 us.
 template <bool DENSE>
 __global__ void __launch_bounds__(256) pages_tail_kernel(const __grid_constant__ PagesDev P) {
   pages_begin();
@@ -439,7 +467,8 @@ __global__ void __launch_bounds__(256) pages_tail_kernel(const __grid_constant__
 
 // Tables rearranged.  A CTA takes the same places of all sequences, up to 8192 entries: it reads them all before it writes
 // any, and since a page stands at one place of the tables, it counts every entry that a page gains before the ones it loses.
-// Lengths change once all CTAs have read them: by the last of them.  Bound by its chain of loads and atomics.
+// Lengths change once all CTAs have read them: by the last of them.  Bound by its chain of loads and atomics: 8 beams 2.5 us,
+// 64 samples of 9 pages 3, 1024 sequences of 32 pages 10.
 constexpr int SELECT_CELLS = 8;   // entries of a thread
 __global__ void __launch_bounds__(1024) pages_select_kernel(const __grid_constant__ PagesDev P, const int *d_src, int cols) {
   __shared__ int s_old[1024 * SELECT_CELLS];
@@ -510,6 +539,7 @@ __global__ void __launch_bounds__(1024) pages_select_kernel(const __grid_constan
   }
 }
 
+// A CTA a sequence.  Bound by latency: 1.4 us where nothing is given back.
 __global__ void __launch_bounds__(256) pages_trim_kernel(const __grid_constant__ PagesDev P, const int *d_length) {
   __shared__ int given;
   pages_begin();
@@ -533,7 +563,8 @@ __global__ void __launch_bounds__(256) pages_trim_kernel(const __grid_constant__
   }
 }
 
-// Which pages move where: the r-th used page from n on to the r-th free one below n, n pages being in use.
+// Which pages move where: the r-th used page from n on to the r-th free one below n, n pages being in use.  Bound by latency: a
+// round of barriers for every 32768 pages, 2.5 us with the copying kernel where nothing moves, 20 for a pool of a million pages.
 __global__ void __launch_bounds__(1024) pages_plan_kernel(const __grid_constant__ PagesDev P) {
   __shared__ int2 s_warp[32];
   pages_begin();
@@ -570,7 +601,8 @@ __global__ void __launch_bounds__(1024) pages_plan_kernel(const __grid_constant_
   for (int w = t; w < P.words; w += 1024) P.bits[w] = below(P.pages, w) & ~below(n, w);
 }
 
-// The moves themselves, and the tables.
+// The moves themselves, and the tables.  Bound by memory: 700 pages of 64 tokens and 8 heads in 8 layers, 174 of which move, 107
+// us (6.8 TB/s).
 template <bool DENSE>
 __global__ void __launch_bounds__(256) pages_move_kernel(const __grid_constant__ PagesDev P) {
   pages_begin();
