@@ -305,7 +305,7 @@ bool dense_map(CUtensorMap *map, bool fp16, const void *base, int64_t heads, int
 }
 
 struct AttnPlan {
-  int G, tpt, n_pr, stream, grid;
+  int G, tpt, n_pr, stream, whole, grid;
   int pre, nb, n_prp;
   int part_rows, pre_rows;
   int64_t rows, off_runs, off_l, off_o, off_pl, off_po, bytes;
@@ -325,6 +325,20 @@ constexpr float WIDE_CAP = 64.f;
 // Rows of trees over pages from which a warp merges four of them: 64 nodes of 1 / 2 / 3 sequences of 32 heads against 8K keys
 // take 29 / 33 / 44 us with a warp a row, 35 / 38 / 43 with four rows, 26 nodes of 16 against 33K 237 and 230.
 constexpr int MANY_ROWS = 6144;
+
+// Units of one row tile over pages, `tiles` key tiles at most: drawn whole by the CTAs, in one launch, or cut into shares and
+// merged?  Estimates of both in us, from batches of 1 to 64 of 8 KV heads, equal and ragged lengths, on 152 SMs.  Whole: 1.45
+// a tile and round of units (1.2 where some SMs are idle, so that memory is), 2 a further round, 5.5 to start.  Cut: 1.45 a
+// tile and 6 a unit over all SMs, 11.5 to start and merge (13.5 with units for all SMs); with fewer units than SMs whole ones
+// wait for the longest sequence, so ragged batches count 1.25 a tile.  Single tokens, whole and cut: 3 sequences of 8 KV heads
+// against 300 keys 9 and 11 us, 12 against 1040 19 and 23, 64 against 560 33 and 51, 64 against 4160 124 and 126; one
+// against 1040 16 and 11, 4 against 4160 47 and 21.
+bool whole_units(int64_t units, int64_t tiles, int64_t sms) {
+  const double rounds = (double)(units / sms), all = (double)units / sms;
+  const double whole = 5.5 + tiles * (1.45 * rounds + (units % sms ? 1.2 : 0.0)) + 2.0 * rounds;
+  const double cut = units > sms ? 13.5 + all * (1.45 * tiles + 6.0) : 11.5 + all * (1.25 * tiles + 6.0);
+  return whole <= cut;
+}
 
 bool stride_ok(int64_t st, int64_t size, bool zero) {
   if (size <= 1) return true;
@@ -380,7 +394,11 @@ qevict_status attn_plan(const qevict_attn_desc *d, int s_prefix, AttnPlan *p, bo
     if (s_prefix) return QEVICT_EINVAL;
     p->stream = 0;
   }
-  p->grid = (int)std::min(sms, p->stream ? (total + MIN_TILES - 1) / MIN_TILES : units);
+  if (paged && n_qt == 1) {   // (the stream's instances, which take a single row tile's keys two tiles at a time, for both)
+    p->whole = !p->stream || whole_units(units, tiles, sms) || total > (1 << 30) || p->rows > (1ll << 30);
+    p->stream = 1;
+  }
+  p->grid = (int)std::min(sms, p->stream && !p->whole ? (total + MIN_TILES - 1) / MIN_TILES : units);
   int64_t off = 256;
   auto take = [&](int64_t n) {
     const int64_t o = off;
@@ -388,7 +406,7 @@ qevict_status attn_plan(const qevict_attn_desc *d, int s_prefix, AttnPlan *p, bo
     return o;
   };
   if (!s_prefix && !paged) p->off_runs = take((int64_t)d->batch * d->s_kv * 8);
-  if (p->stream) {
+  if (p->stream && !p->whole) {
     p->part_rows = std::min(d->s_q, 2 * p->tpt) * p->G;
     const int64_t parts = p->grid + units;
     p->off_l = take(parts * p->part_rows * 8);
@@ -455,7 +473,7 @@ qevict_status attn_launch(const qevict_attn_desc *d, const AttnPlan &pl, const q
   A.tpt = pl.tpt, A.n_pr = pl.n_pr;
   A.pre = pl.pre, A.nb = std::max(1, pl.nb), A.n_prp = pl.n_prp;
   A.part_rows = pl.part_rows, A.pre_rows = pl.pre_rows;
-  A.stream = pl.stream, A.min_tiles = MIN_TILES;
+  A.stream = pl.stream, A.whole = pl.whole, A.min_tiles = MIN_TILES;
   const float scale = logit_scale(d), log2e = 1.4426950408889634f;
   A.scale_log2 = scale * log2e;
   if (d->softcap > 0.f) {
@@ -499,7 +517,7 @@ qevict_status attn_launch(const qevict_attn_desc *d, const AttnPlan &pl, const q
     doc_runs_kernel<<<d->batch, RUN_THREADS, 0, s>>>(m.doc_ids, d->s_kv, const_cast<int2 *>(A.runs));
     if (cudaGetLastError() != cudaSuccess) return QEVICT_ECUDA;
   }
-  if (pl.stream) {
+  if (pl.stream && !pl.whole) {
     A.part_l = reinterpret_cast<float2 *>(w + pl.off_l);
     A.part_o = reinterpret_cast<float *>(w + pl.off_o);
     A.pre_l = reinterpret_cast<float2 *>(w + pl.off_pl);
@@ -512,7 +530,7 @@ qevict_status attn_launch(const qevict_attn_desc *d, const AttnPlan &pl, const q
                       : d->softcap > 0.f    ? (fp16 ? launch_attn_fp16_cap : launch_attn_bf16_cap)
                                             : (fp16 ? launch_attn_fp16 : launch_attn_bf16);
   if (launch(A, pl.grid, m.slopes != nullptr, s) != cudaSuccess) return QEVICT_ECUDA;
-  if (pl.stream) {
+  if (pl.stream && !pl.whole) {
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

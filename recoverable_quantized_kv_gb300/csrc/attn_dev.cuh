@@ -58,6 +58,7 @@ struct AttnArgs {
   const int *parents;          // NULL: query i sees the queries before it; else its ancestors
   int64_t parents_step;        // between sequences: s_q, or 0
   int pages, max_pages, page_lg;
+  int whole;                   // of units of one row tile: none is cut
   int64_t sq[3], sk[3], sv[3], so[3], skp[2], svp[2];
   int batch, s_q, s_kv, h_q, h_kv, G, causal;
   int mul_q, mul_k, mul_v;     // batch coordinate of the tensor maps: 0 for a batch stride of 0
@@ -620,7 +621,8 @@ __global__ void __launch_bounds__(AT_THREADS, 1) attn_kernel(const __grid_consta
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   AttnGroup plan_a;        // the plan warp's lane: its group of the first 32, worked out while the others set up
   int plan_places = 0;     // and the places of all groups
-  if (warp == AT_W_PLAN && STREAM) {
+  const bool whole = !STREAM || (PAGED && P.whole);
+  if (warp == AT_W_PLAN && !whole) {
     const int groups = P.n_pr * P.batch;
 #pragma unroll 1
     for (int g0 = 0; g0 < groups; g0 += 32) {
@@ -673,7 +675,7 @@ __global__ void __launch_bounds__(AT_THREADS, 1) attn_kernel(const __grid_consta
       return I;
     };
     const int groups = P.n_pr * P.batch;
-    if (!STREAM) {
+    if (whole) {
       // Whole units, the longest (last rows of causal prompts) first, each to the CTA that is ready next: lengths and
       // documents make units differ, and a fixed turn leaves some CTAs twice the mean (a padded batch of prefix-mask
       // prompts 54 us, drawn 31).  A CTA's first unit is its own number; it draws the next when its TMA warp has asked
@@ -854,7 +856,7 @@ __global__ void __launch_bounds__(AT_THREADS, 1) attn_kernel(const __grid_consta
         }, prefix ? &P.tkp : &P.tk, prefix ? &P.tvp : &P.tv, I.b * P.mul_k, I.b * P.mul_v);
       }
       ok = __shfl_sync(0xffffffffu, (int)ok, 0);
-      if (!STREAM && lane == 0) mbar_arrive(loaded);
+      if (whole && lane == 0) mbar_arrive(loaded);
     }
     if (lane == 0) {   // copies still in flight land before the CTA leaves
       for (uint32_t i = c > AT_STAGES ? c - AT_STAGES : 0; i < c; ++i)
