@@ -19,7 +19,9 @@ constexpr int AT_TILE_BYTES = AT_TILE * D * 2;        // 32 KB: two 128-byte-swi
 constexpr int AT_HALF_BYTES = AT_TILE_BYTES / 2;
 constexpr int AT_SOFT = 16;                           // softmax warps: four for each quarter of the columns
 constexpr int AT_W_LOAD = AT_SOFT, AT_W_MMA = AT_SOFT + 1, AT_W_PLAN = AT_SOFT + 2;   // TMA, MMA, work items
-constexpr int AT_THREADS = (AT_SOFT + 3) * 32;        // five warps on an SM sub-partition: 96 registers a thread
+constexpr int AT_W_VALUES = AT_SOFT + 3;               // over pages: TMA of the values, beside the keys'
+// five warps on an SM sub-partition: 96 registers a thread
+__host__ __device__ constexpr int attn_threads(bool paged) { return (paged ? AT_SOFT + 4 : AT_SOFT + 3) * 32; }
 constexpr int AT_COLS = AT_TILE / 4;                  // columns of S, and channels of O, per softmax thread
 constexpr int AT_ITEMS = 4;                           // work items described ahead
 constexpr int AT_OFF_KV = 2 * AT_TILE_BYTES;
@@ -584,7 +586,7 @@ __device__ __forceinline__ void attn_exact_rows(const AttnArgs &P, const AttnIte
 // held 64 a time in the copying warp's registers, the next 32 on their way while the last are used.  A row of a tree of drafts
 // sees the keys before the tree and a line of up to 64 nodes, found by a walk while the first keys are on their way.
 template <bool FP16, int CAP, bool BIAS, bool STREAM, bool PAGED = false>
-__global__ void __launch_bounds__(AT_THREADS, 1) attn_kernel(const __grid_constant__ AttnArgs P) {
+__global__ void __launch_bounds__(attn_threads(PAGED), 1) attn_kernel(const __grid_constant__ AttnArgs P) {
   extern __shared__ __align__(1024) uint8_t sm[];   // swizzle atoms: 1024-aligned
   uint64_t *bars = reinterpret_cast<uint64_t *>(sm + AT_OFF_BAR);
   uint64_t *full = bars, *empty = full + AT_STAGES, *qfull = empty + AT_STAGES, *qempty = qfull + 2;
@@ -610,7 +612,7 @@ __global__ void __launch_bounds__(AT_THREADS, 1) attn_kernel(const __grid_consta
   } else if (threadIdx.x < AT_NBAR) {
     const uint64_t *p = &bars[threadIdx.x];
     const int n = p < pfull ? 1 : p < ofull ? AT_SOFT :
-                  p < ifull ? 2 : p < iempty ? 1 : p < loaded ? AT_SOFT + 2 : 1;
+                  p < ifull ? 2 : p < iempty ? 1 : p < loaded ? AT_SOFT + (PAGED ? 3 : 2) : 1;
     mbar_init(&bars[threadIdx.x], n);
     fence_mbar_init();
     if (threadIdx.x < 2) bad_item[threadIdx.x] = 0;
@@ -778,8 +780,9 @@ __global__ void __launch_bounds__(AT_THREADS, 1) attn_kernel(const __grid_consta
         const int ql = P.q_len ? clampi(P.q_len[b], 0, P.s_q) : P.s_q;
         if (P.ctx_len[b] < 0 || P.ctx_len[b] > P.s_kv - ql) atomicOr(status, QV_ERR_BOUNDS);
       }
-  } else if (warp == AT_W_LOAD) {
+  } else if (warp == AT_W_LOAD || (PAGED && warp == AT_W_VALUES)) {
     // ---- TMA loads
+    const bool values = PAGED && warp == AT_W_VALUES;
     const uint32_t qbytes = (uint32_t)(P.G * P.tpt) * 256u, qpbytes = (uint32_t)(P.G * P.s_q * P.nb) * 256u;
     uint32_t c = 0, qn = 0;
     bool ok = true;
@@ -809,7 +812,7 @@ __global__ void __launch_bounds__(AT_THREADS, 1) attn_kernel(const __grid_consta
         }
       };
       if (PAGED && I.n > 0) {   // the whole warp, in step
-        if (lane == 0) queries();
+        if (!values && lane == 0) queries();
         ok = __shfl_sync(0xffffffffu, (int)ok, 0);
         qn = __shfl_sync(0xffffffffu, qn, 0);
         const int lg = P.page_lg, per = AT_TILE >> lg, used = (I.kl + (1 << lg) - 1) >> lg;   // pages of a tile, of the sequence
@@ -817,6 +820,10 @@ __global__ void __launch_bounds__(AT_THREADS, 1) attn_kernel(const __grid_consta
         int w = ((I.t_hi - 1) * per) & ~31;   // a tile's pages lie in one window of 32: [w, w + 32) or the one below
         int here = entry(w + lane), below = entry(w - 32 + lane);
         in_order([&](const CUtensorMap *map, int j, int) {
+          if ((map == &P.tv) != values) {   // the other warp's
+            ++c;
+            return;
+          }
           const uint32_t st = c % AT_STAGES;
           if (!ok || !(ok = attn_wait_warp(&empty[st], ((c / AT_STAGES) & 1) ^ 1, status))) return;
           const uint32_t dst = smem_u32(sm) + AT_OFF_KV + st * AT_TILE_BYTES;
@@ -856,9 +863,9 @@ __global__ void __launch_bounds__(AT_THREADS, 1) attn_kernel(const __grid_consta
         }, prefix ? &P.tkp : &P.tk, prefix ? &P.tvp : &P.tv, I.b * P.mul_k, I.b * P.mul_v);
       }
       ok = __shfl_sync(0xffffffffu, (int)ok, 0);
-      if (whole && lane == 0) mbar_arrive(loaded);
+      if (whole && !values && lane == 0) mbar_arrive(loaded);
     }
-    if (lane == 0) {   // copies still in flight land before the CTA leaves
+    if (!values && lane == 0) {   // copies still in flight land before the CTA leaves
       for (uint32_t i = c > AT_STAGES ? c - AT_STAGES : 0; i < c; ++i)
         attn_wait(&full[i % AT_STAGES], (i / AT_STAGES) & 1, status);
       for (uint32_t i = qn > 2 ? qn - 2 : 0; i < qn; ++i) attn_wait(&qfull[i & 1], (i >> 1) & 1, status);
@@ -1457,13 +1464,13 @@ __global__ void __launch_bounds__(AT_THREADS, 1) attn_kernel(const __grid_consta
 
 // (Programmatic launch: the kernel's setup overlaps the end of the one before.)
 template <typename Kernel>
-cudaError_t launch_attn_kernel(Kernel kern, const AttnArgs &P, int grid, cudaStream_t s) {
+cudaError_t launch_attn_kernel(Kernel kern, bool paged, const AttnArgs &P, int grid, cudaStream_t s) {
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.gridDim = dim3((unsigned)grid);
-  cfg.blockDim = dim3(AT_THREADS);
+  cfg.blockDim = dim3(attn_threads(paged));
   cfg.dynamicSmemBytes = AT_SMEM;
   cfg.stream = s;
   cfg.attrs = attr;
@@ -1477,8 +1484,8 @@ cudaError_t launch_attn_variant(const AttnArgs &P, int grid, cudaStream_t s) {
   cudaError_t e = P.stream ? stream.ensure(attn_kernel<FP16, CAP, BIAS, true, PAGED>, AT_SMEM)
                            : units.ensure(attn_kernel<FP16, CAP, BIAS, false, PAGED>, AT_SMEM);
   if (e != cudaSuccess) return e;
-  return P.stream ? launch_attn_kernel(attn_kernel<FP16, CAP, BIAS, true, PAGED>, P, grid, s)
-                  : launch_attn_kernel(attn_kernel<FP16, CAP, BIAS, false, PAGED>, P, grid, s);
+  return P.stream ? launch_attn_kernel(attn_kernel<FP16, CAP, BIAS, true, PAGED>, PAGED, P, grid, s)
+                  : launch_attn_kernel(attn_kernel<FP16, CAP, BIAS, false, PAGED>, PAGED, P, grid, s);
 }
 
 }  // namespace qv
