@@ -327,16 +327,16 @@ constexpr float WIDE_CAP = 64.f;
 constexpr int MANY_ROWS = 6144;
 
 // Units of one row tile over pages, `tiles` key tiles at most: drawn whole by the CTAs, in one launch, or cut into shares and
-// merged?  Estimates of both in us, from batches of 1 to 64 of 8 KV heads, equal and ragged lengths, on 152 SMs.  Whole: 1.45
-// a tile and round of units (1.2 where some SMs are idle, so that memory is), 2 a further round, 5.5 to start.  Cut: 1.45 a
-// tile and 6 a unit over all SMs, 11.5 to start and merge (13.5 with units for all SMs); with fewer units than SMs whole ones
-// wait for the longest sequence, so ragged batches count 1.25 a tile.  Single tokens, whole and cut: 3 sequences of 8 KV heads
-// against 300 keys 9 and 11 us, 12 against 1040 19 and 23, 64 against 560 33 and 51, 64 against 4160 124 and 126; one
-// against 1040 16 and 11, 4 against 4160 47 and 21.
+// merged?  Both are estimated in us.  Whole: a round of units on all SMs takes 1.45 a tile and 1 more, the last one on some of
+// them 0.55 to 0.95 a tile.  Cut: 1.4 a tile and 6 a unit, shared by all SMs; with fewer units than SMs, where whole ones wait for
+// the longest sequence, 0.97 a tile.  The rates are those with which the choice cost least over batches of 1 to 64, equal and
+// ragged, against 420 to 32500 keys: 0.8% on average, 20% at most.  Single tokens of ragged batches of 8 KV heads, whole and cut:
+// 4 sequences against 420 / 1040 / 4160 keys 9.7 / 14.1 / 36 and 11.8 / 14.9 / 21 us, 12 against 1040 / 2040 / 4160 16.0 / 23.0 /
+// 39 and 21.9 / 27.0 / 37, 16 against 32500 255 and 218, 64 against 1040 / 4160 45 / 119 and 64 / 124.
 bool whole_units(int64_t units, int64_t tiles, int64_t sms) {
-  const double rounds = (double)(units / sms), all = (double)units / sms;
-  const double whole = 5.5 + tiles * (1.45 * rounds + (units % sms ? 1.2 : 0.0)) + 2.0 * rounds;
-  const double cut = units > sms ? 13.5 + all * (1.45 * tiles + 6.0) : 11.5 + all * (1.25 * tiles + 6.0);
+  const double rounds = (double)(units / sms), last = (double)(units % sms) / sms, all = (double)units / sms;
+  const double whole = 5.0 + tiles * (1.45 * rounds + (last > 0.0 ? 0.55 + 0.4 * last : 0.0)) + rounds;
+  const double cut = units > sms ? 16.0 + all * (1.4 * tiles + 6.0) : 8.0 + all * (0.97 * tiles + 6.0);
   return whole <= cut;
 }
 
