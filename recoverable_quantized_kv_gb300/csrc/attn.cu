@@ -339,6 +339,12 @@ bool whole_units(int64_t units, int64_t tiles, int64_t sms) {
   const double cut = units > sms ? 16.0 + all * (1.4 * tiles + 6.0) : 8.0 + all * (0.97 * tiles + 6.0);
   return whole <= cut;
 }
+// The same for pairs of row tiles, whose parts are 256 rows.  60 nodes of 4 query heads a group, whole and cut: 8 units against
+// 560 / 1040 / 2040 keys 13.9 / 19.8 / 33.4 and 16.1 / 16.0 / 18.6 us, 32 against 1040 / 2040 20 / 35 and 23 / 28, 64 against
+// 2040 / 4160 37 / 59 and 40 / 50, 112 against 4160 60 and 72.
+bool whole_pairs(int64_t units, int64_t tiles, int64_t sms) {
+  return 5.5 + 1.5 * tiles * (double)((units + sms - 1) / sms) <= 14.5 + (double)units / sms * (1.45 * tiles + 28.0);
+}
 
 bool stride_ok(int64_t st, int64_t size, bool zero) {
   if (size <= 1) return true;
@@ -394,6 +400,7 @@ qevict_status attn_plan(const qevict_attn_desc *d, int s_prefix, AttnPlan *p, bo
     if (s_prefix) return QEVICT_EINVAL;
     p->stream = 0;
   }
+  if (paged && n_qt > 1 && total <= (1 << 30) && p->rows <= (1ll << 30)) p->stream = !whole_pairs(units, tiles, sms);
   if (paged && n_qt == 1) {   // (the stream's instances, which take a single row tile's keys two tiles at a time, for both)
     p->whole = !p->stream || whole_units(units, tiles, sms) || total > (1 << 30) || p->rows > (1ll << 30);
     p->stream = 1;
