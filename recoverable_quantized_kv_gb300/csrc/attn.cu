@@ -183,12 +183,14 @@ __global__ void __launch_bounds__(128) attn_combine_kernel(const __grid_constant
   if (lane == 0 && P.lse) P.lse[row] = l == 0.f ? -INFINITY : (mu + log2f(l)) * 0.69314718055994531f;
 }
 
-// The same for the many rows of trees and chunks over pages: a warp takes four rows of a unit, so that what their parts
-// are is worked out once and eight loads are in flight with few parts too.  Lane 4 s + r looks up part s of row r.
-template <bool FP16>
-__global__ void __launch_bounds__(128) attn_combine_rows_kernel(const __grid_constant__ AttnArgs P, int ctas) {
-  const int lane = threadIdx.x & 31, chunks = (P.part_rows + 3) / 4;
-  const uint32_t w = blockIdx.x * 4 + (threadIdx.x >> 5), unit = w / (uint32_t)chunks;   // fewer than 2^31
+// The same over pages.  WARPS warps take four rows of a unit, every warp its share of the parts: what the parts are is worked out
+// once for four rows, and eight loads are in flight with few parts too.  Lane 4 s + r looks up the s-th part of row r; of the outputs
+// lane 8 g + 2 r + x holds half x of every fourth 8 channels of row r, from the g-th on: runs of 128 bytes.
+template <bool FP16, int WARPS>
+__global__ void __launch_bounds__(WARPS == 1 ? 128 : 32 * WARPS) attn_combine_rows_kernel(const __grid_constant__ AttnArgs P, int ctas) {
+  static_assert(WARPS == 1 || WARPS >= 4, "four warps write the outputs");
+  const int lane = threadIdx.x & 31, warp = WARPS == 1 ? 0 : threadIdx.x >> 5, chunks = (P.part_rows + 3) / 4;
+  const uint32_t w = WARPS == 1 ? blockIdx.x * 4 + (threadIdx.x >> 5) : blockIdx.x, unit = w / (uint32_t)chunks;   // below 2^31
   const int r0 = (int)(w - unit * chunks) * 4, gi = (int)(unit / (uint32_t)P.h_kv), g = (int)(unit - (uint32_t)gi * P.h_kv);
   if (gi >= P.n_pr * P.batch) return attn_wait_previous();
   const AttnGroup A = attn_group(P, gi);
@@ -207,15 +209,14 @@ __global__ void __launch_bounds__(128) attn_combine_rows_kernel(const __grid_con
   const int t = A.tiles, u0 = before * P.h_kv + g * attn_places(t), c0 = u0 / share;
   const int n = t ? (u0 + t - 1) / share - c0 + 1 : 0;   // parts: the CTAs whose shares hold tiles u0 .. u0 + t - 1
   if (n == 1) return attn_wait_previous();   // the unit was not cut: its rows are written
-  const int64_t at = (int64_t)(c0 + unit) * P.part_rows + r0;
+  const int64_t at = (int64_t)(c0 + unit) * P.part_rows;
   attn_wait_previous();
-  const int r = lane & 3;
-  auto sum_of = [&](int s) {   // (m, l)
-    return s < n && r0 + r < rows ? P.part_l[at + (int64_t)s * P.part_rows + r] : make_float2(0.f, 0.f);
+  auto sum_of = [&](int s, int r) {   // (m, l)
+    return s < n && r0 + r < rows ? P.part_l[at + (int64_t)s * P.part_rows + r0 + r] : make_float2(0.f, 0.f);
   };
   float mx = -INFINITY;
   for (int s = lane >> 2; s < n; s += 8) {
-    const float2 ml = sum_of(s);
+    const float2 ml = sum_of(s, lane & 3);
     if (ml.y != 0.f) mx = fmaxf(mx, ml.x);
   }
   for (int o = 16; o >= 4; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
@@ -224,49 +225,74 @@ __global__ void __launch_bounds__(128) attn_combine_rows_kernel(const __grid_con
   float4 acc[4];
 #pragma unroll
   for (int k = 0; k < 4; ++k) acc[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int s0 = 0; s0 < n; s0 += 8) {
-    const float2 ml = sum_of(s0 + (lane >> 2));
+  const int mine = lane >> 1 & 3, row = min(r0 + mine, rows - 1), c = (lane >> 3) * 8 + (lane & 1) * 4;   // channels c + 32 k
+  const float *src = P.part_o + at * D + attn_part_at<true>(P.part_rows, row, c);
+  const int64_t step = (int64_t)P.part_rows * D;
+  for (int s0 = warp; s0 < n; s0 += 8 * WARPS) {   // of this warp: parts s0, s0 + WARPS, ...
+    const float2 ml = sum_of(s0 + (lane >> 2) * WARPS, lane & 3);
     float weight = -1.f;   // no such part, or one without keys for the row, which wrote no output
     if (ml.y != 0.f) {
       weight = ml.y * ex2(ml.x - mu);
       l += weight;
     }
 #pragma unroll 1
-    for (int s = 0; s < min(8, n - s0); s += 2) {
-      const float *src = P.part_o + (at + (int64_t)(s0 + s) * P.part_rows) * D + 4 * lane;
+    for (int j = 0; j < 8 && s0 + j * WARPS < n; j += 2) {
       float4 o[2][4];
 #pragma unroll
       for (int x = 0; x < 2; ++x)
 #pragma unroll
         for (int k = 0; k < 4; ++k)
-          if (s0 + s + x < n && r0 + k < rows)
-            o[x][k] = *reinterpret_cast<const float4 *>(src + (int64_t)x * P.part_rows * D + k * D);
+          if (s0 + (j + x) * WARPS < n)
+            o[x][k] = *reinterpret_cast<const float4 *>(src + (s0 + (j + x) * WARPS) * step + k * 32 * P.part_rows);
 #pragma unroll
-      for (int x = 0; x < 2; ++x)
+      for (int x = 0; x < 2; ++x) {
+        const float ws = __shfl_sync(0xffffffffu, weight, (j + x) * 4 + mine);
+        if (s0 + (j + x) * WARPS < n && !(ws < 0.f)) {   // a NaN weight goes on
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const float ws = __shfl_sync(0xffffffffu, weight, (s + x) * 4 + k);   // (of part 7 + 1: lane k, not used)
-          if (s0 + s + x < n && !(ws < 0.f)) {   // a NaN weight goes on
+          for (int k = 0; k < 4; ++k) {
             acc[k].x = fmaf(ws, o[x][k].x, acc[k].x);
             acc[k].y = fmaf(ws, o[x][k].y, acc[k].y);
             acc[k].z = fmaf(ws, o[x][k].z, acc[k].z);
             acc[k].w = fmaf(ws, o[x][k].w, acc[k].w);
           }
         }
+      }
     }
   }
   for (int o = 16; o >= 4; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+  if (WARPS > 1) {   // warp k < 4 finishes channels c + 32 k
+    __shared__ float4 sums[WARPS][4][32];
+    __shared__ float parts_l[WARPS][4];
 #pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    const float lk = __shfl_sync(0xffffffffu, l, k), mk = __shfl_sync(0xffffffffu, mu, k);
-    if (r0 + k >= rows) break;
-    const int token = (r0 + k) / P.G, i = first + token, h = g * P.G + (r0 + k) - token * P.G;
-    const float inv = lk == 0.f ? 0.f : 1.f / lk;
-    *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(P.out) + A.b * P.so[0] + i * P.so[1] + h * P.so[2] + 4 * lane) =
-        make_uint2(pack2<FP16>(acc[k].x * inv, acc[k].y * inv), pack2<FP16>(acc[k].z * inv, acc[k].w * inv));
-    if (lane == 0 && P.lse)
-      P.lse[((int64_t)A.b * P.s_q + i) * P.h_q + h] = lk == 0.f ? -INFINITY : (mk + log2f(lk)) * 0.69314718055994531f;
+    for (int k = 0; k < 4; ++k) sums[warp][k][lane] = acc[k];
+    if (lane < 4) parts_l[warp][lane] = l;
+    __syncthreads();
+    if (warp >= 4) return;
+    l = 0.f;
+    acc[0] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int v = 0; v < WARPS; ++v) {
+      if (v < n) {
+        const float4 o = sums[v][warp][lane];
+        l += parts_l[v][lane & 3];
+        acc[0].x += o.x;
+        acc[0].y += o.y;
+        acc[0].z += o.z;
+        acc[0].w += o.w;
+      }
+    }
   }
+  const float lk = __shfl_sync(0xffffffffu, l, mine), mk = __shfl_sync(0xffffffffu, mu, mine);
+  if (r0 + mine >= rows) return;
+  const int token = (r0 + mine) / P.G, i = first + token, h = g * P.G + (r0 + mine) - token * P.G;
+  const float inv = lk == 0.f ? 0.f : 1.f / lk;
+  uint16_t *dst = static_cast<uint16_t *>(P.out) + A.b * P.so[0] + i * P.so[1] + h * P.so[2] + c + 32 * warp;
+#pragma unroll
+  for (int k = 0; k < (WARPS == 1 ? 4 : 1); ++k)
+    *reinterpret_cast<uint2 *>(dst + 32 * k) =
+        make_uint2(pack2<FP16>(acc[k].x * inv, acc[k].y * inv), pack2<FP16>(acc[k].z * inv, acc[k].w * inv));
+  if (warp == 0 && (lane & ~6) == 0 && P.lse)
+    P.lse[((int64_t)A.b * P.s_q + i) * P.h_q + h] = lk == 0.f ? -INFINITY : (mk + log2f(lk)) * 0.69314718055994531f;
 }
 
 namespace {
@@ -322,9 +348,15 @@ constexpr int WHOLE_TILES = 8;
 // is 2^-16 of a weight at 64.
 constexpr float WIDE_CAP = 64.f;
 
-// Rows of trees over pages from which a warp merges four of them: 64 nodes of 1 / 2 / 3 sequences of 32 heads against 8K keys
-// take 29 / 33 / 44 us with a warp a row, 35 / 38 / 43 with four rows, 26 nodes of 16 against 33K 237 and 230.
-constexpr int MANY_ROWS = 6144;
+// Warps that merge four rows over pages: one where there are rows enough for all SMs, else more, the fewer the rows and the
+// more the parts of a unit.  With 1 / 4 / 8 / 16: 64 rows of 5 parts 11.3 / 10.4 / 10.6 / 10.9 us with the attention, of 76 parts (32
+// nodes against 60K keys) - / 34 / 29 / 27, 512 rows of 17 parts 19.6 / 16.4 / 15.1 / 14.2, 1024 of 17 - / 16.9 / 15.7 / 18.4, 4096
+// rows 27.4 / 23.9 / - / -, 8192 of 5 31.6 / 32 / - / -, 13312 of 2 222 / 228 / - / -.
+int merge_warps(const AttnPlan &p, const qevict_attn_desc *d) {
+  const int64_t units = (int64_t)p.n_pr * d->batch * d->h_kv, tiles = (d->s_kv + AT_TILE - 1) / AT_TILE;
+  const int64_t parts = std::min(p.grid / units, tiles / MIN_TILES) + 1;   // of a unit, if all are alike
+  return p.rows > 6144 ? 1 : parts <= 8 || p.rows > 1024 ? 4 : p.rows > 512 ? 8 : 16;
+}
 
 // Units of one row tile over pages, `tiles` key tiles at most: drawn whole by the CTAs, in one launch, or cut into shares and
 // merged?  Both are estimated in us.  Whole: a round of units on all SMs takes 1.45 a tile and 1 more, the last one on some of
@@ -542,16 +574,21 @@ qevict_status attn_launch(const qevict_attn_desc *d, const AttnPlan &pl, const q
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
-    const bool few = pl.rows <= 1024, many = pg && pl.rows > MANY_ROWS;
+    const bool few = pl.rows <= 1024;
+    const int warps = merge_warps(pl, d);   // over pages
     const int64_t fours = ((int64_t)pl.part_rows + 3) / 4 * pl.n_pr * d->batch * d->h_kv;
-    cfg.gridDim = dim3((unsigned)(few ? pl.rows : many ? (fours + 3) / 4 : (pl.rows + 3) / 4));
-    cfg.blockDim = dim3(128);
+    cfg.gridDim = dim3((unsigned)(pg ? (warps > 1 ? fours : (fours + 3) / 4) : few ? pl.rows : (pl.rows + 3) / 4));
+    cfg.blockDim = dim3(pg && warps > 4 ? 32 * warps : 128);
     cfg.stream = s;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    const auto combine = few ? (fp16 ? attn_combine_kernel<true, 4> : attn_combine_kernel<false, 4>)
-                      : many ? (fp16 ? attn_combine_rows_kernel<true> : attn_combine_rows_kernel<false>)
-                             : (fp16 ? attn_combine_kernel<true, 1> : attn_combine_kernel<false, 1>);
+    const auto combine =
+        !pg ? (few ? (fp16 ? attn_combine_kernel<true, 4> : attn_combine_kernel<false, 4>)
+                   : (fp16 ? attn_combine_kernel<true, 1> : attn_combine_kernel<false, 1>))
+        : warps == 16 ? (fp16 ? attn_combine_rows_kernel<true, 16> : attn_combine_rows_kernel<false, 16>)
+        : warps == 8  ? (fp16 ? attn_combine_rows_kernel<true, 8> : attn_combine_rows_kernel<false, 8>)
+        : warps == 4  ? (fp16 ? attn_combine_rows_kernel<true, 4> : attn_combine_rows_kernel<false, 4>)
+                      : (fp16 ? attn_combine_rows_kernel<true, 1> : attn_combine_rows_kernel<false, 1>);
     if (cudaLaunchKernelEx(&cfg, combine, A, pl.grid) != cudaSuccess) return QEVICT_ECUDA;
   }
   return QEVICT_OK;

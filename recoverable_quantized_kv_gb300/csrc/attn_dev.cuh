@@ -207,6 +207,13 @@ __device__ __forceinline__ bool attn_row(const AttnArgs &P, const AttnItem &I, i
   return R.tok < P.tpt && i < I.ql;
 }
 
+// Place of channel c (a multiple of 4) of a row of a part, counted from the part's first element.  Over pages the rows of 8
+// channels follow one another, so that a warp's rows are written as one run of 1 KB, and not 32 pieces of 32 bytes.
+template <bool PAGED>
+__host__ __device__ __forceinline__ int attn_part_at(int rows, int row, int c) {
+  return PAGED ? ((c >> 3) * rows + row) * 8 + (c & 7) : row * D + c;
+}
+
 // Position of query i of sequence b behind the prefix.
 __device__ __forceinline__ int attn_prefix_pos(const AttnArgs &P, int b, int i) {
   return P.pre + ((P.kv_len ? clampi(P.kv_len[b], 0, P.s_kv) : P.s_kv) - P.s_q + i);
@@ -1413,10 +1420,10 @@ __global__ void __launch_bounds__(attn_threads(PAGED), 1) attn_kernel(const __gr
             for (int q = 0; q < 2; ++q) {
               uint32_t o[16];
               take(q, o);
-              float *dst = part_o + (part_row + prow) * D + AT_COLS * quarter + 16 * q;
+              float *dst = part_o + part_row * D + attn_part_at<PAGED>(P.part_rows, prow, AT_COLS * quarter + 16 * q);
               if (valid && lt != 0.f) {
                 st_global_v8(dst, o);
-                st_global_v8(dst + 8, o + 8);
+                st_global_v8(dst + (PAGED ? 8 * P.part_rows : 8), o + 8);
               }
             }
           } else {
@@ -1440,7 +1447,8 @@ __global__ void __launch_bounds__(attn_threads(PAGED), 1) attn_kernel(const __gr
             const float o2 = rl == 0.f ? 0.f : acc[2] * ri_l, o3 = rl == 0.f ? 0.f : acc[3] * ri_l;
             if (parts) {
               if (lane == 0) part_l[part_row + rp] = make_float2(rm, rl);
-              *reinterpret_cast<float4 *>(part_o + (part_row + rp) * D + 4 * lane) = make_float4(o0, o1, o2, o3);
+              *reinterpret_cast<float4 *>(part_o + part_row * D + attn_part_at<PAGED>(P.part_rows, rp, 4 * lane)) =
+                  make_float4(o0, o1, o2, o3);
             } else {
               if (lane == 0 && P.lse)
                 P.lse[((int64_t)rb * P.s_q + ri) * P.h_q + rh] =
