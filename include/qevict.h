@@ -515,7 +515,7 @@ qevict_status qevict_prefix_attn(const qevict_prefix_attn_desc *desc, const floa
  * pool it is a snapshot.  Its arrays, in int32 elements from its start (qevict_pages_get_layout): the status word
  * (qevict_ops_status), the number of free pages, length [batch], held [batch], table [batch][max_pages], refs [pages], one bit per
  * free page.  They may be read any time behind the calls in the stream; of them length alone may be written, to a value within
- * the pages held (an undo of tokens, say).
+ * the pages held (an undo of the last tokens, say; qevict_pages_trim goes back into pages that other sequences hold).
  * The calls of one cache run one after the other (one stream, or ordered by events).  Nothing is synchronised.
  * Faults set bits of the status word: 2 too few free pages, 4 a table that cannot be (qevict_pages_load), 8 an argument or index
  * out of range.  A sequence that sets bit 8 is left as it was, unless stated; the others are served. */
@@ -581,7 +581,9 @@ qevict_status qevict_pages_compact(const qevict_pages_desc *desc, void *k, void 
  *   without parents: new tokens j < i; its position is length[b] + i;
  *   with parents: its ancestors; parents[i] < i is the node that it follows, -1 the last of the length[b] tokens; its
  *     position is length[b] + the number of its ancestors.
- * Scores, out and lse as for qevict_attn with causal = 1; the bias goes by these positions.  s_q up to 64 with parents. */
+ * Scores, out and lse as for qevict_attn with causal = 1; the bias goes by these positions.  s_q up to 64 with parents.
+ * How the work is divided goes by max_pages, as lengths are on the device: a table with room for far more than the sequences
+ * hold costs short ones time. */
 typedef struct {
   int32_t dtype;                           /* QEVICT_BF16 or QEVICT_FP16 */
   int32_t batch, s_q, h_q, h_kv, d_head;   /* as for qevict_attn */

@@ -589,9 +589,12 @@ __device__ __forceinline__ void attn_exact_rows(const AttnArgs &P, const AttnIte
 // Every wait is bounded; the TMEM columns are released on every path.
 // STREAM = false: whole units, always as pairs (of a last odd row tile the second is empty).  CAP: 0 none, 1 up to 64, 2 wider
 // (instances of their own: its code in the others costs capped prompts 2%).
-// PAGED: keys and values in pages of 16 to 128 tokens, a copy a page and half instead of one a tile and half, the page numbers
-// held 64 a time in the copying warp's registers, the next 32 on their way while the last are used.  A row of a tree of drafts
-// sees the keys before the tree and a line of up to 64 nodes, found by a walk while the first keys are on their way.
+// PAGED: keys and values in pages of 16 to 128 tokens, a copy a page and half instead of one a tile and half.  A copy takes the
+// warp that asks for it about 70 cycles, so keys and values have a warp each (16 tokens of 32 heads against 33K keys in pages of
+// 16: 220 us, with one warp 230).  They hold 64 page numbers of a sequence in their registers, the next 32 on their way while the
+// last are used.  Either meets its tiles of the ring only; it has filled one at most three places ago, for which the tile eight
+// places ago was consumed, so a phase parity is enough for it.  A row of a tree of drafts sees the keys before the tree and a
+// line of up to 64 nodes, found by a walk while the first keys are on their way.
 template <bool FP16, int CAP, bool BIAS, bool STREAM, bool PAGED = false>
 __global__ void __launch_bounds__(attn_threads(PAGED), 1) attn_kernel(const __grid_constant__ AttnArgs P) {
   extern __shared__ __align__(1024) uint8_t sm[];   // swizzle atoms: 1024-aligned

@@ -164,6 +164,39 @@ def test_many_sequences_of_all_lengths(lib):
     run_case(length[:40], 13, 16, 8, 64, FP, parents=[tree(13, b) for b in range(40)])
 
 
+def test_more_units_than_sms_drawn_again_and_again(lib):
+    """240 units of all lengths drawn one by one, sequences without queries or tokens among them; the count starts again for the
+    next call, and for replays of a captured one."""
+    g = torch.Generator().manual_seed(7)
+    length = [int(x) for x in torch.randint(0, 901, (60,), generator=g)]
+    ql = [int(x) for x in torch.randint(0, 6, (60,), generator=g)]
+    length[0], length[50], ql[3], ql[59] = 0, 900, 0, 0
+    plan, (q, k, v, table, out, lse) = run_case(length, 5, 4, 4, 32, q_len=ql, parents=[tree(5, b) for b in range(60)])
+    args, kw = (q, k, v, table, i32(length)), dict(parents=i32([tree(5, b) for b in range(60)]), q_len=i32(ql))
+    o, s = torch.full_like(out, 7.0), torch.full_like(lse, 7.0)
+    for _ in range(3):
+        plan.run(*args, out=o, lse=s, **kw)
+        assert torch.equal(o, out) and torch.equal(s, lse)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        for _ in range(2):
+            plan.run(*args, out=o, lse=s, **kw)
+    for _ in range(3):
+        o.fill_(7.0)
+        graph.replay()
+        assert torch.equal(o, out) and torch.equal(s, lse)
+    plan.check()
+
+
+@pytest.mark.parametrize("b,nodes,n,hq,hkv", [(1, 16, 4200, 32, 8), (1, 32, 4200, 32, 8), (1, 1, 20000, 4, 1), (2, 60, 2000, 32, 8),
+                                              (13, 64, 3000, 8, 2), (1, 3, 33000, 6, 2)])
+def test_parts_merged_by_one_to_sixteen_warps(lib, b, nodes, n, hq, hkv):
+    """Few rows of many parts to many rows of few, counts of rows that are no multiple of four, one row without parts."""
+    run_case([n - 77 * i for i in range(b)], nodes, hq, hkv, 64, parents=[tree(nodes, 20 + i) for i in range(b)])
+    if b > 1:
+        run_case([n] + [5] * (b - 1), nodes, hq, hkv, 16, FP, q_len=[nodes] + [max(1, nodes - 7 * i) for i in range(1, b)])
+
+
 @pytest.mark.parametrize("n,nodes,hkv,page", [(40000, 26, 2, 16), (131000, 1, 1, 16), (70000, 64, 1, 128)])
 def test_long_contexts(lib, n, nodes, hkv, page):
     """Units cut into parts, tables longer than the copying warp holds, trees cut by a tile's end."""
