@@ -549,7 +549,8 @@ qevict_status qevict_pages_reserve(const qevict_pages_desc *desc, void *k, void 
                                    int32_t n_new, qevict_stream_t stream);
 /* Writes rows length[b] + i, i < n[b], of layers [layer, layer + layers) from k_new, v_new
  * [layers][batch][n][h_kv][128]; n[b] = d_n[b] (at most n), or n where d_n is NULL.  Lengths stay: the rows count once
- * qevict_pages_accept takes them.  Rows whose page is missing or shared are not written (bit 8). */
+ * qevict_pages_accept takes them.  Rows whose page is missing or shared are not written (bit 8).  k_new and v_new share no
+ * bytes with the pool. */
 typedef struct {
   int32_t layer, layers, n, reserved0;   /* layers 1.., n 1.., reserved0 0 */
   int64_t k[4], v[4];                    /* strides {layer, sequence, token, head}: multiples of 8, 0 allowed */
