@@ -267,7 +267,7 @@ __global__ void __launch_bounds__(256) pages_accept_kernel(const __grid_constant
     ok = ok && is_page(P, src) && is_page(P, dst);
     moves = ok && at != j;
     if (ok) ok = P.refs[dst] == 1;   // rows of shared pages are never written
-  } else if (fits && !d_path) {
+  } else if (fits && !d_path && count > 0) {   // (no row: the last page may stay another's too)
     for (int c = (len >> P.lg) + j; (int64_t)c << P.lg < (int64_t)len + count; c += blockDim.x)
       if (!is_page(P, row[c]) || P.refs[row[c]] != 1) ok = false;
   }
