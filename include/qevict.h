@@ -515,7 +515,7 @@ qevict_status qevict_prefix_attn(const qevict_prefix_attn_desc *desc, const floa
  * pool it is a snapshot.  Its arrays, in int32 elements from its start (qevict_pages_get_layout): the status word
  * (qevict_ops_status), the number of free pages, length [batch], held [batch], table [batch][max_pages], refs [pages], one bit per
  * free page.  They may be read any time behind the calls in the stream; of them length alone may be written, to a value within
- * the pages held (an undo of the last tokens, say; qevict_pages_trim goes back into pages that other sequences hold).
+ * the pages held (an undo of the last tokens, say, which keeps the pages behind them; qevict_pages_trim gives them back).
  * The calls of one cache run one after the other (one stream, or ordered by events).  Nothing is synchronised.
  * Faults set bits of the status word: 2 too few free pages, 4 a table that cannot be (qevict_pages_load), 8 an argument or index
  * out of range.  A sequence that sets bit 8 is left as it was, unless stated; the others are served. */
@@ -542,9 +542,11 @@ qevict_status qevict_pages_load(const qevict_pages_desc *desc, void *d_state, co
 /* Makes rows length[b] .. length[b] + new - 1 of every sequence writable; new = d_new[b], or n_new where d_new is NULL.
  * Missing pages are taken from the free ones, the lowest number first, sequence after sequence.  Where the row of the
  * next token stands in a page that other sequences hold too, the sequence gets a page of its own with a copy of its rows
- * (all layers); of several sequences that hold it and reserve in one call, the first keeps it if no other holds it.  A
- * sequence with new = 0 is left as it is.  If the free pages do not suffice (bit 2), or a sequence would pass max_pages
- * (bit 8, also for new < 0), nothing changes for any sequence. */
+ * (all layers); of several sequences that hold it and reserve in one call, the first keeps it if no other holds it.  Held pages
+ * without tokens of the sequence (after qevict_pages_load, or a length written back) from the first one on that the rows reach and
+ * other sequences hold too are given back, and free ones taken for them.  A sequence with new = 0 is left as it is.  If the
+ * pages that are free before the call do not suffice (bit 2), or a sequence would pass max_pages (bit 8, also for new < 0),
+ * nothing changes for any sequence. */
 qevict_status qevict_pages_reserve(const qevict_pages_desc *desc, void *k, void *v, void *d_state, const int32_t *d_new,
                                    int32_t n_new, qevict_stream_t stream);
 /* Writes rows length[b] + i, i < n[b], of layers [layer, layer + layers) from k_new, v_new

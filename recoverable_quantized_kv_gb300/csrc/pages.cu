@@ -329,10 +329,14 @@ __global__ void __launch_bounds__(256) pages_accept_kernel(const __grid_constant
 
 // Who needs which pages, a thread a sequence; then the free bits are walked from the lowest page on, a word a thread, and
 // the r-th free page goes to whom the running sum of needs says, a thread a page: it finds word and sequence by their sums.
-// Nothing is written before the pages are known to suffice.  Bound by latency: lengths, table, counts in a chain of
+// Nothing is written before the pages are known to suffice.  Held pages behind a sequence's tokens that the rows reach and that
+// stand in other sequences too (a loaded table, a length written back) are given back first: each thread looks at the first
+// OWN pages from its sequence's last token on, the CTA at the others (16 sequences that hold 8 pages in advance 4 us, 1100
+// pages 11.5).  Bound by latency: lengths, table, counts in a chain of
 // loads, then a few barriers for every 32768 pages: 2.5 us with the copying kernel where nothing is needed, 5 for 16
 // sequences of 33K tokens that grow.  (A thread that hands out all pages of its 128 bits took 30 us for 64 samples of 4 prompts.)
-__global__ void __launch_bounds__(1024) pages_reserve_kernel(const __grid_constant__ PagesDev P, const int *d_new, int n_new) {
+constexpr int OWN = 3;   // a step of a few rows reaches no more
+__global__ void __launch_bounds__(1024, 1) pages_reserve_kernel(const __grid_constant__ PagesDev P, const int *d_new, int n_new) {
   __shared__ int s_tail[PG_BATCH], s_start[PG_BATCH], s_len[PG_BATCH], s_held[PG_BATCH], s_copy[PG_BATCH], s_rank[1024];
   __shared__ uint32_t s_word[1024];
   __shared__ int2 s_warp[32];
@@ -340,29 +344,73 @@ __global__ void __launch_bounds__(1024) pages_reserve_kernel(const __grid_consta
   const int t = threadIdx.x;
   uint32_t word = t < P.words ? P.bits[t] : 0u;
   const int n_free = *P.n_free;
-  int len = 0, held = 0, add = 0, tail = -1, refs = 0;
+  int len = 0, held = 0, keep = 0, want = 0, tail = -1, refs = 0;   // keep: held pages that it goes on with
+  int lo = 0, hi = 0;   // those that the CTA looks at
   bool bad = false;
   if (t < P.batch) {
-    held = held_of(P, t);
+    held = keep = held_of(P, t);
     len = length_of(P, t, held);
-    const int64_t n = d_new ? d_new[t] : n_new, want = (len + n + P.page - 1) >> P.lg;
-    bad = n < 0 || want > P.max_pages;
+    const int64_t n = d_new ? d_new[t] : n_new, up = (len + n + P.page - 1) >> P.lg;
+    bad = n < 0 || up > P.max_pages;
     if (!bad && n > 0) {
-      add = max((int)want - held, 0);
-      if (len & (P.page - 1)) {
-        tail = row_of(P, t)[len >> P.lg];
-        bad = !is_page(P, tail);
-        if (!bad) refs = P.refs[tail];
-      }
+      want = (int)up;
+      const int *row = row_of(P, t), c0 = len >> P.lg, reach = min(want, held);
+      const bool part = len & (P.page - 1);   // page c0 holds tokens
+      int entry[OWN], holders[OWN];
+#pragma unroll
+      for (int i = 0; i < OWN; ++i) entry[i] = c0 + i < reach ? row[c0 + i] : -1;
+#pragma unroll
+      for (int i = 0; i < OWN; ++i) holders[i] = is_page(P, entry[i]) ? P.refs[entry[i]] : 0;
+      if (part) tail = entry[0], refs = holders[0], bad = !is_page(P, tail);
+#pragma unroll
+      for (int i = OWN - 1; i >= 0; --i)
+        if (holders[i] > 1 && (i > 0 || !part)) keep = c0 + i;
+      if (keep == held) lo = c0 + OWN, hi = reach;
     }
-    s_len[t] = len, s_held[t] = held;
+    s_len[t] = len, s_held[t] = keep;
   }
   s_tail[t] = tail;
   if (t == 0) *P.n_copies = 0, *P.drawn = 0;
-  if (__syncthreads_or(bad)) {
+  bool rare = __syncthreads_or(bad || lo < hi || keep < held);   // one barrier for a step without any of them
+  if (rare && __syncthreads_or(bad)) {
     if (t == 0) atomicOr(P.status, QV_ERR_BOUNDS);
     return;
   }
+  auto owner = [&](int r) {   // the last sequence that starts at r or before: it has some
+    int a = 0, z = P.batch - 1;
+    while (a < z) {
+      const int mid = (a + z + 1) >> 1;
+      if (s_start[mid] <= r)
+        a = mid;
+      else
+        z = mid - 1;
+    }
+    return a;
+  };
+  if (rare && __syncthreads_or(lo < hi)) {
+    const Sums at = scan_1024(max(hi - lo, 0), 0, s_warp);
+    if (t < P.batch) s_start[t] = at.x, s_copy[t] = lo;
+    __syncthreads();
+    for (int r = t; r < at.all_x; r += 4 * 1024) {
+      int b[4], c[4], p[4], n[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        p[i] = -1;
+        if (r + i * 1024 >= at.all_x) continue;
+        b[i] = owner(r + i * 1024), c[i] = s_copy[b[i]] + r + i * 1024 - s_start[b[i]];
+        p[i] = row_of(P, b[i])[c[i]];
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) n[i] = is_page(P, p[i]) ? P.refs[p[i]] : 0;
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (n[i] > 1) atomicMin(&s_held[b[i]], c[i]);
+    }
+    __syncthreads();
+    if (t < P.batch) keep = s_held[t];
+  }
+  if (rare) rare = __syncthreads_or(keep < held);   // some give pages back
+  const int add = max(want - keep, 0);
   bool copy = false;
   // Shared pages: how many that reserve now hold each, and is this the first of them.  A look at every other sequence costs
   // 8 of them 0.6 us less than counts in memory, 256 the same, 1024 30 us more.
@@ -395,30 +443,40 @@ __global__ void __launch_bounds__(1024) pages_reserve_kernel(const __grid_consta
   }
   if (total == 0) return;
   if (t < P.batch) s_start[t] = need.x, s_copy[t] = copy ? need.y : -1;
-  if (t == 0) *P.n_copies = need.all_y;
-  auto assign = [&](int r, int id) {
-    int lo = 0, hi = P.batch - 1;   // the last sequence that starts at r or before: it needs pages
-    while (lo < hi) {
-      const int mid = (lo + hi + 1) >> 1;
-      if (s_start[mid] <= r)
-        lo = mid;
-      else
-        hi = mid - 1;
+  if (t == 0) {
+    *P.n_copies = need.all_y;
+    *P.n_free = n_free - total;
+  }
+  if (rare) {
+    __syncthreads();   // the count is written
+    int free = 0;
+    if (keep < held) {
+      int *row = row_of(P, t);
+      for (int c = keep; c < held; ++c) {
+        const int p = row[c];
+        row[c] = -1;
+        if (is_page(P, p)) free += give_back(P, p);
+      }
     }
-    const int k = r - s_start[lo], l = s_len[lo];
-    int *row = row_of(P, lo);
-    if (s_copy[lo] >= 0 && k == 0) {
-      P.copies[s_copy[lo]] = make_int4(s_tail[lo], id, l & (P.page - 1), 0);
+    if (free) atomicAdd(P.n_free, free);
+    __syncthreads();
+    word = t < P.words ? __ldcg(&P.bits[t]) : 0u;   // (not the line that this SM has read before)
+  }
+  auto assign = [&](int r, int id) {
+    const int b = owner(r), k = r - s_start[b], l = s_len[b];
+    int *row = row_of(P, b);
+    if (s_copy[b] >= 0 && k == 0) {
+      P.copies[s_copy[b]] = make_int4(s_tail[b], id, l & (P.page - 1), 0);
       row[l >> P.lg] = id;
     } else {
-      row[s_held[lo] + k - (s_copy[lo] >= 0)] = id;
+      row[s_held[b] + k - (s_copy[b] >= 0)] = id;
     }
     P.refs[id] = 1;
   };
   int found = 0;
   for (int base = 0; base < P.words && found < total; base += 1024) {
     const int w = base + t;
-    if (base) word = w < P.words ? P.bits[w] : 0u;
+    if (base) word = w < P.words ? __ldcg(&P.bits[w]) : 0u;
     const int here = __popc(word);
     const Sums at = scan_1024(here, 0, s_warp);   // (its barriers also part this round's lists from the last one's readers)
     s_rank[t] = at.x, s_word[t] = word;
@@ -446,14 +504,15 @@ __global__ void __launch_bounds__(1024) pages_reserve_kernel(const __grid_consta
     }
     found += at.all_x;
   }
-  if (copy) atomicSub(&P.refs[tail], 1);
-  if (add) P.held[t] = held + add;
-  if (t == 0) {
-    *P.n_free = n_free - total;
-    if (found < total) {   // the count and the bits disagree: not every copy has a page
-      *P.n_copies = 0;
-      atomicOr(P.status, QV_ERR_STATE);
-    }
+  if (!rare) {
+    if (copy) atomicSub(&P.refs[tail], 1);
+  } else if (copy && give_back(P, tail)) {   // its other holders gave the page back in this call (all words are written)
+    atomicAdd(P.n_free, 1);
+  }
+  if (add) P.held[t] = keep + add;
+  if (t == 0 && found < total) {   // the count and the bits disagree: not every copy has a page
+    *P.n_copies = 0;
+    atomicOr(P.status, QV_ERR_STATE);
   }
 }
 
