@@ -562,8 +562,8 @@ qevict_status qevict_pages_append(const qevict_pages_desc *desc, const qevict_pa
                                   qevict_stream_t stream);
 /* The first d_count[b] rows behind every sequence's length become part of it; with d_path [batch][max_path], row
  * length[b] + path[b][j] moves to length[b] + j first, in all layers (the accepted nodes of a tree of drafts:
- * strictly ascending).  0 <= count[b], with a path at most max_path (1..256).  count[b] = 0 leaves the sequence as it is,
- * whoever holds its pages. */
+ * strictly ascending).  0 <= count[b], with a path at most max_path (1..256; 0 without one).  count[b] = 0 leaves the
+ * sequence as it is, whoever holds its pages. */
 qevict_status qevict_pages_accept(const qevict_pages_desc *desc, void *k, void *v, void *d_state, const int32_t *d_count,
                                   const int32_t *d_path, int32_t max_path, qevict_stream_t stream);
 /* All at once, sequence b becomes what sequence d_src[b] was: it holds the same pages, as far as they hold tokens, and the

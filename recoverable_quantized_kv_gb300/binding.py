@@ -925,11 +925,12 @@ class PagedCache:
         return self._rows[key]
 
     def accept(self, count, path=None, stream=None):
-        """The first count[b] rows behind each length count from now on; with path int32 [batch][max_path], rows path[b][j]
-        (strictly ascending) move there first."""
+        """The first count[b] rows behind each length count from now on; with path int32 [batch][max_path], max_path 1 to 256,
+        rows path[b][j] (strictly ascending) move there first."""
         where, most = "PagedCache.accept", 0
         if path is not None:
-            _need(path.dim() == 2, where, "path must be [batch][max_path]")
+            _need(path.dim() == 2 and 1 <= path.shape[1] <= 256, where,   # (one of no columns has no address: it would be none)
+                  f"path must be [batch][1 to 256], has shape {tuple(path.shape)}")
             most = path.shape[1]
             path_at = self._ints(where, "path", path, (self.batch, most))
         self._run("qevict_pages_accept", stream, (count, path), *self._pool, self._state,

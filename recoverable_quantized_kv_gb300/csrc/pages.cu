@@ -853,7 +853,8 @@ qevict_status qevict_pages_accept(const qevict_pages_desc *desc, void *k, void *
   qv::PagesDev P;
   const qevict_status st = qv::pages_args(desc, true, k, v, d_state, &p, &P);
   if (st != QEVICT_OK) return st;
-  if (!qv::word_ok(d_count, true) || !qv::word_ok(d_path, false) || (d_path && (max_path < 1 || max_path > qv::PG_PATH)))
+  if (!qv::word_ok(d_count, true) || !qv::word_ok(d_path, false) ||
+      (d_path ? max_path < 1 || max_path > qv::PG_PATH : max_path != 0))
     return QEVICT_EINVAL;
   // CTAs for every 256 columns of 16 bytes, or four on each of 152 SMs over all sequences: the table and path are looked
   // up once a CTA
