@@ -451,8 +451,8 @@ def _tensor(t, where, name, shape, dtype, device, dense=False):
 
 def _enter(device_index, stream, tensors, home=None, own=()):
     """The raw stream of a call on a device, and the device to make current for it (None: it is).  Tensors used on
-    another stream than the device's current one are made known to the allocator, and so are the operator's `own`, which
-    its caller does not see, on any stream but the one they were made on, `home`."""
+    another stream than the device's current one are made known to the allocator (so they are checked before), and so are
+    the operator's `own`, which its caller does not see, on any stream but the one they were made on, `home`."""
     torch = _torch_module or _torch()
     other = None if torch._C._cuda_getDevice() == device_index else torch.device("cuda", device_index)
     if stream is None:
@@ -796,11 +796,11 @@ class PrefixAttention(_AttnPlan):
         if not (_fits(k_prefix, self.prefix_shape, self.dtype, i) and _fits(v_prefix, self.prefix_shape, self.dtype, i)):
             for name, t in (("k_prefix", k_prefix), ("v_prefix", v_prefix)):
                 _tensor(t, where, name, self.prefix_shape, self.dtype, self.device)
+        args = (desc, _array(where, "slopes", slopes, (d.h_q,), _torch().float32, i),
+                _array(where, "kv_len", kv_len, self.q_shape[:1], _torch().int32, i), q.data_ptr(), k_prefix.data_ptr(),
+                v_prefix.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), lse.data_ptr(), *self._work)
         s, other = _enter(i, stream, (q, k_prefix, v_prefix, k, v, out, lse, slopes, kv_len), self._home, self._own)
-        _call("qevict_prefix_attn", other,
-              (desc, _array(where, "slopes", slopes, (d.h_q,), _torch().float32, i),
-               _array(where, "kv_len", kv_len, self.q_shape[:1], _torch().int32, i), q.data_ptr(), k_prefix.data_ptr(),
-               v_prefix.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), lse.data_ptr(), *self._work, s))
+        _call("qevict_prefix_attn", other, (*args, s))
         return out, lse
 
     def _with_strides(self, key):
@@ -994,10 +994,10 @@ class PagedAttention(_AttnPlan):
             mask.parents = _array(where, "parents", parents, self._tree if one else self._trees, i32, i)
             mask.one_tree = one
             mask = self._mask_ref
+        args = (desc, mask, q.data_ptr(), k.data_ptr(), v.data_ptr(), _array(where, "table", table, self.table_shape, i32, i),
+                _array(where, "length", length, self._seqs, i32, i), out.data_ptr(), lse.data_ptr(), *self._work)
         s, other = _enter(i, stream, (q, k, v, table, length, out, lse, parents, q_len, slopes), self._home, self._own)
-        _call("qevict_paged_attn", other,
-              (desc, mask, q.data_ptr(), k.data_ptr(), v.data_ptr(), _array(where, "table", table, self.table_shape, i32, i),
-               _array(where, "length", length, self._seqs, i32, i), out.data_ptr(), lse.data_ptr(), *self._work, s))
+        _call("qevict_paged_attn", other, (*args, s))
         return out, lse
 
     def _with_strides(self, key):
