@@ -317,17 +317,12 @@ int sm_count() {   // of the current device
 // `bt` tokens x `bb` sequences, 128-byte swizzled.  batch: 1 when the batch stride is 0.
 bool dense_map(CUtensorMap *map, bool fp16, const void *base, int64_t heads, int64_t tokens, int64_t batch, int64_t st_h,
                int64_t st_t, int64_t st_b, int bh, int bt, int bb) {
-  PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
-  if (!enc) return false;
   const cuuint64_t dims[4] = {(cuuint64_t)D, (cuuint64_t)heads, (cuuint64_t)tokens, (cuuint64_t)batch};
   // a dimension of one element has no step: any valid one will do
   const cuuint64_t strides[3] = {(cuuint64_t)(heads > 1 ? st_h : D) * 2, (cuuint64_t)(tokens > 1 ? st_t : D) * 2,
                                  (cuuint64_t)(batch > 1 ? st_b : D) * 2};
   const cuuint32_t box[4] = {64, (cuuint32_t)bh, (cuuint32_t)bt, (cuuint32_t)bb};
-  const cuuint32_t estr[4] = {1, 1, 1, 1};
-  return enc(map, fp16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void *>(base),
-             dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+  return tensor_map_4d(map, fp16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, base, dims, strides, box);
 }
 
 struct AttnPlan {

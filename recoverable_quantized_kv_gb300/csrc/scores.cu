@@ -285,15 +285,10 @@ __global__ void window_sum_kernel(const CacheDev C, float *s0) {
 namespace {
 // [B][P][heads][128] bf16 as a 4-D tensor map; a box is 64 dims x 1 head x 128 rows, 128-byte swizzled
 bool prompt_map(CUtensorMap *map, const __nv_bfloat16 *base, int B, int P, int heads) {
-  PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
-  if (!enc) return false;
   const cuuint64_t dims[4] = {(cuuint64_t)D, (cuuint64_t)heads, (cuuint64_t)P, (cuuint64_t)B};
   const cuuint64_t strides[3] = {(cuuint64_t)D * 2, (cuuint64_t)heads * D * 2, (cuuint64_t)P * heads * D * 2};
   const cuuint32_t box[4] = {64, 1, (cuuint32_t)TC_ROWS, 1};
-  const cuuint32_t estr[4] = {1, 1, 1, 1};
-  return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<__nv_bfloat16 *>(base), dims, strides, box, estr,
-             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+  return tensor_map_4d(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, base, dims, strides, box);
 }
 }  // namespace
 
