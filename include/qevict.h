@@ -481,7 +481,8 @@ typedef struct {
 /* Bytes of device workspace of a call (a bound for every mask).  The workspace is 256-byte aligned; its first 256 bytes
  * hold the status word and a count, and must be cleared once before its first use, and again after a wait ran
  * out (bit 1 of the status word).  Calls that may overlap on the GPU (two streams, two replayed graphs) need
- * workspaces of their own. */
+ * workspaces of their own.  A call enqueues up to three kernels that belong together: host threads that share a
+ * workspace on one stream take turns, a call at a time. */
 qevict_status qevict_attn_bytes(const qevict_attn_desc *desc, size_t *bytes);
 /* q [batch][s_q][h_q][128], k, v [batch][s_kv][h_kv][128], out like q (16-byte aligned); lse fp32
  * [batch][s_q][h_q] or NULL. */
@@ -516,7 +517,8 @@ qevict_status qevict_prefix_attn(const qevict_prefix_attn_desc *desc, const floa
  * (qevict_ops_status), the number of free pages, length [batch], held [batch], table [batch][max_pages], refs [pages], one bit per
  * free page.  They may be read any time behind the calls in the stream; of them length alone may be written, to a value within
  * the pages held (an undo of the last tokens, say, which keeps the pages behind them; qevict_pages_trim gives them back).
- * The calls of one cache run one after the other (one stream, or ordered by events).  Nothing is synchronised.
+ * The calls of one cache run one after the other (one stream, or ordered by events; host threads that share it take turns, a
+ * call at a time, since a call enqueues up to three kernels that belong together).  Nothing is synchronised.
  * Faults set bits of the status word: 2 too few free pages, 4 a table that cannot be (qevict_pages_load), 8 an argument or index
  * out of range.  A sequence that sets bit 8 is left as it was, unless stated; the others are served. */
 typedef struct {

@@ -8,6 +8,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import threading
 from typing import Optional
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -477,8 +478,12 @@ def _home(index):
     return _torch()._C._cuda_getCurrentRawStream(index)
 
 
-def _call(name, other, args):
-    """One C call, with the call's device current."""
+def _call(name, other, args, turns=None):
+    """One C call, with the call's device current.  ctypes lets other threads run meanwhile; of a plan or cache, whose calls
+    enqueue kernels that belong together, they take turns by its lock."""
+    if turns is not None:
+        with turns:
+            return _call(name, other, args)
     fn = getattr(_lib or load(), name)
     if other is None:
         st = fn(*args)
@@ -654,8 +659,8 @@ class Rope:
             desc.k_in, desc.k_out = _Stride3(*k.stride()[:3]), _Stride3(*k_out.stride()[:3])
         if len(self._descs) > 64:
             self._descs.clear()
-        self._descs[key] = ctypes.byref(desc)
-        return self._descs[key]
+        ref = self._descs[key] = ctypes.byref(desc)
+        return ref
 
     def check(self, stream=None):
         """Raises EDEVICE if a call since the last check met a position outside the table.  Synchronises `stream` (the
@@ -665,7 +670,8 @@ class Rope:
 
 class _AttnPlan:
     """Sizes, options and the workspace of an attention operator.  A plan serves one call at a time: calls that can
-    overlap on the GPU (two streams, two replayed graphs) need plans of their own."""
+    overlap on the GPU (two streams, two replayed graphs) need plans of their own.  Host threads may share a plan on one
+    stream."""
 
     def _setup(self, where, batch, s_q, s_kv, h_q, h_kv, dtype, causal, softcap, scale, device):
         import torch
@@ -687,7 +693,7 @@ class _AttnPlan:
         _settled(self.work)
         d = self.desc
         self.index, self._descs = self.work.get_device(), {}
-        self._home, self._own = _home(self.index), (self.work,)
+        self._home, self._own, self._turns = _home(self.index), (self.work,), threading.RLock()
         self._work = (self.work.data_ptr(), nbytes)
         self.q_shape, self.kv_shape = (d.batch, d.s_q, d.h_q, 128), (d.batch, d.s_kv, d.h_kv, 128)
 
@@ -767,7 +773,7 @@ class Attention(_AttnPlan):
                                          _array(where, "doc_ids", doc_ids, (d.batch, d.s_kv), i32, i)))
         s, other = _enter(i, stream, (q, k, v, out, lse, slopes, q_len, kv_len, prefix_len, doc_ids), self._home, self._own)
         _call("qevict_attn", other, (desc, mask, q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), lse.data_ptr(),
-                                     *self._work, s))
+                                     *self._work, s), self._turns)
         return out, lse
 
 
@@ -800,7 +806,7 @@ class PrefixAttention(_AttnPlan):
                 _array(where, "kv_len", kv_len, self.q_shape[:1], _torch().int32, i), q.data_ptr(), k_prefix.data_ptr(),
                 v_prefix.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), lse.data_ptr(), *self._work)
         s, other = _enter(i, stream, (q, k_prefix, v_prefix, k, v, out, lse, slopes, kv_len), self._home, self._own)
-        _call("qevict_prefix_attn", other, (*args, s))
+        _call("qevict_prefix_attn", other, (*args, s), self._turns)
         return out, lse
 
     def _with_strides(self, key):
@@ -821,7 +827,8 @@ class PagedCache:
     use at the pool's beginning.  See qevict_pages_* for what each does.
 
     length, held [batch], table [batch][max_pages], refs [pages] and n_free are views of `state`, one int32 tensor: with copies
-    of it and the pool a cache is saved and restored.  Calls of a cache run in order: one stream, or ordered by the caller."""
+    of it and the pool a cache is saved and restored.  Calls of a cache run in order: one stream (host threads may share it), or
+    ordered by the caller."""
 
     def __init__(self, layers, pages, page, h_kv, batch, max_pages, dtype=None, device="cuda", k=None, v=None):
         import torch
@@ -858,6 +865,7 @@ class PagedCache:
         self.table = part(lay.table, desc.batch * desc.max_pages).view(desc.batch, desc.max_pages)
         self.index, self._i32 = self.state.get_device(), torch.int32
         self._seqs, self._home, self._own = self.length.shape, _home(self.index), (self.state, k, v)
+        self._turns = threading.RLock()
         self._desc, self._state, self._pool, self._rows = ctypes.byref(desc), self.state.data_ptr(), \
             (k.data_ptr(), v.data_ptr()), {}
         self.load()
@@ -871,7 +879,7 @@ class PagedCache:
 
     def _run(self, name, stream, tensors, *args):
         s, other = _enter(self.index, stream, tensors, self._home, self._own)
-        _call(name, other, (self._desc, *args, s))
+        _call(name, other, (self._desc, *args, s), self._turns)
 
     def load(self, table=None, length=None, stream=None):
         """Starts the bookkeeping from a table int32 [batch][max_pages] (-1: no page) and lengths int32 [batch], or empty."""
@@ -917,12 +925,12 @@ class PagedCache:
         st = [(0,) * (4 - len(shape) + 1) + tuple(t.stride()[:-1]) for t in (k, v)]
         if layer is not None:
             _need(0 <= layer < layers, where, f"layer must be in [0, {layers}), is {layer}")
-        rows = PagesRows(0 if layer is None else int(layer), layers if layer is None else 1, shape[-3], 0, _Stride4(*st[0]),
-                         _Stride4(*st[1]))
-        if len(self._rows) > 256:
+        rows = ctypes.byref(PagesRows(0 if layer is None else int(layer), layers if layer is None else 1, shape[-3], 0,
+                                      _Stride4(*st[0]), _Stride4(*st[1])))
+        if len(self._rows) > 256:   # (another thread may clear them too)
             self._rows.clear()
-        self._rows[key] = ctypes.byref(rows)
-        return self._rows[key]
+        self._rows[key] = rows
+        return rows
 
     def accept(self, count, path=None, stream=None):
         """The first count[b] rows behind each length count from now on; with path int32 [batch][max_path], max_path 1 to 256,
@@ -974,8 +982,6 @@ class PagedAttention(_AttnPlan):
         self._workspace(n.value)
         self.kv_shape, self._i32 = self.pool_shape, torch.int32
         self._heads, self._seqs, self._tree, self._trees = (d.h_q,), (d.batch,), (d.s_q,), (d.batch, d.s_q)
-        self._mask = PagedAttnMask()   # (filled by every call that has one)
-        self._mask_ref = ctypes.byref(self._mask)
 
     def run(self, q, k, v, table, length, out=None, lse=None, parents=None, q_len=None, slopes=None, stream=None):
         """q [batch][s_q][h_q][128], k, v [pages][page][h_kv][128] (one layer's pool), table int32 [batch][max_pages], length
@@ -988,16 +994,15 @@ class PagedAttention(_AttnPlan):
         desc, out, lse = self._tensors(where, q, k, v, out, lse, stream)
         _need(table is not None and length is not None, where, "table and length are needed")
         if not (slopes is None and q_len is None and parents is None):
-            mask, one = self._mask, parents is not None and parents.dim() == 1
-            mask.slopes = _array(where, "slopes", slopes, self._heads, _torch().float32, i)
-            mask.q_len = _array(where, "q_len", q_len, self._seqs, i32, i)
-            mask.parents = _array(where, "parents", parents, self._tree if one else self._trees, i32, i)
-            mask.one_tree = one
-            mask = self._mask_ref
+            one = parents is not None and parents.dim() == 1
+            mask = ctypes.byref(PagedAttnMask(_array(where, "slopes", slopes, self._heads, _torch().float32, i),
+                                              _array(where, "q_len", q_len, self._seqs, i32, i),
+                                              _array(where, "parents", parents, self._tree if one else self._trees, i32, i),
+                                              one))
         args = (desc, mask, q.data_ptr(), k.data_ptr(), v.data_ptr(), _array(where, "table", table, self.table_shape, i32, i),
                 _array(where, "length", length, self._seqs, i32, i), out.data_ptr(), lse.data_ptr(), *self._work)
         s, other = _enter(i, stream, (q, k, v, table, length, out, lse, parents, q_len, slopes), self._home, self._own)
-        _call("qevict_paged_attn", other, (*args, s))
+        _call("qevict_paged_attn", other, (*args, s), self._turns)
         return out, lse
 
     def _with_strides(self, key):
