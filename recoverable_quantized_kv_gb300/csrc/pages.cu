@@ -372,7 +372,7 @@ __global__ void __launch_bounds__(1024, 1) pages_reserve_kernel(const __grid_con
   s_tail[t] = tail;
   if (t == 0) *P.n_copies = 0, *P.drawn = 0;
   bool rare = __syncthreads_or(bad || lo < hi || keep < held);   // one barrier for a step without any of them
-  if (rare && __syncthreads_or(bad)) {
+  if (__builtin_expect(rare, false) && __syncthreads_or(bad)) {
     if (t == 0) atomicOr(P.status, QV_ERR_BOUNDS);
     return;
   }
@@ -387,7 +387,7 @@ __global__ void __launch_bounds__(1024, 1) pages_reserve_kernel(const __grid_con
     }
     return a;
   };
-  if (rare && __syncthreads_or(lo < hi)) {
+  if (__builtin_expect(rare, false) && __syncthreads_or(lo < hi)) {
     const Sums at = scan_1024(max(hi - lo, 0), 0, s_warp);
     if (t < P.batch) s_start[t] = at.x, s_copy[t] = lo;
     __syncthreads();
@@ -409,7 +409,7 @@ __global__ void __launch_bounds__(1024, 1) pages_reserve_kernel(const __grid_con
     __syncthreads();
     if (t < P.batch) keep = s_held[t];
   }
-  if (rare) rare = __syncthreads_or(keep < held);   // some give pages back
+  if (__builtin_expect(rare, false)) rare = __syncthreads_or(keep < held);   // some give pages back
   const int add = max(want - keep, 0);
   bool copy = false;
   // Shared pages: how many that reserve now hold each, and is this the first of them.  A look at every other sequence costs
@@ -447,7 +447,7 @@ __global__ void __launch_bounds__(1024, 1) pages_reserve_kernel(const __grid_con
     *P.n_copies = need.all_y;
     *P.n_free = n_free - total;
   }
-  if (rare) {
+  if (__builtin_expect(rare, false)) {
     __syncthreads();   // the count is written
     int free = 0;
     if (keep < held) {
@@ -504,7 +504,7 @@ __global__ void __launch_bounds__(1024, 1) pages_reserve_kernel(const __grid_con
     }
     found += at.all_x;
   }
-  if (!rare) {
+  if (__builtin_expect(!rare, true)) {
     if (copy) atomicSub(&P.refs[tail], 1);
   } else if (copy && give_back(P, tail)) {   // its other holders gave the page back in this call (all words are written)
     atomicAdd(P.n_free, 1);
