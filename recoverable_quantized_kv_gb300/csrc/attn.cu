@@ -4,12 +4,12 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
-#include <atomic>
 #include <cmath>
 #include <cstdint>
 
 #include "attn_dev.cuh"
 #include "qevict.h"
+#include "sm_count.h"
 
 namespace qv {
 cudaError_t launch_attn_bf16(const AttnArgs &P, int grid, bool bias, cudaStream_t s);
@@ -298,20 +298,6 @@ __global__ void __launch_bounds__(WARPS == 1 ? 128 : 32 * WARPS) attn_combine_ro
 namespace {
 
 int64_t align256(int64_t x) { return (x + 255) & ~int64_t(255); }
-
-int sm_count() {   // of the current device
-  static std::atomic<int> known[64];
-  int dev = 0, n = 0;
-  if (cudaGetDevice(&dev) == cudaSuccess && dev >= 0 && dev < 64) {
-    if ((n = known[dev].load(std::memory_order_relaxed)) > 0) return n;
-    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) == cudaSuccess && n > 0) {
-      known[dev].store(n, std::memory_order_relaxed);
-      return n;
-    }
-  }
-  cudaGetLastError();
-  return 152;
-}
 
 // [tokens][heads][128] tensors of `batch` sequences as a 4-D tensor map; a box is 64 channels x `bh` heads x
 // `bt` tokens x `bb` sequences, 128-byte swizzled.  batch: 1 when the batch stride is 0.

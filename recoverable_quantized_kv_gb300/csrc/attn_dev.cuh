@@ -688,9 +688,9 @@ __global__ void __launch_bounds__(attn_threads(PAGED), 1) attn_kernel(const __gr
     };
     const int groups = P.n_pr * P.batch;
     if (whole) {
-      // Whole units, the longest (last rows of causal prompts) first, each to the CTA that is ready next: lengths and
-      // documents make units differ, and a fixed turn leaves some CTAs twice the mean (a padded batch of prefix-mask
-      // prompts 54 us, drawn 31).  A CTA's first unit is its own number; it draws the next when its TMA warp has asked
+      // Whole units, last rows of causal prompts first, sequences as they stand in the batch, each unit to the CTA that is
+      // ready next: lengths and documents make units differ, and a fixed turn leaves some CTAs twice the mean (a padded batch
+      // of prefix-mask prompts 54 us, drawn 31).  (The longest units first would be best.)  A CTA's first unit is its own number; it draws the next when its TMA warp has asked
       // for the last one's tiles, two or three tiles before it needs it.  Every CTA draws once past the end, so the draw
       // that takes the count to the number of units is the last, and starts it again for the next call.
       const int units = groups * P.h_kv;
@@ -837,7 +837,7 @@ __global__ void __launch_bounds__(attn_threads(PAGED), 1) attn_kernel(const __gr
           const uint32_t st = c % AT_STAGES;
           if (!ok || !(ok = attn_wait_warp(&empty[st], ((c / AT_STAGES) & 1) ^ 1, status))) return;
           const uint32_t dst = smem_u32(sm) + AT_OFF_KV + st * AT_TILE_BYTES;
-          const int first = (I.t_hi - 1 - j) * per, n = min(per, used - first);   // (values lag by two tiles at most)
+          const int first = (I.t_hi - 1 - j) * per, n = min(per, used - first);   // (a warp's own tiles only descend)
           if (first < w - 32) {
             w -= 32;
             here = below;

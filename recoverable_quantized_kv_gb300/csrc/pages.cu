@@ -11,6 +11,7 @@
 
 #include "common.cuh"
 #include "qevict.h"
+#include "sm_count.h"
 
 namespace qv {
 namespace {
@@ -779,10 +780,10 @@ bool launch(void (*kern)(Params...), dim3 grid, int threads, qevict_stream_t str
 }
 
 unsigned ceil_div(int64_t x, int64_t y) { return (unsigned)((x + y - 1) / y); }
-// At most `most` pages to copy: no more CTAs than fit on 152 SMs at once.
+// At most `most` pages to copy: no more CTAs than fit on the SMs at once, three on each.
 dim3 copy_grid(const PagesDev &P, int64_t most) {
   const int64_t parts = ceil_div((int64_t)P.page * P.h_kv * 16, PART_PIECES);
-  return dim3((unsigned)std::min<int64_t>(most * parts * 2 * P.layers, 152 * 3));
+  return dim3((unsigned)std::min<int64_t>(most * parts * 2 * P.layers, qv::sm_count() * 3));
 }
 bool word_ok(const void *p, bool needed) { return !((uintptr_t)p & 3) && (p || !needed); }
 
@@ -856,10 +857,10 @@ qevict_status qevict_pages_accept(const qevict_pages_desc *desc, void *k, void *
   if (!qv::word_ok(d_count, true) || !qv::word_ok(d_path, false) ||
       (d_path ? max_path < 1 || max_path > qv::PG_PATH : max_path != 0))
     return QEVICT_EINVAL;
-  // CTAs for every 256 columns of 16 bytes, or four on each of 152 SMs over all sequences: the table and path are looked
+  // CTAs for every 256 columns of 16 bytes, or four on each SM over all sequences: the table and path are looked
   // up once a CTA
   const unsigned cols = qv::ceil_div((int64_t)P.layers * 2 * P.h_kv * 16, 256);
-  const dim3 grid(d_path ? std::min(cols, std::max(1u, 4u * 152u / P.batch)) : 1, P.batch);
+  const dim3 grid(d_path ? std::min(cols, std::max(1u, 4u * qv::sm_count() / P.batch)) : 1, P.batch);
   return qv::launch(qv::pages_accept_kernel, grid, 256, stream, P, (const int *)d_count, (const int *)d_path, (int)max_path)
              ? QEVICT_OK : QEVICT_ECUDA;
 }
