@@ -814,10 +814,17 @@ class PrefixAttention(_AttnPlan):
 
 
 def _sizes(where, **sizes):
-    """Sizes as ints of the C interface; one that is larger would be another there."""
+    """Sizes as ints of the C interface; one that is larger, or no whole number, would be another there."""
+    res = []
     for name, n in sizes.items():
-        _need(-2 ** 31 <= int(n) < 2 ** 31, where, f"{name} is out of range: {n}")
-    return tuple(int(n) for n in sizes.values())
+        try:
+            whole = int(n)
+        except (TypeError, ValueError, OverflowError):
+            whole = None
+        _need(whole is not None and whole == n, where, f"{name} is no whole number: {n!r}")
+        _need(-2 ** 31 <= whole < 2 ** 31, where, f"{name} is out of range: {n}")
+        res.append(whole)
+    return tuple(res)
 
 
 class PagedCache:
@@ -923,9 +930,11 @@ class PagedCache:
         for name, t in (("k", k), ("v", v)):
             _tensor(t, where, name, shape, self.dtype, self.device)
         st = [(0,) * (4 - len(shape) + 1) + tuple(t.stride()[:-1]) for t in (k, v)]
+        first = 0
         if layer is not None:
-            _need(0 <= layer < layers, where, f"layer must be in [0, {layers}), is {layer}")
-        rows = ctypes.byref(PagesRows(0 if layer is None else int(layer), layers if layer is None else 1, shape[-3], 0,
+            first, = _sizes(where, layer=layer)
+            _need(0 <= first < layers, where, f"layer must be in [0, {layers}), is {layer}")
+        rows = ctypes.byref(PagesRows(first, layers if layer is None else 1, shape[-3], 0,
                                       _Stride4(*st[0]), _Stride4(*st[1])))
         if len(self._rows) > 256:   # (another thread may clear them too)
             self._rows.clear()
