@@ -481,15 +481,18 @@ def _home(index):
 def _call(name, other, args, turns=None):
     """One C call, with the call's device current.  ctypes lets other threads run meanwhile; of a plan or cache, whose calls
     enqueue kernels that belong together, they take turns by its lock."""
-    if turns is not None:
-        with turns:
-            return _call(name, other, args)
     fn = getattr(_lib or load(), name)
-    if other is None:
-        st = fn(*args)
-    else:
-        with _torch().cuda.device(other):
+    if turns is not None:
+        turns.acquire()
+    try:
+        if other is None:
             st = fn(*args)
+        else:
+            with _torch().cuda.device(other):
+                st = fn(*args)
+    finally:
+        if turns is not None:
+            turns.release()
     if st != OK:
         _check(st, name)
 
