@@ -552,8 +552,8 @@ qevict_status qevict_pages_load(const qevict_pages_desc *desc, void *d_state, co
 qevict_status qevict_pages_reserve(const qevict_pages_desc *desc, void *k, void *v, void *d_state, const int32_t *d_new,
                                    int32_t n_new, qevict_stream_t stream);
 /* Writes rows length[b] + i, i < n[b], of layers [layer, layer + layers) from k_new, v_new
- * [layers][batch][n][h_kv][128]; n[b] = d_n[b] (at most n), or n where d_n is NULL.  Lengths stay: the rows count once
- * qevict_pages_accept takes them.  Rows whose page is missing or shared are not written (bit 8).  k_new and v_new share no
+ * [layers][batch][n][h_kv][128]; n[b] = d_n[b], clamped to 0 .. n (bit 8), or n where d_n is NULL.  Lengths stay: the rows count
+ * once qevict_pages_accept takes them.  Rows whose page is missing or shared are not written (bit 8).  k_new and v_new share no
  * bytes with the pool. */
 typedef struct {
   int32_t layer, layers, n, reserved0;   /* layers 1.., n 1.., reserved0 0 */

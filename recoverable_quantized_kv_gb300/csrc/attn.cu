@@ -343,7 +343,9 @@ int merge_warps(const AttnPlan &p, const qevict_attn_desc *d) {
 // merged?  Both are estimated in us.  Whole: a round of units on all SMs takes 1.45 a tile and 1 more, the last one on some of
 // them 0.55 to 0.95 a tile.  Cut: 1.4 a tile and 6 a unit, shared by all SMs; with fewer units than SMs, where whole ones wait for
 // the longest sequence, 0.97 a tile.  The rates are those with which the choice cost least over batches of 1 to 64, equal and
-// ragged, against 420 to 32500 keys: 0.8% on average, 20% at most.  Single tokens of ragged batches of 8 KV heads, whole and cut:
+// ragged with falling lengths, against 420 to 32500 keys in tables without room to spare: 0.8% on average, 20% at most.
+// (Lengths are on the device: with room for 33K keys, 64 tokens against up to 1040 are cut and take 62 us instead of 44.)
+// Single tokens of ragged batches of 8 KV heads, whole and cut:
 // 4 sequences against 420 / 1040 / 4160 keys 9.7 / 14.1 / 36 and 11.8 / 14.9 / 21 us, 12 against 1040 / 2040 / 4160 16.0 / 23.0 /
 // 39 and 21.9 / 27.0 / 37, 16 against 32500 255 and 218, 64 against 1040 / 4160 45 / 119 and 64 / 124.
 bool whole_units(int64_t units, int64_t tiles, int64_t sms) {
