@@ -538,7 +538,8 @@ typedef struct {
 qevict_status qevict_pages_get_layout(const qevict_pages_desc *desc, qevict_pages_layout *layout);
 /* Starts the bookkeeping: from d_table [batch][max_pages] and d_length [batch], or empty (both NULL).  The entries of a sequence
  * up to the first that is not a page of the pool are its pages (entries other than -1 there set bit 8), a length past them or below 0
- * is clamped (bit 8).  A page at two different places of the tables sets bit 4.  Clears the status word first. */
+ * is clamped (bit 8).  A page at two different places of the tables sets bit 4: the cache is to be loaded again before any other
+ * call.  Clears the status word first. */
 qevict_status qevict_pages_load(const qevict_pages_desc *desc, void *d_state, const int32_t *d_table,
                                 const int32_t *d_length, qevict_stream_t stream);
 /* Makes rows length[b] .. length[b] + new - 1 of every sequence writable; new = d_new[b], or n_new where d_new is NULL.
@@ -546,7 +547,7 @@ qevict_status qevict_pages_load(const qevict_pages_desc *desc, void *d_state, co
  * next token stands in a page that other sequences hold too, the sequence gets a page of its own with a copy of its rows
  * (all layers); of several sequences that hold it and reserve in one call, the first keeps it if no other holds it.  Held pages
  * without tokens of the sequence (after qevict_pages_load, or a length written back) from the first one on that the rows reach and
- * other sequences hold too are given back, and free ones taken for them.  A sequence with new = 0 is left as it is.  If the
+ * other sequences hold too are given back, and free ones taken as the rows need them.  A sequence with new = 0 is left as it is.  If the
  * pages that are free before the call do not suffice (bit 2), or a sequence would pass max_pages (bit 8, also for new < 0),
  * nothing changes for any sequence. */
 qevict_status qevict_pages_reserve(const qevict_pages_desc *desc, void *k, void *v, void *d_state, const int32_t *d_new,
